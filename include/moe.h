@@ -588,6 +588,147 @@ moe_status moe_selftest_wait_timeout(void* ws, size_t ws_bytes, int64_t limit_cy
  * FP32 FMA-pipe rate that bounds the fp32 router GEMM. */
 moe_status moe_probe_fp32_fma(int64_t iters, float* out, double* flops, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the layer: the norm before it, the dropout and residual sum after it,
+ * and experts with 4-bit weights for decoding.  These are not steps of the
+ * pages' layer; they are what a transformer block puts next to it:
+ *   training   z = x + dropout(moe(norm(x))), with every gradient;
+ *   decoding   z = x + moe(norm(x)) of a few tokens, the experts in 4 bits.
+ * The conventions at the top hold (contiguous, 16-byte aligned, asynchronous).
+ * ------------------------------------------------------------------------- */
+
+typedef enum moe_norm_kind {
+  MOE_NORM_LAYER = 0, /* y = (z - mean z) / sqrt(var z + eps) * weight + bias */
+  MOE_NORM_RMS = 1    /* y = z / sqrt(mean z^2 + eps) * weight + bias */
+} moe_norm_kind;
+
+typedef struct moe_norm_config {
+  int64_t rows;
+  double dropout;      /* p in [0, 1]; 0: no dropout */
+  int32_t hidden;      /* row length, any value from 1 up to 2^24 */
+  int32_t dtype;       /* moe_dtype of x, residual, z, y and their gradients */
+  int32_t param_dtype; /* moe_dtype of weight and bias (MOE_F32 when dtype is) */
+  int32_t kind;        /* moe_norm_kind */
+  float eps;           /* >= 0 */
+} moe_norm_config;
+
+/*
+ * The dropout mask is a function of rng and of an element's place, and is never
+ * stored: element i of the tensor (row-major, 64-bit) is kept iff word i % 4 of
+ * Philox4x32-10 with the counter (i / 4, rng[1]) and the key rng[0] is at least
+ * floor(p 2^32); kept elements are scaled by 1 / (1 - p), dropped ones are 0
+ * (also where the input is infinite or NaN).  Philox: Salmon, Moraes, Dror,
+ * Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011.  rng is two
+ * uint64 in DEVICE memory, seed and offset, read when the kernel runs: a
+ * captured graph draws other masks once the caller has advanced the offset.
+ * The same rng gives the same mask in every function below.
+ */
+
+/*
+ * z = residual + dropout(x), y = norm(z), all sums in fp32; one rounding each
+ * for z and y (y is formed from the unrounded z).  residual NULL: z = x, and
+ * then z must be NULL and dropout 0.  weight NULL: ones; bias NULL: zeros.
+ * mean, rstd [rows] fp32 (each NULL: not written) are what the backward needs;
+ * mean is not written by the RMS norm.  z may be x or residual itself and y may
+ * be x or residual; y and z are different buffers.
+ */
+moe_status moe_layer_norm(const moe_norm_config* cfg, const void* x, const void* residual,
+                          const uint64_t* rng, const void* weight, const void* bias, void* z,
+                          void* y, float* mean, float* rstd, moe_stream_t stream);
+
+/*
+ * The norm's backward: z is the normed tensor (the forward's z, or its x when
+ * there was no residual), mean (NULL for RMS) and rstd what the forward stored.
+ * With g = dy * weight and xh = (z - mean) * rstd:
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)) + dz     (RMS: no mean(g))
+ *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy   (fp32)
+ * dz (NULL: zeros) is the gradient that reaches z by other paths; dx is the
+ * gradient of z and so of residual; dbranch = dropout's map of dx (before its
+ * rounding), the gradient of the forward's x; it may be NULL, and is the only
+ * use of dropout and rng.  dweight and dbias (each may be NULL) are written in
+ * full (zeros for no rows) and do not depend on timing: fixed order of sums.
+ * dx may be dy or dz itself, dbranch too (another one than dx's).
+ */
+moe_status moe_workspace_size_norm_backward(const moe_norm_config* cfg, size_t* bytes);
+moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, const void* z,
+                                   const void* weight, const float* mean, const float* rstd,
+                                   const void* dz, const uint64_t* rng, void* dx, void* dbranch,
+                                   float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream);
+
+/*
+ * y = residual + dropout(x) over n elements (residual NULL: dropout alone).
+ * The gradient of x is the same call on dy without a residual; the gradient of
+ * residual is dy.  y may be x or residual itself.
+ */
+moe_status moe_dropout_add(int64_t n, int32_t dtype, double dropout, const uint64_t* rng,
+                           const void* x, const void* residual, void* y, moe_stream_t stream);
+
+/*
+ * 4-bit weights.  W [N, K] (one output row of K inputs after another; [E, N, K]
+ * for experts) is held as codes 0..15 with a bf16 scale and, optionally, a zero
+ * point for each group of `group` (32, 64 or 128) inputs of a row:
+ *   W[n, k] = scales[n, k / group] * (code[n, k] - zeros[n, k / group]),
+ * zeros NULL: 8.  K is a multiple of group; scales and zeros (uint8, 0..15) are
+ * [N, K / group].  A row's codes are ceil(K / 128) blocks of 64 bytes; within a
+ * block of 128 inputs the 32-bit word 4t + j (t, j = 0..3, little-endian) holds
+ * the inputs k = 32j + 8t + i, i = 0..7, input i in nibble i / 2 + 4 (i % 2)
+ * (nibble 0: the lowest four bits).  Codes past K are not used.
+ * The products take x in bf16 and sum in fp32; the scales multiply fp32 sums of
+ * one group, so W itself is never rounded.
+ */
+typedef struct moe_w4 {
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+} moe_w4;
+
+/* W [experts, K, N] bf16 (the layout of the layer's W1, W3, W2) -> 4 bits,
+ * rounded to the nearest code.  zeros NULL: symmetric, scale = max |w| / 7;
+ * else scale = (max(w, 0) - min(w, 0)) / 15 and zero = round(-min(w, 0) / scale).
+ * The codes are chosen against the rounded scale.  A group of zeros gets scale
+ * 0.  N and K multiples of 64. */
+moe_status moe_quantize_w4(int32_t experts, int32_t K, int32_t N, int32_t group, const void* W,
+                           uint8_t* codes, void* scales, uint8_t* zeros, moe_stream_t stream);
+/* values [experts, N, K] (one byte each, its low four bits) -> codes; the codes
+ * past K become 0. */
+moe_status moe_pack_w4(int32_t experts, int32_t N, int32_t K, const uint8_t* values,
+                       uint8_t* codes, moe_stream_t stream);
+
+/* y [rows, N] (y_dtype) = x [rows, K] bf16 . W^T.  Made for few rows (decoding):
+ * the weight is read once for every 32 rows. */
+moe_status moe_workspace_size_linear_w4(int64_t rows, int32_t N, int32_t K, size_t* bytes);
+moe_status moe_linear_w4(int64_t rows, int32_t N, int32_t K, int32_t group, const void* x,
+                         const moe_w4* W, void* y, int32_t y_dtype, void* ws, size_t ws_bytes,
+                         moe_stream_t stream);
+
+/*
+ * The routed experts with 4-bit weights, from the router's outputs, without a
+ * permutation step: y[t] = sum_j p[t, j] (silu(x W1^T) * (x W3^T)) W2^T of the
+ * expert topk_idx[t, j], over the pairs with keep (NULL: every pair); a token
+ * without a kept pair gets zeros.  W1, W3 [E, f, h], W2 [E, h, f] in 4 bits, one
+ * group size for the three.  The hidden values enter the second product as two
+ * bf16 each (their sum is within 2^-17 of the fp32 value).  bf16 layers only
+ * (MOE_ERR_UNSUPPORTED).  An expert id out of range is reported in ws
+ * (moe_check) and its pair left out.  Made for decoding: an expert's weights are
+ * read once for every 1024 / k tokens at most; many tokens belong to
+ * moe_forward or moe_forward_e4m3.
+ */
+moe_status moe_workspace_size_experts_w4(const moe_config* cfg, size_t* bytes);
+moe_status moe_experts_w4(const moe_config* cfg, int32_t group, const void* x,
+                          const int32_t* topk_idx, const float* topk_prob, const uint8_t* keep,
+                          const moe_w4* W1, const moe_w4* W3, const moe_w4* W2, void* y, void* ws,
+                          size_t ws_bytes, moe_stream_t stream);
+
+/* The layer forward with those experts: moe_route, then moe_experts_w4.
+ * pad_to_capacity changes nothing here (padding rows carry no weight). */
+moe_status moe_workspace_size_w4(const moe_config* cfg, size_t* bytes);
+moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, const float* Wg,
+                          const float* gate_bias, const float* expert_bias, const moe_w4* W1,
+                          const moe_w4* W3, const moe_w4* W2, void* y, int32_t* topk_idx,
+                          float* topk_prob, int32_t* tokens_per_expert, void* ws,
+                          size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,13 @@ EXPORTS = ["moe_abi_version", "moe_status_string", "moe_last_cuda_error", "moe_c
            "moe_shared_expert_backward", "moe_workspace_size_host_shared",
            "moe_forward_host_shared", "moe_workspace_size_host_e4m3", "moe_forward_host_e4m3",
            "moe_permute_map", "moe_permute_map_e4m3", "moe_grouped_fc2_combine",
-           "moe_grouped_fc2_f16s", "moe_combine_f16s", "moe_grouped_fc2_e4m3_f16s"]
+           "moe_grouped_fc2_f16s", "moe_combine_f16s", "moe_grouped_fc2_e4m3_f16s",
+           "moe_layer_norm", "moe_workspace_size_norm_backward", "moe_layer_norm_backward",
+           "moe_dropout_add", "moe_quantize_w4", "moe_pack_w4", "moe_workspace_size_linear_w4",
+           "moe_linear_w4", "moe_workspace_size_experts_w4", "moe_experts_w4",
+           "moe_workspace_size_w4", "moe_forward_w4"]
+
+NORM = {"layer": 0, "rms": 1}
 
 
 class MoeConfig(ctypes.Structure):
@@ -45,6 +51,18 @@ class MoeConfig(ctypes.Structure):
                 ("capacity_factor", ctypes.c_float), ("min_capacity", ctypes.c_int32),
                 ("num_groups", ctypes.c_int32), ("group_topk", ctypes.c_int32),
                 ("pad_to_capacity", ctypes.c_int32)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dropout", ctypes.c_double),
+                ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class W4Pointers(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("zeros", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -68,6 +86,8 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
         cfgp = ctypes.POINTER(MoeConfig)
+        normp, w4p = ctypes.POINTER(NormConfig), ctypes.POINTER(W4Pointers)
+        f64 = ctypes.c_double
         sig = {
             "moe_abi_version": ([], i32),
             "moe_status_string": ([i32], ctypes.c_char_p),
@@ -118,6 +138,19 @@ def lib():
                                         [vp, sz, vp], i32),
             "moe_workspace_size_host_e4m3": ([cfgp, ctypes.POINTER(sz)], i32),
             "moe_forward_host_e4m3": ([cfgp, i32, vp, sz, vp, sz] + [vp] * 9 + [vp, sz, vp], i32),
+            "moe_layer_norm": ([normp] + [vp] * 10, i32),
+            "moe_workspace_size_norm_backward": ([normp, ctypes.POINTER(sz)], i32),
+            "moe_layer_norm_backward": ([normp] + [vp] * 11 + [vp, sz, vp], i32),
+            "moe_dropout_add": ([i64, i32, f64, vp, vp, vp, vp, vp], i32),
+            "moe_quantize_w4": ([i32, i32, i32, i32, vp, vp, vp, vp, vp], i32),
+            "moe_pack_w4": ([i32, i32, i32, vp, vp, vp], i32),
+            "moe_workspace_size_linear_w4": ([i64, i32, i32, ctypes.POINTER(sz)], i32),
+            "moe_linear_w4": ([i64, i32, i32, i32, vp, w4p, vp, i32, vp, sz, vp], i32),
+            "moe_workspace_size_experts_w4": ([cfgp, ctypes.POINTER(sz)], i32),
+            "moe_experts_w4": ([cfgp, i32, vp, vp, vp, vp, w4p, w4p, w4p, vp, vp, sz, vp], i32),
+            "moe_workspace_size_w4": ([cfgp, ctypes.POINTER(sz)], i32),
+            "moe_forward_w4": ([cfgp, i32, vp, vp, vp, vp, w4p, w4p, w4p, vp, vp, vp, vp, vp, sz,
+                                vp], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -591,6 +624,247 @@ def shared_expert_backward(cfg, fs, x, W1s, W3s, W2s, h_mid_s, dy, dx_acc, gs, w
                                             _p(W2s), _p(h_mid_s), _p(dy), _p(dx_acc),
                                             _p(gs.dW1s), _p(gs.dW3s), _p(gs.dW2s), w, wb,
                                             _stream()), "moe_shared_expert_backward")
+
+
+# ------------------------------------------------- norm, dropout (the layer's block)
+
+_DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _code(t, what):
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be float32 or bfloat16, not %s" % (what, t.dtype))
+    return code
+
+
+def _like(t, ref, what):
+    if t is not None and (t.shape != ref.shape or t.dtype != ref.dtype):
+        raise ValueError("%s must have the shape and dtype of its input" % what)
+    return _p(t)
+
+
+def _vec(t, n, dtype, what):
+    if t is not None and (t.numel() != n or t.dtype != dtype):
+        raise ValueError("%s must hold %d values of %s" % (what, n, dtype))
+    return _p(t)
+
+
+def _rng(rng, p):
+    if p > 0 and (rng is None or rng.numel() != 2 or rng.dtype not in (torch.int64,
+                                                                       torch.uint64)):
+        raise ValueError("rng must be a device tensor of two 64-bit integers: seed and offset")
+    return _p(rng)
+
+
+def _norm_config(x, weight, bias, rms, eps, p):
+    if x.dim() == 0:
+        raise ValueError("the normed tensor needs a last dimension")
+    hidden = x.shape[-1]
+    dt = _code(x, "the normed tensor")
+    pt = dt
+    for t, what in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            pt = _code(t, what)
+            if t.numel() != hidden:
+                raise ValueError("%s must hold %d values" % (what, hidden))
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    return NormConfig(x.numel() // hidden if hidden else 0, float(p), hidden, dt, pt, int(rms),
+                      float(eps))
+
+
+def layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, rms=False, residual=None, z=None,
+               p=0.0, rng=None):
+    """y = norm(z) over the last dimension, z = residual + dropout(x) (or x
+    without a residual); layer norm, or RMS norm with rms=True.  weight, bias:
+    float32 or bfloat16, or None.  z (where given), mean and rstd (fp32, one
+    value a row) are what layer_norm_backward needs.  rng: device tensor of
+    two 64-bit integers, seed and offset of the dropout's mask."""
+    cfg = _norm_config(x, weight, bias, rms, eps, p)
+    _check(lib().moe_layer_norm(ctypes.byref(cfg), _p(x), _like(residual, x, "residual"),
+                                _rng(rng, p), _p(weight), _p(bias), _like(z, x, "z"),
+                                _like(y, x, "y"), _vec(mean, cfg.rows, torch.float32, "mean"),
+                                _vec(rstd, cfg.rows, torch.float32, "rstd"), _stream()),
+           "moe_layer_norm")
+
+
+def workspace_size_norm_backward(rows, hidden):
+    v = ctypes.c_size_t()
+    cfg = NormConfig(int(rows), 0.0, int(hidden), 0, 0, 0, 0.0)
+    _check(lib().moe_workspace_size_norm_backward(ctypes.byref(cfg), ctypes.byref(v)),
+           "moe_workspace_size_norm_backward")
+    return v.value
+
+
+def alloc_workspace_norm_backward(rows, hidden, device="cuda"):
+    return torch.zeros(workspace_size_norm_backward(rows, hidden), dtype=torch.uint8,
+                       device=device)
+
+
+def layer_norm_backward(dy, z, weight, mean, rstd, dx, dweight, dbias, ws, rms=False, dz=None,
+                        dbranch=None, p=0.0, rng=None):
+    """Backward of layer_norm: dx = the gradient of z (the norm's, plus dz) and
+    so of the residual, dbranch = that of the dropout's input (p, rng as in the
+    forward), dweight and dbias fp32 (each may be None)."""
+    cfg = _norm_config(z, weight, None, rms, 0.0, p)
+    w, wb = _ws(ws)
+    n = cfg.hidden
+    _check(lib().moe_layer_norm_backward(
+        ctypes.byref(cfg), _like(dy, z, "dy"), _p(z), _p(weight),
+        _vec(mean, cfg.rows, torch.float32, "mean"), _vec(rstd, cfg.rows, torch.float32, "rstd"),
+        _like(dz, z, "dz"), _rng(rng, p if dbranch is not None else 0.0), _like(dx, z, "dx"),
+        _like(dbranch, z, "dbranch"), _vec(dweight, n, torch.float32, "dweight"),
+        _vec(dbias, n, torch.float32, "dbias"), w, wb, _stream()), "moe_layer_norm_backward")
+
+
+def dropout_add(x, y, p, rng, residual=None):
+    """y = residual + dropout(x) (or dropout(x)); on a gradient it is the
+    dropout's backward (same p and rng, no residual)."""
+    _check(lib().moe_dropout_add(x.numel(), _code(x, "x"), float(p), _rng(rng, p), _p(x),
+                                 _like(residual, x, "residual"), _like(y, x, "y"), _stream()),
+           "moe_dropout_add")
+
+
+# ----------------------------------------------------------------- 4-bit weights
+
+def w4_row_bytes(k):
+    """Bytes of one row's codes: blocks of 64 bytes for 128 inputs each."""
+    return -(-k // 128) * 64
+
+
+class W4Weight:
+    """A weight [..., N, K] in 4 bits (device tensors): codes uint8
+    [..., N, w4_row_bytes(K)], scales bf16 [..., N, K/group], zeros uint8 of the
+    scales' shape or None (8).  W = scales * (code - zeros)."""
+
+    def __init__(self, codes, scales, zeros=None, group=128, k=None):
+        k = scales.shape[-1] * group if k is None else k
+        if scales.dtype != torch.bfloat16 or codes.dtype != torch.uint8:
+            raise ValueError("codes must be uint8 and scales bfloat16")
+        if codes.shape[-1] != w4_row_bytes(k) or scales.shape[-1] * group != k \
+                or codes.shape[:-1] != scales.shape[:-1]:
+            raise ValueError("codes, scales, group and k do not fit together")
+        if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
+            raise ValueError("zeros must be uint8, of the scales' shape")
+        self.codes, self.scales, self.zeros, self.group, self.k = codes, scales, zeros, group, k
+        self.n = codes.shape[-2]
+        self._pointers = W4Pointers(_p(codes), _p(scales), _p(zeros))
+        self._ref = ctypes.byref(self._pointers)
+
+
+class W4Experts:
+    """The experts' three weights in 4 bits: W1, W3 [E,f,h], W2 [E,h,f]."""
+
+    def __init__(self, W1, W3, W2):
+        if not W1.group == W3.group == W2.group:
+            raise ValueError("the experts' weights must have one group size")
+        self.W1, self.W3, self.W2, self.group = W1, W3, W2, W1.group
+
+    def fits(self, cfg):
+        E, h, f = cfg.num_experts, cfg.hidden, cfg.ffn_hidden
+        for w, shape, k in ((self.W1, (E, f), h), (self.W3, (E, f), h), (self.W2, (E, h), f)):
+            if w.codes.shape[:-1] != shape or w.k != k:
+                raise ValueError("the 4-bit weights do not fit the configuration")
+
+
+def quantize_w4(W, group=128, zeros=False):
+    """W [..., K, N] bf16 (the layout of the layer's weights) -> W4Weight of
+    [..., N, K]; zeros=True: with zero points."""
+    if W.dtype != torch.bfloat16:
+        raise ValueError("W must be bfloat16")
+    K, N = W.shape[-2:]
+    lead = tuple(W.shape[:-2])
+    codes = torch.empty(lead + (N, w4_row_bytes(K)), dtype=torch.uint8, device=W.device)
+    if K % 128:
+        codes.zero_()  # the codes past K
+    scales = torch.empty(lead + (N, K // group), dtype=torch.bfloat16, device=W.device)
+    z = torch.empty(scales.shape, dtype=torch.uint8, device=W.device) if zeros else None
+    _check(lib().moe_quantize_w4(W.numel() // (K * N), K, N, group, _p(W), _p(codes), _p(scales),
+                                 _p(z), _stream()), "moe_quantize_w4")
+    return W4Weight(codes, scales, z, group=group, k=K)
+
+
+def quantize_experts_w4(W1, W3, W2, group=128, zeros=False):
+    """The layer's W1/W3 [E,h,f] and W2 [E,f,h] bf16 -> W4Experts."""
+    return W4Experts(*(quantize_w4(W, group, zeros) for W in (W1, W3, W2)))
+
+
+def pack_w4(values):
+    """Codes 0..15, one byte each [..., N, K] -> the codes of a W4Weight."""
+    if values.dtype != torch.uint8:
+        raise ValueError("values must be uint8")
+    N, K = values.shape[-2:]
+    codes = torch.empty(tuple(values.shape[:-1]) + (w4_row_bytes(K),), dtype=torch.uint8,
+                        device=values.device)
+    _check(lib().moe_pack_w4(values.numel() // (N * K), N, K, _p(values), _p(codes), _stream()),
+           "moe_pack_w4")
+    return codes
+
+
+def workspace_size_linear_w4(rows, w):
+    v = ctypes.c_size_t()
+    _check(lib().moe_workspace_size_linear_w4(int(rows), w.n, w.k, ctypes.byref(v)),
+           "moe_workspace_size_linear_w4")
+    return v.value
+
+
+def alloc_workspace_linear_w4(rows, w, device="cuda"):
+    return torch.zeros(workspace_size_linear_w4(rows, w), dtype=torch.uint8, device=device)
+
+
+def linear_w4(x, w, y, ws):
+    """y [..., N] (bf16 or fp32) = x [..., K] bf16 . W^T; w: W4Weight [N,K]."""
+    if x.dtype != torch.bfloat16 or x.shape[-1] != w.k or w.codes.dim() != 2:
+        raise ValueError("x must be bfloat16 [..., K] and W [N, K]")
+    if y.shape[:-1] != x.shape[:-1] or y.shape[-1] != w.n:
+        raise ValueError("y must be [..., N]")
+    b, wb = _ws(ws)
+    _check(lib().moe_linear_w4(x.numel() // w.k, w.n, w.k, w.group, _p(x), w._ref, _p(y),
+                               _code(y, "y"), b, wb, _stream()), "moe_linear_w4")
+
+
+def workspace_size_experts_w4(cfg):
+    v = ctypes.c_size_t()
+    _check(lib().moe_workspace_size_experts_w4(ctypes.byref(cfg), ctypes.byref(v)),
+           "moe_workspace_size_experts_w4")
+    return v.value
+
+
+def alloc_workspace_experts_w4(cfg, device="cuda"):
+    return torch.zeros(workspace_size_experts_w4(cfg), dtype=torch.uint8, device=device)
+
+
+def experts_w4(cfg, x, topk_idx, topk_prob, keep, q, y, ws):
+    """The routed SwiGLU experts of few tokens with 4-bit weights (q: W4Experts),
+    from the router's topk_idx, topk_prob and keep (or None), into y [T,h]."""
+    q.fits(cfg)
+    b, wb = _ws(ws)
+    _check(lib().moe_experts_w4(ctypes.byref(cfg), q.group, _p(x), _p(topk_idx), _p(topk_prob),
+                                _p(keep), q.W1._ref, q.W3._ref, q.W2._ref, _p(y), b, wb,
+                                _stream()), "moe_experts_w4")
+
+
+def workspace_size_w4(cfg):
+    v = ctypes.c_size_t()
+    _check(lib().moe_workspace_size_w4(ctypes.byref(cfg), ctypes.byref(v)),
+           "moe_workspace_size_w4")
+    return v.value
+
+
+def alloc_workspace_w4(cfg, device="cuda"):
+    return torch.zeros(workspace_size_w4(cfg), dtype=torch.uint8, device=device)
+
+
+def forward_w4(cfg, x, Wg, gate_bias, expert_bias, q, y, ws, topk_idx=None, topk_prob=None,
+               tokens_per_expert=None):
+    """The layer forward with 4-bit experts (q: W4Experts), for decoding."""
+    q.fits(cfg)
+    b, wb = _ws(ws)
+    _check(lib().moe_forward_w4(ctypes.byref(cfg), q.group, _p(x), _p(Wg), _p(gate_bias),
+                                _p(expert_bias), q.W1._ref, q.W3._ref, q.W2._ref, _p(y),
+                                _p(topk_idx), _p(topk_prob), _p(tokens_per_expert), b, wb,
+                                _stream()), "moe_forward_w4")
 
 
 def probe_fp32_fma(iters, out):

@@ -28,13 +28,19 @@ int device_sm_count() {
   return cache[dev];
 }
 
+thread_local char g_last_cuda_error[256] = "";
+
+moe_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s", cudaGetErrorString(e));
+  return MOE_ERR_CUDA;
+}
+
 }  // namespace moe
 
 namespace {
 
 using namespace moe;
-
-thread_local char g_last_cuda_error[256] = "";
 
 struct Layout {
   size_t err, logits, assigned, tiles, cand_rowmap, cand_src, cand_off, cand_tiles;
@@ -182,12 +188,6 @@ moe_status optional(const void* p, size_t align) {
     const moe_status st_ = (expr);             \
     if (st_ != MOE_OK) return st_;             \
   } while (0)
-
-moe_status cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return MOE_OK;
-  snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s", cudaGetErrorString(e));
-  return MOE_ERR_CUDA;
-}
 
 #define MOE_CUDA(expr) MOE_TRY(cuda_status(expr))
 

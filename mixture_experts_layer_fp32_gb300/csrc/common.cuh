@@ -277,6 +277,43 @@ cudaError_t launch_quantize_rows(int64_t rows, int cols, const void* in, uint8_t
 cudaError_t launch_quantize_cols(int E, int K, int N, const void* W, uint8_t* codes,
                                  float* scales, cudaStream_t s);
 
+// ---- norm, dropout (norm.cu) ----
+// As in moe.h; arguments checked by the caller.  weight, bias, residual, z,
+// mean, rstd, dz, dbranch, dweight, dbias are nullable as there.
+cudaError_t launch_norm(const moe_norm_config& c, const void* x, const void* residual,
+                        const uint64_t* rng, const void* weight, const void* bias, void* z,
+                        void* y, float* mean, float* rstd, cudaStream_t s);
+// part: norm_backward_ctas(c) x 2 x hidden floats
+int norm_backward_ctas(const moe_norm_config& c);
+cudaError_t launch_norm_backward(const moe_norm_config& c, const void* dy, const void* z,
+                                 const void* weight, const float* mean, const float* rstd,
+                                 const void* dz, const uint64_t* rng, void* dx, void* dbranch,
+                                 float* dweight, float* dbias, float* part, cudaStream_t s);
+cudaError_t launch_dropout_add(int64_t n, int dtype, double p, const uint64_t* rng, const void* x,
+                               const void* residual, void* y, cudaStream_t s);
+
+// ---- 4-bit weights (w4.cu, w4_pack.cu) ----
+struct W4 {  // moe_w4, typed
+  const uint8_t* codes;
+  const __nv_bfloat16* scales;
+  const uint8_t* zeros;
+};
+cudaError_t launch_w4_quantize(int E, int K, int N, int group, const void* W, uint8_t* codes,
+                               void* scales, uint8_t* zeros, cudaStream_t s);
+cudaError_t launch_w4_pack(int E, int N, int K, const uint8_t* values, uint8_t* codes,
+                           cudaStream_t s);
+// bytes of scratch, and the product of `rows` rows
+size_t w4_linear_scratch(int64_t rows, int N, int K);
+cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* x, const W4& W,
+                             void* y, int y_dtype, void* scratch, cudaStream_t s);
+size_t w4_experts_scratch(int T, int h, int E, int k, int f);
+cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, const void* x,
+                              const int32_t* topk_idx, const float* topk_prob,
+                              const uint8_t* keep, const W4& W1, const W4& W3, const W4& W2,
+                              void* y, void* scratch, int* err, cudaStream_t s);
+
 int device_sm_count();
+// keeps the text for moe_last_cuda_error() and returns the status
+moe_status cuda_status(cudaError_t e);
 
 }  // namespace moe
