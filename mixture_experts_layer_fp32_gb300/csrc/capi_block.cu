@@ -47,8 +47,14 @@ moe_status validate(const moe_norm_config* c) {
   return MOE_OK;
 }
 
+// One size for both types of a tensor, so that a workspace serves either.
 size_t norm_backward_bytes(const moe_norm_config& c) {
-  return kErrBytes + static_cast<size_t>(norm_backward_ctas(c)) * 2 * c.hidden * 4;
+  moe_norm_config d = c;
+  d.dtype = MOE_F32;
+  const int wide = norm_backward_ctas(d);
+  d.dtype = MOE_BF16;
+  const int narrow = norm_backward_ctas(d);
+  return kErrBytes + static_cast<size_t>(wide > narrow ? wide : narrow) * 2 * c.hidden * 4;
 }
 
 bool is_group(int32_t g) { return g == 32 || g == 64 || g == 128; }

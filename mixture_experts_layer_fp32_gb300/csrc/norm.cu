@@ -1,6 +1,8 @@
 // Layer norm and RMS norm of z = residual + dropout(x), their backward pass
 // with the reduction of the parameters' gradients, and the dropout with the
 // residual sum on its own.
+#include <type_traits>
+
 #include "common.cuh"
 #include "philox.cuh"
 
@@ -55,8 +57,11 @@ __device__ __forceinline__ float2 block_sum(float a, float b, float2* red) {
   return t;
 }
 
-// One block to a row, any width: the row is read once for the mean, once for
-// the variance and once for the output.
+// ---- rows of any width ----
+//
+// One block to a row, for widths past what the kernels below hold on the chip:
+// the row is read once for the mean, once for the variance and once for the
+// output.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads)
     norm_wide_kernel(NormArgs a, const T* x, const T* res, const void* weight, const void* bias,
@@ -138,29 +143,464 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// dweight and dbias: the sums over the blocks' parts, in their order
-__global__ void norm_param_grads_kernel(int parts, int H, const float* part, float* dweight,
-                                        float* dbias) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= H) return;
-  float w = 0.f, b = 0.f;
-  for (int p = 0; p < parts; ++p) {
-    w += part[static_cast<int64_t>(p) * 2 * H + c];
-    b += part[static_cast<int64_t>(p) * 2 * H + H + c];
-  }
-  if (dweight) dweight[c] = w;
-  if (dbias) dbias[c] = b;
-}
+// ---- rows that stay on the chip ----
+//
+// A row belongs to a group of warps that holds it in registers, VPT vectors of
+// 16 bytes to a thread, from the first read to the last write, so every tensor
+// moves once.  Vectors are cut from the whole tensor and not from the row:
+// they are 16-byte aligned for every width, and a row of odd width starts and
+// ends inside one.  Such an edge vector is read and written element by element.
+// Which elements of a vector a column falls on (the row's phase) depends on
+// the row number modulo the vector length; a block takes the rows of one
+// residue, so its phase is fixed, its copy of the weights in shared memory is
+// laid out for it, and in the backward pass a thread keeps the same columns.
 
 template <typename T>
-__global__ void dropout_add_kernel(int64_t n, Dropout d, const uint64_t* rng, const T* x,
-                                   const T* res, T* y) {
-  const Philox g = d.on ? philox_of(rng) : Philox{};
+struct Lanes {
+  static constexpr int V = 16 / static_cast<int>(sizeof(T));
+};
+
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[4], const float*) {
+  v[0] = __uint_as_float(q.x);
+  v[1] = __uint_as_float(q.y);
+  v[2] = __uint_as_float(q.z);
+  v[3] = __uint_as_float(q.w);
+}
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[8], const __nv_bfloat16*) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[4], const float*) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                    __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[8], const __nv_bfloat16*) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The elements of an edge vector that lie in the row, one by one; loops that
+// stay loops: an edge is one thread's in a row.
+__device__ __forceinline__ uint32_t bits_of(const float* p) { return __float_as_uint(*p); }
+__device__ __forceinline__ uint32_t bits_of(const __nv_bfloat16* p) {
+  return __bfloat16_as_ushort(*p);
+}
+__device__ __forceinline__ void put_bits(float* p, uint32_t b) { *p = __uint_as_float(b); }
+__device__ __forceinline__ void put_bits(__nv_bfloat16* p, uint32_t b) {
+  *p = __ushort_as_bfloat16(static_cast<unsigned short>(b));
+}
+template <typename T>
+__device__ __forceinline__ uint4 load_edge(const T* row, int col, int H) {
+  constexpr int V = Lanes<T>::V, B = 32 * 4 / V;  // bits of an element
+  uint4 q = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int e = 0; e < V; ++e) {
+    if (col + e < 0 || col + e >= H) continue;
+    const uint32_t b = bits_of(row + col + e) << (e * B % 32);
+    const int w = e * B / 32;
+    q.x |= w == 0 ? b : 0;
+    q.y |= w == 1 ? b : 0;
+    q.z |= w == 2 ? b : 0;
+    q.w |= w == 3 ? b : 0;
+  }
+  return q;
+}
+template <typename T>
+__device__ __forceinline__ void store_edge(T* row, int col, int H, uint4 q) {
+  constexpr int V = Lanes<T>::V, B = 32 * 4 / V;
+#pragma unroll 1
+  for (int e = 0; e < V; ++e) {
+    const int w = e * B / 32;
+    const uint32_t b = w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w;
+    if (col + e >= 0 && col + e < H) put_bits(row + col + e, b >> (e * B % 32));
+  }
+}
+
+// The vector whose first element is column `col` of `row` (col may be negative
+// or past the row in an edge vector); zeros outside of the row.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ uint4 load_vec(const T* row, int col, int H) {
+  constexpr int V = Lanes<T>::V;
+  if (col >= H) return make_uint4(0, 0, 0, 0);
+  if (ALIGNED || (col >= 0 && col + V <= H)) return *reinterpret_cast<const uint4*>(row + col);
+  return load_edge(row, col, H);
+}
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void store_vec(T* row, int col, int H,
+                                          const float (&v)[Lanes<T>::V]) {
+  constexpr int V = Lanes<T>::V;
+  if (col >= H) return;
+  const uint4 q = pack(v, static_cast<const T*>(row));
+  if (ALIGNED || (col >= 0 && col + V <= H)) *reinterpret_cast<uint4*>(row + col) = q;
+  else store_edge(row, col, H, q);
+}
+
+// dropout of the vector of flat elements first .. first + V - 1 (first % V == 0)
+template <int V>
+__device__ __forceinline__ void drop_vec(const Dropout& d, const Philox& g, int64_t first,
+                                         float (&v)[V]) {
+#pragma unroll
+  for (int b = 0; b < V / 4; ++b) {
+    const uint4 w = philox_words(g, (static_cast<uint64_t>(first) >> 2) + b);
+    v[4 * b] = w.x > d.limit ? v[4 * b] * d.scale : 0.f;
+    v[4 * b + 1] = w.y > d.limit ? v[4 * b + 1] * d.scale : 0.f;
+    v[4 * b + 2] = w.z > d.limit ? v[4 * b + 2] * d.scale : 0.f;
+    v[4 * b + 3] = w.w > d.limit ? v[4 * b + 3] * d.scale : 0.f;
+  }
+}
+
+// The row group of a thread.  group_warps warps hold one row; the groups of a
+// block take rows of the block's residue in turn.
+template <typename T, bool ALIGNED>
+struct Group {
+  int size, id, t, phase;
+  int64_t row, step;
+  __device__ Group(int group_warps, int H) {
+    constexpr int V = Lanes<T>::V;
+    size = group_warps * 32;
+    id = threadIdx.x / size;
+    t = threadIdx.x - id * size;
+    const int groups = blockDim.x / size;
+    step = static_cast<int64_t>(gridDim.x) * groups;
+    if (ALIGNED) {
+      phase = 0;
+      row = static_cast<int64_t>(blockIdx.x) * groups + id;
+    } else {  // gridDim.x is a multiple of V
+      const int residue = blockIdx.x % V;
+      phase = (residue * (H % V)) % V;
+      row = residue + static_cast<int64_t>(V) * ((blockIdx.x / V) * groups + id);
+    }
+  }
+  // first column of the thread's i-th vector
+  __device__ int col(int i) const { return (i * size + t) * Lanes<T>::V - phase; }
+};
+
+// Sum over the group's threads in a fixed order, in every thread.  red:
+// 2 x 32 float2; calls alternate between its halves, which makes one barrier
+// a call enough.
+struct GroupSum {
+  float2* red;
+  int warps, base, half;
+  __device__ GroupSum(float2* smem, int group_warps, int group)
+      : red(smem), warps(group_warps), base(group * group_warps), half(0) {}
+  __device__ float2 operator()(float2 v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(~0u, v.x, o);
+      v.y += __shfl_xor_sync(~0u, v.y, o);
+    }
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31;
+    float2* buf = red + half * 32;
+    half ^= 1;
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
+    // one barrier to a group of warps: they keep different rows
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + base / warps), "r"(warps * 32) : "memory");
+    v = lane < warps ? buf[base + lane] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(~0u, v.x, o);
+      v.y += __shfl_xor_sync(~0u, v.y, o);
+    }
+    return v;
+  }
+  __device__ float operator()(float v) { return (*this)(make_float2(v, 0.f)).x; }
+};
+
+// a parameter's values at phase + column, zeros around them
+__device__ __forceinline__ void stage_param(float* dst, const void* p, int is_bf16, float none,
+                                            int phase, int H, int padded) {
+  for (int c = threadIdx.x; c < padded; c += blockDim.x) {
+    const int col = c - phase;
+    float v = 0.f;
+    if (col >= 0 && col < H) v = p ? param1(p, is_bf16, col) : none;
+    dst[c] = v;
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void read_param(const float* src, int at, float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const float4 q = *reinterpret_cast<const float4*>(src + at + 4 * i);
+    v[4 * i] = q.x;
+    v[4 * i + 1] = q.y;
+    v[4 * i + 2] = q.z;
+    v[4 * i + 3] = q.w;
+  }
+}
+
+template <typename T, int VPT, bool ALIGNED, bool DROP>
+__global__ void __launch_bounds__(1024)
+    norm_rows_kernel(NormArgs a, int group_warps, int padded, const T* x, const T* res,
+                     const void* weight, const void* bias, T* z, T* y, float* mean, float* rstd) {
+  constexpr int V = Lanes<T>::V;
+  extern __shared__ __align__(16) float params[];  // weight, bias: `padded` each
+  __shared__ float2 red[64];
+  const int H = a.hidden;
+  const Group<T, ALIGNED> g(group_warps, H);
+  GroupSum sum(red, group_warps, g.id);
+  const Philox rng = DROP ? philox_of(a.rng) : Philox{};
+  const float inv_h = 1.f / static_cast<float>(H);
+
+  uint4 qx[VPT], qr[VPT];
+  auto fetch = [&](int64_t r) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      qx[i] = load_vec<T, ALIGNED>(x + r * H, g.col(i), H);
+      if (res) qr[i] = load_vec<T, ALIGNED>(res + r * H, g.col(i), H);
+    }
+  };
+  // one row ahead where the registers allow it
+  constexpr bool AHEAD = VPT <= 2;
+  if (AHEAD && g.row < a.rows) fetch(g.row);
+  stage_param(params, weight, a.param_bf16, 1.f, g.phase, H, padded);
+  stage_param(params + padded, bias, a.param_bf16, 0.f, g.phase, H, padded);
+  __syncthreads();
+
+  for (int64_t r = g.row; r < a.rows; r += g.step) {
+    float v[VPT][V];
+    if (!AHEAD) fetch(r);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      unpack(qx[i], v[i], x);
+      if (DROP) drop_vec<V>(a.drop, rng, r * H + g.col(i), v[i]);
+      if (res) {
+        float w[V];
+        unpack(qr[i], w, x);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[i][e] += w[e];
+      }
+    }
+    // the next row's reads run under this row's sums
+    if (AHEAD && r + g.step < a.rows) fetch(r + g.step);
+    float m = 0.f;
+    if (!a.rms) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s += v[i][e];
+      m = sum(s) * inv_h;
+    }
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = g.col(i);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = v[i][e] - m;
+        const bool in = ALIGNED ? c < H : c + e >= 0 && c + e < H;
+        sq += in ? d * d : 0.f;
+      }
+    }
+    const float rs = 1.f / sqrtf(sum(sq) * inv_h + a.eps);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = g.col(i);
+      if (c >= H) continue;
+      if (z) store_vec<T, ALIGNED>(z + r * H, c, H, v[i]);
+      float w[V], b[V];
+      read_param<V>(params, c + g.phase, w);
+      read_param<V>(params + padded, c + g.phase, b);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[i][e] = (v[i][e] - m) * rs * w[e] + b[e];
+      store_vec<T, ALIGNED>(y + r * H, c, H, v[i]);
+    }
+    if (g.t == 0) {
+      if (mean && !a.rms) mean[r] = m;
+      if (rstd) rstd[r] = rs;
+    }
+  }
+}
+
+// The sums for dweight and dbias stay in the thread's registers over all of its
+// rows (in shared memory, SUMS_SMEM, where a row is too wide for that), are
+// added up over the block's groups in order, and go to the block's part.
+template <typename T, int VPT, bool ALIGNED, bool DROP, bool SUMS_SMEM>
+__global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
+    norm_backward_rows_kernel(NormArgs a, int group_warps, int padded, const T* dy, const T* x,
+                              const void* weight, const float* mean, const float* rstd,
+                              const T* dz, T* dx, T* dbranch, float* part) {
+  constexpr int V = Lanes<T>::V;
+  // weight [padded]; the two sums [padded] each, behind it (SUMS_SMEM) or,
+  // after the last row, in its place
+  extern __shared__ __align__(16) float params[];
+  __shared__ float2 red[64];
+  const int H = a.hidden;
+  const Group<T, ALIGNED> g(group_warps, H);
+  GroupSum sum(red, group_warps, g.id);
+  const Philox rng = DROP ? philox_of(a.rng) : Philox{};
+  const float inv_h = 1.f / static_cast<float>(H);
+  constexpr int S = SUMS_SMEM ? 1 : VPT;
+  float sw[S][V], sb[S][V];
+  float* sums = SUMS_SMEM ? params + padded : params;
+  stage_param(params, weight, a.param_bf16, 1.f, g.phase, H, padded);
+  if (SUMS_SMEM)
+    for (int c = threadIdx.x; c < 2 * padded; c += blockDim.x) sums[c] = 0.f;
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int e = 0; e < V; ++e) sw[i][e] = sb[i][e] = 0.f;
+  __syncthreads();
+
+  for (int64_t r = g.row; r < a.rows; r += g.step) {
+    uint4 qx[VPT], qd[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      qx[i] = load_vec<T, ALIGNED>(x + r * H, g.col(i), H);
+      qd[i] = load_vec<T, ALIGNED>(dy + r * H, g.col(i), H);
+    }
+    const float m = a.rms ? 0.f : mean[r], rs = rstd[r];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = g.col(i);
+      if (c >= H) continue;
+      float vx[V], vd[V], w[V];
+      unpack(qx[i], vx, x);
+      unpack(qd[i], vd, x);
+      read_param<V>(params, c + g.phase, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float gw = vd[e] * w[e];
+        s.x += gw;
+        s.y += gw * ((vx[e] - m) * rs);
+      }
+    }
+    s = sum(s);
+    const float c1 = a.rms ? 0.f : s.x * inv_h, c2 = s.y * inv_h;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = g.col(i);
+      if (c >= H) continue;
+      float vx[V], vd[V], w[V], o[V];
+      unpack(qx[i], vx, x);
+      unpack(qd[i], vd, x);
+      read_param<V>(params, c + g.phase, w);
+      if (dz) {
+        unpack(load_vec<T, ALIGNED>(dz + r * H, c, H), o, x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = 0.f;
+      }
+      float tw[V], tb[V];
+      if (SUMS_SMEM) {
+        read_param<V>(sums, c + g.phase, tw);
+        read_param<V>(sums + padded, c + g.phase, tb);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float xh = (vx[e] - m) * rs;
+        o[e] += rs * (vd[e] * w[e] - c1 - xh * c2);
+        if (SUMS_SMEM) {
+          tw[e] += vd[e] * xh;
+          tb[e] += vd[e];
+        } else {
+          sw[i][e] += vd[e] * xh;
+          sb[i][e] += vd[e];
+        }
+      }
+      if (SUMS_SMEM) {
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+          *reinterpret_cast<float4*>(sums + c + g.phase + e) =
+              make_float4(tw[e], tw[e + 1], tw[e + 2], tw[e + 3]);
+          *reinterpret_cast<float4*>(sums + padded + c + g.phase + e) =
+              make_float4(tb[e], tb[e + 1], tb[e + 2], tb[e + 3]);
+        }
+      }
+      store_vec<T, ALIGNED>(dx + r * H, c, H, o);
+      if (dbranch) {
+        if (DROP) drop_vec<V>(a.drop, rng, r * H + c, o);
+        store_vec<T, ALIGNED>(dbranch + r * H, c, H, o);
+      }
+    }
+  }
+
+  __syncthreads();
+  if (!SUMS_SMEM) {
+    const int groups = blockDim.x / g.size;
+    for (int k = 0; k < groups; ++k) {
+      if (g.id == k) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const int at = g.col(i) + g.phase;
+          if (at >= padded) continue;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            sums[at + e] = k == 0 ? sw[i][e] : sums[at + e] + sw[i][e];
+            sums[padded + at + e] = k == 0 ? sb[i][e] : sums[padded + at + e] + sb[i][e];
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * H;
+  for (int c = threadIdx.x; c < H; c += blockDim.x) {
+    out[c] = sums[c + g.phase];
+    out[H + c] = sums[padded + c + g.phase];
+  }
+}
+
+// dweight and dbias: the sums over the blocks' parts, in a fixed order.  One
+// block to 32 columns of one of the two; warp w takes the parts w, w + 16, ...
+constexpr int kGradWarps = 16;
+__global__ void __launch_bounds__(kGradWarps * 32)
+    norm_param_grads_kernel(int parts, int H, const float* part, float* dweight, float* dbias) {
+  __shared__ float buf[kGradWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float* out = blockIdx.y == 0 ? dweight : dbias;
+  pdl_wait();
+  float s = 0.f;
+  if (c < H && out) {
+    const float* p = part + static_cast<int64_t>(blockIdx.y) * H + c;
+#pragma unroll 8
+    for (int i = warp; i < parts; i += kGradWarps) s += p[static_cast<int64_t>(i) * 2 * H];
+  }
+  buf[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < H && out) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kGradWarps; ++w) s += buf[w][lane];
+    out[c] = s;
+  }
+}
+
+// Flat vectors of 16 bytes; the last elements of a length that is no multiple
+// one by one.
+template <typename T, bool DROP>
+__global__ void __launch_bounds__(256)
+    dropout_add_kernel(int64_t n, Dropout d, const uint64_t* rng, const T* x, const T* res, T* y) {
+  constexpr int V = Lanes<T>::V;
+  const Philox g = DROP ? philox_of(rng) : Philox{};
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
-    float v = load1(x, i);
-    if (d.on) v = drop1(d, g, i, v);
-    store1(y, i, res ? load1(res, i) + v : v);
+  const int64_t vecs = (n + V - 1) / V;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < vecs;
+       q += step) {
+    const int64_t first = q * V;
+    const int left = n - first < V ? static_cast<int>(n - first) : V;
+    float v[V], w[V];
+    unpack(load_vec<T, false>(x + first, 0, left), v, x);
+    if (res) unpack(load_vec<T, false>(res + first, 0, left), w, x);
+    if (DROP) drop_vec<V>(d, g, first, v);
+    if (res) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] += w[e];
+    }
+    store_vec<T, false>(y + first, 0, left, v);
   }
 }
 
@@ -176,14 +616,139 @@ NormArgs args_of(const moe_norm_config& c, const uint64_t* rng) {
   return a;
 }
 
+constexpr int kSms = 152;
+constexpr int kMostSmem = 216 * 1024;
+
+// How rows are laid over threads.  vectors: 16-byte vectors that a row can
+// touch; group_warps warps x vpt vectors hold them.
+struct Shape {
+  int vpt = 0;  // 0: too wide for the chip, the wide kernel
+  int group_warps = 0, groups = 1, padded = 0, threads = 0;
+  bool aligned = true, sums_smem = false;
+  unsigned grid = 0;
+};
+
+void shape_common(Shape& s, const moe_norm_config& c, int vectors, int V, int per_sm) {
+  s.group_warps = (vectors + s.vpt * 32 - 1) / (s.vpt * 32);
+  s.groups = s.group_warps >= 8 ? 1 : 8 / s.group_warps;
+  if (c.rows < static_cast<int64_t>(kSms) * s.groups) s.groups = 1;
+  s.threads = s.group_warps * s.groups * 32;
+  s.padded = s.group_warps * 32 * s.vpt * V;
+  const int64_t most = static_cast<int64_t>(kSms) * per_sm;
+  int64_t grid = (c.rows + s.groups - 1) / s.groups;
+  if (!s.aligned) {  // whole sets of residues
+    const int64_t each = ((c.rows + V - 1) / V + s.groups - 1) / s.groups;
+    grid = each * V;
+    s.grid = static_cast<unsigned>(grid < most ? grid : most / V * V);
+  } else {
+    s.grid = static_cast<unsigned>(grid < most ? grid : most);
+  }
+}
+
+int row_vectors(const moe_norm_config& c, int V) {
+  return c.hidden % V == 0 ? c.hidden / V : c.hidden / V + 2;
+}
+
+Shape forward_shape(const moe_norm_config& c) {
+  Shape s;
+  const int V = c.dtype == MOE_F32 ? 4 : 8;
+  if (c.hidden > 32768) return s;
+  const int vectors = row_vectors(c, V);
+  s.aligned = c.hidden % V == 0;
+  if (vectors <= 32 || (c.rows <= kSms && vectors <= 1024)) s.vpt = 1;
+  else if (vectors <= 2048) s.vpt = 2;
+  else if (V == 8 && vectors <= 3072) s.vpt = 3;
+  else if (V == 4 && vectors <= 4096) s.vpt = 4;
+  else if (V == 4 && vectors <= 5120) s.vpt = 5;
+  else return s;
+  const int warps = (vectors + s.vpt * 32 - 1) / (s.vpt * 32);
+  const int smem = 2 * warps * 32 * s.vpt * V * 4;
+  const int threads = warps >= 8 ? warps * 32 : 256;
+  int per_sm = 1024 / threads;
+  if (per_sm > kMostSmem / smem) per_sm = kMostSmem / smem;
+  shape_common(s, c, vectors, V, per_sm < 1 ? 1 : per_sm);
+  return s;
+}
+
+Shape backward_shape(const moe_norm_config& c) {
+  Shape s;
+  const int V = c.dtype == MOE_F32 ? 4 : 8;
+  if (c.hidden > 32768) return s;
+  const int vectors = row_vectors(c, V);
+  s.aligned = c.hidden % V == 0;
+  int most_warps = 16;
+  if (vectors <= 32) s.vpt = 1;
+  else if (vectors <= 2 * 32 * 16) s.vpt = 2;
+  else if (V == 4 && vectors <= 4 * 32 * 16) s.vpt = 4;
+  else {
+    s.sums_smem = true;
+    most_warps = 20;
+    s.vpt = V == 4 ? 8 : 4;
+    if (vectors > s.vpt * 32 * most_warps) s.vpt = 0;
+  }
+  if (s.vpt == 0) return s;
+  const int warps = (vectors + s.vpt * 32 - 1) / (s.vpt * 32);
+  const int smem = (s.sums_smem ? 3 : 2) * warps * 32 * s.vpt * V * 4;
+  if (smem > kMostSmem) {
+    s.vpt = 0;
+    return s;
+  }
+  const int threads = warps >= 8 ? warps * 32 : 256;
+  int per_sm = 512 / threads;
+  if (per_sm > kMostSmem / smem) per_sm = kMostSmem / smem;
+  shape_common(s, c, vectors, V, per_sm < 1 ? 1 : per_sm);
+  return s;
+}
+
+// f with the values of the flags as types
+template <typename F>
+auto with_bool(bool b, F&& f) {
+  return b ? f(std::true_type{}) : f(std::false_type{});
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes));
+}
+
 template <typename T>
 cudaError_t norm_typed(const moe_norm_config& c, const void* x, const void* residual,
                        const uint64_t* rng, const void* weight, const void* bias, void* z, void* y,
                        float* mean, float* rstd, cudaStream_t s) {
+  const NormArgs a = args_of(c, rng);
+  const T *xt = static_cast<const T*>(x), *rt = static_cast<const T*>(residual);
+  T *zt = static_cast<T*>(z), *yt = static_cast<T*>(y);
+  const Shape p = forward_shape(c);
+  auto launch = [&](auto vpt) -> cudaError_t {
+    return with_bool(p.aligned, [&](auto aligned) {
+      return with_bool(a.drop.on, [&](auto drop) -> cudaError_t {
+        auto k = norm_rows_kernel<T, decltype(vpt)::value, decltype(aligned)::value,
+                                  decltype(drop)::value>;
+        const size_t smem = 2 * static_cast<size_t>(p.padded) * 4;
+        const cudaError_t st = allow_smem(k, smem);
+        if (st != cudaSuccess) return st;
+        k<<<p.grid, p.threads, smem, s>>>(a, p.group_warps, p.padded, xt, rt, weight, bias, zt, yt,
+                                          mean, rstd);
+        return cudaGetLastError();
+      });
+    });
+  };
+  switch (p.vpt) {
+    case 1: return launch(std::integral_constant<int, 1>{});
+    case 2: return launch(std::integral_constant<int, 2>{});
+    case 3:
+      if constexpr (sizeof(T) == 2) return launch(std::integral_constant<int, 3>{});
+      break;
+    case 4:
+      if constexpr (sizeof(T) == 4) return launch(std::integral_constant<int, 4>{});
+      break;
+    case 5:
+      if constexpr (sizeof(T) == 4) return launch(std::integral_constant<int, 5>{});
+  }
   const unsigned grid = static_cast<unsigned>(c.rows < 65536 ? c.rows : 65536);
-  norm_wide_kernel<T><<<grid, kRowThreads, 0, s>>>(
-      args_of(c, rng), static_cast<const T*>(x), static_cast<const T*>(residual), weight, bias,
-      static_cast<T*>(z), static_cast<T*>(y), mean, rstd);
+  norm_wide_kernel<T><<<grid, kRowThreads, 0, s>>>(a, xt, rt, weight, bias, zt, yt, mean, rstd);
   return cudaGetLastError();
 }
 
@@ -194,17 +759,45 @@ cudaError_t norm_backward_typed(const moe_norm_config& c, const void* dy, const 
                                 float* part, cudaStream_t s) {
   NormArgs a = args_of(c, rng);
   if (dbranch == nullptr) a.drop.on = 0;
+  const T *dyt = static_cast<const T*>(dy), *zt = static_cast<const T*>(z),
+          *dzt = static_cast<const T*>(dz);
+  T *dxt = static_cast<T*>(dx), *dbt = static_cast<T*>(dbranch);
+  const Shape p = backward_shape(c);
+  auto launch = [&](auto vpt, auto sums_smem) -> cudaError_t {
+    return with_bool(p.aligned, [&](auto aligned) {
+      return with_bool(a.drop.on, [&](auto drop) -> cudaError_t {
+        auto k = norm_backward_rows_kernel<T, decltype(vpt)::value, decltype(aligned)::value,
+                                           decltype(drop)::value, decltype(sums_smem)::value>;
+        const size_t smem = (p.sums_smem ? 3 : 2) * static_cast<size_t>(p.padded) * 4;
+        const cudaError_t st = allow_smem(k, smem);
+        if (st != cudaSuccess) return st;
+        k<<<p.grid, p.threads, smem, s>>>(a, p.group_warps, p.padded, dyt, zt, weight, mean, rstd,
+                                          dzt, dxt, dbt, part);
+        return cudaGetLastError();
+      });
+    });
+  };
+  if (p.vpt != 0 && p.sums_smem)
+    return launch(std::integral_constant<int, sizeof(T) == 4 ? 8 : 4>{}, std::true_type{});
+  switch (p.vpt) {
+    case 1: return launch(std::integral_constant<int, 1>{}, std::false_type{});
+    case 2: return launch(std::integral_constant<int, 2>{}, std::false_type{});
+    case 4:
+      if constexpr (sizeof(T) == 4)
+        return launch(std::integral_constant<int, 4>{}, std::false_type{});
+  }
   norm_backward_wide_kernel<T><<<norm_backward_ctas(c), kRowThreads, 0, s>>>(
-      a, static_cast<const T*>(dy), static_cast<const T*>(z), weight, mean, rstd,
-      static_cast<const T*>(dz), static_cast<T*>(dx), static_cast<T*>(dbranch), part);
+      a, dyt, zt, weight, mean, rstd, dzt, dxt, dbt, part);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 int norm_backward_ctas(const moe_norm_config& c) {
-  constexpr int kMost = 608;
-  return static_cast<int>(c.rows < kMost ? c.rows : kMost);
+  if (c.rows == 0) return 0;
+  const Shape p = backward_shape(c);
+  if (p.vpt != 0) return static_cast<int>(p.grid);
+  return static_cast<int>(c.rows < 4 * kSms ? c.rows : 4 * kSms);
 }
 
 cudaError_t launch_norm(const moe_norm_config& c, const void* x, const void* residual,
@@ -230,8 +823,19 @@ cudaError_t launch_norm_backward(const moe_norm_config& c, const void* dy, const
     if (st != cudaSuccess) return st;
   }
   if (!dweight && !dbias) return cudaSuccess;
-  norm_param_grads_kernel<<<(c.hidden + 255) / 256, 256, 0, s>>>(norm_backward_ctas(c), c.hidden,
-                                                                 part, dweight, dbias);
+  return launch_dependent(norm_param_grads_kernel, dim3((c.hidden + 31) / 32, 2),
+                          dim3(kGradWarps * 32), 0, s, norm_backward_ctas(c), c.hidden,
+                          static_cast<const float*>(part), dweight, dbias);
+}
+
+template <typename T>
+cudaError_t dropout_add_typed(int64_t n, const Dropout& d, const uint64_t* rng, const void* x,
+                              const void* residual, void* y, cudaStream_t s) {
+  const int64_t blocks = (n / Lanes<T>::V + 256) / 256;
+  const unsigned grid = static_cast<unsigned>(blocks < kSms * 8 ? blocks : kSms * 8);
+  auto k = d.on ? dropout_add_kernel<T, true> : dropout_add_kernel<T, false>;
+  k<<<grid, 256, 0, s>>>(n, d, rng, static_cast<const T*>(x), static_cast<const T*>(residual),
+                         static_cast<T*>(y));
   return cudaGetLastError();
 }
 
@@ -239,17 +843,8 @@ cudaError_t launch_dropout_add(int64_t n, int dtype, double p, const uint64_t* r
                                const void* residual, void* y, cudaStream_t s) {
   if (n == 0) return cudaSuccess;
   const Dropout d = dropout_of(p);
-  const int64_t blocks = (n + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(blocks < 8192 ? blocks : 8192);
-  if (dtype == MOE_F32)
-    dropout_add_kernel<float><<<grid, 256, 0, s>>>(n, d, rng, static_cast<const float*>(x),
-                                                   static_cast<const float*>(residual),
-                                                   static_cast<float*>(y));
-  else
-    dropout_add_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
-        n, d, rng, static_cast<const __nv_bfloat16*>(x),
-        static_cast<const __nv_bfloat16*>(residual), static_cast<__nv_bfloat16*>(y));
-  return cudaGetLastError();
+  return dtype == MOE_F32 ? dropout_add_typed<float>(n, d, rng, x, residual, y, s)
+                          : dropout_add_typed<__nv_bfloat16>(n, d, rng, x, residual, y, s);
 }
 
 }  // namespace moe
