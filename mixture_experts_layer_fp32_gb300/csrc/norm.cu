@@ -31,7 +31,10 @@ struct NormArgs {
 };
 
 __device__ __forceinline__ float drop1(const Dropout& d, const Philox& g, int64_t i, float v) {
-  const uint4 w = philox_words(g, static_cast<uint64_t>(i) >> 2);
+  const uint64_t ctr[1] = {static_cast<uint64_t>(i) >> 2};
+  uint4 words[1];
+  philox_words(g, ctr, words);
+  const uint4 w = words[0];
   const uint32_t j = static_cast<uint32_t>(i) & 3;
   const uint32_t u = j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
   return u > d.limit ? v * d.scale : 0.f;
@@ -160,29 +163,54 @@ struct Lanes {
   static constexpr int V = 16 / static_cast<int>(sizeof(T));
 };
 
-__device__ __forceinline__ void unpack(const uint4& q, float (&v)[4], const float*) {
-  v[0] = __uint_as_float(q.x);
-  v[1] = __uint_as_float(q.y);
-  v[2] = __uint_as_float(q.z);
-  v[3] = __uint_as_float(q.w);
+// Two fp32 values in one instruction: the rows' arithmetic is bound by
+// instructions issued, not by the fp32 units.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; "
+      "mov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
-__device__ __forceinline__ void unpack(const uint4& q, float (&v)[8], const __nv_bfloat16*) {
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; "
+      "mov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; "
+      "fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// a vector's values, in pairs
+__device__ __forceinline__ void unpack(const uint4& q, float2 (&v)[2], const float*) {
+  v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+  v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+}
+__device__ __forceinline__ void unpack(const uint4& q, float2 (&v)[4], const __nv_bfloat16*) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[4], const float*) {
-  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                    __float_as_uint(v[3]));
+__device__ __forceinline__ uint4 pack(const float2 (&v)[2], const float*) {
+  return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                    __float_as_uint(v[1].y));
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[8], const __nv_bfloat16*) {
+__device__ __forceinline__ uint4 pack(const float2 (&v)[4], const __nv_bfloat16*) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    const __nv_bfloat162 b = __float22bfloat162_rn(v[i]);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -236,7 +264,7 @@ __device__ __forceinline__ uint4 load_vec(const T* row, int col, int H) {
 }
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ void store_vec(T* row, int col, int H,
-                                          const float (&v)[Lanes<T>::V]) {
+                                          const float2 (&v)[Lanes<T>::V / 2]) {
   constexpr int V = Lanes<T>::V;
   if (col >= H) return;
   const uint4 q = pack(v, static_cast<const T*>(row));
@@ -244,17 +272,26 @@ __device__ __forceinline__ void store_vec(T* row, int col, int H,
   else store_edge(row, col, H, q);
 }
 
-// dropout of the vector of flat elements first .. first + V - 1 (first % V == 0)
-template <int V>
-__device__ __forceinline__ void drop_vec(const Dropout& d, const Philox& g, int64_t first,
-                                         float (&v)[V]) {
+// dropout of N vectors; vector n holds the flat elements first[n] .. first[n] + V - 1,
+// first[n] % V == 0
+template <int V, int N>
+__device__ __forceinline__ void drop_vecs(const Dropout& d, const Philox& g,
+                                          const int64_t (&first)[N], float2 (&v)[N][V / 2]) {
+  constexpr int B = V / 4;  // generator blocks of a vector
+  uint64_t ctr[N * B];
+  uint4 w[N * B];
 #pragma unroll
-  for (int b = 0; b < V / 4; ++b) {
-    const uint4 w = philox_words(g, (static_cast<uint64_t>(first) >> 2) + b);
-    v[4 * b] = w.x > d.limit ? v[4 * b] * d.scale : 0.f;
-    v[4 * b + 1] = w.y > d.limit ? v[4 * b + 1] * d.scale : 0.f;
-    v[4 * b + 2] = w.z > d.limit ? v[4 * b + 2] * d.scale : 0.f;
-    v[4 * b + 3] = w.w > d.limit ? v[4 * b + 3] * d.scale : 0.f;
+  for (int n = 0; n < N * B; ++n) ctr[n] = (static_cast<uint64_t>(first[n / B]) >> 2) + n % B;
+  philox_words(g, ctr, w);
+#pragma unroll
+  for (int n = 0; n < N * B; ++n) {
+    float2 &lo = v[n / B][n % B * 2], &hi = v[n / B][n % B * 2 + 1];
+    lo = mul2(lo, both(d.scale));
+    hi = mul2(hi, both(d.scale));
+    lo.x = w[n].x > d.limit ? lo.x : 0.f;
+    lo.y = w[n].y > d.limit ? lo.y : 0.f;
+    hi.x = w[n].z > d.limit ? hi.x : 0.f;
+    hi.y = w[n].w > d.limit ? hi.y : 0.f;
   }
 }
 
@@ -285,35 +322,42 @@ struct Group {
 };
 
 // Sum over the group's threads in a fixed order, in every thread.  red:
-// 2 x 32 float2; calls alternate between its halves, which makes one barrier
-// a call enough.
+// 2 x 32 values; calls alternate between its halves, which makes one barrier a
+// call enough.
 struct GroupSum {
   float2* red;
   int warps, base, half;
   __device__ GroupSum(float2* smem, int group_warps, int group)
       : red(smem), warps(group_warps), base(group * group_warps), half(0) {}
-  __device__ float2 operator()(float2 v) {
+
+  __device__ static void shuffled(float2& v, int o) {
+    v = add2(v, make_float2(__shfl_xor_sync(~0u, v.x, o), __shfl_xor_sync(~0u, v.y, o)));
+  }
+  __device__ static void shuffled(float& v, int o) { v += __shfl_xor_sync(~0u, v, o); }
+
+  template <typename F>
+  __device__ F operator()(F v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(~0u, v.x, o);
-      v.y += __shfl_xor_sync(~0u, v.y, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) shuffled(v, o);
     if (warps == 1) return v;
     const int lane = threadIdx.x & 31;
-    float2* buf = red + half * 32;
+    F* buf = reinterpret_cast<F*>(red + half * 32);
     half ^= 1;
     if (lane == 0) buf[threadIdx.x >> 5] = v;
-    // one barrier to a group of warps: they keep different rows
+    // one barrier to a group of warps: the groups keep different rows
     asm volatile("bar.sync %0, %1;" ::"r"(1 + base / warps), "r"(warps * 32) : "memory");
-    v = lane < warps ? buf[base + lane] : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(~0u, v.x, o);
-      v.y += __shfl_xor_sync(~0u, v.y, o);
+    const int part = warps <= 8 ? lane & 7 : lane;  // every 8 lanes, or all 32
+    v = F{};
+    if (part < warps) v = buf[base + part];
+    if (warps > 8) {
+      shuffled(v, 16);
+      shuffled(v, 8);
     }
+    shuffled(v, 4);
+    shuffled(v, 2);
+    shuffled(v, 1);
     return v;
   }
-  __device__ float operator()(float v) { return (*this)(make_float2(v, 0.f)).x; }
 };
 
 // a parameter's values at phase + column, zeros around them
@@ -328,14 +372,12 @@ __device__ __forceinline__ void stage_param(float* dst, const void* p, int is_bf
 }
 
 template <int V>
-__device__ __forceinline__ void read_param(const float* src, int at, float (&v)[V]) {
+__device__ __forceinline__ void read_param(const float* src, int at, float2 (&v)[V / 2]) {
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
     const float4 q = *reinterpret_cast<const float4*>(src + at + 4 * i);
-    v[4 * i] = q.x;
-    v[4 * i + 1] = q.y;
-    v[4 * i + 2] = q.z;
-    v[4 * i + 3] = q.w;
+    v[2 * i] = make_float2(q.x, q.y);
+    v[2 * i + 1] = make_float2(q.z, q.w);
   }
 }
 
@@ -343,7 +385,7 @@ template <typename T, int VPT, bool ALIGNED, bool DROP>
 __global__ void __launch_bounds__(1024)
     norm_rows_kernel(NormArgs a, int group_warps, int padded, const T* x, const T* res,
                      const void* weight, const void* bias, T* z, T* y, float* mean, float* rstd) {
-  constexpr int V = Lanes<T>::V;
+  constexpr int V = Lanes<T>::V, P = V / 2;
   extern __shared__ __align__(16) float params[];  // weight, bias: `padded` each
   __shared__ float2 red[64];
   const int H = a.hidden;
@@ -368,53 +410,67 @@ __global__ void __launch_bounds__(1024)
   __syncthreads();
 
   for (int64_t r = g.row; r < a.rows; r += g.step) {
-    float v[VPT][V];
+    float2 v[VPT][P];
     if (!AHEAD) fetch(r);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      unpack(qx[i], v[i], x);
-      if (DROP) drop_vec<V>(a.drop, rng, r * H + g.col(i), v[i]);
-      if (res) {
-        float w[V];
+    for (int i = 0; i < VPT; ++i) unpack(qx[i], v[i], x);
+    if (DROP) {
+      int64_t first[VPT];
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) first[i] = r * H + g.col(i);
+      drop_vecs<V>(a.drop, rng, first, v);
+    }
+    if (res) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float2 w[P];
         unpack(qr[i], w, x);
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[i][e] += w[e];
+        for (int e = 0; e < P; ++e) v[i][e] = add2(v[i][e], w[e]);
+        if (z) store_vec<T, ALIGNED>(z + r * H, g.col(i), H, v[i]);
       }
     }
     // the next row's reads run under this row's sums
     if (AHEAD && r + g.step < a.rows) fetch(r + g.step);
     float m = 0.f;
     if (!a.rms) {
-      float s = 0.f;
+      float2 s = both(0.f);
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) s += v[i][e];
-      m = sum(s) * inv_h;
-    }
-    float sq = 0.f;
+        for (int e = 0; e < P; ++e) s = add2(s, v[i][e]);
+      m = sum(s.x + s.y) * inv_h;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = g.col(i);
+      for (int i = 0; i < VPT; ++i)
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float d = v[i][e] - m;
-        const bool in = ALIGNED ? c < H : c + e >= 0 && c + e < H;
-        sq += in ? d * d : 0.f;
-      }
+        for (int e = 0; e < P; ++e) v[i][e] = add2(v[i][e], both(-m));
     }
-    const float rs = 1.f / sqrtf(sum(sq) * inv_h + a.eps);
+    float2 sq = both(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = g.col(i);
       if (c >= H) continue;
-      if (z) store_vec<T, ALIGNED>(z + r * H, c, H, v[i]);
-      float w[V], b[V];
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        float2 d = v[i][e];
+        if (!ALIGNED) {
+          if (c + 2 * e < 0 || c + 2 * e >= H) d.x = 0.f;
+          if (c + 2 * e + 1 < 0 || c + 2 * e + 1 >= H) d.y = 0.f;
+        }
+        sq = fma2(d, d, sq);
+      }
+    }
+    const float rs = rsqrtf(sum(sq.x + sq.y) * inv_h + a.eps);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = g.col(i);
+      if (c >= H) continue;
+      float2 w[P], b[P];
       read_param<V>(params, c + g.phase, w);
       read_param<V>(params + padded, c + g.phase, b);
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[i][e] = (v[i][e] - m) * rs * w[e] + b[e];
-      store_vec<T, ALIGNED>(y + r * H, c, H, v[i]);
+      for (int e = 0; e < P; ++e) b[e] = fma2(mul2(v[i][e], both(rs)), w[e], b[e]);
+      store_vec<T, ALIGNED>(y + r * H, c, H, b);
     }
     if (g.t == 0) {
       if (mean && !a.rms) mean[r] = m;
@@ -431,7 +487,7 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
     norm_backward_rows_kernel(NormArgs a, int group_warps, int padded, const T* dy, const T* x,
                               const void* weight, const float* mean, const float* rstd,
                               const T* dz, T* dx, T* dbranch, float* part) {
-  constexpr int V = Lanes<T>::V;
+  constexpr int V = Lanes<T>::V, P = V / 2;
   // weight [padded]; the two sums [padded] each, behind it (SUMS_SMEM) or,
   // after the last row, in its place
   extern __shared__ __align__(16) float params[];
@@ -442,7 +498,7 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
   const Philox rng = DROP ? philox_of(a.rng) : Philox{};
   const float inv_h = 1.f / static_cast<float>(H);
   constexpr int S = SUMS_SMEM ? 1 : VPT;
-  float sw[S][V], sb[S][V];
+  float2 sw[S][P], sb[S][P];
   float* sums = SUMS_SMEM ? params + padded : params;
   stage_param(params, weight, a.param_bf16, 1.f, g.phase, H, padded);
   if (SUMS_SMEM)
@@ -450,80 +506,94 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
 #pragma unroll
   for (int i = 0; i < S; ++i)
 #pragma unroll
-    for (int e = 0; e < V; ++e) sw[i][e] = sb[i][e] = 0.f;
+    for (int e = 0; e < P; ++e) sw[i][e] = sb[i][e] = both(0.f);
   __syncthreads();
 
   for (int64_t r = g.row; r < a.rows; r += g.step) {
-    uint4 qx[VPT], qd[VPT];
+    uint4 qx[VPT], qd[VPT], qz[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       qx[i] = load_vec<T, ALIGNED>(x + r * H, g.col(i), H);
       qd[i] = load_vec<T, ALIGNED>(dy + r * H, g.col(i), H);
+      if (!SUMS_SMEM && dz) qz[i] = load_vec<T, ALIGNED>(dz + r * H, g.col(i), H);
     }
     const float m = a.rms ? 0.f : mean[r], rs = rstd[r];
-    float2 s = make_float2(0.f, 0.f);
+    float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = g.col(i);
       if (c >= H) continue;
-      float vx[V], vd[V], w[V];
+      float2 vx[P], vd[P], w[P];
       unpack(qx[i], vx, x);
       unpack(qd[i], vd, x);
       read_param<V>(params, c + g.phase, w);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float gw = vd[e] * w[e];
-        s.x += gw;
-        s.y += gw * ((vx[e] - m) * rs);
+      for (int e = 0; e < P; ++e) {
+        const float2 gw = mul2(vd[e], w[e]);
+        s1 = add2(s1, gw);
+        s2 = fma2(gw, mul2(add2(vx[e], both(-m)), both(rs)), s2);
       }
     }
-    s = sum(s);
+    const float2 s = sum(make_float2(s1.x + s1.y, s2.x + s2.y));
     const float c1 = a.rms ? 0.f : s.x * inv_h, c2 = s.y * inv_h;
+    float2 o[VPT][P];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = g.col(i);
+      float2 vx[P], vd[P], w[P], tw[P], tb[P];
+      if (dz) {
+        unpack(SUMS_SMEM ? load_vec<T, ALIGNED>(dz + r * H, c, H) : qz[i], o[i], x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < P; ++e) o[i][e] = both(0.f);
+      }
       if (c >= H) continue;
-      float vx[V], vd[V], w[V], o[V];
       unpack(qx[i], vx, x);
       unpack(qd[i], vd, x);
       read_param<V>(params, c + g.phase, w);
-      if (dz) {
-        unpack(load_vec<T, ALIGNED>(dz + r * H, c, H), o, x);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = 0.f;
-      }
-      float tw[V], tb[V];
       if (SUMS_SMEM) {
         read_param<V>(sums, c + g.phase, tw);
         read_param<V>(sums + padded, c + g.phase, tb);
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (vx[e] - m) * rs;
-        o[e] += rs * (vd[e] * w[e] - c1 - xh * c2);
+      for (int e = 0; e < P; ++e) {
+        const float2 xh = mul2(add2(vx[e], both(-m)), both(rs));
+        const float2 core = fma2(xh, both(-c2), fma2(vd[e], w[e], both(-c1)));
+        o[i][e] = fma2(core, both(rs), o[i][e]);
         if (SUMS_SMEM) {
-          tw[e] += vd[e] * xh;
-          tb[e] += vd[e];
+          tw[e] = fma2(vd[e], xh, tw[e]);
+          tb[e] = add2(vd[e], tb[e]);
         } else {
-          sw[i][e] += vd[e] * xh;
-          sb[i][e] += vd[e];
+          sw[i][e] = fma2(vd[e], xh, sw[i][e]);
+          sb[i][e] = add2(vd[e], sb[i][e]);
         }
       }
       if (SUMS_SMEM) {
 #pragma unroll
-        for (int e = 0; e < V; e += 4) {
-          *reinterpret_cast<float4*>(sums + c + g.phase + e) =
-              make_float4(tw[e], tw[e + 1], tw[e + 2], tw[e + 3]);
-          *reinterpret_cast<float4*>(sums + padded + c + g.phase + e) =
-              make_float4(tb[e], tb[e + 1], tb[e + 2], tb[e + 3]);
+        for (int e = 0; e < P; e += 2) {
+          *reinterpret_cast<float4*>(sums + c + g.phase + 2 * e) =
+              make_float4(tw[e].x, tw[e].y, tw[e + 1].x, tw[e + 1].y);
+          *reinterpret_cast<float4*>(sums + padded + c + g.phase + 2 * e) =
+              make_float4(tb[e].x, tb[e].y, tb[e + 1].x, tb[e + 1].y);
         }
       }
-      store_vec<T, ALIGNED>(dx + r * H, c, H, o);
-      if (dbranch) {
-        if (DROP) drop_vec<V>(a.drop, rng, r * H + c, o);
-        store_vec<T, ALIGNED>(dbranch + r * H, c, H, o);
+      store_vec<T, ALIGNED>(dx + r * H, c, H, o[i]);
+      if (dbranch && (!DROP || SUMS_SMEM)) {
+        if (DROP) {
+          const int64_t first[1] = {r * H + c};
+          float2(&one)[1][P] = *reinterpret_cast<float2(*)[1][P]>(&o[i]);
+          drop_vecs<V>(a.drop, rng, first, one);
+        }
+        store_vec<T, ALIGNED>(dbranch + r * H, c, H, o[i]);
       }
+    }
+    if (DROP && !SUMS_SMEM) {
+      int64_t first[VPT];
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) first[i] = r * H + g.col(i);
+      drop_vecs<V>(a.drop, rng, first, o);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) store_vec<T, ALIGNED>(dbranch + r * H, g.col(i), H, o[i]);
     }
   }
 
@@ -537,9 +607,11 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
           const int at = g.col(i) + g.phase;
           if (at >= padded) continue;
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            sums[at + e] = k == 0 ? sw[i][e] : sums[at + e] + sw[i][e];
-            sums[padded + at + e] = k == 0 ? sb[i][e] : sums[padded + at + e] + sb[i][e];
+          for (int e = 0; e < P; ++e) {
+            float2* pw = reinterpret_cast<float2*>(sums + at) + e;
+            float2* pb = reinterpret_cast<float2*>(sums + padded + at) + e;
+            *pw = k == 0 ? sw[i][e] : add2(*pw, sw[i][e]);
+            *pb = k == 0 ? sb[i][e] : add2(*pb, sb[i][e]);
           }
         }
       }
@@ -588,19 +660,33 @@ __global__ void __launch_bounds__(256)
   const Philox g = DROP ? philox_of(rng) : Philox{};
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   const int64_t vecs = (n + V - 1) / V;
+  auto left = [&](int64_t q) { return n - q * V < V ? static_cast<int>(n - q * V) : V; };
+  // two vectors at a time: their reads and their generator rounds overlap
   for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < vecs;
-       q += step) {
-    const int64_t first = q * V;
-    const int left = n - first < V ? static_cast<int>(n - first) : V;
-    float v[V], w[V];
-    unpack(load_vec<T, false>(x + first, 0, left), v, x);
-    if (res) unpack(load_vec<T, false>(res + first, 0, left), w, x);
-    if (DROP) drop_vec<V>(d, g, first, v);
-    if (res) {
+       q += 2 * step) {
+    const int64_t at[2] = {q * V, (q + step) * V};
+    const bool two = q + step < vecs;
+    uint4 qx[2] = {}, qr[2] = {};
+    float2 v[2][V / 2], w[V / 2];
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] += w[e];
+    for (int i = 0; i < 2; ++i) {
+      if (i == 1 && !two) break;
+      qx[i] = load_vec<T, false>(x + at[i], 0, left(q + i * step));
+      if (res) qr[i] = load_vec<T, false>(res + at[i], 0, left(q + i * step));
     }
-    store_vec<T, false>(y + first, 0, left, v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) unpack(qx[i], v[i], x);
+    if (DROP) drop_vecs<V>(d, g, at, v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i == 1 && !two) break;
+      if (res) {
+        unpack(qr[i], w, x);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) v[i][e] = add2(v[i][e], w[e]);
+      }
+      store_vec<T, false>(y + at[i], 0, left(q + i * step), v[i]);
+    }
   }
 }
 

@@ -18,22 +18,31 @@ __device__ __forceinline__ Philox philox_of(const uint64_t* rng) {
           static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)};
 }
 
-// the four words of block `ctr`
-__device__ __forceinline__ uint4 philox_words(const Philox& g, uint64_t ctr) {
-  uint32_t x0 = static_cast<uint32_t>(ctr), x1 = static_cast<uint32_t>(ctr >> 32), x2 = g.c2,
-           x3 = g.c3, k0 = g.k0, k1 = g.k1;
+// The four words of each of N blocks.  The blocks go through a round together:
+// they share the key's steps and hide the multiplications' latency.
+template <int N>
+__device__ __forceinline__ void philox_words(const Philox& g, const uint64_t (&ctr)[N],
+                                             uint4 (&out)[N]) {
+  uint32_t k0 = g.k0, k1 = g.k1;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    out[n] = make_uint4(static_cast<uint32_t>(ctr[n]), static_cast<uint32_t>(ctr[n] >> 32), g.c2,
+                        g.c3);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
-    const uint64_t a = static_cast<uint64_t>(x0) * 0xD2511F53u;
-    const uint64_t b = static_cast<uint64_t>(x2) * 0xCD9E8D57u;
-    x0 = static_cast<uint32_t>(b >> 32) ^ x1 ^ k0;
-    x2 = static_cast<uint32_t>(a >> 32) ^ x3 ^ k1;
-    x1 = static_cast<uint32_t>(b);
-    x3 = static_cast<uint32_t>(a);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      uint4& x = out[n];
+      const uint64_t a = static_cast<uint64_t>(x.x) * 0xD2511F53u;
+      const uint64_t b = static_cast<uint64_t>(x.z) * 0xCD9E8D57u;
+      x.x = static_cast<uint32_t>(b >> 32) ^ x.y ^ k0;
+      x.z = static_cast<uint32_t>(a >> 32) ^ x.w ^ k1;
+      x.y = static_cast<uint32_t>(b);
+      x.w = static_cast<uint32_t>(a);
+    }
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  return make_uint4(x0, x1, x2, x3);
 }
 
 // Dropout of probability p, 0 < p <= 1: an element is kept iff its word is
