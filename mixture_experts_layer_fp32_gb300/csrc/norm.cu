@@ -217,7 +217,7 @@ __device__ __forceinline__ uint4 pack(const float2 (&v)[4], const __nv_bfloat16*
 }
 
 // The elements of an edge vector that lie in the row, one by one; loops that
-// stay loops: an edge is one thread's in a row.
+// stay loops: few threads take them.
 __device__ __forceinline__ uint32_t bits_of(const float* p) { return __float_as_uint(*p); }
 __device__ __forceinline__ uint32_t bits_of(const __nv_bfloat16* p) {
   return __bfloat16_as_ushort(*p);
@@ -254,13 +254,25 @@ __device__ __forceinline__ void store_edge(T* row, int col, int H, uint4 q) {
 }
 
 // The vector whose first element is column `col` of `row` (col may be negative
-// or past the row in an edge vector); zeros outside of the row.
+// or past the row in an edge vector).  An edge vector comes whole, foreign
+// elements with it (mask_edge), but for the tensor's last one: `room` elements
+// follow from the row's start on.
 template <typename T, bool ALIGNED>
-__device__ __forceinline__ uint4 load_vec(const T* row, int col, int H) {
+__device__ __forceinline__ uint4 load_vec(const T* row, int col, int H, int64_t room) {
   constexpr int V = Lanes<T>::V;
   if (col >= H) return make_uint4(0, 0, 0, 0);
-  if (ALIGNED || (col >= 0 && col + V <= H)) return *reinterpret_cast<const uint4*>(row + col);
+  if (ALIGNED || col + V <= room) return *reinterpret_cast<const uint4*>(row + col);
   return load_edge(row, col, H);
+}
+// zeros for the elements outside of the row
+template <int P>
+__device__ __forceinline__ void mask_edge(float2 (&v)[P], int col, int H) {
+  if (col >= 0 && col + 2 * P <= H) return;
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    if (col + 2 * e < 0 || col + 2 * e >= H) v[e].x = 0.f;
+    if (col + 2 * e + 1 < 0 || col + 2 * e + 1 >= H) v[e].y = 0.f;
+  }
 }
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ void store_vec(T* row, int col, int H,
@@ -360,15 +372,42 @@ struct GroupSum {
   }
 };
 
-// a parameter's values at phase + column, zeros around them
+// A parameter's values at phase + column of shared memory, zeros around them;
+// without the parameter `none`.  A thread brings the columns that it will read,
+// all its reads in flight at once; one group does it for the block.
+template <typename T, int VPT, bool ALIGNED>
 __device__ __forceinline__ void stage_param(float* dst, const void* p, int is_bf16, float none,
-                                            int phase, int H, int padded) {
-  for (int c = threadIdx.x; c < padded; c += blockDim.x) {
-    const int col = c - phase;
-    float v = 0.f;
-    if (col >= 0 && col < H) v = p ? param1(p, is_bf16, col) : none;
-    dst[c] = v;
+                                            const Group<T, ALIGNED>& g, int H) {
+  constexpr int V = Lanes<T>::V;
+  if (g.id != 0) return;
+  float v[VPT][V];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = g.col(i);
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[i][e] = c + e >= 0 && c + e < H ? none : 0.f;
+    if (p == nullptr || c >= H) continue;
+    if (ALIGNED && !is_bf16) {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + e);
+        v[i][e] = q.x;
+        v[i][e + 1] = q.y;
+        v[i][e + 2] = q.z;
+        v[i][e + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (c + e >= 0 && c + e < H) v[i][e] = param1(p, is_bf16, c + e);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int e = 0; e < V; e += 4)
+      *reinterpret_cast<float4*>(dst + g.col(i) + g.phase + e) =
+          make_float4(v[i][e], v[i][e + 1], v[i][e + 2], v[i][e + 3]);
 }
 
 template <int V>
@@ -395,25 +434,32 @@ __global__ void __launch_bounds__(1024)
   const float inv_h = 1.f / static_cast<float>(H);
 
   uint4 qx[VPT], qr[VPT];
-  auto fetch = [&](int64_t r) {
+  auto fetch = [&](uint4 (&q)[VPT], const T* p, int64_t r) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      qx[i] = load_vec<T, ALIGNED>(x + r * H, g.col(i), H);
-      if (res) qr[i] = load_vec<T, ALIGNED>(res + r * H, g.col(i), H);
-    }
+    for (int i = 0; i < VPT; ++i)
+      q[i] = load_vec<T, ALIGNED>(p + r * H, g.col(i), H, (a.rows - r) * H);
   };
   // one row ahead where the registers allow it
   constexpr bool AHEAD = VPT <= 2;
-  if (AHEAD && g.row < a.rows) fetch(g.row);
-  stage_param(params, weight, a.param_bf16, 1.f, g.phase, H, padded);
-  stage_param(params + padded, bias, a.param_bf16, 0.f, g.phase, H, padded);
+  if (AHEAD && g.row < a.rows) {
+    fetch(qx, x, g.row);
+    if (res) fetch(qr, res, g.row);
+  }
+  stage_param<T, VPT>(params, weight, a.param_bf16, 1.f, g, H);
+  stage_param<T, VPT>(params + padded, bias, a.param_bf16, 0.f, g, H);
   __syncthreads();
 
   for (int64_t r = g.row; r < a.rows; r += g.step) {
     float2 v[VPT][P];
-    if (!AHEAD) fetch(r);
+    if (!AHEAD) {
+      fetch(qx, x, r);
+      if (res) fetch(qr, res, r);
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) unpack(qx[i], v[i], x);
+    // the next row's reads run under this row's work
+    const bool more = AHEAD && r + g.step < a.rows;
+    if (more) fetch(qx, x, r + g.step);
     if (DROP) {
       int64_t first[VPT];
 #pragma unroll
@@ -430,8 +476,11 @@ __global__ void __launch_bounds__(1024)
         if (z) store_vec<T, ALIGNED>(z + r * H, g.col(i), H, v[i]);
       }
     }
-    // the next row's reads run under this row's sums
-    if (AHEAD && r + g.step < a.rows) fetch(r + g.step);
+    if (more && res) fetch(qr, res, r + g.step);
+    if (!ALIGNED) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) mask_edge(v[i], g.col(i), H);
+    }
     float m = 0.f;
     if (!a.rms) {
       float2 s = both(0.f);
@@ -479,17 +528,36 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+// A thread's own vectors of the rows to come, copied to shared memory without
+// registers.  Only the thread itself reads them, so no barrier is needed.
+// Edge vectors are copied whole (their foreign elements are masked after) and
+// the tensor's last vector as far as the tensor goes.
+__device__ __forceinline__ void copy_vec(uint4* slot, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(slot))),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // The sums for dweight and dbias stay in the thread's registers over all of its
-// rows (in shared memory, SUMS_SMEM, where a row is too wide for that), are
-// added up over the block's groups in order, and go to the block's part.
-template <typename T, int VPT, bool ALIGNED, bool DROP, bool SUMS_SMEM>
-__global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
+// rows, are added up over the block's groups in order, and go to the block's
+// part.  The row to come is read two rows ahead (STAGED).  Rows too wide for
+// that keep the sums in shared memory and read a row when they come to it.
+constexpr int kSlots = 3;
+template <typename T, int VPT, bool ALIGNED, bool DROP, bool STAGED>
+__global__ void __launch_bounds__(STAGED ? 512 : 640)
     norm_backward_rows_kernel(NormArgs a, int group_warps, int padded, const T* dy, const T* x,
                               const void* weight, const float* mean, const float* rstd,
                               const T* dz, T* dx, T* dbranch, float* part) {
   constexpr int V = Lanes<T>::V, P = V / 2;
-  // weight [padded]; the two sums [padded] each, behind it (SUMS_SMEM) or,
-  // after the last row, in its place
+  // weight [padded]; then the copied vectors (STAGED) or the two sums [padded]
+  // each.  After the last row the staged sums take the place of all that.
   extern __shared__ __align__(16) float params[];
   __shared__ float2 red[64];
   const int H = a.hidden;
@@ -497,35 +565,76 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
   GroupSum sum(red, group_warps, g.id);
   const Philox rng = DROP ? philox_of(a.rng) : Philox{};
   const float inv_h = 1.f / static_cast<float>(H);
-  constexpr int S = SUMS_SMEM ? 1 : VPT;
+  const int64_t total = a.rows * H;
+  constexpr int S = STAGED ? VPT : 1;
   float2 sw[S][P], sb[S][P];
-  float* sums = SUMS_SMEM ? params + padded : params;
-  stage_param(params, weight, a.param_bf16, 1.f, g.phase, H, padded);
-  if (SUMS_SMEM)
+  float* sums = STAGED ? params : params + padded;
+  uint4* slots = reinterpret_cast<uint4*>(params + padded) + threadIdx.x;
+  auto slot = [&](int n, int tensor, int i) {
+    return slots + ((n * 3 + tensor) * VPT + i) * blockDim.x;
+  };
+  auto fetch = [&](int64_t r, int n) {
+    if (r < a.rows) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = g.col(i);
+        if (c >= H) continue;
+        const int64_t at = r * H + c;
+        int bytes = 16;
+        if (!ALIGNED && at + V > total) bytes = static_cast<int>(total - at) * sizeof(T);
+        copy_vec(slot(n, 0, i), x + at, bytes);
+        copy_vec(slot(n, 1, i), dy + at, bytes);
+        if (dz) copy_vec(slot(n, 2, i), dz + at, bytes);
+      }
+    }
+    copies_commit();
+  };
+  auto read = [&](const T* p, int64_t r, int n, int tensor, int i, float2(&v)[P]) {
+    const int c = g.col(i);
+    if (STAGED) {
+      unpack(*slot(n, tensor, i), v, p);
+    } else {
+      unpack(load_vec<T, ALIGNED>(p + r * H, c, H, (a.rows - r) * H), v, p);
+    }
+    if (!ALIGNED) mask_edge(v, c, H);
+  };
+  if (STAGED) {
+#pragma unroll
+    for (int n = 0; n < kSlots - 1; ++n) fetch(g.row + n * g.step, n);
+  }
+  stage_param<T, VPT>(params, weight, a.param_bf16, 1.f, g, H);
+  if (!STAGED)
     for (int c = threadIdx.x; c < 2 * padded; c += blockDim.x) sums[c] = 0.f;
 #pragma unroll
   for (int i = 0; i < S; ++i)
 #pragma unroll
     for (int e = 0; e < P; ++e) sw[i][e] = sb[i][e] = both(0.f);
+  float m_next = 0.f, rs_next = 0.f;
+  if (g.row < a.rows) {
+    if (!a.rms) m_next = mean[g.row];
+    rs_next = rstd[g.row];
+  }
   __syncthreads();
 
+  int n = 0;  // the slot of row r
   for (int64_t r = g.row; r < a.rows; r += g.step) {
-    uint4 qx[VPT], qd[VPT], qz[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      qx[i] = load_vec<T, ALIGNED>(x + r * H, g.col(i), H);
-      qd[i] = load_vec<T, ALIGNED>(dy + r * H, g.col(i), H);
-      if (!SUMS_SMEM && dz) qz[i] = load_vec<T, ALIGNED>(dz + r * H, g.col(i), H);
+    const float m = m_next, rs = rs_next;
+    if (r + g.step < a.rows) {
+      if (!a.rms) m_next = mean[r + g.step];
+      rs_next = rstd[r + g.step];
     }
-    const float m = a.rms ? 0.f : mean[r], rs = rstd[r];
+    if (STAGED) {
+      fetch(r + (kSlots - 1) * g.step, n == 0 ? kSlots - 1 : n - 1);
+      copies_wait<kSlots - 1>();
+    }
     float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = g.col(i);
       if (c >= H) continue;
       float2 vx[P], vd[P], w[P];
-      unpack(qx[i], vx, x);
-      unpack(qd[i], vd, x);
+      read(x, r, n, 0, i, vx);
+      read(dy, r, n, 1, i, vd);
       read_param<V>(params, c + g.phase, w);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
@@ -540,18 +649,15 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = g.col(i);
-      float2 vx[P], vd[P], w[P], tw[P], tb[P];
-      if (dz) {
-        unpack(SUMS_SMEM ? load_vec<T, ALIGNED>(dz + r * H, c, H) : qz[i], o[i], x);
-      } else {
 #pragma unroll
-        for (int e = 0; e < P; ++e) o[i][e] = both(0.f);
-      }
+      for (int e = 0; e < P; ++e) o[i][e] = both(0.f);
       if (c >= H) continue;
-      unpack(qx[i], vx, x);
-      unpack(qd[i], vd, x);
+      float2 vx[P], vd[P], w[P], tw[P], tb[P];
+      if (dz) read(dz, r, n, 2, i, o[i]);
+      read(x, r, n, 0, i, vx);
+      read(dy, r, n, 1, i, vd);
       read_param<V>(params, c + g.phase, w);
-      if (SUMS_SMEM) {
+      if (!STAGED) {
         read_param<V>(sums, c + g.phase, tw);
         read_param<V>(sums + padded, c + g.phase, tb);
       }
@@ -560,15 +666,15 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
         const float2 xh = mul2(add2(vx[e], both(-m)), both(rs));
         const float2 core = fma2(xh, both(-c2), fma2(vd[e], w[e], both(-c1)));
         o[i][e] = fma2(core, both(rs), o[i][e]);
-        if (SUMS_SMEM) {
-          tw[e] = fma2(vd[e], xh, tw[e]);
-          tb[e] = add2(vd[e], tb[e]);
-        } else {
+        if (STAGED) {
           sw[i][e] = fma2(vd[e], xh, sw[i][e]);
           sb[i][e] = add2(vd[e], sb[i][e]);
+        } else {
+          tw[e] = fma2(vd[e], xh, tw[e]);
+          tb[e] = add2(vd[e], tb[e]);
         }
       }
-      if (SUMS_SMEM) {
+      if (!STAGED) {
 #pragma unroll
         for (int e = 0; e < P; e += 2) {
           *reinterpret_cast<float4*>(sums + c + g.phase + 2 * e) =
@@ -578,7 +684,7 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
         }
       }
       store_vec<T, ALIGNED>(dx + r * H, c, H, o[i]);
-      if (dbranch && (!DROP || SUMS_SMEM)) {
+      if (dbranch && (!DROP || !STAGED)) {
         if (DROP) {
           const int64_t first[1] = {r * H + c};
           float2(&one)[1][P] = *reinterpret_cast<float2(*)[1][P]>(&o[i]);
@@ -587,7 +693,7 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
         store_vec<T, ALIGNED>(dbranch + r * H, c, H, o[i]);
       }
     }
-    if (DROP && !SUMS_SMEM) {
+    if (DROP && STAGED) {
       int64_t first[VPT];
 #pragma unroll
       for (int i = 0; i < VPT; ++i) first[i] = r * H + g.col(i);
@@ -595,10 +701,12 @@ __global__ void __launch_bounds__(SUMS_SMEM ? 640 : 512)
 #pragma unroll
       for (int i = 0; i < VPT; ++i) store_vec<T, ALIGNED>(dbranch + r * H, g.col(i), H, o[i]);
     }
+    n = n == kSlots - 1 ? 0 : n + 1;
   }
 
+  if (STAGED) copies_wait<0>();
   __syncthreads();
-  if (!SUMS_SMEM) {
+  if (STAGED) {
     const int groups = blockDim.x / g.size;
     for (int k = 0; k < groups; ++k) {
       if (g.id == k) {
@@ -638,7 +746,7 @@ __global__ void __launch_bounds__(kGradWarps * 32)
   float s = 0.f;
   if (c < H && out) {
     const float* p = part + static_cast<int64_t>(blockIdx.y) * H + c;
-#pragma unroll 8
+#pragma unroll 10
     for (int i = warp; i < parts; i += kGradWarps) s += p[static_cast<int64_t>(i) * 2 * H];
   }
   buf[warp][lane] = s;
@@ -651,42 +759,46 @@ __global__ void __launch_bounds__(kGradWarps * 32)
   }
 }
 
-// Flat vectors of 16 bytes; the last elements of a length that is no multiple
-// one by one.
+// Flat vectors of 16 bytes, two to a thread at a time so that their reads and
+// their generator rounds overlap; the last elements of a length that is no
+// multiple of the vector's go one by one.
 template <typename T, bool DROP>
 __global__ void __launch_bounds__(256)
     dropout_add_kernel(int64_t n, Dropout d, const uint64_t* rng, const T* x, const T* res, T* y) {
   constexpr int V = Lanes<T>::V;
   const Philox g = DROP ? philox_of(rng) : Philox{};
+  const int64_t vecs = n / V;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  const int64_t vecs = (n + V - 1) / V;
-  auto left = [&](int64_t q) { return n - q * V < V ? static_cast<int>(n - q * V) : V; };
-  // two vectors at a time: their reads and their generator rounds overlap
-  for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < vecs;
-       q += 2 * step) {
-    const int64_t at[2] = {q * V, (q + step) * V};
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const uint4 *xv = reinterpret_cast<const uint4*>(x), *rv = reinterpret_cast<const uint4*>(res);
+  uint4* yv = reinterpret_cast<uint4*>(y);
+  for (int64_t q = me; q < vecs; q += 2 * step) {
     const bool two = q + step < vecs;
-    uint4 qx[2] = {}, qr[2] = {};
+    const int64_t p[2] = {q, two ? q + step : q}, at[2] = {p[0] * V, p[1] * V};
+    uint4 qx[2], qr[2];
     float2 v[2][V / 2], w[V / 2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (i == 1 && !two) break;
-      qx[i] = load_vec<T, false>(x + at[i], 0, left(q + i * step));
-      if (res) qr[i] = load_vec<T, false>(res + at[i], 0, left(q + i * step));
+      qx[i] = xv[p[i]];
+      if (res) qr[i] = rv[p[i]];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) unpack(qx[i], v[i], x);
     if (DROP) drop_vecs<V>(d, g, at, v);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (i == 1 && !two) break;
       if (res) {
         unpack(qr[i], w, x);
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) v[i][e] = add2(v[i][e], w[e]);
       }
-      store_vec<T, false>(y + at[i], 0, left(q + i * step), v[i]);
+      if (i == 0 || two) yv[p[i]] = pack(v[i], x);
     }
+  }
+  const int64_t i = vecs * V + me;
+  if (i < n) {
+    const float v = DROP ? drop1(d, g, i, load1(x, i)) : load1(x, i);
+    store1(y, i, res ? load1(res, i) + v : v);
   }
 }
 
@@ -703,36 +815,42 @@ NormArgs args_of(const moe_norm_config& c, const uint64_t* rng) {
 }
 
 constexpr int kSms = 152;
-constexpr int kMostSmem = 216 * 1024;
+constexpr size_t kMostSmem = 216 * 1024;
 
 // How rows are laid over threads.  vectors: 16-byte vectors that a row can
 // touch; group_warps warps x vpt vectors hold them.
 struct Shape {
   int vpt = 0;  // 0: too wide for the chip, the wide kernel
   int group_warps = 0, groups = 1, padded = 0, threads = 0;
-  bool aligned = true, sums_smem = false;
+  bool aligned = true, staged = false;
   unsigned grid = 0;
 };
 
-void shape_common(Shape& s, const moe_norm_config& c, int vectors, int V, int per_sm) {
+void shape_common(Shape& s, const moe_norm_config& c, int vectors, int V) {
   s.group_warps = (vectors + s.vpt * 32 - 1) / (s.vpt * 32);
   s.groups = s.group_warps >= 8 ? 1 : 8 / s.group_warps;
   if (c.rows < static_cast<int64_t>(kSms) * s.groups) s.groups = 1;
   s.threads = s.group_warps * s.groups * 32;
   s.padded = s.group_warps * 32 * s.vpt * V;
-  const int64_t most = static_cast<int64_t>(kSms) * per_sm;
-  int64_t grid = (c.rows + s.groups - 1) / s.groups;
-  if (!s.aligned) {  // whole sets of residues
-    const int64_t each = ((c.rows + V - 1) / V + s.groups - 1) / s.groups;
-    grid = each * V;
-    s.grid = static_cast<unsigned>(grid < most ? grid : most / V * V);
-  } else {
-    s.grid = static_cast<unsigned>(grid < most ? grid : most);
-  }
 }
 
+// One wave of blocks, per_sm to an SM as far as shared memory allows; for odd
+// widths whole sets of residues.
+void shape_grid(Shape& s, const moe_norm_config& c, int V, int per_sm, size_t smem) {
+  const int fit = static_cast<int>(kMostSmem / smem);
+  if (per_sm > fit) per_sm = fit;
+  const int64_t most = static_cast<int64_t>(kSms) * (per_sm < 1 ? 1 : per_sm);
+  int64_t grid = (c.rows + s.groups - 1) / s.groups, top = most;
+  if (!s.aligned) {
+    grid = ((c.rows + V - 1) / V + s.groups - 1) / s.groups * V;
+    top = most / V * V;
+  }
+  s.grid = static_cast<unsigned>(grid < top ? grid : top);
+}
+
+// vectors that a row of any phase can touch
 int row_vectors(const moe_norm_config& c, int V) {
-  return c.hidden % V == 0 ? c.hidden / V : c.hidden / V + 2;
+  return c.hidden % V == 0 ? c.hidden / V : (c.hidden + 2 * V - 2) / V;
 }
 
 Shape forward_shape(const moe_norm_config& c) {
@@ -747,13 +865,16 @@ Shape forward_shape(const moe_norm_config& c) {
   else if (V == 4 && vectors <= 4096) s.vpt = 4;
   else if (V == 4 && vectors <= 5120) s.vpt = 5;
   else return s;
-  const int warps = (vectors + s.vpt * 32 - 1) / (s.vpt * 32);
-  const int smem = 2 * warps * 32 * s.vpt * V * 4;
-  const int threads = warps >= 8 ? warps * 32 : 256;
-  int per_sm = 1024 / threads;
-  if (per_sm > kMostSmem / smem) per_sm = kMostSmem / smem;
-  shape_common(s, c, vectors, V, per_sm < 1 ? 1 : per_sm);
+  shape_common(s, c, vectors, V);
+  shape_grid(s, c, V, 1024 / s.threads, 2 * static_cast<size_t>(s.padded) * 4);
   return s;
+}
+
+size_t backward_smem(const Shape& s) {
+  const size_t padded = static_cast<size_t>(s.padded) * 4;
+  if (!s.staged) return 3 * padded;
+  const size_t rows = padded + static_cast<size_t>(kSlots) * 3 * s.threads * s.vpt * 16;
+  return rows > 2 * padded ? rows : 2 * padded;
 }
 
 Shape backward_shape(const moe_norm_config& c) {
@@ -762,27 +883,20 @@ Shape backward_shape(const moe_norm_config& c) {
   if (c.hidden > 32768) return s;
   const int vectors = row_vectors(c, V);
   s.aligned = c.hidden % V == 0;
-  int most_warps = 16;
-  if (vectors <= 32) s.vpt = 1;
-  else if (vectors <= 2 * 32 * 16) s.vpt = 2;
-  else if (V == 4 && vectors <= 4 * 32 * 16) s.vpt = 4;
-  else {
-    s.sums_smem = true;
-    most_warps = 20;
-    s.vpt = V == 4 ? 8 : 4;
-    if (vectors > s.vpt * 32 * most_warps) s.vpt = 0;
+  s.vpt = vectors <= 32 ? 1 : 2;
+  s.staged = vectors <= s.vpt * 32 * 16;
+  if (!s.staged) s.vpt = V == 4 && vectors > 4 * 32 * 20 ? 8 : 4;
+  if (vectors > s.vpt * 32 * 20) {
+    s.vpt = 0;
+    return s;
   }
-  if (s.vpt == 0) return s;
-  const int warps = (vectors + s.vpt * 32 - 1) / (s.vpt * 32);
-  const int smem = (s.sums_smem ? 3 : 2) * warps * 32 * s.vpt * V * 4;
+  shape_common(s, c, vectors, V);
+  const size_t smem = backward_smem(s);
   if (smem > kMostSmem) {
     s.vpt = 0;
     return s;
   }
-  const int threads = warps >= 8 ? warps * 32 : 256;
-  int per_sm = 512 / threads;
-  if (per_sm > kMostSmem / smem) per_sm = kMostSmem / smem;
-  shape_common(s, c, vectors, V, per_sm < 1 ? 1 : per_sm);
+  shape_grid(s, c, V, 512 / s.threads, smem);
   return s;
 }
 
@@ -849,12 +963,12 @@ cudaError_t norm_backward_typed(const moe_norm_config& c, const void* dy, const 
           *dzt = static_cast<const T*>(dz);
   T *dxt = static_cast<T*>(dx), *dbt = static_cast<T*>(dbranch);
   const Shape p = backward_shape(c);
-  auto launch = [&](auto vpt, auto sums_smem) -> cudaError_t {
+  auto launch = [&](auto vpt, auto staged) -> cudaError_t {
     return with_bool(p.aligned, [&](auto aligned) {
       return with_bool(a.drop.on, [&](auto drop) -> cudaError_t {
         auto k = norm_backward_rows_kernel<T, decltype(vpt)::value, decltype(aligned)::value,
-                                           decltype(drop)::value, decltype(sums_smem)::value>;
-        const size_t smem = (p.sums_smem ? 3 : 2) * static_cast<size_t>(p.padded) * 4;
+                                           decltype(drop)::value, decltype(staged)::value>;
+        const size_t smem = backward_smem(p);
         const cudaError_t st = allow_smem(k, smem);
         if (st != cudaSuccess) return st;
         k<<<p.grid, p.threads, smem, s>>>(a, p.group_warps, p.padded, dyt, zt, weight, mean, rstd,
@@ -863,15 +977,11 @@ cudaError_t norm_backward_typed(const moe_norm_config& c, const void* dy, const 
       });
     });
   };
-  if (p.vpt != 0 && p.sums_smem)
-    return launch(std::integral_constant<int, sizeof(T) == 4 ? 8 : 4>{}, std::true_type{});
-  switch (p.vpt) {
-    case 1: return launch(std::integral_constant<int, 1>{}, std::false_type{});
-    case 2: return launch(std::integral_constant<int, 2>{}, std::false_type{});
-    case 4:
-      if constexpr (sizeof(T) == 4)
-        return launch(std::integral_constant<int, 4>{}, std::false_type{});
-  }
+  if (p.vpt == 4) return launch(std::integral_constant<int, 4>{}, std::false_type{});
+  if constexpr (sizeof(T) == 4)
+    if (p.vpt == 8) return launch(std::integral_constant<int, 8>{}, std::false_type{});
+  if (p.vpt == 1) return launch(std::integral_constant<int, 1>{}, std::true_type{});
+  if (p.vpt == 2) return launch(std::integral_constant<int, 2>{}, std::true_type{});
   norm_backward_wide_kernel<T><<<norm_backward_ctas(c), kRowThreads, 0, s>>>(
       a, dyt, zt, weight, mean, rstd, dzt, dxt, dbt, part);
   return cudaGetLastError();
