@@ -675,7 +675,9 @@ moe_status moe_dropout_add(int64_t n, int32_t dtype, double dropout, const uint6
  * the inputs k = 32j + 8t + i, i = 0..7, input i in nibble i / 2 + 4 (i % 2)
  * (nibble 0: the lowest four bits).  Codes past K are not used.
  * The products take x in bf16 and sum in fp32; the scales multiply fp32 sums of
- * one group, so W itself is never rounded.
+ * one group, so W itself is never rounded.  x is held as fp16 times a power of
+ * two of its group: exact for values down to 2^-28 of the group's largest.  An
+ * infinity or a NaN in a row of x makes that row of y NaN.
  */
 typedef struct moe_w4 {
   const uint8_t* codes;
@@ -708,7 +710,7 @@ moe_status moe_linear_w4(int64_t rows, int32_t N, int32_t K, int32_t group, cons
  * expert topk_idx[t, j], over the pairs with keep (NULL: every pair); a token
  * without a kept pair gets zeros.  W1, W3 [E, f, h], W2 [E, h, f] in 4 bits, one
  * group size for the three.  The hidden values enter the second product as two
- * bf16 each (their sum is within 2^-17 of the fp32 value).  bf16 layers only
+ * fp16 numbers each (together within 2^-22 of the fp32 value).  bf16 layers only
  * (MOE_ERR_UNSUPPORTED).  An expert id out of range is reported in ws
  * (moe_check) and its pair left out.  Made for decoding: an expert's weights are
  * read once for every 1024 / k tokens at most; many tokens belong to

@@ -1,0 +1,877 @@
+// The kernel behind the products with 4-bit weights and the 4-bit experts.
+//
+// y = x W^T with few rows of x reads every weight once and should be bound by
+// that stream.  What stands in the way is the work per code.  Making numbers of
+// the codes the usual way (bf16 128 + q, less 128 + zero) takes 11 instructions
+// for 8 of them, and the kernel that did so ran at a third of the memory's
+// rate.  Here nothing is converted: the 16 bits 0x000q ARE the fp16 number
+// q 2^-24 (a subnormal), and 0x00q0 is q 2^-20, so a word of 8 codes becomes
+// four A registers of mma.sync m16n8k16 by four masks and one shift.  Every
+// second pair of inputs has its 16 taken out of x beforehand.
+//
+// For that the rows of x are brought to fp16 once (w4_split_kernel): with a
+// power of two for each group of inputs a bf16 number is exact (down to 2^-28
+// of its group's largest), and an fp32 hidden value is two fp16 numbers, a
+// column each, exact to 2^-22.  The products are exact, their sums are fp32,
+// and what the zero point adds is taken off a group's sum:
+// s (sum q x - z sum x).
+//
+// (E4M3 operands would need two masks and one shift, but mma.sync of that type
+// is run as conversions and fp16 products on this machine: 194 instructions a
+// block of 16 x 128 codes against 75.)
+#pragma once
+
+#include "w4.cuh"
+
+namespace moe {
+namespace w4 {
+
+constexpr int kWarps = 8;        // of a block
+constexpr int kMaxRows = 1024;   // rows of x, or (token, slot) pairs, of one launch
+constexpr int kSms = 152;
+constexpr int kBlocksPerSm = 2;
+
+enum { LINEAR = 0, FC1 = 1, FC2 = 2 };
+
+// fp16 numbers to a value of x.
+__host__ __device__ constexpr int pieces_of(int mode) { return mode == FC2 ? 2 : 1; }
+
+struct Args {
+  // The split rows: fp16 [x_rows][pieces][blocks * 128], the inputs 2, 3, 6 and 7
+  // of eight over 16; and for each group and row {f, f sum}: what a sum of
+  // products is multiplied by, and the group's sum of x in its units.
+  const __half* x;
+  const float2* fx;
+  int x_rows;
+  W4 w0, w1;              // FC1: W1 and W3 (rows g and g + 8 of a tile); else w0 twice
+  int blocks, groups;     // of 128 inputs; groups of a row
+  int N, tiles;           // outputs of an expert, its tiles
+  int splits;             // parts of a row's inputs, items of their own
+  int split_blocks, split_rest;  // blocks / splits and the remainder
+  int wk;                 // narrow: warps that share an item's inputs: 1, 2, 4 or 8
+  int each, each_rest;    // their blocks, in a part of split_blocks and of one more
+  int rows;               // LINEAR: rows of x
+  int out_f32;            // LINEAR
+  void* out;              // LINEAR: y or partial sums; FC1: hidden values; FC2: partial sums
+  // experts
+  const int32_t* idx;
+  const uint8_t* keep;
+  int pairs, E, topk;
+  int* err;
+};
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 q;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "r"(at)
+               : "memory");
+  return q;
+}
+
+__device__ __forceinline__ float2 lds8(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
+// c += A B, or c = A B
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The pairs of a launch sorted by expert, in shared memory; every block works
+// it out for itself, which is cheaper than a launch.
+struct Plan {
+  uint16_t pair[kMaxRows];   // pairs by expert, ascending within one
+  uint16_t token[kMaxRows];  // their tokens
+  uint16_t end[MOE_MAX_EXPERTS];
+  uint16_t first[MOE_MAX_EXPERTS];
+  uint16_t warp_count[kWarps][MOE_MAX_EXPERTS];
+  // chunks of rows of one expert
+  uint16_t chunk_expert[kMaxRows];
+  uint16_t chunk_row[kMaxRows];
+  int scan[kWarps][2];
+  int chunks;
+};
+
+__device__ inline void make_plan(Plan& p, const Args& a, int chunk_rows) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kWarps * MOE_MAX_EXPERTS; i += kWarps * 32)
+    (&p.warp_count[0][0])[i] = 0;
+  __syncthreads();
+  // a warp takes up to four times 32 pairs, one after another: ranks by pair
+  // order within the warp
+  constexpr int kRounds = kMaxRows / (kWarps * 32);
+  const int rounds = (a.pairs + kWarps * 32 - 1) / (kWarps * 32);
+  int expert[kRounds], rank[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    expert[r] = -1;
+    if (r >= rounds) continue;
+    const int i = (warp * rounds + r) * 32 + lane;
+    int e = -1;
+    if (i < a.pairs && !(a.keep && a.keep[i] == 0)) {
+      e = a.idx[i];
+      if (e < 0 || e >= a.E) {
+        if (blockIdx.x == 0) report_error(a.err, DEV_ERR_INDEX, e);
+        e = -1;
+      }
+    }
+    const unsigned same = __match_any_sync(~0u, e);
+    const int before = __popc(same & ((1u << lane) - 1));
+    int base = 0;
+    if (e >= 0) base = p.warp_count[warp][e];
+    __syncwarp();
+    if (e >= 0 && before == 0) p.warp_count[warp][e] = base + __popc(same);
+    __syncwarp();
+    expert[r] = e;
+    rank[r] = base + before;
+  }
+  __syncthreads();
+  // thread e: expert e's count, then the scans of the counts and of the chunks
+  static_assert(kWarps * 32 == MOE_MAX_EXPERTS, "one thread to an expert");
+  int n = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    const int c = p.warp_count[w][tid];
+    p.warp_count[w][tid] = n;
+    n += c;
+  }
+  const int chunks = (n + chunk_rows - 1) / chunk_rows;
+  int sn = n, sc = chunks;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int un = __shfl_up_sync(~0u, sn, o), uc = __shfl_up_sync(~0u, sc, o);
+    if (lane >= o) {
+      sn += un;
+      sc += uc;
+    }
+  }
+  if (lane == 31) {
+    p.scan[warp][0] = sn;
+    p.scan[warp][1] = sc;
+  }
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) {
+    sn += p.scan[w][0];
+    sc += p.scan[w][1];
+  }
+  p.end[tid] = sn;
+  p.first[tid] = sn - n;
+  for (int c = 0; c < chunks; ++c) {
+    p.chunk_expert[sc - chunks + c] = tid;
+    p.chunk_row[sc - chunks + c] = sn - n + c * chunk_rows;
+  }
+  if (tid == kWarps * 32 - 1) p.chunks = sc;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r)
+    if (expert[r] >= 0) {
+      const int at = p.first[expert[r]] + p.warp_count[warp][expert[r]] + rank[r];
+      const int pair = (warp * rounds + r) * 32 + lane;
+      p.pair[at] = pair;
+      p.token[at] = pair / a.topk;
+    }
+  __syncthreads();
+}
+
+// Where a group of warps (wide: a block) stands in its list of items: the rows of one chunk x
+// one part of the inputs x one tile of outputs, tiles first, so that neighbours
+// read the same x.  A group takes every step-th.
+struct Item {
+  int chunk, part, tile;
+  __device__ Item(int first, const Args& a) : chunk(0), part(0), tile(first) { carry(a); }
+  __device__ void next(int step, const Args& a) {
+    tile += step;
+    carry(a);
+  }
+  __device__ void carry(const Args& a) {
+    while (tile >= a.tiles) {
+      tile -= a.tiles;
+      if (++part == a.splits) {
+        part = 0;
+        ++chunk;
+      }
+    }
+  }
+};
+
+// Stores of the sums: two outputs, `low` of row g and `high` of row g + 8 of a
+// tile that begins at output o (FC1: the two halves of feature o), of row r of
+// the chunk.
+template <int MODE>
+__device__ __forceinline__ void put(const Args& a, const Plan& plan, int part, int row_first, int r,
+                                    int o, float low, float high) {
+  low *= 16777216.f;  // 2^24 undoes the codes' 2^-24
+  high *= 16777216.f;
+  if (MODE == FC1) {
+    static_cast<float*>(a.out)[static_cast<int64_t>(row_first + r) * a.N + o] =
+        low / (1.f + expf(-low)) * high;
+  } else if (MODE == FC2) {
+    float* out = static_cast<float*>(a.out) +
+                 (static_cast<int64_t>(part) * a.pairs + plan.pair[row_first + r]) * a.N + o;
+    out[0] = low;
+    out[8] = high;
+  } else {
+    const int64_t at = (static_cast<int64_t>(part) * a.rows + row_first + r) * a.N + o;
+    if (a.out_f32) {
+      float* out = static_cast<float*>(a.out) + at;
+      if (o < a.N) out[0] = low;
+      if (o + 8 < a.N) out[8] = high;
+    } else {
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at;
+      if (o < a.N) out[0] = __float2bfloat16_rn(low);
+      if (o + 8 < a.N) out[8] = __float2bfloat16_rn(high);
+    }
+  }
+}
+
+// A row's scales and zeros of one block of inputs.
+template <int GPB>
+struct Scales {
+  uint32_t s[(GPB + 1) / 2], z;
+};
+// at: the first value's place; valid: values of the row from there on
+template <int GPB, bool TAIL>
+__device__ __forceinline__ void load_scales(Scales<GPB>& v, const W4& w, int64_t at, int valid) {
+  const unsigned short* s = reinterpret_cast<const unsigned short*>(w.scales) + at;
+  if (!TAIL) {
+    if (GPB == 1) {
+      v.s[0] = __ldg(s);
+    } else if (GPB == 2) {
+      v.s[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+    } else {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(s));
+      v.s[0] = q.x;
+      v.s[(GPB + 1) / 2 - 1] = q.y;
+    }
+    if (w.zeros) {
+      const uint8_t* z = w.zeros + at;
+      if (GPB == 1) v.z = __ldg(z);
+      else if (GPB == 2) v.z = __ldg(reinterpret_cast<const unsigned short*>(z));
+      else v.z = __ldg(reinterpret_cast<const uint32_t*>(z));
+    }
+  } else {  // rows of any alignment; past the row's last group: 0
+#pragma unroll
+    for (int q = 0; q < (GPB + 1) / 2; ++q) v.s[q] = 0;
+    v.z = 0;
+#pragma unroll
+    for (int q = 0; q < GPB; ++q) {
+      if (q >= valid) continue;
+      v.s[q / 2] |= static_cast<uint32_t>(__ldg(s + q)) << (16 * (q & 1));
+      if (w.zeros) v.z |= static_cast<uint32_t>(__ldg(w.zeros + at + q)) << (8 * q);
+    }
+  }
+}
+template <int GPB>
+__device__ __forceinline__ float scale_of(const Scales<GPB>& v, int q) {
+  return __uint_as_float(q & 1 ? v.s[q / 2] & 0xffff0000u : v.s[q / 2] << 16);
+}
+template <int GPB>
+__device__ __forceinline__ float zero_of(const Scales<GPB>& v, int q, bool zeros) {
+  return zeros ? static_cast<float>((v.z >> (8 * q)) & 255) : 8.f;
+}
+template <int GPB>
+__device__ __forceinline__ Scales<GPB> scales_from(const Scales<GPB>& v, int lane, bool zeros) {
+  Scales<GPB> r;
+#pragma unroll
+  for (int q = 0; q < (GPB + 1) / 2; ++q) r.s[q] = __shfl_sync(~0u, v.s[q], lane);
+  r.z = zeros ? __shfl_sync(~0u, v.z, lane) : 0;
+  return r;
+}
+// a word's inputs 0 1, 2 3 (times 16), 4 5, 6 7 (times 16) as fp16 pairs
+__device__ __forceinline__ void pairs_of(uint32_t word, uint32_t (&p)[4]) {
+  const uint32_t high = word >> 8;
+  p[0] = word & 0x000f000fu;
+  p[1] = word & 0x00f000f0u;
+  p[2] = high & 0x000f000fu;
+  p[3] = high & 0x00f000f0u;
+}
+
+// Up to 8 columns (8 rows of x; FC2: 4) to a chunk.  A tile is 16 outputs (FC1:
+// 8 features, W1's rows and W3's); wk warps share its inputs, each a run of
+// blocks that it takes in stages of four.  Codes are copied one stage ahead
+// into the warp's ring (cp.async, read by the lane that copied, so without
+// barriers), scales one stage ahead and x one block ahead into registers, all
+// of it across the ends of items.
+template <int MODE, int G32, bool TAIL>
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Args a) {
+  constexpr int GPB = 4 / G32;         // groups of a block
+  constexpr int CP = pieces_of(MODE);  // columns of a row
+  constexpr int XR = 2 / CP;           // rows of x in a lane's two columns
+  constexpr int kRows = 8 / CP;
+  constexpr int SB = 4;                // blocks of a stage
+  constexpr int kStage = SB * 1024;
+  constexpr int kTile = MODE == FC1 ? 8 : 16;
+  constexpr int kRed = 2 * XR * 32;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* red = reinterpret_cast<float*>(smem + kWarps * 2 * kStage);  // 2 buffers
+  Plan& plan = *reinterpret_cast<Plan*>(red + 2 * kWarps * kRed);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int wk = a.wk, group = warp / wk, w_in = warp & (wk - 1);
+  const int first_item = blockIdx.x * (kWarps / wk) + group, step = gridDim.x * (kWarps / wk);
+  const bool zeros = a.w0.zeros != nullptr;
+  pdl_trigger();
+
+  int chunks;
+  if (MODE == LINEAR) {
+    chunks = (a.rows + kRows - 1) / kRows;
+  } else {
+    make_plan(plan, a, kRows);
+    chunks = plan.chunks;
+  }
+
+  // ---- codes and scales, a stage ahead ----
+  const int row_bytes = a.blocks * 64;
+  const uint32_t ring =
+      static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * 2 * kStage + lane * 16;
+  Item it(first_item, a);  // of the stage to come
+  int kb = 0, left = 0;    // its first block; the item's blocks from there on
+  const uint8_t *code0, *code1;  // of the lane's outputs g and g + 8
+  // lane t of a row reads the scales of the stage's block t; the row's lanes
+  // have them from each other by shuffles
+  int64_t sat0 = 0, sat1 = 0;
+  Scales<GPB> scale0, scale1;
+  auto enter = [&]() {
+    if (it.chunk >= chunks) return;
+    const bool rest = it.part < a.split_rest;
+    const int each = rest ? a.each_rest : a.each;
+    kb = it.part * a.split_blocks + min(it.part, a.split_rest) + w_in * each;
+    left = min(each, a.split_blocks + rest - w_in * each);
+    const uint32_t e = MODE == LINEAR ? 0 : plan.chunk_expert[it.chunk];
+    const uint32_t row = e * a.N + static_cast<uint32_t>(it.tile) * kTile;
+    int r0 = g, r1 = MODE == FC1 ? g : g + 8;
+    if (MODE == LINEAR) {  // outputs past the last one repeat it and are not stored
+      r0 = min(r0, a.N - 1 - it.tile * kTile);
+      r1 = min(r1, a.N - 1 - it.tile * kTile);
+    }
+    const uint64_t at = static_cast<uint64_t>(row) * row_bytes + kb * 64 + t * 16;
+    code0 = a.w0.codes + at + r0 * row_bytes;
+    code1 = a.w1.codes + at + r1 * row_bytes;
+    sat0 = sat1 = static_cast<uint64_t>(row) * a.groups + (kb + t) * GPB;
+    sat0 += r0 * a.groups;
+    sat1 += r1 * a.groups;
+  };
+  uint32_t fill = ring;
+  auto fetch = [&]() {
+    if (it.chunk < chunks) {
+#pragma unroll
+      for (int b = 0; b < SB; ++b) {
+        if (b >= left) break;
+        copy_async(fill + b * 1024, code0 + b * 64);
+        copy_async(fill + b * 1024 + 512, code1 + b * 64);
+      }
+      if (t < left) {
+        load_scales<GPB, TAIL>(scale0, a.w0, sat0, a.groups - (kb + t) * GPB);
+        load_scales<GPB, TAIL>(scale1, a.w1, sat1, a.groups - (kb + t) * GPB);
+      }
+      left -= SB;
+      if (left > 0) {
+        kb += SB;
+        code0 += SB * 64;
+        code1 += SB * 64;
+        sat0 += SB * GPB;
+        sat1 += SB * GPB;
+      } else {
+        it.next(step, a);
+        enter();
+      }
+    }
+    copies_commit();
+    fill = 2 * ring + kStage - fill;  // the other of two slots
+  };
+  enter();
+  Item now = it;  // of the stage at hand
+  int kb_now = kb, left_now = left;
+  fetch();
+  pdl_wait();  // the split rows
+
+  uint32_t src = ring;
+  int buf = 0;
+  const int x_row = a.blocks * (128 * CP);
+  while (now.chunk < chunks) {
+    int row_first, row_count;  // of the chunk, in sorted order (LINEAR: in x)
+    if (MODE == LINEAR) {
+      row_first = now.chunk * kRows;
+      row_count = min(kRows, a.rows - row_first);
+    } else {
+      row_first = plan.chunk_row[now.chunk];
+      row_count = min(kRows, plan.end[plan.chunk_expert[now.chunk]] - row_first);
+    }
+    // Column g is piece g % CP of row g / CP; rows past the chunk's repeat its
+    // first and are not stored.  A lane's sums are of the columns 2t, 2t + 1.
+    auto row_of = [&](int r) {
+      if (r >= row_count) r = 0;
+      return MODE == FC1 ? static_cast<int>(plan.token[row_first + r]) : row_first + r;
+    };
+    const __half* xp = a.x + static_cast<int64_t>(row_of(g / CP)) * x_row +
+                       (CP == 2 ? (g & 1) * (x_row / 2) : 0) + kb_now * 128 + t * 8;
+    const float2* fk[XR];
+#pragma unroll
+    for (int i = 0; i < XR; ++i)
+      fk[i] = a.fx + static_cast<int64_t>(kb_now) * GPB * a.x_rows + row_of(XR * t + i);
+    // x and its factors, a block ahead of their use (after the item's last block
+    // this reads on: the buffers have room for it)
+    uint4 x_next[4];
+    float2 f_next[XR][GPB];
+    auto fetch_x = [&]() {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x_next[j] = __ldg(reinterpret_cast<const uint4*>(xp + j * 32));
+      xp += 128;
+#pragma unroll
+      for (int i = 0; i < XR; ++i)
+#pragma unroll
+        for (int q = 0; q < GPB; ++q) {
+          f_next[i][q] = __ldg(fk[i]);
+          fk[i] += a.x_rows;
+        }
+    };
+    fetch_x();
+    float acc[2][XR];  // of the outputs g and g + 8
+#pragma unroll
+    for (int i = 0; i < XR; ++i) acc[0][i] = acc[1][i] = 0.f;
+
+    auto block = [&](int b, const Scales<GPB>& st0, const Scales<GPB>& st1) {
+      uint4 x[4];
+      float2 f[XR][GPB];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = x_next[j];
+#pragma unroll
+      for (int i = 0; i < XR; ++i)
+#pragma unroll
+        for (int q = 0; q < GPB; ++q) f[i][q] = f_next[i][q];
+      fetch_x();
+      const uint4 q0 = lds16(src + b * 1024), q1 = lds16(src + b * 1024 + 512);
+      const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w}, c1[4] = {q1.x, q1.y, q1.z, q1.w};
+      const Scales<GPB> s0 = scales_from(st0, (lane & ~3) + b, zeros);
+      const Scales<GPB> s1 = scales_from(st1, (lane & ~3) + b, zeros);
+#pragma unroll
+      for (int q = 0; q < GPB; ++q) {
+        float sum[4];
+#pragma unroll
+        for (int j = q * G32; j < (q + 1) * G32; ++j) {
+          uint32_t p0[4], p1[4];
+          pairs_of(c0[j], p0);
+          pairs_of(c1[j], p1);
+          if (j == q * G32) mma_first(sum, p0[0], p1[0], p0[1], p1[1], x[j].x, x[j].y);
+          else mma(sum, p0[0], p1[0], p0[1], p1[1], x[j].x, x[j].y);
+          mma(sum, p0[2], p1[2], p0[3], p1[3], x[j].z, x[j].w);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float s = scale_of(i ? s1 : s0, q), z = zero_of(i ? s1 : s0, q, zeros);
+          if (CP == 2) {  // the second piece is in 2^-11 of the first's unit
+            acc[i][0] += s * (f[0][q].x * (sum[2 * i] + 0.00048828125f * sum[2 * i + 1]) -
+                              z * f[0][q].y);
+          } else {
+            acc[i][0] += s * (f[0][q].x * sum[2 * i] - z * f[0][q].y);
+            acc[i][XR - 1] += s * (f[XR - 1][q].x * sum[2 * i + 1] - z * f[XR - 1][q].y);
+          }
+        }
+      }
+    };
+
+    const Item mine = now;
+    for (bool more = true; more;) {
+      const Scales<GPB> st0 = scale0, st1 = scale1;
+      const int blocks = left_now;
+      now = it;
+      kb_now = kb;
+      left_now = left;
+      more = blocks > SB;
+      fetch();
+      copies_wait<1>();
+      if (blocks >= SB) {
+#pragma unroll
+        for (int b = 0; b < SB; ++b) block(b, st0, st1);
+      } else {
+#pragma unroll 1
+        for (int b = 0; b < blocks; ++b) block(b, st0, st1);
+      }
+      src = 2 * ring + kStage - src;
+    }
+
+    // ---- the warps' sums, added in order ----
+    float* all = red + (group * 2 + buf) * wk * kRed;
+#pragma unroll
+    for (int i = 0; i < XR; ++i) {
+      all[w_in * kRed + i * 64 + lane] = acc[0][i];
+      all[w_in * kRed + i * 64 + 32 + lane] = acc[1][i];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(wk * 32) : "memory");
+    for (int i = w_in * 32 + lane; i < XR * 32; i += wk * 32) {
+      const int l = i & 31, c = i >> 5, r = XR * (l & 3) + c;
+      if (r >= row_count) continue;
+      const float* p = all + c * 64 + l;
+      float low = 0.f, high = 0.f;
+      for (int w = 0; w < wk; ++w) {
+        low += p[w * kRed];
+        high += p[w * kRed + 32];
+      }
+      put<MODE>(a, plan, mine.part, row_first, r, mine.tile * kTile + (l >> 2), low, high);
+    }
+    buf ^= 1;
+  }
+  copies_wait<0>();
+}
+
+// More columns: up to 32 (32 rows of x; FC2: 16) to a chunk.  Now x is most of
+// what a multiplication reads, so a block's eight warps take the same inputs at
+// the same time, each for 32 outputs of its own (FC1: 16 features), and share x
+// in shared memory.
+constexpr int kWideSlots = 3;
+constexpr int kWideBlocks = 1;                       // of a stage
+constexpr int kWideX = 32 * 320;                     // a block's x: 32 columns, padded
+constexpr int kWideF = 4 * 32 * 8;                   // its factors, for groups of 32
+constexpr int kWideStage = kWarps * 2048 + kWideX + kWideF;
+
+template <int MODE, int G32, bool TAIL>
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args a) {
+  constexpr int GPB = 4 / G32;
+  constexpr int CP = pieces_of(MODE);
+  constexpr int XR = 2 / CP;
+  constexpr int kRows = 32 / CP;
+  constexpr int kTile = (MODE == FC1 ? 8 : 16) * 2;  // of a warp
+  constexpr int NT = 4, MT = 2, R = 4;
+  extern __shared__ __align__(16) uint8_t smem[];
+  Plan& plan = *reinterpret_cast<Plan*>(smem + kWideSlots * kWideStage);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const bool zeros = a.w0.zeros != nullptr;
+  pdl_trigger();
+
+  int chunks;
+  if (MODE == LINEAR) {
+    chunks = (a.rows + kRows - 1) / kRows;
+  } else {
+    make_plan(plan, a, kRows);
+    chunks = plan.chunks;
+  }
+  auto rows_of = [&](const Item& i, int& first, int& count) {
+    if (MODE == LINEAR) {
+      first = i.chunk * kRows;
+      count = min(kRows, a.rows - first);
+    } else {
+      first = plan.chunk_row[i.chunk];
+      count = min(kRows, plan.end[plan.chunk_expert[i.chunk]] - first);
+    }
+  };
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const int row_bytes = a.blocks * 64, x_row = a.blocks * (128 * CP);
+
+  // ---- a block of inputs at a time, two ahead ----
+  Item it(blockIdx.x, a);
+  int kb = 0, left = 0;
+  const uint8_t* code[R];
+  // lane t of a row brings the scales of its output t (of R), one block ahead
+  int64_t sat = 0;
+  const W4* sw = &a.w0;
+  Scales<GPB> scale_in[2];
+  // thread: 16 bytes of up to four columns' x; the factors of one
+  const __half* xp[2];
+  const float2* fp = nullptr;
+  int columns = 0;
+  auto enter = [&]() {
+    if (it.chunk >= chunks) return;
+    const bool rest = it.part < a.split_rest;
+    kb = it.part * a.split_blocks + min(it.part, a.split_rest);
+    left = a.split_blocks + rest;
+    const uint32_t e = MODE == LINEAR ? 0 : plan.chunk_expert[it.chunk];
+    const int tile = it.tile * (kTile * kWarps) + warp * kTile;  // first output
+    const uint32_t row = e * a.N;
+    // outputs past the last one repeat it and are not stored
+    auto output = [&](int i) {
+      const int o = tile + (MODE == FC1 ? (i >> 1) * 8 + g : i * 8 + g);
+      return row + static_cast<uint32_t>(min(o, a.N - 1));
+    };
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      code[i] = (MODE == FC1 && (i & 1) ? a.w1 : a.w0).codes +
+                static_cast<uint64_t>(output(i)) * row_bytes + kb * 64 + t * 16;
+    sw = MODE == FC1 && (t & 1) ? &a.w1 : &a.w0;
+    sat = static_cast<int64_t>(output(t)) * a.groups + kb * GPB;
+    int first, count;
+    rows_of(it, first, count);
+    columns = count * CP;
+    auto row_of = [&](int r) {
+      return MODE == FC1 ? static_cast<int>(plan.token[first + r]) : first + r;
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = (threadIdx.x >> 4) + 16 * i;  // column, 16 threads to its 256 bytes
+      if (c < columns)
+        xp[i] = a.x + static_cast<int64_t>(row_of(c / CP)) * x_row +
+                (CP == 2 ? (c & 1) * (x_row / 2) : 0) + kb * 128 + (threadIdx.x & 15) * 8;
+    }
+    const int r = threadIdx.x & 31, q = threadIdx.x >> 5;
+    if (q < GPB && r < count)
+      fp = a.fx + (static_cast<int64_t>(kb) * GPB + q) * a.x_rows + row_of(r);
+  };
+  int fill = 0, bring = 0;
+  auto fetch = [&]() {
+    if (it.chunk < chunks) {
+      const uint32_t dst = base + fill * kWideStage;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        copy_async(dst + warp * 2048 + i * 512 + lane * 16, code[i]);
+        code[i] += 64;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = (threadIdx.x >> 4) + 16 * i;
+        if (c < columns) {
+          copy_async(dst + kWarps * 2048 + c * 320 + (threadIdx.x & 15) * 16, xp[i]);
+          xp[i] += 128;
+        }
+      }
+      const int r = threadIdx.x & 31, q = threadIdx.x >> 5;
+      if (q < GPB && r * CP < columns) {
+        copy_async8(dst + kWarps * 2048 + kWideX + (q * 32 + r) * 8, fp);
+        fp += static_cast<int64_t>(GPB) * a.x_rows;
+      }
+      if (bring == 0) load_scales<GPB, TAIL>(scale_in[0], *sw, sat, a.groups - kb * GPB);
+      else load_scales<GPB, TAIL>(scale_in[1], *sw, sat, a.groups - kb * GPB);
+      sat += GPB;
+      ++kb;
+      if (--left == 0) {
+        it.next(gridDim.x, a);
+        enter();
+      }
+    }
+    copies_commit();
+    fill = fill + 1 == kWideSlots ? 0 : fill + 1;
+    bring ^= 1;
+  };
+  enter();
+  Item now[2] = {it, it};  // of the stage at hand and of the next
+  int left_now[2] = {left, 0};
+  pdl_wait();  // the split rows
+  fetch();
+  now[1] = it;
+  left_now[1] = left;
+  fetch();
+
+  int slot = 0, use = 0;
+  while (now[0].chunk < chunks) {
+    const Item mine = now[0];
+    int row_first, row_count;
+    rows_of(mine, row_first, row_count);
+    float acc[MT][NT][2][XR];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < XR; ++i) acc[m][n][0][i] = acc[m][n][1][i] = 0.f;
+
+    for (bool more = true; more;) {
+      copies_wait<1>();
+      __syncthreads();  // everybody's copies are there, and the oldest slot is free
+      const Scales<GPB> mine_s = use ? scale_in[1] : scale_in[0];
+      use ^= 1;
+      more = left_now[0] > 1;
+      now[0] = now[1];
+      left_now[0] = left_now[1];
+      now[1] = it;
+      left_now[1] = left;
+      fetch();
+      const uint32_t src = base + slot * kWideStage;
+      slot = slot + 1 == kWideSlots ? 0 : slot + 1;
+      uint32_t w[R][4];
+      Scales<GPB> s[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const uint4 q = lds16(src + warp * 2048 + i * 512 + lane * 16);
+        w[i][0] = q.x;
+        w[i][1] = q.y;
+        w[i][2] = q.z;
+        w[i][3] = q.w;
+        s[i] = scales_from(mine_s, (lane & ~3) + i, zeros);
+      }
+      const uint32_t xs = src + kWarps * 2048 + g * 320 + t * 16;
+      const uint32_t fs = src + kWarps * 2048 + kWideX;
+#pragma unroll
+      for (int q = 0; q < GPB; ++q) {
+        float sum[MT][NT][4];
+#pragma unroll
+        for (int j = q * G32; j < (q + 1) * G32; ++j) {
+          uint32_t p[R][4];
+#pragma unroll
+          for (int i = 0; i < R; ++i) pairs_of(w[i][j], p[i]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (n > 0 && n * 8 >= row_count * CP) break;
+            const uint4 x = lds16(xs + n * (8 * 320) + j * 64);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const uint32_t(&lo)[4] = p[2 * m], (&hi)[4] = p[2 * m + 1];
+              if (j == q * G32) mma_first(sum[m][n], lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+              else mma(sum[m][n], lo[0], hi[0], lo[1], hi[1], x.x, x.y);
+              mma(sum[m][n], lo[2], hi[2], lo[3], hi[3], x.z, x.w);
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (n > 0 && n * 8 >= row_count * CP) break;
+          float2 f[XR];
+          if (CP == 2) {
+            f[0] = lds8(fs + (q * 32 + n * 4 + t) * 8);
+          } else {
+            const uint4 v = lds16(fs + (q * 32 + n * 8 + 2 * t) * 8);
+            f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+            f[XR - 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float sc = scale_of(s[2 * m + i], q), z = zero_of(s[2 * m + i], q, zeros);
+              const float* u = &sum[m][n][2 * i];
+              if (CP == 2) {
+                acc[m][n][i][0] += sc * (f[0].x * (u[0] + 0.00048828125f * u[1]) - z * f[0].y);
+              } else {
+                acc[m][n][i][0] += sc * (f[0].x * u[0] - z * f[0].y);
+                acc[m][n][i][XR - 1] += sc * (f[XR - 1].x * u[1] - z * f[XR - 1].y);
+              }
+            }
+        }
+      }
+    }
+
+    const int o0 = mine.tile * (kTile * kWarps) + warp * kTile;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int o = o0 + m * (kTile / 2) + g;
+      if (o >= a.N) continue;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < XR; ++i) {
+          const int r = (n * 8 + 2 * t) / CP + i;
+          if (r < row_count)
+            put<MODE>(a, plan, mine.part, row_first, r, o, acc[m][n][0][i], acc[m][n][1][i]);
+        }
+    }
+  }
+  copies_wait<0>();
+}
+
+// How an item's inputs are shared out.  A warp's time is about its blocks, and
+// four more for the item's ends; a launch takes as many rounds as the warps at
+// once need for all items.
+struct Share {
+  int wk;
+  int64_t cost;
+};
+// blocks: of a part; every warp of an item has some, in a part of one more too.
+inline Share share_narrow(int64_t items, int blocks) {
+  constexpr int kAtOnce = kBlocksPerSm * kSms * kWarps;
+  Share best = {1, int64_t{1} << 62};
+  for (int wk = 1; wk <= kWarps; wk *= 2) {
+    const int each = (blocks + wk - 1) / wk, each_rest = (blocks + wk) / wk;
+    if ((wk - 1) * each >= blocks || (wk - 1) * each_rest >= blocks + 1) continue;
+    const int64_t at_once = kAtOnce / wk, rounds = (items + at_once - 1) / at_once;
+    const int64_t cost = rounds * (each_rest + 4);
+    if (cost < best.cost) best = {wk, cost};
+  }
+  return best;
+}
+inline Share share_wide(int64_t items, int blocks) {
+  constexpr int kAtOnce = kBlocksPerSm * kSms;
+  return {1, (items + kAtOnce - 1) / kAtOnce * (blocks + 5)};
+}
+// Parts of a row that are items of their own, where whole rows would leave
+// warps idle; `join`: what adding the parts up costs.
+constexpr int kMostSplits = 8;
+inline int splits_of(int64_t chunks, int N, int blocks, int join, bool wide) {
+  int best = 1;
+  int64_t least = int64_t{1} << 62;
+  const int tile = wide ? 32 * kWarps : 16;
+  const int64_t items = chunks * ((N + tile - 1) / tile);
+  for (int s = 1; s <= kMostSplits && s <= blocks; ++s) {
+    const Share h = wide ? share_wide(items * s, blocks / s) : share_narrow(items * s, blocks / s);
+    const int64_t cost = h.cost + (s > 1 ? join : 0);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+template <int MODE, int G32, bool TAIL>
+cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
+  auto k = wide ? w4_wide_kernel<MODE, G32, TAIL> : w4_narrow_kernel<MODE, G32, TAIL>;
+  const int tile = (MODE == FC1 ? 8 : 16) * (wide ? 2 * kWarps : 1);
+  const int rows = (wide ? 32 : 8) / pieces_of(MODE);
+  const size_t smem = (wide ? kWideSlots * kWideStage
+                            : kWarps * 2 * 4096 + 2 * kWarps * (4 / pieces_of(MODE)) * 32 * 4) +
+                      (MODE == LINEAR ? 0 : sizeof(Plan));
+  const cudaError_t st =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (st != cudaSuccess) return st;
+  a.tiles = (a.N + tile - 1) / tile;
+  const int64_t chunks = MODE == LINEAR ? (a.rows + rows - 1) / rows
+                                         : (a.pairs < a.E ? a.pairs : a.E);  // about
+  const int64_t items = chunks * a.tiles * a.splits;
+  a.split_blocks = a.blocks / a.splits;
+  a.split_rest = a.blocks % a.splits;
+  int64_t blocks = items;
+  if (!wide) {
+    a.wk = share_narrow(items, a.split_blocks).wk;
+    a.each = (a.split_blocks + a.wk - 1) / a.wk;
+    a.each_rest = (a.split_blocks + a.wk) / a.wk;
+    blocks = (items * a.wk + kWarps - 1) / kWarps;
+  }
+  const unsigned grid = static_cast<unsigned>(
+      blocks < kBlocksPerSm * kSms ? blocks : kBlocksPerSm * kSms);
+  return launch_dependent(k, dim3(grid), dim3(kWarps * 32), smem, s, a);
+}
+
+template <int MODE>
+cudaError_t launch_mode(int group, int K, bool wide, const Args& a, cudaStream_t s) {
+  constexpr bool kTail = MODE == LINEAR;  // the layer's dimensions are multiples of 128
+  const bool tail = K % 128 != 0;
+  switch (group) {
+    case 32:
+      return tail ? launch_one<MODE, 1, kTail>(a, wide, s) : launch_one<MODE, 1, false>(a, wide, s);
+    case 64:
+      return tail ? launch_one<MODE, 2, kTail>(a, wide, s) : launch_one<MODE, 2, false>(a, wide, s);
+    default: return launch_one<MODE, 4, false>(a, wide, s);
+  }
+}
+
+// whether that many rows (of an expert) are more than the narrow kernel's columns
+inline bool is_wide(int mode, int64_t rows) { return rows > 8 / pieces_of(mode); }
+
+cudaError_t launch_linear(int group, int K, bool wide, const Args& a, cudaStream_t s);
+cudaError_t launch_fc1(int group, int K, bool wide, const Args& a, cudaStream_t s);
+cudaError_t launch_fc2(int group, int K, bool wide, const Args& a, cudaStream_t s);
+
+}  // namespace w4
+}  // namespace moe
