@@ -16,86 +16,122 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
                      __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u));
 }
 
-// Rows of x into fp16.  One warp takes a row's block of 128 inputs, a lane four
-// of them.  With 2^E the largest magnitude of a group (its exponent),
+// Rows of x into fp16.  With 2^E the largest magnitude of a row (its exponent),
 // x = 2^(E-14) (p0 + 2^-11 p1): p0 is the nearest fp16 number, p1 that of what
-// is left.  Inputs past K give zeros.  A group with an infinity or a NaN gives
-// NaN.
+// is left.  Inputs past K give zeros.  A row with an infinity or a NaN gives
+// NaN.  A block of the launch finds its row's largest magnitude by itself, also
+// where several share the row (few rows: reading it again is cheaper than
+// another launch); then a warp takes a block of 128 inputs at a time, a lane
+// four of them.
 template <typename T, int G32, int CP>
 __global__ void __launch_bounds__(256)
-    w4_split_kernel(int rows, int K, int blocks, const T* x, __half* pieces, float2* fx) {
-  const int lane = threadIdx.x & 31, w = blockIdx.x * 8 + (threadIdx.x >> 5);
+    w4_split_kernel(int K, int blocks, int parts, const T* x, __half* pieces, float* units,
+                    float* sums) {
+  __shared__ float tops[8];
+  __shared__ int bads[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x / parts, part = blockIdx.x % parts;
   pdl_trigger();
-  if (w >= rows * blocks) return;
-  const int row = w / blocks, blk = w - row * blocks, k = blk * 128 + lane * 4;
   pdl_wait();
-  float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (k < K) q = load4(x + static_cast<int64_t>(row) * K + k);
-  float v[4] = {q.x, q.y, q.z, q.w};
-  constexpr int kLanes = G32 * 8;  // of a group
-  float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+  const T* xr = x + static_cast<int64_t>(row) * K;
+  float top = 0.f;
   bool bad = false;  // fmaxf drops a NaN
+#pragma unroll 4
+  for (int k = threadIdx.x * 4; k < K; k += 1024) {
+    const float4 q = load4(xr + k);
+    const float v = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
+    bad |= !(isfinite(q.x) && isfinite(q.y) && isfinite(q.z) && isfinite(q.w));
+    top = fmaxf(top, v);
+  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bad |= !isfinite(v[i]);
-  const unsigned group = kLanes == 32 ? ~0u : ((1u << kLanes % 32) - 1) << (lane & ~(kLanes - 1));
-  bad = (__ballot_sync(~0u, bad) & group) != 0;
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  bad = __any_sync(~0u, bad);
+  if (lane == 0) {
+    tops[warp] = top;
+    bads[warp] = bad;
+  }
+  __syncthreads();
 #pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  for (int w = 0; w < 8; ++w) {
+    top = fmaxf(top, tops[w]);
+    bad |= bads[w] != 0;
+  }
   // the exponent field of 2^(E-14), within what its reciprocal can hold
   int e = static_cast<int>(__float_as_uint(top) >> 23) - 14;
-  e = e < 1 ? 1 : e;
-  const float scale = __uint_as_float(static_cast<uint32_t>(e) << 23);
+  e = e < 1 ? 1 : e > 253 ? 253 : e;
   const float inverse = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] *= inverse;
-  float sum = 0.f, unit = 1.f;
-#pragma unroll
-  for (int p = 0; p < CP; ++p) {
-    __half h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // the inputs 2, 3, 6 and 7 of eight meet codes that stand 4 bits higher
-      const float up = i < 2 ? 1.f : 16.f;
-      h[i] = __float2half_rn(v[i] * (1.f / up));
-      const float held = __half2float(h[i]) * up;
-      sum += held * unit;
-      v[i] = (v[i] - held) * 2048.f;
-    }
-    unit *= 0.00048828125f;
-    __half2 out[2] = {__halves2half2(h[0], h[1]), __halves2half2(h[2], h[3])};
-    *reinterpret_cast<uint2*>(pieces + ((static_cast<int64_t>(row) * CP + p) * blocks + blk) * 128 +
-                              lane * 4) = *reinterpret_cast<uint2*>(out);
-  }
-#pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if ((lane & (kLanes - 1)) == 0) {
-    const float f = bad ? __uint_as_float(0x7fffffffu) : scale;
-    // 2^-24, the codes' unit
-    fx[(static_cast<int64_t>(blk) * (4 / G32) + lane / kLanes) * rows + row] =
-        make_float2(f, f * (sum * 5.9604644775390625e-08f));
-  }
-}
+  if (part == 0 && threadIdx.x == 0)
+    units[row] = __uint_as_float(bad ? 0x7fffffffu : static_cast<uint32_t>(e) << 23);
 
-template <typename T, int CP>
-cudaError_t launch_split(bool dependent, int group, int rows, int K, const T* x, __half* pieces,
-                         float2* fx, cudaStream_t s) {
-  const int blocks = w4_blocks(K);
-  auto k = group == 32 ? w4_split_kernel<T, 1, CP>
-                       : group == 64 ? w4_split_kernel<T, 2, CP> : w4_split_kernel<T, 4, CP>;
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(rows) * blocks + 7) / 8));
-  if (dependent) return launch_dependent(k, grid, dim3(256), 0, s, rows, K, blocks, x, pieces, fx);
-  k<<<grid, 256, 0, s>>>(rows, K, blocks, x, pieces, fx);
-  return cudaGetLastError();
+  for (int blk = part * 8 + warp; blk < blocks; blk += parts * 8) {
+    const int k = blk * 128 + lane * 4;
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < K) q = load4(xr + k);
+    float v[4] = {q.x * inverse, q.y * inverse, q.z * inverse, q.w * inverse};
+    float sum = 0.f, unit = 1.f;
+#pragma unroll
+    for (int p = 0; p < CP; ++p) {
+      __half h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // the inputs 2, 3, 6 and 7 of eight meet codes that stand 4 bits higher
+        const float up = i < 2 ? 1.f : 16.f;
+        h[i] = __float2half_rn(v[i] * (1.f / up));
+        const float held = __half2float(h[i]) * up;
+        sum += held * unit;
+        v[i] = (v[i] - held) * 2048.f;
+      }
+      unit *= 0.00048828125f;
+      __half2 out[2] = {__halves2half2(h[0], h[1]), __halves2half2(h[2], h[3])};
+      *reinterpret_cast<uint2*>(pieces +
+                                ((static_cast<int64_t>(row) * CP + p) * blocks + blk) * 128 +
+                                lane * 4) = *reinterpret_cast<uint2*>(out);
+    }
+    constexpr int kLanes = G32 * 8;  // of a group
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if ((lane & (kLanes - 1)) == 0)  // 2^-24, the codes' unit
+      sums[(static_cast<int64_t>(row) * blocks + blk) * (4 / G32) + lane / kLanes] =
+          sum * 5.9604644775390625e-08f;
+  }
 }
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
-// Bytes of split rows, and of their factors for groups of 32, the most.
-size_t pieces_bytes(size_t rows, int K, int pieces) {
-  return rows * w4_blocks(K) * pieces * 256;
+
+// Split rows in the scratch, with room for the block that the kernels read past
+// the last one.
+struct Split {
+  __half* x;
+  float *unit, *sums;
+};
+size_t split_bytes(size_t rows, int K, int pieces) {
+  const size_t blocks = rows * w4_blocks(K);
+  return align256((blocks * pieces + 1) * 256) + align256(rows * 4) +
+         align256((blocks + 1) * 4 * 4);
 }
-size_t factor_bytes(size_t rows, int K) {
-  // the kernels read one block's further than the last
-  return align256(rows * (w4_blocks(K) + 1) * 4 * sizeof(float2));
+Split split_at(char* at, size_t rows, int K, int pieces) {
+  const size_t blocks = rows * w4_blocks(K);
+  Split p;
+  p.x = reinterpret_cast<__half*>(at);
+  p.unit = reinterpret_cast<float*>(at + align256((blocks * pieces + 1) * 256));
+  p.sums = p.unit + align256(rows * 4) / 4;
+  return p;
+}
+
+template <typename T, int CP>
+cudaError_t launch_split(bool dependent, int group, int rows, int K, const T* x, const Split& p,
+                         cudaStream_t s) {
+  const int blocks = w4_blocks(K);
+  auto k = group == 32 ? w4_split_kernel<T, 1, CP>
+                       : group == 64 ? w4_split_kernel<T, 2, CP> : w4_split_kernel<T, 4, CP>;
+  int parts = 2 * kSms / rows;
+  if (parts > (blocks + 7) / 8) parts = (blocks + 7) / 8;
+  if (parts < 1) parts = 1;
+  const dim3 grid(static_cast<unsigned>(rows * parts));
+  if (dependent)
+    return launch_dependent(k, grid, dim3(256), 0, s, K, blocks, parts, x, p.x, p.unit, p.sums);
+  k<<<grid, 256, 0, s>>>(K, blocks, parts, x, p.x, p.unit, p.sums);
+  return cudaGetLastError();
 }
 
 // y[t] = sum_j p[t, j] sum_s part[s][t, j], over the kept pairs
@@ -187,29 +223,28 @@ ExpertsShape experts_shape(int T, int h, int E, int k, int f) {
 
 size_t w4_linear_scratch(int64_t rows, int N, int K) {
   const LinearShape L = linear_shape(rows, N, K);
-  return pieces_bytes(L.rows, K, 1) + factor_bytes(L.rows, K) +
+  return split_bytes(L.rows, K, 1) +
          (L.splits == 1 ? 0 : static_cast<size_t>(L.splits) * L.rows * N * 4);
 }
 
 cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* x, const W4& W,
                              void* y, int y_dtype, void* scratch, cudaStream_t s) {
   const LinearShape L = linear_shape(rows, N, K);
-  char* at = static_cast<char*>(scratch);
-  __half* pieces = reinterpret_cast<__half*>(at);
-  float2* fx = reinterpret_cast<float2*>(at + pieces_bytes(L.rows, K, 1));
-  float* part = reinterpret_cast<float*>(at + pieces_bytes(L.rows, K, 1) +
-                                         factor_bytes(L.rows, K));
+  const Split xs = split_at(static_cast<char*>(scratch), L.rows, K, 1);
+  float* part =
+      reinterpret_cast<float*>(static_cast<char*>(scratch) + split_bytes(L.rows, K, 1));
   const int out_f32 = y_dtype == MOE_F32;
   for (int64_t r = 0; r < rows; r += L.rows) {
     const int m = static_cast<int>(rows - r < L.rows ? rows - r : L.rows);
     void* out = static_cast<char*>(y) + r * N * (out_f32 ? 4 : 2);
     cudaError_t st = launch_split<__nv_bfloat16, 1>(
-        false, group, m, K, static_cast<const __nv_bfloat16*>(x) + r * K, pieces, fx, s);
+        false, group, m, K, static_cast<const __nv_bfloat16*>(x) + r * K, xs, s);
     if (st != cudaSuccess) return st;
     Args a = {};
-    a.x = pieces;
-    a.fx = fx;
-    a.x_rows = a.rows = m;
+    a.x = xs.x;
+    a.unit = xs.unit;
+    a.sums = xs.sums;
+    a.rows = m;
     a.w0 = a.w1 = W;
     a.blocks = w4_blocks(K);
     a.groups = K / group;
@@ -232,9 +267,8 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
 
 size_t w4_experts_scratch(int T, int h, int E, int k, int f) {
   const ExpertsShape S = experts_shape(T, h, E, k, f);
-  return pieces_bytes(S.tokens, h, 1) + factor_bytes(S.tokens, h) +
-         align256(static_cast<size_t>(S.pairs) * f * 4) + pieces_bytes(S.pairs, f, 2) +
-         factor_bytes(S.pairs, f) + static_cast<size_t>(S.splits) * S.pairs * h * 4;
+  return split_bytes(S.tokens, h, 1) + align256(static_cast<size_t>(S.pairs) * f * 4) +
+         split_bytes(S.pairs, f, 2) + static_cast<size_t>(S.splits) * S.pairs * h * 4;
 }
 
 cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, const void* x,
@@ -243,23 +277,19 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
                               void* y, void* scratch, int* err, cudaStream_t s) {
   const ExpertsShape S = experts_shape(T, h, E, k, f);
   char* at = static_cast<char*>(scratch);
-  auto take = [&](size_t bytes) {
-    char* p = at;
-    at += bytes;
-    return p;
-  };
-  __half* xp = reinterpret_cast<__half*>(take(pieces_bytes(S.tokens, h, 1)));
-  float2* xf = reinterpret_cast<float2*>(take(factor_bytes(S.tokens, h)));
-  float* hidden = reinterpret_cast<float*>(take(align256(static_cast<size_t>(S.pairs) * f * 4)));
-  __half* hp = reinterpret_cast<__half*>(take(pieces_bytes(S.pairs, f, 2)));
-  float2* hf = reinterpret_cast<float2*>(take(factor_bytes(S.pairs, f)));
+  const Split xs = split_at(at, S.tokens, h, 1);
+  at += split_bytes(S.tokens, h, 1);
+  float* hidden = reinterpret_cast<float*>(at);
+  at += align256(static_cast<size_t>(S.pairs) * f * 4);
+  const Split hs = split_at(at, S.pairs, f, 2);
+  at += split_bytes(S.pairs, f, 2);
   float* part = reinterpret_cast<float*>(at);
   for (int t = 0; t < T; t += S.tokens) {
     const int n = T - t < S.tokens ? T - t : S.tokens;
     const int64_t first = static_cast<int64_t>(t) * k;
     cudaError_t st = launch_split<__nv_bfloat16, 1>(
-        false, group, n, h, static_cast<const __nv_bfloat16*>(x) + static_cast<int64_t>(t) * h, xp,
-        xf, s);
+        false, group, n, h, static_cast<const __nv_bfloat16*>(x) + static_cast<int64_t>(t) * h, xs,
+        s);
     if (st != cudaSuccess) return st;
     Args a = {};
     a.idx = topk_idx + first;
@@ -268,9 +298,9 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     a.E = E;
     a.topk = k;
     a.err = err;
-    a.x = xp;
-    a.fx = xf;
-    a.x_rows = n;
+    a.x = xs.x;
+    a.unit = xs.unit;
+    a.sums = xs.sums;
     a.w0 = W1;
     a.w1 = W3;
     a.blocks = w4_blocks(h);
@@ -281,11 +311,11 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     st = launch_fc1(group, h, S.wide1, a, s);
     if (st != cudaSuccess) return st;
     // rows of dropped pairs hold nothing; nobody reads their pieces
-    st = launch_split<float, 2>(true, group, n * k, f, hidden, hp, hf, s);
+    st = launch_split<float, 2>(true, group, n * k, f, hidden, hs, s);
     if (st != cudaSuccess) return st;
-    a.x = hp;
-    a.fx = hf;
-    a.x_rows = n * k;
+    a.x = hs.x;
+    a.unit = hs.unit;
+    a.sums = hs.sums;
     a.w0 = a.w1 = W2;
     a.blocks = w4_blocks(f);
     a.groups = f / group;

@@ -10,9 +10,9 @@
 // second pair of inputs has its 16 taken out of x beforehand.
 //
 // For that the rows of x are brought to fp16 once (w4_split_kernel): with a
-// power of two for each group of inputs a bf16 number is exact (down to 2^-28
-// of its group's largest), and an fp32 hidden value is two fp16 numbers, a
-// column each, exact to 2^-22.  The products are exact, their sums are fp32,
+// power of two for each row a bf16 number is exact (down to 2^-28 of its row's
+// largest), and an fp32 hidden value is two fp16 numbers, a column each, exact
+// to 2^-22.  The products are exact, their sums are fp32,
 // and what the zero point adds is taken off a group's sum:
 // s (sum q x - z sum x).
 //
@@ -38,11 +38,11 @@ __host__ __device__ constexpr int pieces_of(int mode) { return mode == FC2 ? 2 :
 
 struct Args {
   // The split rows: fp16 [x_rows][pieces][blocks * 128], the inputs 2, 3, 6 and 7
-  // of eight over 16; and for each group and row {f, f sum}: what a sum of
-  // products is multiplied by, and the group's sum of x in its units.
+  // of eight over 16; each row's unit; and each group's sum of x in it,
+  // [x_rows][blocks * groups of a block]
   const __half* x;
-  const float2* fx;
-  int x_rows;
+  const float* unit;
+  const float* sums;
   W4 w0, w1;              // FC1: W1 and W3 (rows g and g + 8 of a tile); else w0 twice
   int blocks, groups;     // of 128 inputs; groups of a row
   int N, tiles;           // outputs of an expert, its tiles
@@ -63,8 +63,8 @@ struct Args {
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -85,6 +85,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
 __device__ __forceinline__ float2 lds8(uint32_t at) {
   float2 v;
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float lds4(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
 }
 
@@ -227,8 +233,11 @@ struct Item {
 template <int MODE>
 __device__ __forceinline__ void put(const Args& a, const Plan& plan, int part, int row_first, int r,
                                     int o, float low, float high) {
-  low *= 16777216.f;  // 2^24 undoes the codes' 2^-24
-  high *= 16777216.f;
+  // the row's unit, and 2^24 for the codes' 2^-24
+  const float unit =
+      a.unit[MODE == FC1 ? static_cast<int>(plan.token[row_first + r]) : row_first + r];
+  low = low * 16777216.f * unit;
+  high = high * 16777216.f * unit;
   if (MODE == FC1) {
     static_cast<float*>(a.out)[static_cast<int64_t>(row_first + r) * a.N + o] =
         low / (1.f + expf(-low)) * high;
@@ -257,9 +266,9 @@ struct Scales {
   uint32_t s[(GPB + 1) / 2], z;
 };
 // at: the first value's place; valid: values of the row from there on
-template <int GPB, bool TAIL>
-__device__ __forceinline__ void load_scales(Scales<GPB>& v, const W4& w, int64_t at, int valid) {
-  const unsigned short* s = reinterpret_cast<const unsigned short*>(w.scales) + at;
+template <int GPB, bool ZEROS, bool TAIL>
+__device__ __forceinline__ void load_scales(Scales<GPB>& v, const unsigned short* s,
+                                            const uint8_t* z, int valid) {
   if (!TAIL) {
     if (GPB == 1) {
       v.s[0] = __ldg(s);
@@ -270,8 +279,7 @@ __device__ __forceinline__ void load_scales(Scales<GPB>& v, const W4& w, int64_t
       v.s[0] = q.x;
       v.s[(GPB + 1) / 2 - 1] = q.y;
     }
-    if (w.zeros) {
-      const uint8_t* z = w.zeros + at;
+    if (ZEROS) {
       if (GPB == 1) v.z = __ldg(z);
       else if (GPB == 2) v.z = __ldg(reinterpret_cast<const unsigned short*>(z));
       else v.z = __ldg(reinterpret_cast<const uint32_t*>(z));
@@ -284,7 +292,7 @@ __device__ __forceinline__ void load_scales(Scales<GPB>& v, const W4& w, int64_t
     for (int q = 0; q < GPB; ++q) {
       if (q >= valid) continue;
       v.s[q / 2] |= static_cast<uint32_t>(__ldg(s + q)) << (16 * (q & 1));
-      if (w.zeros) v.z |= static_cast<uint32_t>(__ldg(w.zeros + at + q)) << (8 * q);
+      if (ZEROS) v.z |= static_cast<uint32_t>(__ldg(z + q)) << (8 * q);
     }
   }
 }
@@ -292,16 +300,39 @@ template <int GPB>
 __device__ __forceinline__ float scale_of(const Scales<GPB>& v, int q) {
   return __uint_as_float(q & 1 ? v.s[q / 2] & 0xffff0000u : v.s[q / 2] << 16);
 }
-template <int GPB>
-__device__ __forceinline__ float zero_of(const Scales<GPB>& v, int q, bool zeros) {
-  return zeros ? static_cast<float>((v.z >> (8 * q)) & 255) : 8.f;
+template <int GPB, bool ZEROS>
+__device__ __forceinline__ float zero_of(const Scales<GPB>& v, int q) {
+  return ZEROS ? static_cast<float>((v.z >> (8 * q)) & 255) : 8.f;
 }
-template <int GPB>
-__device__ __forceinline__ Scales<GPB> scales_from(const Scales<GPB>& v, int lane, bool zeros) {
+template <int GPB, bool ZEROS>
+__device__ __forceinline__ Scales<GPB> scales_from(const Scales<GPB>& v, int lane) {
   Scales<GPB> r;
 #pragma unroll
   for (int q = 0; q < (GPB + 1) / 2; ++q) r.s[q] = __shfl_sync(~0u, v.s[q], lane);
-  r.z = zeros ? __shfl_sync(~0u, v.z, lane) : 0;
+  r.z = ZEROS ? __shfl_sync(~0u, v.z, lane) : 0;
+  return r;
+}
+// consecutive groups' sums of x
+template <int N>
+struct Sums {
+  float v[N];
+};
+template <int N>
+__device__ __forceinline__ Sums<N> load_sums(const float* p) {
+  Sums<N> r;
+  if (N == 1) {
+    r.v[0] = __ldg(p);
+  } else if (N == 2) {
+    const float2 q = __ldg(reinterpret_cast<const float2*>(p));
+    r.v[0] = q.x;
+    r.v[N - 1] = q.y;
+  } else {
+    const float4 q = __ldg(reinterpret_cast<const float4*>(p));
+    r.v[0] = q.x;
+    r.v[1 % N] = q.y;
+    r.v[2 % N] = q.z;
+    r.v[N - 1] = q.w;
+  }
   return r;
 }
 // a word's inputs 0 1, 2 3 (times 16), 4 5, 6 7 (times 16) as fp16 pairs
@@ -319,7 +350,7 @@ __device__ __forceinline__ void pairs_of(uint32_t word, uint32_t (&p)[4]) {
 // into the warp's ring (cp.async, read by the lane that copied, so without
 // barriers), scales one stage ahead and x one block ahead into registers, all
 // of it across the ends of items.
-template <int MODE, int G32, bool TAIL>
+template <int MODE, int G32, bool ZEROS, bool TAIL>
 __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Args a) {
   constexpr int GPB = 4 / G32;         // groups of a block
   constexpr int CP = pieces_of(MODE);  // columns of a row
@@ -335,7 +366,6 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int wk = a.wk, group = warp / wk, w_in = warp & (wk - 1);
   const int first_item = blockIdx.x * (kWarps / wk) + group, step = gridDim.x * (kWarps / wk);
-  const bool zeros = a.w0.zeros != nullptr;
   pdl_trigger();
 
   int chunks;
@@ -355,7 +385,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
   const uint8_t *code0, *code1;  // of the lane's outputs g and g + 8
   // lane t of a row reads the scales of the stage's block t; the row's lanes
   // have them from each other by shuffles
-  int64_t sat0 = 0, sat1 = 0;
+  const unsigned short *ps0, *ps1;
+  const uint8_t *pz0, *pz1;
   Scales<GPB> scale0, scale1;
   auto enter = [&]() {
     if (it.chunk >= chunks) return;
@@ -373,9 +404,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
     const uint64_t at = static_cast<uint64_t>(row) * row_bytes + kb * 64 + t * 16;
     code0 = a.w0.codes + at + r0 * row_bytes;
     code1 = a.w1.codes + at + r1 * row_bytes;
-    sat0 = sat1 = static_cast<uint64_t>(row) * a.groups + (kb + t) * GPB;
-    sat0 += r0 * a.groups;
-    sat1 += r1 * a.groups;
+    const uint64_t sat = static_cast<uint64_t>(row) * a.groups + (kb + t) * GPB;
+    ps0 = reinterpret_cast<const unsigned short*>(a.w0.scales) + sat + r0 * a.groups;
+    ps1 = reinterpret_cast<const unsigned short*>(a.w1.scales) + sat + r1 * a.groups;
+    if (ZEROS) {
+      pz0 = a.w0.zeros + sat + r0 * a.groups;
+      pz1 = a.w1.zeros + sat + r1 * a.groups;
+    }
   };
   uint32_t fill = ring;
   auto fetch = [&]() {
@@ -387,16 +422,20 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
         copy_async(fill + b * 1024 + 512, code1 + b * 64);
       }
       if (t < left) {
-        load_scales<GPB, TAIL>(scale0, a.w0, sat0, a.groups - (kb + t) * GPB);
-        load_scales<GPB, TAIL>(scale1, a.w1, sat1, a.groups - (kb + t) * GPB);
+        load_scales<GPB, ZEROS, TAIL>(scale0, ps0, pz0, a.groups - (kb + t) * GPB);
+        load_scales<GPB, ZEROS, TAIL>(scale1, ps1, pz1, a.groups - (kb + t) * GPB);
       }
       left -= SB;
       if (left > 0) {
         kb += SB;
         code0 += SB * 64;
         code1 += SB * 64;
-        sat0 += SB * GPB;
-        sat1 += SB * GPB;
+        ps0 += SB * GPB;
+        ps1 += SB * GPB;
+        if (ZEROS) {
+          pz0 += SB * GPB;
+          pz1 += SB * GPB;
+        }
       } else {
         it.next(step, a);
         enter();
@@ -431,45 +470,38 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
     };
     const __half* xp = a.x + static_cast<int64_t>(row_of(g / CP)) * x_row +
                        (CP == 2 ? (g & 1) * (x_row / 2) : 0) + kb_now * 128 + t * 8;
-    const float2* fk[XR];
+    const float* xs[XR];
 #pragma unroll
     for (int i = 0; i < XR; ++i)
-      fk[i] = a.fx + static_cast<int64_t>(kb_now) * GPB * a.x_rows + row_of(XR * t + i);
-    // x and its factors, a block ahead of their use (after the item's last block
+      xs[i] = a.sums + (static_cast<int64_t>(row_of(XR * t + i)) * a.blocks + kb_now) * GPB;
+    // x and its sums, a block ahead of their use (after the item's last block
     // this reads on: the buffers have room for it)
     uint4 x_next[4];
-    float2 f_next[XR][GPB];
-    auto fetch_x = [&]() {
+    Sums<GPB> sums_next[XR];
+    auto fetch_x = [&](int b) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x_next[j] = __ldg(reinterpret_cast<const uint4*>(xp + j * 32));
-      xp += 128;
+      for (int j = 0; j < 4; ++j)
+        x_next[j] = __ldg(reinterpret_cast<const uint4*>(xp + b * 128 + j * 32));
 #pragma unroll
-      for (int i = 0; i < XR; ++i)
-#pragma unroll
-        for (int q = 0; q < GPB; ++q) {
-          f_next[i][q] = __ldg(fk[i]);
-          fk[i] += a.x_rows;
-        }
+      for (int i = 0; i < XR; ++i) sums_next[i] = load_sums<GPB>(xs[i] + b * GPB);
     };
-    fetch_x();
+    fetch_x(0);
     float acc[2][XR];  // of the outputs g and g + 8
 #pragma unroll
     for (int i = 0; i < XR; ++i) acc[0][i] = acc[1][i] = 0.f;
 
     auto block = [&](int b, const Scales<GPB>& st0, const Scales<GPB>& st1) {
       uint4 x[4];
-      float2 f[XR][GPB];
+      Sums<GPB> sx[XR];
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = x_next[j];
 #pragma unroll
-      for (int i = 0; i < XR; ++i)
-#pragma unroll
-        for (int q = 0; q < GPB; ++q) f[i][q] = f_next[i][q];
-      fetch_x();
+      for (int i = 0; i < XR; ++i) sx[i] = sums_next[i];
+      fetch_x(b + 1);
       const uint4 q0 = lds16(src + b * 1024), q1 = lds16(src + b * 1024 + 512);
       const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w}, c1[4] = {q1.x, q1.y, q1.z, q1.w};
-      const Scales<GPB> s0 = scales_from(st0, (lane & ~3) + b, zeros);
-      const Scales<GPB> s1 = scales_from(st1, (lane & ~3) + b, zeros);
+      const Scales<GPB> s0 = scales_from<GPB, ZEROS>(st0, (lane & ~3) + b);
+      const Scales<GPB> s1 = scales_from<GPB, ZEROS>(st1, (lane & ~3) + b);
 #pragma unroll
       for (int q = 0; q < GPB; ++q) {
         float sum[4];
@@ -484,13 +516,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float s = scale_of(i ? s1 : s0, q), z = zero_of(i ? s1 : s0, q, zeros);
+          const float s = scale_of(i ? s1 : s0, q), z = zero_of<GPB, ZEROS>(i ? s1 : s0, q);
           if (CP == 2) {  // the second piece is in 2^-11 of the first's unit
-            acc[i][0] += s * (f[0][q].x * (sum[2 * i] + 0.00048828125f * sum[2 * i + 1]) -
-                              z * f[0][q].y);
+            acc[i][0] += s * (sum[2 * i] + 0.00048828125f * sum[2 * i + 1] - z * sx[0].v[q]);
           } else {
-            acc[i][0] += s * (f[0][q].x * sum[2 * i] - z * f[0][q].y);
-            acc[i][XR - 1] += s * (f[XR - 1][q].x * sum[2 * i + 1] - z * f[XR - 1][q].y);
+            acc[i][0] += s * (sum[2 * i] - z * sx[0].v[q]);
+            acc[i][XR - 1] += s * (sum[2 * i + 1] - z * sx[XR - 1].v[q]);
           }
         }
       }
@@ -514,6 +545,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
         for (int b = 0; b < blocks; ++b) block(b, st0, st1);
       }
       src = 2 * ring + kStage - src;
+      xp += SB * 128;
+#pragma unroll
+      for (int i = 0; i < XR; ++i) xs[i] += SB * GPB;
     }
 
     // ---- the warps' sums, added in order ----
@@ -547,10 +581,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
 constexpr int kWideSlots = 3;
 constexpr int kWideBlocks = 1;                       // of a stage
 constexpr int kWideX = 32 * 320;                     // a block's x: 32 columns, padded
-constexpr int kWideF = 4 * 32 * 8;                   // its factors, for groups of 32
+constexpr int kWideF = 4 * 32 * 4;                   // its groups' sums
 constexpr int kWideStage = kWarps * 2048 + kWideX + kWideF;
 
-template <int MODE, int G32, bool TAIL>
+template <int MODE, int G32, bool ZEROS, bool TAIL>
 __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args a) {
   constexpr int GPB = 4 / G32;
   constexpr int CP = pieces_of(MODE);
@@ -561,7 +595,6 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args
   extern __shared__ __align__(16) uint8_t smem[];
   Plan& plan = *reinterpret_cast<Plan*>(smem + kWideSlots * kWideStage);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const bool zeros = a.w0.zeros != nullptr;
   pdl_trigger();
 
   int chunks;
@@ -588,12 +621,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args
   int kb = 0, left = 0;
   const uint8_t* code[R];
   // lane t of a row brings the scales of its output t (of R), one block ahead
-  int64_t sat = 0;
-  const W4* sw = &a.w0;
+  const unsigned short* ps;
+  const uint8_t* pz;
   Scales<GPB> scale_in[2];
-  // thread: 16 bytes of up to four columns' x; the factors of one
+  // thread: 16 bytes of up to two columns' x; one group's sum
   const __half* xp[2];
-  const float2* fp = nullptr;
+  const float* xs;
   int columns = 0;
   auto enter = [&]() {
     if (it.chunk >= chunks) return;
@@ -612,8 +645,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args
     for (int i = 0; i < R; ++i)
       code[i] = (MODE == FC1 && (i & 1) ? a.w1 : a.w0).codes +
                 static_cast<uint64_t>(output(i)) * row_bytes + kb * 64 + t * 16;
-    sw = MODE == FC1 && (t & 1) ? &a.w1 : &a.w0;
-    sat = static_cast<int64_t>(output(t)) * a.groups + kb * GPB;
+    const W4& w = MODE == FC1 && (t & 1) ? a.w1 : a.w0;
+    const int64_t sat = static_cast<int64_t>(output(t)) * a.groups + kb * GPB;
+    ps = reinterpret_cast<const unsigned short*>(w.scales) + sat;
+    if (ZEROS) pz = w.zeros + sat;
     int first, count;
     rows_of(it, first, count);
     columns = count * CP;
@@ -629,7 +664,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args
     }
     const int r = threadIdx.x & 31, q = threadIdx.x >> 5;
     if (q < GPB && r < count)
-      fp = a.fx + (static_cast<int64_t>(kb) * GPB + q) * a.x_rows + row_of(r);
+      xs = a.sums + (static_cast<int64_t>(row_of(r)) * a.blocks + kb) * GPB + q;
   };
   int fill = 0, bring = 0;
   auto fetch = [&]() {
@@ -650,12 +685,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args
       }
       const int r = threadIdx.x & 31, q = threadIdx.x >> 5;
       if (q < GPB && r * CP < columns) {
-        copy_async8(dst + kWarps * 2048 + kWideX + (q * 32 + r) * 8, fp);
-        fp += static_cast<int64_t>(GPB) * a.x_rows;
+        copy_async4(dst + kWarps * 2048 + kWideX + (q * 32 + r) * 4, xs);
+        xs += GPB;
       }
-      if (bring == 0) load_scales<GPB, TAIL>(scale_in[0], *sw, sat, a.groups - kb * GPB);
-      else load_scales<GPB, TAIL>(scale_in[1], *sw, sat, a.groups - kb * GPB);
-      sat += GPB;
+      if (bring == 0) load_scales<GPB, ZEROS, TAIL>(scale_in[0], ps, pz, a.groups - kb * GPB);
+      else load_scales<GPB, ZEROS, TAIL>(scale_in[1], ps, pz, a.groups - kb * GPB);
+      ps += GPB;
+      if (ZEROS) pz += GPB;
       ++kb;
       if (--left == 0) {
         it.next(gridDim.x, a);
@@ -710,7 +746,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args
         w[i][1] = q.y;
         w[i][2] = q.z;
         w[i][3] = q.w;
-        s[i] = scales_from(mine_s, (lane & ~3) + i, zeros);
+        s[i] = scales_from<GPB, ZEROS>(mine_s, (lane & ~3) + i);
       }
       const uint32_t xs = src + kWarps * 2048 + g * 320 + t * 16;
       const uint32_t fs = src + kWarps * 2048 + kWideX;
@@ -738,25 +774,26 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if (n > 0 && n * 8 >= row_count * CP) break;
-          float2 f[XR];
+          float sx[XR];
           if (CP == 2) {
-            f[0] = lds8(fs + (q * 32 + n * 4 + t) * 8);
+            sx[0] = lds4(fs + (q * 32 + n * 4 + t) * 4);
           } else {
-            const uint4 v = lds16(fs + (q * 32 + n * 8 + 2 * t) * 8);
-            f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-            f[XR - 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+            const float2 v = lds8(fs + (q * 32 + n * 8 + 2 * t) * 4);
+            sx[0] = v.x;
+            sx[XR - 1] = v.y;
           }
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float sc = scale_of(s[2 * m + i], q), z = zero_of(s[2 * m + i], q, zeros);
+              const float sc = scale_of(s[2 * m + i], q);
+              const float z = zero_of<GPB, ZEROS>(s[2 * m + i], q);
               const float* u = &sum[m][n][2 * i];
               if (CP == 2) {
-                acc[m][n][i][0] += sc * (f[0].x * (u[0] + 0.00048828125f * u[1]) - z * f[0].y);
+                acc[m][n][i][0] += sc * (u[0] + 0.00048828125f * u[1] - z * sx[0]);
               } else {
-                acc[m][n][i][0] += sc * (f[0].x * u[0] - z * f[0].y);
-                acc[m][n][i][XR - 1] += sc * (f[XR - 1].x * u[1] - z * f[XR - 1].y);
+                acc[m][n][i][0] += sc * (u[0] - z * sx[0]);
+                acc[m][n][i][XR - 1] += sc * (u[1] - z * sx[XR - 1]);
               }
             }
         }
@@ -824,9 +861,10 @@ inline int splits_of(int64_t chunks, int N, int blocks, int join, bool wide) {
   return best;
 }
 
-template <int MODE, int G32, bool TAIL>
+template <int MODE, int G32, bool ZEROS, bool TAIL>
 cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
-  auto k = wide ? w4_wide_kernel<MODE, G32, TAIL> : w4_narrow_kernel<MODE, G32, TAIL>;
+  auto k = wide ? w4_wide_kernel<MODE, G32, ZEROS, TAIL>
+                : w4_narrow_kernel<MODE, G32, ZEROS, TAIL>;
   const int tile = (MODE == FC1 ? 8 : 16) * (wide ? 2 * kWarps : 1);
   const int rows = (wide ? 32 : 8) / pieces_of(MODE);
   const size_t smem = (wide ? kWideSlots * kWideStage
@@ -853,16 +891,24 @@ cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
   return launch_dependent(k, dim3(grid), dim3(kWarps * 32), smem, s, a);
 }
 
+template <int MODE, int G32>
+cudaError_t launch_group(int K, bool wide, const Args& a, cudaStream_t s) {
+  // K is a multiple of the group, and of 128 in the layer
+  if constexpr (MODE == LINEAR && G32 < 4) {
+    if (K % 128 != 0)
+      return a.w0.zeros ? launch_one<MODE, G32, true, true>(a, wide, s)
+                        : launch_one<MODE, G32, false, true>(a, wide, s);
+  }
+  return a.w0.zeros ? launch_one<MODE, G32, true, false>(a, wide, s)
+                    : launch_one<MODE, G32, false, false>(a, wide, s);
+}
+
 template <int MODE>
 cudaError_t launch_mode(int group, int K, bool wide, const Args& a, cudaStream_t s) {
-  constexpr bool kTail = MODE == LINEAR;  // the layer's dimensions are multiples of 128
-  const bool tail = K % 128 != 0;
   switch (group) {
-    case 32:
-      return tail ? launch_one<MODE, 1, kTail>(a, wide, s) : launch_one<MODE, 1, false>(a, wide, s);
-    case 64:
-      return tail ? launch_one<MODE, 2, kTail>(a, wide, s) : launch_one<MODE, 2, false>(a, wide, s);
-    default: return launch_one<MODE, 4, false>(a, wide, s);
+    case 32: return launch_group<MODE, 1>(K, wide, a, s);
+    case 64: return launch_group<MODE, 2>(K, wide, a, s);
+    default: return launch_group<MODE, 4>(K, wide, a, s);
   }
 }
 
