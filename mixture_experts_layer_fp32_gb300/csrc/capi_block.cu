@@ -80,6 +80,9 @@ moe_status validate_linear(int64_t rows, int32_t N, int32_t K) {
 moe_status validate_experts(const moe_config* cfg) {
   size_t bytes = 0;
   MOE_TRY(moe_workspace_size(cfg, &bytes));
+  // rows of a weight, over all experts, are counted in 32 bits
+  const int64_t most = (int64_t{1} << 31) / cfg->num_experts;
+  if (cfg->hidden >= most || cfg->ffn_hidden >= most) return MOE_ERR_UNSUPPORTED;
   return cfg->dtype == MOE_BF16 ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
@@ -233,7 +236,8 @@ moe_status moe_linear_w4(int64_t rows, int32_t N, int32_t K, int32_t group, cons
   MOE_TRY(need(y, rows));
   MOE_TRY(check_ws(ws, ws_bytes, kErrBytes + w4_linear_scratch(rows, N, K)));
   if (rows == 0) return MOE_OK;
-  MOE_CUDA(launch_w4_linear(rows, N, K, group, x, w, y, y_dtype, past_error_word(ws), stream));
+  MOE_CUDA(launch_w4_linear(rows, N, K, group, x, w, y, y_dtype, past_error_word(ws),
+                            static_cast<int*>(ws), stream));
   return MOE_OK;
 }
 

@@ -305,7 +305,7 @@ cudaError_t launch_w4_pack(int E, int N, int K, const uint8_t* values, uint8_t* 
 // bytes of scratch, and the product of `rows` rows
 size_t w4_linear_scratch(int64_t rows, int N, int K);
 cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* x, const W4& W,
-                             void* y, int y_dtype, void* scratch, cudaStream_t s);
+                             void* y, int y_dtype, void* scratch, int* err, cudaStream_t s);
 size_t w4_experts_scratch(int T, int h, int E, int k, int f);
 cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, const void* x,
                               const int32_t* topk_idx, const float* topk_prob,

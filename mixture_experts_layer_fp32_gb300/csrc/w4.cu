@@ -221,6 +221,34 @@ ExpertsShape experts_shape(int T, int h, int E, int k, int f) {
 
 }  // namespace
 
+namespace w4 {
+
+bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, int box_rows) {
+  typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const EncodeTiledFn encode = []() -> EncodeTiledFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(blocks) * 64, 64};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 4}, unit[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides,
+                box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace w4
+
 size_t w4_linear_scratch(int64_t rows, int N, int K) {
   const LinearShape L = linear_shape(rows, N, K);
   return split_bytes(L.rows, K, 1) +
@@ -228,7 +256,7 @@ size_t w4_linear_scratch(int64_t rows, int N, int K) {
 }
 
 cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* x, const W4& W,
-                             void* y, int y_dtype, void* scratch, cudaStream_t s) {
+                             void* y, int y_dtype, void* scratch, int* err, cudaStream_t s) {
   const LinearShape L = linear_shape(rows, N, K);
   const Split xs = split_at(static_cast<char*>(scratch), L.rows, K, 1);
   float* part =
@@ -245,6 +273,7 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
     a.unit = xs.unit;
     a.sums = xs.sums;
     a.rows = m;
+    a.err = err;
     a.w0 = a.w1 = W;
     a.blocks = w4_blocks(K);
     a.groups = K / group;

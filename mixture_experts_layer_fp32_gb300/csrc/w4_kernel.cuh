@@ -21,6 +21,7 @@
 // block of 16 x 128 codes against 75.)
 #pragma once
 
+#include "sm100_ptx.cuh"
 #include "w4.cuh"
 
 namespace moe {
@@ -47,9 +48,9 @@ struct Args {
   int blocks, groups;     // of 128 inputs; groups of a row
   int N, tiles;           // outputs of an expert, its tiles
   int splits;             // parts of a row's inputs, items of their own
-  int split_blocks, split_rest;  // blocks / splits and the remainder
+  int split_units, split_rest;  // units / splits and the remainder: narrow stages, wide blocks
   int wk;                 // narrow: warps that share an item's inputs: 1, 2, 4 or 8
-  int each, each_rest;    // their blocks, in a part of split_blocks and of one more
+  int each, each_rest;    // their units, in a part of split_units and of one more
   int rows;               // LINEAR: rows of x
   int out_f32;            // LINEAR
   void* out;              // LINEAR: y or partial sums; FC1: hidden values; FC2: partial sums
@@ -346,12 +347,18 @@ __device__ __forceinline__ void pairs_of(uint32_t word, uint32_t (&p)[4]) {
 
 // Up to 8 columns (8 rows of x; FC2: 4) to a chunk.  A tile is 16 outputs (FC1:
 // 8 features, W1's rows and W3's); wk warps share its inputs, each a run of
-// blocks that it takes in stages of four.  Codes are copied one stage ahead
-// into the warp's ring (cp.async, read by the lane that copied, so without
-// barriers), scales one stage ahead and x one block ahead into registers, all
-// of it across the ends of items.
+// stages of four blocks.  Codes come by TMA, one stage ahead and across the ends
+// of items, into a ring of the warp's own: one instruction for 4 KB, and their
+// way is not L1's.  That matters more than the instructions: L1 answers in
+// order, so that a read of x that would hit waits behind every copy that misses
+// (the same kernel with cp.async took 15.8 us for 38912 x 4096 codes, 9.8 us
+// without the reads of x).  Scales are read one stage ahead, x one block ahead,
+// into registers.
+constexpr long long kWaitCycles = 2000000000ll;  // a second: a copy that never arrived
+
 template <int MODE, int G32, bool ZEROS, bool TAIL>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Args a) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(
+    const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1, Args a) {
   constexpr int GPB = 4 / G32;         // groups of a block
   constexpr int CP = pieces_of(MODE);  // columns of a row
   constexpr int XR = 2 / CP;           // rows of x in a lane's two columns
@@ -360,8 +367,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
   constexpr int kStage = SB * 1024;
   constexpr int kTile = MODE == FC1 ? 8 : 16;
   constexpr int kRed = 2 * XR * 32;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   float* red = reinterpret_cast<float*>(smem + kWarps * 2 * kStage);  // 2 buffers
+  __shared__ uint64_t bars[kWarps][2];
   Plan& plan = *reinterpret_cast<Plan*>(red + 2 * kWarps * kRed);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int wk = a.wk, group = warp / wk, w_in = warp & (wk - 1);
@@ -376,15 +384,21 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
     chunks = plan.chunks;
   }
 
+  const uint32_t ring = ptx::smem_u32(smem) + warp * 2 * kStage;
+  const uint32_t bar = ptx::smem_u32(&bars[warp][0]);
+  if (lane == 0) {
+    ptx::mbar_init(bar, 1);
+    ptx::mbar_init(bar + 8, 1);
+    ptx::fence_mbar_init();
+  }
+  __syncwarp();
+
   // ---- codes and scales, a stage ahead ----
-  const int row_bytes = a.blocks * 64;
-  const uint32_t ring =
-      static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * 2 * kStage + lane * 16;
   Item it(first_item, a);  // of the stage to come
-  int kb = 0, left = 0;    // its first block; the item's blocks from there on
-  const uint8_t *code0, *code1;  // of the lane's outputs g and g + 8
-  // lane t of a row reads the scales of the stage's block t; the row's lanes
-  // have them from each other by shuffles
+  int stage = 0, left = 0; // its number in the row; the item's stages from there on
+  uint32_t row = 0;        // the tile's first output
+  // lane t of a row (g, g + 8) reads the scales of the stage's block t; the row's
+  // lanes have them from each other by shuffles
   const unsigned short *ps0, *ps1;
   const uint8_t *pz0, *pz1;
   Scales<GPB> scale0, scale1;
@@ -392,66 +406,62 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
     if (it.chunk >= chunks) return;
     const bool rest = it.part < a.split_rest;
     const int each = rest ? a.each_rest : a.each;
-    kb = it.part * a.split_blocks + min(it.part, a.split_rest) + w_in * each;
-    left = min(each, a.split_blocks + rest - w_in * each);
+    stage = it.part * a.split_units + min(it.part, a.split_rest) + w_in * each;
+    left = min(each, a.split_units + rest - w_in * each);
     const uint32_t e = MODE == LINEAR ? 0 : plan.chunk_expert[it.chunk];
-    const uint32_t row = e * a.N + static_cast<uint32_t>(it.tile) * kTile;
+    row = e * a.N + static_cast<uint32_t>(it.tile) * kTile;
     int r0 = g, r1 = MODE == FC1 ? g : g + 8;
-    if (MODE == LINEAR) {  // outputs past the last one repeat it and are not stored
+    if (MODE == LINEAR) {  // outputs past the last one take its scales and are not stored
       r0 = min(r0, a.N - 1 - it.tile * kTile);
       r1 = min(r1, a.N - 1 - it.tile * kTile);
     }
-    const uint64_t at = static_cast<uint64_t>(row) * row_bytes + kb * 64 + t * 16;
-    code0 = a.w0.codes + at + r0 * row_bytes;
-    code1 = a.w1.codes + at + r1 * row_bytes;
-    const uint64_t sat = static_cast<uint64_t>(row) * a.groups + (kb + t) * GPB;
-    ps0 = reinterpret_cast<const unsigned short*>(a.w0.scales) + sat + r0 * a.groups;
-    ps1 = reinterpret_cast<const unsigned short*>(a.w1.scales) + sat + r1 * a.groups;
+    const uint64_t at = static_cast<uint64_t>(row) * a.groups + (stage * SB + t) * GPB;
+    ps0 = reinterpret_cast<const unsigned short*>(a.w0.scales) + at + r0 * a.groups;
+    ps1 = reinterpret_cast<const unsigned short*>(a.w1.scales) + at + r1 * a.groups;
     if (ZEROS) {
-      pz0 = a.w0.zeros + sat + r0 * a.groups;
-      pz1 = a.w1.zeros + sat + r1 * a.groups;
+      pz0 = a.w0.zeros + at + r0 * a.groups;
+      pz1 = a.w1.zeros + at + r1 * a.groups;
     }
   };
-  uint32_t fill = ring;
+  int fill = 0;
   auto fetch = [&]() {
-    if (it.chunk < chunks) {
-#pragma unroll
-      for (int b = 0; b < SB; ++b) {
-        if (b >= left) break;
-        copy_async(fill + b * 1024, code0 + b * 64);
-        copy_async(fill + b * 1024 + 512, code1 + b * 64);
-      }
-      if (t < left) {
-        load_scales<GPB, ZEROS, TAIL>(scale0, ps0, pz0, a.groups - (kb + t) * GPB);
-        load_scales<GPB, ZEROS, TAIL>(scale1, ps1, pz1, a.groups - (kb + t) * GPB);
-      }
-      left -= SB;
-      if (left > 0) {
-        kb += SB;
-        code0 += SB * 64;
-        code1 += SB * 64;
-        ps0 += SB * GPB;
-        ps1 += SB * GPB;
-        if (ZEROS) {
-          pz0 += SB * GPB;
-          pz1 += SB * GPB;
-        }
-      } else {
-        it.next(step, a);
-        enter();
-      }
+    if (it.chunk >= chunks) return;
+    __syncwarp();  // every lane has read what the slot held
+    if (lane == 0) {
+      const uint32_t dst = ring + fill * kStage, b = bar + fill * 8;
+      ptx::mbar_arrive_expect_tx(b, kStage);
+      // blocks past the row's end come as zeros
+      ptx::tma_load_3d(dst, &map0, 0, static_cast<int>(row), stage * SB, b);
+      if (MODE == FC1)
+        ptx::tma_load_3d(dst + kStage / 2, &map1, 0, static_cast<int>(row), stage * SB, b);
     }
-    copies_commit();
-    fill = 2 * ring + kStage - fill;  // the other of two slots
+    const int valid = a.groups - (stage * SB + t) * GPB;  // groups from the lane's block on
+    if (valid > 0) {
+      load_scales<GPB, ZEROS, TAIL>(scale0, ps0, pz0, valid);
+      load_scales<GPB, ZEROS, TAIL>(scale1, ps1, pz1, valid);
+    }
+    if (--left > 0) {
+      ++stage;
+      ps0 += SB * GPB;
+      ps1 += SB * GPB;
+      if (ZEROS) {
+        pz0 += SB * GPB;
+        pz1 += SB * GPB;
+      }
+    } else {
+      it.next(step, a);
+      enter();
+    }
+    fill ^= 1;
   };
   enter();
   Item now = it;  // of the stage at hand
-  int kb_now = kb, left_now = left;
+  int stage_now = stage, left_now = left;
   fetch();
   pdl_wait();  // the split rows
 
-  uint32_t src = ring;
-  int buf = 0;
+  int use = 0, phase = 0, buf = 0;  // the slot at hand and its barrier's phase
+  bool lost = false;
   const int x_row = a.blocks * (128 * CP);
   while (now.chunk < chunks) {
     int row_first, row_count;  // of the chunk, in sorted order (LINEAR: in x)
@@ -469,11 +479,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
       return MODE == FC1 ? static_cast<int>(plan.token[row_first + r]) : row_first + r;
     };
     const __half* xp = a.x + static_cast<int64_t>(row_of(g / CP)) * x_row +
-                       (CP == 2 ? (g & 1) * (x_row / 2) : 0) + kb_now * 128 + t * 8;
+                       (CP == 2 ? (g & 1) * (x_row / 2) : 0) + stage_now * (SB * 128) + t * 8;
     const float* xs[XR];
 #pragma unroll
     for (int i = 0; i < XR; ++i)
-      xs[i] = a.sums + (static_cast<int64_t>(row_of(XR * t + i)) * a.blocks + kb_now) * GPB;
+      xs[i] = a.sums +
+              (static_cast<int64_t>(row_of(XR * t + i)) * a.blocks + stage_now * SB) * GPB;
     // x and its sums, a block ahead of their use (after the item's last block
     // this reads on: the buffers have room for it)
     uint4 x_next[4];
@@ -490,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
 #pragma unroll
     for (int i = 0; i < XR; ++i) acc[0][i] = acc[1][i] = 0.f;
 
-    auto block = [&](int b, const Scales<GPB>& st0, const Scales<GPB>& st1) {
+    auto block = [&](int b, uint32_t src, const Scales<GPB>& st0, const Scales<GPB>& st1) {
       uint4 x[4];
       Sums<GPB> sx[XR];
 #pragma unroll
@@ -498,7 +509,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
 #pragma unroll
       for (int i = 0; i < XR; ++i) sx[i] = sums_next[i];
       fetch_x(b + 1);
-      const uint4 q0 = lds16(src + b * 1024), q1 = lds16(src + b * 1024 + 512);
+      constexpr uint32_t kSecond = MODE == FC1 ? kStage / 2 : 512;
+      const uint4 q0 = lds16(src + b * (MODE == FC1 ? 512 : 1024));
+      const uint4 q1 = lds16(src + b * (MODE == FC1 ? 512 : 1024) + kSecond);
       const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w}, c1[4] = {q1.x, q1.y, q1.z, q1.w};
       const Scales<GPB> s0 = scales_from<GPB, ZEROS>(st0, (lane & ~3) + b);
       const Scales<GPB> s1 = scales_from<GPB, ZEROS>(st1, (lane & ~3) + b);
@@ -530,21 +543,31 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
     const Item mine = now;
     for (bool more = true; more;) {
       const Scales<GPB> st0 = scale0, st1 = scale1;
-      const int blocks = left_now;
+      const int blocks = min(SB, a.blocks - stage_now * SB);
+      more = left_now > 1;
       now = it;
-      kb_now = kb;
+      stage_now = stage;
       left_now = left;
-      more = blocks > SB;
       fetch();
-      copies_wait<1>();
-      if (blocks >= SB) {
+      if (!lost && !ptx::mbar_try_wait(bar + use * 8, phase)) {
+        const long long began = clock64();
+        while (!lost && !ptx::mbar_try_wait(bar + use * 8, phase))
+          if (clock64() - began > kWaitCycles) {
+            // go on with what is there, so that nobody waits for this warp
+            lost = true;
+            report_error(a.err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
+          }
+      }
+      const uint32_t src = ring + use * kStage + lane * 16;
+      if (blocks == SB) {
 #pragma unroll
-        for (int b = 0; b < SB; ++b) block(b, st0, st1);
+        for (int b = 0; b < SB; ++b) block(b, src, st0, st1);
       } else {
 #pragma unroll 1
-        for (int b = 0; b < blocks; ++b) block(b, st0, st1);
+        for (int b = 0; b < blocks; ++b) block(b, src, st0, st1);
       }
-      src = 2 * ring + kStage - src;
+      phase ^= use;
+      use ^= 1;
       xp += SB * 128;
 #pragma unroll
       for (int i = 0; i < XR; ++i) xs[i] += SB * GPB;
@@ -571,7 +594,6 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(Ar
     }
     buf ^= 1;
   }
-  copies_wait<0>();
 }
 
 // More columns: up to 32 (32 rows of x; FC2: 16) to a chunk.  Now x is most of
@@ -592,7 +614,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args
   constexpr int kRows = 32 / CP;
   constexpr int kTile = (MODE == FC1 ? 8 : 16) * 2;  // of a warp
   constexpr int NT = 4, MT = 2, R = 4;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   Plan& plan = *reinterpret_cast<Plan*>(smem + kWideSlots * kWideStage);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   pdl_trigger();
@@ -631,8 +653,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args
   auto enter = [&]() {
     if (it.chunk >= chunks) return;
     const bool rest = it.part < a.split_rest;
-    kb = it.part * a.split_blocks + min(it.part, a.split_rest);
-    left = a.split_blocks + rest;
+    kb = it.part * a.split_units + min(it.part, a.split_rest);
+    left = a.split_units + rest;
     const uint32_t e = MODE == LINEAR ? 0 : plan.chunk_expert[it.chunk];
     const int tile = it.tile * (kTile * kWarps) + warp * kTile;  // first output
     const uint32_t row = e * a.N;
@@ -825,15 +847,15 @@ struct Share {
   int wk;
   int64_t cost;
 };
-// blocks: of a part; every warp of an item has some, in a part of one more too.
-inline Share share_narrow(int64_t items, int blocks) {
+// stages: of a part; every warp of an item has some, in a part of one more too.
+inline Share share_narrow(int64_t items, int stages) {
   constexpr int kAtOnce = kBlocksPerSm * kSms * kWarps;
   Share best = {1, int64_t{1} << 62};
   for (int wk = 1; wk <= kWarps; wk *= 2) {
-    const int each = (blocks + wk - 1) / wk, each_rest = (blocks + wk) / wk;
-    if ((wk - 1) * each >= blocks || (wk - 1) * each_rest >= blocks + 1) continue;
+    const int each = (stages + wk - 1) / wk, each_rest = (stages + wk) / wk;
+    if ((wk - 1) * each >= stages || (wk - 1) * each_rest >= stages + 1) continue;
     const int64_t at_once = kAtOnce / wk, rounds = (items + at_once - 1) / at_once;
-    const int64_t cost = rounds * (each_rest + 4);
+    const int64_t cost = rounds * (each_rest * 4 + 4);
     if (cost < best.cost) best = {wk, cost};
   }
   return best;
@@ -850,8 +872,9 @@ inline int splits_of(int64_t chunks, int N, int blocks, int join, bool wide) {
   int64_t least = int64_t{1} << 62;
   const int tile = wide ? 32 * kWarps : 16;
   const int64_t items = chunks * ((N + tile - 1) / tile);
-  for (int s = 1; s <= kMostSplits && s <= blocks; ++s) {
-    const Share h = wide ? share_wide(items * s, blocks / s) : share_narrow(items * s, blocks / s);
+  const int units = wide ? blocks : (blocks + 3) / 4;
+  for (int s = 1; s <= kMostSplits && s <= units; ++s) {
+    const Share h = wide ? share_wide(items * s, units / s) : share_narrow(items * s, units / s);
     const int64_t cost = h.cost + (s > 1 ? join : 0);
     if (cost < least) {
       least = cost;
@@ -861,34 +884,51 @@ inline int splits_of(int64_t chunks, int N, int blocks, int join, bool wide) {
   return best;
 }
 
+// The codes of `rows` rows as [blocks][rows][64 bytes], boxes of 4 blocks
+bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, int box_rows);
+
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes));
+}
+
 template <int MODE, int G32, bool ZEROS, bool TAIL>
 cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
-  auto k = wide ? w4_wide_kernel<MODE, G32, ZEROS, TAIL>
-                : w4_narrow_kernel<MODE, G32, ZEROS, TAIL>;
   const int tile = (MODE == FC1 ? 8 : 16) * (wide ? 2 * kWarps : 1);
   const int rows = (wide ? 32 : 8) / pieces_of(MODE);
-  const size_t smem = (wide ? kWideSlots * kWideStage
-                            : kWarps * 2 * 4096 + 2 * kWarps * (4 / pieces_of(MODE)) * 32 * 4) +
-                      (MODE == LINEAR ? 0 : sizeof(Plan));
-  const cudaError_t st =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (st != cudaSuccess) return st;
+  const size_t plan = MODE == LINEAR ? 0 : sizeof(Plan);
   a.tiles = (a.N + tile - 1) / tile;
   const int64_t chunks = MODE == LINEAR ? (a.rows + rows - 1) / rows
                                          : (a.pairs < a.E ? a.pairs : a.E);  // about
   const int64_t items = chunks * a.tiles * a.splits;
-  a.split_blocks = a.blocks / a.splits;
-  a.split_rest = a.blocks % a.splits;
-  int64_t blocks = items;
-  if (!wide) {
-    a.wk = share_narrow(items, a.split_blocks).wk;
-    a.each = (a.split_blocks + a.wk - 1) / a.wk;
-    a.each_rest = (a.split_blocks + a.wk) / a.wk;
-    blocks = (items * a.wk + kWarps - 1) / kWarps;
+  const int units = wide ? a.blocks : (a.blocks + 3) / 4;
+  a.split_units = units / a.splits;
+  a.split_rest = units % a.splits;
+  constexpr int kMostBlocks = kBlocksPerSm * kSms;
+  if (wide) {
+    auto k = w4_wide_kernel<MODE, G32, ZEROS, TAIL>;
+    const size_t smem = kWideSlots * kWideStage + plan;
+    const cudaError_t st = allow_smem(k, smem);
+    if (st != cudaSuccess) return st;
+    const unsigned grid = static_cast<unsigned>(items < kMostBlocks ? items : kMostBlocks);
+    return launch_dependent(k, dim3(grid), dim3(kWarps * 32), smem, s, a);
   }
-  const unsigned grid = static_cast<unsigned>(
-      blocks < kBlocksPerSm * kSms ? blocks : kBlocksPerSm * kSms);
-  return launch_dependent(k, dim3(grid), dim3(kWarps * 32), smem, s, a);
+  auto k = w4_narrow_kernel<MODE, G32, ZEROS, TAIL>;
+  const size_t smem = kWarps * 2 * 4096 + 2 * kWarps * (4 / pieces_of(MODE)) * 32 * 4 + plan;
+  const cudaError_t st = allow_smem(k, smem);
+  if (st != cudaSuccess) return st;
+  a.wk = share_narrow(items, a.split_units).wk;
+  a.each = (a.split_units + a.wk - 1) / a.wk;
+  a.each_rest = (a.split_units + a.wk) / a.wk;
+  const int64_t all = static_cast<int64_t>(MODE == LINEAR ? 1 : a.E) * a.N;
+  CUtensorMap m0, m1;
+  if (!map_codes(&m0, a.w0.codes, all, a.blocks, MODE == FC1 ? 8 : 16) ||
+      !map_codes(&m1, a.w1.codes, all, a.blocks, MODE == FC1 ? 8 : 16))
+    return cudaErrorInvalidValue;
+  const int64_t blocks = (items * a.wk + kWarps - 1) / kWarps;
+  const unsigned grid = static_cast<unsigned>(blocks < kMostBlocks ? blocks : kMostBlocks);
+  return launch_dependent(k, dim3(grid), dim3(kWarps * 32), smem, s, m0, m1, a);
 }
 
 template <int MODE, int G32>
