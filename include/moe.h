@@ -676,7 +676,7 @@ moe_status moe_dropout_add(int64_t n, int32_t dtype, double dropout, const uint6
  * (nibble 0: the lowest four bits).  Codes past K are not used.
  * The products take x in bf16 and sum in fp32; the scales multiply fp32 sums of
  * one group, so W itself is never rounded.  x is held as fp16 times a power of
- * two of its group: exact for values down to 2^-28 of the group's largest.  An
+ * two of its row: exact for values down to 2^-28 of the row's largest.  An
  * infinity or a NaN in a row of x makes that row of y NaN.
  */
 typedef struct moe_w4 {

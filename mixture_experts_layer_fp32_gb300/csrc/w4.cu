@@ -184,23 +184,19 @@ __global__ void __launch_bounds__(256)
 
 struct LinearShape {
   int rows;  // of one launch
-  bool wide;
-  int splits;
+  Way way;
 };
 LinearShape linear_shape(int64_t rows, int N, int K) {
   LinearShape L;
   L.rows = static_cast<int>(rows < kMaxRows ? rows : kMaxRows);
-  L.wide = is_wide(LINEAR, rows);
-  const int64_t chunks = L.wide ? (L.rows + 31) / 32 : 1;
   // a second launch adds the parts up: some 1.5 us, about 6 blocks of a warp
-  L.splits = splits_of(chunks, N, w4_blocks(K), 6, L.wide);
+  L.way = way_of(LINEAR, L.rows, (L.rows + 31) / 32, N, w4_blocks(K), 6);
   return L;
 }
 
 struct ExpertsShape {
   int tokens, pairs;  // of one launch
-  bool wide1, wide2;
-  int splits;         // of the second product
+  Way way1, way2;
 };
 ExpertsShape experts_shape(int T, int h, int E, int k, int f) {
   ExpertsShape S;
@@ -212,10 +208,9 @@ ExpertsShape experts_shape(int T, int h, int E, int k, int f) {
   const double mean = static_cast<double>(S.pairs) / E;
   const double luck = mean + 2.0 * __builtin_sqrt(mean) + 1.0;
   const int64_t rows = static_cast<int64_t>(luck < S.tokens ? luck : S.tokens);
-  S.wide1 = is_wide(FC1, rows);
-  S.wide2 = is_wide(FC2, rows);
   const int64_t hit = S.pairs < E ? S.pairs : E;
-  S.splits = splits_of(hit, h, w4_blocks(f), 0, S.wide2);
+  S.way1 = way_of(FC1, rows, hit, f, w4_blocks(h), -1);
+  S.way2 = way_of(FC2, rows, hit, h, w4_blocks(f), 0);
   return S;
 }
 
@@ -252,7 +247,7 @@ bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, i
 size_t w4_linear_scratch(int64_t rows, int N, int K) {
   const LinearShape L = linear_shape(rows, N, K);
   return split_bytes(L.rows, K, 1) +
-         (L.splits == 1 ? 0 : static_cast<size_t>(L.splits) * L.rows * N * 4);
+         (L.way.splits == 1 ? 0 : static_cast<size_t>(L.way.splits) * L.rows * N * 4);
 }
 
 cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* x, const W4& W,
@@ -278,15 +273,15 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
     a.blocks = w4_blocks(K);
     a.groups = K / group;
     a.N = N;
-    a.splits = L.splits;
-    a.out = L.splits > 1 ? part : out;
-    a.out_f32 = L.splits > 1 ? 1 : out_f32;
-    st = launch_linear(group, K, L.wide, a, s);
+    a.splits = L.way.splits;
+    a.out = L.way.splits > 1 ? part : out;
+    a.out_f32 = L.way.splits > 1 ? 1 : out_f32;
+    st = launch_linear(group, K, L.way.wide, a, s);
     if (st != cudaSuccess) return st;
-    if (L.splits > 1) {
+    if (L.way.splits > 1) {
       const int64_t n = static_cast<int64_t>(m) * N;
       st = launch_dependent(w4_join_kernel, dim3(static_cast<unsigned>((n + 255) / 256)),
-                            dim3(256), 0, s, n, L.splits, static_cast<const float*>(part), out_f32,
+                            dim3(256), 0, s, n, L.way.splits, static_cast<const float*>(part), out_f32,
                             out);
       if (st != cudaSuccess) return st;
     }
@@ -297,7 +292,7 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
 size_t w4_experts_scratch(int T, int h, int E, int k, int f) {
   const ExpertsShape S = experts_shape(T, h, E, k, f);
   return split_bytes(S.tokens, h, 1) + align256(static_cast<size_t>(S.pairs) * f * 4) +
-         split_bytes(S.pairs, f, 2) + static_cast<size_t>(S.splits) * S.pairs * h * 4;
+         split_bytes(S.pairs, f, 2) + static_cast<size_t>(S.way2.splits) * S.pairs * h * 4;
 }
 
 cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, const void* x,
@@ -337,7 +332,7 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     a.N = f;
     a.splits = 1;
     a.out = hidden;
-    st = launch_fc1(group, h, S.wide1, a, s);
+    st = launch_fc1(group, h, S.way1.wide, a, s);
     if (st != cudaSuccess) return st;
     // rows of dropped pairs hold nothing; nobody reads their pieces
     st = launch_split<float, 2>(true, group, n * k, f, hidden, hs, s);
@@ -349,13 +344,13 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     a.blocks = w4_blocks(f);
     a.groups = f / group;
     a.N = h;
-    a.splits = S.splits;
+    a.splits = S.way2.splits;
     a.out = part;
-    st = launch_fc2(group, f, S.wide2, a, s);
+    st = launch_fc2(group, f, S.way2.wide, a, s);
     if (st != cudaSuccess) return st;
     const int64_t vecs = static_cast<int64_t>(n) * (h / 4);
     st = launch_dependent(w4_combine_kernel, dim3(static_cast<unsigned>((vecs + 255) / 256)),
-                          dim3(256), 0, s, n, h, k, E, S.splits, static_cast<const float*>(part),
+                          dim3(256), 0, s, n, h, k, E, S.way2.splits, static_cast<const float*>(part),
                           a.idx, topk_prob + first, a.keep,
                           static_cast<__nv_bfloat16*>(y) + static_cast<int64_t>(t) * h);
     if (st != cudaSuccess) return st;

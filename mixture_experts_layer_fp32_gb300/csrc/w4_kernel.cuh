@@ -27,7 +27,8 @@
 namespace moe {
 namespace w4 {
 
-constexpr int kWarps = 8;        // of a block
+constexpr int kWarps = 8;        // of a block of the wide kernel, and the plan's
+constexpr int kNarrowWarps = 16; // of a block of the narrow kernel, one to an SM
 constexpr int kMaxRows = 1024;   // rows of x, or (token, slot) pairs, of one launch
 constexpr int kSms = 152;
 constexpr int kBlocksPerSm = 2;
@@ -51,6 +52,8 @@ struct Args {
   int split_units, split_rest;  // units / splits and the remainder: narrow stages, wide blocks
   int wk;                 // narrow: warps that share an item's inputs: 1, 2, 4 or 8
   int each, each_rest;    // their units, in a part of split_units and of one more
+  int chunk_rows;         // narrow: rows of a chunk
+  int x_pitch, s_pitch;   // narrow: bytes of a column of x and of a row's sums in shared memory
   int rows;               // LINEAR: rows of x
   int out_f32;            // LINEAR
   void* out;              // LINEAR: y or partial sums; FC1: hidden values; FC2: partial sums
@@ -130,8 +133,8 @@ struct Plan {
 
 __device__ inline void make_plan(Plan& p, const Args& a, int chunk_rows) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kWarps * MOE_MAX_EXPERTS; i += kWarps * 32)
-    (&p.warp_count[0][0])[i] = 0;
+  const bool works = warp < kWarps;
+  for (int i = tid; i < kWarps * MOE_MAX_EXPERTS; i += blockDim.x) (&p.warp_count[0][0])[i] = 0;
   __syncthreads();
   // a warp takes up to four times 32 pairs, one after another: ranks by pair
   // order within the warp
@@ -141,7 +144,8 @@ __device__ inline void make_plan(Plan& p, const Args& a, int chunk_rows) {
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
     expert[r] = -1;
-    if (r >= rounds) continue;
+    rank[r] = 0;
+    if (r >= rounds || !works) continue;
     const int i = (warp * rounds + r) * 32 + lane;
     int e = -1;
     if (i < a.pairs && !(a.keep && a.keep[i] == 0)) {
@@ -165,7 +169,7 @@ __device__ inline void make_plan(Plan& p, const Args& a, int chunk_rows) {
   // thread e: expert e's count, then the scans of the counts and of the chunks
   static_assert(kWarps * 32 == MOE_MAX_EXPERTS, "one thread to an expert");
   int n = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; works && w < kWarps; ++w) {
     const int c = p.warp_count[w][tid];
     p.warp_count[w][tid] = n;
     n += c;
@@ -179,22 +183,24 @@ __device__ inline void make_plan(Plan& p, const Args& a, int chunk_rows) {
       sc += uc;
     }
   }
-  if (lane == 31) {
+  if (works && lane == 31) {
     p.scan[warp][0] = sn;
     p.scan[warp][1] = sc;
   }
   __syncthreads();
-  for (int w = 0; w < warp; ++w) {
-    sn += p.scan[w][0];
-    sc += p.scan[w][1];
+  if (works) {
+    for (int w = 0; w < warp; ++w) {
+      sn += p.scan[w][0];
+      sc += p.scan[w][1];
+    }
+    p.end[tid] = sn;
+    p.first[tid] = sn - n;
+    for (int c = 0; c < chunks; ++c) {
+      p.chunk_expert[sc - chunks + c] = tid;
+      p.chunk_row[sc - chunks + c] = sn - n + c * chunk_rows;
+    }
+    if (tid == kWarps * 32 - 1) p.chunks = sc;
   }
-  p.end[tid] = sn;
-  p.first[tid] = sn - n;
-  for (int c = 0; c < chunks; ++c) {
-    p.chunk_expert[sc - chunks + c] = tid;
-    p.chunk_row[sc - chunks + c] = sn - n + c * chunk_rows;
-  }
-  if (tid == kWarps * 32 - 1) p.chunks = sc;
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < kRounds; ++r)
@@ -212,7 +218,12 @@ __device__ inline void make_plan(Plan& p, const Args& a, int chunk_rows) {
 // read the same x.  A group takes every step-th.
 struct Item {
   int chunk, part, tile;
-  __device__ Item(int first, const Args& a) : chunk(0), part(0), tile(first) { carry(a); }
+  __device__ Item(int first, const Args& a) {
+    tile = first % a.tiles;
+    first /= a.tiles;
+    part = first % a.splits;
+    chunk = first / a.splits;
+  }
   __device__ void next(int step, const Args& a) {
     tile += step;
     carry(a);
@@ -319,20 +330,20 @@ struct Sums {
   float v[N];
 };
 template <int N>
-__device__ __forceinline__ Sums<N> load_sums(const float* p) {
+__device__ __forceinline__ Sums<N> lds_sums(uint32_t at) {
   Sums<N> r;
   if (N == 1) {
-    r.v[0] = __ldg(p);
+    r.v[0] = lds4(at);
   } else if (N == 2) {
-    const float2 q = __ldg(reinterpret_cast<const float2*>(p));
+    const float2 q = lds8(at);
     r.v[0] = q.x;
     r.v[N - 1] = q.y;
   } else {
-    const float4 q = __ldg(reinterpret_cast<const float4*>(p));
-    r.v[0] = q.x;
-    r.v[1 % N] = q.y;
-    r.v[2 % N] = q.z;
-    r.v[N - 1] = q.w;
+    const uint4 q = lds16(at);
+    r.v[0] = __uint_as_float(q.x);
+    r.v[1 % N] = __uint_as_float(q.y);
+    r.v[2 % N] = __uint_as_float(q.z);
+    r.v[N - 1] = __uint_as_float(q.w);
   }
   return r;
 }
@@ -348,42 +359,45 @@ __device__ __forceinline__ void pairs_of(uint32_t word, uint32_t (&p)[4]) {
 // Up to 8 columns (8 rows of x; FC2: 4) to a chunk.  A tile is 16 outputs (FC1:
 // 8 features, W1's rows and W3's); wk warps share its inputs, each a run of
 // stages of four blocks.  Codes come by TMA, one stage ahead and across the ends
-// of items, into a ring of the warp's own: one instruction for 4 KB, and their
-// way is not L1's.  That matters more than the instructions: L1 answers in
-// order, so that a read of x that would hit waits behind every copy that misses
-// (the same kernel with cp.async took 15.8 us for 38912 x 4096 codes, 9.8 us
-// without the reads of x).  Scales are read one stage ahead, x one block ahead,
-// into registers.
+// of items, into a ring of the warp's own: one instruction for 4 KB.  A block
+// takes consecutive items, so that it has few changes of the chunk or the part;
+// at each it brings the chunk's x (of the part's inputs) into shared memory.
+// Reading x through L1 instead cost a third of the time: L1 answers in order,
+// and a read that would hit waits behind every one that misses.
 constexpr long long kWaitCycles = 2000000000ll;  // a second: a copy that never arrived
+constexpr int kNarrowX = 66 * 1024;              // bytes of x and its sums, at most
 
 template <int MODE, int G32, bool ZEROS, bool TAIL>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(
+__global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
     const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1, Args a) {
   constexpr int GPB = 4 / G32;         // groups of a block
   constexpr int CP = pieces_of(MODE);  // columns of a row
   constexpr int XR = 2 / CP;           // rows of x in a lane's two columns
-  constexpr int kRows = 8 / CP;
   constexpr int SB = 4;                // blocks of a stage
   constexpr int kStage = SB * 1024;
   constexpr int kTile = MODE == FC1 ? 8 : 16;
   constexpr int kRed = 2 * XR * 32;
+  constexpr int W = kNarrowWarps;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* red = reinterpret_cast<float*>(smem + kWarps * 2 * kStage);  // 2 buffers
-  __shared__ uint64_t bars[kWarps][2];
-  Plan& plan = *reinterpret_cast<Plan*>(red + 2 * kWarps * kRed);
+  float* red = reinterpret_cast<float*>(smem + W * 2 * kStage);  // 2 buffers
+  uint8_t* x_at = reinterpret_cast<uint8_t*>(red + 2 * W * kRed);
+  Plan& plan = *reinterpret_cast<Plan*>(x_at + kNarrowX);
+  __shared__ uint64_t bars[W][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int wk = a.wk, group = warp / wk, w_in = warp & (wk - 1);
-  const int first_item = blockIdx.x * (kWarps / wk) + group, step = gridDim.x * (kWarps / wk);
+  const int wk = a.wk, group = warp / wk, w_in = warp & (wk - 1), step = W / wk;
   pdl_trigger();
 
   int chunks;
   if (MODE == LINEAR) {
-    chunks = (a.rows + kRows - 1) / kRows;
+    chunks = (a.rows + a.chunk_rows - 1) / a.chunk_rows;
   } else {
-    make_plan(plan, a, kRows);
+    make_plan(plan, a, a.chunk_rows);
     chunks = plan.chunks;
   }
-
+  // this block's items
+  const int64_t items = static_cast<int64_t>(chunks) * a.splits * a.tiles;
+  const int begin = static_cast<int>(items * blockIdx.x / gridDim.x);
+  const int end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
   const uint32_t ring = ptx::smem_u32(smem) + warp * 2 * kStage;
   const uint32_t bar = ptx::smem_u32(&bars[warp][0]);
   if (lane == 0) {
@@ -394,16 +408,17 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(
   __syncwarp();
 
   // ---- codes and scales, a stage ahead ----
-  Item it(first_item, a);  // of the stage to come
-  int stage = 0, left = 0; // its number in the row; the item's stages from there on
-  uint32_t row = 0;        // the tile's first output
+  int next = begin + group;  // the item of the stage to come
+  Item it(next, a);
+  int stage = 0, left = 0;  // its number in the row; the item's stages from there on
+  uint32_t row = 0;         // the tile's first output
   // lane t of a row (g, g + 8) reads the scales of the stage's block t; the row's
   // lanes have them from each other by shuffles
   const unsigned short *ps0, *ps1;
   const uint8_t *pz0, *pz1;
   Scales<GPB> scale0, scale1;
   auto enter = [&]() {
-    if (it.chunk >= chunks) return;
+    if (next >= end) return;
     const bool rest = it.part < a.split_rest;
     const int each = rest ? a.each_rest : a.each;
     stage = it.part * a.split_units + min(it.part, a.split_rest) + w_in * each;
@@ -425,7 +440,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(
   };
   int fill = 0;
   auto fetch = [&]() {
-    if (it.chunk >= chunks) return;
+    if (next >= end) return;
     __syncwarp();  // every lane has read what the slot held
     if (lane == 0) {
       const uint32_t dst = ring + fill * kStage, b = bar + fill * 8;
@@ -449,13 +464,15 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(
         pz1 += SB * GPB;
       }
     } else {
+      next += step;
       it.next(step, a);
       enter();
     }
     fill ^= 1;
   };
   enter();
-  Item now = it;  // of the stage at hand
+  int at_hand = next;  // the item of the stage at hand
+  Item now = it;
   int stage_now = stage, left_now = left;
   fetch();
   pdl_wait();  // the split rows
@@ -463,136 +480,154 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_narrow_kernel(
   int use = 0, phase = 0, buf = 0;  // the slot at hand and its barrier's phase
   bool lost = false;
   const int x_row = a.blocks * (128 * CP);
-  while (now.chunk < chunks) {
+  const uint32_t xs = ptx::smem_u32(x_at);
+  Item epoch(begin, a);
+  for (int from = begin; from < end;) {
+    const int to = min(end, from + a.tiles - epoch.tile);  // the epoch's items
     int row_first, row_count;  // of the chunk, in sorted order (LINEAR: in x)
     if (MODE == LINEAR) {
-      row_first = now.chunk * kRows;
-      row_count = min(kRows, a.rows - row_first);
+      row_first = epoch.chunk * a.chunk_rows;
+      row_count = min(a.chunk_rows, a.rows - row_first);
     } else {
-      row_first = plan.chunk_row[now.chunk];
-      row_count = min(kRows, plan.end[plan.chunk_expert[now.chunk]] - row_first);
+      row_first = plan.chunk_row[epoch.chunk];
+      row_count = min(a.chunk_rows, plan.end[plan.chunk_expert[epoch.chunk]] - row_first);
     }
-    // Column g is piece g % CP of row g / CP; rows past the chunk's repeat its
-    // first and are not stored.  A lane's sums are of the columns 2t, 2t + 1.
-    auto row_of = [&](int r) {
-      if (r >= row_count) r = 0;
-      return MODE == FC1 ? static_cast<int>(plan.token[row_first + r]) : row_first + r;
-    };
-    const __half* xp = a.x + static_cast<int64_t>(row_of(g / CP)) * x_row +
-                       (CP == 2 ? (g & 1) * (x_row / 2) : 0) + stage_now * (SB * 128) + t * 8;
-    const float* xs[XR];
+    const int first = epoch.part * a.split_units + min(epoch.part, a.split_rest);  // stage
+    const int stages = a.split_units + (epoch.part < a.split_rest);
+    const int blocks_in = min(stages * SB, a.blocks - first * SB);
+    // ---- the epoch's x: column c is piece c % CP of row c / CP ----
+    __syncthreads();
+    {
+      auto row_of = [&](int r) {
+        return MODE == FC1 ? static_cast<int>(plan.token[row_first + r]) : row_first + r;
+      };
+      // 16 warps: 16 / columns of them to a column
+      const int columns = row_count * CP, share = W / columns;
+      if (warp < columns * share) {
+        const int c = warp / share;
+        const __half* p = a.x + static_cast<int64_t>(row_of(c / CP)) * x_row +
+                          (CP == 2 ? (c & 1) * (x_row / 2) : 0) + first * (SB * 128);
+        for (int i = warp % share * 32 + lane; i < blocks_in * 16; i += share * 32)
+          copy_async(xs + c * a.x_pitch + i * 16, p + i * 8);
+      }
+      const uint32_t ss = xs + a.chunk_rows * CP * a.x_pitch;
+      for (int r = W - 1 - warp; r < row_count; r += W) {
+        const float* p =
+            a.sums + (static_cast<int64_t>(row_of(r)) * a.blocks + first * SB) * GPB;
+        for (int i = lane; i < blocks_in * GPB; i += 32)
+          copy_async4(ss + r * a.s_pitch + i * 4, p + i);
+      }
+      copies_commit();
+      copies_wait<0>();
+    }
+    __syncthreads();
+    // columns past the chunk's repeat its first and are not stored; a lane's sums
+    // are of the columns 2t, 2t + 1
+    const uint32_t x_lane = xs + (g < row_count * CP ? g : 0) * a.x_pitch + t * 16;
+    uint32_t s_lane[XR];
 #pragma unroll
     for (int i = 0; i < XR; ++i)
-      xs[i] = a.sums +
-              (static_cast<int64_t>(row_of(XR * t + i)) * a.blocks + stage_now * SB) * GPB;
-    // x and its sums, a block ahead of their use (after the item's last block
-    // this reads on: the buffers have room for it)
-    uint4 x_next[4];
-    Sums<GPB> sums_next[XR];
-    auto fetch_x = [&](int b) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x_next[j] = __ldg(reinterpret_cast<const uint4*>(xp + b * 128 + j * 32));
-#pragma unroll
-      for (int i = 0; i < XR; ++i) sums_next[i] = load_sums<GPB>(xs[i] + b * GPB);
-    };
-    fetch_x(0);
-    float acc[2][XR];  // of the outputs g and g + 8
-#pragma unroll
-    for (int i = 0; i < XR; ++i) acc[0][i] = acc[1][i] = 0.f;
+      s_lane[i] = xs + a.chunk_rows * CP * a.x_pitch +
+                  (XR * t + i < row_count ? XR * t + i : 0) * a.s_pitch;
 
-    auto block = [&](int b, uint32_t src, const Scales<GPB>& st0, const Scales<GPB>& st1) {
-      uint4 x[4];
-      Sums<GPB> sx[XR];
+    while (at_hand < to) {
+      float acc[2][XR];  // of the outputs g and g + 8
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = x_next[j];
+      for (int i = 0; i < XR; ++i) acc[0][i] = acc[1][i] = 0.f;
+      auto block = [&](uint32_t src, uint32_t xb, int k, const Scales<GPB>& st0,
+                       const Scales<GPB>& st1, int b) {
+        constexpr uint32_t kBlock = MODE == FC1 ? 512 : 1024;
+        constexpr uint32_t kSecond = MODE == FC1 ? kStage / 2 : 512;
+        const uint4 q0 = lds16(src + b * kBlock), q1 = lds16(src + b * kBlock + kSecond);
+        const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w}, c1[4] = {q1.x, q1.y, q1.z, q1.w};
+        const Scales<GPB> s0 = scales_from<GPB, ZEROS>(st0, (lane & ~3) + b);
+        const Scales<GPB> s1 = scales_from<GPB, ZEROS>(st1, (lane & ~3) + b);
+        Sums<GPB> sx[XR];
 #pragma unroll
-      for (int i = 0; i < XR; ++i) sx[i] = sums_next[i];
-      fetch_x(b + 1);
-      constexpr uint32_t kSecond = MODE == FC1 ? kStage / 2 : 512;
-      const uint4 q0 = lds16(src + b * (MODE == FC1 ? 512 : 1024));
-      const uint4 q1 = lds16(src + b * (MODE == FC1 ? 512 : 1024) + kSecond);
-      const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w}, c1[4] = {q1.x, q1.y, q1.z, q1.w};
-      const Scales<GPB> s0 = scales_from<GPB, ZEROS>(st0, (lane & ~3) + b);
-      const Scales<GPB> s1 = scales_from<GPB, ZEROS>(st1, (lane & ~3) + b);
+        for (int i = 0; i < XR; ++i) sx[i] = lds_sums<GPB>(s_lane[i] + (k + b) * (GPB * 4));
 #pragma unroll
-      for (int q = 0; q < GPB; ++q) {
-        float sum[4];
+        for (int q = 0; q < GPB; ++q) {
+          float sum[4];
 #pragma unroll
-        for (int j = q * G32; j < (q + 1) * G32; ++j) {
-          uint32_t p0[4], p1[4];
-          pairs_of(c0[j], p0);
-          pairs_of(c1[j], p1);
-          if (j == q * G32) mma_first(sum, p0[0], p1[0], p0[1], p1[1], x[j].x, x[j].y);
-          else mma(sum, p0[0], p1[0], p0[1], p1[1], x[j].x, x[j].y);
-          mma(sum, p0[2], p1[2], p0[3], p1[3], x[j].z, x[j].w);
-        }
+          for (int j = q * G32; j < (q + 1) * G32; ++j) {
+            uint32_t p0[4], p1[4];
+            pairs_of(c0[j], p0);
+            pairs_of(c1[j], p1);
+            const uint4 x = lds16(xb + b * 256 + j * 64);
+            if (j == q * G32) mma_first(sum, p0[0], p1[0], p0[1], p1[1], x.x, x.y);
+            else mma(sum, p0[0], p1[0], p0[1], p1[1], x.x, x.y);
+            mma(sum, p0[2], p1[2], p0[3], p1[3], x.z, x.w);
+          }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float s = scale_of(i ? s1 : s0, q), z = zero_of<GPB, ZEROS>(i ? s1 : s0, q);
-          if (CP == 2) {  // the second piece is in 2^-11 of the first's unit
-            acc[i][0] += s * (sum[2 * i] + 0.00048828125f * sum[2 * i + 1] - z * sx[0].v[q]);
-          } else {
-            acc[i][0] += s * (sum[2 * i] - z * sx[0].v[q]);
-            acc[i][XR - 1] += s * (sum[2 * i + 1] - z * sx[XR - 1].v[q]);
+          for (int i = 0; i < 2; ++i) {
+            const float s = scale_of(i ? s1 : s0, q), z = zero_of<GPB, ZEROS>(i ? s1 : s0, q);
+            if (CP == 2) {  // the second piece is in 2^-11 of the first's unit
+              acc[i][0] +=
+                  s * (sum[2 * i] + 0.00048828125f * sum[2 * i + 1] - z * sx[0].v[q]);
+            } else {
+              acc[i][0] += s * (sum[2 * i] - z * sx[0].v[q]);
+              acc[i][XR - 1] += s * (sum[2 * i + 1] - z * sx[XR - 1].v[q]);
+            }
           }
         }
-      }
-    };
+      };
 
-    const Item mine = now;
-    for (bool more = true; more;) {
-      const Scales<GPB> st0 = scale0, st1 = scale1;
-      const int blocks = min(SB, a.blocks - stage_now * SB);
-      more = left_now > 1;
-      now = it;
-      stage_now = stage;
-      left_now = left;
-      fetch();
-      if (!lost && !ptx::mbar_try_wait(bar + use * 8, phase)) {
-        const long long began = clock64();
-        while (!lost && !ptx::mbar_try_wait(bar + use * 8, phase))
-          if (clock64() - began > kWaitCycles) {
-            // go on with what is there, so that nobody waits for this warp
-            lost = true;
-            report_error(a.err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
-          }
-      }
-      const uint32_t src = ring + use * kStage + lane * 16;
-      if (blocks == SB) {
+      const Item mine = now;
+      for (bool more = true; more;) {
+        const Scales<GPB> st0 = scale0, st1 = scale1;
+        const int blocks = min(SB, a.blocks - stage_now * SB);
+        const int k = (stage_now - first) * SB;  // its first block in the epoch's x
+        more = left_now > 1;
+        at_hand = next;
+        now = it;
+        stage_now = stage;
+        left_now = left;
+        fetch();
+        if (!lost && !ptx::mbar_try_wait(bar + use * 8, phase)) {
+          const long long began = clock64();
+          while (!lost && !ptx::mbar_try_wait(bar + use * 8, phase))
+            if (clock64() - began > kWaitCycles) {
+              // go on with what is there, so that nobody waits for this warp
+              lost = true;
+              report_error(a.err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
+            }
+        }
+        const uint32_t src = ring + use * kStage + lane * 16, xb = x_lane + k * 256;
+        if (blocks == SB) {
 #pragma unroll
-        for (int b = 0; b < SB; ++b) block(b, src, st0, st1);
-      } else {
+          for (int b = 0; b < SB; ++b) block(src, xb, k, st0, st1, b);
+        } else {
 #pragma unroll 1
-        for (int b = 0; b < blocks; ++b) block(b, src, st0, st1);
+          for (int b = 0; b < blocks; ++b) block(src, xb, k, st0, st1, b);
+        }
+        phase ^= use;
+        use ^= 1;
       }
-      phase ^= use;
-      use ^= 1;
-      xp += SB * 128;
-#pragma unroll
-      for (int i = 0; i < XR; ++i) xs[i] += SB * GPB;
-    }
 
-    // ---- the warps' sums, added in order ----
-    float* all = red + (group * 2 + buf) * wk * kRed;
+      // ---- the warps' sums, added in order ----
+      float* all = red + (group * 2 + buf) * wk * kRed;
 #pragma unroll
-    for (int i = 0; i < XR; ++i) {
-      all[w_in * kRed + i * 64 + lane] = acc[0][i];
-      all[w_in * kRed + i * 64 + 32 + lane] = acc[1][i];
-    }
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(wk * 32) : "memory");
-    for (int i = w_in * 32 + lane; i < XR * 32; i += wk * 32) {
-      const int l = i & 31, c = i >> 5, r = XR * (l & 3) + c;
-      if (r >= row_count) continue;
-      const float* p = all + c * 64 + l;
-      float low = 0.f, high = 0.f;
-      for (int w = 0; w < wk; ++w) {
-        low += p[w * kRed];
-        high += p[w * kRed + 32];
+      for (int i = 0; i < XR; ++i) {
+        all[w_in * kRed + i * 64 + lane] = acc[0][i];
+        all[w_in * kRed + i * 64 + 32 + lane] = acc[1][i];
       }
-      put<MODE>(a, plan, mine.part, row_first, r, mine.tile * kTile + (l >> 2), low, high);
+      if (wk == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(wk * 32) : "memory");
+      for (int i = w_in * 32 + lane; i < XR * 32; i += wk * 32) {
+        const int l = i & 31, c = i >> 5, r = XR * (l & 3) + c;
+        if (r >= row_count) continue;
+        const float* p = all + c * 64 + l;
+        float low = 0.f, high = 0.f;
+        for (int w = 0; w < wk; ++w) {
+          low += p[w * kRed];
+          high += p[w * kRed + 32];
+        }
+        put<MODE>(a, plan, mine.part, row_first, r, mine.tile * kTile + (l >> 2), low, high);
+      }
+      buf ^= 1;
     }
-    buf ^= 1;
+    epoch.next(to - from, a);
+    from = to;
   }
 }
 
@@ -849,9 +884,9 @@ struct Share {
 };
 // stages: of a part; every warp of an item has some, in a part of one more too.
 inline Share share_narrow(int64_t items, int stages) {
-  constexpr int kAtOnce = kBlocksPerSm * kSms * kWarps;
+  constexpr int kAtOnce = kSms * kNarrowWarps;
   Share best = {1, int64_t{1} << 62};
-  for (int wk = 1; wk <= kWarps; wk *= 2) {
+  for (int wk = 1; wk <= kNarrowWarps; wk *= 2) {
     const int each = (stages + wk - 1) / wk, each_rest = (stages + wk) / wk;
     if ((wk - 1) * each >= stages || (wk - 1) * each_rest >= stages + 1) continue;
     const int64_t at_once = kAtOnce / wk, rounds = (items + at_once - 1) / at_once;
@@ -884,6 +919,22 @@ inline int splits_of(int64_t chunks, int N, int blocks, int join, bool wide) {
   return best;
 }
 
+// The narrow kernel's x: bytes of a column and of a row's sums of the longest
+// part; the columns' starts fall on the banks' halves in turn.
+inline int part_blocks(int blocks, int splits) {
+  return ((blocks + 3) / 4 + splits - 1) / splits * 4;
+}
+inline int narrow_x_pitch(int blocks, int splits) { return part_blocks(blocks, splits) * 256 + 64; }
+inline int narrow_s_pitch(int blocks, int splits) { return part_blocks(blocks, splits) * 16 + 16; }
+// rows that a chunk of the narrow kernel can have; 0: none fits
+inline int narrow_rows(int mode, int blocks, int splits) {
+  const int cp = pieces_of(mode);
+  const int64_t fit =
+      kNarrowX / (static_cast<int64_t>(cp) * narrow_x_pitch(blocks, splits) +
+                  narrow_s_pitch(blocks, splits));
+  return static_cast<int>(fit < 8 / cp ? fit : 8 / cp);
+}
+
 // The codes of `rows` rows as [blocks][rows][64 bytes], boxes of 4 blocks
 bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, int box_rows);
 
@@ -896,10 +947,11 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 template <int MODE, int G32, bool ZEROS, bool TAIL>
 cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
   const int tile = (MODE == FC1 ? 8 : 16) * (wide ? 2 * kWarps : 1);
-  const int rows = (wide ? 32 : 8) / pieces_of(MODE);
   const size_t plan = MODE == LINEAR ? 0 : sizeof(Plan);
   a.tiles = (a.N + tile - 1) / tile;
-  const int64_t chunks = MODE == LINEAR ? (a.rows + rows - 1) / rows
+  if (!wide) a.chunk_rows = narrow_rows(MODE, a.blocks, a.splits);
+  const int chunk_rows = wide ? 32 / pieces_of(MODE) : a.chunk_rows;
+  const int64_t chunks = MODE == LINEAR ? (a.rows + chunk_rows - 1) / chunk_rows
                                          : (a.pairs < a.E ? a.pairs : a.E);  // about
   const int64_t items = chunks * a.tiles * a.splits;
   const int units = wide ? a.blocks : (a.blocks + 3) / 4;
@@ -915,7 +967,8 @@ cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
     return launch_dependent(k, dim3(grid), dim3(kWarps * 32), smem, s, a);
   }
   auto k = w4_narrow_kernel<MODE, G32, ZEROS, TAIL>;
-  const size_t smem = kWarps * 2 * 4096 + 2 * kWarps * (4 / pieces_of(MODE)) * 32 * 4 + plan;
+  const size_t smem = kNarrowWarps * 2 * 4096 +
+                      2 * kNarrowWarps * (4 / pieces_of(MODE)) * 32 * 4 + kNarrowX + plan;
   const cudaError_t st = allow_smem(k, smem);
   if (st != cudaSuccess) return st;
   a.wk = share_narrow(items, a.split_units).wk;
@@ -926,9 +979,11 @@ cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
   if (!map_codes(&m0, a.w0.codes, all, a.blocks, MODE == FC1 ? 8 : 16) ||
       !map_codes(&m1, a.w1.codes, all, a.blocks, MODE == FC1 ? 8 : 16))
     return cudaErrorInvalidValue;
-  const int64_t blocks = (items * a.wk + kWarps - 1) / kWarps;
-  const unsigned grid = static_cast<unsigned>(blocks < kMostBlocks ? blocks : kMostBlocks);
-  return launch_dependent(k, dim3(grid), dim3(kWarps * 32), smem, s, m0, m1, a);
+  a.x_pitch = narrow_x_pitch(a.blocks, a.splits);
+  a.s_pitch = narrow_s_pitch(a.blocks, a.splits);
+  const int64_t blocks = (items * a.wk + kNarrowWarps - 1) / kNarrowWarps;
+  const unsigned grid = static_cast<unsigned>(blocks < kSms ? blocks : kSms);
+  return launch_dependent(k, dim3(grid), dim3(kNarrowWarps * 32), smem, s, m0, m1, a);
 }
 
 template <int MODE, int G32>
@@ -952,8 +1007,25 @@ cudaError_t launch_mode(int group, int K, bool wide, const Args& a, cudaStream_t
   }
 }
 
-// whether that many rows (of an expert) are more than the narrow kernel's columns
-inline bool is_wide(int mode, int64_t rows) { return rows > 8 / pieces_of(mode); }
+// How a product of about `rows` rows of x (of an expert), `chunks` of them (of
+// the experts hit) and N outputs is run.  The narrow kernel for as few rows as
+// it can hold; join: see splits_of, negative: no splits.
+struct Way {
+  bool wide;
+  int splits;
+};
+inline Way way_of(int mode, int64_t rows, int64_t chunks, int N, int blocks, int join) {
+  Way w = {true, 1};
+  if (rows <= 8 / pieces_of(mode)) {
+    w.splits = join < 0 ? 1 : splits_of(chunks, N, blocks, join, false);
+    // more parts where the rows' x would not fit
+    while (join >= 0 && narrow_rows(mode, blocks, w.splits) < rows && w.splits < kMostSplits)
+      ++w.splits;
+    w.wide = narrow_rows(mode, blocks, w.splits) < rows;
+  }
+  if (w.wide) w.splits = join < 0 ? 1 : splits_of(chunks, N, blocks, join, true);
+  return w;
+}
 
 cudaError_t launch_linear(int group, int K, bool wide, const Args& a, cudaStream_t s);
 cudaError_t launch_fc1(int group, int K, bool wide, const Args& a, cudaStream_t s);
