@@ -23,17 +23,25 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 // where several share the row (few rows: reading it again is cheaper than
 // another launch); then a warp takes a block of 128 inputs at a time, a lane
 // four of them.
-template <typename T, int G32, int CP>
+// SORTED: row i is the token of the i-th pair in the plan's order.
+template <typename T, int G32, int CP, bool SORTED>
 __global__ void __launch_bounds__(256)
     w4_split_kernel(int K, int blocks, int parts, const T* x, __half* pieces, float* units,
-                    float* sums) {
+                    float* sums, Args a) {
   __shared__ float tops[8];
   __shared__ int bads[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x / parts, part = blockIdx.x % parts;
   pdl_trigger();
   pdl_wait();
-  const T* xr = x + static_cast<int64_t>(row) * K;
+  int from = row;
+  if constexpr (SORTED) {
+    __shared__ Plan plan;
+    make_plan(plan, a, kTallColumns);
+    if (row >= plan.end[MOE_MAX_EXPERTS - 1]) return;  // dropped pairs
+    from = plan.token[row];
+  }
+  const T* xr = x + static_cast<int64_t>(from) * K;
   float top = 0.f;
   bool bad = false;  // fmaxf drops a NaN
 #pragma unroll 4
@@ -118,19 +126,22 @@ Split split_at(char* at, size_t rows, int K, int pieces) {
   return p;
 }
 
-template <typename T, int CP>
+// a: the pairs, if SORTED
+template <typename T, int CP, bool SORTED>
 cudaError_t launch_split(bool dependent, int group, int rows, int K, const T* x, const Split& p,
-                         cudaStream_t s) {
+                         const Args& a, cudaStream_t s) {
   const int blocks = w4_blocks(K);
-  auto k = group == 32 ? w4_split_kernel<T, 1, CP>
-                       : group == 64 ? w4_split_kernel<T, 2, CP> : w4_split_kernel<T, 4, CP>;
+  auto k = group == 32   ? w4_split_kernel<T, 1, CP, SORTED>
+           : group == 64 ? w4_split_kernel<T, 2, CP, SORTED>
+                         : w4_split_kernel<T, 4, CP, SORTED>;
   int parts = 2 * kSms / rows;
   if (parts > (blocks + 7) / 8) parts = (blocks + 7) / 8;
   if (parts < 1) parts = 1;
   const dim3 grid(static_cast<unsigned>(rows * parts));
   if (dependent)
-    return launch_dependent(k, grid, dim3(256), 0, s, K, blocks, parts, x, p.x, p.unit, p.sums);
-  k<<<grid, 256, 0, s>>>(K, blocks, parts, x, p.x, p.unit, p.sums);
+    return launch_dependent(k, grid, dim3(256), 0, s, K, blocks, parts, x, p.x, p.unit, p.sums,
+                            a);
+  k<<<grid, 256, 0, s>>>(K, blocks, parts, x, p.x, p.unit, p.sums, a);
   return cudaGetLastError();
 }
 
@@ -190,7 +201,7 @@ LinearShape linear_shape(int64_t rows, int N, int K) {
   LinearShape L;
   L.rows = static_cast<int>(rows < kMaxRows ? rows : kMaxRows);
   // a second launch adds the parts up: some 1.5 us, about 6 blocks of a warp
-  L.way = way_of(LINEAR, L.rows, (L.rows + 31) / 32, N, w4_blocks(K), 6);
+  L.way = way_of(LINEAR, L.rows, (L.rows + 63) / 64, N, w4_blocks(K), 6);
   return L;
 }
 
@@ -218,11 +229,15 @@ ExpertsShape experts_shape(int T, int h, int E, int k, int f) {
 
 namespace w4 {
 
-bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, int box_rows) {
-  typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+bool map_3d(CUtensorMap* m, CUtensorMapDataType type, void* at, const cuuint64_t (&dims)[3],
+            const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3],
+            CUtensorMapSwizzle swizzle) {
   static const EncodeTiledFn encode = []() -> EncodeTiledFn {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -232,14 +247,29 @@ bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, i
       return nullptr;
     return reinterpret_cast<EncodeTiledFn>(p);
   }();
-  if (encode == nullptr) return false;
-  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(blocks)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(blocks) * 64, 64};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 4}, unit[3] = {1, 1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides,
-                box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+  const cuuint32_t unit[3] = {1, 1, 1};
+  return encode != nullptr &&
+         encode(m, type, 3, at, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, int box_rows,
+               bool swapped) {
+  return map_3d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(codes),
+                {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(blocks)},
+                {static_cast<cuuint64_t>(blocks) * 64, 64},
+                {64, static_cast<cuuint32_t>(box_rows), swapped ? 2u : 4u},
+                swapped ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+bool map_x(CUtensorMap* m, const __half* x, int64_t columns, int blocks) {
+  return map_3d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, const_cast<__half*>(x),
+                {64, static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(blocks) * 2},
+                {static_cast<cuuint64_t>(blocks) * 256, 128}, {64, 8, 2},
+                CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace w4
@@ -260,10 +290,10 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
   for (int64_t r = 0; r < rows; r += L.rows) {
     const int m = static_cast<int>(rows - r < L.rows ? rows - r : L.rows);
     void* out = static_cast<char*>(y) + r * N * (out_f32 ? 4 : 2);
-    cudaError_t st = launch_split<__nv_bfloat16, 1>(
-        false, group, m, K, static_cast<const __nv_bfloat16*>(x) + r * K, xs, s);
-    if (st != cudaSuccess) return st;
     Args a = {};
+    cudaError_t st = launch_split<__nv_bfloat16, 1, false>(
+        false, group, m, K, static_cast<const __nv_bfloat16*>(x) + r * K, xs, a, s);
+    if (st != cudaSuccess) return st;
     a.x = xs.x;
     a.unit = xs.unit;
     a.sums = xs.sums;
@@ -291,7 +321,7 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
 
 size_t w4_experts_scratch(int T, int h, int E, int k, int f) {
   const ExpertsShape S = experts_shape(T, h, E, k, f);
-  return split_bytes(S.tokens, h, 1) + align256(static_cast<size_t>(S.pairs) * f * 4) +
+  return split_bytes(S.way1.wide ? S.pairs : S.tokens, h, 1) + align256(static_cast<size_t>(S.pairs) * f * 4) +
          split_bytes(S.pairs, f, 2) + static_cast<size_t>(S.way2.splits) * S.pairs * h * 4;
 }
 
@@ -301,8 +331,9 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
                               void* y, void* scratch, int* err, cudaStream_t s) {
   const ExpertsShape S = experts_shape(T, h, E, k, f);
   char* at = static_cast<char*>(scratch);
-  const Split xs = split_at(at, S.tokens, h, 1);
-  at += split_bytes(S.tokens, h, 1);
+  const int x_rows = S.way1.wide ? S.pairs : S.tokens;
+  const Split xs = split_at(at, x_rows, h, 1);
+  at += split_bytes(x_rows, h, 1);
   float* hidden = reinterpret_cast<float*>(at);
   at += align256(static_cast<size_t>(S.pairs) * f * 4);
   const Split hs = split_at(at, S.pairs, f, 2);
@@ -311,10 +342,6 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
   for (int t = 0; t < T; t += S.tokens) {
     const int n = T - t < S.tokens ? T - t : S.tokens;
     const int64_t first = static_cast<int64_t>(t) * k;
-    cudaError_t st = launch_split<__nv_bfloat16, 1>(
-        false, group, n, h, static_cast<const __nv_bfloat16*>(x) + static_cast<int64_t>(t) * h, xs,
-        s);
-    if (st != cudaSuccess) return st;
     Args a = {};
     a.idx = topk_idx + first;
     a.keep = keep ? keep + first : nullptr;
@@ -322,6 +349,11 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     a.E = E;
     a.topk = k;
     a.err = err;
+    const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(x) + static_cast<int64_t>(t) * h;
+    cudaError_t st =
+        S.way1.wide ? launch_split<__nv_bfloat16, 1, true>(false, group, n * k, h, in, xs, a, s)
+                    : launch_split<__nv_bfloat16, 1, false>(false, group, n, h, in, xs, a, s);
+    if (st != cudaSuccess) return st;
     a.x = xs.x;
     a.unit = xs.unit;
     a.sums = xs.sums;
@@ -335,7 +367,7 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     st = launch_fc1(group, h, S.way1.wide, a, s);
     if (st != cudaSuccess) return st;
     // rows of dropped pairs hold nothing; nobody reads their pieces
-    st = launch_split<float, 2>(true, group, n * k, f, hidden, hs, s);
+    st = launch_split<float, 2, false>(true, group, n * k, f, hidden, hs, a, s);
     if (st != cudaSuccess) return st;
     a.x = hs.x;
     a.unit = hs.unit;

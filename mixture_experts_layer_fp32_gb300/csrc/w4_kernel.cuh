@@ -27,11 +27,10 @@
 namespace moe {
 namespace w4 {
 
-constexpr int kWarps = 8;        // of a block of the wide kernel, and the plan's
+constexpr int kWarps = 8;        // that work out the plan
 constexpr int kNarrowWarps = 16; // of a block of the narrow kernel, one to an SM
 constexpr int kMaxRows = 1024;   // rows of x, or (token, slot) pairs, of one launch
 constexpr int kSms = 152;
-constexpr int kBlocksPerSm = 2;
 
 enum { LINEAR = 0, FC1 = 1, FC2 = 2 };
 
@@ -39,7 +38,8 @@ enum { LINEAR = 0, FC1 = 1, FC2 = 2 };
 __host__ __device__ constexpr int pieces_of(int mode) { return mode == FC2 ? 2 : 1; }
 
 struct Args {
-  // The split rows: fp16 [x_rows][pieces][blocks * 128], the inputs 2, 3, 6 and 7
+  // The split rows, of tokens in the narrow FC1, of the pairs sorted by expert in
+  // the wide one: fp16 [x_rows][pieces][blocks * 128], the inputs 2, 3, 6 and 7
   // of eight over 16; each row's unit; and each group's sum of x in it,
   // [x_rows][blocks * groups of a block]
   const __half* x;
@@ -49,10 +49,10 @@ struct Args {
   int blocks, groups;     // of 128 inputs; groups of a row
   int N, tiles;           // outputs of an expert, its tiles
   int splits;             // parts of a row's inputs, items of their own
-  int split_units, split_rest;  // units / splits and the remainder: narrow stages, wide blocks
+  int split_units, split_rest;  // stages of 4 blocks / splits, and the remainder
   int wk;                 // narrow: warps that share an item's inputs: a power of two
   int each, each_rest;    // their units, in a part of split_units and of one more
-  int chunk_rows;         // narrow: rows of a chunk
+  int chunk_rows;         // rows of x of a chunk
   int x_pitch, s_pitch;   // narrow: bytes of a column of x and of a row's sums in shared memory
   int rows;               // LINEAR: rows of x
   int out_f32;            // LINEAR
@@ -631,249 +631,13 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
   }
 }
 
-// More columns: up to 32 (32 rows of x; FC2: 16) to a chunk.  Now x is most of
-// what a multiplication reads, so a block's eight warps take the same inputs at
-// the same time, each for 32 outputs of its own (FC1: 16 features), and share x
-// in shared memory.
-constexpr int kWideSlots = 3;
-constexpr int kWideBlocks = 1;                       // of a stage
-constexpr int kWideX = 32 * 320;                     // a block's x: 32 columns, padded
-constexpr int kWideF = 4 * 32 * 4;                   // its groups' sums
-constexpr int kWideStage = kWarps * 2048 + kWideX + kWideF;
+}  // namespace w4
+}  // namespace moe
 
-template <int MODE, int G32, bool ZEROS, bool TAIL>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) w4_wide_kernel(Args a) {
-  constexpr int GPB = 4 / G32;
-  constexpr int CP = pieces_of(MODE);
-  constexpr int XR = 2 / CP;
-  constexpr int kRows = 32 / CP;
-  constexpr int kTile = (MODE == FC1 ? 8 : 16) * 2;  // of a warp
-  constexpr int NT = 4, MT = 2, R = 4;
-  extern __shared__ __align__(128) uint8_t smem[];
-  Plan& plan = *reinterpret_cast<Plan*>(smem + kWideSlots * kWideStage);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  pdl_trigger();
+#include "w4_wide.cuh"
 
-  int chunks;
-  if (MODE == LINEAR) {
-    chunks = (a.rows + kRows - 1) / kRows;
-  } else {
-    make_plan(plan, a, kRows);
-    chunks = plan.chunks;
-  }
-  auto rows_of = [&](const Item& i, int& first, int& count) {
-    if (MODE == LINEAR) {
-      first = i.chunk * kRows;
-      count = min(kRows, a.rows - first);
-    } else {
-      first = plan.chunk_row[i.chunk];
-      count = min(kRows, plan.end[plan.chunk_expert[i.chunk]] - first);
-    }
-  };
-  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-  const int row_bytes = a.blocks * 64, x_row = a.blocks * (128 * CP);
-
-  // ---- a block of inputs at a time, two ahead ----
-  Item it(blockIdx.x, a);
-  int kb = 0, left = 0;
-  const uint8_t* code[R];
-  // lane t of a row brings the scales of its output t (of R), one block ahead
-  const unsigned short* ps;
-  const uint8_t* pz;
-  Scales<GPB> scale_in[2];
-  // thread: 16 bytes of up to two columns' x; one group's sum
-  const __half* xp[2];
-  const float* xs;
-  int columns = 0;
-  auto enter = [&]() {
-    if (it.chunk >= chunks) return;
-    const bool rest = it.part < a.split_rest;
-    kb = it.part * a.split_units + min(it.part, a.split_rest);
-    left = a.split_units + rest;
-    const uint32_t e = MODE == LINEAR ? 0 : plan.chunk_expert[it.chunk];
-    const int tile = it.tile * (kTile * kWarps) + warp * kTile;  // first output
-    const uint32_t row = e * a.N;
-    // outputs past the last one repeat it and are not stored
-    auto output = [&](int i) {
-      const int o = tile + (MODE == FC1 ? (i >> 1) * 8 + g : i * 8 + g);
-      return row + static_cast<uint32_t>(min(o, a.N - 1));
-    };
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      code[i] = (MODE == FC1 && (i & 1) ? a.w1 : a.w0).codes +
-                static_cast<uint64_t>(output(i)) * row_bytes + kb * 64 + t * 16;
-    const W4& w = MODE == FC1 && (t & 1) ? a.w1 : a.w0;
-    const int64_t sat = static_cast<int64_t>(output(t)) * a.groups + kb * GPB;
-    ps = reinterpret_cast<const unsigned short*>(w.scales) + sat;
-    if (ZEROS) pz = w.zeros + sat;
-    int first, count;
-    rows_of(it, first, count);
-    columns = count * CP;
-    auto row_of = [&](int r) {
-      return MODE == FC1 ? static_cast<int>(plan.token[first + r]) : first + r;
-    };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = (threadIdx.x >> 4) + 16 * i;  // column, 16 threads to its 256 bytes
-      if (c < columns)
-        xp[i] = a.x + static_cast<int64_t>(row_of(c / CP)) * x_row +
-                (CP == 2 ? (c & 1) * (x_row / 2) : 0) + kb * 128 + (threadIdx.x & 15) * 8;
-    }
-    const int r = threadIdx.x & 31, q = threadIdx.x >> 5;
-    if (q < GPB && r < count)
-      xs = a.sums + (static_cast<int64_t>(row_of(r)) * a.blocks + kb) * GPB + q;
-  };
-  int fill = 0, bring = 0;
-  auto fetch = [&]() {
-    if (it.chunk < chunks) {
-      const uint32_t dst = base + fill * kWideStage;
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        copy_async(dst + warp * 2048 + i * 512 + lane * 16, code[i]);
-        code[i] += 64;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = (threadIdx.x >> 4) + 16 * i;
-        if (c < columns) {
-          copy_async(dst + kWarps * 2048 + c * 320 + (threadIdx.x & 15) * 16, xp[i]);
-          xp[i] += 128;
-        }
-      }
-      const int r = threadIdx.x & 31, q = threadIdx.x >> 5;
-      if (q < GPB && r * CP < columns) {
-        copy_async4(dst + kWarps * 2048 + kWideX + (q * 32 + r) * 4, xs);
-        xs += GPB;
-      }
-      if (bring == 0) load_scales<GPB, ZEROS, TAIL>(scale_in[0], ps, pz, a.groups - kb * GPB);
-      else load_scales<GPB, ZEROS, TAIL>(scale_in[1], ps, pz, a.groups - kb * GPB);
-      ps += GPB;
-      if (ZEROS) pz += GPB;
-      ++kb;
-      if (--left == 0) {
-        it.next(gridDim.x, a);
-        enter();
-      }
-    }
-    copies_commit();
-    fill = fill + 1 == kWideSlots ? 0 : fill + 1;
-    bring ^= 1;
-  };
-  enter();
-  Item now[2] = {it, it};  // of the stage at hand and of the next
-  int left_now[2] = {left, 0};
-  pdl_wait();  // the split rows
-  fetch();
-  now[1] = it;
-  left_now[1] = left;
-  fetch();
-
-  int slot = 0, use = 0;
-  while (now[0].chunk < chunks) {
-    const Item mine = now[0];
-    int row_first, row_count;
-    rows_of(mine, row_first, row_count);
-    float acc[MT][NT][2][XR];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < XR; ++i) acc[m][n][0][i] = acc[m][n][1][i] = 0.f;
-
-    for (bool more = true; more;) {
-      copies_wait<1>();
-      __syncthreads();  // everybody's copies are there, and the oldest slot is free
-      const Scales<GPB> mine_s = use ? scale_in[1] : scale_in[0];
-      use ^= 1;
-      more = left_now[0] > 1;
-      now[0] = now[1];
-      left_now[0] = left_now[1];
-      now[1] = it;
-      left_now[1] = left;
-      fetch();
-      const uint32_t src = base + slot * kWideStage;
-      slot = slot + 1 == kWideSlots ? 0 : slot + 1;
-      uint32_t w[R][4];
-      Scales<GPB> s[R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const uint4 q = lds16(src + warp * 2048 + i * 512 + lane * 16);
-        w[i][0] = q.x;
-        w[i][1] = q.y;
-        w[i][2] = q.z;
-        w[i][3] = q.w;
-        s[i] = scales_from<GPB, ZEROS>(mine_s, (lane & ~3) + i);
-      }
-      const uint32_t xs = src + kWarps * 2048 + g * 320 + t * 16;
-      const uint32_t fs = src + kWarps * 2048 + kWideX;
-#pragma unroll
-      for (int q = 0; q < GPB; ++q) {
-        float sum[MT][NT][4];
-#pragma unroll
-        for (int j = q * G32; j < (q + 1) * G32; ++j) {
-          uint32_t p[R][4];
-#pragma unroll
-          for (int i = 0; i < R; ++i) pairs_of(w[i][j], p[i]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (n > 0 && n * 8 >= row_count * CP) break;
-            const uint4 x = lds16(xs + n * (8 * 320) + j * 64);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const uint32_t(&lo)[4] = p[2 * m], (&hi)[4] = p[2 * m + 1];
-              if (j == q * G32) mma_first(sum[m][n], lo[0], hi[0], lo[1], hi[1], x.x, x.y);
-              else mma(sum[m][n], lo[0], hi[0], lo[1], hi[1], x.x, x.y);
-              mma(sum[m][n], lo[2], hi[2], lo[3], hi[3], x.z, x.w);
-            }
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n > 0 && n * 8 >= row_count * CP) break;
-          float sx[XR];
-          if (CP == 2) {
-            sx[0] = lds4(fs + (q * 32 + n * 4 + t) * 4);
-          } else {
-            const float2 v = lds8(fs + (q * 32 + n * 8 + 2 * t) * 4);
-            sx[0] = v.x;
-            sx[XR - 1] = v.y;
-          }
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float sc = scale_of(s[2 * m + i], q);
-              const float z = zero_of<GPB, ZEROS>(s[2 * m + i], q);
-              const float* u = &sum[m][n][2 * i];
-              if (CP == 2) {
-                acc[m][n][i][0] += sc * (u[0] + 0.00048828125f * u[1] - z * sx[0]);
-              } else {
-                acc[m][n][i][0] += sc * (u[0] - z * sx[0]);
-                acc[m][n][i][XR - 1] += sc * (u[1] - z * sx[XR - 1]);
-              }
-            }
-        }
-      }
-    }
-
-    const int o0 = mine.tile * (kTile * kWarps) + warp * kTile;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int o = o0 + m * (kTile / 2) + g;
-      if (o >= a.N) continue;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < XR; ++i) {
-          const int r = (n * 8 + 2 * t) / CP + i;
-          if (r < row_count)
-            put<MODE>(a, plan, mine.part, row_first, r, o, acc[m][n][0][i], acc[m][n][1][i]);
-        }
-    }
-  }
-  copies_wait<0>();
-}
+namespace moe {
+namespace w4 {
 
 // How an item's inputs are shared out.  A warp's time is about its blocks, and
 // four more for the item's ends; a launch takes as many rounds as the warps at
@@ -895,9 +659,9 @@ inline Share share_narrow(int64_t items, int stages, bool rest) {
   }
   return best;
 }
+// blocks: of inputs, of the longest part
 inline Share share_wide(int64_t items, int blocks) {
-  constexpr int kAtOnce = kBlocksPerSm * kSms;
-  return {1, (items + kAtOnce - 1) / kAtOnce * (blocks + 5)};
+  return {1, (items + kSms - 1) / kSms * (blocks + 4)};
 }
 // Parts of a row that are items of their own, where whole rows would leave
 // warps idle; `join`: what adding the parts up costs.
@@ -905,11 +669,11 @@ constexpr int kMostSplits = 8;
 inline int splits_of(int64_t chunks, int N, int blocks, int join, bool wide) {
   int best = 1;
   int64_t least = int64_t{1} << 62;
-  const int tile = wide ? 32 * kWarps : 16;
+  const int tile = wide ? 256 : 16;
   const int64_t items = chunks * ((N + tile - 1) / tile);
-  const int units = wide ? blocks : (blocks + 3) / 4;
+  const int units = (blocks + 3) / 4;
   for (int s = 1; s <= kMostSplits && s <= units; ++s) {
-    const Share h = wide ? share_wide(items * s, units / s)
+    const Share h = wide ? share_wide(items * s, (units + s - 1) / s * 4)
                          : share_narrow(items * s, units / s, units % s != 0);
     const int64_t cost = h.cost + (s > 1 ? join : 0);
     if (cost < least) {
@@ -936,8 +700,13 @@ inline int narrow_rows(int mode, int blocks, int splits) {
   return static_cast<int>(fit < 8 / cp ? fit : 8 / cp);
 }
 
-// The codes of `rows` rows as [blocks][rows][64 bytes], boxes of 4 blocks
-bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, int box_rows);
+// The codes of `rows` rows as [blocks][rows][64 bytes]; boxes of 4 blocks, or of
+// 2 with their 16-byte pieces swapped
+bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, int box_rows,
+               bool swapped);
+// Columns of split x as [blocks of 64 inputs][columns][128 bytes], boxes of 2 and
+// 8 columns
+bool map_x(CUtensorMap* m, const __half* x, int64_t columns, int blocks);
 
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
@@ -946,27 +715,16 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 }
 
 template <int MODE, int G32, bool ZEROS, bool TAIL>
-cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
-  const int tile = (MODE == FC1 ? 8 : 16) * (wide ? 2 * kWarps : 1);
+cudaError_t launch_narrow(Args a, cudaStream_t s) {
+  const int tile = (MODE == FC1 ? 8 : 16);
   const size_t plan = MODE == LINEAR ? 0 : sizeof(Plan);
   a.tiles = (a.N + tile - 1) / tile;
-  if (!wide) a.chunk_rows = narrow_rows(MODE, a.blocks, a.splits);
-  const int chunk_rows = wide ? 32 / pieces_of(MODE) : a.chunk_rows;
-  const int64_t chunks = MODE == LINEAR ? (a.rows + chunk_rows - 1) / chunk_rows
+  a.chunk_rows = narrow_rows(MODE, a.blocks, a.splits);
+  const int64_t chunks = MODE == LINEAR ? (a.rows + a.chunk_rows - 1) / a.chunk_rows
                                          : (a.pairs < a.E ? a.pairs : a.E);  // about
   const int64_t items = chunks * a.tiles * a.splits;
-  const int units = wide ? a.blocks : (a.blocks + 3) / 4;
-  a.split_units = units / a.splits;
-  a.split_rest = units % a.splits;
-  constexpr int kMostBlocks = kBlocksPerSm * kSms;
-  if (wide) {
-    auto k = w4_wide_kernel<MODE, G32, ZEROS, TAIL>;
-    const size_t smem = kWideSlots * kWideStage + plan;
-    const cudaError_t st = allow_smem(k, smem);
-    if (st != cudaSuccess) return st;
-    const unsigned grid = static_cast<unsigned>(items < kMostBlocks ? items : kMostBlocks);
-    return launch_dependent(k, dim3(grid), dim3(kWarps * 32), smem, s, a);
-  }
+  a.split_units = (a.blocks + 3) / 4 / a.splits;
+  a.split_rest = (a.blocks + 3) / 4 % a.splits;
   auto k = w4_narrow_kernel<MODE, G32, ZEROS, TAIL>;
   const size_t smem = kNarrowWarps * 2 * 4096 +
                       2 * kNarrowWarps * (4 / pieces_of(MODE)) * 32 * 4 + kNarrowX + plan;
@@ -977,8 +735,8 @@ cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
   a.each_rest = (a.split_units + a.wk) / a.wk;
   const int64_t all = static_cast<int64_t>(MODE == LINEAR ? 1 : a.E) * a.N;
   CUtensorMap m0, m1;
-  if (!map_codes(&m0, a.w0.codes, all, a.blocks, MODE == FC1 ? 8 : 16) ||
-      !map_codes(&m1, a.w1.codes, all, a.blocks, MODE == FC1 ? 8 : 16))
+  if (!map_codes(&m0, a.w0.codes, all, a.blocks, MODE == FC1 ? 8 : 16, false) ||
+      !map_codes(&m1, a.w1.codes, all, a.blocks, MODE == FC1 ? 8 : 16, false))
     return cudaErrorInvalidValue;
   a.x_pitch = narrow_x_pitch(a.blocks, a.splits);
   a.s_pitch = narrow_s_pitch(a.blocks, a.splits);
@@ -991,15 +749,41 @@ cudaError_t launch_one(Args a, bool wide, cudaStream_t s) {
 }
 
 template <int MODE, int G32>
+cudaError_t launch_wide(Args a, cudaStream_t s) {
+  const int tile = MODE == FC1 ? 128 : 256;
+  a.tiles = (a.N + tile - 1) / tile;
+  a.chunk_rows = kTallColumns / pieces_of(MODE);
+  const int64_t chunks = MODE == LINEAR ? (a.rows + a.chunk_rows - 1) / a.chunk_rows
+                                         : (a.pairs < a.E ? a.pairs : a.E);  // about
+  const int64_t items = chunks * a.tiles * a.splits;
+  a.split_units = (a.blocks + 3) / 4 / a.splits;
+  a.split_rest = (a.blocks + 3) / 4 % a.splits;
+  auto k = w4_wide_kernel<MODE, G32>;
+  const size_t smem = kTallSmem + (MODE == LINEAR ? 0 : sizeof(Plan));
+  const cudaError_t st = allow_smem(k, smem);
+  if (st != cudaSuccess) return st;
+  const int64_t all = static_cast<int64_t>(MODE == LINEAR ? 1 : a.E) * a.N;
+  const int64_t columns = static_cast<int64_t>(MODE == LINEAR ? a.rows : a.pairs) * pieces_of(MODE);
+  CUtensorMap m0, m1, mx;
+  if (!map_codes(&m0, a.w0.codes, all, a.blocks, 128, true) ||
+      !map_codes(&m1, a.w1.codes, all, a.blocks, 128, true) ||
+      !map_x(&mx, a.x, columns, a.blocks))
+    return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(items < kSms ? items : kSms);
+  return launch_dependent(k, dim3(grid), dim3(kTallRoles * 32), smem, s, m0, m1, mx, a);
+}
+
+template <int MODE, int G32>
 cudaError_t launch_group(int K, bool wide, const Args& a, cudaStream_t s) {
+  if (wide) return launch_wide<MODE, G32>(a, s);
   // K is a multiple of the group, and of 128 in the layer
   if constexpr (MODE == LINEAR && G32 < 4) {
     if (K % 128 != 0)
-      return a.w0.zeros ? launch_one<MODE, G32, true, true>(a, wide, s)
-                        : launch_one<MODE, G32, false, true>(a, wide, s);
+      return a.w0.zeros ? launch_narrow<MODE, G32, true, true>(a, s)
+                        : launch_narrow<MODE, G32, false, true>(a, s);
   }
-  return a.w0.zeros ? launch_one<MODE, G32, true, false>(a, wide, s)
-                    : launch_one<MODE, G32, false, false>(a, wide, s);
+  return a.w0.zeros ? launch_narrow<MODE, G32, true, false>(a, s)
+                    : launch_narrow<MODE, G32, false, false>(a, s);
 }
 
 template <int MODE>

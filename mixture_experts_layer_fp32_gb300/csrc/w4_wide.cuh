@@ -1,0 +1,452 @@
+// Products with 4-bit weights for more rows: chunks of up to 64 columns (64 rows
+// of x; FC2: 32, two columns each) on the tensor cores' own memory.
+//
+// A block, one to an SM, takes 256 outputs of a chunk at a time (FC1: 128 gate
+// rows and the 128 up rows of the same features) as two tiles of 128.  For each
+// 128 inputs
+//   - TMA brings the tiles' codes (two blocks of inputs in a copy) and x;
+//   - four warps a tile turn a row's 64 bytes of codes, a row to a thread, into
+//     fp16 differences q - zero in the tensor memory, the A operand: masks of the
+//     words as in the narrow kernel, and one exact subtraction of subnormals for
+//     two codes (the narrow kernel takes the zeros off a group's sum instead: it
+//     has 8 columns and this one has 64, so there the sums are the cheaper place
+//     and here the codes are);
+//   - one thread multiplies, a fresh sum for each group of inputs;
+//   - eight warps, an output to a thread and half the columns each, read the
+//     group's sums back and add them up under its scale in fp32.
+// All of them run at once and hand each other slots through mbarriers.
+//
+// mma.sync from registers ran the same work at 24% of the memory's rate: every
+// warp reads the whole x for its 32 outputs, and the conversion, the products
+// and the scaling wait for one another within a warp.
+#pragma once
+
+namespace moe {
+namespace w4 {
+
+constexpr int kTallRoles = 19;             // warps: 8 add up, 8 convert, codes, x, products
+constexpr int kTallColumns = 64;           // most columns of a chunk
+constexpr int kTallStages = 4;             // of codes: 2 blocks of inputs of 2 tiles
+constexpr int kTallStage = 2 * 2 * 128 * 64;
+constexpr int kTallXs = 4;                 // of x: a block of inputs
+constexpr int kTallX = kTallColumns * 256;
+constexpr int kTallSmem = kTallStages * kTallStage + kTallXs * kTallX + 1024;
+
+struct TallBars {
+  uint64_t code_full[kTallStages], code_free[kTallStages];
+  uint64_t x_full[kTallXs], x_free[kTallXs];
+  uint64_t a_full[2][2], a_free[2][2];  // [tile][slot]
+  uint64_t d_full[2][2], d_free[2][2];
+};
+
+// Waits of one warp or thread; after one that ran out it goes on with what is
+// there, so that nobody waits for it.
+struct Waits {
+  int* err;
+  bool lost = false;
+  // by a warp
+  __device__ __forceinline__ void operator()(uint32_t bar, int parity) {
+    alone(bar, parity);
+    __syncwarp();
+  }
+  // by a thread
+  __device__ __forceinline__ void alone(uint32_t bar, int parity) {
+    if (lost || ptx::mbar_try_wait(bar, parity)) return;
+    const long long began = clock64();
+    while (!ptx::mbar_try_wait(bar, parity))
+      if (clock64() - began > kWaitCycles) {
+        lost = true;
+        report_error(err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
+        return;
+      }
+  }
+};
+
+// A slot of a ring and the parity of its barriers' phase.
+template <int SLOTS>
+struct Ring {
+  int at = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == SLOTS) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
+                 "=f"(r[6]), "=f"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem], fp16 operands, by one thread
+__device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Four neighbouring groups' scales (bf16) and zeros of a row, `left` the groups
+// from there to the row's end; past it 0.  `whole`: rows of a multiple of 4 groups.
+__device__ __forceinline__ uint2 four_scales(const unsigned short* p, int left, bool whole) {
+  if (whole) return left > 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0u, 0u);
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = i < left ? __ldg(p + i) : 0u;
+  return make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+}
+__device__ __forceinline__ uint32_t four_zeros(const uint8_t* p, int left, bool whole) {
+  if (whole) return left > 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+  uint32_t v = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v |= (i < left ? static_cast<uint32_t>(__ldg(p + i)) : 0u) << 8 * i;
+  return v;
+}
+
+__device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
+  const __half2 d = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+template <int MODE, int G32>
+__global__ void __launch_bounds__(kTallRoles * 32, 1)
+    w4_wide_kernel(const __grid_constant__ CUtensorMap map0,
+                   const __grid_constant__ CUtensorMap map1,
+                   const __grid_constant__ CUtensorMap map_x, Args a) {
+  constexpr int GPB = 4 / G32;
+  constexpr int CP = pieces_of(MODE);
+  constexpr int kTile = MODE == FC1 ? 128 : 256;  // outputs of an item
+  constexpr int SB = 4;                           // blocks of a unit of a part
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TallBars bars;
+  __shared__ uint32_t tmem_at;
+  const uint32_t base = (ptx::smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t xs_at = base + kTallStages * kTallStage;
+  Plan& plan = *reinterpret_cast<Plan*>(smem_raw + kTallSmem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto bar = [](const uint64_t& b) { return ptx::smem_u32(&b); };
+  pdl_trigger();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTallStages; ++i) {
+      ptx::mbar_init(bar(bars.code_full[i]), 1);
+      ptx::mbar_init(bar(bars.code_free[i]), 8);
+    }
+    for (int i = 0; i < kTallXs; ++i) {
+      ptx::mbar_init(bar(bars.x_full[i]), 1);
+      ptx::mbar_init(bar(bars.x_free[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(bar(bars.a_full[i / 2][i % 2]), 4);
+      ptx::mbar_init(bar(bars.a_free[i / 2][i % 2]), 1);
+      ptx::mbar_init(bar(bars.d_full[i / 2][i % 2]), 1);
+      ptx::mbar_init(bar(bars.d_free[i / 2][i % 2]), 8);
+    }
+    ptx::fence_mbar_init();
+  }
+  if (warp == 18) {
+    ptx::tmem_alloc(ptx::smem_u32(&tmem_at), 512);
+    ptx::tmem_relinquish();
+  }
+  int chunks;
+  if (MODE == LINEAR) {
+    chunks = (a.rows + a.chunk_rows - 1) / a.chunk_rows;
+  } else {
+    make_plan(plan, a, a.chunk_rows);
+    chunks = plan.chunks;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  // A: 64 columns of a block's 128 inputs, [tile][slot]; D: 64 columns, [tile][slot]
+  auto a_at = [&](int d, int slot) { return tmem + d * 128 + slot * 64; };
+  auto d_at = [&](int d, int slot) { return tmem + 256 + d * 128 + slot * 64; };
+
+  Waits wait{a.err};
+  Item it(blockIdx.x, a);
+  // of the item: its first block of inputs, how many, its rows of x
+  int kb = 0, nb = 0, row_first = 0, row_count = 0;
+  uint32_t row = 0;  // of its weights
+  auto enter = [&]() {
+    if (it.chunk >= chunks) return false;
+    const int first = it.part * a.split_units + min(it.part, a.split_rest);
+    const int units = a.split_units + (it.part < a.split_rest);
+    kb = first * SB;
+    nb = min(units * SB, a.blocks - kb);
+    uint32_t e = 0;
+    if (MODE == LINEAR) {
+      row_first = it.chunk * a.chunk_rows;
+      row_count = min(a.chunk_rows, a.rows - row_first);
+    } else {
+      e = plan.chunk_expert[it.chunk];
+      row_first = plan.chunk_row[it.chunk];
+      row_count = min(a.chunk_rows, plan.end[e] - row_first);
+    }
+    row = e * a.N + static_cast<uint32_t>(it.tile) * kTile;
+    return true;
+  };
+
+  if (warp < 8) {
+    // ---- sums: an output of each tile, half of the columns ----
+    const int e = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // << 16, by 32
+    const bool whole = a.groups % 4 == 0;
+    constexpr int R = 32 / CP;  // rows of x
+    pdl_wait();                 // the rows' units; and the output is free
+    Ring<2> ring;               // of D; both tiles' go on together
+    for (; enter(); it.next(gridDim.x, a)) {
+      const int half = (row_count * CP + 15) / 16 * 8;
+      const int o[2] = {it.tile * kTile + r, it.tile * kTile + (MODE == FC1 ? 0 : 128) + r};
+      const unsigned short* ps[2];
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const W4& w = MODE == FC1 && d ? a.w1 : a.w0;
+        ps[d] = reinterpret_cast<const unsigned short*>(w.scales) +
+                static_cast<uint64_t>(row - it.tile * kTile + min(o[d], a.N - 1)) * a.groups +
+                kb * GPB;
+      }
+      const int n = nb * GPB, left = a.groups - kb * GPB;
+      uint2 now[2], next[2];
+#pragma unroll
+      for (int d = 0; d < 2; ++d) next[d] = four_scales(ps[d], left, whole);
+      float acc[2][R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) acc[0][i] = acc[1][i] = 0.f;
+#pragma unroll 1
+      for (int g = 0; g < n; ++g) {
+        if ((g & 3) == 0) {
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            now[d] = next[d];
+            next[d] = four_scales(ps[d] + g + 4, left - g - 4, whole);
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const float s = __uint_as_float(now[d].x << 16);
+          now[d].x = __funnelshift_r(now[d].x, now[d].y, 16);
+          now[d].y >>= 16;
+          wait(bar(bars.d_full[d][ring.at]), ring.phase);
+          ptx::tc_fence_after();
+          const uint32_t at = d_at(d, ring.at) + lanes + e * half;
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            if (c * 8 >= half) break;
+            float v[16];
+            tmem_ld8(at + c * 8, v);
+            if (c * 8 + 8 < half) tmem_ld8(at + c * 8 + 8, v + 8);
+            ptx::tmem_wait_ld();
+            if (c * 8 + 16 >= half) {  // the last of them
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(bar(bars.d_free[d][ring.at]));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += CP) {
+              if (i == 8 && c * 8 + 8 >= half) break;
+              // FC2: the second piece is in 2^-11 of the first's unit
+              const float sum = CP == 2 ? v[i] + 0.00048828125f * v[i + 1] : v[i];
+              acc[d][(c * 8 + i) / CP] += s * sum;
+            }
+          }
+        }
+        ring.next();
+      }
+      // the row's unit, and 2^24 for the codes' 2^-24
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int rx = e * (half / CP) + i;
+        if (i * CP >= half || rx >= row_count) break;
+        const float unit = a.unit[row_first + rx];
+        const float v0 = acc[0][i] * 16777216.f * unit, v1 = acc[1][i] * 16777216.f * unit;
+        if (MODE == FC1) {
+          if (o[0] < a.N)
+            static_cast<float*>(a.out)[static_cast<int64_t>(row_first + rx) * a.N + o[0]] =
+                v0 / (1.f + expf(-v0)) * v1;
+        } else {
+          const int64_t at =
+              MODE == FC2
+                  ? static_cast<int64_t>(it.part) * a.pairs + plan.pair[row_first + rx]
+                  : static_cast<int64_t>(it.part) * a.rows + row_first + rx;
+          if (MODE == FC2 || a.out_f32) {
+            float* out = static_cast<float*>(a.out) + at * a.N;
+            if (o[0] < a.N) out[o[0]] = v0;
+            if (o[1] < a.N) out[o[1]] = v1;
+          } else {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * a.N;
+            if (o[0] < a.N) out[o[0]] = __float2bfloat16_rn(v0);
+            if (o[1] < a.N) out[o[1]] = __float2bfloat16_rn(v1);
+          }
+        }
+      }
+    }
+  } else if (warp < 16) {
+    // ---- codes: a row to a thread ----
+    const int d = (warp - 8) >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const bool whole = a.groups % 4 == 0;
+    const W4& w = MODE == FC1 && d ? a.w1 : a.w0;
+    Ring<kTallStages> code;
+    Ring<2> ring;
+    for (; enter(); it.next(gridDim.x, a)) {
+      const int o = it.tile * kTile + (MODE == FC1 ? 0 : d * 128) + r;
+      const int left = a.groups - kb * GPB;
+      const uint8_t* pz = nullptr;
+      uint32_t z = 0x08080808u, z_next = z;
+      if (w.zeros != nullptr) {
+        pz = w.zeros +
+             static_cast<uint64_t>(row - it.tile * kTile + min(o, a.N - 1)) * a.groups + kb * GPB;
+        z_next = four_zeros(pz, left, whole);
+      }
+#pragma unroll 1
+      for (int b = 0; b < nb; ++b) {
+        if ((b & (G32 - 1)) == 0) {  // four groups further
+          z = z_next;
+          const int g = b * GPB + 4;
+          if (pz != nullptr) z_next = four_zeros(pz + g, left - g, whole);
+        }
+        if ((b & 1) == 0) wait(bar(bars.code_full[code.at]), code.phase);
+        // the copy's 16-byte pieces are swapped by bits 7 and 8 of their place
+        const uint32_t src =
+            base + code.at * kTallStage + d * (kTallStage / 2) + (b & 1) * 8192 + r * 64;
+        uint4 q[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) q[c] = lds16(src + ((c ^ ((r >> 1) & 3)) << 4));
+        if ((b & 1) == 1 || b + 1 == nb) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(bars.code_free[code.at]));
+          code.next();
+        }
+        wait(bar(bars.a_free[d][ring.at]), ring.phase ^ 1);
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int j = h * 2 + jj;  // inputs 32 j ..
+            const uint32_t zero = (z >> (G32 == 4 ? 0 : 8 * (j / G32))) & 15u;
+            const uint32_t z0 = zero * 0x00010001u, z1 = z0 << 4;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t p[4];
+              pairs_of(j == 0 ? q[c].x : j == 1 ? q[c].y : j == 2 ? q[c].z : q[c].w, p);
+              v[jj * 16 + c * 4 + 0] = less(p[0], z0);
+              v[jj * 16 + c * 4 + 1] = less(p[1], z1);
+              v[jj * 16 + c * 4 + 2] = less(p[2], z0);
+              v[jj * 16 + c * 4 + 3] = less(p[3], z1);
+            }
+          }
+          tmem_st32(a_at(d, ring.at) + lanes + h * 32, v);
+        }
+        z >>= G32 == 4 ? 8 : G32 == 2 ? 16 : 0;
+        tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(bars.a_full[d][ring.at]));
+        ring.next();
+      }
+    }
+  } else if (warp == 16) {
+    // ---- the codes' copies ----
+    Ring<kTallStages> code;
+    for (; enter(); it.next(gridDim.x, a)) {
+      const bool second = MODE == FC1 || it.tile * kTile + 128 < a.N;
+      for (int b = 0; b < nb; b += 2) {
+        wait(bar(bars.code_free[code.at]), code.phase ^ 1);
+        if (lane == 0) {
+          const uint32_t dst = base + code.at * kTallStage, full = bar(bars.code_full[code.at]);
+          ptx::mbar_arrive_expect_tx(full, second ? kTallStage : kTallStage / 2);
+          // blocks past the row's end come as zeros
+          ptx::tma_load_3d(dst, &map0, 0, static_cast<int>(row), kb + b, full);
+          if (second)
+            ptx::tma_load_3d(dst + kTallStage / 2, MODE == FC1 ? &map1 : &map0, 0,
+                             static_cast<int>(row) + (MODE == FC1 ? 0 : 128), kb + b, full);
+        }
+        __syncwarp();
+        code.next();
+      }
+    }
+  } else if (warp == 17) {
+    // ---- the copies of x: 8 columns of a block's inputs each ----
+    pdl_wait();
+    Ring<kTallXs> ring;
+    for (; enter(); it.next(gridDim.x, a)) {
+      const int copies = (row_count * CP + 7) / 8;
+      for (int b = 0; b < nb; ++b) {
+        const uint32_t full = bar(bars.x_full[ring.at]);
+        wait(bar(bars.x_free[ring.at]), ring.phase ^ 1);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full, copies * 2048);
+        __syncwarp();
+        if (lane < copies)
+          ptx::tma_load_3d(xs_at + ring.at * kTallX + lane * 2048, &map_x, 0,
+                           row_first * CP + lane * 8, (kb + b) * 2, full);
+        ring.next();
+      }
+    }
+  } else if (lane == 0) {
+    // ---- products ----
+    Ring<kTallXs> ring;
+    Ring<2> as, ds;  // of A and D, both tiles' together
+    for (; enter(); it.next(gridDim.x, a)) {
+      const uint32_t columns = (row_count * CP + 15) / 16 * 16;
+      const uint32_t idesc = (1u << 4) | (columns >> 3) << 17 | (128u >> 4) << 24;
+      for (int b = 0; b < nb; ++b) {
+        wait.alone(bar(bars.x_full[ring.at]), ring.phase);
+        wait.alone(bar(bars.a_full[0][as.at]), as.phase);
+        wait.alone(bar(bars.a_full[1][as.at]), as.phase);
+        const uint32_t xb = xs_at + ring.at * kTallX;
+#pragma unroll
+        for (int q = 0; q < GPB; ++q) {
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            wait.alone(bar(bars.d_free[d][ds.at]), ds.phase ^ 1);
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int k = q * G32 * 2; k < (q + 1) * G32 * 2; ++k)
+              umma_f16_ta(d_at(d, ds.at), a_at(d, as.at) + k * 8,
+                          ptx::sw128_desc(xb + (k >> 2) * 1024 + (k & 3) * 32, 0, 2048), idesc,
+                          k > q * G32 * 2);
+            ptx::umma_commit(bar(bars.d_full[d][ds.at]));
+          }
+          ds.next();
+        }
+        ptx::umma_commit(bar(bars.a_free[0][as.at]));
+        ptx::umma_commit(bar(bars.a_free[1][as.at]));
+        ptx::umma_commit(bar(bars.x_free[ring.at]));
+        as.next();
+        ring.next();
+      }
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 18) ptx::tmem_dealloc(tmem, 512);
+}
+
+}  // namespace w4
+}  // namespace moe
