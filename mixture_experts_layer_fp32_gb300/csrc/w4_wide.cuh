@@ -24,7 +24,7 @@
 namespace moe {
 namespace w4 {
 
-constexpr int kTallRoles = 19;             // warps: 8 add up, 8 convert, codes, x, products
+constexpr int kTallRoles = 20;             // warps: 8 add up, 8 convert, codes, x, products, none
 constexpr int kTallColumns = 64;           // most columns of a chunk
 constexpr int kTallStages = 4;             // of codes: 2 blocks of inputs of 2 tiles
 constexpr int kTallStage = 2 * 2 * 128 * 64;
@@ -39,26 +39,21 @@ struct TallBars {
   uint64_t d_full[2][2], d_free[2][2];
 };
 
-// Waits of one warp or thread; after one that ran out it goes on with what is
+// Waits of a warp; after one that ran out it goes on with what is
 // there, so that nobody waits for it.
 struct Waits {
   int* err;
   bool lost = false;
-  // by a warp
   __device__ __forceinline__ void operator()(uint32_t bar, int parity) {
-    alone(bar, parity);
+    if (!lost && !ptx::mbar_try_wait(bar, parity)) {
+      const long long began = clock64();
+      while (!lost && !ptx::mbar_try_wait(bar, parity))
+        if (clock64() - began > kWaitCycles) {
+          lost = true;
+          report_error(err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
+        }
+    }
     __syncwarp();
-  }
-  // by a thread
-  __device__ __forceinline__ void alone(uint32_t bar, int parity) {
-    if (lost || ptx::mbar_try_wait(bar, parity)) return;
-    const long long began = clock64();
-    while (!ptx::mbar_try_wait(bar, parity))
-      if (clock64() - began > kWaitCycles) {
-        lost = true;
-        report_error(err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
-        return;
-      }
   }
 };
 
@@ -125,6 +120,24 @@ __device__ __forceinline__ uint32_t four_zeros(const uint8_t* p, int left, bool 
   return v;
 }
 
+// This warpgroup's registers to a thread.
+template <int N, bool MORE>
+__device__ __forceinline__ void registers() {
+  if (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
   const __half2 d = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&d);
@@ -185,6 +198,8 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
   auto a_at = [&](int d, int slot) { return tmem + d * 128 + slot * 64; };
   auto d_at = [&](int d, int slot) { return tmem + 256 + d * 128 + slot * 64; };
 
+  // Registers: 640 threads are launched with 96 each; 256 with 120, 256 with 88
+  // and 128 with 64 come to the same.
   Waits wait{a.err};
   Item it(blockIdx.x, a);
   // of the item: its first block of inputs, how many, its rows of x
@@ -210,6 +225,7 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
   };
 
   if (warp < 8) {
+    registers<120, true>();
     // ---- sums: an output of each tile, half of the columns ----
     const int e = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // << 16, by 32
@@ -304,6 +320,7 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
       }
     }
   } else if (warp < 16) {
+    registers<88, false>();
     // ---- codes: a row to a thread ----
     const int d = (warp - 8) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
@@ -370,7 +387,9 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
         ring.next();
       }
     }
-  } else if (warp == 16) {
+  } else {
+  registers<64, false>();
+  if (warp == 16) {
     // ---- the codes' copies ----
     Ring<kTallStages> code;
     for (; enter(); it.next(gridDim.x, a)) {
@@ -407,40 +426,50 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
         ring.next();
       }
     }
-  } else if (lane == 0) {
-    // ---- products ----
+  } else if (warp == 18) {
+    // ---- products: the warp keeps together, so that addresses stay in uniform
+    // registers, and one thread of it issues ----
+    const bool issues = elect_one();
     Ring<kTallXs> ring;
     Ring<2> as, ds;  // of A and D, both tiles' together
     for (; enter(); it.next(gridDim.x, a)) {
       const uint32_t columns = (row_count * CP + 15) / 16 * 16;
       const uint32_t idesc = (1u << 4) | (columns >> 3) << 17 | (128u >> 4) << 24;
+#pragma unroll 1
       for (int b = 0; b < nb; ++b) {
-        wait.alone(bar(bars.x_full[ring.at]), ring.phase);
-        wait.alone(bar(bars.a_full[0][as.at]), as.phase);
-        wait.alone(bar(bars.a_full[1][as.at]), as.phase);
-        const uint32_t xb = xs_at + ring.at * kTallX;
+        wait(bar(bars.x_full[ring.at]), ring.phase);
+        wait(bar(bars.a_full[0][as.at]), as.phase);
+        wait(bar(bars.a_full[1][as.at]), as.phase);
+        // a step of 16 inputs is 32 bytes on, 64 inputs 1024
+        const uint64_t x = ptx::sw128_desc(xs_at + ring.at * kTallX, 0, 2048);
 #pragma unroll
         for (int q = 0; q < GPB; ++q) {
 #pragma unroll
           for (int d = 0; d < 2; ++d) {
-            wait.alone(bar(bars.d_free[d][ds.at]), ds.phase ^ 1);
+            wait(bar(bars.d_free[d][ds.at]), ds.phase ^ 1);
             ptx::tc_fence_after();
+            if (issues) {
 #pragma unroll
-            for (int k = q * G32 * 2; k < (q + 1) * G32 * 2; ++k)
-              umma_f16_ta(d_at(d, ds.at), a_at(d, as.at) + k * 8,
-                          ptx::sw128_desc(xb + (k >> 2) * 1024 + (k & 3) * 32, 0, 2048), idesc,
-                          k > q * G32 * 2);
-            ptx::umma_commit(bar(bars.d_full[d][ds.at]));
+              for (int k = q * G32 * 2; k < (q + 1) * G32 * 2; ++k)
+                umma_f16_ta(d_at(d, ds.at), a_at(d, as.at) + k * 8,
+                            x + ((k >> 2) * 64 + (k & 3) * 2), idesc, k > q * G32 * 2);
+              ptx::umma_commit(bar(bars.d_full[d][ds.at]));
+            }
+            __syncwarp();
           }
           ds.next();
         }
-        ptx::umma_commit(bar(bars.a_free[0][as.at]));
-        ptx::umma_commit(bar(bars.a_free[1][as.at]));
-        ptx::umma_commit(bar(bars.x_free[ring.at]));
+        if (issues) {
+          ptx::umma_commit(bar(bars.a_free[0][as.at]));
+          ptx::umma_commit(bar(bars.a_free[1][as.at]));
+          ptx::umma_commit(bar(bars.x_free[ring.at]));
+        }
+        __syncwarp();
         as.next();
         ring.next();
       }
     }
+  }
   }
   __syncwarp();
   ptx::tc_fence_before();
