@@ -304,6 +304,7 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
     a.groups = K / group;
     a.N = N;
     a.splits = L.way.splits;
+    a.few = L.way.few;
     a.out = L.way.splits > 1 ? part : out;
     a.out_f32 = L.way.splits > 1 ? 1 : out_f32;
     st = launch_linear(group, K, L.way.wide, a, s);
@@ -363,6 +364,7 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     a.groups = h / group;
     a.N = f;
     a.splits = 1;
+    a.few = S.way1.few;
     a.out = hidden;
     st = launch_fc1(group, h, S.way1.wide, a, s);
     if (st != cudaSuccess) return st;
@@ -377,6 +379,7 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     a.groups = f / group;
     a.N = h;
     a.splits = S.way2.splits;
+    a.few = S.way2.few;
     a.out = part;
     st = launch_fc2(group, f, S.way2.wide, a, s);
     if (st != cudaSuccess) return st;

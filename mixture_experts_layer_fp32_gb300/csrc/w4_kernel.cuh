@@ -53,6 +53,7 @@ struct Args {
   int wk;                 // narrow: warps that share an item's inputs: a power of two
   int each, each_rest;    // their units, in a part of split_units and of one more
   int chunk_rows;         // rows of x of a chunk
+  bool few;               // wide: chunks of 32 columns
   int x_pitch, s_pitch;   // narrow: bytes of a column of x and of a row's sums in shared memory
   int rows;               // LINEAR: rows of x
   int out_f32;            // LINEAR
@@ -748,11 +749,14 @@ cudaError_t launch_narrow(Args a, cudaStream_t s) {
   return launch_dependent(k, dim3(grid), dim3(kNarrowWarps * 32), smem, s, m0, m1, a);
 }
 
+// rows of a chunk of the wide kernel; few: 32 columns will do
+constexpr int wide_rows(int mode, bool few) { return kTallColumns / (few ? 2 : 1) / pieces_of(mode); }
+
 template <int MODE, int G32>
 cudaError_t launch_wide(Args a, cudaStream_t s) {
   const int tile = MODE == FC1 ? 128 : 256;
   a.tiles = (a.N + tile - 1) / tile;
-  a.chunk_rows = kTallColumns / pieces_of(MODE);
+  a.chunk_rows = wide_rows(MODE, a.few);
   const int64_t chunks = MODE == LINEAR ? (a.rows + a.chunk_rows - 1) / a.chunk_rows
                                          : (a.pairs < a.E ? a.pairs : a.E);  // about
   const int64_t items = chunks * a.tiles * a.splits;
@@ -799,11 +803,11 @@ cudaError_t launch_mode(int group, int K, bool wide, const Args& a, cudaStream_t
 // the experts hit) and N outputs is run.  The narrow kernel for as few rows as
 // it can hold; join: see splits_of, negative: no splits.
 struct Way {
-  bool wide;
+  bool wide, few;
   int splits;
 };
 inline Way way_of(int mode, int64_t rows, int64_t chunks, int N, int blocks, int join) {
-  Way w = {true, 1};
+  Way w = {true, rows * pieces_of(mode) <= kTallColumns / 2, 1};
   if (rows <= 8 / pieces_of(mode)) {
     w.splits = join < 0 ? 1 : splits_of(chunks, N, blocks, join, false);
     // more parts where the rows' x would not fit

@@ -21,10 +21,12 @@
 // and the scaling wait for one another within a warp.
 #pragma once
 
+#include <type_traits>
+
 namespace moe {
 namespace w4 {
 
-constexpr int kTallRoles = 20;             // warps: 8 add up, 8 convert, codes, x, products, none
+constexpr int kTallRoles = 28;             // warps: 8 add up, 16 convert, codes, x, products, none
 constexpr int kTallColumns = 64;           // most columns of a chunk
 constexpr int kTallStages = 4;             // of codes: 2 blocks of inputs of 2 tiles
 constexpr int kTallStage = 2 * 2 * 128 * 64;
@@ -35,8 +37,8 @@ constexpr int kTallSmem = kTallStages * kTallStage + kTallXs * kTallX + 1024;
 struct TallBars {
   uint64_t code_full[kTallStages], code_free[kTallStages];
   uint64_t x_full[kTallXs], x_free[kTallXs];
-  uint64_t a_full[2][2], a_free[2][2];  // [tile][slot]
-  uint64_t d_full[2][2], d_free[2][2];
+  uint64_t a_full[2], a_free[2];  // of both tiles
+  uint64_t d_full[4], d_free[4];
 };
 
 // Waits of a warp; after one that ran out it goes on with what is
@@ -58,28 +60,23 @@ struct Waits {
 };
 
 // A slot of a ring and the parity of its barriers' phase.
-template <int SLOTS>
 struct Ring {
-  int at = 0, phase = 0;
+  int slots, at = 0, phase = 0;
   __device__ __forceinline__ void next() {
-    if (++at == SLOTS) {
+    if (++at == slots) {
       at = 0;
       phase ^= 1;
     }
   }
 };
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
-          r[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -91,6 +88,16 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* r) {
                  "=f"(r[6]), "=f"(r[7])
                : "r"(taddr)
                : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+        "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem], fp16 operands, by one thread
 __device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
@@ -165,21 +172,23 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTallStages; ++i) {
       ptx::mbar_init(bar(bars.code_full[i]), 1);
-      ptx::mbar_init(bar(bars.code_free[i]), 8);
+      ptx::mbar_init(bar(bars.code_free[i]), 16);
     }
     for (int i = 0; i < kTallXs; ++i) {
       ptx::mbar_init(bar(bars.x_full[i]), 1);
       ptx::mbar_init(bar(bars.x_free[i]), 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(bars.a_full[i]), 8);
+      ptx::mbar_init(bar(bars.a_free[i]), 1);
+    }
     for (int i = 0; i < 4; ++i) {
-      ptx::mbar_init(bar(bars.a_full[i / 2][i % 2]), 4);
-      ptx::mbar_init(bar(bars.a_free[i / 2][i % 2]), 1);
-      ptx::mbar_init(bar(bars.d_full[i / 2][i % 2]), 1);
-      ptx::mbar_init(bar(bars.d_free[i / 2][i % 2]), 8);
+      ptx::mbar_init(bar(bars.d_full[i]), 1);
+      ptx::mbar_init(bar(bars.d_free[i]), 8);
     }
     ptx::fence_mbar_init();
   }
-  if (warp == 18) {
+  if (warp == 26) {
     ptx::tmem_alloc(ptx::smem_u32(&tmem_at), 512);
     ptx::tmem_relinquish();
   }
@@ -194,12 +203,14 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_at;
-  // A: 64 columns of a block's 128 inputs, [tile][slot]; D: 64 columns, [tile][slot]
+  // A: 64 columns of a block's 128 inputs, [tile][slot]; D: 64 columns or, if no
+  // chunk has more than 32, 32, [tile][slot]
+  const int d_columns = a.chunk_rows * CP, d_slots = 128 / d_columns;
   auto a_at = [&](int d, int slot) { return tmem + d * 128 + slot * 64; };
-  auto d_at = [&](int d, int slot) { return tmem + 256 + d * 128 + slot * 64; };
+  auto d_at = [&](int d, int slot) { return tmem + 256 + d * 128 + slot * d_columns; };
 
-  // Registers: 640 threads are launched with 96 each; 256 with 120, 256 with 88
-  // and 128 with 64 come to the same.
+  // Registers: 896 threads are launched with 72 each; 256 with 112 and 640
+  // with 56 come to the same.
   Waits wait{a.err};
   Item it(blockIdx.x, a);
   // of the item: its first block of inputs, how many, its rows of x
@@ -225,16 +236,14 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
   };
 
   if (warp < 8) {
-    registers<120, true>();
+    registers<112, true>();
     // ---- sums: an output of each tile, half of the columns ----
     const int e = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // << 16, by 32
     const bool whole = a.groups % 4 == 0;
-    constexpr int R = 32 / CP;  // rows of x
-    pdl_wait();                 // the rows' units; and the output is free
-    Ring<2> ring;               // of D; both tiles' go on together
+    pdl_wait();  // the rows' units; and the output is free
+    Ring ring{d_slots};
     for (; enter(); it.next(gridDim.x, a)) {
-      const int half = (row_count * CP + 15) / 16 * 8;
       const int o[2] = {it.tile * kTile + r, it.tile * kTile + (MODE == FC1 ? 0 : 128) + r};
       const unsigned short* ps[2];
 #pragma unroll
@@ -245,6 +254,10 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
                 kb * GPB;
       }
       const int n = nb * GPB, left = a.groups - kb * GPB;
+      // with half of the columns known, what is read of a group is fixed
+      auto item = [&](auto known) {
+      constexpr int half = decltype(known)::value;
+      constexpr int R = half / CP;  // rows of x
       uint2 now[2], next[2];
 #pragma unroll
       for (int d = 0; d < 2; ++d) next[d] = four_scales(ps[d], left, whole);
@@ -260,42 +273,52 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
             next[d] = four_scales(ps[d] + g + 4, left - g - 4, whole);
           }
         }
+        float s[2];
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
-          const float s = __uint_as_float(now[d].x << 16);
+          s[d] = __uint_as_float(now[d].x << 16);
           now[d].x = __funnelshift_r(now[d].x, now[d].y, 16);
           now[d].y >>= 16;
-          wait(bar(bars.d_full[d][ring.at]), ring.phase);
-          ptx::tc_fence_after();
-          const uint32_t at = d_at(d, ring.at) + lanes + e * half;
+        }
+        wait(bar(bars.d_full[ring.at]), ring.phase);
+        ptx::tc_fence_after();
+        const uint32_t at = d_at(0, ring.at) + lanes + e * half;
+        // a few columns of both tiles at a time, as the registers allow
+        constexpr int some = half <= 16 ? half : 8;
 #pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            if (c * 8 >= half) break;
-            float v[16];
-            tmem_ld8(at + c * 8, v);
-            if (c * 8 + 8 < half) tmem_ld8(at + c * 8 + 8, v + 8);
-            ptx::tmem_wait_ld();
-            if (c * 8 + 16 >= half) {  // the last of them
-              ptx::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(bar(bars.d_free[d][ring.at]));
-            }
+        for (int c = 0; c < half; c += some) {
+          float v[2][some];
 #pragma unroll
-            for (int i = 0; i < 16; i += CP) {
-              if (i == 8 && c * 8 + 8 >= half) break;
-              // FC2: the second piece is in 2^-11 of the first's unit
-              const float sum = CP == 2 ? v[i] + 0.00048828125f * v[i + 1] : v[i];
-              acc[d][(c * 8 + i) / CP] += s * sum;
-            }
+          for (int d = 0; d < 2; ++d) {
+            if (some == 8) tmem_ld8(at + d * 128 + c, v[d]);
+            else tmem_ld16(at + d * 128 + c, v[d]);
           }
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < some; ++i)
+            asm volatile("" : "+f"(v[0][i]), "+f"(v[1][i]));
+          if (c + some == half) {  // the last of them
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(bars.d_free[ring.at]));
+          }
+#pragma unroll
+          for (int i = 0; i < some; i += CP)
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              // FC2: the second piece is in 2^-11 of the first's unit
+              const float sum =
+                  CP == 2 ? v[d][i] + 0.00048828125f * v[d][i + CP - 1] : v[d][i];
+              acc[d][(c + i) / CP] += s[d] * sum;
+            }
         }
         ring.next();
       }
       // the row's unit, and 2^24 for the codes' 2^-24
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int rx = e * (half / CP) + i;
-        if (i * CP >= half || rx >= row_count) break;
+        const int rx = e * R + i;
+        if (rx >= row_count) break;
         const float unit = a.unit[row_first + rx];
         const float v0 = acc[0][i] * 16777216.f * unit, v1 = acc[1][i] * 16777216.f * unit;
         if (MODE == FC1) {
@@ -318,80 +341,89 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
           }
         }
       }
+      };
+      switch ((row_count * CP + 15) / 16) {
+        case 1: item(std::integral_constant<int, 8>()); break;
+        case 2: item(std::integral_constant<int, 16>()); break;
+        case 3: item(std::integral_constant<int, 24>()); break;
+        default: item(std::integral_constant<int, 32>());
+      }
     }
-  } else if (warp < 16) {
-    registers<88, false>();
-    // ---- codes: a row to a thread ----
-    const int d = (warp - 8) >> 2, r = (warp & 3) * 32 + lane;
+  } else if (warp < 24) {
+    registers<56, false>();
+    // ---- codes: a row to a thread; a slot of A and a tile to four warps ----
+    const int d = (warp >> 2) & 1, slot = (warp - 8) >> 3, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const bool whole = a.groups % 4 == 0;
     const W4& w = MODE == FC1 && d ? a.w1 : a.w0;
-    Ring<kTallStages> code;
-    Ring<2> ring;
+    // the copy's 16-byte pieces are swapped by bits 7 and 8 of their place
+    const uint32_t src = base + d * (kTallStage / 2) + r * 64;
+    const uint32_t swap = ((r >> 1) & 3) << 4;
+    const uint32_t a_slot = a_at(d, slot) + lanes;
+    Ring code{kTallStages};
+    int turn = 0, phase = 0;  // the slot of the block to come; this slot's phase
     for (; enter(); it.next(gridDim.x, a)) {
       const int o = it.tile * kTile + (MODE == FC1 ? 0 : d * 128) + r;
       const int left = a.groups - kb * GPB;
       const uint8_t* pz = nullptr;
-      uint32_t z = 0x08080808u, z_next = z;
+      // zeros of four groups, one block of this slot's ahead
+      uint32_t z_next = 0x08080808u;
+      const int mine = (slot - turn) & 1;  // this slot's blocks: mine, mine + 2, ..
       if (w.zeros != nullptr) {
         pz = w.zeros +
              static_cast<uint64_t>(row - it.tile * kTile + min(o, a.N - 1)) * a.groups + kb * GPB;
-        z_next = four_zeros(pz, left, whole);
+        const int g = mine * GPB & ~3;
+        z_next = four_zeros(pz + g, left - g, whole);
       }
 #pragma unroll 1
-      for (int b = 0; b < nb; ++b) {
-        if ((b & (G32 - 1)) == 0) {  // four groups further
-          z = z_next;
-          const int g = b * GPB + 4;
-          if (pz != nullptr) z_next = four_zeros(pz + g, left - g, whole);
-        }
-        if ((b & 1) == 0) wait(bar(bars.code_full[code.at]), code.phase);
-        // the copy's 16-byte pieces are swapped by bits 7 and 8 of their place
-        const uint32_t src =
-            base + code.at * kTallStage + d * (kTallStage / 2) + (b & 1) * 8192 + r * 64;
-        uint4 q[4];
+      for (int b = mine; b < nb + mine; b += 2) {
+        wait(bar(bars.code_full[code.at]), code.phase);
+        if (b < nb) {
+          uint4 q[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) q[c] = lds16(src + ((c ^ ((r >> 1) & 3)) << 4));
-        if ((b & 1) == 1 || b + 1 == nb) {
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(bars.code_free[code.at]));
-          code.next();
-        }
-        wait(bar(bars.a_free[d][ring.at]), ring.phase ^ 1);
-        ptx::tc_fence_after();
+          for (int c = 0; c < 4; ++c)
+            q[c] = lds16(src + code.at * kTallStage + mine * 8192 + ((c << 4) ^ swap));
+          uint32_t z = z_next >> (8 * (b * GPB & 3));
+          if (pz != nullptr) {
+            const int g = (b + 2) * GPB & ~3;
+            z_next = four_zeros(pz + g, left - g, whole);
+          }
+          wait(bar(bars.a_free[slot]), phase ^ 1);
+          ptx::tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const int j = h * 2 + jj;  // inputs 32 j ..
-            const uint32_t zero = (z >> (G32 == 4 ? 0 : 8 * (j / G32))) & 15u;
+          for (int j = 0; j < 4; ++j) {  // inputs 32 j ..
+            const uint32_t zero = (z >> (8 * (j / G32))) & 15u;
             const uint32_t z0 = zero * 0x00010001u, z1 = z0 << 4;
+            uint32_t v[16];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t p[4];
               pairs_of(j == 0 ? q[c].x : j == 1 ? q[c].y : j == 2 ? q[c].z : q[c].w, p);
-              v[jj * 16 + c * 4 + 0] = less(p[0], z0);
-              v[jj * 16 + c * 4 + 1] = less(p[1], z1);
-              v[jj * 16 + c * 4 + 2] = less(p[2], z0);
-              v[jj * 16 + c * 4 + 3] = less(p[3], z1);
+              v[c * 4 + 0] = less(p[0], z0);
+              v[c * 4 + 1] = less(p[1], z1);
+              v[c * 4 + 2] = less(p[2], z0);
+              v[c * 4 + 3] = less(p[3], z1);
             }
+            tmem_st16(a_slot + j * 16, v);
           }
-          tmem_st32(a_at(d, ring.at) + lanes + h * 32, v);
+          tmem_wait_st();
+          ptx::tc_fence_before();
+          phase ^= 1;
         }
-        z >>= G32 == 4 ? 8 : G32 == 2 ? 16 : 0;
-        tmem_wait_st();
-        ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(bars.a_full[d][ring.at]));
-        ring.next();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(bars.code_free[code.at]));
+          if (b < nb) ptx::mbar_arrive(bar(bars.a_full[slot]));
+        }
+        code.next();
       }
+      turn ^= nb & 1;
     }
   } else {
-  registers<64, false>();
-  if (warp == 16) {
+  registers<56, false>();
+  if (warp == 24) {
     // ---- the codes' copies ----
-    Ring<kTallStages> code;
+    Ring code{kTallStages};
     for (; enter(); it.next(gridDim.x, a)) {
       const bool second = MODE == FC1 || it.tile * kTile + 128 < a.N;
       for (int b = 0; b < nb; b += 2) {
@@ -409,10 +441,10 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
         code.next();
       }
     }
-  } else if (warp == 17) {
+  } else if (warp == 25) {
     // ---- the copies of x: 8 columns of a block's inputs each ----
     pdl_wait();
-    Ring<kTallXs> ring;
+    Ring ring{kTallXs};
     for (; enter(); it.next(gridDim.x, a)) {
       const int copies = (row_count * CP + 7) / 8;
       for (int b = 0; b < nb; ++b) {
@@ -426,42 +458,39 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
         ring.next();
       }
     }
-  } else if (warp == 18) {
+  } else if (warp == 26) {
     // ---- products: the warp keeps together, so that addresses stay in uniform
     // registers, and one thread of it issues ----
     const bool issues = elect_one();
-    Ring<kTallXs> ring;
-    Ring<2> as, ds;  // of A and D, both tiles' together
+    Ring ring{kTallXs};
+    Ring as{2}, ds{d_slots};  // of A and D, both tiles' together
     for (; enter(); it.next(gridDim.x, a)) {
       const uint32_t columns = (row_count * CP + 15) / 16 * 16;
       const uint32_t idesc = (1u << 4) | (columns >> 3) << 17 | (128u >> 4) << 24;
 #pragma unroll 1
       for (int b = 0; b < nb; ++b) {
         wait(bar(bars.x_full[ring.at]), ring.phase);
-        wait(bar(bars.a_full[0][as.at]), as.phase);
-        wait(bar(bars.a_full[1][as.at]), as.phase);
+        wait(bar(bars.a_full[as.at]), as.phase);
         // a step of 16 inputs is 32 bytes on, 64 inputs 1024
         const uint64_t x = ptx::sw128_desc(xs_at + ring.at * kTallX, 0, 2048);
 #pragma unroll
         for (int q = 0; q < GPB; ++q) {
+          wait(bar(bars.d_free[ds.at]), ds.phase ^ 1);
+          ptx::tc_fence_after();
+          if (issues) {
 #pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            wait(bar(bars.d_free[d][ds.at]), ds.phase ^ 1);
-            ptx::tc_fence_after();
-            if (issues) {
+            for (int d = 0; d < 2; ++d)
 #pragma unroll
               for (int k = q * G32 * 2; k < (q + 1) * G32 * 2; ++k)
                 umma_f16_ta(d_at(d, ds.at), a_at(d, as.at) + k * 8,
                             x + ((k >> 2) * 64 + (k & 3) * 2), idesc, k > q * G32 * 2);
-              ptx::umma_commit(bar(bars.d_full[d][ds.at]));
-            }
-            __syncwarp();
+            ptx::umma_commit(bar(bars.d_full[ds.at]));
           }
+          __syncwarp();
           ds.next();
         }
         if (issues) {
-          ptx::umma_commit(bar(bars.a_free[0][as.at]));
-          ptx::umma_commit(bar(bars.a_free[1][as.at]));
+          ptx::umma_commit(bar(bars.a_free[as.at]));
           ptx::umma_commit(bar(bars.x_free[ring.at]));
         }
         __syncwarp();
@@ -474,7 +503,7 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 18) ptx::tmem_dealloc(tmem, 512);
+  if (warp == 26) ptx::tmem_dealloc(tmem, 512);
 }
 
 }  // namespace w4
