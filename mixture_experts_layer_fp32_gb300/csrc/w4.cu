@@ -16,22 +16,30 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
                      __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u));
 }
 
+// the largest magnitude of four values and one so far; infinity for any that
+// is none or not a number (fmaxf would drop it)
+__device__ __forceinline__ float top_of(float top, float4 q) {
+  const float m = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
+  const bool good = isfinite(q.x) && isfinite(q.y) && isfinite(q.z) && isfinite(q.w);
+  return fmaxf(top, good ? m : __uint_as_float(0x7f800000u));
+}
+
 // Rows of x into fp16.  With 2^E the largest magnitude of a row (its exponent),
 // x = 2^(E-14) (p0 + 2^-11 p1): p0 is the nearest fp16 number, p1 that of what
 // is left.  Inputs past K give zeros.  A row with an infinity or a NaN gives
-// NaN.  A block of the launch finds its row's largest magnitude by itself, also
-// where several share the row (few rows: reading it again is cheaper than
-// another launch); then a warp takes a block of 128 inputs at a time, a lane
-// four of them.
+// NaN.  A row to a block, which holds up to 16384 inputs from the search for the
+// largest to the splitting (two blocks that each searched the whole row took
+// 9.7 us for 128 rows of 14336, cold, where one takes @@); a warp has 128
+// inputs, a block of the weights' layout, at a time.
 // SORTED: row i is the token of the i-th pair in the plan's order.
+constexpr int kSplitWarps = 16, kHeld = 8;
 template <typename T, int G32, int CP, bool SORTED>
-__global__ void __launch_bounds__(256)
-    w4_split_kernel(int K, int blocks, int parts, const T* x, __half* pieces, float* units,
-                    float* sums, Args a) {
-  __shared__ float tops[8];
-  __shared__ int bads[8];
+__global__ void __launch_bounds__(kSplitWarps * 32)
+    w4_split_kernel(int K, int blocks, const T* x, __half* pieces, float* units, float* sums,
+                    Args a) {
+  __shared__ float tops[kSplitWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x / parts, part = blockIdx.x % parts;
+  const int row = blockIdx.x;
   pdl_trigger();
   pdl_wait();
   int from = row;
@@ -42,39 +50,32 @@ __global__ void __launch_bounds__(256)
     from = plan.token[row];
   }
   const T* xr = x + static_cast<int64_t>(from) * K;
+  float4 held[kHeld];
   float top = 0.f;
-  bool bad = false;  // fmaxf drops a NaN
-#pragma unroll 4
-  for (int k = threadIdx.x * 4; k < K; k += 1024) {
-    const float4 q = load4(xr + k);
-    const float v = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
-    bad |= !(isfinite(q.x) && isfinite(q.y) && isfinite(q.z) && isfinite(q.w));
-    top = fmaxf(top, v);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int k = (i * kSplitWarps + warp) * 128 + lane * 4;
+    held[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < K) held[i] = load4(xr + k);
   }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) top = top_of(top, held[i]);
+  for (int k = kHeld * kSplitWarps * 128 + threadIdx.x * 4; k < K; k += kSplitWarps * 128)
+    top = top_of(top, load4(xr + k));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  bad = __any_sync(~0u, bad);
-  if (lane == 0) {
-    tops[warp] = top;
-    bads[warp] = bad;
-  }
+  if (lane == 0) tops[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    top = fmaxf(top, tops[w]);
-    bad |= bads[w] != 0;
-  }
+  for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, tops[w]);
   // the exponent field of 2^(E-14), within what its reciprocal can hold
   int e = static_cast<int>(__float_as_uint(top) >> 23) - 14;
-  e = e < 1 ? 1 : e > 253 ? 253 : e;
+  e = e < 1 ? 1 : e;
   const float inverse = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-  if (part == 0 && threadIdx.x == 0)
-    units[row] = __uint_as_float(bad ? 0x7fffffffu : static_cast<uint32_t>(e) << 23);
+  if (threadIdx.x == 0)
+    units[row] = __uint_as_float(isfinite(top) ? static_cast<uint32_t>(e) << 23 : 0x7fffffffu);
 
-  for (int blk = part * 8 + warp; blk < blocks; blk += parts * 8) {
-    const int k = blk * 128 + lane * 4;
-    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (k < K) q = load4(xr + k);
+  auto split = [&](int blk, float4 q) {
     float v[4] = {q.x * inverse, q.y * inverse, q.z * inverse, q.w * inverse};
     float sum = 0.f, unit = 1.f;
 #pragma unroll
@@ -85,9 +86,9 @@ __global__ void __launch_bounds__(256)
         // the inputs 2, 3, 6 and 7 of eight meet codes that stand 4 bits higher
         const float up = i < 2 ? 1.f : 16.f;
         h[i] = __float2half_rn(v[i] * (1.f / up));
-        const float held = __half2float(h[i]) * up;
-        sum += held * unit;
-        v[i] = (v[i] - held) * 2048.f;
+        const float had = __half2float(h[i]) * up;
+        sum += had * unit;
+        v[i] = (v[i] - had) * 2048.f;
       }
       unit *= 0.00048828125f;
       __half2 out[2] = {__halves2half2(h[0], h[1]), __halves2half2(h[2], h[3])};
@@ -101,6 +102,13 @@ __global__ void __launch_bounds__(256)
     if ((lane & (kLanes - 1)) == 0)  // 2^-24, the codes' unit
       sums[(static_cast<int64_t>(row) * blocks + blk) * (4 / G32) + lane / kLanes] =
           sum * 5.9604644775390625e-08f;
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (i * kSplitWarps + warp < blocks) split(i * kSplitWarps + warp, held[i]);
+  for (int blk = kHeld * kSplitWarps + warp; blk < blocks; blk += kSplitWarps) {
+    const int k = blk * 128 + lane * 4;
+    split(blk, k < K ? load4(xr + k) : make_float4(0.f, 0.f, 0.f, 0.f));
   }
 }
 
@@ -134,14 +142,10 @@ cudaError_t launch_split(bool dependent, int group, int rows, int K, const T* x,
   auto k = group == 32   ? w4_split_kernel<T, 1, CP, SORTED>
            : group == 64 ? w4_split_kernel<T, 2, CP, SORTED>
                          : w4_split_kernel<T, 4, CP, SORTED>;
-  int parts = 2 * kSms / rows;
-  if (parts > (blocks + 7) / 8) parts = (blocks + 7) / 8;
-  if (parts < 1) parts = 1;
-  const dim3 grid(static_cast<unsigned>(rows * parts));
+  const dim3 grid(static_cast<unsigned>(rows)), block(kSplitWarps * 32);
   if (dependent)
-    return launch_dependent(k, grid, dim3(256), 0, s, K, blocks, parts, x, p.x, p.unit, p.sums,
-                            a);
-  k<<<grid, 256, 0, s>>>(K, blocks, parts, x, p.x, p.unit, p.sums, a);
+    return launch_dependent(k, grid, block, 0, s, K, blocks, x, p.x, p.unit, p.sums, a);
+  k<<<grid, block, 0, s>>>(K, blocks, x, p.x, p.unit, p.sums, a);
   return cudaGetLastError();
 }
 

@@ -662,7 +662,7 @@ inline Share share_narrow(int64_t items, int stages, bool rest) {
 }
 // blocks: of inputs, of the longest part
 inline Share share_wide(int64_t items, int blocks) {
-  return {1, (items + kSms - 1) / kSms * (blocks + 4)};
+  return {1, (items + kSms - 1) / kSms * (blocks + 2)};
 }
 // Parts of a row that are items of their own, where whole rows would leave
 // warps idle; `join`: what adding the parts up costs.
