@@ -198,7 +198,8 @@ def _host(t):
 
 
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle without the object around it (0.3 us, not 3)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ws(ws):
@@ -815,9 +816,10 @@ def alloc_workspace_linear_w4(rows, w, device="cuda"):
 
 def linear_w4(x, w, y, ws):
     """y [..., N] (bf16 or fp32) = x [..., K] bf16 . W^T; w: W4Weight [N,K]."""
-    if x.dtype != torch.bfloat16 or x.shape[-1] != w.k or w.codes.dim() != 2:
+    xs, ys = x.shape, y.shape
+    if x.dtype != torch.bfloat16 or not xs or xs[-1] != w.k or w.codes.dim() != 2:
         raise ValueError("x must be bfloat16 [..., K] and W [N, K]")
-    if y.shape[:-1] != x.shape[:-1] or y.shape[-1] != w.n:
+    if not ys or ys[-1] != w.n or ys[:-1] != xs[:-1]:
         raise ValueError("y must be [..., N]")
     b, wb = _ws(ws)
     _check(lib().moe_linear_w4(x.numel() // w.k, w.n, w.k, w.group, _p(x), w._ref, _p(y),
