@@ -309,3 +309,20 @@ def test_on_another_stream_and_in_a_graph():
     second = take()
     graph.replay()
     assert all(torch.equal(a, c) for a, c in zip(second, take()))
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M,N,K,group", [
+    (20, 40000, 384, 128),    # more tiles than SMs, rows of an odd number of blocks
+    (33, 39200, 160, 32),     # two blocks, the second a quarter full; more than 32 columns
+    (64, 40001, 64, 64),      # one block, half full; an odd number of outputs
+    (70, 1100, 1440, 32)])    # two chunks of rows; parts of different lengths
+def test_linear_more_rows(M, N, K, group, zeros):
+    import mixture_experts_layer_fp32_gb300 as moe
+    w, W = _weight((N,), K, group, zeros, M + K)
+    x = torch.randn((M, K), device="cuda").to(torch.bfloat16)
+    y = torch.full((M, N), float("nan"), device="cuda")
+    ws = moe.alloc_workspace_linear_w4(M, w)
+    moe.linear_w4(x, w, y, ws)
+    moe.check(ws)
+    bc.assert_within("y", y, x.double() @ W.t(), bc.w4_product_bound(x.double(), W), y.dtype)
