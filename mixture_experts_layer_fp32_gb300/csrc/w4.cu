@@ -1,5 +1,5 @@
 // Products with 4-bit weights (group scales) for few rows, and the routed
-// SwiGLU experts built from them: the launches around w4_kernel.
+// SwiGLU experts built from them: the launches around w4_kernel.cuh and w4_wide.cuh.
 #include "w4_kernel.cuh"
 
 namespace moe {
@@ -29,7 +29,7 @@ __device__ __forceinline__ float top_of(float top, float4 q) {
 // is left.  Inputs past K give zeros.  A row with an infinity or a NaN gives
 // NaN.  A row to a block, which holds up to 16384 inputs from the search for the
 // largest to the splitting (two blocks that each searched the whole row took
-// 9.7 us for 128 rows of 14336, cold, where one takes @@); a warp has 128
+// 9.7 us for 128 rows of 14336 where one takes 7.5, both from cold caches); a warp has 128
 // inputs, a block of the weights' layout, at a time.
 // SORTED: row i is the token of the i-th pair in the plan's order.
 constexpr int kSplitWarps = 16, kHeld = 8;

@@ -1,4 +1,5 @@
-// The kernel behind the products with 4-bit weights and the 4-bit experts.
+// The products with 4-bit weights and the 4-bit experts: the kernel for the
+// fewest rows, and how a product is shared out between kernels, parts and warps.
 //
 // y = x W^T with few rows of x reads every weight once and should be bound by
 // that stream.  What stands in the way is the work per code.  Making numbers of
@@ -12,13 +13,20 @@
 // For that the rows of x are brought to fp16 once (w4_split_kernel): with a
 // power of two for each row a bf16 number is exact (down to 2^-28 of its row's
 // largest), and an fp32 hidden value is two fp16 numbers, a column each, exact
-// to 2^-22.  The products are exact, their sums are fp32,
-// and what the zero point adds is taken off a group's sum:
-// s (sum q x - z sum x).
+// to 2^-22.  The products are exact, their sums are fp32, and what the zero
+// point adds is taken off a group's sum: s (sum q x - z sum x).
 //
 // (E4M3 operands would need two masks and one shift, but mma.sync of that type
-// is run as conversions and fp16 products on this machine: 194 instructions a
-// block of 16 x 128 codes against 75.)
+// costs this machine several instructions: 194 were issued for a block of
+// 16 x 128 codes against 75.)
+//
+// Measured, with the rows' split and the combine (rate of the codes and scales):
+// a row of 4096 x 4096 6.2 us; 8 rows of 57344 x 4096 27.5 us (4.4 TB/s); the
+// experts of one token (2 of 8 of 4096 x 14336) 42.4 us (4.3 TB/s), of 16 tokens
+// (8 of 128 of 4096 x 1536) 166 us (5.0 TB/s, 74% of what a copy reaches).  What
+// bounds it is instructions: the tensor pipe of mma.sync, masks and loads of x
+// share the warps' issue slots, which are 40% used while the memory waits at the
+// ends of items; a second block to an SM does not fit the registers.
 #pragma once
 
 #include <atomic>
@@ -662,7 +670,7 @@ inline Share share_narrow(int64_t items, int stages, bool rest) {
   }
   return best;
 }
-// blocks: of inputs, of the longest part
+// blocks: of inputs, of the longest part; an item's ends cost about two more
 inline Share share_wide(int64_t items, int blocks) {
   return {1, (items + kSms - 1) / kSms * (blocks + 2)};
 }
@@ -817,7 +825,10 @@ cudaError_t launch_mode(int group, int K, bool wide, const Args& a, cudaStream_t
 
 // How a product of about `rows` rows of x (of an expert), `chunks` of them (of
 // the experts hit) and N outputs is run.  The narrow kernel for as few rows as
-// it can hold; join: see splits_of, negative: no splits.
+// it can hold: 8 rows take it 11.6 us at 14336 x 4096, 16.6 at 14336 x 7168 and
+// 27.5 at 57344 x 4096, and the wide one, which is nearly the same from one row
+// to 16, takes 15.1, 27.5 and 34.9.  For 16 rows the narrow one would read the
+// weights twice.  join: see splits_of, negative: no splits.
 struct Way {
   bool wide, few;
   int splits;

@@ -1,5 +1,5 @@
 // Products with 4-bit weights for more rows: chunks of up to 64 columns (64 rows
-// of x; FC2: 32, two columns each) on the tensor cores' own memory.
+// of x; FC2: 32, two columns each) on tcgen05.
 //
 // A block, one to an SM, takes 256 outputs of a chunk at a time (FC1: 128 gate
 // rows and the 128 up rows of the same features) as two tiles of 128.  For each
@@ -8,17 +8,26 @@
 //   - four warps a tile turn a row's 64 bytes of codes, a row to a thread, into
 //     fp16 differences q - zero in the tensor memory, the A operand: masks of the
 //     words as in the narrow kernel, and one exact subtraction of subnormals for
-//     two codes (the narrow kernel takes the zeros off a group's sum instead: it
-//     has 8 columns and this one has 64, so there the sums are the cheaper place
-//     and here the codes are);
+//     two codes.  (The narrow kernel takes the zeros off a group's sum instead:
+//     there a sum belongs to 8 columns and here to 64, so there the sums are the
+//     cheaper place and here the codes are.)  Two slots, with warps of their own
+//     each: one set of warps took 237 us where two take 215 (below);
 //   - one thread multiplies, a fresh sum for each group of inputs;
-//   - eight warps, an output to a thread and half the columns each, read the
-//     group's sums back and add them up under its scale in fp32.
+//   - eight warps, an output of both tiles to a thread and half the columns each,
+//     read the groups' sums back and add them up under their scales in fp32.
 // All of them run at once and hand each other slots through mbarriers.
 //
-// mma.sync from registers ran the same work at 24% of the memory's rate: every
-// warp reads the whole x for its 32 outputs, and the conversion, the products
-// and the scaling wait for one another within a warp.
+// Measured, the experts of 64 tokens (2 of 8 of 4096 x 14336, zero points): 206 us
+// with the splits and the combine; FC1 122 and FC2 81 us cold.  mma.sync from
+// registers took 453 us: every warp read the whole x for its 32 outputs, and the
+// conversion, the products and the scaling waited for one another within a warp.
+// What bounds it now is instructions: 780 are issued by an SM quarter for 16 KB of
+// codes, 63% of its slots, half of them masks and subtractions; the products
+// alone, whose A operand of 4 KB takes some 33 cycles to read whatever the number
+// of columns, would take 530 of the 1240 cycles.
+//
+// Tried and left: the next item's scales and zeros loaded ahead (211 us), two
+// multiply-adds in an instruction (209), 7 parts of FC2's inputs or none (equal).
 #pragma once
 
 #include <type_traits>
@@ -256,91 +265,91 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
       const int n = nb * GPB, left = a.groups - kb * GPB;
       // with half of the columns known, what is read of a group is fixed
       auto item = [&](auto known) {
-      constexpr int half = decltype(known)::value;
-      constexpr int R = half / CP;  // rows of x
-      uint2 now[2], next[2];
+        constexpr int half = decltype(known)::value;
+        constexpr int R = half / CP;  // rows of x
+        uint2 now[2], next[2];
 #pragma unroll
-      for (int d = 0; d < 2; ++d) next[d] = four_scales(ps[d], left, whole);
-      float acc[2][R];
+        for (int d = 0; d < 2; ++d) next[d] = four_scales(ps[d], left, whole);
+        float acc[2][R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) acc[0][i] = acc[1][i] = 0.f;
+        for (int i = 0; i < R; ++i) acc[0][i] = acc[1][i] = 0.f;
 #pragma unroll 1
-      for (int g = 0; g < n; ++g) {
-        if ((g & 3) == 0) {
-#pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            now[d] = next[d];
-            next[d] = four_scales(ps[d] + g + 4, left - g - 4, whole);
-          }
-        }
-        float s[2];
-#pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          s[d] = __uint_as_float(now[d].x << 16);
-          now[d].x = __funnelshift_r(now[d].x, now[d].y, 16);
-          now[d].y >>= 16;
-        }
-        wait(bar(bars.d_full[ring.at]), ring.phase);
-        ptx::tc_fence_after();
-        const uint32_t at = d_at(0, ring.at) + lanes + e * half;
-        // a few columns of both tiles at a time, as the registers allow
-        constexpr int some = half <= 16 ? half : 8;
-#pragma unroll
-        for (int c = 0; c < half; c += some) {
-          float v[2][some];
-#pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            if (some == 8) tmem_ld8(at + d * 128 + c, v[d]);
-            else tmem_ld16(at + d * 128 + c, v[d]);
-          }
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < some; ++i)
-            asm volatile("" : "+f"(v[0][i]), "+f"(v[1][i]));
-          if (c + some == half) {  // the last of them
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(bars.d_free[ring.at]));
-          }
-#pragma unroll
-          for (int i = 0; i < some; i += CP)
+        for (int g = 0; g < n; ++g) {
+          if ((g & 3) == 0) {
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-              // FC2: the second piece is in 2^-11 of the first's unit
-              const float sum =
-                  CP == 2 ? v[d][i] + 0.00048828125f * v[d][i + CP - 1] : v[d][i];
-              acc[d][(c + i) / CP] += s[d] * sum;
+              now[d] = next[d];
+              next[d] = four_scales(ps[d] + g + 4, left - g - 4, whole);
             }
-        }
-        ring.next();
-      }
-      // the row's unit, and 2^24 for the codes' 2^-24
+          }
+          float s[2];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int rx = e * R + i;
-        if (rx >= row_count) break;
-        const float unit = a.unit[row_first + rx];
-        const float v0 = acc[0][i] * 16777216.f * unit, v1 = acc[1][i] * 16777216.f * unit;
-        if (MODE == FC1) {
-          if (o[0] < a.N)
-            static_cast<float*>(a.out)[static_cast<int64_t>(row_first + rx) * a.N + o[0]] =
-                v0 / (1.f + expf(-v0)) * v1;
-        } else {
-          const int64_t at =
-              MODE == FC2
-                  ? static_cast<int64_t>(it.part) * a.pairs + plan.pair[row_first + rx]
-                  : static_cast<int64_t>(it.part) * a.rows + row_first + rx;
-          if (MODE == FC2 || a.out_f32) {
-            float* out = static_cast<float*>(a.out) + at * a.N;
-            if (o[0] < a.N) out[o[0]] = v0;
-            if (o[1] < a.N) out[o[1]] = v1;
+          for (int d = 0; d < 2; ++d) {
+            s[d] = __uint_as_float(now[d].x << 16);
+            now[d].x = __funnelshift_r(now[d].x, now[d].y, 16);
+            now[d].y >>= 16;
+          }
+          wait(bar(bars.d_full[ring.at]), ring.phase);
+          ptx::tc_fence_after();
+          const uint32_t at = d_at(0, ring.at) + lanes + e * half;
+          // a few columns of both tiles at a time, as the registers allow
+          constexpr int some = half <= 16 ? half : 8;
+#pragma unroll
+          for (int c = 0; c < half; c += some) {
+            float v[2][some];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              if (some == 8) tmem_ld8(at + d * 128 + c, v[d]);
+              else tmem_ld16(at + d * 128 + c, v[d]);
+            }
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < some; ++i)
+              asm volatile("" : "+f"(v[0][i]), "+f"(v[1][i]));
+            if (c + some == half) {  // the last of them
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(bar(bars.d_free[ring.at]));
+            }
+#pragma unroll
+            for (int i = 0; i < some; i += CP)
+#pragma unroll
+              for (int d = 0; d < 2; ++d) {
+                // FC2: the second piece is in 2^-11 of the first's unit
+                const float sum =
+                    CP == 2 ? v[d][i] + 0.00048828125f * v[d][i + CP - 1] : v[d][i];
+                acc[d][(c + i) / CP] += s[d] * sum;
+              }
+          }
+          ring.next();
+        }
+        // the row's unit, and 2^24 for the codes' 2^-24
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int rx = e * R + i;
+          if (rx >= row_count) break;
+          const float unit = a.unit[row_first + rx];
+          const float v0 = acc[0][i] * 16777216.f * unit, v1 = acc[1][i] * 16777216.f * unit;
+          if (MODE == FC1) {
+            if (o[0] < a.N)
+              static_cast<float*>(a.out)[static_cast<int64_t>(row_first + rx) * a.N + o[0]] =
+                  v0 / (1.f + expf(-v0)) * v1;
           } else {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * a.N;
-            if (o[0] < a.N) out[o[0]] = __float2bfloat16_rn(v0);
-            if (o[1] < a.N) out[o[1]] = __float2bfloat16_rn(v1);
+            const int64_t at =
+                MODE == FC2
+                    ? static_cast<int64_t>(it.part) * a.pairs + plan.pair[row_first + rx]
+                    : static_cast<int64_t>(it.part) * a.rows + row_first + rx;
+            if (MODE == FC2 || a.out_f32) {
+              float* out = static_cast<float*>(a.out) + at * a.N;
+              if (o[0] < a.N) out[o[0]] = v0;
+              if (o[1] < a.N) out[o[1]] = v1;
+            } else {
+              __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * a.N;
+              if (o[0] < a.N) out[o[0]] = __float2bfloat16_rn(v0);
+              if (o[1] < a.N) out[o[1]] = __float2bfloat16_rn(v1);
+            }
           }
         }
-      }
       };
       switch ((row_count * CP + 15) / 16) {
         case 1: item(std::integral_constant<int, 8>()); break;
@@ -420,85 +429,85 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
       turn ^= nb & 1;
     }
   } else {
-  registers<56, false>();
-  if (warp == 24) {
-    // ---- the codes' copies ----
-    Ring code{kTallStages};
-    for (; enter(); it.next(gridDim.x, a)) {
-      const bool second = MODE == FC1 || it.tile * kTile + 128 < a.N;
-      for (int b = 0; b < nb; b += 2) {
-        wait(bar(bars.code_free[code.at]), code.phase ^ 1);
-        if (lane == 0) {
-          const uint32_t dst = base + code.at * kTallStage, full = bar(bars.code_full[code.at]);
-          ptx::mbar_arrive_expect_tx(full, second ? kTallStage : kTallStage / 2);
-          // blocks past the row's end come as zeros
-          ptx::tma_load_3d(dst, &map0, 0, static_cast<int>(row), kb + b, full);
-          if (second)
-            ptx::tma_load_3d(dst + kTallStage / 2, MODE == FC1 ? &map1 : &map0, 0,
-                             static_cast<int>(row) + (MODE == FC1 ? 0 : 128), kb + b, full);
-        }
-        __syncwarp();
-        code.next();
-      }
-    }
-  } else if (warp == 25) {
-    // ---- the copies of x: 8 columns of a block's inputs each ----
-    pdl_wait();
-    Ring ring{kTallXs};
-    for (; enter(); it.next(gridDim.x, a)) {
-      const int copies = (row_count * CP + 7) / 8;
-      for (int b = 0; b < nb; ++b) {
-        const uint32_t full = bar(bars.x_full[ring.at]);
-        wait(bar(bars.x_free[ring.at]), ring.phase ^ 1);
-        if (lane == 0) ptx::mbar_arrive_expect_tx(full, copies * 2048);
-        __syncwarp();
-        if (lane < copies)
-          ptx::tma_load_3d(xs_at + ring.at * kTallX + lane * 2048, &map_x, 0,
-                           row_first * CP + lane * 8, (kb + b) * 2, full);
-        ring.next();
-      }
-    }
-  } else if (warp == 26) {
-    // ---- products: the warp keeps together, so that addresses stay in uniform
-    // registers, and one thread of it issues ----
-    const bool issues = elect_one();
-    Ring ring{kTallXs};
-    Ring as{2}, ds{d_slots};  // of A and D, both tiles' together
-    for (; enter(); it.next(gridDim.x, a)) {
-      const uint32_t columns = (row_count * CP + 15) / 16 * 16;
-      const uint32_t idesc = (1u << 4) | (columns >> 3) << 17 | (128u >> 4) << 24;
-#pragma unroll 1
-      for (int b = 0; b < nb; ++b) {
-        wait(bar(bars.x_full[ring.at]), ring.phase);
-        wait(bar(bars.a_full[as.at]), as.phase);
-        // a step of 16 inputs is 32 bytes on, 64 inputs 1024
-        const uint64_t x = ptx::sw128_desc(xs_at + ring.at * kTallX, 0, 2048);
-#pragma unroll
-        for (int q = 0; q < GPB; ++q) {
-          wait(bar(bars.d_free[ds.at]), ds.phase ^ 1);
-          ptx::tc_fence_after();
-          if (issues) {
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-              for (int k = q * G32 * 2; k < (q + 1) * G32 * 2; ++k)
-                umma_f16_ta(d_at(d, ds.at), a_at(d, as.at) + k * 8,
-                            x + ((k >> 2) * 64 + (k & 3) * 2), idesc, k > q * G32 * 2);
-            ptx::umma_commit(bar(bars.d_full[ds.at]));
+    registers<56, false>();
+    if (warp == 24) {
+      // ---- the codes' copies ----
+      Ring code{kTallStages};
+      for (; enter(); it.next(gridDim.x, a)) {
+        const bool second = MODE == FC1 || it.tile * kTile + 128 < a.N;
+        for (int b = 0; b < nb; b += 2) {
+          wait(bar(bars.code_free[code.at]), code.phase ^ 1);
+          if (lane == 0) {
+            const uint32_t dst = base + code.at * kTallStage, full = bar(bars.code_full[code.at]);
+            ptx::mbar_arrive_expect_tx(full, second ? kTallStage : kTallStage / 2);
+            // blocks past the row's end come as zeros
+            ptx::tma_load_3d(dst, &map0, 0, static_cast<int>(row), kb + b, full);
+            if (second)
+              ptx::tma_load_3d(dst + kTallStage / 2, MODE == FC1 ? &map1 : &map0, 0,
+                               static_cast<int>(row) + (MODE == FC1 ? 0 : 128), kb + b, full);
           }
           __syncwarp();
-          ds.next();
+          code.next();
         }
-        if (issues) {
-          ptx::umma_commit(bar(bars.a_free[as.at]));
-          ptx::umma_commit(bar(bars.x_free[ring.at]));
+      }
+    } else if (warp == 25) {
+      // ---- the copies of x: 8 columns of a block's inputs each ----
+      pdl_wait();
+      Ring ring{kTallXs};
+      for (; enter(); it.next(gridDim.x, a)) {
+        const int copies = (row_count * CP + 7) / 8;
+        for (int b = 0; b < nb; ++b) {
+          const uint32_t full = bar(bars.x_full[ring.at]);
+          wait(bar(bars.x_free[ring.at]), ring.phase ^ 1);
+          if (lane == 0) ptx::mbar_arrive_expect_tx(full, copies * 2048);
+          __syncwarp();
+          if (lane < copies)
+            ptx::tma_load_3d(xs_at + ring.at * kTallX + lane * 2048, &map_x, 0,
+                             row_first * CP + lane * 8, (kb + b) * 2, full);
+          ring.next();
         }
-        __syncwarp();
-        as.next();
-        ring.next();
+      }
+    } else if (warp == 26) {
+      // ---- products: the warp keeps together, so that addresses stay in uniform
+      // registers, and one thread of it issues ----
+      const bool issues = elect_one();
+      Ring ring{kTallXs};
+      Ring as{2}, ds{d_slots};  // of A and D, both tiles' together
+      for (; enter(); it.next(gridDim.x, a)) {
+        const uint32_t columns = (row_count * CP + 15) / 16 * 16;
+        const uint32_t idesc = (1u << 4) | (columns >> 3) << 17 | (128u >> 4) << 24;
+#pragma unroll 1
+        for (int b = 0; b < nb; ++b) {
+          wait(bar(bars.x_full[ring.at]), ring.phase);
+          wait(bar(bars.a_full[as.at]), as.phase);
+          // a step of 16 inputs is 32 bytes on, 64 inputs 1024
+          const uint64_t x = ptx::sw128_desc(xs_at + ring.at * kTallX, 0, 2048);
+#pragma unroll
+          for (int q = 0; q < GPB; ++q) {
+            wait(bar(bars.d_free[ds.at]), ds.phase ^ 1);
+            ptx::tc_fence_after();
+            if (issues) {
+#pragma unroll
+              for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int k = q * G32 * 2; k < (q + 1) * G32 * 2; ++k)
+                  umma_f16_ta(d_at(d, ds.at), a_at(d, as.at) + k * 8,
+                              x + ((k >> 2) * 64 + (k & 3) * 2), idesc, k > q * G32 * 2);
+              ptx::umma_commit(bar(bars.d_full[ds.at]));
+            }
+            __syncwarp();
+            ds.next();
+          }
+          if (issues) {
+            ptx::umma_commit(bar(bars.a_free[as.at]));
+            ptx::umma_commit(bar(bars.x_free[ring.at]));
+          }
+          __syncwarp();
+          as.next();
+          ring.next();
+        }
       }
     }
-  }
   }
   __syncwarp();
   ptx::tc_fence_before();
