@@ -372,12 +372,23 @@ struct GroupSum {
   }
 };
 
-// A parameter's values at phase + column of shared memory, zeros around them;
+// Where the value at phase + column of a parameter lies in shared memory.  A
+// thread of bf16 rows reads eight values: the first halves of all threads' lie
+// before the second halves, so that neighbours read neighbouring 16 bytes
+// (8192 x 4096 bf16 33.2 -> 27.5 us: with the halves together, half of the banks
+// waited).
+template <int V>
+__device__ __forceinline__ int place(int at, int padded) {
+  if (V == 4) return at;
+  return (at & 4 ? padded / 2 : 0) + (at >> 3) * 4 + (at & 3);
+}
+
+// A parameter's values at phase + column, zeros around them;
 // without the parameter `none`.  A thread brings the columns that it will read,
 // all its reads in flight at once; one group does it for the block.
 template <typename T, int VPT, bool ALIGNED>
-__device__ __forceinline__ void stage_param(float* dst, const void* p, int is_bf16, float none,
-                                            const Group<T, ALIGNED>& g, int H) {
+__device__ __forceinline__ void stage_param(float* dst, int padded, const void* p, int is_bf16,
+                                            float none, const Group<T, ALIGNED>& g, int H) {
   constexpr int V = Lanes<T>::V;
   if (g.id != 0) return;
   float v[VPT][V];
@@ -406,15 +417,16 @@ __device__ __forceinline__ void stage_param(float* dst, const void* p, int is_bf
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int e = 0; e < V; e += 4)
-      *reinterpret_cast<float4*>(dst + g.col(i) + g.phase + e) =
+      *reinterpret_cast<float4*>(dst + place<V>(g.col(i) + g.phase + e, padded)) =
           make_float4(v[i][e], v[i][e + 1], v[i][e + 2], v[i][e + 3]);
 }
 
 template <int V>
-__device__ __forceinline__ void read_param(const float* src, int at, float2 (&v)[V / 2]) {
+__device__ __forceinline__ void read_param(const float* src, int at, int padded,
+                                           float2 (&v)[V / 2]) {
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
-    const float4 q = *reinterpret_cast<const float4*>(src + at + 4 * i);
+    const float4 q = *reinterpret_cast<const float4*>(src + place<V>(at + 4 * i, padded));
     v[2 * i] = make_float2(q.x, q.y);
     v[2 * i + 1] = make_float2(q.z, q.w);
   }
@@ -445,8 +457,8 @@ __global__ void __launch_bounds__(1024)
     fetch(qx, x, g.row);
     if (res) fetch(qr, res, g.row);
   }
-  stage_param<T, VPT>(params, weight, a.param_bf16, 1.f, g, H);
-  stage_param<T, VPT>(params + padded, bias, a.param_bf16, 0.f, g, H);
+  stage_param<T, VPT>(params, padded, weight, a.param_bf16, 1.f, g, H);
+  stage_param<T, VPT>(params + padded, padded, bias, a.param_bf16, 0.f, g, H);
   __syncthreads();
 
   for (int64_t r = g.row; r < a.rows; r += g.step) {
@@ -515,8 +527,8 @@ __global__ void __launch_bounds__(1024)
       const int c = g.col(i);
       if (c >= H) continue;
       float2 w[P], b[P];
-      read_param<V>(params, c + g.phase, w);
-      read_param<V>(params + padded, c + g.phase, b);
+      read_param<V>(params, c + g.phase, padded, w);
+      read_param<V>(params + padded, c + g.phase, padded, b);
 #pragma unroll
       for (int e = 0; e < P; ++e) b[e] = fma2(mul2(v[i][e], both(rs)), w[e], b[e]);
       store_vec<T, ALIGNED>(y + r * H, c, H, b);
@@ -602,7 +614,7 @@ __global__ void __launch_bounds__(STAGED ? 512 : 640)
 #pragma unroll
     for (int n = 0; n < kSlots - 1; ++n) fetch(g.row + n * g.step, n);
   }
-  stage_param<T, VPT>(params, weight, a.param_bf16, 1.f, g, H);
+  stage_param<T, VPT>(params, padded, weight, a.param_bf16, 1.f, g, H);
   if (!STAGED)
     for (int c = threadIdx.x; c < 2 * padded; c += blockDim.x) sums[c] = 0.f;
 #pragma unroll
@@ -635,7 +647,7 @@ __global__ void __launch_bounds__(STAGED ? 512 : 640)
       float2 vx[P], vd[P], w[P];
       read(x, r, n, 0, i, vx);
       read(dy, r, n, 1, i, vd);
-      read_param<V>(params, c + g.phase, w);
+      read_param<V>(params, c + g.phase, padded, w);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         const float2 gw = mul2(vd[e], w[e]);
@@ -656,10 +668,10 @@ __global__ void __launch_bounds__(STAGED ? 512 : 640)
       if (dz) read(dz, r, n, 2, i, o[i]);
       read(x, r, n, 0, i, vx);
       read(dy, r, n, 1, i, vd);
-      read_param<V>(params, c + g.phase, w);
+      read_param<V>(params, c + g.phase, padded, w);
       if (!STAGED) {
-        read_param<V>(sums, c + g.phase, tw);
-        read_param<V>(sums + padded, c + g.phase, tb);
+        read_param<V>(sums, c + g.phase, padded, tw);
+        read_param<V>(sums + padded, c + g.phase, padded, tb);
       }
 #pragma unroll
       for (int e = 0; e < P; ++e) {
@@ -677,9 +689,10 @@ __global__ void __launch_bounds__(STAGED ? 512 : 640)
       if (!STAGED) {
 #pragma unroll
         for (int e = 0; e < P; e += 2) {
-          *reinterpret_cast<float4*>(sums + c + g.phase + 2 * e) =
+          const int at = place<V>(c + g.phase + 2 * e, padded);
+          *reinterpret_cast<float4*>(sums + at) =
               make_float4(tw[e].x, tw[e].y, tw[e + 1].x, tw[e + 1].y);
-          *reinterpret_cast<float4*>(sums + padded + c + g.phase + 2 * e) =
+          *reinterpret_cast<float4*>(sums + padded + at) =
               make_float4(tb[e].x, tb[e].y, tb[e + 1].x, tb[e + 1].y);
         }
       }
@@ -716,8 +729,8 @@ __global__ void __launch_bounds__(STAGED ? 512 : 640)
           if (at >= padded) continue;
 #pragma unroll
           for (int e = 0; e < P; ++e) {
-            float2* pw = reinterpret_cast<float2*>(sums + at) + e;
-            float2* pb = reinterpret_cast<float2*>(sums + padded + at) + e;
+            float2* pw = reinterpret_cast<float2*>(sums + place<V>(at + 2 * e, padded));
+            float2* pb = pw + padded / 2;
             *pw = k == 0 ? sw[i][e] : add2(*pw, sw[i][e]);
             *pb = k == 0 ? sb[i][e] : add2(*pb, sb[i][e]);
           }
@@ -728,8 +741,9 @@ __global__ void __launch_bounds__(STAGED ? 512 : 640)
   }
   float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * H;
   for (int c = threadIdx.x; c < H; c += blockDim.x) {
-    out[c] = sums[c + g.phase];
-    out[H + c] = sums[padded + c + g.phase];
+    const int at = place<V>(c + g.phase, padded);
+    out[c] = sums[at];
+    out[H + c] = sums[padded + at];
   }
 }
 
