@@ -216,8 +216,8 @@ __device__ __forceinline__ uint4 pack(const float2 (&v)[4], const __nv_bfloat16*
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The elements of an edge vector that lie in the row, one by one; loops that
-// stay loops: few threads take them.
+// The elements of an edge vector that lie in the row, one by one.  The reads
+// stay a loop: only the tensor's last vector takes it.
 __device__ __forceinline__ uint32_t bits_of(const float* p) { return __float_as_uint(*p); }
 __device__ __forceinline__ uint32_t bits_of(const __nv_bfloat16* p) {
   return __bfloat16_as_ushort(*p);
@@ -245,7 +245,7 @@ __device__ __forceinline__ uint4 load_edge(const T* row, int col, int H) {
 template <typename T>
 __device__ __forceinline__ void store_edge(T* row, int col, int H, uint4 q) {
   constexpr int V = Lanes<T>::V, B = 32 * 4 / V;
-#pragma unroll 1
+#pragma unroll
   for (int e = 0; e < V; ++e) {
     const int w = e * B / 32;
     const uint32_t b = w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w;
@@ -505,6 +505,10 @@ __global__ void __launch_bounds__(1024)
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < P; ++e) v[i][e] = add2(v[i][e], both(-m));
+      if (!ALIGNED) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) mask_edge(v[i], g.col(i), H);
+      }
     }
     float2 sq = both(0.f);
 #pragma unroll
@@ -512,14 +516,7 @@ __global__ void __launch_bounds__(1024)
       const int c = g.col(i);
       if (c >= H) continue;
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        float2 d = v[i][e];
-        if (!ALIGNED) {
-          if (c + 2 * e < 0 || c + 2 * e >= H) d.x = 0.f;
-          if (c + 2 * e + 1 < 0 || c + 2 * e + 1 >= H) d.y = 0.f;
-        }
-        sq = fma2(d, d, sq);
-      }
+      for (int e = 0; e < P; ++e) sq = fma2(v[i][e], v[i][e], sq);
     }
     const float rs = rsqrtf(sum(sq.x + sq.y) * inv_h + a.eps);
 #pragma unroll
