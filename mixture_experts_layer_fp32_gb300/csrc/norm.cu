@@ -157,6 +157,16 @@ __global__ void __launch_bounds__(kRowThreads)
 // the row number modulo the vector length; a block takes the rows of one
 // residue, so its phase is fixed, its copy of the weights in shared memory is
 // laid out for it, and in the backward pass a thread keeps the same columns.
+//
+// Measured, bf16 with fp32 parameters, bytes once in and once out: forward 8192 x
+// 4096 27.5 us (4.9 TB/s, of 6.8 that a copy reaches), with dropout and residual
+// 59.6 us (4.5 TB/s); backward 16384 x 4096 90 us (4.5 TB/s), with dropout 138 us
+// (4.9 TB/s); fp32 forward 4096 x 4096 25.7 us (5.2), backward 8192 x 4096 70 us
+// (5.7).  Beside the memory, reads of the parameters from shared memory and the
+// instructions for 8 values in 16 bytes bound bf16; the generator's rounds, at
+// least 80 cycles of an SM quarter for 128 elements, bound the dropout.  Odd
+// widths (8192 x 4099: 42 us, backward 86) pay for edge vectors and an odd number
+// of warps.
 
 template <typename T>
 struct Lanes {
@@ -432,6 +442,24 @@ __device__ __forceinline__ void read_param(const float* src, int at, int padded,
   }
 }
 
+// A row brought into L2 ahead of its reads, by one thread; the bytes around it
+// that belong to its first and last 16 come too.  For the kernels that hold no
+// row ahead (forward 1024 x 24568 bf16 35.2 -> 30.9 us, backward 4096 x 16384
+// 160 -> 128 us); behind rows that are held it gains nothing.
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const T* p, int64_t row, int64_t rows, int H) {
+  if (row >= rows) return;
+  constexpr int64_t size = sizeof(T), ones = 15;
+  const int64_t from = row * H * size & ~ones, most = rows * H * size & ~ones;
+  int64_t to = ((row + 1) * H * size + ones) & ~ones;
+  to = to < most ? to : most;
+  if (to > from)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                     reinterpret_cast<const char*>(p) + from),
+                 "r"(static_cast<uint32_t>(to - from))
+                 : "memory");
+}
+
 template <typename T, int VPT, bool ALIGNED, bool DROP>
 __global__ void __launch_bounds__(1024)
     norm_rows_kernel(NormArgs a, int group_warps, int padded, const T* x, const T* res,
@@ -466,6 +494,10 @@ __global__ void __launch_bounds__(1024)
     if (!AHEAD) {
       fetch(qx, x, r);
       if (res) fetch(qr, res, r);
+      if (g.t == 0) {
+        prefetch_row(x, r + g.step, a.rows, H);
+        if (res) prefetch_row(res, r + g.step, a.rows, H);
+      }
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) unpack(qx[i], v[i], x);
@@ -635,6 +667,10 @@ __global__ void __launch_bounds__(STAGED ? 512 : 640)
     if (STAGED) {
       fetch(r + (kSlots - 1) * g.step, n == 0 ? kSlots - 1 : n - 1);
       copies_wait<kSlots - 1>();
+    } else if (g.t == 0) {
+      prefetch_row(x, r + g.step, a.rows, H);
+      prefetch_row(dy, r + g.step, a.rows, H);
+      if (dz) prefetch_row(dz, r + g.step, a.rows, H);
     }
     float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
@@ -772,7 +808,8 @@ __global__ void __launch_bounds__(kGradWarps * 32)
 
 // Flat vectors of 16 bytes, two to a thread at a time so that their reads and
 // their generator rounds overlap; the last elements of a length that is no
-// multiple of the vector's go one by one.
+// multiple of the vector's go one by one.  8192 x 4096 bf16 with a residual:
+// 36 us (5.6 TB/s); half of it is the generator's, under the memory's time.
 template <typename T, bool DROP>
 __global__ void __launch_bounds__(256)
     dropout_add_kernel(int64_t n, Dropout d, const uint64_t* rng, const T* x, const T* res, T* y) {
@@ -864,13 +901,19 @@ int row_vectors(const moe_norm_config& c, int V) {
   return c.hidden % V == 0 ? c.hidden / V : (c.hidden + 2 * V - 2) / V;
 }
 
+// Two vectors to a thread: with one, more threads wait at each row's sums
+// (8192 x 4096 bf16 27.5 us, one 36.1; 100 x 8192 4.0, one 4.6).  One for a few
+// short rows, where all threads are few (100 x 2048 bf16 2.98 us, two 3.16) and
+// for rows that one warp holds.  More where 1024 threads with two do not hold a
+// row, without a row ahead in registers (1024 x 24568 bf16 30.9 us; the wide
+// kernel 104).
 Shape forward_shape(const moe_norm_config& c) {
   Shape s;
   const int V = c.dtype == MOE_F32 ? 4 : 8;
   if (c.hidden > 32768) return s;
   const int vectors = row_vectors(c, V);
   s.aligned = c.hidden % V == 0;
-  if (vectors <= 32 || (c.rows <= kSms && vectors <= 1024)) s.vpt = 1;
+  if (vectors <= 32 || (c.rows <= kSms && vectors <= 256)) s.vpt = 1;
   else if (vectors <= 2048) s.vpt = 2;
   else if (V == 8 && vectors <= 3072) s.vpt = 3;
   else if (V == 4 && vectors <= 4096) s.vpt = 4;
@@ -888,6 +931,10 @@ size_t backward_smem(const Shape& s) {
   return rows > 2 * padded ? rows : 2 * padded;
 }
 
+// Staged up to what 16 warps hold with two vectors to a thread (16384 x 4096 bf16
+// 90 us, 109 with the sums in shared memory and rows read as they come; 8192 x
+// 8192 90 and 120; the wide kernel takes 355 and more).  Past that the sums need
+// the shared memory (4096 x 16384 bf16 128 us; 735 in the wide kernel).
 Shape backward_shape(const moe_norm_config& c) {
   Shape s;
   const int V = c.dtype == MOE_F32 ? 4 : 8;
@@ -917,9 +964,10 @@ auto with_bool(bool b, F&& f) {
   return b ? f(std::true_type{}) : f(std::false_type{});
 }
 
+// 48 KB need no leave, but the kernels' own variables are among them.
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
+  if (bytes <= 47 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(bytes));
 }

@@ -333,3 +333,14 @@ def test_on_another_stream_and_in_a_graph():
     for want in (first, second):
         graph.replay()
         assert all(torch.equal(a, c) for a, c in zip(want, values()))
+
+
+@pytest.mark.parametrize("dtype,hidden", [("bf16", 6144), ("f32", 6144), ("bf16", 6100),
+                                          ("f32", 3000), ("bf16", 12288), ("f32", 12288)])
+def test_shared_memory_around_48_kb(dtype, hidden):
+    """Widths whose parameters take just the shared memory that a kernel has without asking."""
+    rows = _rows(hidden)
+    _check_forward(rows, hidden, dtype, "f32", False, True, 0.1, seed=hidden)
+    _check_forward(rows, hidden, dtype, dtype, True, False, 0.0, seed=hidden)
+    _check_backward(rows, hidden, dtype, "f32", False, True, 0.1, seed=hidden)
+    _check_backward(rows, hidden, dtype, dtype, True, False, 0.0, seed=hidden)
