@@ -26,7 +26,9 @@
 // (8 of 128 of 4096 x 1536) 166 us (5.0 TB/s, 74% of what a copy reaches).  What
 // bounds it is instructions: the tensor pipe of mma.sync, masks and loads of x
 // share the warps' issue slots, which are 40% used while the memory waits at the
-// ends of items; a second block to an SM does not fit the registers.
+// ends of items; a second block to an SM does not fit the registers.  Two chains
+// of products in a warp, or a warp's stages next to its neighbours' instead of in
+// runs, made no difference.
 #pragma once
 
 #include <atomic>
