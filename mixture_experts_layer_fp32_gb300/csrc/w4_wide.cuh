@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
   constexpr int SB = 4;                           // blocks of a unit of a part
   extern __shared__ uint8_t smem_raw[];
   __shared__ TallBars bars;
+  __shared__ float units[8][32];
   __shared__ uint32_t tmem_at;
   const uint32_t base = (ptx::smem_u32(smem_raw) + 1023) & ~1023u;
   const uint32_t xs_at = base + kTallStages * kTallStage;
@@ -270,6 +271,10 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
         uint2 now[2], next[2];
 #pragma unroll
         for (int d = 0; d < 2; ++d) next[d] = four_scales(ps[d], left, whole);
+        // the rows' units, read at the end
+        if (lane < R && e * R + lane < row_count)
+          copy_async4(ptx::smem_u32(&units[warp][lane]), a.unit + row_first + e * R + lane);
+        copies_commit();
         float acc[2][R];
 #pragma unroll
         for (int i = 0; i < R; ++i) acc[0][i] = acc[1][i] = 0.f;
@@ -323,31 +328,39 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
           }
           ring.next();
         }
-        // the row's unit, and 2^24 for the codes' 2^-24
+        // The row's unit, and 2^24 for the codes' 2^-24.  Rows past the last one are
+        // worked out too and not stored: no branch stands between one and the next.
+        copies_wait<0>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float unit = units[warp][i] * 16777216.f;
+          acc[0][i] *= unit;
+          acc[1][i] *= unit;
+          if (MODE == FC1) acc[0][i] = acc[0][i] / (1.f + expf(-acc[0][i])) * acc[1][i];
+        }
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const int rx = e * R + i;
           if (rx >= row_count) break;
-          const float unit = a.unit[row_first + rx];
-          const float v0 = acc[0][i] * 16777216.f * unit, v1 = acc[1][i] * 16777216.f * unit;
           if (MODE == FC1) {
             if (o[0] < a.N)
               static_cast<float*>(a.out)[static_cast<int64_t>(row_first + rx) * a.N + o[0]] =
-                  v0 / (1.f + expf(-v0)) * v1;
+                  acc[0][i];
+            continue;
+          }
+          const int64_t at =
+              MODE == FC2 ? static_cast<int64_t>(it.part) * a.pairs + plan.pair[row_first + rx]
+                          : static_cast<int64_t>(it.part) * a.rows + row_first + rx;
+          if (MODE == FC2 || a.out_f32) {
+            float* out = static_cast<float*>(a.out) + at * a.N;
+            if (o[0] < a.N) out[o[0]] = acc[0][i];
+            if (o[1] < a.N) out[o[1]] = acc[1][i];
           } else {
-            const int64_t at =
-                MODE == FC2
-                    ? static_cast<int64_t>(it.part) * a.pairs + plan.pair[row_first + rx]
-                    : static_cast<int64_t>(it.part) * a.rows + row_first + rx;
-            if (MODE == FC2 || a.out_f32) {
-              float* out = static_cast<float*>(a.out) + at * a.N;
-              if (o[0] < a.N) out[o[0]] = v0;
-              if (o[1] < a.N) out[o[1]] = v1;
-            } else {
-              __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * a.N;
-              if (o[0] < a.N) out[o[0]] = __float2bfloat16_rn(v0);
-              if (o[1] < a.N) out[o[1]] = __float2bfloat16_rn(v1);
-            }
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * a.N;
+            if (o[0] < a.N) out[o[0]] = __float2bfloat16_rn(acc[0][i]);
+            if (o[1] < a.N) out[o[1]] = __float2bfloat16_rn(acc[1][i]);
           }
         }
       };
