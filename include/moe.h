@@ -698,7 +698,7 @@ moe_status moe_pack_w4(int32_t experts, int32_t N, int32_t K, const uint8_t* val
                        uint8_t* codes, moe_stream_t stream);
 
 /* y [rows, N] (y_dtype) = x [rows, K] bf16 . W^T.  Made for few rows (decoding):
- * the weight is read once for every 32 rows. */
+ * the weight is read once for every 64 rows. */
 moe_status moe_workspace_size_linear_w4(int64_t rows, int32_t N, int32_t K, size_t* bytes);
 moe_status moe_linear_w4(int64_t rows, int32_t N, int32_t K, int32_t group, const void* x,
                          const moe_w4* W, void* y, int32_t y_dtype, void* ws, size_t ws_bytes,
@@ -713,8 +713,8 @@ moe_status moe_linear_w4(int64_t rows, int32_t N, int32_t K, int32_t group, cons
  * fp16 numbers each (together within 2^-22 of the fp32 value).  bf16 layers only
  * (MOE_ERR_UNSUPPORTED).  An expert id out of range is reported in ws
  * (moe_check) and its pair left out.  Made for decoding: an expert's weights are
- * read once for every 1024 / k tokens at most; many tokens belong to
- * moe_forward or moe_forward_e4m3.
+ * read once for every 64 of its rows (W2: 32); many tokens belong to moe_forward
+ * or moe_forward_e4m3.
  */
 moe_status moe_workspace_size_experts_w4(const moe_config* cfg, size_t* bytes);
 moe_status moe_experts_w4(const moe_config* cfg, int32_t group, const void* x,
