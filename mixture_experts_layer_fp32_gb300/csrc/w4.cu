@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32)
                                 ((static_cast<int64_t>(row) * CP + p) * blocks + blk) * 128 +
                                 lane * 4) = *reinterpret_cast<uint2*>(out);
     }
+    if (sums == nullptr) return;  // the wide kernel takes the zeros off the codes
     constexpr int kLanes = G32 * 8;  // of a group
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -125,12 +126,12 @@ size_t split_bytes(size_t rows, int K, int pieces) {
   return align256((blocks * pieces + 1) * 256) + align256(rows * 4) +
          align256((blocks + 1) * 4 * 4);
 }
-Split split_at(char* at, size_t rows, int K, int pieces) {
+Split split_at(char* at, size_t rows, int K, int pieces, bool wide) {
   const size_t blocks = rows * w4_blocks(K);
   Split p;
   p.x = reinterpret_cast<__half*>(at);
   p.unit = reinterpret_cast<float*>(at + align256((blocks * pieces + 1) * 256));
-  p.sums = p.unit + align256(rows * 4) / 4;
+  p.sums = wide ? nullptr : p.unit + align256(rows * 4) / 4;
   return p;
 }
 
@@ -287,7 +288,7 @@ size_t w4_linear_scratch(int64_t rows, int N, int K) {
 cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* x, const W4& W,
                              void* y, int y_dtype, void* scratch, int* err, cudaStream_t s) {
   const LinearShape L = linear_shape(rows, N, K);
-  const Split xs = split_at(static_cast<char*>(scratch), L.rows, K, 1);
+  const Split xs = split_at(static_cast<char*>(scratch), L.rows, K, 1, L.way.wide);
   float* part =
       reinterpret_cast<float*>(static_cast<char*>(scratch) + split_bytes(L.rows, K, 1));
   const int out_f32 = y_dtype == MOE_F32;
@@ -316,8 +317,8 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
     if (L.way.splits > 1) {
       const int64_t n = static_cast<int64_t>(m) * N;
       st = launch_dependent(w4_join_kernel, dim3(static_cast<unsigned>((n + 255) / 256)),
-                            dim3(256), 0, s, n, L.way.splits, static_cast<const float*>(part), out_f32,
-                            out);
+                            dim3(256), 0, s, n, L.way.splits,
+                            static_cast<const float*>(part), out_f32, out);
       if (st != cudaSuccess) return st;
     }
   }
@@ -326,7 +327,8 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
 
 size_t w4_experts_scratch(int T, int h, int E, int k, int f) {
   const ExpertsShape S = experts_shape(T, h, E, k, f);
-  return split_bytes(S.way1.wide ? S.pairs : S.tokens, h, 1) + align256(static_cast<size_t>(S.pairs) * f * 4) +
+  return split_bytes(S.way1.wide ? S.pairs : S.tokens, h, 1) +
+         align256(static_cast<size_t>(S.pairs) * f * 4) +
          split_bytes(S.pairs, f, 2) + static_cast<size_t>(S.way2.splits) * S.pairs * h * 4;
 }
 
@@ -337,11 +339,11 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
   const ExpertsShape S = experts_shape(T, h, E, k, f);
   char* at = static_cast<char*>(scratch);
   const int x_rows = S.way1.wide ? S.pairs : S.tokens;
-  const Split xs = split_at(at, x_rows, h, 1);
+  const Split xs = split_at(at, x_rows, h, 1, S.way1.wide);
   at += split_bytes(x_rows, h, 1);
   float* hidden = reinterpret_cast<float*>(at);
   at += align256(static_cast<size_t>(S.pairs) * f * 4);
-  const Split hs = split_at(at, S.pairs, f, 2);
+  const Split hs = split_at(at, S.pairs, f, 2, S.way2.wide);
   at += split_bytes(S.pairs, f, 2);
   float* part = reinterpret_cast<float*>(at);
   for (int t = 0; t < T; t += S.tokens) {
@@ -389,8 +391,8 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     if (st != cudaSuccess) return st;
     const int64_t vecs = static_cast<int64_t>(n) * (h / 4);
     st = launch_dependent(w4_combine_kernel, dim3(static_cast<unsigned>((vecs + 255) / 256)),
-                          dim3(256), 0, s, n, h, k, E, S.way2.splits, static_cast<const float*>(part),
-                          a.idx, topk_prob + first, a.keep,
+                          dim3(256), 0, s, n, h, k, E, S.way2.splits,
+                          static_cast<const float*>(part), a.idx, topk_prob + first, a.keep,
                           static_cast<__nv_bfloat16*>(y) + static_cast<int64_t>(t) * h);
     if (st != cudaSuccess) return st;
   }

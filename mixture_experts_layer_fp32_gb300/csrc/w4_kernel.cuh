@@ -778,7 +778,9 @@ cudaError_t launch_narrow(Args a, cudaStream_t s) {
 }
 
 // rows of a chunk of the wide kernel; few: 32 columns will do
-constexpr int wide_rows(int mode, bool few) { return kTallColumns / (few ? 2 : 1) / pieces_of(mode); }
+constexpr int wide_rows(int mode, bool few) {
+  return kTallColumns / (few ? 2 : 1) / pieces_of(mode);
+}
 
 template <int MODE, int G32>
 cudaError_t launch_wide(Args a, cudaStream_t s) {
