@@ -934,7 +934,9 @@ size_t backward_smem(const Shape& s) {
 // Staged up to what 16 warps hold with two vectors to a thread (16384 x 4096 bf16
 // 90 us, 109 with the sums in shared memory and rows read as they come; 8192 x
 // 8192 90 and 120; the wide kernel takes 355 and more).  Past that the sums need
-// the shared memory (4096 x 16384 bf16 128 us; 735 in the wide kernel).
+// the shared memory (4096 x 16384 bf16 124 us; 735 in the wide kernel), and as
+// many warps as hold the row with two to four vectors to a thread hide the reads
+// best (7455 x 9001 bf16, two vectors 161 us, four 273).
 Shape backward_shape(const moe_norm_config& c) {
   Shape s;
   const int V = c.dtype == MOE_F32 ? 4 : 8;
@@ -943,8 +945,11 @@ Shape backward_shape(const moe_norm_config& c) {
   s.aligned = c.hidden % V == 0;
   s.vpt = vectors <= 32 ? 1 : 2;
   s.staged = vectors <= s.vpt * 32 * 16;
-  if (!s.staged) s.vpt = V == 4 && vectors > 4 * 32 * 20 ? 8 : 4;
-  if (vectors > s.vpt * 32 * 20) {
+  if (!s.staged) {
+    s.vpt = (vectors + 32 * 20 - 1) / (32 * 20);  // 2, 3, 4 or 8
+    if (s.vpt > 4 && V == 4) s.vpt = 8;
+  }
+  if (s.vpt > 8 || (s.vpt > 4 && V == 8) || vectors > s.vpt * 32 * 20) {
     s.vpt = 0;
     return s;
   }
@@ -1036,11 +1041,15 @@ cudaError_t norm_backward_typed(const moe_norm_config& c, const void* dy, const 
       });
     });
   };
+  if (p.vpt != 0 && p.staged) {
+    if (p.vpt == 1) return launch(std::integral_constant<int, 1>{}, std::true_type{});
+    return launch(std::integral_constant<int, 2>{}, std::true_type{});
+  }
+  if (p.vpt == 2) return launch(std::integral_constant<int, 2>{}, std::false_type{});
+  if (p.vpt == 3) return launch(std::integral_constant<int, 3>{}, std::false_type{});
   if (p.vpt == 4) return launch(std::integral_constant<int, 4>{}, std::false_type{});
   if constexpr (sizeof(T) == 4)
     if (p.vpt == 8) return launch(std::integral_constant<int, 8>{}, std::false_type{});
-  if (p.vpt == 1) return launch(std::integral_constant<int, 1>{}, std::true_type{});
-  if (p.vpt == 2) return launch(std::integral_constant<int, 2>{}, std::true_type{});
   norm_backward_wide_kernel<T><<<norm_backward_ctas(c), kRowThreads, 0, s>>>(
       a, dyt, zt, weight, mean, rstd, dzt, dxt, dbt, part);
   return cudaGetLastError();
