@@ -328,15 +328,16 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
           }
           ring.next();
         }
-        // The row's unit, and 2^24 for the codes' 2^-24.  Rows past the last one are
-        // worked out too and not stored: no branch stands between one and the next.
+        // 2^24 for the codes' 2^-24, then the row's unit: that is up to 2^113, and the
+        // two together pass the range of fp32.  Rows past the last one are worked out
+        // too and not stored: no branch stands between one and the next.
         copies_wait<0>();
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          const float unit = units[warp][i] * 16777216.f;
-          acc[0][i] *= unit;
-          acc[1][i] *= unit;
+          const float unit = units[warp][i];
+          acc[0][i] = acc[0][i] * 16777216.f * unit;
+          acc[1][i] = acc[1][i] * 16777216.f * unit;
           if (MODE == FC1) acc[0][i] = acc[0][i] / (1.f + expf(-acc[0][i])) * acc[1][i];
         }
         __syncwarp();
