@@ -737,7 +737,9 @@ def w4_row_bytes(k):
 class W4Weight:
     """A weight [..., N, K] in 4 bits (device tensors): codes uint8
     [..., N, w4_row_bytes(K)], scales bf16 [..., N, K/group], zeros uint8 of the
-    scales' shape or None (8).  W = scales * (code - zeros)."""
+    scales' shape or None (8).  W = scales * (code - zeros).  The tensors'
+    contents may change, the tensors themselves are the weight's for good; their
+    addresses are read at each call."""
 
     def __init__(self, codes, scales, zeros=None, group=128, k=None):
         k = scales.shape[-1] * group if k is None else k
@@ -748,10 +750,19 @@ class W4Weight:
             raise ValueError("codes, scales, group and k do not fit together")
         if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
             raise ValueError("zeros must be uint8, of the scales' shape")
-        self.codes, self.scales, self.zeros, self.group, self.k = codes, scales, zeros, group, k
-        self.n = codes.shape[-2]
-        self._pointers = W4Pointers(_p(codes), _p(scales), _p(zeros))
-        self._ref = ctypes.byref(self._pointers)
+        self._codes, self._scales, self._zeros = codes, scales, zeros
+        self._group, self._k, self._n = group, k, codes.shape[-2]
+        self._pointers()
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    zeros = property(lambda self: self._zeros)
+    group = property(lambda self: self._group)
+    k = property(lambda self: self._k)
+    n = property(lambda self: self._n)
+
+    def _pointers(self):
+        return W4Pointers(_p(self._codes), _p(self._scales), _p(self._zeros))
 
 
 class W4Experts:
@@ -760,13 +771,21 @@ class W4Experts:
     def __init__(self, W1, W3, W2):
         if not W1.group == W3.group == W2.group:
             raise ValueError("the experts' weights must have one group size")
-        self.W1, self.W3, self.W2, self.group = W1, W3, W2, W1.group
+        self._weights = W1, W3, W2
+
+    W1 = property(lambda self: self._weights[0])
+    W3 = property(lambda self: self._weights[1])
+    W2 = property(lambda self: self._weights[2])
+    group = property(lambda self: self._weights[0].group)
 
     def fits(self, cfg):
         E, h, f = cfg.num_experts, cfg.hidden, cfg.ffn_hidden
         for w, shape, k in ((self.W1, (E, f), h), (self.W3, (E, f), h), (self.W2, (E, h), f)):
             if w.codes.shape[:-1] != shape or w.k != k:
                 raise ValueError("the 4-bit weights do not fit the configuration")
+
+    def _pointers(self):
+        return [w._pointers() for w in self._weights]
 
 
 def quantize_w4(W, group=128, zeros=False):
@@ -822,7 +841,7 @@ def linear_w4(x, w, y, ws):
     if not ys or ys[-1] != w.n or ys[:-1] != xs[:-1]:
         raise ValueError("y must be [..., N]")
     b, wb = _ws(ws)
-    _check(lib().moe_linear_w4(x.numel() // w.k, w.n, w.k, w.group, _p(x), w._ref, _p(y),
+    _check(lib().moe_linear_w4(x.numel() // w.k, w.n, w.k, w.group, _p(x), w._pointers(), _p(y),
                                _code(y, "y"), b, wb, _stream()), "moe_linear_w4")
 
 
@@ -843,8 +862,8 @@ def experts_w4(cfg, x, topk_idx, topk_prob, keep, q, y, ws):
     q.fits(cfg)
     b, wb = _ws(ws)
     _check(lib().moe_experts_w4(ctypes.byref(cfg), q.group, _p(x), _p(topk_idx), _p(topk_prob),
-                                _p(keep), q.W1._ref, q.W3._ref, q.W2._ref, _p(y), b, wb,
-                                _stream()), "moe_experts_w4")
+                                _p(keep), *q._pointers(), _p(y), b, wb, _stream()),
+           "moe_experts_w4")
 
 
 def workspace_size_w4(cfg):
@@ -864,9 +883,9 @@ def forward_w4(cfg, x, Wg, gate_bias, expert_bias, q, y, ws, topk_idx=None, topk
     q.fits(cfg)
     b, wb = _ws(ws)
     _check(lib().moe_forward_w4(ctypes.byref(cfg), q.group, _p(x), _p(Wg), _p(gate_bias),
-                                _p(expert_bias), q.W1._ref, q.W3._ref, q.W2._ref, _p(y),
-                                _p(topk_idx), _p(topk_prob), _p(tokens_per_expert), b, wb,
-                                _stream()), "moe_forward_w4")
+                                _p(expert_bias), *q._pointers(), _p(y), _p(topk_idx),
+                                _p(topk_prob), _p(tokens_per_expert), b, wb, _stream()),
+           "moe_forward_w4")
 
 
 def probe_fp32_fma(iters, out):
