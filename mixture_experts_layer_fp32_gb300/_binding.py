@@ -651,6 +651,14 @@ def _vec(t, n, dtype, what):
     return _p(t)
 
 
+def _table(t, rows, cols, dtype, what):
+    """A tensor [..., cols] (or flat) of rows x cols values."""
+    ok = t is None or (t.numel() == rows * cols and (t.dim() == 1 or t.shape[-1:] == (cols,)))
+    if not ok or (t is not None and t.dtype != dtype):
+        raise ValueError("%s must be [%d, %d] of %s" % (what, rows, cols, dtype))
+    return _p(t)
+
+
 def _rng(rng, p):
     if p > 0 and (rng is None or rng.numel() != 2 or rng.dtype not in (torch.int64,
                                                                        torch.uint64)):
@@ -858,12 +866,17 @@ def alloc_workspace_experts_w4(cfg, device="cuda"):
 
 def experts_w4(cfg, x, topk_idx, topk_prob, keep, q, y, ws):
     """The routed SwiGLU experts of few tokens with 4-bit weights (q: W4Experts),
-    from the router's topk_idx, topk_prob and keep (or None), into y [T,h]."""
+    from the router's topk_idx (int32), topk_prob (fp32) and keep (one byte each,
+    or None), [T,k], into y [T,h]."""
     q.fits(cfg)
+    T, k, h, dt = cfg.num_tokens, cfg.topk, cfg.hidden, act_dtype(cfg)
+    kept = torch.bool if keep is not None and keep.dtype == torch.bool else torch.uint8
     b, wb = _ws(ws)
-    _check(lib().moe_experts_w4(ctypes.byref(cfg), q.group, _p(x), _p(topk_idx), _p(topk_prob),
-                                _p(keep), *q._pointers(), _p(y), b, wb, _stream()),
-           "moe_experts_w4")
+    _check(lib().moe_experts_w4(ctypes.byref(cfg), q.group, _table(x, T, h, dt, "x"),
+                                _table(topk_idx, T, k, torch.int32, "topk_idx"),
+                                _table(topk_prob, T, k, torch.float32, "topk_prob"),
+                                _table(keep, T, k, kept, "keep"), *q._pointers(),
+                                _table(y, T, h, dt, "y"), b, wb, _stream()), "moe_experts_w4")
 
 
 def workspace_size_w4(cfg):
@@ -881,11 +894,16 @@ def forward_w4(cfg, x, Wg, gate_bias, expert_bias, q, y, ws, topk_idx=None, topk
                tokens_per_expert=None):
     """The layer forward with 4-bit experts (q: W4Experts), for decoding."""
     q.fits(cfg)
+    T, k, h, E, dt = cfg.num_tokens, cfg.topk, cfg.hidden, cfg.num_experts, act_dtype(cfg)
+    f32, i32 = torch.float32, torch.int32
     b, wb = _ws(ws)
-    _check(lib().moe_forward_w4(ctypes.byref(cfg), q.group, _p(x), _p(Wg), _p(gate_bias),
-                                _p(expert_bias), *q._pointers(), _p(y), _p(topk_idx),
-                                _p(topk_prob), _p(tokens_per_expert), b, wb, _stream()),
-           "moe_forward_w4")
+    _check(lib().moe_forward_w4(ctypes.byref(cfg), q.group, _table(x, T, h, dt, "x"),
+                                _table(Wg, h, E, f32, "Wg"), _vec(gate_bias, E, f32, "gate_bias"),
+                                _vec(expert_bias, E, f32, "expert_bias"), *q._pointers(),
+                                _table(y, T, h, dt, "y"), _table(topk_idx, T, k, i32, "topk_idx"),
+                                _table(topk_prob, T, k, f32, "topk_prob"),
+                                _vec(tokens_per_expert, E, i32, "tokens_per_expert"), b, wb,
+                                _stream()), "moe_forward_w4")
 
 
 def probe_fp32_fma(iters, out):

@@ -83,3 +83,74 @@ def test_addresses_are_read_at_each_call(moe):
     for t, other in zip((w.codes, w.scales, w.zeros), others):
         t.set_(other)
     assert _linear(moe, w) == tuple(t.data_ptr() for t in others)
+
+
+T, H, E, K, F = 6, 256, 8, 2, 128
+
+
+def _layer(moe):
+    q = moe.W4Experts(_weight(moe, E, F, K=H), _weight(moe, E, F, K=H), _weight(moe, E, H, K=F))
+    return moe.config(T=T, h=H, E=E, k=K, f=F), q, torch.zeros(1 << 20, dtype=torch.uint8)
+
+
+def _wrong(t):
+    """Tensors that must not be taken in the place of t: another type, fewer and
+    more values, rows of another length."""
+    other = torch.int64 if t.dtype == torch.int32 else torch.float16
+    short, long = t[:-1].clone(), torch.cat((t, t[:1]))
+    return [t.to(other), t.double(), short, long] + ([t.t().contiguous()] if t.dim() == 2 else [])
+
+
+EXPERTS = dict(x=torch.zeros((T, H), dtype=BF), topk_idx=torch.zeros((T, K), dtype=torch.int32),
+               topk_prob=torch.zeros((T, K)), keep=torch.ones((T, K), dtype=torch.uint8),
+               y=torch.zeros((T, H), dtype=BF))
+
+
+@pytest.mark.parametrize("name", list(EXPERTS))
+def test_experts_take_no_other_tensors(moe, name):
+    cfg, q, ws = _layer(moe)
+    for bad in _wrong(EXPERTS[name]):
+        a = dict(EXPERTS, **{name: bad})
+        with pytest.raises(ValueError, match=name):
+            moe.experts_w4(cfg, a["x"], a["topk_idx"], a["topk_prob"], a["keep"], q, a["y"], ws)
+    assert not moe.calls
+
+
+@pytest.mark.parametrize("keep", [None, torch.ones((T, K), dtype=torch.uint8),
+                                  torch.ones((T, K), dtype=torch.bool),
+                                  torch.ones(T * K, dtype=torch.uint8)])
+def test_experts_take_what_the_router_writes(moe, keep):
+    cfg, q, ws = _layer(moe)
+    a = EXPERTS
+    moe.experts_w4(cfg, a["x"].view(2, 3, H), a["topk_idx"], a["topk_prob"], keep, q, a["y"], ws)
+    name, args = moe.calls[-1]
+    assert name == "moe_experts_w4" and args[1] == 64
+    assert args[2:6] == (a["x"].data_ptr(), a["topk_idx"].data_ptr(), a["topk_prob"].data_ptr(),
+                         None if keep is None else keep.data_ptr())
+    assert [_pointers(w) for w in args[6:9]] == [_pointers(w) for w in q._pointers()]
+    assert args[9:12] == (a["y"].data_ptr(), ws.data_ptr(), ws.numel())
+
+
+FORWARD = dict(x=EXPERTS["x"], Wg=torch.zeros((H, E)), gate_bias=torch.zeros(E),
+               expert_bias=torch.zeros(E), y=EXPERTS["y"], topk_idx=EXPERTS["topk_idx"],
+               topk_prob=EXPERTS["topk_prob"],
+               tokens_per_expert=torch.zeros(E, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("name", list(FORWARD))
+def test_forward_takes_no_other_tensors(moe, name):
+    cfg, q, ws = _layer(moe)
+
+    def call(a):
+        moe.forward_w4(cfg, a["x"], a["Wg"], a["gate_bias"], a["expert_bias"], q, a["y"], ws,
+                       topk_idx=a["topk_idx"], topk_prob=a["topk_prob"],
+                       tokens_per_expert=a["tokens_per_expert"])
+
+    for bad in _wrong(FORWARD[name]):
+        with pytest.raises(ValueError, match=name):
+            call(dict(FORWARD, **{name: bad}))
+    assert not moe.calls
+    call(FORWARD)
+    if name not in ("x", "Wg", "y"):
+        call(dict(FORWARD, **{name: None}))
+    assert all(n == "moe_forward_w4" for n, _ in moe.calls)
