@@ -698,7 +698,9 @@ moe_status moe_pack_w4(int32_t experts, int32_t N, int32_t K, const uint8_t* val
                        uint8_t* codes, moe_stream_t stream);
 
 /* y [rows, N] (y_dtype) = x [rows, K] bf16 . W^T.  Made for few rows (decoding):
- * the weight is read once for every 64 rows. */
+ * the weight is read once for every 64 rows.  The workspace of `rows` rows serves
+ * every call of fewer rows too (that a call of fewer needs less does not follow:
+ * it is cut into more parts). */
 moe_status moe_workspace_size_linear_w4(int64_t rows, int32_t N, int32_t K, size_t* bytes);
 moe_status moe_linear_w4(int64_t rows, int32_t N, int32_t K, int32_t group, const void* x,
                          const moe_w4* W, void* y, int32_t y_dtype, void* ws, size_t ws_bytes,
@@ -716,6 +718,7 @@ moe_status moe_linear_w4(int64_t rows, int32_t N, int32_t K, int32_t group, cons
  * read once for every 64 of its rows (W2: 32); many tokens belong to moe_forward
  * or moe_forward_e4m3.
  */
+/* The workspaces of cfg's num_tokens serve every call of fewer tokens too. */
 moe_status moe_workspace_size_experts_w4(const moe_config* cfg, size_t* bytes);
 moe_status moe_experts_w4(const moe_config* cfg, int32_t group, const void* x,
                           const int32_t* topk_idx, const float* topk_prob, const uint8_t* keep,

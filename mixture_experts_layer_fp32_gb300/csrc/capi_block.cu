@@ -86,9 +86,11 @@ moe_status validate_experts(const moe_config* cfg) {
   return cfg->dtype == MOE_BF16 ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
-size_t experts_bytes(const moe_config& c) {
+// most: what any call of up to that many tokens needs, not this one alone
+size_t experts_bytes(const moe_config& c, bool most) {
   return kErrBytes +
-         w4_experts_scratch(c.num_tokens, c.hidden, c.num_experts, c.topk, c.ffn_hidden);
+         (most ? w4_experts_scratch_most : w4_experts_scratch)(c.num_tokens, c.hidden,
+                                                               c.num_experts, c.topk, c.ffn_hidden);
 }
 
 // moe_forward_w4: the layer's workspace (moe_route's, with the error word),
@@ -96,7 +98,7 @@ size_t experts_bytes(const moe_config& c) {
 struct ForwardLayout {
   size_t idx, prob, keep, tpe, experts, total;
 };
-moe_status forward_layout(const moe_config& c, ForwardLayout* L) {
+moe_status forward_layout(const moe_config& c, bool most, ForwardLayout* L) {
   size_t o = 0;
   MOE_TRY(moe_workspace_size(&c, &o));
   auto take = [&](size_t bytes) {
@@ -109,7 +111,7 @@ moe_status forward_layout(const moe_config& c, ForwardLayout* L) {
   L->prob = take(pairs * 4);
   L->keep = take(pairs);
   L->tpe = take(static_cast<size_t>(c.num_experts) * 4);
-  L->experts = take(experts_bytes(c) - kErrBytes);
+  L->experts = take(experts_bytes(c, most) - kErrBytes);
   L->total = o;
   return MOE_OK;
 }
@@ -220,7 +222,7 @@ moe_status moe_pack_w4(int32_t experts, int32_t N, int32_t K, const uint8_t* val
 moe_status moe_workspace_size_linear_w4(int64_t rows, int32_t N, int32_t K, size_t* bytes) {
   MOE_TRY(validate_linear(rows, N, K));
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-  *bytes = kErrBytes + w4_linear_scratch(rows, N, K);
+  *bytes = kErrBytes + w4_linear_scratch_most(rows, N, K);
   return MOE_OK;
 }
 
@@ -244,7 +246,7 @@ moe_status moe_linear_w4(int64_t rows, int32_t N, int32_t K, int32_t group, cons
 moe_status moe_workspace_size_experts_w4(const moe_config* cfg, size_t* bytes) {
   MOE_TRY(validate_experts(cfg));
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-  *bytes = experts_bytes(*cfg);
+  *bytes = experts_bytes(*cfg, true);
   return MOE_OK;
 }
 
@@ -261,7 +263,7 @@ moe_status moe_experts_w4(const moe_config* cfg, int32_t group, const void* x,
   MOE_TRY(need(topk_idx, T, 4));
   MOE_TRY(need(topk_prob, T, 4));
   MOE_TRY(need(y, T));
-  MOE_TRY(check_ws(ws, ws_bytes, experts_bytes(c)));
+  MOE_TRY(check_ws(ws, ws_bytes, experts_bytes(c, false)));
   if (T == 0) return MOE_OK;
   MOE_CUDA(launch_w4_experts(c.num_tokens, c.hidden, c.num_experts, c.topk, c.ffn_hidden, group, x,
                              topk_idx, topk_prob, keep, w1, w3, w2, y, past_error_word(ws),
@@ -273,7 +275,7 @@ moe_status moe_workspace_size_w4(const moe_config* cfg, size_t* bytes) {
   MOE_TRY(validate_experts(cfg));
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
   ForwardLayout L;
-  MOE_TRY(forward_layout(*cfg, &L));
+  MOE_TRY(forward_layout(*cfg, true, &L));
   *bytes = L.total;
   return MOE_OK;
 }
@@ -297,7 +299,7 @@ moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, c
   MOE_TRY(optional(topk_prob, 4));
   MOE_TRY(optional(tokens_per_expert, 4));
   ForwardLayout L;
-  MOE_TRY(forward_layout(c, &L));
+  MOE_TRY(forward_layout(c, false, &L));
   MOE_TRY(check_ws(ws, ws_bytes, L.total));
   char* base = static_cast<char*>(ws);
   int32_t* idx = topk_idx ? topk_idx : reinterpret_cast<int32_t*>(base + L.idx);

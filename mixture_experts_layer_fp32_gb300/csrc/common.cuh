@@ -302,11 +302,14 @@ cudaError_t launch_w4_quantize(int E, int K, int N, int group, const void* W, ui
                                void* scales, uint8_t* zeros, cudaStream_t s);
 cudaError_t launch_w4_pack(int E, int N, int K, const uint8_t* values, uint8_t* codes,
                            cudaStream_t s);
-// bytes of scratch, and the product of `rows` rows
+// bytes of scratch of one call, the most that a call of up to `rows` rows (T
+// tokens) needs, and the product of `rows` rows
 size_t w4_linear_scratch(int64_t rows, int N, int K);
+size_t w4_linear_scratch_most(int64_t rows, int N, int K);
 cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* x, const W4& W,
                              void* y, int y_dtype, void* scratch, int* err, cudaStream_t s);
 size_t w4_experts_scratch(int T, int h, int E, int k, int f);
+size_t w4_experts_scratch_most(int T, int h, int E, int k, int f);
 cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, const void* x,
                               const int32_t* topk_idx, const float* topk_prob,
                               const uint8_t* keep, const W4& W1, const W4& W3, const W4& W2,

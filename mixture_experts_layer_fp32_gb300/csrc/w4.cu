@@ -285,6 +285,17 @@ size_t w4_linear_scratch(int64_t rows, int N, int K) {
          (L.way.splits == 1 ? 0 : static_cast<size_t>(L.way.splits) * L.rows * N * 4);
 }
 
+// Fewer rows are cut into more parts, so a call of them can need more.  A launch
+// has kMaxRows rows at most: all of them are tried, some 10 us in all.
+size_t w4_linear_scratch_most(int64_t rows, int N, int K) {
+  size_t most = 0;
+  for (int64_t r = 0; r <= rows && r <= kMaxRows; ++r) {
+    const size_t bytes = w4_linear_scratch(r, N, K);
+    most = bytes > most ? bytes : most;
+  }
+  return most;
+}
+
 cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* x, const W4& W,
                              void* y, int y_dtype, void* scratch, int* err, cudaStream_t s) {
   const LinearShape L = linear_shape(rows, N, K);
@@ -330,6 +341,15 @@ size_t w4_experts_scratch(int T, int h, int E, int k, int f) {
   return split_bytes(S.way1.wide ? S.pairs : S.tokens, h, 1) +
          align256(static_cast<size_t>(S.pairs) * f * 4) +
          split_bytes(S.pairs, f, 2) + static_cast<size_t>(S.way2.splits) * S.pairs * h * 4;
+}
+
+size_t w4_experts_scratch_most(int T, int h, int E, int k, int f) {
+  size_t most = 0;
+  for (int t = 0; t <= T && t <= kMaxRows / k; ++t) {
+    const size_t bytes = w4_experts_scratch(t, h, E, k, f);
+    most = bytes > most ? bytes : most;
+  }
+  return most;
 }
 
 cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, const void* x,
