@@ -647,7 +647,8 @@ moe_status moe_layer_norm(const moe_norm_config* cfg, const void* x, const void*
  * rounding), the gradient of the forward's x; it may be NULL, and is the only
  * use of dropout and rng.  dweight and dbias (each may be NULL) are written in
  * full (zeros for no rows) and do not depend on timing: fixed order of sums.
- * dx may be dy or dz itself, dbranch too (another one than dx's).
+ * dx may be dy or dz itself, dbranch too (another one than dx's).  The workspace of
+ * `rows` rows serves every call of that hidden and fewer rows, of either dtype.
  */
 moe_status moe_workspace_size_norm_backward(const moe_norm_config* cfg, size_t* bytes);
 moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, const void* z,

@@ -47,14 +47,8 @@ moe_status validate(const moe_norm_config* c) {
   return MOE_OK;
 }
 
-// One size for both types of a tensor, so that a workspace serves either.
-size_t norm_backward_bytes(const moe_norm_config& c) {
-  moe_norm_config d = c;
-  d.dtype = MOE_F32;
-  const int wide = norm_backward_ctas(d);
-  d.dtype = MOE_BF16;
-  const int narrow = norm_backward_ctas(d);
-  return kErrBytes + static_cast<size_t>(wide > narrow ? wide : narrow) * 2 * c.hidden * 4;
+size_t norm_backward_bytes(const moe_norm_config& c, int ctas) {
+  return kErrBytes + static_cast<size_t>(ctas) * 2 * c.hidden * 4;
 }
 
 bool is_group(int32_t g) { return g == 32 || g == 64 || g == 128; }
@@ -155,7 +149,7 @@ moe_status moe_layer_norm(const moe_norm_config* cfg, const void* x, const void*
 moe_status moe_workspace_size_norm_backward(const moe_norm_config* cfg, size_t* bytes) {
   MOE_TRY(validate(cfg));
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-  *bytes = norm_backward_bytes(*cfg);
+  *bytes = norm_backward_bytes(*cfg, norm_backward_ctas_most(*cfg));
   return MOE_OK;
 }
 
@@ -179,7 +173,7 @@ moe_status moe_layer_norm_backward(const moe_norm_config* cfg, const void* dy, c
   MOE_TRY(optional(dbias));
   if (dbranch != nullptr && dbranch == dx) return MOE_ERR_INVALID_ARG;
   if (dbranch != nullptr && c.dropout > 0.0) MOE_TRY(need(rng, n));
-  MOE_TRY(check_ws(ws, ws_bytes, norm_backward_bytes(c)));
+  MOE_TRY(check_ws(ws, ws_bytes, norm_backward_bytes(c, norm_backward_ctas(c))));
   MOE_CUDA(launch_norm_backward(c, dy, z, weight, mean, rstd, dz, rng, dx, dbranch, dweight,
                                 dbias, static_cast<float*>(past_error_word(ws)), stream));
   return MOE_OK;

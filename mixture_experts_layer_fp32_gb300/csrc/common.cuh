@@ -283,8 +283,10 @@ cudaError_t launch_quantize_cols(int E, int K, int N, const void* W, uint8_t* co
 cudaError_t launch_norm(const moe_norm_config& c, const void* x, const void* residual,
                         const uint64_t* rng, const void* weight, const void* bias, void* z,
                         void* y, float* mean, float* rstd, cudaStream_t s);
-// part: norm_backward_ctas(c) x 2 x hidden floats
+// part: norm_backward_ctas(c) x 2 x hidden floats; the most that up to c.rows rows
+// of either type take
 int norm_backward_ctas(const moe_norm_config& c);
+int norm_backward_ctas_most(const moe_norm_config& c);
 cudaError_t launch_norm_backward(const moe_norm_config& c, const void* dy, const void* z,
                                  const void* weight, const float* mean, const float* rstd,
                                  const void* dz, const uint64_t* rng, void* dx, void* dbranch,

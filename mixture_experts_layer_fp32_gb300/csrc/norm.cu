@@ -1064,6 +1064,23 @@ int norm_backward_ctas(const moe_norm_config& c) {
   return static_cast<int>(c.rows < 4 * kSms ? c.rows : 4 * kSms);
 }
 
+// The blocks grow with the rows but for one step down: from 152 times the groups of
+// a block on, a block has several groups (shape_common).
+int norm_backward_ctas_most(const moe_norm_config& c) {
+  moe_norm_config d = c;
+  int most = 0;
+  for (const int dtype : {MOE_F32, MOE_BF16}) {
+    d.dtype = dtype;
+    for (const int64_t groups : {2, 4, 8, 0}) {
+      const int64_t before = kSms * groups - 1;
+      d.rows = groups != 0 && before < c.rows ? before : c.rows;
+      const int ctas = norm_backward_ctas(d);
+      most = ctas > most ? ctas : most;
+    }
+  }
+  return most;
+}
+
 cudaError_t launch_norm(const moe_norm_config& c, const void* x, const void* residual,
                         const uint64_t* rng, const void* weight, const void* bias, void* z,
                         void* y, float* mean, float* rstd, cudaStream_t s) {

@@ -42,3 +42,10 @@ def test_experts_and_forward(moe, h, E, k, f):
         sizes = [ask(moe.config(T=T, h=h, E=E, k=k, f=f))
                  for T in list(range(0, 100)) + [128, 256, 511, 512, 513, 1024, 1025]]
         assert _grows(sizes)
+
+
+@pytest.mark.parametrize("H", [1, 64, 256, 511, 1021, 1023, 1024, 2048, 4096, 4099, 8200, 16384,
+                               33000])
+def test_norm_backward(moe, H):
+    sizes = [moe.workspace_size_norm_backward(rows, H) for rows in range(0, 5000)]
+    assert _grows(sizes)

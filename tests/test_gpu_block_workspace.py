@@ -43,3 +43,22 @@ def test_experts_and_forward():
         moe.check(ws)
         moe.check(ws_layer)
         assert torch.equal(y, own) and torch.equal(layer, layer_own)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H", [64, 1021, 1024])
+def test_norm_backward(H, dtype):
+    import mixture_experts_layer_fp32_gb300 as moe
+    most = 4000
+    z, dy = (torch.randn((most, H), device="cuda").to(dtype) for _ in range(2))
+    mean, rstd = z.float().mean(1), torch.rsqrt(z.float().var(1) + 1e-5)
+    ws = moe.alloc_workspace_norm_backward(most, H)
+    for rows in (1, 151, 303, 304, 607, 608, 1215, 1216, most):
+        outs = []
+        for use in (ws, moe.alloc_workspace_norm_backward(rows, H)):
+            dx = torch.full((rows, H), float("nan"), dtype=dtype, device="cuda")
+            dw, db = (torch.full((H,), float("nan"), device="cuda") for _ in range(2))
+            moe.layer_norm_backward(dy[:rows], z[:rows], None, mean[:rows], rstd[:rows], dx, dw,
+                                    db, use)
+            outs.append((dx, dw, db))
+        assert all(torch.equal(a, c) for a, c in zip(*outs))
