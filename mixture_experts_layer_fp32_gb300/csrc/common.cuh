@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe.h"
 
 namespace moe {
@@ -41,6 +43,28 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// Leave for all the dynamic shared memory that a block can have, once for a kernel
+// and device: asking at every launch costs the host more than the launch's own
+// arguments, and an amount of one call's would be another thread's limit between
+// its own asking and its launch.
+template <auto KERNEL>
+cudaError_t allow_most_smem() {
+  constexpr size_t most = 227 * 1024;  // a block's, the kernel's own variables among it
+  static std::atomic<uint64_t> done{0};
+  int device = 0;
+  cudaError_t st = cudaGetDevice(&device);
+  if (st != cudaSuccess) return st;
+  const uint64_t bit = uint64_t{1} << (device & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes f;
+  st = cudaFuncGetAttributes(&f, KERNEL);
+  if (st != cudaSuccess) return st;
+  st = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                            static_cast<int>(most - f.sharedSizeBytes));
+  if (st == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return st;
 }
 
 __device__ __forceinline__ void report_error(int* err, int code, int info) {

@@ -970,11 +970,9 @@ auto with_bool(bool b, F&& f) {
 }
 
 // 48 KB need no leave, but the kernels' own variables are among them.
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-  if (bytes <= 47 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes));
+template <auto KERNEL>
+cudaError_t allow_smem(size_t bytes) {
+  return bytes <= 47 * 1024 ? cudaSuccess : allow_most_smem<KERNEL>();
 }
 
 template <typename T>
@@ -988,10 +986,10 @@ cudaError_t norm_typed(const moe_norm_config& c, const void* x, const void* resi
   auto launch = [&](auto vpt) -> cudaError_t {
     return with_bool(p.aligned, [&](auto aligned) {
       return with_bool(a.drop.on, [&](auto drop) -> cudaError_t {
-        auto k = norm_rows_kernel<T, decltype(vpt)::value, decltype(aligned)::value,
-                                  decltype(drop)::value>;
+        constexpr auto k = norm_rows_kernel<T, decltype(vpt)::value, decltype(aligned)::value,
+                                            decltype(drop)::value>;
         const size_t smem = 2 * static_cast<size_t>(p.padded) * 4;
-        const cudaError_t st = allow_smem(k, smem);
+        const cudaError_t st = allow_smem<k>(smem);
         if (st != cudaSuccess) return st;
         k<<<p.grid, p.threads, smem, s>>>(a, p.group_warps, p.padded, xt, rt, weight, bias, zt, yt,
                                           mean, rstd);
@@ -1030,10 +1028,11 @@ cudaError_t norm_backward_typed(const moe_norm_config& c, const void* dy, const 
   auto launch = [&](auto vpt, auto staged) -> cudaError_t {
     return with_bool(p.aligned, [&](auto aligned) {
       return with_bool(a.drop.on, [&](auto drop) -> cudaError_t {
-        auto k = norm_backward_rows_kernel<T, decltype(vpt)::value, decltype(aligned)::value,
-                                           decltype(drop)::value, decltype(staged)::value>;
+        constexpr auto k =
+            norm_backward_rows_kernel<T, decltype(vpt)::value, decltype(aligned)::value,
+                                      decltype(drop)::value, decltype(staged)::value>;
         const size_t smem = backward_smem(p);
-        const cudaError_t st = allow_smem(k, smem);
+        const cudaError_t st = allow_smem<k>(smem);
         if (st != cudaSuccess) return st;
         k<<<p.grid, p.threads, smem, s>>>(a, p.group_warps, p.padded, dyt, zt, weight, mean, rstd,
                                           dzt, dxt, dbt, part);

@@ -31,8 +31,6 @@
 // runs, made no difference.
 #pragma once
 
-#include <atomic>
-
 #include "sm100_ptx.cuh"
 #include "w4.cuh"
 
@@ -723,26 +721,6 @@ bool map_codes(CUtensorMap* m, const uint8_t* codes, int64_t rows, int blocks, i
 // 8 columns
 bool map_x(CUtensorMap* m, const __half* x, int64_t columns, int blocks);
 
-// Once for a kernel and device; asking at every launch costs the host more than
-// the launch's own arguments.
-template <auto KERNEL>
-cudaError_t allow_smem() {
-  constexpr size_t most = 227 * 1024;  // a block's, the kernel's own variables among it
-  static std::atomic<uint64_t> done{0};
-  int device = 0;
-  cudaError_t st = cudaGetDevice(&device);
-  if (st != cudaSuccess) return st;
-  const uint64_t bit = uint64_t{1} << (device & 63);
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  cudaFuncAttributes f;
-  st = cudaFuncGetAttributes(&f, KERNEL);
-  if (st != cudaSuccess) return st;
-  st = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                            static_cast<int>(most - f.sharedSizeBytes));
-  if (st == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return st;
-}
-
 template <int MODE, int G32, bool ZEROS, bool TAIL>
 cudaError_t launch_narrow(Args a, cudaStream_t s) {
   const int tile = (MODE == FC1 ? 8 : 16);
@@ -757,7 +735,7 @@ cudaError_t launch_narrow(Args a, cudaStream_t s) {
   constexpr auto k = w4_narrow_kernel<MODE, G32, ZEROS, TAIL>;
   const size_t smem = kNarrowWarps * 2 * 4096 +
                       2 * kNarrowWarps * (4 / pieces_of(MODE)) * 32 * 4 + kNarrowX + plan;
-  const cudaError_t st = allow_smem<k>();
+  const cudaError_t st = allow_most_smem<k>();
   if (st != cudaSuccess) return st;
   a.wk = share_narrow(items, a.split_units, a.split_rest != 0).wk;
   a.each = (a.split_units + a.wk - 1) / a.wk;
@@ -794,7 +772,7 @@ cudaError_t launch_wide(Args a, cudaStream_t s) {
   a.split_rest = (a.blocks + 3) / 4 % a.splits;
   constexpr auto k = w4_wide_kernel<MODE, G32>;
   const size_t smem = kTallSmem + (MODE == LINEAR ? 0 : sizeof(Plan));
-  const cudaError_t st = allow_smem<k>();
+  const cudaError_t st = allow_most_smem<k>();
   if (st != cudaSuccess) return st;
   const int64_t all = static_cast<int64_t>(MODE == LINEAR ? 1 : a.E) * a.N;
   const int64_t columns = static_cast<int64_t>(MODE == LINEAR ? a.rows : a.pairs) * pieces_of(MODE);
