@@ -653,8 +653,10 @@ def _vec(t, n, dtype, what):
 
 def _table(t, rows, cols, dtype, what):
     """A tensor [..., cols] (or flat) of rows x cols values."""
-    ok = t is None or (t.numel() == rows * cols and (t.dim() == 1 or t.shape[-1:] == (cols,)))
-    if not ok or (t is not None and t.dtype != dtype):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != (rows, cols) and (
+            t.numel() != rows * cols or (t.dim() != 1 and t.shape[-1:] != (cols,))):
         raise ValueError("%s must be [%d, %d] of %s" % (what, rows, cols, dtype))
     return _p(t)
 
@@ -760,6 +762,8 @@ class W4Weight:
             raise ValueError("zeros must be uint8, of the scales' shape")
         self._codes, self._scales, self._zeros = codes, scales, zeros
         self._group, self._k, self._n = group, k, codes.shape[-2]
+        self._form = tuple(codes.shape[:-1]), k
+        self._at = None
         self._pointers()
 
     codes = property(lambda self: self._codes)
@@ -770,7 +774,12 @@ class W4Weight:
     n = property(lambda self: self._n)
 
     def _pointers(self):
-        return W4Pointers(_p(self._codes), _p(self._scales), _p(self._zeros))
+        codes, scales, zeros = self._codes, self._scales, self._zeros
+        at = (codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr())
+        if at != self._at:  # making the structure takes longer than looking (0.3 us, not 1)
+            self._ref = ctypes.byref(W4Pointers(_p(codes), _p(scales), _p(zeros)))
+            self._at = at
+        return self._ref
 
 
 class W4Experts:
@@ -788,12 +797,14 @@ class W4Experts:
 
     def fits(self, cfg):
         E, h, f = cfg.num_experts, cfg.hidden, cfg.ffn_hidden
-        for w, shape, k in ((self.W1, (E, f), h), (self.W3, (E, f), h), (self.W2, (E, h), f)):
-            if w.codes.shape[:-1] != shape or w.k != k:
-                raise ValueError("the 4-bit weights do not fit the configuration")
+        W1, W3, W2 = self._weights
+        up = (E, f), h
+        if W1._form != up or W3._form != up or W2._form != ((E, h), f):
+            raise ValueError("the 4-bit weights do not fit the configuration")
 
     def _pointers(self):
-        return [w._pointers() for w in self._weights]
+        W1, W3, W2 = self._weights
+        return W1._pointers(), W3._pointers(), W2._pointers()
 
 
 def quantize_w4(W, group=128, zeros=False):
