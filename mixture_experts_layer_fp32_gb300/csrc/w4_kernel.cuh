@@ -109,6 +109,16 @@ __device__ __forceinline__ float lds4(uint32_t at) {
   return v;
 }
 
+// Whether a barrier's phase ends within a second.
+constexpr long long kWaitCycles = 2000000000ll;
+__device__ __forceinline__ bool arrives(uint32_t bar, int parity) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const long long began = clock64();
+  while (!ptx::mbar_try_wait(bar, parity))
+    if (clock64() - began > kWaitCycles) return false;
+  return true;
+}
+
 // c += A B, or c = A B
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -375,8 +385,10 @@ __device__ __forceinline__ void pairs_of(uint32_t word, uint32_t (&p)[4]) {
 // at each it brings the chunk's x (of the part's inputs) into shared memory.
 // Reading x through L1 instead cost a third of the time: L1 answers in order,
 // and a read that would hit waits behind every one that misses.
-constexpr long long kWaitCycles = 2000000000ll;  // a second: a copy that never arrived
-constexpr int kNarrowX = 66 * 1024;              // bytes of x and its sums, at most
+//
+// A wait that runs out reports it and the warp goes on with what is there, so that
+// nobody waits for it, but copies nothing more; the block ends after its copies.
+constexpr int kNarrowX = 66 * 1024;  // bytes of x and its sums, at most
 
 template <int MODE, int G32, bool ZEROS, bool TAIL>
 __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
@@ -450,10 +462,11 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
     }
   };
   int fill = 0;
+  bool lost = false;  // a wait ran out
   auto fetch = [&]() {
     if (next >= end) return;
     __syncwarp();  // every lane has read what the slot held
-    if (lane == 0) {
+    if (lane == 0 && !lost) {
       const uint32_t dst = ring + fill * kStage, b = bar + fill * 8;
       ptx::mbar_arrive_expect_tx(b, kStage);
       // blocks past the row's end come as zeros
@@ -489,7 +502,6 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
   pdl_wait();  // the split rows
 
   int use = 0, phase = 0, buf = 0;  // the slot at hand and its barrier's phase
-  bool lost = false;
   const int x_row = a.blocks * (128 * CP);
   const uint32_t xs = ptx::smem_u32(x_at);
   Item epoch(begin, a);
@@ -593,15 +605,15 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
         now = it;
         stage_now = stage;
         left_now = left;
+        const bool ahead = next < end;  // a copy into the other slot
         fetch();
-        if (!lost && !ptx::mbar_try_wait(bar + use * 8, phase)) {
-          const long long began = clock64();
-          while (!lost && !ptx::mbar_try_wait(bar + use * 8, phase))
-            if (clock64() - began > kWaitCycles) {
-              // go on with what is there, so that nobody waits for this warp
-              lost = true;
-              report_error(a.err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
-            }
+        if (!lost && !arrives(bar + use * 8, phase)) {
+          lost = true;
+          report_error(a.err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
+          if (lane == 0) {  // whose copies they are
+            arrives(bar + use * 8, phase);
+            if (ahead) arrives(bar + (use ^ 1) * 8, phase ^ use);
+          }
         }
         const uint32_t src = ring + use * kStage + lane * 16, xb = x_lane + k * 256;
         if (blocks == SB) {

@@ -15,7 +15,9 @@
 //   - one thread multiplies, a fresh sum for each group of inputs;
 //   - eight warps, an output of both tiles to a thread and half the columns each,
 //     read the groups' sums back and add them up under their scales in fp32.
-// All of them run at once and hand each other slots through mbarriers.
+// All of them run at once and hand each other slots through mbarriers.  A warp whose
+// wait runs out reports it, and then every warp leaves its loop; the block's copies
+// and products end (again within a limit) before its tensor memory is freed.
 //
 // Measured, the experts of 64 tokens (2 of 8 of 4096 x 14336, zero points): 198 us
 // with the splits and the combine; FC1 122 and FC2 81 us cold.  mma.sync from
@@ -48,23 +50,33 @@ struct TallBars {
   uint64_t x_full[kTallXs], x_free[kTallXs];
   uint64_t a_full[2], a_free[2];  // of both tiles
   uint64_t d_full[4], d_free[4];
+  uint64_t products;  // all of them
 };
 
-// Waits of a warp; after one that ran out it goes on with what is
-// there, so that nobody waits for it.
+// Waits of a converged warp.
 struct Waits {
   int* err;
-  bool lost = false;
-  __device__ __forceinline__ void operator()(uint32_t bar, int parity) {
-    if (!lost && !ptx::mbar_try_wait(bar, parity)) {
-      const long long began = clock64();
-      while (!lost && !ptx::mbar_try_wait(bar, parity))
-        if (clock64() - began > kWaitCycles) {
-          lost = true;
-          report_error(err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
-        }
+  volatile int* given_up;  // the block's
+
+  // false, for the whole warp, where this wait or another warp's ran out
+  __device__ __forceinline__ bool operator()(uint32_t bar, int parity) const {
+    if (__all_sync(~0u, ptx::mbar_try_wait(bar, parity))) return true;
+    const long long began = clock64();
+    do {
+      if (__any_sync(~0u, *given_up != 0 || clock64() - began > kWaitCycles)) {
+        *given_up = 1;
+        report_error(err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
+        return false;
+      }
+    } while (!__all_sync(~0u, ptx::mbar_try_wait(bar, parity)));
+    return true;
+  }
+  // what is in flight, given up or not
+  __device__ __forceinline__ void end(uint32_t bar, int parity) const {
+    if (!__all_sync(~0u, arrives(bar, parity))) {
+      *given_up = 1;
+      report_error(err, DEV_ERR_TIMEOUT, static_cast<int>(blockIdx.x));
     }
-    __syncwarp();
   }
 };
 
@@ -77,6 +89,8 @@ struct Ring {
       phase ^= 1;
     }
   }
+  // the parity of a slot's last use (a barrier that was never used counts as past 1)
+  __device__ __forceinline__ int last(int slot) const { return slot < at ? phase : phase ^ 1; }
 };
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -172,6 +186,7 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
   __shared__ TallBars bars;
   __shared__ float units[8][32];
   __shared__ uint32_t tmem_at;
+  __shared__ int given_up;
   const uint32_t base = (ptx::smem_u32(smem_raw) + 1023) & ~1023u;
   const uint32_t xs_at = base + kTallStages * kTallStage;
   Plan& plan = *reinterpret_cast<Plan*>(smem_raw + kTallSmem);
@@ -196,6 +211,8 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
       ptx::mbar_init(bar(bars.d_full[i]), 1);
       ptx::mbar_init(bar(bars.d_free[i]), 8);
     }
+    ptx::mbar_init(bar(bars.products), 1);
+    given_up = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 26) {
@@ -221,7 +238,7 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
 
   // Registers: 896 threads are launched with 72 each; 256 with 112 and 640
   // with 56 come to the same.
-  Waits wait{a.err};
+  const Waits wait{a.err, &given_up};
   Item it(blockIdx.x, a);
   // of the item: its first block of inputs, how many, its rows of x
   int kb = 0, nb = 0, row_first = 0, row_count = 0;
@@ -253,7 +270,8 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
     const bool whole = a.groups % 4 == 0;
     pdl_wait();  // the rows' units; and the output is free
     Ring ring{d_slots};
-    for (; enter(); it.next(gridDim.x, a)) {
+    bool on = true;
+    for (; on && enter(); it.next(gridDim.x, a)) {
       const int o[2] = {it.tile * kTile + r, it.tile * kTile + (MODE == FC1 ? 0 : 128) + r};
       const unsigned short* ps[2];
 #pragma unroll
@@ -294,7 +312,10 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
             now[d].x = __funnelshift_r(now[d].x, now[d].y, 16);
             now[d].y >>= 16;
           }
-          wait(bar(bars.d_full[ring.at]), ring.phase);
+          if (!wait(bar(bars.d_full[ring.at]), ring.phase)) {
+            copies_wait<0>();
+            return false;
+          }
           ptx::tc_fence_after();
           const uint32_t at = d_at(0, ring.at) + lanes + e * half;
           // a few columns of both tiles at a time, as the registers allow
@@ -364,12 +385,13 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
             if (o[1] < a.N) out[o[1]] = __float2bfloat16_rn(acc[1][i]);
           }
         }
+        return true;
       };
       switch ((row_count * CP + 15) / 16) {
-        case 1: item(std::integral_constant<int, 8>()); break;
-        case 2: item(std::integral_constant<int, 16>()); break;
-        case 3: item(std::integral_constant<int, 24>()); break;
-        default: item(std::integral_constant<int, 32>());
+        case 1: on = item(std::integral_constant<int, 8>()); break;
+        case 2: on = item(std::integral_constant<int, 16>()); break;
+        case 3: on = item(std::integral_constant<int, 24>()); break;
+        default: on = item(std::integral_constant<int, 32>());
       }
     }
   } else if (warp < 24) {
@@ -385,7 +407,8 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
     const uint32_t a_slot = a_at(d, slot) + lanes;
     Ring code{kTallStages};
     int turn = 0, phase = 0;  // the slot of the block to come; this slot's phase
-    for (; enter(); it.next(gridDim.x, a)) {
+    bool on = true;
+    for (; on && enter(); it.next(gridDim.x, a)) {
       const int o = it.tile * kTile + (MODE == FC1 ? 0 : d * 128) + r;
       const int left = a.groups - kb * GPB;
       const uint8_t* pz = nullptr;
@@ -400,7 +423,8 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
       }
 #pragma unroll 1
       for (int b = mine; b < nb + mine; b += 2) {
-        wait(bar(bars.code_full[code.at]), code.phase);
+        on = wait(bar(bars.code_full[code.at]), code.phase);
+        if (!on) break;
         if (b < nb) {
           uint4 q[4];
 #pragma unroll
@@ -411,7 +435,8 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
             const int g = (b + 2) * GPB & ~3;
             z_next = four_zeros(pz + g, left - g, whole);
           }
-          wait(bar(bars.a_free[slot]), phase ^ 1);
+          on = wait(bar(bars.a_free[slot]), phase ^ 1);
+          if (!on) break;
           ptx::tc_fence_after();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // inputs 32 j ..
@@ -447,10 +472,12 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
     if (warp == 24) {
       // ---- the codes' copies ----
       Ring code{kTallStages};
-      for (; enter(); it.next(gridDim.x, a)) {
+      bool on = true;
+      for (; on && enter(); it.next(gridDim.x, a)) {
         const bool second = MODE == FC1 || it.tile * kTile + 128 < a.N;
         for (int b = 0; b < nb; b += 2) {
-          wait(bar(bars.code_free[code.at]), code.phase ^ 1);
+          on = wait(bar(bars.code_free[code.at]), code.phase ^ 1);
+          if (!on) break;
           if (lane == 0) {
             const uint32_t dst = base + code.at * kTallStage, full = bar(bars.code_full[code.at]);
             ptx::mbar_arrive_expect_tx(full, second ? kTallStage : kTallStage / 2);
@@ -464,15 +491,18 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
           code.next();
         }
       }
+      for (int i = 0; i < kTallStages; ++i) wait.end(bar(bars.code_full[i]), code.last(i));
     } else if (warp == 25) {
       // ---- the copies of x: 8 columns of a block's inputs each ----
       pdl_wait();
       Ring ring{kTallXs};
-      for (; enter(); it.next(gridDim.x, a)) {
+      bool on = true;
+      for (; on && enter(); it.next(gridDim.x, a)) {
         const int copies = (row_count * CP + 7) / 8;
         for (int b = 0; b < nb; ++b) {
           const uint32_t full = bar(bars.x_full[ring.at]);
-          wait(bar(bars.x_free[ring.at]), ring.phase ^ 1);
+          on = wait(bar(bars.x_free[ring.at]), ring.phase ^ 1);
+          if (!on) break;
           if (lane == 0) ptx::mbar_arrive_expect_tx(full, copies * 2048);
           __syncwarp();
           if (lane < copies)
@@ -481,24 +511,28 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
           ring.next();
         }
       }
+      for (int i = 0; i < kTallXs; ++i) wait.end(bar(bars.x_full[i]), ring.last(i));
     } else if (warp == 26) {
       // ---- products: the warp keeps together, so that addresses stay in uniform
       // registers, and one thread of it issues ----
       const bool issues = elect_one();
       Ring ring{kTallXs};
       Ring as{2}, ds{d_slots};  // of A and D, both tiles' together
-      for (; enter(); it.next(gridDim.x, a)) {
+      bool on = true;
+      for (; on && enter(); it.next(gridDim.x, a)) {
         const uint32_t columns = (row_count * CP + 15) / 16 * 16;
         const uint32_t idesc = (1u << 4) | (columns >> 3) << 17 | (128u >> 4) << 24;
 #pragma unroll 1
-        for (int b = 0; b < nb; ++b) {
-          wait(bar(bars.x_full[ring.at]), ring.phase);
-          wait(bar(bars.a_full[as.at]), as.phase);
+        for (int b = 0; on && b < nb; ++b) {
+          on = wait(bar(bars.x_full[ring.at]), ring.phase) &&
+               wait(bar(bars.a_full[as.at]), as.phase);
+          if (!on) break;
           // a step of 16 inputs is 32 bytes on, 64 inputs 1024
           const uint64_t x = ptx::sw128_desc(xs_at + ring.at * kTallX, 0, 2048);
 #pragma unroll
           for (int q = 0; q < GPB; ++q) {
-            wait(bar(bars.d_free[ds.at]), ds.phase ^ 1);
+            on = wait(bar(bars.d_free[ds.at]), ds.phase ^ 1);
+            if (!on) break;
             ptx::tc_fence_after();
             if (issues) {
 #pragma unroll
@@ -521,6 +555,9 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
           ring.next();
         }
       }
+      if (issues) ptx::umma_commit(bar(bars.products));
+      __syncwarp();
+      wait.end(bar(bars.products), 0);
     }
   }
   __syncwarp();
