@@ -33,10 +33,9 @@ __device__ __forceinline__ float top_of(float top, float4 q) {
 // inputs, a block of the weights' layout, at a time.
 // SORTED: row i is the token of the i-th pair in the plan's order.
 constexpr int kSplitWarps = 16, kHeld = 8;
-template <typename T, int G32, int CP, bool SORTED>
+template <typename T, int CP, bool SORTED>
 __global__ void __launch_bounds__(kSplitWarps * 32)
-    w4_split_kernel(int K, int blocks, const T* x, __half* pieces, float* units, float* sums,
-                    Args a) {
+    w4_split_kernel(int K, int blocks, const T* x, __half* pieces, float* units, Args a) {
   __shared__ float tops[kSplitWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x;
@@ -77,7 +76,6 @@ __global__ void __launch_bounds__(kSplitWarps * 32)
 
   auto split = [&](int blk, float4 q) {
     float v[4] = {q.x * inverse, q.y * inverse, q.z * inverse, q.w * inverse};
-    float sum = 0.f, unit = 1.f;
 #pragma unroll
     for (int p = 0; p < CP; ++p) {
       __half h[4];
@@ -87,22 +85,13 @@ __global__ void __launch_bounds__(kSplitWarps * 32)
         const float up = i < 2 ? 1.f : 16.f;
         h[i] = __float2half_rn(v[i] * (1.f / up));
         const float had = __half2float(h[i]) * up;
-        sum += had * unit;
         v[i] = (v[i] - had) * 2048.f;
       }
-      unit *= 0.00048828125f;
       __half2 out[2] = {__halves2half2(h[0], h[1]), __halves2half2(h[2], h[3])};
       *reinterpret_cast<uint2*>(pieces +
                                 ((static_cast<int64_t>(row) * CP + p) * blocks + blk) * 128 +
                                 lane * 4) = *reinterpret_cast<uint2*>(out);
     }
-    if (sums == nullptr) return;  // the wide kernel takes the zeros off the codes
-    constexpr int kLanes = G32 * 8;  // of a group
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if ((lane & (kLanes - 1)) == 0)  // 2^-24, the codes' unit
-      sums[(static_cast<int64_t>(row) * blocks + blk) * (4 / G32) + lane / kLanes] =
-          sum * 5.9604644775390625e-08f;
   };
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
@@ -119,34 +108,30 @@ size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 // the last one.
 struct Split {
   __half* x;
-  float *unit, *sums;
+  float* unit;
 };
 size_t split_bytes(size_t rows, int K, int pieces) {
   const size_t blocks = rows * w4_blocks(K);
-  return align256((blocks * pieces + 1) * 256) + align256(rows * 4) +
-         align256((blocks + 1) * 4 * 4);
+  return align256((blocks * pieces + 1) * 256) + align256(rows * 4);
 }
-Split split_at(char* at, size_t rows, int K, int pieces, bool wide) {
+Split split_at(char* at, size_t rows, int K, int pieces) {
   const size_t blocks = rows * w4_blocks(K);
   Split p;
   p.x = reinterpret_cast<__half*>(at);
   p.unit = reinterpret_cast<float*>(at + align256((blocks * pieces + 1) * 256));
-  p.sums = wide ? nullptr : p.unit + align256(rows * 4) / 4;
   return p;
 }
 
 // a: the pairs, if SORTED
 template <typename T, int CP, bool SORTED>
-cudaError_t launch_split(bool dependent, int group, int rows, int K, const T* x, const Split& p,
+cudaError_t launch_split(bool dependent, int rows, int K, const T* x, const Split& p,
                          const Args& a, cudaStream_t s) {
   const int blocks = w4_blocks(K);
-  auto k = group == 32   ? w4_split_kernel<T, 1, CP, SORTED>
-           : group == 64 ? w4_split_kernel<T, 2, CP, SORTED>
-                         : w4_split_kernel<T, 4, CP, SORTED>;
+  auto k = w4_split_kernel<T, CP, SORTED>;
   const dim3 grid(static_cast<unsigned>(rows)), block(kSplitWarps * 32);
   if (dependent)
-    return launch_dependent(k, grid, block, 0, s, K, blocks, x, p.x, p.unit, p.sums, a);
-  k<<<grid, block, 0, s>>>(K, blocks, x, p.x, p.unit, p.sums, a);
+    return launch_dependent(k, grid, block, 0, s, K, blocks, x, p.x, p.unit, a);
+  k<<<grid, block, 0, s>>>(K, blocks, x, p.x, p.unit, a);
   return cudaGetLastError();
 }
 
@@ -299,7 +284,7 @@ size_t w4_linear_scratch_most(int64_t rows, int N, int K) {
 cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* x, const W4& W,
                              void* y, int y_dtype, void* scratch, int* err, cudaStream_t s) {
   const LinearShape L = linear_shape(rows, N, K);
-  const Split xs = split_at(static_cast<char*>(scratch), L.rows, K, 1, L.way.wide);
+  const Split xs = split_at(static_cast<char*>(scratch), L.rows, K, 1);
   float* part =
       reinterpret_cast<float*>(static_cast<char*>(scratch) + split_bytes(L.rows, K, 1));
   const int out_f32 = y_dtype == MOE_F32;
@@ -308,11 +293,10 @@ cudaError_t launch_w4_linear(int64_t rows, int N, int K, int group, const void* 
     void* out = static_cast<char*>(y) + r * N * (out_f32 ? 4 : 2);
     Args a = {};
     cudaError_t st = launch_split<__nv_bfloat16, 1, false>(
-        false, group, m, K, static_cast<const __nv_bfloat16*>(x) + r * K, xs, a, s);
+        false, m, K, static_cast<const __nv_bfloat16*>(x) + r * K, xs, a, s);
     if (st != cudaSuccess) return st;
     a.x = xs.x;
     a.unit = xs.unit;
-    a.sums = xs.sums;
     a.rows = m;
     a.err = err;
     a.w0 = a.w1 = W;
@@ -359,11 +343,11 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
   const ExpertsShape S = experts_shape(T, h, E, k, f);
   char* at = static_cast<char*>(scratch);
   const int x_rows = S.way1.wide ? S.pairs : S.tokens;
-  const Split xs = split_at(at, x_rows, h, 1, S.way1.wide);
+  const Split xs = split_at(at, x_rows, h, 1);
   at += split_bytes(x_rows, h, 1);
   float* hidden = reinterpret_cast<float*>(at);
   at += align256(static_cast<size_t>(S.pairs) * f * 4);
-  const Split hs = split_at(at, S.pairs, f, 2, S.way2.wide);
+  const Split hs = split_at(at, S.pairs, f, 2);
   at += split_bytes(S.pairs, f, 2);
   float* part = reinterpret_cast<float*>(at);
   for (int t = 0; t < T; t += S.tokens) {
@@ -378,12 +362,11 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     a.err = err;
     const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(x) + static_cast<int64_t>(t) * h;
     cudaError_t st =
-        S.way1.wide ? launch_split<__nv_bfloat16, 1, true>(false, group, n * k, h, in, xs, a, s)
-                    : launch_split<__nv_bfloat16, 1, false>(false, group, n, h, in, xs, a, s);
+        S.way1.wide ? launch_split<__nv_bfloat16, 1, true>(false, n * k, h, in, xs, a, s)
+                    : launch_split<__nv_bfloat16, 1, false>(false, n, h, in, xs, a, s);
     if (st != cudaSuccess) return st;
     a.x = xs.x;
     a.unit = xs.unit;
-    a.sums = xs.sums;
     a.w0 = W1;
     a.w1 = W3;
     a.blocks = w4_blocks(h);
@@ -395,11 +378,10 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
     st = launch_fc1(group, h, S.way1.wide, a, s);
     if (st != cudaSuccess) return st;
     // rows of dropped pairs hold nothing; nobody reads their pieces
-    st = launch_split<float, 2, false>(true, group, n * k, f, hidden, hs, a, s);
+    st = launch_split<float, 2, false>(true, n * k, f, hidden, hs, a, s);
     if (st != cudaSuccess) return st;
     a.x = hs.x;
     a.unit = hs.unit;
-    a.sums = hs.sums;
     a.w0 = a.w1 = W2;
     a.blocks = w4_blocks(f);
     a.groups = f / group;

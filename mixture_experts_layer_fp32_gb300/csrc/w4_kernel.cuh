@@ -2,23 +2,29 @@
 // fewest rows, and how a product is shared out between kernels, parts and warps.
 //
 // y = x W^T with few rows of x reads every weight once and should be bound by
-// that stream.  What stands in the way is the work per code.  Making numbers of
-// the codes the usual way (bf16 128 + q, less 128 + zero) takes 11 instructions
-// for 8 of them, and the kernel that did so ran at a third of the memory's
-// rate.  Here nothing is converted: the 16 bits 0x000q ARE the fp16 number
-// q 2^-24 (a subnormal), and 0x00q0 is q 2^-20, so a word of 8 codes becomes
-// four A registers of mma.sync m16n8k16 by four masks and one shift.  Every
-// second pair of inputs has its 16 taken out of x beforehand.
+// that stream.  What stands in the way is the work per code.  The fp16 number
+// with the bits 0x640q is 1024 + q, and 0x64q0 is 1024 + 16 q, so a word of 8
+// codes becomes four pairs of numbers by four masks with an or (one instruction:
+// as two, the experts of one token took 53.7 us for 46.8) and one shift, and four
+// subtractions of 1024 + z and 1024 + 16 z make q - z and 16 (q - z) of them, the
+// A registers of mma.sync m16n8k16.  Every second pair of inputs has the 16 taken
+// out of x beforehand.
 //
-// For that the rows of x are brought to fp16 once (w4_split_kernel): with a
-// power of two for each row a bf16 number is exact (down to 2^-28 of its row's
-// largest), and an fp32 hidden value is two fp16 numbers, a column each, exact
-// to 2^-22.  The products are exact, their sums are fp32, and what the zero
-// point adds is taken off a group's sum: s (sum q x - z sum x).
+// The subtractions could be spared: 0x000q is the subnormal q 2^-24, and a zero
+// point's share is z times the sum of x.  But the tensor cores add products up
+// under the largest exponent, and behave as if a subnormal's were 2^-14: up to 10
+// bits of the small products beside a large one were lost (rows with values 1000
+// times the others came out 1e-5 off in the mean, 1e-7 now; the hidden values'
+// product 3e-6, and 2e-7 now), while the time is the same.
+//
+// The rows of x are brought to fp16 once (w4_split_kernel): with a power of two
+// for each row a bf16 number is exact (down to 2^-27 of its row's largest), and an
+// fp32 hidden value is two fp16 numbers, a column each, exact to 2^-22.  The
+// products are exact and their sums are fp32.
 //
 // (E4M3 operands would need two masks and one shift, but mma.sync of that type
 // costs this machine several instructions: 194 were issued for a block of
-// 16 x 128 codes against 75.)
+// 16 x 128 codes.)
 //
 // Measured, with the rows' split and the combine (rate of the codes and scales):
 // a row of 4096 x 4096 6.2 us; 8 rows of 57344 x 4096 27.5 us (4.4 TB/s); the
@@ -50,11 +56,9 @@ __host__ __device__ constexpr int pieces_of(int mode) { return mode == FC2 ? 2 :
 struct Args {
   // The split rows, of tokens in the narrow FC1, of the pairs sorted by expert in
   // the wide one: fp16 [x_rows][pieces][blocks * 128], the inputs 2, 3, 6 and 7
-  // of eight over 16; each row's unit; and each group's sum of x in it,
-  // [x_rows][blocks * groups of a block]
+  // of eight over 16; and each row's unit
   const __half* x;
   const float* unit;
-  const float* sums;
   W4 w0, w1;              // FC1: W1 and W3 (rows g and g + 8 of a tile); else w0 twice
   int blocks, groups;     // of 128 inputs; groups of a row
   int N, tiles;           // outputs of an expert, its tiles
@@ -64,7 +68,7 @@ struct Args {
   int each, each_rest;    // their units, in a part of split_units and of one more
   int chunk_rows;         // rows of x of a chunk
   bool few;               // wide: chunks of 32 columns
-  int x_pitch, s_pitch;   // narrow: bytes of a column of x and of a row's sums in shared memory
+  int x_pitch;            // narrow: bytes of a column of x in shared memory
   int rows;               // LINEAR: rows of x
   int out_f32;            // LINEAR
   void* out;              // LINEAR: y or partial sums; FC1: hidden values; FC2: partial sums
@@ -95,18 +99,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
                : "r"(at)
                : "memory");
   return q;
-}
-
-__device__ __forceinline__ float2 lds8(uint32_t at) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ float lds4(uint32_t at) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
 }
 
 // Whether a barrier's phase ends within a second.
@@ -266,11 +258,10 @@ struct Item {
 template <int MODE>
 __device__ __forceinline__ void put(const Args& a, const Plan& plan, int part, int row_first, int r,
                                     int o, float low, float high) {
-  // the row's unit, and 2^24 for the codes' 2^-24
   const float unit =
       a.unit[MODE == FC1 ? static_cast<int>(plan.token[row_first + r]) : row_first + r];
-  low = low * 16777216.f * unit;
-  high = high * 16777216.f * unit;
+  low *= unit;
+  high *= unit;
   if (MODE == FC1) {
     static_cast<float*>(a.out)[static_cast<int64_t>(row_first + r) * a.N + o] =
         low / (1.f + expf(-low)) * high;
@@ -334,8 +325,8 @@ __device__ __forceinline__ float scale_of(const Scales<GPB>& v, int q) {
   return __uint_as_float(q & 1 ? v.s[q / 2] & 0xffff0000u : v.s[q / 2] << 16);
 }
 template <int GPB, bool ZEROS>
-__device__ __forceinline__ float zero_of(const Scales<GPB>& v, int q) {
-  return ZEROS ? static_cast<float>((v.z >> (8 * q)) & 255) : 8.f;
+__device__ __forceinline__ uint32_t zero_of(const Scales<GPB>& v, int q) {
+  return ZEROS ? (v.z >> (8 * q)) & 15u : 8u;
 }
 template <int GPB, bool ZEROS>
 __device__ __forceinline__ Scales<GPB> scales_from(const Scales<GPB>& v, int lane) {
@@ -345,36 +336,38 @@ __device__ __forceinline__ Scales<GPB> scales_from(const Scales<GPB>& v, int lan
   r.z = ZEROS ? __shfl_sync(~0u, v.z, lane) : 0;
   return r;
 }
-// consecutive groups' sums of x
-template <int N>
-struct Sums {
-  float v[N];
-};
-template <int N>
-__device__ __forceinline__ Sums<N> lds_sums(uint32_t at) {
-  Sums<N> r;
-  if (N == 1) {
-    r.v[0] = lds4(at);
-  } else if (N == 2) {
-    const float2 q = lds8(at);
-    r.v[0] = q.x;
-    r.v[N - 1] = q.y;
-  } else {
-    const uint4 q = lds16(at);
-    r.v[0] = __uint_as_float(q.x);
-    r.v[1 % N] = __uint_as_float(q.y);
-    r.v[2 % N] = __uint_as_float(q.z);
-    r.v[N - 1] = __uint_as_float(q.w);
-  }
-  return r;
+// Codes as fp16 pairs: of a word's inputs 0 1, 2 3, 4 5, 6 7 the numbers 1024 + q,
+// 1024 + 16 q, 1024 + q, 1024 + 16 q; less the same of the zero point, which is
+// exact (whole numbers below 2048).
+__device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
+  const __half2 d = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
-// a word's inputs 0 1, 2 3 (times 16), 4 5, 6 7 (times 16) as fp16 pairs
-__device__ __forceinline__ void pairs_of(uint32_t word, uint32_t (&p)[4]) {
+struct ZeroPair {
+  uint32_t one, sixteen;
+};
+__device__ __forceinline__ ZeroPair zero_pair(uint32_t z) {
+  return {0x64006400u + z * 0x00010001u, 0x64006400u + z * 0x00100010u};
+}
+// (word & MASK) | base in one instruction, which takes one constant: base is held
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t masked(uint32_t word, uint32_t base) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(word), "n"(MASK), "r"(base));
+  return d;
+}
+__device__ __forceinline__ uint32_t held_1024() {
+  uint32_t v;
+  asm("mov.b32 %0, 0x64006400;" : "=r"(v));
+  return v;
+}
+__device__ __forceinline__ void pairs_of(uint32_t word, uint32_t base, const ZeroPair& z,
+                                         uint32_t (&p)[4]) {
   const uint32_t high = word >> 8;
-  p[0] = word & 0x000f000fu;
-  p[1] = word & 0x00f000f0u;
-  p[2] = high & 0x000f000fu;
-  p[3] = high & 0x00f000f0u;
+  p[0] = less(masked<0x000f000fu>(word, base), z.one);
+  p[1] = less(masked<0x00f000f0u>(word, base), z.sixteen);
+  p[2] = less(masked<0x000f000fu>(high, base), z.one);
+  p[3] = less(masked<0x00f000f0u>(high, base), z.sixteen);
 }
 
 // Up to 8 columns (8 rows of x; FC2: 4) to a chunk.  A tile is 16 outputs (FC1:
@@ -388,7 +381,7 @@ __device__ __forceinline__ void pairs_of(uint32_t word, uint32_t (&p)[4]) {
 //
 // A wait that runs out reports it and the warp goes on with what is there, so that
 // nobody waits for it, but copies nothing more; the block ends after its copies.
-constexpr int kNarrowX = 66 * 1024;  // bytes of x and its sums, at most
+constexpr int kNarrowX = 66 * 1024;  // bytes of x, at most
 
 template <int MODE, int G32, bool ZEROS, bool TAIL>
 __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
@@ -501,6 +494,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
   fetch();
   pdl_wait();  // the split rows
 
+  const uint32_t base = held_1024();
   int use = 0, phase = 0, buf = 0;  // the slot at hand and its barrier's phase
   const int x_row = a.blocks * (128 * CP);
   const uint32_t xs = ptx::smem_u32(x_at);
@@ -533,13 +527,6 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
         for (int i = warp % share * 32 + lane; i < blocks_in * 16; i += share * 32)
           copy_async(xs + c * a.x_pitch + i * 16, p + i * 8);
       }
-      const uint32_t ss = xs + a.chunk_rows * CP * a.x_pitch;
-      for (int r = W - 1 - warp; r < row_count; r += W) {
-        const float* p =
-            a.sums + (static_cast<int64_t>(row_of(r)) * a.blocks + first * SB) * GPB;
-        for (int i = lane; i < blocks_in * GPB; i += 32)
-          copy_async4(ss + r * a.s_pitch + i * 4, p + i);
-      }
       copies_commit();
       copies_wait<0>();
     }
@@ -547,17 +534,12 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
     // columns past the chunk's repeat its first and are not stored; a lane's sums
     // are of the columns 2t, 2t + 1
     const uint32_t x_lane = xs + (g < row_count * CP ? g : 0) * a.x_pitch + t * 16;
-    uint32_t s_lane[XR];
-#pragma unroll
-    for (int i = 0; i < XR; ++i)
-      s_lane[i] = xs + a.chunk_rows * CP * a.x_pitch +
-                  (XR * t + i < row_count ? XR * t + i : 0) * a.s_pitch;
 
     while (at_hand < to) {
       float acc[2][XR];  // of the outputs g and g + 8
 #pragma unroll
       for (int i = 0; i < XR; ++i) acc[0][i] = acc[1][i] = 0.f;
-      auto block = [&](uint32_t src, uint32_t xb, int k, const Scales<GPB>& st0,
+      auto block = [&](uint32_t src, uint32_t xb, const Scales<GPB>& st0,
                        const Scales<GPB>& st1, int b) {
         constexpr uint32_t kBlock = MODE == FC1 ? 512 : 1024;
         constexpr uint32_t kSecond = MODE == FC1 ? kStage / 2 : 512;
@@ -565,17 +547,16 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
         const uint32_t c0[4] = {q0.x, q0.y, q0.z, q0.w}, c1[4] = {q1.x, q1.y, q1.z, q1.w};
         const Scales<GPB> s0 = scales_from<GPB, ZEROS>(st0, (lane & ~3) + b);
         const Scales<GPB> s1 = scales_from<GPB, ZEROS>(st1, (lane & ~3) + b);
-        Sums<GPB> sx[XR];
-#pragma unroll
-        for (int i = 0; i < XR; ++i) sx[i] = lds_sums<GPB>(s_lane[i] + (k + b) * (GPB * 4));
 #pragma unroll
         for (int q = 0; q < GPB; ++q) {
+          const ZeroPair z0 = zero_pair(zero_of<GPB, ZEROS>(s0, q));
+          const ZeroPair z1 = zero_pair(zero_of<GPB, ZEROS>(s1, q));
           float sum[4];
 #pragma unroll
           for (int j = q * G32; j < (q + 1) * G32; ++j) {
             uint32_t p0[4], p1[4];
-            pairs_of(c0[j], p0);
-            pairs_of(c1[j], p1);
+            pairs_of(c0[j], base, z0, p0);
+            pairs_of(c1[j], base, z1, p1);
             const uint4 x = lds16(xb + b * 256 + j * 64);
             if (j == q * G32) mma_first(sum, p0[0], p1[0], p0[1], p1[1], x.x, x.y);
             else mma(sum, p0[0], p1[0], p0[1], p1[1], x.x, x.y);
@@ -583,13 +564,12 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float s = scale_of(i ? s1 : s0, q), z = zero_of<GPB, ZEROS>(i ? s1 : s0, q);
+            const float s = scale_of(i ? s1 : s0, q);
             if (CP == 2) {  // the second piece is in 2^-11 of the first's unit
-              acc[i][0] +=
-                  s * (sum[2 * i] + 0.00048828125f * sum[2 * i + 1] - z * sx[0].v[q]);
+              acc[i][0] += s * (sum[2 * i] + 0.00048828125f * sum[2 * i + 1]);
             } else {
-              acc[i][0] += s * (sum[2 * i] - z * sx[0].v[q]);
-              acc[i][XR - 1] += s * (sum[2 * i + 1] - z * sx[XR - 1].v[q]);
+              acc[i][0] += s * sum[2 * i];
+              acc[i][XR - 1] += s * sum[2 * i + 1];
             }
           }
         }
@@ -618,10 +598,10 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) w4_narrow_kernel(
         const uint32_t src = ring + use * kStage + lane * 16, xb = x_lane + k * 256;
         if (blocks == SB) {
 #pragma unroll
-          for (int b = 0; b < SB; ++b) block(src, xb, k, st0, st1, b);
+          for (int b = 0; b < SB; ++b) block(src, xb, st0, st1, b);
         } else {
 #pragma unroll 1
-          for (int b = 0; b < blocks; ++b) block(src, xb, k, st0, st1, b);
+          for (int b = 0; b < blocks; ++b) block(src, xb, st0, st1, b);
         }
         phase ^= use;
         use ^= 1;
@@ -709,19 +689,16 @@ inline int splits_of(int64_t chunks, int N, int blocks, int join, bool wide) {
   return best;
 }
 
-// The narrow kernel's x: bytes of a column and of a row's sums of the longest
-// part; the columns' starts fall on the banks' halves in turn.
+// The narrow kernel's x: bytes of a column of the longest part; the columns' starts
+// fall on the banks' halves in turn.
 inline int part_blocks(int blocks, int splits) {
   return ((blocks + 3) / 4 + splits - 1) / splits * 4;
 }
 inline int narrow_x_pitch(int blocks, int splits) { return part_blocks(blocks, splits) * 256 + 64; }
-inline int narrow_s_pitch(int blocks, int splits) { return part_blocks(blocks, splits) * 16 + 16; }
 // rows that a chunk of the narrow kernel can have; 0: none fits
 inline int narrow_rows(int mode, int blocks, int splits) {
   const int cp = pieces_of(mode);
-  const int64_t fit =
-      kNarrowX / (static_cast<int64_t>(cp) * narrow_x_pitch(blocks, splits) +
-                  narrow_s_pitch(blocks, splits));
+  const int64_t fit = kNarrowX / (static_cast<int64_t>(cp) * narrow_x_pitch(blocks, splits));
   return static_cast<int>(fit < 8 / cp ? fit : 8 / cp);
 }
 
@@ -758,7 +735,6 @@ cudaError_t launch_narrow(Args a, cudaStream_t s) {
       !map_codes(&m1, a.w1.codes, all, a.blocks, MODE == FC1 ? 8 : 16, false))
     return cudaErrorInvalidValue;
   a.x_pitch = narrow_x_pitch(a.blocks, a.splits);
-  a.s_pitch = narrow_s_pitch(a.blocks, a.splits);
   // no more blocks than the longest share of the items asks for: each holds x
   // (512 items: 128 blocks of 4 and not 152 of 3 or 4, 43.9 us instead of 45.8
   // for the experts of one token, 8 x 4096 x 14336)

@@ -6,12 +6,9 @@
 // 128 inputs
 //   - TMA brings the tiles' codes (two blocks of inputs in a copy) and x;
 //   - four warps a tile turn a row's 64 bytes of codes, a row to a thread, into
-//     fp16 differences q - zero in the tensor memory, the A operand: masks of the
-//     words as in the narrow kernel, and one exact subtraction of subnormals for
-//     two codes.  (The narrow kernel takes the zeros off a group's sum instead:
-//     there a sum belongs to 8 columns and here to 64, so there the sums are the
-//     cheaper place and here the codes are.)  Two slots, with warps of their own
-//     each: one set of warps took 237 us where two take 215 (below);
+//     fp16 differences q - zero in the tensor memory, the A operand, as the narrow
+//     kernel does in registers.  Two slots, with warps of their own each: one set of
+//     warps took 237 us where two take 215 (below);
 //   - one thread multiplies, a fresh sum for each group of inputs;
 //   - eight warps, an output of both tiles to a thread and half the columns each,
 //     read the groups' sums back and add them up under their scales in fp32.
@@ -166,11 +163,6 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(one));
   return one != 0;
-}
-
-__device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
-  const __half2 d = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&d);
 }
 
 template <int MODE, int G32>
@@ -349,16 +341,15 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
           }
           ring.next();
         }
-        // 2^24 for the codes' 2^-24, then the row's unit: that is up to 2^113, and the
-        // two together pass the range of fp32.  Rows past the last one are worked out
-        // too and not stored: no branch stands between one and the next.
+        // Rows past the last one are worked out too and not stored: no branch stands
+        // between one and the next.
         copies_wait<0>();
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const float unit = units[warp][i];
-          acc[0][i] = acc[0][i] * 16777216.f * unit;
-          acc[1][i] = acc[1][i] * 16777216.f * unit;
+          acc[0][i] *= unit;
+          acc[1][i] *= unit;
           if (MODE == FC1) acc[0][i] = acc[0][i] / (1.f + expf(-acc[0][i])) * acc[1][i];
         }
         __syncwarp();
@@ -405,6 +396,7 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
     const uint32_t src = base + d * (kTallStage / 2) + r * 64;
     const uint32_t swap = ((r >> 1) & 3) << 4;
     const uint32_t a_slot = a_at(d, slot) + lanes;
+    const uint32_t held = held_1024();
     Ring code{kTallStages};
     int turn = 0, phase = 0;  // the slot of the block to come; this slot's phase
     bool on = true;
@@ -440,17 +432,14 @@ __global__ void __launch_bounds__(kTallRoles * 32, 1)
           ptx::tc_fence_after();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // inputs 32 j ..
-            const uint32_t zero = (z >> (8 * (j / G32))) & 15u;
-            const uint32_t z0 = zero * 0x00010001u, z1 = z0 << 4;
+            const ZeroPair zero = zero_pair((z >> (8 * (j / G32))) & 15u);
             uint32_t v[16];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t p[4];
-              pairs_of(j == 0 ? q[c].x : j == 1 ? q[c].y : j == 2 ? q[c].z : q[c].w, p);
-              v[c * 4 + 0] = less(p[0], z0);
-              v[c * 4 + 1] = less(p[1], z1);
-              v[c * 4 + 2] = less(p[2], z0);
-              v[c * 4 + 3] = less(p[3], z1);
+              pairs_of(j == 0 ? q[c].x : j == 1 ? q[c].y : j == 2 ? q[c].z : q[c].w, held, zero, p);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[c * 4 + i] = p[i];
             }
             tmem_st16(a_slot + j * 16, v);
           }

@@ -10,8 +10,8 @@ from test_gpu_w4 import _routing
 
 pytestmark = pytest.mark.gpu
 
-# of a row's values; the unit of a row is clamped below 2^-112, and times the
-# codes' 2^24 it passes the fp32 range from 2^118 on
+# of a row's values; the unit of a row is clamped below 2^-112, and from 2^118 on
+# it leaves no room for another factor of 2^24 in fp32
 LOW = [-133, -130, -126, -120, -114, -113, -112, -111, -110, -100, -60]
 HIGH = [60, 100, 103, 104, 110, 116, 117, 118, 119, 120, 125, 127]
 
