@@ -197,9 +197,15 @@ def _host(t):
     return t.data_ptr()
 
 
+# The current stream's handle without the object around it (0.3 us, not 3); the name
+# is not a public one, so a torch without it takes the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    # the current stream's handle without the object around it (0.3 us, not 3)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _ws(ws):
