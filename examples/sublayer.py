@@ -46,7 +46,7 @@ def train_step(cfg, h, d_out, weights, norm, p, rng, saved, grads, ws, norm_ws):
 
 
 class Decoder:
-    """Buffers and 4-bit weights of decode_step for up to cfg's tokens."""
+    """Buffers and 4-bit weights of decode_step for cfg's number of tokens."""
 
     def __init__(self, cfg, Wg, experts, norms, head):
         self.cfg, self.Wg, self.experts, self.norms, self.head = cfg, Wg, experts, norms, head

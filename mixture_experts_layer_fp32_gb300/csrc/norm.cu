@@ -162,11 +162,11 @@ __global__ void __launch_bounds__(kRowThreads)
 // 4096 27.5 us (4.9 TB/s, of 6.8 that a copy reaches), with dropout and residual
 // 59.6 us (4.5 TB/s); backward 16384 x 4096 90 us (4.5 TB/s), with dropout 138 us
 // (4.9 TB/s); fp32 forward 4096 x 4096 25.7 us (5.2), backward 8192 x 4096 70 us
-// (5.7).  Beside the memory, reads of the parameters from shared memory and the
-// instructions for 8 values in 16 bytes bound bf16; the generator's rounds, at
-// least 80 cycles of an SM quarter for 128 elements, bound the dropout.  Odd
-// widths (8192 x 4099: 42 us, backward 86) pay for edge vectors and an odd number
-// of warps.
+// (5.7).  No unit is full in bf16 (with dropout the issue slots and the fp32 pipe
+// 55-59%, the memory 52-72%): a row's reads, its parameters from shared memory, the
+// generator's rounds (at least 80 cycles of an SM quarter for 128 elements) and its
+// sums follow one another in the few warps that hold it.  Odd widths (8192 x 4099:
+// 42 us, backward 86) pay for edge vectors and an odd number of warps.
 
 template <typename T>
 struct Lanes {

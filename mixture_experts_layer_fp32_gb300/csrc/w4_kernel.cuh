@@ -27,14 +27,14 @@
 // 16 x 128 codes.)
 //
 // Measured, with the rows' split and the combine (rate of the codes and scales):
-// a row of 4096 x 4096 6.2 us; 8 rows of 57344 x 4096 27.5 us (4.4 TB/s); the
-// experts of one token (2 of 8 of 4096 x 14336) 42.4 us (4.3 TB/s), of 16 tokens
-// (8 of 128 of 4096 x 1536) 166 us (5.0 TB/s, 74% of what a copy reaches).  What
-// bounds it is instructions: the tensor pipe of mma.sync, masks and loads of x
-// share the warps' issue slots, which are 40% used while the memory waits at the
-// ends of items; a second block to an SM does not fit the registers.  Two chains
-// of products in a warp, or a warp's stages next to its neighbours' instead of in
-// runs, made no difference.
+// a row of 4096 x 4096 6.0 us; 8 rows of 57344 x 4096 25.0 us (4.9 TB/s); the
+// experts of one token (2 of 8 of 4096 x 14336) 43.7 us (4.2 TB/s), of 16 tokens
+// (8 of 128 of 4096 x 1536) 164 us (5.0 TB/s, 74% of what a copy reaches).  No unit
+// is full: the issue slots are used to 36-58%, the shared memory to 42-60%, the
+// tensor pipe to 14-28%; a warp's reads, masks and products follow one another,
+// the memory waits at the ends of items, and a second block to an SM does not fit
+// the registers.  Two chains of products in a warp, or a warp's stages next to its
+// neighbours' instead of in runs, made no difference.
 #pragma once
 
 #include "sm100_ptx.cuh"
@@ -797,10 +797,10 @@ cudaError_t launch_mode(int group, int K, bool wide, const Args& a, cudaStream_t
 
 // How a product of about `rows` rows of x (of an expert), `chunks` of them (of
 // the experts hit) and N outputs is run.  The narrow kernel for as few rows as
-// it can hold: 8 rows take it 11.6 us at 14336 x 4096, 16.6 at 14336 x 7168 and
-// 27.5 at 57344 x 4096, and the wide one, which is nearly the same from one row
-// to 16, takes 15.1, 27.5 and 34.9.  For 16 rows the narrow one would read the
-// weights twice.  join: see splits_of, negative: no splits.
+// it can hold: 8 rows take it 10.2 us at 14336 x 4096, 15.7 at 14336 x 7168 and
+// 25.0 at 57344 x 4096, and the wide one, which is nearly the same from one row
+// to 16, takes 14.7, 21.6 and 33.9 for 9.  For 16 rows the narrow one would read
+// the weights twice.  join: see splits_of, negative: no splits.
 struct Way {
   bool wide, few;
   int splits;

@@ -16,17 +16,18 @@
 // wait runs out reports it, and then every warp leaves its loop; the block's copies
 // and products end (again within a limit) before its tensor memory is freed.
 //
-// Measured, the experts of 64 tokens (2 of 8 of 4096 x 14336, zero points): 198 us
-// with the splits and the combine; FC1 122 and FC2 81 us cold.  mma.sync from
+// Measured, the experts of 64 tokens (2 of 8 of 4096 x 14336, zero points): 194 us
+// with the splits and the combine; FC1 117 and FC2 78 us cold.  mma.sync from
 // registers took 453 us: every warp read the whole x for its 32 outputs, and the
 // conversion, the products and the scaling waited for one another within a warp.
-// What bounds it now is instructions: 780 are issued by an SM quarter for 16 KB of
-// codes, 63% of its slots, half of them masks and subtractions; the products
-// alone, whose A operand of 4 KB takes some 33 cycles to read whatever the number
-// of columns, would take 530 of the 1240 cycles.
+// What is used most now is the issue slots: 740 instructions of an SM quarter for
+// 16 KB of codes, 62% of its slots, half of them masks and subtractions; the
+// products alone, whose A operand of 4 KB takes some 33 cycles to read whatever the
+// number of columns, would take 530 of the 1190 cycles.
 //
-// Tried and left: the next item's scales and zeros loaded ahead (211 us), two
-// multiply-adds in an instruction (209), those lines brought into L2 ahead (203).
+// Tried and left: the next item's scales and zeros loaded ahead (211 us where the
+// kernel took 206), two multiply-adds in an instruction (209), those lines brought
+// into L2 ahead (203 where it took 198).
 #pragma once
 
 #include <type_traits>
