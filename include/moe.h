@@ -691,7 +691,7 @@ typedef struct moe_w4 {
  * rounded to the nearest code.  zeros NULL: symmetric, scale = max |w| / 7;
  * else scale = (max(w, 0) - min(w, 0)) / 15 and zero = round(-min(w, 0) / scale).
  * The codes are chosen against the rounded scale.  A group of zeros gets scale
- * 0.  N and K multiples of 64. */
+ * 0, one with an infinity or a NaN the scale NaN.  N and K multiples of 64. */
 moe_status moe_quantize_w4(int32_t experts, int32_t K, int32_t N, int32_t group, const void* W,
                            uint8_t* codes, void* scales, uint8_t* zeros, moe_stream_t stream);
 /* values [experts, N, K] (one byte each, its low four bits) -> codes; the codes

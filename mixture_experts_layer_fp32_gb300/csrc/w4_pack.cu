@@ -22,12 +22,14 @@ __global__ void __launch_bounds__(256)
   __syncthreads();
   if (ty == 0) {
     float lo = 0.f, hi = 0.f;
+    bool good = true;  // (the minimum and the maximum drop a NaN)
     for (int k = 0; k < group; ++k) {
       lo = fminf(lo, tile[k][tx]);
       hi = fmaxf(hi, tile[k][tx]);
+      good &= isfinite(tile[k][tx]);
     }
-    const __nv_bfloat16 s16 =
-        __float2bfloat16_rn(zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f);
+    const float range = zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
+    const __nv_bfloat16 s16 = __float2bfloat16_rn(good ? range : __uint_as_float(0x7fffffffu));
     const float s = __bfloat162float(s16);
     float z = 8.f;
     if (zeros) z = s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;
