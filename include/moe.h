@@ -743,6 +743,37 @@ moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, c
                           float* topk_prob, int32_t* tokens_per_expert, void* ws,
                           size_t ws_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A decoding step: the whole layer for a few tokens.  The conventions at the top
+ * hold (contiguous, 16-byte aligned, asynchronous).
+ * ------------------------------------------------------------------------- */
+
+/*
+ * The layer forward of moe_forward (fs = 0; W1s, W3s, W2s NULL) or of
+ * moe_forward_shared (fs > 0) for up to MOE_FEW_MAX_TOKENS tokens, in one kernel
+ * launch that reads the weights of the experts that are hit once: router, capacity
+ * drops, SwiGLU experts, shared expert, combine.  Arguments and their limits are
+ * those of the two; more tokens are MOE_ERR_UNSUPPORTED.  Routing follows the same
+ * formulas in fp32.  pad_to_capacity changes nothing here (padding rows carry no
+ * weight): tokens_per_expert counts kept pairs.  With bf16 the hidden values are
+ * not rounded to bf16 between the products (they enter the second one as two
+ * bf16 numbers each), sums are fp32, y is rounded once; repeats give equal bits.
+ * y may be x.  A token whose logits are NaN is reported in ws (moe_check).
+ * The kernel takes every SM's shared memory and its blocks wait for one another
+ * (a cooperative launch; waits that run out are reported in ws): a call whose
+ * other work on the GPU never ends does not begin.
+ *   ws: moe_workspace_size_few bytes; a workspace of cfg's num_tokens serves
+ *   every call of fewer tokens too.
+ */
+#define MOE_FEW_MAX_TOKENS 64
+moe_status moe_workspace_size_few(const moe_config* cfg, int32_t fs, size_t* bytes);
+moe_status moe_forward_few(const moe_config* cfg, int32_t fs, const void* x, const float* Wg,
+                           const float* gate_bias, const float* expert_bias, const void* W1,
+                           const void* W3, const void* W2, const void* W1s, const void* W3s,
+                           const void* W2s, void* y, int32_t* topk_idx, float* topk_prob,
+                           int32_t* tokens_per_expert, void* ws, size_t ws_bytes,
+                           moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

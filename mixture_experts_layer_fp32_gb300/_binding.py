@@ -38,7 +38,8 @@ EXPORTS = ["moe_abi_version", "moe_status_string", "moe_last_cuda_error", "moe_c
            "moe_layer_norm", "moe_workspace_size_norm_backward", "moe_layer_norm_backward",
            "moe_dropout_add", "moe_quantize_w4", "moe_pack_w4", "moe_workspace_size_linear_w4",
            "moe_linear_w4", "moe_workspace_size_experts_w4", "moe_experts_w4",
-           "moe_workspace_size_w4", "moe_forward_w4"]
+           "moe_workspace_size_w4", "moe_forward_w4", "moe_workspace_size_few",
+           "moe_forward_few"]
 
 NORM = {"layer": 0, "rms": 1}
 
@@ -151,6 +152,8 @@ def lib():
             "moe_workspace_size_w4": ([cfgp, ctypes.POINTER(sz)], i32),
             "moe_forward_w4": ([cfgp, i32, vp, vp, vp, vp, w4p, w4p, w4p, vp, vp, vp, vp, vp, sz,
                                 vp], i32),
+            "moe_workspace_size_few": ([cfgp, i32, ctypes.POINTER(sz)], i32),
+            "moe_forward_few": ([cfgp, i32] + [vp] * 14 + [vp, sz, vp], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -921,6 +924,46 @@ def forward_w4(cfg, x, Wg, gate_bias, expert_bias, q, y, ws, topk_idx=None, topk
                                 _table(topk_prob, T, k, f32, "topk_prob"),
                                 _vec(tokens_per_expert, E, i32, "tokens_per_expert"), b, wb,
                                 _stream()), "moe_forward_w4")
+
+
+# ---------------------------------------------------------------- a decoding step
+
+FEW_MAX_TOKENS = 64
+
+
+def workspace_size_few(cfg, fs=0):
+    v = ctypes.c_size_t()
+    _check(lib().moe_workspace_size_few(ctypes.byref(cfg), int(fs), ctypes.byref(v)),
+           "moe_workspace_size_few")
+    return v.value
+
+
+def alloc_workspace_few(cfg, fs=0, device="cuda"):
+    return torch.zeros(workspace_size_few(cfg, fs), dtype=torch.uint8, device=device)
+
+
+def forward_few(cfg, x, Wg, gate_bias, expert_bias, W1, W3, W2, y, ws, topk_idx=None,
+                topk_prob=None, tokens_per_expert=None, shared=None):
+    """The layer forward of up to FEW_MAX_TOKENS tokens in one launch; shared: the
+    shared expert's (W1s, W3s [h,fs], W2s [fs,h]) or None."""
+    T, k, h, E, f, dt = (cfg.num_tokens, cfg.topk, cfg.hidden, cfg.num_experts, cfg.ffn_hidden,
+                         act_dtype(cfg))
+    f32, i32 = torch.float32, torch.int32
+    s1 = s3 = s2 = None
+    fs = 0
+    if shared is not None:
+        s1, s3, s2 = shared
+        fs = s1.shape[-1]
+    b, wb = _ws(ws)
+    _check(lib().moe_forward_few(
+        ctypes.byref(cfg), fs, _table(x, T, h, dt, "x"), _table(Wg, h, E, f32, "Wg"),
+        _vec(gate_bias, E, f32, "gate_bias"), _vec(expert_bias, E, f32, "expert_bias"),
+        _table(W1, E * h, f, dt, "W1"), _table(W3, E * h, f, dt, "W3"),
+        _table(W2, E * f, h, dt, "W2"), _table(s1, h, fs, dt, "W1s"),
+        _table(s3, h, fs, dt, "W3s"), _table(s2, fs, h, dt, "W2s"), _table(y, T, h, dt, "y"),
+        _table(topk_idx, T, k, i32, "topk_idx"), _table(topk_prob, T, k, f32, "topk_prob"),
+        _vec(tokens_per_expert, E, i32, "tokens_per_expert"), b, wb, _stream()),
+        "moe_forward_few")
 
 
 def probe_fp32_fma(iters, out):

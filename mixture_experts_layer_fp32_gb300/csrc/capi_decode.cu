@@ -1,0 +1,90 @@
+// C ABI of a decoding step: the whole layer for a few tokens.  Argument checks and
+// workspace carve-up, as in capi.cu.
+#include "common.cuh"
+
+namespace {
+
+using namespace moe;
+
+#define MOE_TRY(expr)                      \
+  do {                                     \
+    const moe_status st_ = (expr);         \
+    if (st_ != MOE_OK) return st_;         \
+  } while (0)
+#define MOE_CUDA(expr) MOE_TRY(cuda_status(expr))
+
+moe_status need(const void* p, uint64_t nelem, size_t align = 16) {
+  if (nelem == 0) return MOE_OK;
+  return p == nullptr || reinterpret_cast<uintptr_t>(p) % align != 0 ? MOE_ERR_INVALID_ARG
+                                                                     : MOE_OK;
+}
+moe_status optional(const void* p, size_t align = 16) {
+  return reinterpret_cast<uintptr_t>(p) % align != 0 ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+moe_status check_ws(const void* ws, size_t have, size_t want) {
+  if (ws == nullptr || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return MOE_ERR_INVALID_ARG;
+  return have < want ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+void* past_error_word(void* ws) { return static_cast<char*>(ws) + kErrBytes; }
+
+// The layer's own checks of the configuration, then those of few tokens.
+moe_status validate_few(const moe_config* cfg, int32_t fs) {
+  size_t bytes = 0;
+  MOE_TRY(moe_workspace_size(cfg, &bytes));
+  if (fs < 0) return MOE_ERR_INVALID_ARG;
+  if (fs % (cfg->dtype == MOE_BF16 ? 128 : 8) != 0) return MOE_ERR_UNSUPPORTED;
+  if (cfg->num_tokens > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  // a row's inputs and all rows' inputs are counted in 32 bits
+  constexpr int32_t most = 1 << 21;
+  if (cfg->hidden > most || cfg->ffn_hidden > most || fs > most) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_workspace_size_few(const moe_config* cfg, int32_t fs, size_t* bytes) {
+  MOE_TRY(validate_few(cfg, fs));
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = kErrBytes + few_scratch(*cfg, fs);
+  return MOE_OK;
+}
+
+moe_status moe_forward_few(const moe_config* cfg, int32_t fs, const void* x, const float* Wg,
+                           const float* gate_bias, const float* expert_bias, const void* W1,
+                           const void* W3, const void* W2, const void* W1s, const void* W3s,
+                           const void* W2s, void* y, int32_t* topk_idx, float* topk_prob,
+                           int32_t* tokens_per_expert, void* ws, size_t ws_bytes,
+                           moe_stream_t stream) {
+  MOE_TRY(validate_few(cfg, fs));
+  const uint64_t T = cfg->num_tokens;
+  MOE_TRY(need(x, T));
+  MOE_TRY(need(Wg, 1));
+  MOE_TRY(optional(gate_bias, 4));
+  MOE_TRY(optional(expert_bias, 4));
+  MOE_TRY(need(W1, 1));
+  MOE_TRY(need(W3, 1));
+  MOE_TRY(need(W2, 1));
+  MOE_TRY(need(W1s, fs));
+  MOE_TRY(need(W3s, fs));
+  MOE_TRY(need(W2s, fs));
+  MOE_TRY(need(y, T));
+  MOE_TRY(optional(topk_idx, 4));
+  MOE_TRY(optional(topk_prob, 4));
+  MOE_TRY(optional(tokens_per_expert, 4));
+  MOE_TRY(check_ws(ws, ws_bytes, kErrBytes + few_scratch(*cfg, fs)));
+  int64_t capacity = -1;
+  MOE_TRY(moe_capacity(cfg, &capacity));
+  if (T == 0) {
+    if (tokens_per_expert != nullptr)
+      MOE_CUDA(cudaMemsetAsync(tokens_per_expert, 0, sizeof(int32_t) * cfg->num_experts, stream));
+    return MOE_OK;
+  }
+  MOE_CUDA(launch_few(*cfg, fs, capacity, x, Wg, gate_bias, expert_bias, W1, W3, W2, W1s, W3s, W2s,
+                      y, topk_idx, topk_prob, tokens_per_expert, past_error_word(ws),
+                      static_cast<int*>(ws), stream));
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -341,6 +341,19 @@ cudaError_t launch_w4_experts(int T, int h, int E, int k, int f, int group, cons
                               const uint8_t* keep, const W4& W1, const W4& W3, const W4& W2,
                               void* y, void* scratch, int* err, cudaStream_t s);
 
+// ---- the layer for few tokens (few.cu) ----
+constexpr int kFewBlocks = 152;    // of its grid at most: an SM each
+constexpr int kFewCounters = 32;   // words of a workspace's first 256 bytes: the grid's two
+size_t few_scratch(const moe_config& c, int fs);
+// capacity < 0: dropless; fs 0: no shared expert.  topk_idx, topk_prob and
+// tokens_per_expert are nullable.
+cudaError_t launch_few(const moe_config& c, int fs, int64_t capacity, const void* x,
+                       const float* Wg, const float* gate_bias, const float* expert_bias,
+                       const void* W1, const void* W3, const void* W2, const void* W1s,
+                       const void* W3s, const void* W2s, void* y, int32_t* topk_idx,
+                       float* topk_prob, int32_t* tokens_per_expert, void* scratch, int* err,
+                       cudaStream_t s);
+
 int device_sm_count();
 // keeps the text for moe_last_cuda_error() and returns the status
 moe_status cuda_status(cudaError_t e);

@@ -1,0 +1,1031 @@
+// The whole layer for a few tokens in one launch: router, capacity drops, SwiGLU
+// experts (and a shared expert), combine.
+//
+// At up to 64 tokens the layer is bound by reading the weights of the experts that
+// are hit, once: everything else has to stay out of that stream's way.  One
+// cooperative grid, a block to an SM, goes through
+//   0  logits: a block takes some features and up to 32 experts, partial sums out;
+//   1  top-k: a block takes a token, adds its partial sums up and chooses; then every
+//      block builds the same plan (rows by expert, drops) in its shared memory;
+//   2  FC1: the stream of all hit experts' W1 and W3, cut into equal runs of units;
+//   3  hidden values: the runs' partial sums added in order, silu(a) b;
+//   4  FC2: the stream of W2, cut the same way;
+//   5  combine: partial sums of a token's experts added in order, one rounding.
+// A block's part of both streams is one sequence of units, a unit the 4 KB of each
+// of its 8 warps: 32 (fp32: 16) inputs of 64 outputs.  A warp copies its own units
+// with cp.async into a ring of its own, up to kSlots - 1 units ahead, across the
+// steps 3 and 4 too: the weights do not depend on them, so memory stays busy while
+// the grid's barriers are passed.  No block waits for another within a step.
+//
+// bf16: mma.sync with the weights as the operand of 16 rows (ldmatrix.trans out of
+// the ring, whose 16-byte pieces are swapped so that it meets no bank twice) and 8
+// tokens as the columns.  The tensor cores' rate does not matter here (tcgen05 would
+// need 128 rows and its operands in another layout than the stream's): a unit feeds
+// 8 instructions for every 8 tokens.  The inputs of 32 are permuted between the
+// instructions so that a lane's share of x is 16 bytes in a row.  A hidden value
+// enters FC2 as two bf16 numbers (together within 2^-17 of it), so the layer has no
+// rounding between x and y but y's own.  fp32: FMAs, two outputs to a lane.
+//
+// All partial sums are added in an order given by sizes alone: repeats are equal
+// bit for bit.
+#include "topk.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kSlots = 6;                       // units of a warp's ring
+constexpr int kUnit = 4096;                     // bytes
+constexpr int kRing = kWarps * kSlots * kUnit;  // 192 KB
+constexpr int kTokens = MOE_FEW_MAX_TOKENS;
+constexpr int kPairs = kTokens * MOE_MAX_TOPK;
+constexpr int kRowsAtMost = kPairs + kTokens;
+constexpr int kChunk = 384;                     // features of the router's operands at a time
+constexpr int kColumns = 512;                   // a tile's outputs: 8 warps of 64
+// a grid barrier gives up after about a second
+constexpr long long kWaitCycles = 2000000000ll;
+
+static_assert(kChunk * (32 + kTokens) * 4 <= kRing, "router operands");
+
+struct Args {
+  int T, h, E, k, f, fs;
+  int score, groups, group_topk, capacity, policy;  // capacity < 0: no drops
+  const void *x, *W1, *W3, *W2, *V1, *V3, *V2;      // V: the shared expert's
+  const float *Wg, *gate_bias, *expert_bias;
+  void* y;
+  int32_t* idx_out;
+  float* prob_out;
+  int32_t* tpe_out;
+  // workspace
+  int* err;
+  int* bar;  // barrier count, blocks gone
+  float* logits;
+  int32_t* idx;
+  float* prob;
+  float* main;   // partial sums that begin a tile: rows x outputs
+  float* extra;  // those that go on with one: [block][T][512]
+  void* hid;     // [rows, f]; bf16: twice (the second pieces)
+  int64_t hid_lo;
+};
+
+struct Plan {
+  int pairs, rows, hits;             // routed rows, experts hit
+  int16_t expert[kPairs];            // -1: none
+  float prob[kPairs];
+  int16_t row_of[kPairs];            // -1: none
+  uint16_t token[kRowsAtMost];       // of a row (the shared expert's behind the routed)
+  int16_t hit_of_row[kRowsAtMost];
+  int16_t hit[MOE_MAX_EXPERTS];      // experts hit
+  int16_t first[MOE_MAX_EXPERTS + 1];  // their first rows
+  int16_t total[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS];
+  int16_t before[kWarps][MOE_MAX_EXPERTS];
+  uint8_t rank[kPairs];
+  float logit[MOE_MAX_EXPERTS], gsel[MOE_MAX_EXPERTS];
+  float part[kThreads];
+  int on, dropped;
+};
+
+// ------------------------------------------------------------------ the grid
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// The n-th barrier of all blocks.  false, for the whole block, where the wait ran out.
+__device__ bool grid_barrier(const Args& a, Plan& plan, int n) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(a.bar, 1);
+    const int want = n * static_cast<int>(gridDim.x);
+    const long long began = clock64();
+    int on = 1;
+    while (load_acquire(a.bar) < want)
+      if (clock64() - began > kWaitCycles) {
+        report_error(a.err, DEV_ERR_TIMEOUT, n);
+        on = 0;
+        break;
+      }
+    __threadfence();
+    plan.on = on;
+  }
+  __syncthreads();
+  return plan.on != 0;
+}
+
+// The last block to leave sets the counters back, a wait that ran out or not.
+__device__ void leave(const Args& a) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(a.bar + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+      a.bar[0] = 0;
+      a.bar[1] = 0;
+      __threadfence();
+    }
+  }
+}
+
+// ------------------------------------------------------------------ copies
+__device__ __forceinline__ uint32_t smem_at(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T>
+struct Form;
+template <>
+struct Form<__nv_bfloat16> {
+  static constexpr int kInputs = 32;  // of a unit
+  static constexpr int kPieces = 8;   // 16-byte pieces of 64 outputs
+  // rows read together by ldmatrix differ in bits 0, 3 and 4 of the input
+  __device__ static int place(int row, int piece) {
+    return row * 128 + ((piece ^ (((row >> 3) & 3) * 2 + (row & 1))) << 4);
+  }
+};
+template <>
+struct Form<float> {
+  static constexpr int kInputs = 16, kPieces = 16;
+  __device__ static int place(int row, int piece) { return row * 256 + (piece << 4); }
+};
+
+// ------------------------------------------------------------------ the streams
+// One product's stream: tiles of 512 outputs (FC1: 256 of W1 and the same of W3), an
+// expert's one after another, the shared expert's last; a tile's units follow the
+// inputs.  Block b of the first G has the units [S b / G, S (b + 1) / G).
+struct Stream {
+  int64_t S, begin, end;
+  int tiles, units;        // of a routed expert; of a tile
+  int routed;              // tiles of all of them
+  int shared_units;        // of one of the shared expert's tiles
+  int64_t routed_units;
+  int G;
+
+  __device__ void set(int hits, int tiles_, int units_, int shared_tiles, int shared_units_) {
+    tiles = tiles_, units = units_, shared_units = shared_units_;
+    routed = hits * tiles;
+    routed_units = static_cast<int64_t>(routed) * units;
+    S = routed_units + static_cast<int64_t>(shared_tiles) * shared_units;
+    // no more blocks than units, so that every block between two has some
+    G = static_cast<int>(min(S, static_cast<int64_t>(gridDim.x)));
+    const int b = min(static_cast<int>(blockIdx.x), G);
+    begin = G ? S * b / G : 0;
+    end = b < G ? S * (b + 1) / G : S;
+  }
+  __device__ void find(int64_t u, int& tile, int& unit) const {
+    if (u < routed_units) {
+      tile = static_cast<int>(u / units);
+      unit = static_cast<int>(u - static_cast<int64_t>(tile) * units);
+    } else {
+      const int64_t v = u - routed_units;
+      const int t = static_cast<int>(v / shared_units);
+      tile = routed + t;
+      unit = static_cast<int>(v - static_cast<int64_t>(t) * shared_units);
+    }
+  }
+  __device__ int units_of(int tile) const { return tile < routed ? units : shared_units; }
+  __device__ int block_of(int64_t u) const {
+    return static_cast<int>(((u + 1) * G - 1) / S);
+  }
+  // the blocks that have a tile's units
+  __device__ void blocks(int tile, int& first, int& last) const {
+    const int64_t u = tile < routed
+                          ? static_cast<int64_t>(tile) * units
+                          : routed_units + static_cast<int64_t>(tile - routed) * shared_units;
+    first = block_of(u);
+    last = block_of(u + units_of(tile) - 1);
+  }
+};
+
+// What a tile is: its expert (plan.hits: the shared one) and its place among the
+// expert's outputs.
+struct Tile {
+  int hit, at, rows, first;
+};
+__device__ __forceinline__ Tile tile_of(const Args& a, const Plan& plan, const Stream& s, int tile) {
+  Tile t;
+  if (tile < s.routed) {
+    t.hit = tile / s.tiles;
+    t.at = tile - t.hit * s.tiles;
+    t.first = plan.first[t.hit];
+    t.rows = plan.first[t.hit + 1] - t.first;
+  } else {
+    t.hit = plan.hits;
+    t.at = tile - s.routed;
+    t.first = plan.rows;
+    t.rows = a.T;
+  }
+  return t;
+}
+
+// A warp's copies: both streams' units in order.
+template <typename T>
+struct Copies {
+  using F = Form<T>;
+  static constexpr int kStep = 32 / F::kPieces;  // inputs of an instruction
+  const Args& a;
+  const Plan& plan;
+  const Stream* streams;
+  uint32_t ring;      // this lane's place in a slot
+  int product = 0, left = 0, slot = 0;
+  int64_t next = 0;   // unit
+  int unit = 0, units = 0, inputs = 0, outputs = 0;
+  bool real = false;
+  const T* src = nullptr;
+  int dst[8];
+
+  __device__ Copies(const Args& a_, const Plan& p, const Stream* s, const void* smem)
+      : a(a_), plan(p), streams(s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    ring = smem_at(smem) + warp * kSlots * kUnit;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      dst[i] = F::place(lane / F::kPieces + i * kStep, lane % F::kPieces);
+    left = static_cast<int>(s[0].end - s[0].begin);
+    next = s[0].begin;
+  }
+
+  __device__ void enter(int tile, int unit_) {
+    const Stream& s = streams[product];
+    const Tile t = tile_of(a, plan, s, tile);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool shared = t.hit == plan.hits;
+    const int f = shared ? a.fs : a.f;
+    const void* W;
+    int column;
+    if (product == 0) {
+      inputs = a.h, outputs = f;
+      column = t.at * 256 + (warp & 3) * 64;
+      W = shared ? (warp < 4 ? a.V1 : a.V3) : (warp < 4 ? a.W1 : a.W3);
+    } else {
+      inputs = f, outputs = a.h;
+      column = t.at * kColumns + warp * 64;
+      W = shared ? a.V2 : a.W2;
+    }
+    column += lane % F::kPieces * (16 / static_cast<int>(sizeof(T)));
+    real = column < outputs;
+    const int64_t e = shared ? 0 : plan.hit[t.hit];
+    const int row = unit_ * F::kInputs + lane / F::kPieces;
+    src = static_cast<const T*>(W) +
+          (real ? (e * inputs + row) * outputs + column : int64_t{0});
+    unit = unit_;
+    units = s.units_of(tile);
+  }
+
+  // the next unit, if there is one, and a group in any case
+  __device__ __forceinline__ void issue() {
+    if (left == 0 && product == 0) {
+      product = 1;
+      left = static_cast<int>(streams[1].end - streams[1].begin);
+      next = streams[1].begin;
+      unit = units = 0;
+    }
+    if (left > 0) {
+      if (unit == units) {
+        int tile, u;
+        streams[product].find(next, tile, u);
+        enter(tile, u);
+      }
+      const int row = unit * F::kInputs + (threadIdx.x & 31) / F::kPieces;
+      const uint32_t to = ring + slot * kUnit;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool there = real && row + i * kStep < inputs;
+        copy16(to + dst[i], there ? src + static_cast<int64_t>(i) * kStep * outputs : src, there);
+      }
+      if (real) src += static_cast<int64_t>(F::kInputs) * outputs;
+      ++unit;
+      ++next;
+      --left;
+      if (++slot == kSlots) slot = 0;
+    }
+    commit();
+  }
+};
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Not through the read-only path: hidden values are written by this launch.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// Where a run's sums of a tile go: the row `n` of the tile's, an output of the warp's 64.
+struct Out {
+  float* at;
+  int64_t stride;
+  int limit;  // outputs from `at` on
+};
+
+// A run of units of one tile, bf16, up to 8 NT rows.  rows: offsets of the rows' inputs.
+template <int NT, int PIECES>
+__device__ __forceinline__ void run_units(Copies<__nv_bfloat16>& copies, int& slot, int units,
+                                          const __nv_bfloat16* x, int64_t x_lo,
+                                          const uint16_t* row_at, int first, int count, int width,
+                                          const Out& out) {
+  using F = Form<__nv_bfloat16>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float acc[4][NT][4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+  // rows past the last one repeat it; their sums are not stored
+  uint32_t off[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = first + min(n * 8 + g, count - 1);
+    off[n] = (row_at ? static_cast<uint32_t>(row_at[r]) : static_cast<uint32_t>(r - first)) *
+                 static_cast<uint32_t>(width) + t * 8;
+  }
+  // instruction s of the unit takes the inputs 8 t + 4 s .. + 3 of each t: its slots
+  // 2 t, 2 t + 1 are the first two and 2 t + 8, 2 t + 9 the others
+  const int j = lane >> 3, r = lane & 7;
+  const int row = 8 * (r >> 1) + 2 * (j >> 1) + (r & 1);
+  uint32_t from[2][4];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int m = 0; m < 4; ++m) from[s][m] = F::place(row + 4 * s, m * 2 + (j & 1));
+
+#pragma unroll 1
+  for (int u = 0; u < units; ++u) {
+    uint4 v[PIECES][NT];
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) v[p][n] = load16(x + p * x_lo + off[n]);
+    x += F::kInputs;
+    wait_copies<kSlots - 2>();
+    __syncwarp();
+    copies.issue();  // into the slot that was read last
+    const uint32_t at = copies.ring + slot * kUnit;
+    if (++slot == kSlots) slot = 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        uint32_t w[4];
+        ldmatrix_x4_trans(at + from[s][m], w);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int p = 0; p < PIECES; ++p)
+            mma_bf16(acc[m][n], w, s ? v[p][n].z : v[p][n].x, s ? v[p][n].w : v[p][n].y);
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int at = n * 8 + t * 2 + c;
+      if (at < count) {
+        float* o = out.at + at * out.stride;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          if (m * 16 + g < out.limit) o[m * 16 + g] = acc[m][n][c];
+          if (m * 16 + g + 8 < out.limit) o[m * 16 + g + 8] = acc[m][n][2 + c];
+        }
+      }
+    }
+}
+
+// The same, fp32: two outputs to a lane.
+template <int NR>
+__device__ __forceinline__ void run_units(Copies<float>& copies, int& slot, int units,
+                                          const float* x, const uint16_t* row_at, int first,
+                                          int count, int width, int inputs, const Out& out) {
+  const int lane = threadIdx.x & 31;
+  float acc[NR][2];
+#pragma unroll
+  for (int n = 0; n < NR; ++n) acc[n][0] = acc[n][1] = 0.f;
+  int k = 0;
+#pragma unroll 1
+  for (int u = 0; u < units; ++u) {
+    wait_copies<kSlots - 2>();
+    __syncwarp();
+    copies.issue();
+    const uint32_t at = copies.ring + slot * kUnit + lane * 8;
+    if (++slot == kSlots) slot = 0;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q, k += 4) {
+      if (k >= inputs) break;  // inputs are a multiple of 8
+      float w[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(w[i][0]), "=f"(w[i][1])
+                     : "r"(at + (q * 4 + i) * 256)
+                     : "memory");
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const int r = first + min(n, count - 1);
+        const uint32_t row = row_at ? row_at[r] : r - first;
+        const uint4 b = load16(x + row * static_cast<uint32_t>(width) + k);
+        const float v[4] = {__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z),
+                            __uint_as_float(b.w)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[n][0] = fmaf(v[i], w[i][0], acc[n][0]);
+          acc[n][1] = fmaf(v[i], w[i][1], acc[n][1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NR; ++n)
+    if (n < count && lane * 2 < out.limit)  // the outputs are a multiple of 8
+      *reinterpret_cast<float2*>(out.at + n * out.stride + lane * 2) =
+          make_float2(acc[n][0], acc[n][1]);
+}
+
+// ------------------------------------------------------------------ the steps
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+__host__ __device__ inline int expert_tiles(int E) { return (E + 31) / 32; }
+__host__ __device__ inline int slabs(int G, int E, int h) {
+  const int n = G / expert_tiles(E);
+  return n < 1 ? 1 : n < h / 8 ? n : h / 8;
+}
+
+// Partial logits [slab][T][E] of this block's features and experts.
+template <typename T>
+__device__ void partial_logits(const Args& a, char* smem) {
+  const int tiles = expert_tiles(a.E), n_slabs = slabs(gridDim.x, a.E, a.h);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // more than G tiles of experts only where the grid is smaller than 8 blocks
+  for (int job = blockIdx.x; job < tiles * n_slabs; job += gridDim.x) {
+    const int e0 = job % tiles * 32, slab = job / tiles;
+    const int width = a.E > 16 ? 32 : a.E > 8 ? 16 : 8;  // lanes of experts
+    const int ne = min(32, a.E - e0);
+    const int begin = static_cast<int>(static_cast<int64_t>(a.h / 8) * slab / n_slabs) * 8;
+    const int end = static_cast<int>(static_cast<int64_t>(a.h / 8) * (slab + 1) / n_slabs) * 8;
+    const int Tp = a.T <= 16 ? 16 : a.T <= 32 ? 32 : 64;
+    float* ws = reinterpret_cast<float*>(smem);                 // [rows][32]
+    float* xs = reinterpret_cast<float*>(smem) + kChunk * 32;   // [rows][Tp]
+    const int tg = warp % (Tp / 16), splits = kWarps / (Tp / 16) * (32 / width);
+    const int split = warp / (Tp / 16) * (32 / width) + lane / width, le = lane % width;
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    for (int r0 = begin; r0 < end; r0 += kChunk) {
+      const int rows = min(kChunk, end - r0);
+      __syncthreads();
+      if (ne == 32 && a.E % 4 == 0) {
+        for (int i = threadIdx.x; i < rows * 8; i += kThreads)
+          copy16(smem_at(ws + i * 4),
+                 a.Wg + static_cast<int64_t>(r0 + i / 8) * a.E + e0 + i % 8 * 4, true);
+      } else {
+        for (int i = threadIdx.x; i < rows * 32; i += kThreads)
+          if (i % 32 < ne)
+            copy4(smem_at(ws + i), a.Wg + static_cast<int64_t>(r0 + i / 32) * a.E + e0 + i % 32);
+      }
+      commit();
+      constexpr int V = 16 / sizeof(T);
+      for (int i = threadIdx.x; i < rows / V * a.T; i += kThreads) {
+        const int t = i % a.T, r = i / a.T * V;
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) +
+                                                             static_cast<int64_t>(t) * a.h + r0 + r));
+        T v[V];
+        memcpy(v, &q, 16);
+#pragma unroll
+        for (int j = 0; j < V; ++j) xs[(r + j) * Tp + t] = as_float(v[j]);
+      }
+      wait_copies<0>();
+      __syncthreads();
+      if (le < ne)
+        for (int r = split; r < rows; r += splits) {
+          const float w = ws[r * 32 + le];
+          const float4* q = reinterpret_cast<const float4*>(xs + r * Tp + tg * 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = q[i];  // past T: not stored
+            acc[i * 4] = fmaf(v.x, w, acc[i * 4]);
+            acc[i * 4 + 1] = fmaf(v.y, w, acc[i * 4 + 1]);
+            acc[i * 4 + 2] = fmaf(v.z, w, acc[i * 4 + 2]);
+            acc[i * 4 + 3] = fmaf(v.w, w, acc[i * 4 + 3]);
+          }
+        }
+    }
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem);  // [split][Tp][width]
+#pragma unroll
+    for (int i = 0; i < 16; ++i) red[(split * Tp + tg * 16 + i) * width + le] = acc[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T * ne; i += kThreads) {
+      const int t = i / ne, e = i % ne;
+      float sum = 0.f;
+      for (int s = 0; s < splits; ++s) sum += red[(s * Tp + t) * width + e];
+      a.logits[(static_cast<int64_t>(slab) * a.T + t) * a.E + e0 + e] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+template <int PL>
+__device__ void choose(const Args& a, Plan& plan, int t) {
+  const int lane = threadIdx.x & 31;
+  float s[PL];
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    const int e = lane + 32 * i;
+    s[i] = e < a.E ? plan.logit[e] : -FLT_MAX;
+  }
+  int idx;
+  float p;
+  choose_topk<PL>(s, t, a.E, a.k, a.score, a.groups, a.group_topk, a.expert_bias, plan.gsel, a.err,
+                  idx, p);
+  if (lane < a.k) {
+    a.idx[t * a.k + lane] = idx;
+    a.prob[t * a.k + lane] = p;
+    if (a.idx_out) a.idx_out[t * a.k + lane] = idx;
+    if (a.prob_out) a.prob_out[t * a.k + lane] = p;
+  }
+}
+
+__device__ void choose_experts(const Args& a, Plan& plan) {
+  const int n_slabs = slabs(gridDim.x, a.E, a.h);
+  int width = 8;
+  while (width < a.E) width *= 2;
+  const int parts = kThreads / width, e = threadIdx.x % width, part = threadIdx.x / width;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    float sum = 0.f;
+    if (e < a.E) {
+#pragma unroll 8
+      for (int s = part; s < n_slabs; s += parts)
+        sum += __ldcg(a.logits + (static_cast<int64_t>(s) * a.T + t) * a.E + e);
+    }
+    __syncthreads();
+    plan.part[threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.x < a.E) {
+      float l = 0.f;
+      for (int i = 0; i < parts; ++i) l += plan.part[i * width + threadIdx.x];
+      plan.logit[threadIdx.x] = a.gate_bias ? l + a.gate_bias[threadIdx.x] : l;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      if (a.E <= 32) choose<1>(a, plan, t);
+      else if (a.E <= 64) choose<2>(a, plan, t);
+      else if (a.E <= 128) choose<4>(a, plan, t);
+      else choose<8>(a, plan, t);
+    }
+  }
+}
+
+// Rows by expert: pairs counted and ranked in their order, 64 of them to a warp.
+__device__ void order_pairs(const Args& a, Plan& plan) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < kWarps * MOE_MAX_EXPERTS; i += kThreads)
+    plan.before[i / MOE_MAX_EXPERTS][i % MOE_MAX_EXPERTS] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int i = warp * 64 + r * 32 + lane;
+    const int e = i < plan.pairs ? plan.expert[i] : -1;
+    const uint32_t same = __match_any_sync(~0u, e);
+    if (e >= 0) {
+      const int base = plan.before[warp][e];
+      plan.rank[i] = static_cast<uint8_t>(base + __popc(same & ((1u << lane) - 1)));
+      __syncwarp(same);
+      if (lane == __ffs(same) - 1) plan.before[warp][e] = static_cast<int16_t>(base + __popc(same));
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (threadIdx.x < MOE_MAX_EXPERTS) {
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int n = plan.before[w][threadIdx.x];
+      plan.before[w][threadIdx.x] = static_cast<int16_t>(sum);
+      sum += n;
+    }
+    plan.total[threadIdx.x] = static_cast<int16_t>(sum);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {  // eight experts to a lane
+    int n[8], rows = 0, hits = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      n[i] = plan.total[lane * 8 + i];
+      rows += n[i];
+      hits += n[i] > 0;
+    }
+    int row = rows, hit = hits;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int r = __shfl_up_sync(~0u, row, o), q = __shfl_up_sync(~0u, hit, o);
+      if (lane >= o) row += r, hit += q;
+    }
+    if (lane == 31) {
+      plan.rows = row;
+      plan.hits = hit;
+      plan.first[hit] = static_cast<int16_t>(row);
+    }
+    row -= rows, hit -= hits;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      plan.start[lane * 8 + i] = static_cast<int16_t>(row);
+      if (n[i] > 0) {
+        plan.hit[hit] = static_cast<int16_t>(lane * 8 + i);
+        plan.first[hit++] = static_cast<int16_t>(row);
+        row += n[i];
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// Every block builds the same plan.
+__device__ void make_plan(const Args& a, Plan& plan) {
+  const int pairs = a.T * a.k;
+  if (threadIdx.x == 0) plan.pairs = pairs, plan.dropped = 0;
+  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+    plan.expert[i] = static_cast<int16_t>(__ldcg(a.idx + i));
+    plan.prob[i] = __ldcg(a.prob + i);
+  }
+  __syncthreads();
+  // A token without k experts to choose (NaN logits, reported) names one twice; the
+  // first of them stands, so that no expert has more rows than there are tokens.
+  bool twice[2] = {false, false};
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int i = threadIdx.x + r * kThreads;
+    if (i < pairs)
+      for (int q = i - i % a.k; q < i; ++q) twice[r] |= plan.expert[q] == plan.expert[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    if (twice[r]) plan.expert[threadIdx.x + r * kThreads] = -1;
+  __syncthreads();
+  order_pairs(a, plan);
+  if (a.capacity >= 0) {
+    bool drop[2] = {false, false};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = threadIdx.x + r * kThreads;
+      const int e = i < pairs ? plan.expert[i] : -1;
+      if (e < 0 || plan.total[e] <= a.capacity) continue;
+      int place = plan.before[i / 64][e] + plan.rank[i];
+      if (a.policy == MOE_DROP_PROBS) {
+        // a larger probability first, equal ones in token order (bits of numbers >= 0)
+        const uint32_t p = __float_as_uint(plan.prob[i]);
+        place = 0;
+        for (int q = 0; q < pairs; ++q) {
+          const uint32_t o = __float_as_uint(plan.prob[q]);
+          place += plan.expert[q] == e && (o > p || (o == p && q < i));
+        }
+      }
+      drop[r] = place >= a.capacity;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (drop[r]) {
+        const int i = threadIdx.x + r * kThreads;
+        plan.expert[i] = -1;
+        plan.dropped = 1;
+        if (blockIdx.x == 0 && a.prob_out) a.prob_out[i] = 0.f;
+      }
+    __syncthreads();
+    if (plan.dropped) order_pairs(a, plan);
+  }
+  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+    const int e = plan.expert[i];
+    int row = -1;
+    if (e >= 0) {
+      row = plan.start[e] + plan.before[i / 64][e] + plan.rank[i];
+      plan.token[row] = static_cast<uint16_t>(i / a.k);
+    }
+    plan.row_of[i] = static_cast<int16_t>(row);
+  }
+  for (int t = threadIdx.x; t < a.T; t += kThreads)
+    plan.token[plan.rows + t] = static_cast<uint16_t>(t);
+  for (int i = threadIdx.x; i < plan.hits; i += kThreads)
+    for (int r = plan.first[i]; r < plan.first[i + 1]; ++r)
+      plan.hit_of_row[r] = static_cast<int16_t>(i);
+  if (blockIdx.x == 0 && a.tpe_out)
+    for (int e = threadIdx.x; e < a.E; e += kThreads) a.tpe_out[e] = plan.total[e];
+  __syncthreads();
+}
+
+// Partial sums of a row's outputs in main: FC1's two products side by side.
+__device__ __forceinline__ float* main_row(const Args& a, const Plan& plan, int product, int row,
+                                           bool shared) {
+  if (product == 1) return a.main + static_cast<int64_t>(row) * a.h;
+  if (!shared) return a.main + static_cast<int64_t>(row) * 2 * a.f;
+  return a.main + static_cast<int64_t>(plan.rows) * 2 * a.f +
+         static_cast<int64_t>(row - plan.rows) * 2 * a.fs;
+}
+__device__ __forceinline__ int64_t hid_row(const Args& a, const Plan& plan, int row, bool shared) {
+  if (!shared) return static_cast<int64_t>(row) * a.f;
+  return static_cast<int64_t>(plan.rows) * a.f + static_cast<int64_t>(row - plan.rows) * a.fs;
+}
+
+// This block's units of a product.
+template <typename T>
+__device__ void stream_product(const Args& a, const Plan& plan, const Stream& s, int product,
+                               Copies<T>& copies, int& slot) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t u = s.begin; u < s.end;) {
+    int tile, unit;
+    s.find(u, tile, unit);
+    const Tile t = tile_of(a, plan, s, tile);
+    const bool shared = t.hit == plan.hits;
+    const int f = shared ? a.fs : a.f, units =
+        static_cast<int>(min(static_cast<int64_t>(s.units_of(tile) - unit), s.end - u));
+    const int outputs = product ? a.h : f, inputs = product ? f : a.h;
+    const int column = product ? t.at * kColumns + warp * 64 : t.at * 256 + (warp & 3) * 64;
+    Out out;
+    out.limit = outputs - column;
+    if (unit == 0) {
+      out.at = main_row(a, plan, product, t.first, shared) + column +
+               (product == 0 && warp >= 4 ? f : 0);
+      out.stride = product ? a.h : 2 * f;
+    } else {
+      out.at = a.extra + static_cast<int64_t>(blockIdx.x) * a.T * kColumns + warp * 64;
+      out.stride = kColumns;
+    }
+    const int k0 = unit * Form<T>::kInputs;
+    // FC1 reads the rows' tokens, FC2 the hidden values in the rows' order
+    const uint16_t* row_at = product ? nullptr : plan.token;
+    const T* x = product ? static_cast<const T*>(a.hid) + hid_row(a, plan, t.first, shared)
+                         : static_cast<const T*>(a.x);
+    x += k0;
+    if constexpr (sizeof(T) == 2) {
+      if (product == 0) {
+        if (t.rows <= 8) run_units<1, 1>(copies, slot, units, x, 0, row_at, t.first, t.rows, inputs, out);
+        else if (t.rows <= 16) run_units<2, 1>(copies, slot, units, x, 0, row_at, t.first, t.rows, inputs, out);
+        else if (t.rows <= 32) run_units<4, 1>(copies, slot, units, x, 0, row_at, t.first, t.rows, inputs, out);
+        else run_units<8, 1>(copies, slot, units, x, 0, row_at, t.first, t.rows, inputs, out);
+      } else {
+        if (t.rows <= 8) run_units<1, 2>(copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, out);
+        else if (t.rows <= 16) run_units<2, 2>(copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, out);
+        else if (t.rows <= 32) run_units<4, 2>(copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, out);
+        else run_units<8, 2>(copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, out);
+      }
+    } else {
+      const int left = inputs - k0;
+      if (t.rows <= 1) run_units<1>(copies, slot, units, x, row_at, t.first, t.rows, inputs, left, out);
+      else if (t.rows <= 4) run_units<4>(copies, slot, units, x, row_at, t.first, t.rows, inputs, left, out);
+      else if (t.rows <= 16) run_units<16>(copies, slot, units, x, row_at, t.first, t.rows, inputs, left, out);
+      else run_units<64>(copies, slot, units, x, row_at, t.first, t.rows, inputs, left, out);
+    }
+    u += units;
+  }
+  (void)lane;
+}
+
+// A row's sums of four neighbouring outputs, the runs in order.
+__device__ __forceinline__ float4 sum_runs(const Args& a, const Stream& s, const float* main,
+                                           int tile, int row, int column) {
+  float4 v = __ldcg(reinterpret_cast<const float4*>(main));
+  int first, last;
+  s.blocks(tile, first, last);
+  for (int b = first + 1; b <= last; ++b) {
+    const float4 w = __ldcg(reinterpret_cast<const float4*>(
+        a.extra + (static_cast<int64_t>(b) * a.T + row) * kColumns + column));
+    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+  }
+  return v;
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+template <typename T>
+__device__ void hidden_values(const Args& a, const Plan& plan, const Stream& s) {
+  const int rows = plan.rows + (a.fs ? a.T : 0);
+  const int64_t routed = static_cast<int64_t>(plan.rows) * (a.f / 4);
+  const int64_t all = routed + static_cast<int64_t>(rows - plan.rows) * (a.fs / 4);
+  for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < all; i += gridDim.x * kThreads) {
+    const bool shared = i >= routed;
+    const int f = shared ? a.fs : a.f;
+    const int64_t v = shared ? i - routed : i;
+    const int in = static_cast<int>(v / (f / 4));
+    const int column = static_cast<int>(v - static_cast<int64_t>(in) * (f / 4)) * 4;
+    const int row = in + (shared ? plan.rows : 0);
+    int tile, n;
+    if (shared) {
+      tile = s.routed + column / 256;
+      n = in;
+    } else {
+      const int hit = plan.hit_of_row[row];
+      tile = hit * s.tiles + column / 256;
+      n = row - plan.first[hit];
+    }
+    const float* m = main_row(a, plan, 0, row, shared) + column;
+    const float4 g = sum_runs(a, s, m, tile, n, column % 256);
+    const float4 w = sum_runs(a, s, m + f, tile, n, 256 + column % 256);
+    const float o[4] = {swiglu(g.x, w.x), swiglu(g.y, w.y), swiglu(g.z, w.z), swiglu(g.w, w.w)};
+    T* to = static_cast<T*>(a.hid) + hid_row(a, plan, row, shared) + column;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
+    } else {
+      // the nearest bf16 number and that of what is left (none past the largest one)
+      __nv_bfloat16 hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        hi[q] = __float2bfloat16_rn(o[q]);
+        const float r = o[q] - __bfloat162float(hi[q]);
+        lo[q] = __float2bfloat16_rn(isfinite(r) ? r : 0.f);
+      }
+      memcpy(to, hi, 8);
+      memcpy(to + a.hid_lo, lo, 8);
+    }
+  }
+}
+
+__device__ __forceinline__ void store4(float* p, float4 v) {
+  *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 q[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+  memcpy(p, q, 8);
+}
+
+template <typename T>
+__device__ void combine(const Args& a, const Plan& plan, const Stream& s) {
+  const int per = a.h / 4;
+  for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < static_cast<int64_t>(a.T) * per;
+       i += gridDim.x * kThreads) {
+    const int t = static_cast<int>(i / per);
+    const int column = static_cast<int>(i - static_cast<int64_t>(t) * per) * 4;
+    const int at = column / kColumns;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < a.k; ++j) {
+      const int row = plan.row_of[t * a.k + j];
+      if (row < 0) continue;
+      const int hit = plan.hit_of_row[row];
+      const float p = plan.prob[t * a.k + j];
+      const float4 v = sum_runs(a, s, main_row(a, plan, 1, row, false) + column,
+                                hit * s.tiles + at, row - plan.first[hit], column % kColumns);
+      y.x = fmaf(p, v.x, y.x), y.y = fmaf(p, v.y, y.y);
+      y.z = fmaf(p, v.z, y.z), y.w = fmaf(p, v.w, y.w);
+    }
+    if (a.fs) {
+      const float4 v = sum_runs(a, s, main_row(a, plan, 1, plan.rows + t, true) + column,
+                                s.routed + at, t, column % kColumns);
+      y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+    }
+    store4(static_cast<T*>(a.y) + static_cast<int64_t>(t) * a.h + column, y);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Args a) {
+  extern __shared__ __align__(1024) char smem[];
+  Plan& plan = *reinterpret_cast<Plan*>(smem + kRing);
+  __shared__ Stream streams[2];
+  partial_logits<T>(a, smem);
+  bool on = grid_barrier(a, plan, 1);
+  if (on) {
+    choose_experts(a, plan);
+    on = grid_barrier(a, plan, 2);
+  }
+  if (on) {
+    make_plan(a, plan);
+    if (threadIdx.x == 0) {
+      constexpr int U = Form<T>::kInputs;
+      auto up = [](int n, int d) { return (n + d - 1) / d; };
+      streams[0].set(plan.hits, up(a.f, 256), up(a.h, U), up(a.fs, 256), up(a.h, U));
+      streams[1].set(plan.hits, up(a.h, kColumns), up(a.f, U), a.fs ? up(a.h, kColumns) : 0,
+                     up(a.fs, U));
+    }
+    __syncthreads();
+    Copies<T> copies(a, plan, streams, smem);
+#pragma unroll 1
+    for (int i = 0; i < kSlots - 1; ++i) copies.issue();
+    int slot = 0;
+    stream_product<T>(a, plan, streams[0], 0, copies, slot);
+    on = grid_barrier(a, plan, 3);
+    if (on) {
+      hidden_values<T>(a, plan, streams[0]);
+      on = grid_barrier(a, plan, 4);
+    }
+    if (on) {
+      stream_product<T>(a, plan, streams[1], 1, copies, slot);
+      on = grid_barrier(a, plan, 5);
+    }
+    wait_copies<0>();
+    if (on) combine<T>(a, plan, streams[1]);
+  }
+  leave(a);
+}
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+struct Layout {
+  size_t logits, idx, prob, main, extra, hid, total;
+  int64_t hid_lo;
+};
+Layout layout(int T, int h, int E, int k, int f, int fs, int dtype) {
+  Layout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = o;
+    o += up256(bytes);
+    return r;
+  };
+  const size_t pairs = static_cast<size_t>(T) * k, rows = pairs + (fs ? T : 0);
+  const size_t values = pairs * f + static_cast<size_t>(fs) * T;
+  L.logits = take(static_cast<size_t>(slabs(kFewBlocks, E, h)) * T * E * 4);
+  L.idx = take(pairs * 4);
+  L.prob = take(pairs * 4);
+  L.main = take((2 * values > rows * h ? 2 * values : rows * h) * 4);
+  L.extra = take(static_cast<size_t>(kFewBlocks) * T * kColumns * 4);
+  L.hid_lo = static_cast<int64_t>(up256(values * 2) / 2);
+  L.hid = take(dtype == MOE_F32 ? values * 4 : static_cast<size_t>(L.hid_lo) * 2 * 2);
+  L.total = o;
+  return L;
+}
+
+template <typename T>
+cudaError_t launch(Args& a, cudaStream_t s) {
+  cudaError_t st = allow_most_smem<few_kernel<T>>();
+  if (st != cudaSuccess) return st;
+  cudaLaunchConfig_t cfg = {};
+  const int sms = device_sm_count();
+  cfg.gridDim = dim3(sms < kFewBlocks ? sms : kFewBlocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRing + sizeof(Plan);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_kernel<T>, static_cast<const Args>(a));
+}
+
+}  // namespace
+
+size_t few_scratch(const moe_config& c, int fs) {
+  return layout(c.num_tokens, c.hidden, c.num_experts, c.topk, c.ffn_hidden, fs, c.dtype).total;
+}
+
+cudaError_t launch_few(const moe_config& c, int fs, int64_t capacity, const void* x,
+                       const float* Wg, const float* gate_bias, const float* expert_bias,
+                       const void* W1, const void* W3, const void* W2, const void* W1s,
+                       const void* W3s, const void* W2s, void* y, int32_t* topk_idx,
+                       float* topk_prob, int32_t* tokens_per_expert, void* scratch, int* err,
+                       cudaStream_t s) {
+  const Layout L = layout(c.num_tokens, c.hidden, c.num_experts, c.topk, c.ffn_hidden, fs, c.dtype);
+  char* at = static_cast<char*>(scratch);
+  Args a;
+  a.T = c.num_tokens, a.h = c.hidden, a.E = c.num_experts, a.k = c.topk, a.f = c.ffn_hidden;
+  a.fs = fs;
+  a.score = c.score, a.groups = c.num_groups, a.group_topk = c.group_topk;
+  a.capacity = capacity < 0 || capacity >= c.num_tokens ? -1 : static_cast<int>(capacity);
+  a.policy = c.drop_policy;
+  a.x = x, a.W1 = W1, a.W3 = W3, a.W2 = W2, a.V1 = W1s, a.V3 = W3s, a.V2 = W2s;
+  a.Wg = Wg, a.gate_bias = gate_bias, a.expert_bias = expert_bias;
+  a.y = y, a.idx_out = topk_idx, a.prob_out = topk_prob, a.tpe_out = tokens_per_expert;
+  a.err = err;
+  a.bar = err + kFewCounters;
+  a.logits = reinterpret_cast<float*>(at + L.logits);
+  a.idx = reinterpret_cast<int32_t*>(at + L.idx);
+  a.prob = reinterpret_cast<float*>(at + L.prob);
+  a.main = reinterpret_cast<float*>(at + L.main);
+  a.extra = reinterpret_cast<float*>(at + L.extra);
+  a.hid = at + L.hid;
+  a.hid_lo = L.hid_lo;
+  return c.dtype == MOE_F32 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);
+}
+
+}  // namespace moe
