@@ -744,8 +744,9 @@ moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, c
                           size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
- * A decoding step: the whole layer for a few tokens.  The conventions at the top
- * hold (contiguous, 16-byte aligned, asynchronous).
+ * A decoding step: the whole layer for a few tokens, and the choice of the next
+ * token.  The conventions at the top hold (contiguous, 16-byte aligned,
+ * asynchronous).
  * ------------------------------------------------------------------------- */
 
 /*
@@ -773,6 +774,42 @@ moe_status moe_forward_few(const moe_config* cfg, int32_t fs, const void* x, con
                            const void* W2s, void* y, int32_t* topk_idx, float* topk_prob,
                            int32_t* tokens_per_expert, void* ws, size_t ws_bytes,
                            moe_stream_t stream);
+
+/*
+ * The next token of each row of logits, from a given random number u[r] (in [0, 1);
+ * values outside are brought to its ends, a NaN to 0).
+ * The tokens of a row are ordered by logit, equal logits by index, the lower first.
+ * With m the largest logit and t the temperature, token i has the weight
+ * w_i = exp((l_i - m) / t).  Kept are, from the start of the order,
+ *   top_k    at most so many tokens (0 or less: no limit);
+ *   top_p    of those, the fewest, but one at least, whose weights add up to top_p of
+ *            theirs (1 or more, or a NaN: all);
+ *   min_p    of those, the ones of at least that weight (the largest weight is 1, so
+ *            that this is relative to the likeliest; the first one always stays).
+ * tokens[r] is the lowest index at which the running sum of the kept weights, in index
+ * order, exceeds u[r] times their sum; prob[r] (NULL: not written) its share of that
+ * sum.  t = 0 (or less, or a NaN): the first token of the order, with prob 1.
+ * A logit of -infinity or NaN is never kept, and a row of nothing else gives the token
+ * -1 with prob 0; with logits of +infinity those alone have weight.
+ * Weights are whole numbers of 2^-40 in sums, so a row's token does not depend on the
+ * batch, and repeats are equal.  Values for each row stand in the *_of arrays [rows] in
+ * device memory; NULL: the one value for all (temperature >= 0, top_k >= 0, top_p and
+ * min_p in [0, 1]; MOE_ERR_INVALID_ARG otherwise).  vocab is at most 2^30.
+ *   logits [rows, vocab] dtype, u [rows] fp32, tokens [rows] int32 out, prob [rows] fp32 out.
+ */
+typedef struct moe_sample_choices {
+  float temperature;
+  int32_t top_k;
+  float top_p;
+  float min_p;
+  const float* temperature_of;
+  const int32_t* top_k_of;
+  const float* top_p_of;
+  const float* min_p_of;
+} moe_sample_choices;
+moe_status moe_sample(int64_t rows, int32_t vocab, int32_t dtype, const void* logits,
+                      const float* u, const moe_sample_choices* choices, int32_t* tokens,
+                      float* prob, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -39,7 +39,7 @@ EXPORTS = ["moe_abi_version", "moe_status_string", "moe_last_cuda_error", "moe_c
            "moe_dropout_add", "moe_quantize_w4", "moe_pack_w4", "moe_workspace_size_linear_w4",
            "moe_linear_w4", "moe_workspace_size_experts_w4", "moe_experts_w4",
            "moe_workspace_size_w4", "moe_forward_w4", "moe_workspace_size_few",
-           "moe_forward_few"]
+           "moe_forward_few", "moe_sample"]
 
 NORM = {"layer": 0, "rms": 1}
 
@@ -64,6 +64,13 @@ class NormConfig(ctypes.Structure):
 class W4Pointers(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("zeros", ctypes.c_void_p)]
+
+
+class SampleChoices(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("top_p", ctypes.c_float), ("min_p", ctypes.c_float),
+                ("temperature_of", ctypes.c_void_p), ("top_k_of", ctypes.c_void_p),
+                ("top_p_of", ctypes.c_void_p), ("min_p_of", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -154,6 +161,8 @@ def lib():
                                 vp], i32),
             "moe_workspace_size_few": ([cfgp, i32, ctypes.POINTER(sz)], i32),
             "moe_forward_few": ([cfgp, i32] + [vp] * 14 + [vp, sz, vp], i32),
+            "moe_sample": ([i64, i32, i32, vp, vp, ctypes.POINTER(SampleChoices), vp, vp, vp],
+                           i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -964,6 +973,28 @@ def forward_few(cfg, x, Wg, gate_bias, expert_bias, W1, W3, W2, y, ws, topk_idx=
         _table(topk_idx, T, k, i32, "topk_idx"), _table(topk_prob, T, k, f32, "topk_prob"),
         _vec(tokens_per_expert, E, i32, "tokens_per_expert"), b, wb, _stream()),
         "moe_forward_few")
+
+
+def sample(logits, u, tokens, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, prob=None):
+    """tokens [rows] int32 from logits [rows, V] (fp32 or bf16) and random numbers
+    u [rows] fp32 in [0, 1): the tokens that top_k, then top_p, then min_p leave, drawn
+    by their probabilities at that temperature (0: the likeliest).  Each choice is a
+    number or a device tensor [rows] (fp32; top_k int32).  prob [rows] fp32, where
+    given: the token's probability among those."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, V]")
+    rows, V = logits.shape
+    f32, i32 = torch.float32, torch.int32
+    one, each = [], []
+    for v, off, dt, what in ((temperature, 1.0, f32, "temperature"), (top_k, 0, i32, "top_k"),
+                             (top_p, 1.0, f32, "top_p"), (min_p, 0.0, f32, "min_p")):
+        tensor = isinstance(v, torch.Tensor)
+        one.append(off if tensor else v)
+        each.append(_vec(v, rows, dt, what) if tensor else None)
+    choices = SampleChoices(*one, *each)
+    _check(lib().moe_sample(rows, V, _code(logits, "logits"), _p(logits), _vec(u, rows, f32, "u"),
+                            ctypes.byref(choices), _vec(tokens, rows, i32, "tokens"),
+                            _vec(prob, rows, f32, "prob"), _stream()), "moe_sample")
 
 
 def probe_fp32_fma(iters, out):

@@ -1,5 +1,5 @@
-// C ABI of a decoding step: the whole layer for a few tokens.  Argument checks and
-// workspace carve-up, as in capi.cu.
+// C ABI of a decoding step: the whole layer for a few tokens and the choice of the
+// next token.  Argument checks and workspace carve-up, as in capi.cu.
 #include "common.cuh"
 
 namespace {
@@ -26,6 +26,8 @@ moe_status check_ws(const void* ws, size_t have, size_t want) {
   return have < want ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 void* past_error_word(void* ws) { return static_cast<char*>(ws) + kErrBytes; }
+
+bool is_dtype(int32_t d) { return d == MOE_F32 || d == MOE_BF16; }
 
 // The layer's own checks of the configuration, then those of few tokens.
 moe_status validate_few(const moe_config* cfg, int32_t fs) {
@@ -84,6 +86,32 @@ moe_status moe_forward_few(const moe_config* cfg, int32_t fs, const void* x, con
   MOE_CUDA(launch_few(*cfg, fs, capacity, x, Wg, gate_bias, expert_bias, W1, W3, W2, W1s, W3s, W2s,
                       y, topk_idx, topk_prob, tokens_per_expert, past_error_word(ws),
                       static_cast<int*>(ws), stream));
+  return MOE_OK;
+}
+
+moe_status moe_sample(int64_t rows, int32_t vocab, int32_t dtype, const void* logits,
+                      const float* u, const moe_sample_choices* choices, int32_t* tokens,
+                      float* prob, moe_stream_t stream) {
+  if (rows < 0 || vocab <= 0 || choices == nullptr || !is_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  if (vocab > (1 << 30) || rows > (int64_t{1} << 31)) return MOE_ERR_UNSUPPORTED;
+  const moe_sample_choices& c = *choices;
+  // false for NaN
+  if (!(c.temperature >= 0.f) || c.top_k < 0 || !(c.top_p >= 0.f && c.top_p <= 1.f) ||
+      !(c.min_p >= 0.f && c.min_p <= 1.f))
+    return MOE_ERR_INVALID_ARG;
+  const uint64_t n = rows;
+  MOE_TRY(need(logits, n));
+  MOE_TRY(need(u, n, 4));
+  MOE_TRY(need(tokens, n, 4));
+  MOE_TRY(optional(prob, 4));
+  MOE_TRY(optional(c.temperature_of, 4));
+  MOE_TRY(optional(c.top_k_of, 4));
+  MOE_TRY(optional(c.top_p_of, 4));
+  MOE_TRY(optional(c.min_p_of, 4));
+  if (rows == 0) return MOE_OK;
+  const SampleChoices own = {c.temperature,    c.top_k,    c.top_p,    c.min_p,
+                             c.temperature_of, c.top_k_of, c.top_p_of, c.min_p_of};
+  MOE_CUDA(launch_sample(rows, vocab, dtype, logits, u, own, tokens, prob, stream));
   return MOE_OK;
 }
 

@@ -354,6 +354,18 @@ cudaError_t launch_few(const moe_config& c, int fs, int64_t capacity, const void
                        float* topk_prob, int32_t* tokens_per_expert, void* scratch, int* err,
                        cudaStream_t s);
 
+// ---- sampling (sample.cu) ----
+struct SampleChoices {  // moe_sample_choices
+  float temperature;
+  int32_t top_k;
+  float top_p, min_p;
+  const float* temperature_of;
+  const int32_t* top_k_of;
+  const float *top_p_of, *min_p_of;
+};
+cudaError_t launch_sample(int64_t rows, int V, int dtype, const void* logits, const float* u,
+                          const SampleChoices& c, int32_t* tokens, float* prob, cudaStream_t s);
+
 int device_sm_count();
 // keeps the text for moe_last_cuda_error() and returns the status
 moe_status cuda_status(cudaError_t e);

@@ -163,3 +163,39 @@ def assert_close(got, y, bound, dtype):
     over = (got.double() - y).abs() / limit
     assert bool(torch.isfinite(got).all())
     assert float(over.max()) <= 1.0, "error %.2f of what is allowed" % float(over.max())
+
+
+# ----------------------------------------------------------------- sampling
+
+def sample_ref(l, u, t, top_k, top_p, min_p):
+    """One row (float64 numpy logits) -> (token, its probability, the least gap between
+    u or top_p and a border between two tokens, in units of the whole mass, and that
+    between min_p and a weight)."""
+    V = l.size
+    order = sorted(range(V), key=lambda i: (-l[i], i))
+    order = np.array([i for i in order if l[i] > -np.inf], dtype=np.int64)
+    if order.size == 0:
+        return -1, 0.0, 1.0, 1.0
+    if not t > 0 or top_k == 1:
+        return int(order[0]), 1.0, 1.0, 1.0
+    top = l[order[0]]
+    w = np.array([1.0 if l[i] == top else math.exp((l[i] - top) / t) for i in order])
+    gap = gap_min = 1.0
+    if top_k > 0:
+        w = w[:top_k]
+    if top_p < 1:
+        cum = np.cumsum(w) / w.sum()
+        n = int(np.argmax(cum >= top_p))
+        gap = min(gap, np.abs(cum - top_p).min() if top_p > 0 else 1.0)
+        w = w[:n + 1]
+    if min_p > 0:
+        gap_min = np.abs(w / min(min_p, 1.0) - 1)[1:].min(initial=1.0)
+        w = w[np.concatenate(([True], w[1:] >= min(min_p, 1.0)))]
+    kept = np.sort(order[:w.size])
+    by = np.argsort(order[:w.size], kind="stable")
+    share = w[by] / w.sum()
+    cum = np.cumsum(share)
+    u = min(max(u, 0.0), 1 - 2.0 ** -24)
+    at = min(int(np.searchsorted(cum, u, side="right")), w.size - 1)
+    gap = min(gap, np.abs(cum - u)[:-1].min(initial=1.0) if u > 0 else 1.0)
+    return int(kept[at]), float(share[at]), gap, gap_min
