@@ -60,7 +60,11 @@ typedef enum moe_status {
   MOE_ERR_TIMEOUT = 6        /* a bounded device wait ran out (moe_check) */
 } moe_status;
 
-typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+typedef enum moe_dtype {
+  MOE_F32 = 0,
+  MOE_BF16 = 1,
+  MOE_I8 = 2 /* codes with a scale for each row: moe_linear_i8's x alone */
+} moe_dtype;
 
 /* Score functions of §5 of the Megatron Core page (topk_routing_with_score_function). */
 typedef enum moe_score {
@@ -744,9 +748,9 @@ moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, c
                           size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
- * A decoding step: the whole layer for a few tokens, and the choice of the next
- * token.  The conventions at the top hold (contiguous, 16-byte aligned,
- * asynchronous).
+ * A decoding step: the whole layer for a few tokens, the choice of the next token,
+ * and products in 8-bit integers (prompts too).  The conventions at the top hold
+ * (contiguous, 16-byte aligned, asynchronous).
  * ------------------------------------------------------------------------- */
 
 /*
@@ -810,6 +814,37 @@ typedef struct moe_sample_choices {
 moe_status moe_sample(int64_t rows, int32_t vocab, int32_t dtype, const void* logits,
                       const float* u, const moe_sample_choices* choices, int32_t* tokens,
                       float* prob, moe_stream_t stream);
+
+/*
+ * Rows in 8-bit integers: scales[r] = max |x[r]| / 127 (fp32), codes[r, k] the nearest
+ * whole number of x[r, k] / scales[r], ties to even, -127..127.  A row of zeros gets
+ * the scale 0, one with an infinity or a NaN the scale NaN (codes 0 in both).
+ *   x [rows, K] dtype (MOE_F32 or MOE_BF16), codes [rows, K] int8 out, scales [rows]
+ *   fp32 out.  K is a multiple of 16 up to 131056.  Tokens and weights alike: a
+ *   weight's rows are its outputs.
+ */
+moe_status moe_quantize_rows_i8(int64_t rows, int32_t K, int32_t dtype, const void* x,
+                                int8_t* codes, float* scales, moe_stream_t stream);
+
+/*
+ * The product in 8-bit integers with a scale for each row of x and each output:
+ *   y[m, n] = (sum_k x[m, k] W[n, k]) * x_scale[m] * w_scale[n] + bias[n].
+ * The sum is whole (exact, whatever the order); it is rounded to fp32 once, as are its
+ * product with x_scale[m] and the sum of that times w_scale[n] and the bias; y is
+ * rounded once more to its type.  A row whose scale is NaN gives NaN.
+ *   x        [rows, K]: codes (x_dtype MOE_I8, -128..127) with x_scale [rows] fp32, or
+ *            fp32 or bf16 values that the call quantises as moe_quantize_rows_i8 does
+ *            (x_scale NULL)
+ *   W        [N, K] int8, w_scale [N] fp32, bias [N] fp32 or NULL: zeros
+ *   y        [rows, N] y_dtype (MOE_F32 or MOE_BF16) out
+ * K is a multiple of 16 up to 131056 (a sum stays below 2^31), rows at most 2^28.  The
+ * workspace of `rows` rows serves every call of fewer rows too.
+ */
+moe_status moe_workspace_size_linear_i8(int64_t rows, int32_t N, int32_t K, size_t* bytes);
+moe_status moe_linear_i8(int64_t rows, int32_t N, int32_t K, const void* x, int32_t x_dtype,
+                         const float* x_scale, const int8_t* W, const float* w_scale,
+                         const float* bias, void* y, int32_t y_dtype, void* ws, size_t ws_bytes,
+                         moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -39,7 +39,8 @@ EXPORTS = ["moe_abi_version", "moe_status_string", "moe_last_cuda_error", "moe_c
            "moe_dropout_add", "moe_quantize_w4", "moe_pack_w4", "moe_workspace_size_linear_w4",
            "moe_linear_w4", "moe_workspace_size_experts_w4", "moe_experts_w4",
            "moe_workspace_size_w4", "moe_forward_w4", "moe_workspace_size_few",
-           "moe_forward_few", "moe_sample"]
+           "moe_forward_few", "moe_sample", "moe_quantize_rows_i8",
+           "moe_workspace_size_linear_i8", "moe_linear_i8"]
 
 NORM = {"layer": 0, "rms": 1}
 
@@ -161,6 +162,9 @@ def lib():
                                 vp], i32),
             "moe_workspace_size_few": ([cfgp, i32, ctypes.POINTER(sz)], i32),
             "moe_forward_few": ([cfgp, i32] + [vp] * 14 + [vp, sz, vp], i32),
+            "moe_quantize_rows_i8": ([i64, i32, i32, vp, vp, vp, vp], i32),
+            "moe_workspace_size_linear_i8": ([i64, i32, i32, ctypes.POINTER(sz)], i32),
+            "moe_linear_i8": ([i64, i32, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, sz, vp], i32),
             "moe_sample": ([i64, i32, i32, vp, vp, ctypes.POINTER(SampleChoices), vp, vp, vp],
                            i32),
         }
@@ -995,6 +999,77 @@ def sample(logits, u, tokens, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, pr
     _check(lib().moe_sample(rows, V, _code(logits, "logits"), _p(logits), _vec(u, rows, f32, "u"),
                             ctypes.byref(choices), _vec(tokens, rows, i32, "tokens"),
                             _vec(prob, rows, f32, "prob"), _stream()), "moe_sample")
+
+
+def quantize_rows_i8(x, codes, scales):
+    """x [..., K] (bf16 or fp32) -> codes int8 of its shape, scales fp32, one a row."""
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must be [..., K]")
+    K = x.shape[-1]
+    rows = x.numel() // K
+    if codes.dtype != torch.int8 or codes.shape != x.shape:
+        raise ValueError("codes must be int8, of x's shape")
+    _check(lib().moe_quantize_rows_i8(rows, K, _code(x, "x"), _p(x), _p(codes),
+                                      _vec(scales, rows, torch.float32, "scales"), _stream()),
+           "moe_quantize_rows_i8")
+
+
+class I8Weight:
+    """A weight [N, K] in 8-bit integers (device tensors): codes int8 [N, K], scales
+    fp32 [N].  W = scales * codes."""
+
+    def __init__(self, codes, scales):
+        if codes.dtype != torch.int8 or scales.dtype != torch.float32:
+            raise ValueError("codes must be int8 and scales float32")
+        if codes.dim() != 2 or tuple(scales.shape) != (codes.shape[0],):
+            raise ValueError("codes must be [N, K] and scales [N]")
+        self._codes, self._scales = codes, scales
+        self._n, self._k = codes.shape
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    n = property(lambda self: self._n)
+    k = property(lambda self: self._k)
+
+
+def quantize_i8(W):
+    """W [N, K] (bf16 or fp32), a row an output -> I8Weight."""
+    if W.dim() != 2:
+        raise ValueError("W must be [N, K]")
+    codes = torch.empty(W.shape, dtype=torch.int8, device=W.device)
+    scales = torch.empty(W.shape[0], device=W.device)
+    quantize_rows_i8(W, codes, scales)
+    return I8Weight(codes, scales)
+
+
+def workspace_size_linear_i8(rows, w):
+    v = ctypes.c_size_t()
+    _check(lib().moe_workspace_size_linear_i8(int(rows), w.n, w.k, ctypes.byref(v)),
+           "moe_workspace_size_linear_i8")
+    return v.value
+
+
+def alloc_workspace_linear_i8(rows, w, device="cuda"):
+    return torch.zeros(workspace_size_linear_i8(rows, w), dtype=torch.uint8, device=device)
+
+
+def linear_i8(x, w, y, ws, x_scale=None, bias=None):
+    """y [..., N] (bf16 or fp32) = x [..., K] . W^T + bias; w: I8Weight [N,K].  x: codes
+    int8 with x_scale (fp32, one a row), or bf16 or fp32 values, quantised in the call."""
+    xs, ys = x.shape, y.shape
+    if not xs or xs[-1] != w.k:
+        raise ValueError("x must be [..., K]")
+    if not ys or ys[-1] != w.n or ys[:-1] != xs[:-1]:
+        raise ValueError("y must be [..., N]")
+    rows = x.numel() // w.k
+    coded = x.dtype == torch.int8
+    if coded != (x_scale is not None):
+        raise ValueError("x_scale belongs to codes (int8), and codes need it")
+    b, wb = _ws(ws)
+    _check(lib().moe_linear_i8(rows, w.n, w.k, _p(x), 2 if coded else _code(x, "x"),
+                               _vec(x_scale, rows, torch.float32, "x_scale"), _p(w.codes),
+                               _p(w.scales), _vec(bias, w.n, torch.float32, "bias"), _p(y),
+                               _code(y, "y"), b, wb, _stream()), "moe_linear_i8")
 
 
 def probe_fp32_fma(iters, out):

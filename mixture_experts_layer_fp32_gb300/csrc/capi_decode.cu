@@ -1,5 +1,6 @@
-// C ABI of a decoding step: the whole layer for a few tokens and the choice of the
-// next token.  Argument checks and workspace carve-up, as in capi.cu.
+// C ABI of a decoding step: the whole layer for a few tokens, the choice of the next
+// token, products in 8-bit integers.  Argument checks and workspace carve-up, as in
+// capi.cu.
 #include "common.cuh"
 
 namespace {
@@ -39,6 +40,12 @@ moe_status validate_few(const moe_config* cfg, int32_t fs) {
   // a row's inputs and all rows' inputs are counted in 32 bits
   constexpr int32_t most = 1 << 21;
   if (cfg->hidden > most || cfg->ffn_hidden > most || fs > most) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status validate_i8(int64_t rows, int32_t N, int32_t K) {
+  if (rows < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > 131056 || N > (1 << 28) || rows > (1 << 28)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -112,6 +119,45 @@ moe_status moe_sample(int64_t rows, int32_t vocab, int32_t dtype, const void* lo
   const SampleChoices own = {c.temperature,    c.top_k,    c.top_p,    c.min_p,
                              c.temperature_of, c.top_k_of, c.top_p_of, c.min_p_of};
   MOE_CUDA(launch_sample(rows, vocab, dtype, logits, u, own, tokens, prob, stream));
+  return MOE_OK;
+}
+
+moe_status moe_quantize_rows_i8(int64_t rows, int32_t K, int32_t dtype, const void* x,
+                                int8_t* codes, float* scales, moe_stream_t stream) {
+  MOE_TRY(validate_i8(rows, 1, K));
+  if (!is_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(x, rows));
+  MOE_TRY(need(codes, rows));
+  MOE_TRY(need(scales, rows, 4));
+  if (rows == 0) return MOE_OK;
+  MOE_CUDA(launch_quantize_rows_i8(rows, K, dtype, x, codes, scales, stream));
+  return MOE_OK;
+}
+
+moe_status moe_workspace_size_linear_i8(int64_t rows, int32_t N, int32_t K, size_t* bytes) {
+  MOE_TRY(validate_i8(rows, N, K));
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = kErrBytes + i8_linear_scratch(rows, N, K);
+  return MOE_OK;
+}
+
+moe_status moe_linear_i8(int64_t rows, int32_t N, int32_t K, const void* x, int32_t x_dtype,
+                         const float* x_scale, const int8_t* W, const float* w_scale,
+                         const float* bias, void* y, int32_t y_dtype, void* ws, size_t ws_bytes,
+                         moe_stream_t stream) {
+  MOE_TRY(validate_i8(rows, N, K));
+  if ((!is_dtype(x_dtype) && x_dtype != MOE_I8) || !is_dtype(y_dtype)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(x, rows));
+  if (x_dtype == MOE_I8) MOE_TRY(need(x_scale, rows, 4));
+  else if (x_scale != nullptr) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(W, 1));
+  MOE_TRY(need(w_scale, 1, 4));
+  MOE_TRY(optional(bias, 4));
+  MOE_TRY(need(y, rows));
+  MOE_TRY(check_ws(ws, ws_bytes, kErrBytes + i8_linear_scratch(rows, N, K)));
+  if (rows == 0) return MOE_OK;
+  MOE_CUDA(launch_linear_i8(rows, N, K, x, x_dtype, x_scale, W, w_scale, bias, y, y_dtype,
+                            past_error_word(ws), static_cast<int*>(ws), stream));
   return MOE_OK;
 }
 

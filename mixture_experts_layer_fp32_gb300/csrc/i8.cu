@@ -1,0 +1,291 @@
+// 8-bit integers: rows to codes with a scale each, and the product for few rows.
+#include "i8.cuh"
+
+namespace moe {
+namespace i8 {
+namespace {
+
+// ------------------------------------------------------------------ quantising
+// A row's scale is its largest magnitude over 127, in fp32, a code the nearest whole
+// number of x over the scale, ties to even: the quotient is estimated by a product
+// with the reciprocal, and what is left of x (exact by fma: it has few bits) decides
+// whether the neighbour is nearer.  A row's values stay in registers between the
+// search and the codes as far as a block holds them (kHeld 16-byte pieces a thread).
+// Bound by memory.
+constexpr int kQuantThreads = 256, kHeld = 4;
+
+template <typename T>
+struct Piece {
+  static constexpr int n = 16 / sizeof(T);
+  T v[n];
+};
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+__device__ __forceinline__ int code_of(float x, float scale, float inverse) {
+  float q = rintf(x * inverse);
+  const float twice = 2.f * fmaf(-q, scale, x);
+  const bool odd = static_cast<int>(q) & 1;
+  if (twice > scale || (twice == scale && odd)) q += 1.f;
+  else if (-twice > scale || (-twice == scale && odd)) q -= 1.f;
+  return static_cast<int>(fminf(fmaxf(q, -127.f), 127.f));
+}
+
+__device__ __forceinline__ void store_codes(int8_t* at, const int (&c)[4]) {
+  const char4 v = make_char4(c[0], c[1], c[2], c[3]);
+  *reinterpret_cast<char4*>(at) = v;
+}
+__device__ __forceinline__ void store_codes(__half* at, const int (&c)[4]) {
+  const __half2 v[2] = {__halves2half2(__int2half_rn(c[0]), __int2half_rn(c[1])),
+                        __halves2half2(__int2half_rn(c[2]), __int2half_rn(c[3]))};
+  memcpy(at, v, 8);
+}
+
+template <typename T, typename Code>
+__global__ void __launch_bounds__(kQuantThreads)
+    quantize_kernel(int K, const T* x, Code* codes, float* scales) {
+  constexpr int V = Piece<T>::n;
+  __shared__ float tops[kQuantThreads / 32];
+  const int64_t row = blockIdx.x;
+  const T* xr = x + row * K;
+  Code* out = codes + row * K;
+  pdl_trigger();
+  Piece<T> held[kHeld];
+  float top = 0.f;
+  bool good = true;  // neither an infinity nor a NaN
+  auto look = [&](const Piece<T>& p) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float a = fabsf(as_float(p.v[i]));
+      top = fmaxf(top, a);
+      good &= a < INFINITY;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int k = (i * kQuantThreads + threadIdx.x) * V;
+    if (k < K) memcpy(&held[i], __builtin_assume_aligned(xr + k, 16), 16);
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if ((i * kQuantThreads + threadIdx.x) * V < K) look(held[i]);
+  for (int k = (kHeld * kQuantThreads + threadIdx.x) * V; k < K; k += kQuantThreads * V) {
+    Piece<T> p;
+    memcpy(&p, __builtin_assume_aligned(xr + k, 16), 16);
+    look(p);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+  good = __syncthreads_and(good);
+#pragma unroll
+  for (int w = 0; w < kQuantThreads / 32; ++w) top = fmaxf(top, tops[w]);
+  const float scale = good ? top / 127.f : NAN;
+  if (threadIdx.x == 0) scales[row] = scale;
+  // no reciprocal of a scale past 2^-126 is lost to overflow
+  const float up = scale < 0x1p-100f ? 0x1p64f : 1.f;
+  const bool some = scale > 0.f;  // neither 0 nor NaN
+  const float s = scale * up, inverse = some ? 1.f / s : 0.f;
+  auto put = [&](const Piece<T>& p, int k) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      int c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = some ? code_of(as_float(p.v[i + j]) * up, s, inverse) : 0;
+      store_codes(out + k + i, c);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int k = (i * kQuantThreads + threadIdx.x) * V;
+    if (k < K) put(held[i], k);
+  }
+  for (int k = (kHeld * kQuantThreads + threadIdx.x) * V; k < K; k += kQuantThreads * V) {
+    Piece<T> p;
+    memcpy(&p, __builtin_assume_aligned(xr + k, 16), 16);
+    put(p, k);
+  }
+}
+
+template <typename T, typename Code>
+cudaError_t quantize(int64_t rows, int K, const void* x, Code* codes, float* scales,
+                     cudaStream_t s) {
+  quantize_kernel<T, Code><<<static_cast<unsigned>(rows), kQuantThreads, 0, s>>>(
+      K, static_cast<const T*>(x), codes, scales);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ few rows
+// Sixteen outputs to a warp, 8 NT rows of x as the columns of the integer
+// instruction m16n8k32, whose sums are whole.  64 inputs of a row of W are 16 bytes to
+// each of four lanes: the inputs are permuted within 64, the same for x, so that both
+// operands come straight from memory in 16-byte pieces.  A block's 8 warps share
+// 8 / parts groups of 16 outputs, `parts` warps to the inputs of one.
+constexpr int kNarrowWarps = 8;
+constexpr int kSteps = 4;  // of 64 inputs, in flight
+
+__device__ __forceinline__ uint4 read_codes(const int8_t* p, bool there) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (there) v = __ldg(reinterpret_cast<const uint4*>(p));
+  return v;
+}
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kNarrowWarps * 32)
+    narrow_kernel(const __grid_constant__ Args a, int parts, int first_row) {
+  __shared__ int sums[kNarrowWarps][16 * 8 * NT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int part = warp % parts, group = blockIdx.x * (kNarrowWarps / parts) + warp / parts;
+  const int n0 = group * 16;
+  const int64_t row0 = static_cast<int64_t>(first_row) + blockIdx.y * 8 * NT;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(8 * NT), a.rows - row0));
+  int acc[NT][4];
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[c][i] = 0;
+  const int steps = (a.K + 63) / 64;
+  const int begin = steps * part / parts, end = steps * (part + 1) / parts;
+  // outputs and rows past the last one repeat it; what they give is not stored
+  const int8_t* w0 = a.W + static_cast<int64_t>(min(n0 + g, a.N - 1)) * a.K + t * 16;
+  const int8_t* w1 = a.W + static_cast<int64_t>(min(n0 + g + 8, a.N - 1)) * a.K + t * 16;
+  const int8_t* xs[NT];
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+    xs[c] = a.x + (row0 + min(c * 8 + g, rows - 1)) * a.K + t * 16;
+  uint4 w[2][kSteps][2];
+  auto load = [&](int set, int step) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int k = (step + i) * 64;
+      const bool there = step + i < end && k + t * 16 < a.K;
+      w[set][i][0] = read_codes(w0 + k, there);
+      w[set][i][1] = read_codes(w1 + k, there);
+    }
+  };
+  load(0, begin);
+  pdl_wait();  // x
+  auto use = [&](int set, int step) {
+    uint4 x[NT][kSteps];
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int k = (step + i) * 64;
+        x[c][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (step + i < end && k + t * 16 < a.K)
+          x[c][i] = *reinterpret_cast<const uint4*>(xs[c] + k);
+      }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        const uint4 &p = w[set][i][0], &q = w[set][i][1], &v = x[c][i];
+        mma_s8(acc[c], p.x, q.x, p.y, q.y, v.x, v.y);
+        mma_s8(acc[c], p.z, q.z, p.w, q.w, v.z, v.w);
+      }
+  };
+  for (int s = begin; s < end; s += 2 * kSteps) {
+    load(1, s + kSteps);
+    use(0, s);
+    load(0, s + 2 * kSteps);
+    use(1, s + kSteps);
+  }
+  // sums[warp][column][output]
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sums[warp][(c * 8 + t * 2 + (i & 1)) * 16 + g + (i >> 1) * 8] = acc[c][i];
+  __syncthreads();
+  const int groups = kNarrowWarps / parts;
+  for (int i = threadIdx.x; i < groups * rows * 16; i += kNarrowWarps * 32) {
+    const int n = i & 15, at = i >> 4, gr = at % groups, m = at / groups;
+    const int out = (blockIdx.x * groups + gr) * 16 + n;
+    if (out >= a.N) continue;
+    int sum = 0;
+    for (int p = 0; p < parts; ++p) sum += sums[gr * parts + p][m * 16 + n];
+    const float v = scaled(sum, a.x_scale[row0 + m], a.w_scale[out], a.bias ? a.bias[out] : 0.f);
+    const int64_t to = (row0 + m) * a.N + out;
+    if (a.out_f32) static_cast<float*>(a.y)[to] = v;
+    else static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
+  }
+}
+
+// The kernel reads weights before it waits for the launch before it, which therefore
+// has to be this call's own quantising (itself begun after all that came earlier);
+// after anything else it is launched as usual.
+template <int NT>
+cudaError_t narrow(const Args& a, bool after_own, cudaStream_t s) {
+  // warps for 16 on each of 152 SMs, where the inputs allow it
+  const int groups = (a.N + 15) / 16;
+  int parts = 1;
+  while (parts < kNarrowWarps && groups * parts < 2432 && a.K / (parts * 2) >= 256) parts *= 2;
+  const int each = kNarrowWarps / parts;
+  for (int64_t r = 0; r < a.rows; r += 65535ll * 8 * NT) {
+    const int64_t left = (a.rows - r + 8 * NT - 1) / (8 * NT);
+    const dim3 grid((groups + each - 1) / each, static_cast<unsigned>(left < 65535 ? left : 65535));
+    const dim3 block(kNarrowWarps * 32);
+    cudaError_t st;
+    if (after_own) {
+      st = launch_dependent(narrow_kernel<NT>, grid, block, 0, s, a, parts, static_cast<int>(r));
+    } else {
+      narrow_kernel<NT><<<grid, block, 0, s>>>(a, parts, static_cast<int>(r));
+      st = cudaGetLastError();
+    }
+    if (st != cudaSuccess) return st;
+    after_own = false;
+  }
+  return cudaSuccess;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+}  // namespace i8
+
+cudaError_t launch_quantize_rows_i8(int64_t rows, int K, int dtype, const void* x, int8_t* codes,
+                                    float* scales, cudaStream_t s) {
+  return dtype == MOE_F32 ? i8::quantize<float>(rows, K, x, codes, scales, s)
+                          : i8::quantize<__nv_bfloat16>(rows, K, x, codes, scales, s);
+}
+
+// Codes and scales of x, where it does not come as such.
+size_t i8_linear_scratch(int64_t rows, int N, int K) {
+  (void)N;
+  return i8::up256(static_cast<size_t>(rows) * K) + i8::up256(static_cast<size_t>(rows) * 4);
+}
+
+cudaError_t launch_linear_i8(int64_t rows, int N, int K, const void* x, int x_dtype,
+                             const float* x_scale, const int8_t* W, const float* w_scale,
+                             const float* bias, void* y, int y_dtype, void* scratch, int* err,
+                             cudaStream_t s) {
+  i8::Args a = {};
+  a.rows = static_cast<int>(rows), a.N = N, a.K = K;
+  a.W = W, a.w_scale = w_scale, a.bias = bias;
+  a.y = y, a.out_f32 = y_dtype == MOE_F32;
+  a.err = err;
+  if (x_dtype == MOE_I8) {
+    a.x = static_cast<const int8_t*>(x);
+    a.x_scale = x_scale;
+  } else {
+    int8_t* codes = static_cast<int8_t*>(scratch);
+    float* scales = reinterpret_cast<float*>(static_cast<char*>(scratch) +
+                                             i8::up256(static_cast<size_t>(rows) * K));
+    const cudaError_t st = launch_quantize_rows_i8(rows, K, x_dtype, x, codes, scales, s);
+    if (st != cudaSuccess) return st;
+    a.x = codes, a.x_scale = scales;
+  }
+  const bool own = x_dtype != MOE_I8;
+  return rows <= 8 ? i8::narrow<1>(a, own, s) : i8::narrow<2>(a, own, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,193 @@
+"""8-bit integers on the GPU: quantising and the product.  Both are defined to the bit: codes are
+the nearest whole number of the exact quotient, sums are whole, and each rounding after them is
+named; so everything here is equality, but for a bias (fma, half a step of fp32)."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def quantised(x):
+    """Codes and scales by the definition, in 64 bits (a quotient of two fp32 numbers that is not
+    half of an odd number is further from one than 64 bits lose)."""
+    x = x.float()
+    # (torch multiplies fp32 by the reciprocal of a number, so the quotient is formed in 64 bits)
+    s = (x.abs().amax(-1).double() / 127).float()
+    bad = ~torch.isfinite(x).all(-1)
+    safe = torch.where((s > 0) & ~bad, s, 1.0)
+    q = torch.round(x.double() / safe.double()[..., None]).clamp(-127, 127)
+    q = torch.where(((s > 0) & ~bad)[..., None], q, 0.0)
+    return q.to(torch.int8), torch.where(bad, float("nan"), s)
+
+
+def product(xq, xs, wq, ws, out, bias=None):
+    whole = xq.double() @ wq.double().t()  # exact: below 2^31
+    y = whole.float() * xs[:, None]
+    if bias is None:
+        return (y * ws).to(out)
+    return y.double() * ws.double() + bias.double()
+
+
+def codes(shape, seed, top=127):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-top - (top == 127), top + 1, shape, dtype=torch.int8, device="cuda",
+                         generator=g)
+
+
+def scales(n, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return 1e-3 * (0.1 + torch.rand(n, device="cuda", generator=g))
+
+
+def linear(x, wq, ws, out, x_scale=None, bias=None, workspace=None):
+    import mixture_experts_layer_fp32_gb300 as moe
+    w = moe.I8Weight(wq, ws)
+    m, n = x.shape[0], w.n
+    room = torch.full((m * n + 128,), 7.0, dtype=out, device="cuda")
+    y = room[64:64 + m * n].view(m, n)
+    workspace = moe.alloc_workspace_linear_i8(m, w) if workspace is None else workspace
+    moe.linear_i8(x, w, y, workspace, x_scale=x_scale, bias=bias)
+    moe.check(workspace)
+    assert room[:64].eq(7).all() and room[64 + m * n:].eq(7).all()
+    return y
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,K", [(1, 16), (3, 48), (7, 1040), (2, 4096), (5, 8208), (300, 256),
+                                    (2, 131056)])
+def test_quantise(rows, K, dtype):
+    import mixture_experts_layer_fp32_gb300 as moe
+    g = torch.Generator(device="cuda").manual_seed(rows + K)
+    x = torch.randn(rows, K, device="cuda", generator=g)
+    x[0] *= 1e-20
+    x[-1, 5:9] = 100.0
+    x = x.to(DT[dtype])
+    q = torch.full(x.shape, 99, dtype=torch.int8, device="cuda")
+    s = torch.full((rows,), 7.0, device="cuda")
+    moe.quantize_rows_i8(x, q, s)
+    rq, rs = quantised(x)
+    assert torch.equal(s, rs) and torch.equal(q, rq)
+    w = moe.quantize_i8(x)
+    assert torch.equal(w.codes, rq) and torch.equal(w.scales, rs)
+
+
+def test_quantise_borders_and_special_values():
+    """Quotients that are a half of an odd number go to the even code; zeros, the smallest and
+    largest numbers, infinities and NaN."""
+    import mixture_experts_layer_fp32_gb300 as moe
+    K, rows = 256, 12
+    half = torch.arange(-127, 128, device="cuda").float() / 2     # scale 1: x / s = n / 2
+    x = torch.zeros(rows, K, device="cuda")
+    x[0, :255], x[0, 255] = half, 127.0
+    x[1] = x[0] * 2.0 ** -100
+    x[2] = x[0] * 2.0 ** -130                                     # a scale below the normal ones
+    x[3] = x[0] * 2.0 ** -142
+    x[5] = x[0] * 2.0 ** 120
+    x[6, 3] = torch.finfo(torch.float32).max
+    x[7, 9] = float("inf")
+    x[8, 200], x[8, 1] = float("nan"), 5.0
+    x[9] = 1e-45
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x[10:] = torch.randn(2, K, device="cuda", generator=g)
+    x[11, 7] = -9.0
+    q = torch.empty(x.shape, dtype=torch.int8, device="cuda")
+    s = torch.empty(rows, device="cuda")
+    moe.quantize_rows_i8(x, q, s)
+    rq, rs = quantised(x)
+    assert torch.equal(torch.isnan(s), torch.isnan(rs))
+    assert torch.equal(s.nan_to_num(-1), rs.nan_to_num(-1))
+    assert torch.equal(q, rq)
+    assert int(q[0, 130]) == 2 and int(q[0, 128]) == 0            # 1.5 -> 2, 0.5 -> 0
+
+
+SHAPES = [(1, 1, 16), (1, 17, 64), (1, 4096, 512), (2, 33, 48), (5, 16, 1040), (8, 100, 4112),
+          (9, 40, 128), (13, 1437, 720), (16, 256, 1024), (17, 300, 2064), (31, 129, 1152),
+          (33, 130, 4096), (64, 511, 1536), (65, 257, 1040), (100, 128, 8208), (129, 1000, 256),
+          (200, 300, 3088), (257, 513, 1168), (300, 64, 16)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product_of_codes(M, N, K, out):
+    xq, wq, xs, ws = codes((M, K), M + K), codes((N, K), N), scales(M, M), scales(N, N)
+    y = linear(xq, wq, ws, DT[out], x_scale=xs)
+    assert torch.equal(y, product(xq, xs, wq, ws, DT[out]))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 131056), (20, 40, 131056), (70, 300, 16384),
+                                   (300, 260, 16400)])
+def test_sums_past_what_fp32_holds(M, N, K):
+    """All codes at their ends: sums near 2^31."""
+    xq = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    wq = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    wq[::2] = 127
+    xq[:, 3], wq[:, 5] = 1, 1
+    xs, ws = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    y = linear(xq, wq, ws, torch.float32, x_scale=xs)
+    assert torch.equal(y, product(xq, xs, wq, ws, torch.float32))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", SHAPES[:14])
+def test_product_of_values(M, N, K, dtype):
+    g = torch.Generator(device="cuda").manual_seed(M * N)
+    x = torch.randn(M, K, device="cuda", generator=g).to(DT[dtype])
+    wq, ws = codes((N, K), N), scales(N, N)
+    y = linear(x, wq, ws, torch.float32)
+    xq, xs = quantised(x)
+    assert torch.equal(y, product(xq, xs, wq, ws, torch.float32))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 33, 80), (12, 513, 1024), (150, 260, 528)])
+def test_bias(M, N, K):
+    xq, wq, xs, ws = codes((M, K), M + K), codes((N, K), N), scales(M, M), scales(N, N)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    bias = torch.randn(N, device="cuda", generator=g)
+    y = linear(xq, wq, ws, torch.float32, x_scale=xs, bias=bias)
+    want = product(xq, xs, wq, ws, None, bias)
+    assert bool(((y.double() - want).abs() <= 2.0 ** -24 * want.abs() * (1 + 1e-6) + 1e-30).all())
+    y16 = linear(xq, wq, ws, torch.bfloat16, x_scale=xs, bias=bias)
+    assert torch.equal(y16, y.to(torch.bfloat16))
+
+
+def test_rows_that_are_not_numbers_stay_alone():
+    x = torch.randn(20, 64, device="cuda")
+    x[3, 5], x[17, 9] = float("inf"), float("nan")
+    wq, ws = codes((50, 64), 1), scales(50, 1)
+    y = linear(x, wq, ws, torch.float32)
+    bad = torch.zeros(20, dtype=torch.bool)
+    bad[3] = bad[17] = True
+    assert torch.equal(torch.isnan(y).all(1).cpu(), bad)
+    assert torch.equal(torch.isnan(y).any(1).cpu(), bad)
+
+
+def test_no_rows_and_a_workspace_of_more():
+    import mixture_experts_layer_fp32_gb300 as moe
+    wq, ws = codes((70, 256), 1), scales(70, 1)
+    w = moe.I8Weight(wq, ws)
+    room = moe.alloc_workspace_linear_i8(300, w)
+    for M in (300, 64, 20, 9, 1, 0):
+        x = torch.randn(M, 256, device="cuda")
+        y = linear(x, wq, ws, torch.float32, workspace=room)
+        xq, xs = quantised(x) if M else (x, x[:, 0])
+        assert M == 0 or torch.equal(y, product(xq, xs, wq, ws, torch.float32))
+
+
+def test_weights_just_quantised_are_read():
+    """The product follows the quantising of its weights at once, many times."""
+    import mixture_experts_layer_fp32_gb300 as moe
+    g = torch.Generator(device="cuda").manual_seed(1)
+    W = [torch.randn(4096, 1024, device="cuda", generator=g) for _ in range(4)]
+    w = moe.quantize_i8(W[0])
+    for M in (1, 8, 12, 40, 200):
+        xq, xs = codes((M, 1024), M), scales(M, M)
+        y = torch.empty(M, 4096, device="cuda")
+        ws = moe.alloc_workspace_linear_i8(M, w)
+        for i in range(12):
+            moe.quantize_rows_i8(W[i % 4], w.codes, w.scales)
+            moe.linear_i8(xq, w, y, ws, x_scale=xs)
+            got = y.clone()
+            wq, wsc = quantised(W[i % 4])
+            assert torch.equal(got, product(xq, xs, wq, wsc, torch.float32))
