@@ -137,7 +137,7 @@ moe_status moe_quantize_rows_i8(int64_t rows, int32_t K, int32_t dtype, const vo
 moe_status moe_workspace_size_linear_i8(int64_t rows, int32_t N, int32_t K, size_t* bytes) {
   MOE_TRY(validate_i8(rows, N, K));
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-  *bytes = kErrBytes + i8_linear_scratch(rows, N, K);
+  *bytes = kErrBytes + i8_linear_scratch_most(rows, N, K);
   return MOE_OK;
 }
 

@@ -357,7 +357,9 @@ cudaError_t launch_few(const moe_config& c, int fs, int64_t capacity, const void
 // ---- 8-bit integers (i8.cu, i8_wide.cu) ----
 cudaError_t launch_quantize_rows_i8(int64_t rows, int K, int dtype, const void* x, int8_t* codes,
                                     float* scales, cudaStream_t s);
+// bytes of scratch of one call, and the most that a call of up to `rows` rows needs
 size_t i8_linear_scratch(int64_t rows, int N, int K);
+size_t i8_linear_scratch_most(int64_t rows, int N, int K);
 cudaError_t launch_linear_i8(int64_t rows, int N, int K, const void* x, int x_dtype,
                              const float* x_scale, const int8_t* W, const float* w_scale,
                              const float* bias, void* y, int y_dtype, void* scratch, int* err,

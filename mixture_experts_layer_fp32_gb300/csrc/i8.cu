@@ -247,6 +247,23 @@ cudaError_t narrow(const Args& a, bool after_own, cudaStream_t s) {
   return cudaSuccess;
 }
 
+// Codes as fp16 numbers, for the wide kernel.
+__global__ void __launch_bounds__(256) halves_kernel(int64_t n, const int8_t* codes, __half* out) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 16;
+  pdl_trigger();
+  if (i >= n) return;  // n is a multiple of 16
+  const int4 q = *reinterpret_cast<const int4*>(codes + i);
+  int8_t c[16];
+  memcpy(c, &q, 16);
+  __half h[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) h[j] = __int2half_rn(c[j]);
+  uint4 v[2];
+  memcpy(v, h, 32);
+  *reinterpret_cast<uint4*>(out + i) = v[0];
+  *reinterpret_cast<uint4*>(out + i + 8) = v[1];
+}
+
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
@@ -258,34 +275,80 @@ cudaError_t launch_quantize_rows_i8(int64_t rows, int K, int dtype, const void* 
                           : i8::quantize<__nv_bfloat16>(rows, K, x, codes, scales, s);
 }
 
-// Codes and scales of x, where it does not come as such.
-size_t i8_linear_scratch(int64_t rows, int N, int K) {
-  (void)N;
-  return i8::up256(static_cast<size_t>(rows) * K) + i8::up256(static_cast<size_t>(rows) * 4);
+// Up to so many rows take the narrow kernel.
+constexpr int64_t kNarrowRows = 8;
+
+// x as codes or fp16 numbers, its scales, partial sums.
+struct LinearScratch {
+  size_t scales, part, total;
+};
+static LinearScratch linear_scratch(int64_t rows, int N, int K) {
+  LinearScratch L;
+  L.scales = i8::up256(static_cast<size_t>(rows) * K * (rows <= kNarrowRows ? 1 : 2));
+  L.part = L.scales + i8::up256(static_cast<size_t>(rows) * 4);
+  const int splits = rows <= kNarrowRows ? 1 : i8::wide_splits(rows, N, K);
+  L.total = L.part + (splits > 1 ? static_cast<size_t>(splits) * rows * N * 4 : 0);
+  return L;
+}
+size_t i8_linear_scratch(int64_t rows, int N, int K) { return linear_scratch(rows, N, K).total; }
+
+// What any call of up to so many rows needs: the most rows of each number of parts are
+// among those that fill 32, 64 or multiples of 128 columns, and past 152 chunks of 128
+// nothing is cut.
+size_t i8_linear_scratch_most(int64_t rows, int N, int K) {
+  size_t most = i8_linear_scratch(rows, N, K);
+  auto look = [&](int64_t r) {
+    const size_t bytes = i8_linear_scratch(r < rows ? r : rows, N, K);
+    most = bytes > most ? bytes : most;
+  };
+  look(kNarrowRows);
+  look(32);
+  look(64);
+  for (int64_t r = 128; r < rows && r <= 152 * 128; r += 128) look(r);
+  return most;
 }
 
 cudaError_t launch_linear_i8(int64_t rows, int N, int K, const void* x, int x_dtype,
                              const float* x_scale, const int8_t* W, const float* w_scale,
                              const float* bias, void* y, int y_dtype, void* scratch, int* err,
                              cudaStream_t s) {
+  const LinearScratch L = linear_scratch(rows, N, K);
+  char* at = static_cast<char*>(scratch);
   i8::Args a = {};
   a.rows = static_cast<int>(rows), a.N = N, a.K = K;
   a.W = W, a.w_scale = w_scale, a.bias = bias;
   a.y = y, a.out_f32 = y_dtype == MOE_F32;
   a.err = err;
-  if (x_dtype == MOE_I8) {
+  a.x_scale = x_scale;
+  float* scales = reinterpret_cast<float*>(at + L.scales);
+  const bool coded = x_dtype == MOE_I8;
+  if (!coded) a.x_scale = scales;
+  if (rows <= kNarrowRows) {
     a.x = static_cast<const int8_t*>(x);
-    a.x_scale = x_scale;
-  } else {
-    int8_t* codes = static_cast<int8_t*>(scratch);
-    float* scales = reinterpret_cast<float*>(static_cast<char*>(scratch) +
-                                             i8::up256(static_cast<size_t>(rows) * K));
-    const cudaError_t st = launch_quantize_rows_i8(rows, K, x_dtype, x, codes, scales, s);
-    if (st != cudaSuccess) return st;
-    a.x = codes, a.x_scale = scales;
+    if (!coded) {
+      int8_t* codes = reinterpret_cast<int8_t*>(at);
+      const cudaError_t st = launch_quantize_rows_i8(rows, K, x_dtype, x, codes, scales, s);
+      if (st != cudaSuccess) return st;
+      a.x = codes;
+    }
+    return i8::narrow<1>(a, !coded, s);
   }
-  const bool own = x_dtype != MOE_I8;
-  return rows <= 8 ? i8::narrow<1>(a, own, s) : i8::narrow<2>(a, own, s);
+  __half* halves = reinterpret_cast<__half*>(at);
+  cudaError_t st;
+  if (coded) {
+    const int64_t n = rows * K;
+    i8::halves_kernel<<<static_cast<unsigned>((n / 16 + 255) / 256), 256, 0, s>>>(
+        n, static_cast<const int8_t*>(x), halves);
+    st = cudaGetLastError();
+  } else if (x_dtype == MOE_F32) {
+    st = i8::quantize<float>(rows, K, x, halves, scales, s);
+  } else {
+    st = i8::quantize<__nv_bfloat16>(rows, K, x, halves, scales, s);
+  }
+  if (st != cudaSuccess) return st;
+  a.splits = i8::wide_splits(rows, N, K);
+  a.part = reinterpret_cast<int32_t*>(at + L.part);
+  return i8::launch_wide(a, halves, s);
 }
 
 }  // namespace moe

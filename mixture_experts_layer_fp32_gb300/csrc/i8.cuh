@@ -27,8 +27,10 @@ __device__ __forceinline__ float scaled(int sum, float x_scale, float w_scale, f
   return __fmaf_rn(static_cast<float>(sum) * x_scale, w_scale, bias);
 }
 
-cudaError_t launch_wide(const Args& a, const __half* x, int64_t x_stride, cudaStream_t s);
+// More rows (i8_wide.cu): x as fp16 numbers, laid out by the launch before; the weights
+// are read before that has ended.
 int wide_splits(int64_t rows, int N, int K);
+cudaError_t launch_wide(const Args& a, const __half* x, cudaStream_t s);
 
 }  // namespace i8
 }  // namespace moe

@@ -1,0 +1,446 @@
+// 8-bit integer products for more rows: tcgen05 on whole numbers in fp16.
+//
+// This chip's integer tensor-core instruction runs at 150 TOP/s (measured), fp16 at
+// 1.9 PFLOP/s: so the codes become fp16 numbers, which hold them exactly.  x is laid
+// out as fp16 by the launch before (it is the smaller operand); W stays in 8 bits until
+// it is on the SM, where warps turn it into the A operand in the tensor memory (a byte
+// under a mask with 0x64 before it is the fp16 number 1024 + 128 + code; a subtraction
+// takes the 1152 off).  A product is 2^14 at most, so fp32 sums of 1024 of them are whole
+// numbers up to 2^24, exact; then they are read out and added up as integers.
+//
+// A block, one to an SM, takes 256 outputs (two tiles of 128, which share x) of NC rows
+// of x at a time, with roles for its warps that hand each other slots through
+// mbarriers:
+//   8 add up: an output of both tiles to a thread and half of the columns each;
+//   8 convert: an output of a tile to a thread, 128 inputs at a time;
+//   one copies W (TMA), one x (TMA), one thread multiplies.
+// The two tiles' sums are read out 4 blocks of 128 inputs apart, so that products of
+// one go on while the other's are read.
+#include "i8.cuh"
+#include "roles.cuh"
+
+namespace moe {
+namespace i8 {
+namespace {
+
+using namespace roles;
+
+constexpr int kWarpsWide = 20;
+constexpr int kWStage = 2 * 128 * 128;       // of W: 128 inputs of both tiles
+constexpr int kExact = 8;                    // blocks of 128 inputs whose sums are exact
+template <int NC>
+struct Wide {
+  static constexpr int kWStages = NC == 128 ? 4 : 5;
+  static constexpr int kXStages = NC == 128 ? 3 : 4;
+  static constexpr int kXStage = NC * 256;
+  static constexpr int kSlots = 128 / NC;    // of sums, each tile's
+  static constexpr int kSmem = kWStages * kWStage + kXStages * kXStage + 1024;
+};
+
+struct Items {
+  int tiles, chunks, splits, blocks;  // blocks of 128 inputs
+  int total;
+};
+
+struct Bars {
+  uint64_t w_full[5], w_free[5];
+  uint64_t x_full[4], x_free[4];
+  uint64_t a_full[2][2], a_free[2][2];  // [tile][slot]
+  uint64_t d_full[2][4], d_free[2][4];
+  uint64_t products;
+};
+
+// One item: 256 outputs, NC rows, a part of the inputs.  Sixteen tiles of W go with all
+// chunks of x before the next sixteen: what runs at a time then reads few of either.
+constexpr int kRaster = 16;
+struct Item {
+  int tile, chunk, part, first, count;  // count: blocks of inputs
+  __device__ __forceinline__ Item(int i, const Items& s) {
+    part = i % s.splits;
+    i /= s.splits;
+    const int group = i / (kRaster * s.chunks), in = i - group * kRaster * s.chunks;
+    const int width = min(kRaster, s.tiles - group * kRaster);
+    chunk = in / width;
+    tile = group * kRaster + in - chunk * width;
+    first = static_cast<int>(static_cast<int64_t>(s.blocks) * part / s.splits);
+    count = static_cast<int>(static_cast<int64_t>(s.blocks) * (part + 1) / s.splits) - first;
+  }
+};
+// whether tile d's sums are read out after block b of an item
+__device__ __forceinline__ bool read_after(int d, int b, int count) {
+  return b + 1 == count || (b + 1) % kExact == d * (kExact / 2);
+}
+
+// Four codes to two pairs of fp16 numbers.
+__device__ __forceinline__ void pairs_of(uint32_t word, uint32_t& p, uint32_t& q) {
+  const uint32_t v = word ^ 0x80808080u;  // code + 128
+  const uint32_t lo = __byte_perm(v, 0x64646464u, 0x4140), hi = __byte_perm(v, 0x64646464u, 0x4342);
+  const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+  __half2 a, b;
+  memcpy(&a, &lo, 4);
+  memcpy(&b, &hi, 4);
+  a = __hsub2(a, off), b = __hsub2(b, off);
+  memcpy(&p, &a, 4);
+  memcpy(&q, &b, 4);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 q;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "r"(at)
+               : "memory");
+  return q;
+}
+
+template <int NC>
+__global__ void __launch_bounds__(kWarpsWide * 32, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                const __grid_constant__ Args a, const __grid_constant__ Items items) {
+  using W = Wide<NC>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t tmem_at;
+  __shared__ int given_up;
+  const uint32_t base = (ptx::smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t xs_at = base + W::kWStages * kWStage;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto bar = [](const uint64_t& b) { return ptx::smem_u32(&b); };
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < W::kWStages; ++i) {
+      ptx::mbar_init(bar(bars.w_full[i]), 1);
+      ptx::mbar_init(bar(bars.w_free[i]), 8);
+    }
+    for (int i = 0; i < W::kXStages; ++i) {
+      ptx::mbar_init(bar(bars.x_full[i]), 1);
+      ptx::mbar_init(bar(bars.x_free[i]), 1);
+    }
+    for (int d = 0; d < 2; ++d) {
+      for (int i = 0; i < 2; ++i) {
+        ptx::mbar_init(bar(bars.a_full[d][i]), 4);
+        ptx::mbar_init(bar(bars.a_free[d][i]), 1);
+      }
+      for (int i = 0; i < W::kSlots; ++i) {
+        ptx::mbar_init(bar(bars.d_full[d][i]), 1);
+        ptx::mbar_init(bar(bars.d_free[d][i]), 8);
+      }
+    }
+    ptx::mbar_init(bar(bars.products), 1);
+    given_up = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 18) {
+    ptx::tmem_alloc(ptx::smem_u32(&tmem_at), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  // sums: 128 columns a tile, [tile][slot]; A: 64 columns of 128 inputs, [tile][slot]
+  auto d_at = [&](int d, int slot) { return tmem + d * 128 + slot * NC; };
+  auto a_at = [&](int d, int slot) { return tmem + 256 + d * 128 + slot * 64; };
+  const Waits wait{a.err, &given_up};
+  const int step = gridDim.x;
+
+  // 640 threads are launched with 96 registers each; 256 with 152 and 384 with 56 are
+  // less than those.
+  if (warp < 8) {
+    registers<152, true>();
+    // ---- sums ----
+    constexpr int half = NC / 2;
+    const int e = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // << 16, by 32
+    pdl_wait();  // the rows' scales; and the output is free
+    Ring ring[2] = {{W::kSlots}, {W::kSlots}};
+    bool on = true;
+    for (int i = blockIdx.x; on && i < items.total; i += step) {
+      const Item it(i, items);
+      int acc[2][half];
+#pragma unroll
+      for (int c = 0; c < half; ++c) acc[0][c] = acc[1][c] = 0;
+#pragma unroll 1
+      for (int b = 0; on && b < it.count; ++b)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          if (!on || !read_after(d, b, it.count)) continue;
+          on = wait(bar(bars.d_full[d][ring[d].at]), ring[d].phase);
+          if (!on) break;
+          ptx::tc_fence_after();
+          const uint32_t at = d_at(d, ring[d].at) + lanes + e * half;
+#pragma unroll
+          for (int c = 0; c < half; c += 16) {
+            float v[16];
+            tmem_ld16(at + c, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 16; ++q) asm volatile("" : "+f"(v[q]));
+            if (c + 16 == half) {
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(bar(bars.d_free[d][ring[d].at]));
+            }
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[d][c + q] += __float2int_rn(v[q]);
+          }
+          ring[d].next();
+        }
+      if (!on) break;
+      const int row0 = it.chunk * NC + e * half;
+      const int rows = min(half, a.rows - row0);
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const int o = it.tile * 256 + d * 128 + r;
+        if (o >= a.N) continue;
+        if (items.splits > 1) {
+          int32_t* to = a.part + (static_cast<int64_t>(it.part) * a.rows + row0) * a.N + o;
+#pragma unroll
+          for (int c = 0; c < half; ++c) {
+            if (c >= rows) break;
+            to[static_cast<int64_t>(c) * a.N] = acc[d][c];
+          }
+          continue;
+        }
+        const float scale = a.w_scale[o], bias = a.bias ? a.bias[o] : 0.f;
+        const int64_t at = static_cast<int64_t>(row0) * a.N + o;
+#pragma unroll
+        for (int c = 0; c < half; ++c) {
+          if (c >= rows) break;
+          const float v = scaled(acc[d][c], __ldg(a.x_scale + row0 + c), scale, bias);
+          if (a.out_f32) static_cast<float*>(a.y)[at + static_cast<int64_t>(c) * a.N] = v;
+          else static_cast<__nv_bfloat16*>(a.y)[at + static_cast<int64_t>(c) * a.N] = __float2bfloat16_rn(v);
+        }
+      }
+    }
+  } else if (warp < 16) {
+    registers<56, false>();
+    // ---- codes ----
+    const int d = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t src = base + d * (kWStage / 2) + r * 128, swap = (r & 7) << 4;
+    Ring ws{W::kWStages}, as{2};
+    bool on = true;
+    for (int i = blockIdx.x; on && i < items.total; i += step) {
+      const Item it(i, items);
+#pragma unroll 1
+      for (int b = 0; b < it.count; ++b) {
+        on = wait(bar(bars.w_full[ws.at]), ws.phase) &&
+             wait(bar(bars.a_free[d][as.at]), as.phase ^ 1);
+        if (!on) break;
+        ptx::tc_fence_after();
+        const uint32_t from = src + ws.at * kWStage, to = a_at(d, as.at) + lanes;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // 32 inputs
+          const uint4 p = lds16(from + ((j * 32) ^ swap)), q = lds16(from + ((j * 32 + 16) ^ swap));
+          uint32_t v[16];
+          pairs_of(p.x, v[0], v[1]), pairs_of(p.y, v[2], v[3]);
+          pairs_of(p.z, v[4], v[5]), pairs_of(p.w, v[6], v[7]);
+          pairs_of(q.x, v[8], v[9]), pairs_of(q.y, v[10], v[11]);
+          pairs_of(q.z, v[12], v[13]), pairs_of(q.w, v[14], v[15]);
+          tmem_st16(to + j * 16, v);
+        }
+        tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(bars.w_free[ws.at]));
+          ptx::mbar_arrive(bar(bars.a_full[d][as.at]));
+        }
+        ws.next();
+        as.next();
+      }
+    }
+  } else {
+    registers<56, false>();
+    if (warp == 16) {
+      // ---- copies of W ----
+      Ring ws{W::kWStages};
+      bool on = true;
+      for (int i = blockIdx.x; on && i < items.total; i += step) {
+        const Item it(i, items);
+        const bool second = it.tile * 256 + 128 < a.N;
+        for (int b = 0; b < it.count; ++b) {
+          on = wait(bar(bars.w_free[ws.at]), ws.phase ^ 1);
+          if (!on) break;
+          if (lane == 0) {
+            const uint32_t dst = base + ws.at * kWStage, full = bar(bars.w_full[ws.at]);
+            ptx::mbar_arrive_expect_tx(full, second ? kWStage : kWStage / 2);
+            ptx::tma_load_2d(dst, &map_w, (it.first + b) * 128, it.tile * 256, full);
+            if (second)
+              ptx::tma_load_2d(dst + kWStage / 2, &map_w, (it.first + b) * 128, it.tile * 256 + 128,
+                               full);
+          }
+          __syncwarp();
+          ws.next();
+        }
+      }
+      for (int i = 0; i < W::kWStages; ++i) wait.end(bar(bars.w_full[i]), ws.last(i));
+    } else if (warp == 17) {
+      // ---- copies of x ----
+      pdl_wait();
+      Ring xs{W::kXStages};
+      bool on = true;
+      for (int i = blockIdx.x; on && i < items.total; i += step) {
+        const Item it(i, items);
+        for (int b = 0; b < it.count; ++b) {
+          on = wait(bar(bars.x_free[xs.at]), xs.phase ^ 1);
+          if (!on) break;
+          if (lane == 0) {
+            const uint32_t dst = xs_at + xs.at * W::kXStage, full = bar(bars.x_full[xs.at]);
+            ptx::mbar_arrive_expect_tx(full, W::kXStage);
+            // rows and inputs past the last one come as zeros
+            ptx::tma_load_2d(dst, &map_x, (it.first + b) * 128, it.chunk * NC, full);
+            ptx::tma_load_2d(dst + NC * 128, &map_x, (it.first + b) * 128 + 64, it.chunk * NC, full);
+          }
+          __syncwarp();
+          xs.next();
+        }
+      }
+      for (int i = 0; i < W::kXStages; ++i) wait.end(bar(bars.x_full[i]), xs.last(i));
+    } else if (warp == 18) {
+      // ---- products: the warp keeps together, one thread of it issues ----
+      const bool issues = elect_one();
+      constexpr uint32_t idesc = (1u << 4) | (NC >> 3) << 17 | (128u >> 4) << 24;
+      Ring xs{W::kXStages}, as[2] = {{2}, {2}}, ds[2] = {{W::kSlots}, {W::kSlots}};
+      bool on = true;
+      for (int i = blockIdx.x; on && i < items.total; i += step) {
+        const Item it(i, items);
+        bool fresh[2] = {true, true};
+#pragma unroll 1
+        for (int b = 0; on && b < it.count; ++b) {
+          on = wait(bar(bars.x_full[xs.at]), xs.phase);
+          if (!on) break;
+          const uint64_t x = ptx::sw128_desc(xs_at + xs.at * W::kXStage, 0, 1024);
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            if (fresh[d]) on = on && wait(bar(bars.d_free[d][ds[d].at]), ds[d].phase ^ 1);
+            on = on && wait(bar(bars.a_full[d][as[d].at]), as[d].phase);
+            if (!on) break;
+            ptx::tc_fence_after();
+            const bool ends = read_after(d, b, it.count);
+            if (issues) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)  // 16 inputs
+                umma_f16_ta(d_at(d, ds[d].at), a_at(d, as[d].at) + k * 8,
+                            x + ((k >> 2) * (NC * 8) + (k & 3) * 2), idesc, !fresh[d] || k > 0);
+              ptx::umma_commit(bar(bars.a_free[d][as[d].at]));
+              if (ends) ptx::umma_commit(bar(bars.d_full[d][ds[d].at]));
+            }
+            __syncwarp();
+            as[d].next();
+            fresh[d] = ends;
+            if (ends) ds[d].next();
+          }
+          if (!on) break;
+          if (issues) ptx::umma_commit(bar(bars.x_free[xs.at]));
+          __syncwarp();
+          xs.next();
+        }
+      }
+      if (issues) ptx::umma_commit(bar(bars.products));
+      __syncwarp();
+      wait.end(bar(bars.products), 0);
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 18) ptx::tmem_dealloc(tmem, 512);
+}
+
+// The parts of the inputs added up, scaled and stored.
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+  const int64_t n = static_cast<int64_t>(a.rows) * a.N;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  pdl_wait();
+  if (i >= n) return;
+  const int m = static_cast<int>(i / a.N), o = static_cast<int>(i - static_cast<int64_t>(m) * a.N);
+  int sum = 0;
+#pragma unroll 4
+  for (int p = 0; p < a.splits; ++p) sum += a.part[p * n + i];
+  const float v = scaled(sum, a.x_scale[m], a.w_scale[o], a.bias ? a.bias[o] : 0.f);
+  if (a.out_f32) static_cast<float*>(a.y)[i] = v;
+  else static_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(v);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// A matrix of `width` values a row, boxes of 128 bytes by `rows`.
+bool map_2d(CUtensorMap* m, CUtensorMapDataType type, int size, const void* at, int64_t width,
+            int64_t height, int rows) {
+  static const EncodeTiledFn encode = []() -> EncodeTiledFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(height)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width) * size};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(rows)};
+  const cuuint32_t unit[2] = {1, 1};
+  return encode != nullptr &&
+         encode(m, type, 2, const_cast<void*>(at), dims, strides, box, unit,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int columns_of(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+constexpr int kSMs = 152;
+
+template <int NC>
+cudaError_t launch(const Args& a, const __half* x, cudaStream_t s) {
+  cudaError_t st = allow_most_smem<wide_kernel<NC>>();
+  if (st != cudaSuccess) return st;
+  CUtensorMap mw, mx;
+  if (!map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W, a.K, a.N, 128) ||
+      !map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x, a.K, a.rows, NC))
+    return cudaErrorInvalidValue;
+  Items items;
+  items.tiles = (a.N + 255) / 256;
+  items.chunks = (a.rows + NC - 1) / NC;
+  items.splits = a.splits;
+  items.blocks = (a.K + 127) / 128;
+  items.total = items.tiles * items.chunks * items.splits;
+  const int grid = items.total < kSMs ? items.total : kSMs;
+  st = launch_dependent(wide_kernel<NC>, dim3(grid), dim3(kWarpsWide * 32), Wide<NC>::kSmem, s, mw,
+                        mx, a, items);
+  if (st != cudaSuccess || a.splits == 1) return st;
+  const int64_t n = static_cast<int64_t>(a.rows) * a.N;
+  return launch_dependent(join_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s,
+                          a);
+}
+
+}  // namespace
+
+// Into how many parts the inputs are cut, where the outputs alone do not fill the SMs:
+// counted in blocks of inputs, with three for an item's beginning and end and three for
+// the launch that adds the parts up.
+int wide_splits(int64_t rows, int N, int K) {
+  const int64_t items = static_cast<int64_t>((N + 255) / 256) *
+                        ((rows + columns_of(rows) - 1) / columns_of(rows));
+  const int blocks = (K + 127) / 128;
+  int best = 1;
+  int64_t least = 0;
+  for (int s = 1; s <= 16 && s <= blocks; ++s) {
+    const int64_t cost = (items * s + kSMs - 1) / kSMs * ((blocks + s - 1) / s + 3) + (s > 1 ? 3 : 0);
+    if (s == 1 || cost < least) best = s, least = cost;
+  }
+  return best;
+}
+
+cudaError_t launch_wide(const Args& a, const __half* x, cudaStream_t s) {
+  switch (columns_of(a.rows)) {
+    case 32: return launch<32>(a, x, s);
+    case 64: return launch<64>(a, x, s);
+    default: return launch<128>(a, x, s);
+  }
+}
+
+}  // namespace i8
+}  // namespace moe

@@ -37,11 +37,14 @@
 // neighbours' instead of in runs, made no difference.
 #pragma once
 
+#include "roles.cuh"
 #include "sm100_ptx.cuh"
 #include "w4.cuh"
 
 namespace moe {
 namespace w4 {
+
+using namespace roles;
 
 constexpr int kWarps = 8;        // that work out the plan
 constexpr int kNarrowWarps = 16; // of a block of the narrow kernel, one to an SM
@@ -99,16 +102,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
                : "r"(at)
                : "memory");
   return q;
-}
-
-// Whether a barrier's phase ends within a second.
-constexpr long long kWaitCycles = 2000000000ll;
-__device__ __forceinline__ bool arrives(uint32_t bar, int parity) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const long long began = clock64();
-  while (!ptx::mbar_try_wait(bar, parity))
-    if (clock64() - began > kWaitCycles) return false;
-  return true;
 }
 
 // c += A B, or c = A B
