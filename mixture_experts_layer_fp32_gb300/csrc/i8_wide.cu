@@ -13,9 +13,13 @@
 // mbarriers:
 //   8 add up: an output of both tiles to a thread and half of the columns each;
 //   8 convert: an output of a tile to a thread, 128 inputs at a time;
-//   one copies W (TMA), one x (TMA), one thread multiplies.
-// The two tiles' sums are read out 4 blocks of 128 inputs apart, so that products of
-// one go on while the other's are read.
+//   one copies W (TMA), one x (TMA), a thread of one more each multiplies a tile.
+// The two tiles' sums are read out 4 blocks of 128 inputs apart, and three places for
+// sums serve the two: a tile goes on in the spare one while its last is read (8192 x
+// 14336 x 4096, with one warp for all products: 837 us with two places, 805 with three,
+// and 712 with a warp for each tile's products, which are issued as fast as they run).
+#include <type_traits>
+
 #include "i8.cuh"
 #include "roles.cuh"
 
@@ -33,7 +37,7 @@ struct Wide {
   static constexpr int kWStages = NC == 128 ? 4 : 5;
   static constexpr int kXStages = NC == 128 ? 3 : 4;
   static constexpr int kXStage = NC * 256;
-  static constexpr int kSlots = 128 / NC;    // of sums, each tile's
+  static constexpr int kASlots = NC == 128 ? 2 : 4;  // of A, each tile's: 64 inputs
   static constexpr int kSmem = kWStages * kWStage + kXStages * kXStage + 1024;
 };
 
@@ -45,8 +49,8 @@ struct Items {
 struct Bars {
   uint64_t w_full[5], w_free[5];
   uint64_t x_full[4], x_free[4];
-  uint64_t a_full[2][2], a_free[2][2];  // [tile][slot]
-  uint64_t d_full[2][4], d_free[2][4];
+  uint64_t a_full[2][4], a_free[2][4];  // [tile][slot]
+  uint64_t d_full[3], d_free[3];        // places of sums
   uint64_t products;
 };
 
@@ -70,6 +74,21 @@ struct Item {
 __device__ __forceinline__ bool read_after(int d, int b, int count) {
   return b + 1 == count || (b + 1) % kExact == d * (kExact / 2);
 }
+
+// Which of the three places for sums is whose, and the parity of each one's use; the
+// same for the warp that multiplies and those that read.
+struct Places {
+  int of[2] = {0, 1}, spare = 2;
+  uint32_t phase = 0;  // a bit each
+  __device__ __forceinline__ int parity(int d) const { return phase >> of[d] & 1; }
+  // tile d goes on in the spare place
+  __device__ __forceinline__ void next(int d) {
+    phase ^= 1u << of[d];
+    const int was = of[d];
+    of[d] = spare;
+    spare = was;
+  }
+};
 
 // Four codes to two pairs of fp16 numbers.
 __device__ __forceinline__ void pairs_of(uint32_t word, uint32_t& p, uint32_t& q) {
@@ -113,19 +132,18 @@ __global__ void __launch_bounds__(kWarpsWide * 32, 1)
     }
     for (int i = 0; i < W::kXStages; ++i) {
       ptx::mbar_init(bar(bars.x_full[i]), 1);
-      ptx::mbar_init(bar(bars.x_free[i]), 1);
+      ptx::mbar_init(bar(bars.x_free[i]), 2);
     }
-    for (int d = 0; d < 2; ++d) {
-      for (int i = 0; i < 2; ++i) {
+    for (int d = 0; d < 2; ++d)
+      for (int i = 0; i < W::kASlots; ++i) {
         ptx::mbar_init(bar(bars.a_full[d][i]), 4);
         ptx::mbar_init(bar(bars.a_free[d][i]), 1);
       }
-      for (int i = 0; i < W::kSlots; ++i) {
-        ptx::mbar_init(bar(bars.d_full[d][i]), 1);
-        ptx::mbar_init(bar(bars.d_free[d][i]), 8);
-      }
+    for (int i = 0; i < 3; ++i) {
+      ptx::mbar_init(bar(bars.d_full[i]), 1);
+      ptx::mbar_init(bar(bars.d_free[i]), 8);
     }
-    ptx::mbar_init(bar(bars.products), 1);
+    ptx::mbar_init(bar(bars.products), 2);
     given_up = 0;
     ptx::fence_mbar_init();
   }
@@ -137,9 +155,9 @@ __global__ void __launch_bounds__(kWarpsWide * 32, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_at;
-  // sums: 128 columns a tile, [tile][slot]; A: 64 columns of 128 inputs, [tile][slot]
-  auto d_at = [&](int d, int slot) { return tmem + d * 128 + slot * NC; };
-  auto a_at = [&](int d, int slot) { return tmem + 256 + d * 128 + slot * 64; };
+  // A: 32 columns of 64 inputs, [tile][slot]; sums: three places
+  auto a_at = [&](int d, int slot) { return tmem + (d * W::kASlots + slot) * 32; };
+  auto d_at = [&](int place) { return tmem + 2 * W::kASlots * 32 + place * NC; };
   const Waits wait{a.err, &given_up};
   const int step = gridDim.x;
 
@@ -152,7 +170,7 @@ __global__ void __launch_bounds__(kWarpsWide * 32, 1)
     const int e = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // << 16, by 32
     pdl_wait();  // the rows' scales; and the output is free
-    Ring ring[2] = {{W::kSlots}, {W::kSlots}};
+    Places places;
     bool on = true;
     for (int i = blockIdx.x; on && i < items.total; i += step) {
       const Item it(i, items);
@@ -164,10 +182,10 @@ __global__ void __launch_bounds__(kWarpsWide * 32, 1)
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
           if (!on || !read_after(d, b, it.count)) continue;
-          on = wait(bar(bars.d_full[d][ring[d].at]), ring[d].phase);
+          on = wait(bar(bars.d_full[places.of[d]]), places.parity(d));
           if (!on) break;
           ptx::tc_fence_after();
-          const uint32_t at = d_at(d, ring[d].at) + lanes + e * half;
+          const uint32_t at = d_at(places.of[d]) + lanes + e * half;
 #pragma unroll
           for (int c = 0; c < half; c += 16) {
             float v[16];
@@ -178,12 +196,12 @@ __global__ void __launch_bounds__(kWarpsWide * 32, 1)
             if (c + 16 == half) {
               ptx::tc_fence_before();
               __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(bar(bars.d_free[d][ring[d].at]));
+              if (lane == 0) ptx::mbar_arrive(bar(bars.d_free[places.of[d]]));
             }
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[d][c + q] += __float2int_rn(v[q]);
           }
-          ring[d].next();
+          places.next(d);
         }
       if (!on) break;
       const int row0 = it.chunk * NC + e * half;
@@ -218,36 +236,43 @@ __global__ void __launch_bounds__(kWarpsWide * 32, 1)
     const int d = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t src = base + d * (kWStage / 2) + r * 128, swap = (r & 7) << 4;
-    Ring ws{W::kWStages}, as{2};
+    Ring ws{W::kWStages}, as{W::kASlots};
     bool on = true;
     for (int i = blockIdx.x; on && i < items.total; i += step) {
       const Item it(i, items);
 #pragma unroll 1
       for (int b = 0; b < it.count; ++b) {
-        on = wait(bar(bars.w_full[ws.at]), ws.phase) &&
-             wait(bar(bars.a_free[d][as.at]), as.phase ^ 1);
-        if (!on) break;
-        ptx::tc_fence_after();
-        const uint32_t from = src + ws.at * kWStage, to = a_at(d, as.at) + lanes;
+        on = wait(bar(bars.w_full[ws.at]), ws.phase);
+        const uint32_t from = src + ws.at * kWStage;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // 32 inputs
-          const uint4 p = lds16(from + ((j * 32) ^ swap)), q = lds16(from + ((j * 32 + 16) ^ swap));
-          uint32_t v[16];
-          pairs_of(p.x, v[0], v[1]), pairs_of(p.y, v[2], v[3]);
-          pairs_of(p.z, v[4], v[5]), pairs_of(p.w, v[6], v[7]);
-          pairs_of(q.x, v[8], v[9]), pairs_of(q.y, v[10], v[11]);
-          pairs_of(q.z, v[12], v[13]), pairs_of(q.w, v[14], v[15]);
-          tmem_st16(to + j * 16, v);
+        for (int h = 0; on && h < 2; ++h) {
+          uint4 q[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) q[c] = lds16(from + ((h * 64 + c * 16) ^ swap));
+          on = wait(bar(bars.a_free[d][as.at]), as.phase ^ 1);
+          if (!on) break;
+          ptx::tc_fence_after();
+          const uint32_t to = a_at(d, as.at) + lanes;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {  // 32 inputs
+            uint32_t v[16];
+            pairs_of(q[j * 2].x, v[0], v[1]), pairs_of(q[j * 2].y, v[2], v[3]);
+            pairs_of(q[j * 2].z, v[4], v[5]), pairs_of(q[j * 2].w, v[6], v[7]);
+            pairs_of(q[j * 2 + 1].x, v[8], v[9]), pairs_of(q[j * 2 + 1].y, v[10], v[11]);
+            pairs_of(q[j * 2 + 1].z, v[12], v[13]), pairs_of(q[j * 2 + 1].w, v[14], v[15]);
+            tmem_st16(to + j * 16, v);
+          }
+          tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (h == 1) ptx::mbar_arrive(bar(bars.w_free[ws.at]));
+            ptx::mbar_arrive(bar(bars.a_full[d][as.at]));
+          }
+          as.next();
         }
-        tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(bar(bars.w_free[ws.at]));
-          ptx::mbar_arrive(bar(bars.a_full[d][as.at]));
-        }
+        if (!on) break;
         ws.next();
-        as.next();
       }
     }
   } else {
@@ -297,46 +322,55 @@ __global__ void __launch_bounds__(kWarpsWide * 32, 1)
         }
       }
       for (int i = 0; i < W::kXStages; ++i) wait.end(bar(bars.x_full[i]), xs.last(i));
-    } else if (warp == 18) {
-      // ---- products: the warp keeps together, one thread of it issues ----
+    } else {
+      // ---- products of a tile: the warp keeps together, one thread of it issues.
       const bool issues = elect_one();
-      constexpr uint32_t idesc = (1u << 4) | (NC >> 3) << 17 | (128u >> 4) << 24;
-      Ring xs{W::kXStages}, as[2] = {{2}, {2}}, ds[2] = {{W::kSlots}, {W::kSlots}};
-      bool on = true;
-      for (int i = blockIdx.x; on && i < items.total; i += step) {
-        const Item it(i, items);
-        bool fresh[2] = {true, true};
+      auto products = [&](auto tile) {  // places are kept in registers with the tile known
+        constexpr int d = decltype(tile)::value;
+        constexpr uint32_t idesc = (1u << 4) | (NC >> 3) << 17 | (128u >> 4) << 24;
+        Ring xs{W::kXStages}, as{W::kASlots};
+        Places places;
+        bool on = true;
+        for (int i = blockIdx.x; on && i < items.total; i += step) {
+          const Item it(i, items);
+          bool fresh = true;
 #pragma unroll 1
-        for (int b = 0; on && b < it.count; ++b) {
-          on = wait(bar(bars.x_full[xs.at]), xs.phase);
-          if (!on) break;
-          const uint64_t x = ptx::sw128_desc(xs_at + xs.at * W::kXStage, 0, 1024);
+          for (int b = 0; on && b < it.count; ++b) {
+            if (fresh) on = wait(bar(bars.d_free[places.of[d]]), places.parity(d) ^ 1);
+            on = on && wait(bar(bars.x_full[xs.at]), xs.phase);
+            const uint64_t x = ptx::sw128_desc(xs_at + xs.at * W::kXStage, 0, 1024);
+            const uint32_t to = d_at(places.of[d]);
 #pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            if (fresh[d]) on = on && wait(bar(bars.d_free[d][ds[d].at]), ds[d].phase ^ 1);
-            on = on && wait(bar(bars.a_full[d][as[d].at]), as[d].phase);
+            for (int h = 0; h < 2; ++h) {
+              on = on && wait(bar(bars.a_full[d][as.at]), as.phase);
+              if (!on) break;
+              ptx::tc_fence_after();
+              if (issues) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // 16 inputs
+                  umma_f16_ta(to, a_at(d, as.at) + k * 8, x + (h * (NC * 8) + k * 2), idesc,
+                              h > 0 || k > 0 || !fresh);
+                ptx::umma_commit(bar(bars.a_free[d][as.at]));
+              }
+              __syncwarp();
+              as.next();
+            }
             if (!on) break;
-            ptx::tc_fence_after();
-            const bool ends = read_after(d, b, it.count);
             if (issues) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)  // 16 inputs
-                umma_f16_ta(d_at(d, ds[d].at), a_at(d, as[d].at) + k * 8,
-                            x + ((k >> 2) * (NC * 8) + (k & 3) * 2), idesc, !fresh[d] || k > 0);
-              ptx::umma_commit(bar(bars.a_free[d][as[d].at]));
-              if (ends) ptx::umma_commit(bar(bars.d_full[d][ds[d].at]));
+              ptx::umma_commit(bar(bars.x_free[xs.at]));
+              if (read_after(d, b, it.count)) ptx::umma_commit(bar(bars.d_full[places.of[d]]));
             }
             __syncwarp();
-            as[d].next();
-            fresh[d] = ends;
-            if (ends) ds[d].next();
+            xs.next();
+            fresh = read_after(d, b, it.count);
+            // the other tile's turns too: both tiles' places follow one order
+            if (read_after(0, b, it.count)) places.next(0);
+            if (read_after(1, b, it.count)) places.next(1);
           }
-          if (!on) break;
-          if (issues) ptx::umma_commit(bar(bars.x_free[xs.at]));
-          __syncwarp();
-          xs.next();
         }
-      }
+      };
+      if (warp == 18) products(std::integral_constant<int, 0>());
+      else products(std::integral_constant<int, 1>());
       if (issues) ptx::umma_commit(bar(bars.products));
       __syncwarp();
       wait.end(bar(bars.products), 0);
