@@ -9,14 +9,16 @@
 // min_p.  The token is the lowest index whose running sum of kept weights exceeds u
 // times their total.
 //
-// A row belongs to a cluster of up to 8 blocks, which hold it in their shared memory
+// A row belongs to a cluster of up to 16 blocks, which hold it in their shared memory
 // from its only read to the end (rows too long for that are read again from L2).
-// Instead of a sort, one pass counts tokens and adds weights up in 1024 bins of 1/32
-// of a nat below the largest; only the bin that a border falls into is gathered and
-// sorted, by its exact order (a bin with more than 1024 tokens is first narrowed
-// down by further passes over ever finer ranges of that order).  What bounds it: a
-// row's latency (load, five to seven passes with a cluster barrier each), not
-// memory.
+// With a top-k of up to 600 (or so few tokens in all) the largest logits of the threads'
+// tokens give a threshold above which there are that many and few more; those are
+// gathered and sorted by one block, which draws the token.  Otherwise one pass counts tokens and adds weights up in 1024 bins of 1/32 of a nat below the
+// largest; the bin that a border falls into is gathered and sorted, by its exact order
+// (a bin with more than 1024 tokens is first narrowed down by further passes over ever
+// finer ranges of that order).  What bounds it: a row's latency (load, passes with
+// cluster barriers, sorts), not memory.
+#include <float.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -25,12 +27,15 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+static_assert(kWarps == 32, "a warp looks at all warps' sums");
 constexpr int kBins = 1024, kList = 1024;
+constexpr int kLikely = 600;             // top-k that is searched for among the largest
 constexpr float kBinsPerNat = 32.f;
 constexpr float kOne = 1099511627776.f;  // 2^40
-constexpr int kMaxBlocks = 8;            // of a cluster
-constexpr size_t kMaxData = 176 * 1024;  // bytes of a block's part of a row
+constexpr int kMaxBlocks = 16;           // of a cluster
+constexpr size_t kMaxData = 160 * 1024;  // bytes of a block's part of a row
+constexpr int kSMs = 152;
 constexpr int kFewest = 2048;            // tokens of a block, where a row is split
 
 typedef unsigned long long u64;
@@ -59,7 +64,14 @@ struct Shared {
   uint32_t fine_counts[kBins];  // the row's, of a narrowed range
   u64 fine_masses[kBins];
   u64 list[kList];         // block 0's
-  uint32_t listed;
+  union {
+    struct {
+      u64 sums[kList];     // running sums of its weights
+      u64 own[kList];      // what this block adds to it
+    };
+    uint32_t pieces[3][kBins];  // of the masses while they are added up, 15 bits each
+  };
+  uint32_t listed, owned, base;
   u64 warp_sum[kWarps];
   uint32_t warp_count[kWarps];
   float warp_max[kWarps];
@@ -74,6 +86,9 @@ struct Shared {
   uint32_t count_above;
   u64 mass_above;
 };
+
+constexpr size_t kShared = (sizeof(Shared) + 15) / 16 * 16;
+static_assert(kShared + kMaxData <= 227 * 1024, "shared memory");
 
 // ------------------------------------------------------------------ other blocks
 __device__ __forceinline__ uint32_t there(const void* p, int rank) {
@@ -123,13 +138,51 @@ __device__ __forceinline__ u64 order_of(uint32_t key, uint32_t i) {
 }
 
 struct Scale {
-  float max, t;
+  float max, inverse;  // 1 / t
   __device__ __forceinline__ float below(float l) const {  // in nats, >= 0
-    return l == max ? 0.f : (max - l) / t;
+    return l == max ? 0.f : (max - l) * inverse;
   }
   __device__ __forceinline__ float weight(float l) const { return expf(-below(l)); }
 };
-__device__ __forceinline__ u64 whole(float w) { return __float2ull_rn(w * kOne); }
+// w 2^40 for 0 <= w <= 1 as a whole number: its upper part, and 20 bits (rounded)
+__device__ __forceinline__ void whole(float w, uint32_t& hi, uint32_t& lo) {
+  const float v = w * 0x1p20f;  // exact
+  hi = __float2uint_rd(v);
+  lo = __float2uint_rn((v - __uint2float_rn(hi)) * 0x1p20f);
+}
+__device__ __forceinline__ u64 whole(float w) {
+  uint32_t hi, lo;
+  whole(w, hi, lo);
+  return (static_cast<u64>(hi) << 20) + lo;
+}
+// A bin's mass from this block: whole numbers of 41 bits in pieces of 15, whose sums
+// over 2^17 tokens stay in 32 bits, since the 64-bit addition in shared memory is a
+// loop.
+__device__ __forceinline__ void add_mass(Shared& s, int bin, u64 w, bool pieces) {
+  if (!pieces) {
+    atomicAdd(&s.mass[bin], w);
+    return;
+  }
+  const uint32_t low = static_cast<uint32_t>(w), lo = low & 0x7fffu, mid = low >> 15 & 0x7fffu;
+  const uint32_t hi = static_cast<uint32_t>(w >> 30);
+  if (lo) atomicAdd(&s.pieces[0][bin], lo);
+  if (mid) atomicAdd(&s.pieces[1][bin], mid);
+  if (hi) atomicAdd(&s.pieces[2][bin], hi);
+}
+__device__ void clear_bins(Shared& s) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    s.count[i] = 0, s.mass[i] = 0;
+    s.pieces[0][i] = s.pieces[1][i] = s.pieces[2][i] = 0;
+  }
+  __syncthreads();
+}
+__device__ void join_pieces(Shared& s) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kThreads)
+    s.mass[i] += s.pieces[0][i] + (static_cast<u64>(s.pieces[1][i]) << 15) +
+                 (static_cast<u64>(s.pieces[2][i]) << 30);
+}
 __device__ __forceinline__ int bin_of(float below) {
   return static_cast<int>(fminf(below * kBinsPerNat, static_cast<float>(kBins - 1)));
 }
@@ -144,22 +197,33 @@ __device__ __forceinline__ u64 warp_total(u64 v) {
 }
 
 // The blocks' bins added up, in every block.
+template <bool MASS>
 __device__ void merge(Shared& s, int rank, int blocks, uint32_t* counts, u64* masses) {
   sync_cluster();
   const int each = kBins / blocks;
   for (int i = rank * each + threadIdx.x; i < (rank + 1) * each; i += kThreads) {
-    uint32_t c = 0;
-    u64 m = 0;
-    for (int b = 0; b < blocks; ++b) {
-      c += get32(there(&s.count[i], b));
-      m += get64(there(&s.mass[i], b));
+    // all blocks' at a time, so that their latencies are one
+    uint32_t cs[kMaxBlocks], c = 0;
+    u64 ms[kMaxBlocks], m = 0;
+#pragma unroll
+    for (int b = 0; b < kMaxBlocks; ++b) {
+      cs[b] = b < blocks ? get32(there(&s.count[i], b)) : 0u;
+      ms[b] = MASS && b < blocks ? get64(there(&s.mass[i], b)) : 0ull;
     }
+#pragma unroll
+    for (int b = 0; b < kMaxBlocks; ++b) c += cs[b], m += ms[b];
     for (int b = 0; b < blocks; ++b) {
       put(there(&counts[i], b), c);
-      put(there(&masses[i], b), m);
+      if (MASS) put(there(&masses[i], b), m);
     }
   }
   sync_cluster();
+}
+
+// The sums of the warps before this one, from s.warp_sum.
+__device__ __forceinline__ u64 sums_before(const Shared& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  return warp_total(lane < warp ? s.warp_sum[lane] : 0);
 }
 
 // The first of n entries (n <= 1024, 2 to a thread) at which the running sum of
@@ -187,10 +251,8 @@ __device__ void first_reached(Shared& s, int n, Count count, Mass mass, Reached 
   if (lane == 31) s.warp_count[warp] = cs, s.warp_sum[warp] = ms;
   if (threadIdx.x == 0) s.bin = n - 1;
   __syncthreads();
-  uint32_t cb = 0;
-  u64 mb = 0;
-  for (int w = 0; w < warp; ++w) cb += s.warp_count[w], mb += s.warp_sum[w];
-  cs += cb, ms += mb;
+  cs += __reduce_add_sync(~0u, lane < warp ? s.warp_count[lane] : 0u);
+  ms += sums_before(s);
   cs -= c[0] + c[1], ms -= m[0] + m[1];  // before this thread's two
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -207,19 +269,86 @@ __device__ void first_reached(Shared& s, int n, Count count, Mass mass, Reached 
   __syncthreads();
 }
 
-// list[0 .. n) in descending order, n a power of two
+// list[0 .. n) in descending order (bitonic; n a power of two from 64 on, kList at most):
+// two entries to a thread, 64 to a warp, which orders those among itself.
 __device__ void sort_descending(u64* list, int n) {
-  for (int size = 2; size <= n; size *= 2)
-    for (int step = size / 2; step > 0; step /= 2) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-        const int a = 2 * i - (i & (step - 1)), b = a + step;
-        const bool down = (a & size) == 0;
-        const u64 x = list[a], y = list[b];
-        if ((x < y) == down) list[a] = y, list[b] = x;
-      }
-    }
+  const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 64 + lane;
+  const bool active = first < n;
+  u64 v[2] = {0, 0};
   __syncthreads();
+  if (active) v[0] = list[first], v[1] = list[first + 32];
+  auto keep = [](u64 mine, u64 other, bool larger) { return (mine > other) == larger ? mine : other; };
+#pragma unroll 1
+  for (int size = 2; size <= n; size *= 2) {
+#pragma unroll 1
+    for (int step = size / 2; step >= 64; step /= 2) {
+      __syncthreads();
+      if (active) list[first] = v[0], list[first + 32] = v[1];
+      __syncthreads();
+      if (active)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = first + j * 32;
+          v[j] = keep(v[j], list[e ^ step], ((e & size) == 0) == ((e & step) == 0));
+        }
+    }
+    if (!active) continue;
+    if (size >= 64) {
+      const bool down = (first & size) == 0;
+      const u64 a = v[0], b = v[1];
+      v[0] = keep(a, b, down), v[1] = keep(b, a, !down);
+    }
+#pragma unroll 1
+    for (int step = min(size / 2, 16); step > 0; step /= 2)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int e = first + j * 32;
+        const u64 other = __shfl_xor_sync(~0u, v[j], step);
+        v[j] = keep(v[j], other, ((e & size) == 0) == ((e & step) == 0));
+      }
+  }
+  __syncthreads();
+  if (active) list[first] = v[0], list[first + 32] = v[1];
+  __syncthreads();
+}
+__device__ __forceinline__ int sorted_size(int n) {
+  int size = 64;
+  while (size < n) size *= 2;
+  return size;
+}
+
+// sums[i] = value(0) + .. + value(i), i < n <= kList
+template <typename Value>
+__device__ void running_sums(Shared& s, int n, Value value) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i0 = threadIdx.x * 2;
+  const u64 a = i0 < n ? value(i0) : 0, b = i0 + 1 < n ? value(i0 + 1) : 0;
+  u64 sum = a + b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 v = __shfl_up_sync(~0u, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) s.warp_sum[warp] = sum;
+  __syncthreads();
+  sum += sums_before(s);
+  if (i0 < n) s.sums[i0] = sum - b;
+  if (i0 + 1 < n) s.sums[i0 + 1] = sum;
+  __syncthreads();
+}
+// the first i < n at which sums[i] is past a border, or n
+template <typename Past>
+__device__ int first_past(Shared& s, int n, Past past) {
+  if (threadIdx.x == 0) s.bin = n;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kList / kThreads; ++j) {
+    const int i = threadIdx.x + j * kThreads;
+    if (i < n && past(s.sums[i]) && (i == 0 || !past(s.sums[i - 1]))) s.bin = i;
+  }
+  __syncthreads();
+  const int at = s.bin;
+  __syncthreads();
+  return at;
 }
 
 template <typename T>
@@ -228,20 +357,57 @@ struct Row {
   int n;            // tokens of it
   int first;        // the first one's index in the row
   // a warp has a run of them, a token to a lane
+  __device__ __forceinline__ int run() const { return (n + kWarps * 32 - 1) / (kWarps * 32) * 32; }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int run = (n + kWarps * 32 - 1) / (kWarps * 32) * 32;
-    const int end = min(n, (warp + 1) * run);
+    const int end = min(n, (warp + 1) * run());
 #pragma unroll 4
-    for (int i = warp * run + lane; i < end; i += 32) f(to_float(at[i]), first + i);
+    for (int i = warp * run() + lane; i < end; i += 32) f(to_float(at[i]), first + i);
   }
 };
+
+// The orders of the tokens of at least `least` for which `in` holds, into block 0's
+// list; s.listed, there, says how many there are (0 before, which a cluster barrier has
+// made known).  Four tokens of a lane are looked at
+// together, as mostly none is wanted.
+template <typename T, typename In>
+__device__ void gather(Shared& s, const Row<T>& row, int blocks, float least, In in) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) s.owned = 0;
+  __syncthreads();
+  const int run = row.run(), end = min(row.n, (warp + 1) * run);
+  for (int i0 = warp * run + lane; i0 < (warp + 1) * run; i0 += 128) {
+    float l[4];
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      l[j] = i0 + j * 32 < end ? to_float(row.at[i0 + j * 32]) : -INFINITY;
+      any |= l[j] >= least;
+    }
+    if (!any) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = row.first + i0 + j * 32;
+      if (l[j] >= least && in(l[j], i)) {
+        const uint32_t at = atomicAdd(&s.owned, 1u);
+        if (at < kList) s.own[at] = order_of(key_of(l[j]), i);
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s.base = add32(there(&s.listed, 0), s.owned);
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < s.owned && s.base + i < kList; i += kThreads)
+    put(there(&s.list[s.base + i], 0), s.own[i]);
+  sync_cluster();
+}
 
 // Which of the tokens with orders in [low, high) is the one at which the running sum
 // reaches what is wanted, counting from the sums `above` those.
 template <typename T, typename In, typename Reached>
-__device__ Result search(Shared& s, const Row<T>& row, int rank, int blocks, const Scale& scale,
+__device__ Result search(Shared& s, const Row<T>& row, int rank, int blocks, bool pieces,
+                         const Scale& scale,
                          uint32_t n, uint32_t count_above, u64 mass_above, In in,
                          Reached reached) {
   u64 low = 0, high = ~0ull;  // of the tokens that are `in`
@@ -275,18 +441,17 @@ __device__ Result search(Shared& s, const Row<T>& row, int rank, int blocks, con
       // 1024 equal ranges of [low, high], the highest first
       int shift = 0;
       while (((high - low) >> shift) >= kBins) ++shift;
-      __syncthreads();
-      for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = 0, s.mass[i] = 0;
-      __syncthreads();
+      clear_bins(s);
       row.each([&](float l, int i) {
         if (!in(l)) return;
         const u64 o = order_of(key_of(l), i);
         if (o < low || o > high) return;
         const int b = static_cast<int>((high - o) >> shift);
         atomicAdd(&s.count[b], 1u);
-        atomicAdd(&s.mass[b], whole(scale.weight(l)));
+        add_mass(s, b, whole(scale.weight(l)), pieces);
       });
-      merge(s, rank, blocks, s.fine_counts, s.fine_masses);
+      join_pieces(s);
+      merge<true>(s, rank, blocks, s.fine_counts, s.fine_masses);
       first_reached(
           s, kBins, [&](int i) { return s.fine_counts[i]; },
           [&](int i) { return s.fine_masses[i]; },
@@ -301,20 +466,15 @@ __device__ Result search(Shared& s, const Row<T>& row, int rank, int blocks, con
     }
   }
   // the rest into block 0's list
-  if (threadIdx.x == 0) s.listed = 0;
-  sync_cluster();
-  row.each([&](float l, int i) {
-    if (!in(l)) return;
+  gather(s, row, blocks, -FLT_MAX, [&](float l, int i) {
+    if (!in(l)) return false;
     const u64 o = order_of(key_of(l), i);
-    if (o < low || o > high) return;
-    const uint32_t at = add32(there(&s.listed, 0), 1u);
-    if (at < kList) put(there(&s.list[min(at, static_cast<uint32_t>(kList - 1))], 0), o);
+    return o >= low && o <= high;
   });
-  sync_cluster();
   if (rank == 0) {
-    const int got = min(static_cast<int>(s.listed), kList);
-    int size = 32;
-    while (size < got) size *= 2;
+    const int got = min(static_cast<int>(s.listed), kList), size = sorted_size(got);
+    __syncthreads();
+    if (threadIdx.x == 0) s.listed = 0;
     for (int i = got + threadIdx.x; i < size; i += kThreads) s.list[i] = 0;
     sort_descending(s.list, size);
     auto mass = [&](int i) { return whole(scale.weight(logit_of(static_cast<uint32_t>(s.list[i] >> 32)))); };
@@ -335,10 +495,61 @@ __device__ Result search(Shared& s, const Row<T>& row, int rank, int blocks, con
   return r;
 }
 
+// Block 0: the token, if the gathered ones are enough.  The list has all tokens from some
+// logit on, or all there are.
+__device__ bool draw_likely(Shared& s, const Args& a, int64_t r, const Scale& scale, int k,
+                            float top_p, float min_p, float u) {
+  const bool all = a.V <= kList;
+  const uint32_t listed = s.listed;
+  __syncthreads();
+  if (threadIdx.x == 0) s.listed = 0;
+  if (listed > kList || (!all && k > 0 && listed < static_cast<uint32_t>(k))) return false;
+  int n = static_cast<int>(listed);
+  auto weight = [&](uint32_t key) { return scale.weight(logit_of(key)); };
+  int size = sorted_size(n);
+  for (int i = n + threadIdx.x; i < size; i += kThreads) s.list[i] = 0;
+  sort_descending(s.list, size);
+  if (k > 0) n = min(n, k);
+  if (top_p < 1.f) {
+    running_sums(s, n, [&](int i) { return whole(weight(static_cast<uint32_t>(s.list[i] >> 32))); });
+    const double want =
+        static_cast<double>(fmaxf(top_p, 0.f)) * static_cast<double>(s.sums[n - 1]);
+    n = min(n, first_past(s, n, [&](u64 m) { return static_cast<double>(m) >= want; }) + 1);
+  }
+  // in index order: the list anew with the index in front
+  u64 mine[kList / kThreads];
+#pragma unroll
+  for (int j = 0; j < kList / kThreads; ++j) {
+    const int i = j * kThreads + threadIdx.x;
+    mine[j] = i < n ? s.list[i] << 32 | s.list[i] >> 32 : 0;
+  }
+  __syncthreads();
+  size = sorted_size(n);
+#pragma unroll
+  for (int j = 0; j < kList / kThreads; ++j)
+    if (j * kThreads + static_cast<int>(threadIdx.x) < size) s.list[j * kThreads + threadIdx.x] = mine[j];
+  sort_descending(s.list, size);
+  running_sums(s, n, [&](int i) {
+    const float w = weight(static_cast<uint32_t>(s.list[i]));
+    return w >= min_p ? whole(w) : u64{0};
+  });
+  const u64 total = s.sums[n - 1];
+  const double at = static_cast<double>(u) * static_cast<double>(total);
+  const int i = first_past(s, n, [&](u64 m) { return static_cast<double>(m) > at; });
+  if (threadIdx.x == 0) {
+    a.tokens[r] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(s.list[i] >> 32));
+    if (a.prob)
+      a.prob[r] = static_cast<float>(static_cast<double>(weight(static_cast<uint32_t>(s.list[i]))) *
+                                     kOne / static_cast<double>(total));
+  }
+  return true;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ Args a) {
-  extern __shared__ __align__(16) char data[];
-  __shared__ Shared s;
+  extern __shared__ __align__(16) char smem[];
+  Shared& s = *reinterpret_cast<Shared*>(smem);
+  char* data = smem + kShared;
   const int blocks = gridDim.x, rank = blockIdx.x;  // the cluster is a row of the grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
@@ -372,24 +583,29 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   float min_p = a.c.min_p_of ? a.c.min_p_of[r] : a.c.min_p;
   const float u = fminf(fmaxf(a.u[r], 0.f), 0x1.fffffep-1f);  // NaN: 0
   min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
+  if (threadIdx.x == 0) s.listed = 0;
   __syncthreads();
 
   // the largest logit
   float top = -INFINITY;
   row.each([&](float l, int) { top = fmaxf(top, l); });  // NaN: none
+  const float mine = top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) s.warp_max[warp] = top;
   __syncthreads();
-  if (threadIdx.x < blocks) {
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s.warp_max[w]);
-    put(there(&s.max_of[rank], threadIdx.x), top);
+  if (warp == 0) {
+    top = s.warp_max[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane < blocks) put(there(&s.max_of[rank], lane), top);
   }
   sync_cluster();
   Scale scale;
   scale.max = s.max_of[0];
   for (int b = 1; b < blocks; ++b) scale.max = fmaxf(scale.max, s.max_of[b]);
-  scale.t = t;
+  // past 1e30 all finite logits of any use weigh the same
+  scale.inverse = 1.f / fminf(t, 1e30f);
 
   const bool none = scale.max == -INFINITY;
   const bool greedy = !(t > 0.f) || k == 1;
@@ -418,16 +634,41 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   u64 last = 0;  // orders from there on are kept
   const bool by_p = top_p < 1.f;
   if (k > 0 || by_p) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = 0, s.mass[i] = 0;
-    __syncthreads();
+    const bool pieces = a.part <= 1 << 17;
+    // Few tokens, or a top-k: those that it can be about are gathered at once.
+    if (a.V <= kList || (k > 0 && k <= kLikely)) {
+      float least = -FLT_MAX;
+      if (a.V > kList) {
+        for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = 0;
+        __syncthreads();
+        if (mine > -INFINITY) atomicAdd(&s.count[bin_of(scale.below(mine))], 1u);
+        merge<false>(s, rank, blocks, s.counts, s.masses);
+        const uint32_t want = k;
+        first_reached(
+            s, kBins, [&](int i) { return s.counts[i]; }, [](int) { return u64{0}; },
+            [=](uint32_t c, u64) { return c >= want; });
+        // the bin's lower end; any threshold would do, the same in every block
+        least = scale.max - static_cast<float>(s.bin + 1) / (kBinsPerNat * scale.inverse);
+      }
+      gather(s, row, blocks, least, [](float, int) { return true; });
+      if (rank == 0) {
+        const bool drawn = draw_likely(s, a, r, scale, k, top_p, min_p, u);
+        if (threadIdx.x < blocks) put(there(&s.first_of[0], threadIdx.x), drawn ? 1u : 0u);
+      }
+      sync_cluster();
+      if (s.first_of[0]) return;
+    }
+
+    clear_bins(s);
     row.each([&](float l, int) {
       if (!(l > -INFINITY)) return;
       const float below = scale.below(l);
       const int b = bin_of(below);
       atomicAdd(&s.count[b], 1u);
-      if (by_p) atomicAdd(&s.mass[b], whole(expf(-below)));
+      if (by_p) add_mass(s, b, whole(expf(-below)), pieces);
     });
-    merge(s, rank, blocks, s.counts, s.masses);
+    join_pieces(s);
+    merge<true>(s, rank, blocks, s.counts, s.masses);
     auto in_bin = [&](int bin) {
       return [=](float l) { return l > -INFINITY && bin_of(scale.below(l)) == bin; };
     };
@@ -438,7 +679,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       const uint32_t ca = s.count_above, n = s.counts[bin];
       const u64 ma = s.mass_above;
       __syncthreads();
-      return search(s, row, rank, blocks, scale, n, ca, ma, in_bin(bin), reached);
+      return search(s, row, rank, blocks, pieces, scale, n, ca, ma, in_bin(bin), reached);
     };
     // all of them, where top-k leaves them
     u64 mass = 0;
@@ -448,8 +689,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     tokens = __reduce_add_sync(~0u, tokens);
     if (lane == 0) s.warp_sum[warp] = mass, s.warp_count[warp] = tokens;
     __syncthreads();
-    mass = 0, tokens = 0;
-    for (int w = 0; w < kWarps; ++w) mass += s.warp_sum[w], tokens += s.warp_count[w];
+    mass = warp_total(s.warp_sum[lane]);
+    tokens = __reduce_add_sync(~0u, s.warp_count[lane]);
     __syncthreads();
     if (k > 0 && static_cast<uint32_t>(k) < tokens) {
       const uint32_t want = k;
@@ -473,14 +714,24 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   };
   u64 sum = 0;
   float w;
-  row.each([&](float l, int i) { sum += kept(l, i, w); });
+  if (last == 0 && min_p <= 0.f && a.part <= kThreads * 4096) {
+    // all of them: a thread's halves of 20 bits over 4096 tokens stay in 32
+    uint32_t his = 0, los = 0;
+    row.each([&](float l, int) {
+      uint32_t hi, lo;
+      whole(l > -INFINITY ? scale.weight(l) : 0.f, hi, lo);
+      his += hi, los += lo;
+    });
+    sum = (static_cast<u64>(his) << 20) + los;
+  } else {
+    row.each([&](float l, int i) { sum += kept(l, i, w); });
+  }
   sum = warp_total(sum);
   if (lane == 0) s.warp_sum[warp] = sum;
   __syncthreads();
-  if (threadIdx.x < blocks) {
-    sum = 0;
-    for (int v = 0; v < kWarps; ++v) sum += s.warp_sum[v];
-    put(there(&s.sum_of[rank], threadIdx.x), sum);
+  if (warp == 0) {
+    sum = warp_total(s.warp_sum[lane]);
+    if (lane < blocks) put(there(&s.sum_of[rank], lane), sum);
   }
   sync_cluster();
   u64 before = 0, total = 0;
@@ -490,10 +741,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   }
   const double at = static_cast<double>(u) * static_cast<double>(total);
   auto past = [&](u64 v) { return static_cast<double>(v) > at; };
-  for (int v = 0; v < warp; ++v) before += s.warp_sum[v];
+  before += sums_before(s);
   if (past(before) || !past(before + s.warp_sum[warp])) return;
   // this warp's run has the token
-  const int run = (row.n + kWarps * 32 - 1) / (kWarps * 32) * 32;
+  const int run = row.run();
   const int end = min(row.n, (warp + 1) * run);
   for (int i0 = warp * run; i0 < end; i0 += 32) {
     const int i = i0 + lane;
@@ -517,14 +768,52 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   }
 }
 
+// 16 blocks where the device takes a cluster of them (more than 8 is asked for), else 8;
+// looked up once for a kernel and device.
+template <auto KERNEL>
+cudaError_t widest_cluster(int* most) {
+  static std::atomic<int8_t> known[64];
+  int device = 0;
+  cudaError_t st = cudaGetDevice(&device);
+  if (st != cudaSuccess) return st;
+  std::atomic<int8_t>& entry = known[device & 63];
+  if (entry.load(std::memory_order_acquire) == 0) {
+    int n = 8;
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+        cudaSuccess) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(16);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kShared + kMaxData;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 16;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      if (cudaOccupancyMaxActiveClusters(&clusters, KERNEL, &cfg) == cudaSuccess && clusters > 0)
+        n = 16;
+    }
+    (void)cudaGetLastError();
+    entry.store(static_cast<int8_t>(n), std::memory_order_release);
+  }
+  *most = entry.load(std::memory_order_acquire);
+  return cudaSuccess;
+}
+
 template <typename T>
 cudaError_t launch(Args& a, cudaStream_t s) {
   cudaError_t st = allow_most_smem<sample_kernel<T>>();
   if (st != cudaSuccess) return st;
+  int most = 8;
+  st = widest_cluster<sample_kernel<T>>(&most);
+  if (st != cudaSuccess) return st;
   int blocks = 1;
   // more blocks to a row as long as there is work for each and room for all
-  while (blocks < kMaxBlocks && (a.V + blocks - 1) / blocks >= 2 * kFewest &&
-         (a.rows * blocks * 2 <= 2 * 304 ||
+  while (blocks < most && (a.V + blocks - 1) / blocks >= 2 * kFewest &&
+         (a.rows * blocks * 2 <= kSMs ||
           (a.V + blocks - 1) / blocks * sizeof(T) + 32 > kMaxData))
     blocks *= 2;
   a.part = static_cast<int>((a.V + blocks - 1) / blocks);
@@ -534,7 +823,7 @@ cudaError_t launch(Args& a, cudaStream_t s) {
   const unsigned ys = static_cast<unsigned>(a.rows < 65535 ? a.rows : 65535);
   cfg.gridDim = dim3(blocks, ys, static_cast<unsigned>((a.rows + 65534) / 65535));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = a.held ? bytes : 0;
+  cfg.dynamicSmemBytes = kShared + (a.held ? bytes : 0);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
