@@ -4,30 +4,43 @@
 // At up to 64 tokens the layer is bound by reading the weights of the experts that
 // are hit, once: everything else has to stay out of that stream's way.  One
 // cooperative grid, a block to an SM, goes through
-//   0  logits: a block takes some features and up to 32 experts, partial sums out;
-//   1  top-k: a block takes a token, adds its partial sums up and chooses; then every
-//      block builds the same plan (rows by expert, drops) in its shared memory;
-//   2  FC1: the stream of all hit experts' W1 and W3, cut into equal runs of units;
-//   3  hidden values: the runs' partial sums added in order, silu(a) b;
-//   4  FC2: the stream of W2, cut the same way;
-//   5  combine: partial sums of a token's experts added in order, one rounding.
+//   logits: a block takes some features and up to 32 experts, partial sums out;
+//   top-k: a block takes a token, adds its partial sums up and chooses (up to 4 tokens:
+//     every block, which spares a barrier); then every block builds the same plan (rows
+//     by expert, drops) in its shared memory;
+//   FC1: the stream of all hit experts' W1 and W3, cut into equal runs of units;
+//   hidden values: the last block to bring a partial sum of a tile adds them up, in
+//     order, forms silu(a) b and counts the tile as done for its expert;
+//   FC2: the stream of W2, cut the same way, an expert's part as soon as it is ready;
+//   combine: partial sums of a token's experts added in order, one rounding.
+// The barriers of all blocks are those around the top-k and the one before the combine:
+// a block's parts of the two streams are nearly the same experts', so that a slow
+// block delays its neighbours alone (a barrier and a step of its own for the hidden
+// values took XXX).
 // A block's part of both streams is one sequence of units, a unit the 4 KB of each
 // of its 8 warps: 32 (fp32: 16) inputs of 64 outputs.  A warp copies its own units
-// with cp.async into a ring of its own, up to kSlots - 1 units ahead, across the
-// steps 3 and 4 too: the weights do not depend on them, so memory stays busy while
-// the grid's barriers are passed.  No block waits for another within a step.
+// with cp.async into a ring of its own, up to kSlots - 1 units ahead, from FC1 into FC2
+// too: the weights do not depend on the hidden values, so memory stays busy while those
+// are waited for.
 //
-// bf16: mma.sync with the weights as the operand of 16 rows (ldmatrix.trans out of
-// the ring, whose 16-byte pieces are swapped so that it meets no bank twice) and 8
-// tokens as the columns.  The tensor cores' rate does not matter here (tcgen05 would
-// need 128 rows and its operands in another layout than the stream's): a unit feeds
-// 8 instructions for every 8 tokens.  The inputs of 32 are permuted between the
-// instructions so that a lane's share of x is 16 bytes in a row.  A hidden value
-// enters FC2 as two bf16 numbers (together within 2^-17 of it), so the layer has no
-// rounding between x and y but y's own.  fp32: FMAs, two outputs to a lane.
+// The products are mma.sync with the weights as the operand of 16 rows and 8 tokens as
+// the columns.  The tensor cores' rate does not matter here (tcgen05 would need 128 rows
+// and its operands in another layout than the stream's): a unit feeds 8 instructions for
+// every 8 tokens.
+//   bf16: weights by ldmatrix.trans out of the ring, whose 16-byte pieces are swapped so
+//     that it meets no bank twice; the inputs of 32 are permuted between the instructions
+//     so that a lane's share of x is 16 bytes in a row.  A hidden value enters FC2 as two
+//     bf16 numbers (together within 2^-17 of it), so the layer has no rounding between x
+//     and y but y's own.
+//   fp32: each operand as two tf32 numbers, v = p + q with |q| <= 2^-11 |v| and q itself
+//     rounded (2^-22 of v); p p', p q' and q p' are multiplied, q q' (2^-22) is left out.
+//     Three instructions cost less than the FMAs from two rows on (7 tokens, 3 of 12 of
+//     1032 x 1416: XXX us with FMAs), and an infinity in x gives NaN.
 //
 // All partial sums are added in an order given by sizes alone: repeats are equal
 // bit for bit.
+#include <type_traits>
+
 #include "topk.cuh"
 
 namespace moe {
@@ -42,6 +55,7 @@ constexpr int kPairs = kTokens * MOE_MAX_TOPK;
 constexpr int kRowsAtMost = kPairs + kTokens;
 constexpr int kChunk = 384;                     // features of the router's operands at a time
 constexpr int kColumns = 512;                   // a tile's outputs: 8 warps of 64
+constexpr int kOwnTokens = 4;                   // up to so many every block chooses for itself
 // a grid barrier gives up after about a second
 constexpr long long kWaitCycles = 2000000000ll;
 
@@ -62,8 +76,11 @@ struct Args {
   float* logits;
   int32_t* idx;
   float* prob;
-  float* main;   // partial sums that begin a tile: rows x outputs
-  float* extra;  // those that go on with one: [block][T][512]
+  float* main[2];   // of a product: partial sums that begin a tile, rows x outputs
+  float* extra[2];  // those that go on with one: [block][T][512]
+  int* tiles;       // partial sums that a tile of FC1 has
+  int* ready;       // tiles of an expert whose hidden values are there
+  int counters;     // of the two
   void* hid;     // [rows, f]; bf16: twice (the second pieces)
   int64_t hid_lo;
 };
@@ -80,7 +97,7 @@ struct Plan {
   int16_t total[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS];
   int16_t before[kWarps][MOE_MAX_EXPERTS];
   uint8_t rank[kPairs];
-  float logit[MOE_MAX_EXPERTS], gsel[MOE_MAX_EXPERTS];
+  float logit[kOwnTokens][MOE_MAX_EXPERTS], gsel[kOwnTokens][MOE_MAX_EXPERTS];
   float part[kThreads];
   int on, dropped;
 };
@@ -107,11 +124,29 @@ __device__ bool grid_barrier(const Args& a, Plan& plan, int n) {
         on = 0;
         break;
       }
-    __threadfence();
     plan.on = on;
   }
   __syncthreads();
   return plan.on != 0;
+}
+
+// Until an expert's hidden values are there.  false as above.
+__device__ bool expert_ready(const Args& a, Plan& plan, int hit, int tiles) {
+  if (threadIdx.x == 0) {
+    const long long began = clock64();
+    int on = 1;
+    while (load_acquire(a.ready + hit) < tiles)
+      if (clock64() - began > kWaitCycles) {
+        report_error(a.err, DEV_ERR_TIMEOUT, hit);
+        on = 0;
+        break;
+      }
+    plan.on = on;
+  }
+  __syncthreads();
+  const bool on = plan.on != 0;
+  __syncthreads();
+  return on;
 }
 
 // The last block to leave sets the counters back, a wait that ran out or not.
@@ -159,7 +194,10 @@ struct Form<__nv_bfloat16> {
 template <>
 struct Form<float> {
   static constexpr int kInputs = 16, kPieces = 16;
-  __device__ static int place(int row, int piece) { return row * 256 + (piece << 4); }
+  // rows read together differ in bits 2 and 3 of the input, eight outputs of each
+  __device__ static int place(int row, int piece) {
+    return row * 256 + ((piece ^ (((row >> 2) & 3) * 2)) << 4);
+  }
 };
 
 // ------------------------------------------------------------------ the streams
@@ -170,12 +208,13 @@ struct Stream {
   int64_t S, begin, end;
   int tiles, units;        // of a routed expert; of a tile
   int routed;              // tiles of all of them
+  int shared_tiles;        // of the shared expert
   int shared_units;        // of one of the shared expert's tiles
   int64_t routed_units;
   int G;
 
-  __device__ void set(int hits, int tiles_, int units_, int shared_tiles, int shared_units_) {
-    tiles = tiles_, units = units_, shared_units = shared_units_;
+  __device__ void set(int hits, int tiles_, int units_, int shared_tiles_, int shared_units_) {
+    tiles = tiles_, units = units_, shared_tiles = shared_tiles_, shared_units = shared_units_;
     routed = hits * tiles;
     routed_units = static_cast<int64_t>(routed) * units;
     S = routed_units + static_cast<int64_t>(shared_tiles) * shared_units;
@@ -331,6 +370,26 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// v as two tf32 numbers: the nearest (halves away from zero, by the carry of half a
+// step), and that of the rest, whose last bits the instruction does not read.
+__device__ __forceinline__ void two_tf32(uint32_t v, uint32_t& p, uint32_t& q) {
+  p = (v + 0x1000u) & 0xffffe000u;
+  q = __float_as_uint(__uint_as_float(v) - __uint_as_float(p)) + 0x1000u;
+}
+__device__ __forceinline__ uint32_t load_shared(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
 // Not through the read-only path: hidden values are written by this launch.
 __device__ __forceinline__ uint4 load16(const void* p) {
   uint4 v;
@@ -348,13 +407,15 @@ struct Out {
   int limit;  // outputs from `at` on
 };
 
-// A run of units of one tile, bf16, up to 8 NT rows.  rows: offsets of the rows' inputs.
-template <int NT, int PIECES>
-__device__ __forceinline__ void run_units(Copies<__nv_bfloat16>& copies, int& slot, int units,
-                                          const __nv_bfloat16* x, int64_t x_lo,
-                                          const uint16_t* row_at, int first, int count, int width,
-                                          const Out& out) {
-  using F = Form<__nv_bfloat16>;
+// A run of units of one tile, up to 8 NT rows, PIECES numbers to an input of bf16.
+// x: the rows' inputs from this run's first on; `left`: how many there are.
+template <typename T, int NT, int PIECES>
+__device__ __forceinline__ void run_units(Copies<T>& copies, int& slot, int units, const T* x,
+                                          int64_t x_lo, const uint16_t* row_at, int first,
+                                          int count, int width, int left, const Out& out) {
+  using F = Form<T>;
+  constexpr bool kHalf = sizeof(T) == 2;
+  constexpr int kLane = F::kInputs / 4;  // inputs of a lane: 16 bytes
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   float acc[4][NT][4];
 #pragma unroll
@@ -369,43 +430,93 @@ __device__ __forceinline__ void run_units(Copies<__nv_bfloat16>& copies, int& sl
   for (int n = 0; n < NT; ++n) {
     const int r = first + min(n * 8 + g, count - 1);
     off[n] = (row_at ? static_cast<uint32_t>(row_at[r]) : static_cast<uint32_t>(r - first)) *
-                 static_cast<uint32_t>(width) + t * 8;
+                 static_cast<uint32_t>(width) + t * kLane;
   }
-  // instruction s of the unit takes the inputs 8 t + 4 s .. + 3 of each t: its slots
-  // 2 t, 2 t + 1 are the first two and 2 t + 8, 2 t + 9 the others
-  const int j = lane >> 3, r = lane & 7;
-  const int row = 8 * (r >> 1) + 2 * (j >> 1) + (r & 1);
+  // The unit's inputs are kLane to each t.  bf16: instruction s takes 8 t + 4 s .. + 3, its
+  // slots 2 t, 2 t + 1 the first two and 2 t + 8, 2 t + 9 the others.  fp32: 4 t + 2 s, + 1,
+  // the slots t and t + 4.
   uint32_t from[2][4];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int m = 0; m < 4; ++m) from[s][m] = F::place(row + 4 * s, m * 2 + (j & 1));
+    for (int m = 0; m < 4; ++m) {
+      if (kHalf) {
+        const int j = lane >> 3, r = lane & 7;
+        from[s][m] = F::place(8 * (r >> 1) + 2 * (j >> 1) + (r & 1) + 4 * s, m * 2 + (j & 1));
+      } else {
+        from[s][m] = F::place(4 * t + 2 * s, m * 4 + (g >> 2)) + (g & 3) * 4;
+      }
+    }
 
-#pragma unroll 1
-  for (int u = 0; u < units; ++u) {
-    uint4 v[PIECES][NT];
+  uint4 v[PIECES][NT];
+  auto read = [&](int at) {  // inputs past the row's end are none
 #pragma unroll
     for (int p = 0; p < PIECES; ++p)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) v[p][n] = load16(x + p * x_lo + off[n]);
+      for (int n = 0; n < NT; ++n) {
+        if (kHalf) {
+          v[p][n] = load16(x + p * x_lo + off[n]);
+        } else {
+          v[p][n] = make_uint4(0u, 0u, 0u, 0u);
+          if (at + t * kLane < left) v[p][n] = load16(x + off[n]);
+        }
+      }
     x += F::kInputs;
+  };
+  constexpr bool kAhead = NT * PIECES <= 8;  // as the registers allow
+  if (kAhead) read(0);
+#pragma unroll 1
+  for (int u = 0; u < units; ++u) {
+    if (!kAhead) read(u * F::kInputs);
+    uint4 now[PIECES][NT];
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) now[p][n] = v[p][n];
+    if (kAhead && u + 1 < units) read((u + 1) * F::kInputs);
     wait_copies<kSlots - 2>();
     __syncwarp();
     copies.issue();  // into the slot that was read last
     const uint32_t at = copies.ring + slot * kUnit;
     if (++slot == kSlots) slot = 0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < 2; ++s) {
+      if constexpr (kHalf) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        uint32_t w[4];
-        ldmatrix_x4_trans(at + from[s][m], w);
+        for (int m = 0; m < 4; ++m) {
+          uint32_t w[4];
+          ldmatrix_x4_trans(at + from[s][m], w);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int p = 0; p < PIECES; ++p)
-            mma_bf16(acc[m][n], w, s ? v[p][n].z : v[p][n].x, s ? v[p][n].w : v[p][n].y);
+            for (int p = 0; p < PIECES; ++p)
+              mma_bf16(acc[m][n], w, s ? now[p][n].z : now[p][n].x, s ? now[p][n].w : now[p][n].y);
+        }
+      } else {
+        uint32_t xp[NT][2], xq[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          two_tf32(s ? now[0][n].z : now[0][n].x, xp[n][0], xq[n][0]);
+          two_tf32(s ? now[0][n].w : now[0][n].y, xp[n][1], xq[n][1]);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          // outputs g and g + 8 of 16 (two pieces on), inputs of the slots t and t + 4
+          const uint32_t q = at + from[s][m], q8 = at + (from[s][m] ^ 32);
+          uint32_t wp[4], wq[4];
+          two_tf32(load_shared(q), wp[0], wq[0]);
+          two_tf32(load_shared(q8), wp[1], wq[1]);
+          two_tf32(load_shared(q + 256), wp[2], wq[2]);
+          two_tf32(load_shared(q8 + 256), wp[3], wq[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_tf32(acc[m][n], wp, xq[n][0], xq[n][1]);
+            mma_tf32(acc[m][n], wq, xp[n][0], xp[n][1]);
+            mma_tf32(acc[m][n], wp, xp[n][0], xp[n][1]);
+          }
+        }
       }
+    }
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -421,55 +532,6 @@ __device__ __forceinline__ void run_units(Copies<__nv_bfloat16>& copies, int& sl
         }
       }
     }
-}
-
-// The same, fp32: two outputs to a lane.
-template <int NR>
-__device__ __forceinline__ void run_units(Copies<float>& copies, int& slot, int units,
-                                          const float* x, const uint16_t* row_at, int first,
-                                          int count, int width, int inputs, const Out& out) {
-  const int lane = threadIdx.x & 31;
-  float acc[NR][2];
-#pragma unroll
-  for (int n = 0; n < NR; ++n) acc[n][0] = acc[n][1] = 0.f;
-  int k = 0;
-#pragma unroll 1
-  for (int u = 0; u < units; ++u) {
-    wait_copies<kSlots - 2>();
-    __syncwarp();
-    copies.issue();
-    const uint32_t at = copies.ring + slot * kUnit + lane * 8;
-    if (++slot == kSlots) slot = 0;
-#pragma unroll 1
-    for (int q = 0; q < 4; ++q, k += 4) {
-      if (k >= inputs) break;  // inputs are a multiple of 8
-      float w[4][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                     : "=f"(w[i][0]), "=f"(w[i][1])
-                     : "r"(at + (q * 4 + i) * 256)
-                     : "memory");
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        const int r = first + min(n, count - 1);
-        const uint32_t row = row_at ? row_at[r] : r - first;
-        const uint4 b = load16(x + row * static_cast<uint32_t>(width) + k);
-        const float v[4] = {__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z),
-                            __uint_as_float(b.w)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[n][0] = fmaf(v[i], w[i][0], acc[n][0]);
-          acc[n][1] = fmaf(v[i], w[i][1], acc[n][1]);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < NR; ++n)
-    if (n < count && lane * 2 < out.limit)  // the outputs are a multiple of 8
-      *reinterpret_cast<float2*>(out.at + n * out.stride + lane * 2) =
-          make_float2(acc[n][0], acc[n][1]);
 }
 
 // ------------------------------------------------------------------ the steps
@@ -556,55 +618,68 @@ __device__ void partial_logits(const Args& a, char* smem) {
   }
 }
 
+// A token's experts, by one warp; logits in plan.logit[at].  own: into this block's plan.
 template <int PL>
-__device__ void choose(const Args& a, Plan& plan, int t) {
+__device__ void choose(const Args& a, Plan& plan, int t, int at, bool own) {
   const int lane = threadIdx.x & 31;
   float s[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = lane + 32 * i;
-    s[i] = e < a.E ? plan.logit[e] : -FLT_MAX;
+    s[i] = e < a.E ? plan.logit[at][e] : -FLT_MAX;
   }
   int idx;
   float p;
-  choose_topk<PL>(s, t, a.E, a.k, a.score, a.groups, a.group_topk, a.expert_bias, plan.gsel, a.err,
-                  idx, p);
-  if (lane < a.k) {
-    a.idx[t * a.k + lane] = idx;
-    a.prob[t * a.k + lane] = p;
-    if (a.idx_out) a.idx_out[t * a.k + lane] = idx;
-    if (a.prob_out) a.prob_out[t * a.k + lane] = p;
+  choose_topk<PL>(s, t, a.E, a.k, a.score, a.groups, a.group_topk, a.expert_bias, plan.gsel[at],
+                  a.err, idx, p);
+  if (lane >= a.k) return;
+  const int i = t * a.k + lane;
+  if (own) {
+    plan.expert[i] = static_cast<int16_t>(idx);
+    plan.prob[i] = p;
+    if (blockIdx.x != 0) return;
+  } else {
+    a.idx[i] = idx;
+    a.prob[i] = p;
   }
+  if (a.idx_out) a.idx_out[i] = idx;
+  if (a.prob_out) a.prob_out[i] = p;
 }
 
-__device__ void choose_experts(const Args& a, Plan& plan) {
+// own: every block for all tokens, else each block for its own.
+__device__ void choose_experts(const Args& a, Plan& plan, bool own) {
   const int n_slabs = slabs(gridDim.x, a.E, a.h);
   int width = 8;
   while (width < a.E) width *= 2;
   const int parts = kThreads / width, e = threadIdx.x % width, part = threadIdx.x / width;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float sum = 0.f;
-    if (e < a.E) {
+  const int warp = threadIdx.x >> 5;
+  const int first = own ? 0 : blockIdx.x, step = own ? a.T : gridDim.x, each = own ? a.T : 1;
+  for (int t0 = first; t0 < a.T; t0 += step) {
+    for (int q = 0; q < each; ++q) {
+      float sum = 0.f;
+      if (e < a.E) {
 #pragma unroll 8
-      for (int s = part; s < n_slabs; s += parts)
-        sum += __ldcg(a.logits + (static_cast<int64_t>(s) * a.T + t) * a.E + e);
+        for (int s = part; s < n_slabs; s += parts)
+          sum += __ldcg(a.logits + (static_cast<int64_t>(s) * a.T + t0 + q) * a.E + e);
+      }
+      __syncthreads();
+      plan.part[threadIdx.x] = sum;
+      __syncthreads();
+      if (threadIdx.x < a.E) {
+        float l = 0.f;
+        for (int i = 0; i < parts; ++i) l += plan.part[i * width + threadIdx.x];
+        plan.logit[q][threadIdx.x] = a.gate_bias ? l + a.gate_bias[threadIdx.x] : l;
+      }
     }
     __syncthreads();
-    plan.part[threadIdx.x] = sum;
-    __syncthreads();
-    if (threadIdx.x < a.E) {
-      float l = 0.f;
-      for (int i = 0; i < parts; ++i) l += plan.part[i * width + threadIdx.x];
-      plan.logit[threadIdx.x] = a.gate_bias ? l + a.gate_bias[threadIdx.x] : l;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      if (a.E <= 32) choose<1>(a, plan, t);
-      else if (a.E <= 64) choose<2>(a, plan, t);
-      else if (a.E <= 128) choose<4>(a, plan, t);
-      else choose<8>(a, plan, t);
+    if (warp < each) {
+      if (a.E <= 32) choose<1>(a, plan, t0 + warp, warp, own);
+      else if (a.E <= 64) choose<2>(a, plan, t0 + warp, warp, own);
+      else if (a.E <= 128) choose<4>(a, plan, t0 + warp, warp, own);
+      else choose<8>(a, plan, t0 + warp, warp, own);
     }
   }
+  __syncthreads();
 }
 
 // Rows by expert: pairs counted and ranked in their order, 64 of them to a warp.
@@ -671,15 +746,88 @@ __device__ void order_pairs(const Args& a, Plan& plan) {
   __syncthreads();
 }
 
-// Every block builds the same plan.
-__device__ void make_plan(const Args& a, Plan& plan) {
+// The plan of up to 32 pairs, by one warp: a pair to a lane, places by counting.
+__device__ void plan_of_few(const Args& a, Plan& plan) {
+  const int lane = threadIdx.x, pairs = plan.pairs;
+  int e = lane < pairs ? plan.expert[lane] : -1;
+  const uint32_t bits = lane < pairs ? __float_as_uint(plan.prob[lane]) : 0u;
+  const int token = lane < pairs ? lane / a.k : -1;
+  // as in make_plan: an expert named twice by a token, drops
+  int place = 0, members = 0;
+  bool twice = false;
+  for (int q = 0; q < pairs; ++q) {
+    const int oe = __shfl_sync(~0u, e, q), ot = __shfl_sync(~0u, token, q);
+    twice |= q < lane && oe == e && ot == token;
+  }
+  if (twice) e = -1;
+  if (a.capacity >= 0) {
+    for (int q = 0; q < pairs; ++q) {
+      const int oe = __shfl_sync(~0u, e, q);
+      const uint32_t ob = __shfl_sync(~0u, bits, q);
+      const bool before = a.policy == MOE_DROP_PROBS ? ob > bits || (ob == bits && q < lane) : q < lane;
+      place += oe == e && before;
+    }
+    if (e >= 0 && place >= a.capacity) {
+      e = -1;
+      if (blockIdx.x == 0 && a.prob_out) a.prob_out[lane] = 0.f;
+    }
+  }
+  // rows before this one, those of its expert, experts before its own
+  int row = 0, hit = 0;
+  bool leads = e >= 0;
+  for (int q = 0; q < pairs; ++q) {
+    const int oe = __shfl_sync(~0u, e, q);
+    row += oe >= 0 && (oe < e || (oe == e && q < lane));
+    members += oe == e;
+    leads &= !(oe == e && q < lane);
+  }
+  for (int q = 0; q < pairs; ++q) {
+    const int oe = __shfl_sync(~0u, e, q);
+    const bool ol = __shfl_sync(~0u, static_cast<int>(leads), q);
+    hit += ol && oe < e;
+  }
+  const int rows = __popc(__ballot_sync(~0u, e >= 0)), hits = __popc(__ballot_sync(~0u, leads));
+  if (lane < pairs) {
+    plan.expert[lane] = static_cast<int16_t>(e);
+    plan.row_of[lane] = static_cast<int16_t>(e >= 0 ? row : -1);
+  }
+  if (e >= 0) {
+    plan.token[row] = static_cast<uint16_t>(token);
+    plan.hit_of_row[row] = static_cast<int16_t>(hit);
+  }
+  if (leads) {
+    plan.hit[hit] = static_cast<int16_t>(e);
+    plan.first[hit] = static_cast<int16_t>(row);
+  }
+  if (lane == 0) {
+    plan.rows = rows;
+    plan.hits = hits;
+    plan.first[hits] = static_cast<int16_t>(rows);
+  }
+  __syncwarp();
+  for (int t = lane; t < a.T; t += 32) plan.token[rows + t] = static_cast<uint16_t>(t);
+  if (blockIdx.x == 0 && a.tpe_out) {
+    for (int i = lane; i < a.E; i += 32) a.tpe_out[i] = 0;
+    __syncwarp();
+    if (leads) a.tpe_out[e] = members;
+  }
+}
+
+// Every block builds the same plan.  own: experts and weights are in it already.
+__device__ void make_plan(const Args& a, Plan& plan, bool own) {
   const int pairs = a.T * a.k;
   if (threadIdx.x == 0) plan.pairs = pairs, plan.dropped = 0;
-  for (int i = threadIdx.x; i < pairs; i += kThreads) {
-    plan.expert[i] = static_cast<int16_t>(__ldcg(a.idx + i));
-    plan.prob[i] = __ldcg(a.prob + i);
-  }
+  if (!own)
+    for (int i = threadIdx.x; i < pairs; i += kThreads) {
+      plan.expert[i] = static_cast<int16_t>(__ldcg(a.idx + i));
+      plan.prob[i] = __ldcg(a.prob + i);
+    }
   __syncthreads();
+  if (pairs <= 32) {
+    if (threadIdx.x < 32) plan_of_few(a, plan);
+    __syncthreads();
+    return;
+  }
   // A token without k experts to choose (NaN logits, reported) names one twice; the
   // first of them stands, so that no expert has more rows than there are tokens.
   bool twice[2] = {false, false};
@@ -748,9 +896,9 @@ __device__ void make_plan(const Args& a, Plan& plan) {
 // Partial sums of a row's outputs in main: FC1's two products side by side.
 __device__ __forceinline__ float* main_row(const Args& a, const Plan& plan, int product, int row,
                                            bool shared) {
-  if (product == 1) return a.main + static_cast<int64_t>(row) * a.h;
-  if (!shared) return a.main + static_cast<int64_t>(row) * 2 * a.f;
-  return a.main + static_cast<int64_t>(plan.rows) * 2 * a.f +
+  if (product == 1) return a.main[1] + static_cast<int64_t>(row) * a.h;
+  if (!shared) return a.main[0] + static_cast<int64_t>(row) * 2 * a.f;
+  return a.main[0] + static_cast<int64_t>(plan.rows) * 2 * a.f +
          static_cast<int64_t>(row - plan.rows) * 2 * a.fs;
 }
 __device__ __forceinline__ int64_t hid_row(const Args& a, const Plan& plan, int row, bool shared) {
@@ -758,69 +906,13 @@ __device__ __forceinline__ int64_t hid_row(const Args& a, const Plan& plan, int 
   return static_cast<int64_t>(plan.rows) * a.f + static_cast<int64_t>(row - plan.rows) * a.fs;
 }
 
-// This block's units of a product.
-template <typename T>
-__device__ void stream_product(const Args& a, const Plan& plan, const Stream& s, int product,
-                               Copies<T>& copies, int& slot) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t u = s.begin; u < s.end;) {
-    int tile, unit;
-    s.find(u, tile, unit);
-    const Tile t = tile_of(a, plan, s, tile);
-    const bool shared = t.hit == plan.hits;
-    const int f = shared ? a.fs : a.f, units =
-        static_cast<int>(min(static_cast<int64_t>(s.units_of(tile) - unit), s.end - u));
-    const int outputs = product ? a.h : f, inputs = product ? f : a.h;
-    const int column = product ? t.at * kColumns + warp * 64 : t.at * 256 + (warp & 3) * 64;
-    Out out;
-    out.limit = outputs - column;
-    if (unit == 0) {
-      out.at = main_row(a, plan, product, t.first, shared) + column +
-               (product == 0 && warp >= 4 ? f : 0);
-      out.stride = product ? a.h : 2 * f;
-    } else {
-      out.at = a.extra + static_cast<int64_t>(blockIdx.x) * a.T * kColumns + warp * 64;
-      out.stride = kColumns;
-    }
-    const int k0 = unit * Form<T>::kInputs;
-    // FC1 reads the rows' tokens, FC2 the hidden values in the rows' order
-    const uint16_t* row_at = product ? nullptr : plan.token;
-    const T* x = product ? static_cast<const T*>(a.hid) + hid_row(a, plan, t.first, shared)
-                         : static_cast<const T*>(a.x);
-    x += k0;
-    if constexpr (sizeof(T) == 2) {
-      if (product == 0) {
-        if (t.rows <= 8) run_units<1, 1>(copies, slot, units, x, 0, row_at, t.first, t.rows, inputs, out);
-        else if (t.rows <= 16) run_units<2, 1>(copies, slot, units, x, 0, row_at, t.first, t.rows, inputs, out);
-        else if (t.rows <= 32) run_units<4, 1>(copies, slot, units, x, 0, row_at, t.first, t.rows, inputs, out);
-        else run_units<8, 1>(copies, slot, units, x, 0, row_at, t.first, t.rows, inputs, out);
-      } else {
-        if (t.rows <= 8) run_units<1, 2>(copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, out);
-        else if (t.rows <= 16) run_units<2, 2>(copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, out);
-        else if (t.rows <= 32) run_units<4, 2>(copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, out);
-        else run_units<8, 2>(copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, out);
-      }
-    } else {
-      const int left = inputs - k0;
-      if (t.rows <= 1) run_units<1>(copies, slot, units, x, row_at, t.first, t.rows, inputs, left, out);
-      else if (t.rows <= 4) run_units<4>(copies, slot, units, x, row_at, t.first, t.rows, inputs, left, out);
-      else if (t.rows <= 16) run_units<16>(copies, slot, units, x, row_at, t.first, t.rows, inputs, left, out);
-      else run_units<64>(copies, slot, units, x, row_at, t.first, t.rows, inputs, left, out);
-    }
-    u += units;
-  }
-  (void)lane;
-}
-
 // A row's sums of four neighbouring outputs, the runs in order.
-__device__ __forceinline__ float4 sum_runs(const Args& a, const Stream& s, const float* main,
-                                           int tile, int row, int column) {
+__device__ __forceinline__ float4 sum_runs(const Args& a, int product, const float* main,
+                                           int first, int last, int row, int column) {
   float4 v = __ldcg(reinterpret_cast<const float4*>(main));
-  int first, last;
-  s.blocks(tile, first, last);
   for (int b = first + 1; b <= last; ++b) {
     const float4 w = __ldcg(reinterpret_cast<const float4*>(
-        a.extra + (static_cast<int64_t>(b) * a.T + row) * kColumns + column));
+        a.extra[product] + (static_cast<int64_t>(b) * a.T + row) * kColumns + column));
     v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
   }
   return v;
@@ -828,30 +920,18 @@ __device__ __forceinline__ float4 sum_runs(const Args& a, const Stream& s, const
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
+// A tile's hidden values, from the partial sums of the blocks `first` to `last`.
 template <typename T>
-__device__ void hidden_values(const Args& a, const Plan& plan, const Stream& s) {
-  const int rows = plan.rows + (a.fs ? a.T : 0);
-  const int64_t routed = static_cast<int64_t>(plan.rows) * (a.f / 4);
-  const int64_t all = routed + static_cast<int64_t>(rows - plan.rows) * (a.fs / 4);
-  for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < all; i += gridDim.x * kThreads) {
-    const bool shared = i >= routed;
-    const int f = shared ? a.fs : a.f;
-    const int64_t v = shared ? i - routed : i;
-    const int in = static_cast<int>(v / (f / 4));
-    const int column = static_cast<int>(v - static_cast<int64_t>(in) * (f / 4)) * 4;
-    const int row = in + (shared ? plan.rows : 0);
-    int tile, n;
-    if (shared) {
-      tile = s.routed + column / 256;
-      n = in;
-    } else {
-      const int hit = plan.hit_of_row[row];
-      tile = hit * s.tiles + column / 256;
-      n = row - plan.first[hit];
-    }
+__device__ void hidden_tile(const Args& a, const Plan& plan, const Tile& t, int first, int last) {
+  const bool shared = t.hit == plan.hits;
+  const int f = shared ? a.fs : a.f;
+  for (int i = threadIdx.x; i < t.rows * 64; i += kThreads) {
+    const int n = i / 64, in = i % 64 * 4, column = t.at * 256 + in;
+    if (column >= f) continue;
+    const int row = t.first + n;
     const float* m = main_row(a, plan, 0, row, shared) + column;
-    const float4 g = sum_runs(a, s, m, tile, n, column % 256);
-    const float4 w = sum_runs(a, s, m + f, tile, n, 256 + column % 256);
+    const float4 g = sum_runs(a, 0, m, first, last, n, in);
+    const float4 w = sum_runs(a, 0, m + f, first, last, n, 256 + in);
     const float o[4] = {swiglu(g.x, w.x), swiglu(g.y, w.y), swiglu(g.z, w.z), swiglu(g.w, w.w)};
     T* to = static_cast<T*>(a.hid) + hid_row(a, plan, row, shared) + column;
     if constexpr (sizeof(T) == 4) {
@@ -869,6 +949,88 @@ __device__ void hidden_values(const Args& a, const Plan& plan, const Stream& s) 
       memcpy(to + a.hid_lo, lo, 8);
     }
   }
+}
+
+// A run of one of FC1's tiles is through: the last block to come forms the hidden values.
+template <typename T>
+__device__ void tile_done(const Args& a, Plan& plan, const Stream& s, int tile, const Tile& t) {
+  int first, last;
+  s.blocks(tile, first, last);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int is_last = 1;
+    if (last > first) {
+      __threadfence();
+      is_last = atomicAdd(a.tiles + tile, 1) == last - first;
+    }
+    __threadfence();
+    plan.on = is_last;
+  }
+  __syncthreads();
+  if (plan.on) {
+    hidden_tile<T>(a, plan, t, first, last);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      __threadfence();
+      atomicAdd(a.ready + t.hit, 1);
+    }
+  }
+}
+
+// This block's units of a product.  false where a wait ran out.
+template <typename T>
+__device__ bool stream_product(const Args& a, Plan& plan, const Stream* streams, int product,
+                               Copies<T>& copies, int& slot) {
+  const Stream& s = streams[product];
+  const int warp = threadIdx.x >> 5;
+  int ready = -1;
+  for (int64_t u = s.begin; u < s.end;) {
+    int tile, unit;
+    s.find(u, tile, unit);
+    const Tile t = tile_of(a, plan, s, tile);
+    const bool shared = t.hit == plan.hits;
+    const int f = shared ? a.fs : a.f, units =
+        static_cast<int>(min(static_cast<int64_t>(s.units_of(tile) - unit), s.end - u));
+    if (product == 1 && ready != t.hit) {
+      if (!expert_ready(a, plan, t.hit, shared ? streams[0].shared_tiles : streams[0].tiles))
+        return false;
+      ready = t.hit;
+    }
+    const int outputs = product ? a.h : f, inputs = product ? f : a.h;
+    const int column = product ? t.at * kColumns + warp * 64 : t.at * 256 + (warp & 3) * 64;
+    Out out;
+    out.limit = outputs - column;
+    if (unit == 0) {
+      out.at = main_row(a, plan, product, t.first, shared) + column +
+               (product == 0 && warp >= 4 ? f : 0);
+      out.stride = product ? a.h : 2 * f;
+    } else {
+      out.at = a.extra[product] + static_cast<int64_t>(blockIdx.x) * a.T * kColumns + warp * 64;
+      out.stride = kColumns;
+    }
+    const int k0 = unit * Form<T>::kInputs;
+    // FC1 reads the rows' tokens, FC2 the hidden values in the rows' order
+    const uint16_t* row_at = product ? nullptr : plan.token;
+    const T* x = product ? static_cast<const T*>(a.hid) + hid_row(a, plan, t.first, shared)
+                         : static_cast<const T*>(a.x);
+    x += k0;
+    constexpr int P2 = sizeof(T) == 2 ? 2 : 1;
+    auto run = [&](auto nt, auto pieces) {
+      run_units<T, decltype(nt)::value, decltype(pieces)::value>(
+          copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, inputs - k0, out);
+    };
+    auto by_rows = [&](auto pieces) {
+      if (t.rows <= 8) run(std::integral_constant<int, 1>(), pieces);
+      else if (t.rows <= 16) run(std::integral_constant<int, 2>(), pieces);
+      else if (t.rows <= 32) run(std::integral_constant<int, 4>(), pieces);
+      else run(std::integral_constant<int, 8>(), pieces);
+    };
+    if (product == 0 || P2 == 1) by_rows(std::integral_constant<int, 1>());
+    else by_rows(std::integral_constant<int, P2>());
+    if (product == 0) tile_done<T>(a, plan, s, tile, t);
+    u += units;
+  }
+  return true;
 }
 
 __device__ __forceinline__ void store4(float* p, float4 v) {
@@ -893,14 +1055,18 @@ __device__ void combine(const Args& a, const Plan& plan, const Stream& s) {
       if (row < 0) continue;
       const int hit = plan.hit_of_row[row];
       const float p = plan.prob[t * a.k + j];
-      const float4 v = sum_runs(a, s, main_row(a, plan, 1, row, false) + column,
-                                hit * s.tiles + at, row - plan.first[hit], column % kColumns);
+      int first, last;
+      s.blocks(hit * s.tiles + at, first, last);
+      const float4 v = sum_runs(a, 1, main_row(a, plan, 1, row, false) + column, first, last,
+                                row - plan.first[hit], column % kColumns);
       y.x = fmaf(p, v.x, y.x), y.y = fmaf(p, v.y, y.y);
       y.z = fmaf(p, v.z, y.z), y.w = fmaf(p, v.w, y.w);
     }
     if (a.fs) {
-      const float4 v = sum_runs(a, s, main_row(a, plan, 1, plan.rows + t, true) + column,
-                                s.routed + at, t, column % kColumns);
+      int first, last;
+      s.blocks(s.routed + at, first, last);
+      const float4 v = sum_runs(a, 1, main_row(a, plan, 1, plan.rows + t, true) + column, first,
+                                last, t, column % kColumns);
       y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
     }
     store4(static_cast<T*>(a.y) + static_cast<int64_t>(t) * a.h + column, y);
@@ -912,37 +1078,36 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   extern __shared__ __align__(1024) char smem[];
   Plan& plan = *reinterpret_cast<Plan*>(smem + kRing);
   __shared__ Stream streams[2];
+  // nobody counts in these before the barrier after the logits
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.counters; i += gridDim.x * kThreads)
+    a.tiles[i] = 0;
   partial_logits<T>(a, smem);
   bool on = grid_barrier(a, plan, 1);
+  const bool own = a.T <= kOwnTokens;
   if (on) {
-    choose_experts(a, plan);
-    on = grid_barrier(a, plan, 2);
+    choose_experts(a, plan, own);
+    if (!own) on = grid_barrier(a, plan, 2);
   }
   if (on) {
-    make_plan(a, plan);
-    if (threadIdx.x == 0) {
+    make_plan(a, plan, own);
+    if (threadIdx.x < 2) {
       constexpr int U = Form<T>::kInputs;
       auto up = [](int n, int d) { return (n + d - 1) / d; };
-      streams[0].set(plan.hits, up(a.f, 256), up(a.h, U), up(a.fs, 256), up(a.h, U));
-      streams[1].set(plan.hits, up(a.h, kColumns), up(a.f, U), a.fs ? up(a.h, kColumns) : 0,
-                     up(a.fs, U));
+      if (threadIdx.x == 0)
+        streams[0].set(plan.hits, up(a.f, 256), up(a.h, U), up(a.fs, 256), up(a.h, U));
+      else
+        streams[1].set(plan.hits, up(a.h, kColumns), up(a.f, U), a.fs ? up(a.h, kColumns) : 0,
+                       up(a.fs, U));
     }
     __syncthreads();
     Copies<T> copies(a, plan, streams, smem);
 #pragma unroll 1
     for (int i = 0; i < kSlots - 1; ++i) copies.issue();
     int slot = 0;
-    stream_product<T>(a, plan, streams[0], 0, copies, slot);
-    on = grid_barrier(a, plan, 3);
-    if (on) {
-      hidden_values<T>(a, plan, streams[0]);
-      on = grid_barrier(a, plan, 4);
-    }
-    if (on) {
-      stream_product<T>(a, plan, streams[1], 1, copies, slot);
-      on = grid_barrier(a, plan, 5);
-    }
+    on = stream_product<T>(a, plan, streams, 0, copies, slot) &&
+         stream_product<T>(a, plan, streams, 1, copies, slot);
     wait_copies<0>();
+    on = on && grid_barrier(a, plan, own ? 2 : 3);
     if (on) combine<T>(a, plan, streams[1]);
   }
   leave(a);
@@ -951,8 +1116,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct Layout {
-  size_t logits, idx, prob, main, extra, hid, total;
+  size_t logits, idx, prob, main[2], extra[2], counters, hid, total;
   int64_t hid_lo;
+  int tiles, all;  // counters
 };
 Layout layout(int T, int h, int E, int k, int f, int fs, int dtype) {
   Layout L;
@@ -967,8 +1133,13 @@ Layout layout(int T, int h, int E, int k, int f, int fs, int dtype) {
   L.logits = take(static_cast<size_t>(slabs(kFewBlocks, E, h)) * T * E * 4);
   L.idx = take(pairs * 4);
   L.prob = take(pairs * 4);
-  L.main = take((2 * values > rows * h ? 2 * values : rows * h) * 4);
-  L.extra = take(static_cast<size_t>(kFewBlocks) * T * kColumns * 4);
+  L.main[0] = take(2 * values * 4);
+  L.main[1] = take(rows * h * 4);
+  for (int i = 0; i < 2; ++i) L.extra[i] = take(static_cast<size_t>(kFewBlocks) * T * kColumns * 4);
+  const int most = pairs < static_cast<size_t>(E) ? static_cast<int>(pairs) : E;  // experts hit
+  L.tiles = most * ((f + 255) / 256) + (fs + 255) / 256;
+  L.all = L.tiles + most + 1;
+  L.counters = take(static_cast<size_t>(L.all) * 4);
   L.hid_lo = static_cast<int64_t>(up256(values * 2) / 2);
   L.hid = take(dtype == MOE_F32 ? values * 4 : static_cast<size_t>(L.hid_lo) * 2 * 2);
   L.total = o;
@@ -1021,8 +1192,13 @@ cudaError_t launch_few(const moe_config& c, int fs, int64_t capacity, const void
   a.logits = reinterpret_cast<float*>(at + L.logits);
   a.idx = reinterpret_cast<int32_t*>(at + L.idx);
   a.prob = reinterpret_cast<float*>(at + L.prob);
-  a.main = reinterpret_cast<float*>(at + L.main);
-  a.extra = reinterpret_cast<float*>(at + L.extra);
+  for (int i = 0; i < 2; ++i) {
+    a.main[i] = reinterpret_cast<float*>(at + L.main[i]);
+    a.extra[i] = reinterpret_cast<float*>(at + L.extra[i]);
+  }
+  a.tiles = reinterpret_cast<int*>(at + L.counters);
+  a.ready = a.tiles + L.tiles;
+  a.counters = L.all;
   a.hid = at + L.hid;
   a.hid_lo = L.hid_lo;
   return c.dtype == MOE_F32 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);
