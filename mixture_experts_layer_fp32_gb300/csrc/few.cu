@@ -203,47 +203,46 @@ struct Form<float> {
 // ------------------------------------------------------------------ the streams
 // One product's stream: tiles of 512 outputs (FC1: 256 of W1 and the same of W3), an
 // expert's one after another, the shared expert's last; a tile's units follow the
-// inputs.  Block b of the first G has the units [S b / G, S (b + 1) / G).
+// inputs.  They are cut into equal runs, one to a block.  Units are counted in 32 bits:
+// 2^31 of 32 KB are past any memory (the caller checks).
 struct Stream {
-  int64_t S, begin, end;
+  int S, begin, end;
   int tiles, units;        // of a routed expert; of a tile
   int routed;              // tiles of all of them
   int shared_tiles;        // of the shared expert
   int shared_units;        // of one of the shared expert's tiles
-  int64_t routed_units;
-  int G;
+  int routed_units;
+  int each, rest;          // units of a block; the first `rest` blocks have one more
 
   __device__ void set(int hits, int tiles_, int units_, int shared_tiles_, int shared_units_) {
     tiles = tiles_, units = units_, shared_tiles = shared_tiles_, shared_units = shared_units_;
     routed = hits * tiles;
-    routed_units = static_cast<int64_t>(routed) * units;
-    S = routed_units + static_cast<int64_t>(shared_tiles) * shared_units;
-    // no more blocks than units, so that every block between two has some
-    G = static_cast<int>(min(S, static_cast<int64_t>(gridDim.x)));
-    const int b = min(static_cast<int>(blockIdx.x), G);
-    begin = G ? S * b / G : 0;
-    end = b < G ? S * (b + 1) / G : S;
+    routed_units = routed * units;
+    S = routed_units + shared_tiles * shared_units;
+    const int G = gridDim.x, b = blockIdx.x;
+    each = S / G, rest = S - each * G;
+    begin = b * each + min(b, rest);
+    end = begin + each + (b < rest);
   }
-  __device__ void find(int64_t u, int& tile, int& unit) const {
+  __device__ void find(int u, int& tile, int& unit) const {
     if (u < routed_units) {
-      tile = static_cast<int>(u / units);
-      unit = static_cast<int>(u - static_cast<int64_t>(tile) * units);
+      tile = u / units;
+      unit = u - tile * units;
     } else {
-      const int64_t v = u - routed_units;
-      const int t = static_cast<int>(v / shared_units);
+      const int t = (u - routed_units) / shared_units;
       tile = routed + t;
-      unit = static_cast<int>(v - static_cast<int64_t>(t) * shared_units);
+      unit = u - routed_units - t * shared_units;
     }
   }
   __device__ int units_of(int tile) const { return tile < routed ? units : shared_units; }
-  __device__ int block_of(int64_t u) const {
-    return static_cast<int>(((u + 1) * G - 1) / S);
+  __device__ int block_of(int u) const {
+    const int longer = rest * (each + 1);
+    return u < longer ? u / (each + 1) : rest + (u - longer) / each;
   }
   // the blocks that have a tile's units
   __device__ void blocks(int tile, int& first, int& last) const {
-    const int64_t u = tile < routed
-                          ? static_cast<int64_t>(tile) * units
-                          : routed_units + static_cast<int64_t>(tile - routed) * shared_units;
+    const int u =
+        tile < routed ? tile * units : routed_units + (tile - routed) * shared_units;
     first = block_of(u);
     last = block_of(u + units_of(tile) - 1);
   }
@@ -280,7 +279,7 @@ struct Copies {
   const Stream* streams;
   uint32_t ring;      // this lane's place in a slot
   int product = 0, left = 0, slot = 0;
-  int64_t next = 0;   // unit
+  int next = 0;       // unit
   int unit = 0, units = 0, inputs = 0, outputs = 0;
   bool real = false;
   const T* src = nullptr;
@@ -293,7 +292,7 @@ struct Copies {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       dst[i] = F::place(lane / F::kPieces + i * kStep, lane % F::kPieces);
-    left = static_cast<int>(s[0].end - s[0].begin);
+    left = s[0].end - s[0].begin;
     next = s[0].begin;
   }
 
@@ -328,7 +327,7 @@ struct Copies {
   __device__ __forceinline__ void issue() {
     if (left == 0 && product == 0) {
       product = 1;
-      left = static_cast<int>(streams[1].end - streams[1].begin);
+      left = streams[1].end - streams[1].begin;
       next = streams[1].begin;
       unit = units = 0;
     }
@@ -658,7 +657,7 @@ __device__ void choose_experts(const Args& a, Plan& plan, bool own) {
     for (int q = 0; q < each; ++q) {
       float sum = 0.f;
       if (e < a.E) {
-#pragma unroll 8
+#pragma unroll 16
         for (int s = part; s < n_slabs; s += parts)
           sum += __ldcg(a.logits + (static_cast<int64_t>(s) * a.T + t0 + q) * a.E + e);
       }
@@ -910,10 +909,17 @@ __device__ __forceinline__ int64_t hid_row(const Args& a, const Plan& plan, int 
 __device__ __forceinline__ float4 sum_runs(const Args& a, int product, const float* main,
                                            int first, int last, int row, int column) {
   float4 v = __ldcg(reinterpret_cast<const float4*>(main));
-  for (int b = first + 1; b <= last; ++b) {
-    const float4 w = __ldcg(reinterpret_cast<const float4*>(
-        a.extra[product] + (static_cast<int64_t>(b) * a.T + row) * kColumns + column));
-    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+  for (int b = first + 1; b <= last; b += 8) {  // eight loads at a time
+    float4 w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (b + i <= last)
+        w[i] = __ldcg(reinterpret_cast<const float4*>(
+            a.extra[product] + (static_cast<int64_t>(b + i) * a.T + row) * kColumns + column));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.x += w[i].x, v.y += w[i].y, v.z += w[i].z, v.w += w[i].w;
   }
   return v;
 }
@@ -984,13 +990,12 @@ __device__ bool stream_product(const Args& a, Plan& plan, const Stream* streams,
   const Stream& s = streams[product];
   const int warp = threadIdx.x >> 5;
   int ready = -1;
-  for (int64_t u = s.begin; u < s.end;) {
+  for (int u = s.begin; u < s.end;) {
     int tile, unit;
     s.find(u, tile, unit);
     const Tile t = tile_of(a, plan, s, tile);
     const bool shared = t.hit == plan.hits;
-    const int f = shared ? a.fs : a.f, units =
-        static_cast<int>(min(static_cast<int64_t>(s.units_of(tile) - unit), s.end - u));
+    const int f = shared ? a.fs : a.f, units = min(s.units_of(tile) - unit, s.end - u);
     if (product == 1 && ready != t.hit) {
       if (!expert_ready(a, plan, t.hit, shared ? streams[0].shared_tiles : streams[0].tiles))
         return false;
