@@ -1,4 +1,6 @@
 // 8-bit integers: rows to codes with a scale each, and the product for few rows.
+#include <type_traits>
+
 #include "i8.cuh"
 
 namespace moe {
@@ -41,6 +43,57 @@ __device__ __forceinline__ void store_codes(__half* at, const int (&c)[4]) {
   memcpy(at, v, 8);
 }
 
+template <typename T>
+__device__ __forceinline__ Piece<T> read_piece(const T* at) {
+  const uint4 q = *reinterpret_cast<const uint4*>(at);
+  Piece<T> p;
+  memcpy(&p, &q, 16);
+  return p;
+}
+
+// The largest magnitude, and whether all are numbers.
+struct Top {
+  float most = 0.f;
+  bool good = true;
+  template <typename T>
+  __device__ __forceinline__ void look(const Piece<T>& p) {
+#pragma unroll
+    for (int i = 0; i < Piece<T>::n; ++i) {
+      const float v = fabsf(as_float(p.v[i]));
+      most = fmaxf(most, v);
+      good &= v < INFINITY;
+    }
+  }
+  __device__ __forceinline__ void of_warp() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+    good = __all_sync(~0u, good);
+  }
+};
+
+struct Coder {
+  float scale, up, s, inverse;
+  bool some;
+  __device__ __forceinline__ explicit Coder(const Top& top) {
+    scale = top.good ? top.most / 127.f : NAN;
+    // no reciprocal of a scale past 2^-126 is lost to overflow
+    up = scale < 0x1p-100f ? 0x1p64f : 1.f;
+    some = scale > 0.f;  // neither 0 nor NaN
+    s = scale * up;
+    inverse = some ? 1.f / s : 0.f;
+  }
+  template <typename T, typename Code>
+  __device__ __forceinline__ void put(const Piece<T>& p, Code* out) const {
+#pragma unroll
+    for (int i = 0; i < Piece<T>::n; i += 4) {
+      int c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = some ? code_of(as_float(p.v[i + j]) * up, s, inverse) : 0;
+      store_codes(out + i, c);
+    }
+  }
+};
+
 template <typename T, typename Code>
 __global__ void __launch_bounds__(kQuantThreads)
     quantize_kernel(int K, const T* x, Code* codes, float* scales) {
@@ -51,60 +104,31 @@ __global__ void __launch_bounds__(kQuantThreads)
   Code* out = codes + row * K;
   pdl_trigger();
   Piece<T> held[kHeld];
-  float top = 0.f;
-  bool good = true;  // neither an infinity nor a NaN
-  auto look = [&](const Piece<T>& p) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float a = fabsf(as_float(p.v[i]));
-      top = fmaxf(top, a);
-      good &= a < INFINITY;
-    }
-  };
+  Top top;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int k = (i * kQuantThreads + threadIdx.x) * V;
-    if (k < K) memcpy(&held[i], __builtin_assume_aligned(xr + k, 16), 16);
+    if (k < K) held[i] = read_piece(xr + k);
   }
 #pragma unroll
   for (int i = 0; i < kHeld; ++i)
-    if ((i * kQuantThreads + threadIdx.x) * V < K) look(held[i]);
-  for (int k = (kHeld * kQuantThreads + threadIdx.x) * V; k < K; k += kQuantThreads * V) {
-    Piece<T> p;
-    memcpy(&p, __builtin_assume_aligned(xr + k, 16), 16);
-    look(p);
-  }
+    if ((i * kQuantThreads + threadIdx.x) * V < K) top.look(held[i]);
+  for (int k = (kHeld * kQuantThreads + threadIdx.x) * V; k < K; k += kQuantThreads * V)
+    top.look(read_piece(xr + k));
+  top.of_warp();
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top.most;
+  top.good = __syncthreads_and(top.good);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-  good = __syncthreads_and(good);
-#pragma unroll
-  for (int w = 0; w < kQuantThreads / 32; ++w) top = fmaxf(top, tops[w]);
-  const float scale = good ? top / 127.f : NAN;
-  if (threadIdx.x == 0) scales[row] = scale;
-  // no reciprocal of a scale past 2^-126 is lost to overflow
-  const float up = scale < 0x1p-100f ? 0x1p64f : 1.f;
-  const bool some = scale > 0.f;  // neither 0 nor NaN
-  const float s = scale * up, inverse = some ? 1.f / s : 0.f;
-  auto put = [&](const Piece<T>& p, int k) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      int c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = some ? code_of(as_float(p.v[i + j]) * up, s, inverse) : 0;
-      store_codes(out + k + i, c);
-    }
-  };
+  for (int w = 0; w < kQuantThreads / 32; ++w) top.most = fmaxf(top.most, tops[w]);
+  const Coder coder(top);
+  if (threadIdx.x == 0) scales[row] = coder.scale;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int k = (i * kQuantThreads + threadIdx.x) * V;
-    if (k < K) put(held[i], k);
+    if (k < K) coder.put(held[i], out + k);
   }
-  for (int k = (kHeld * kQuantThreads + threadIdx.x) * V; k < K; k += kQuantThreads * V) {
-    Piece<T> p;
-    memcpy(&p, __builtin_assume_aligned(xr + k, 16), 16);
-    put(p, k);
-  }
+  for (int k = (kHeld * kQuantThreads + threadIdx.x) * V; k < K; k += kQuantThreads * V)
+    coder.put(read_piece(xr + k), out + k);
 }
 
 template <typename T, typename Code>
@@ -138,9 +162,46 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kNarrowWarps * 32)
+// The rows' codes into shared memory (`pitch` bytes a row), scales beside them, by the
+// whole block: 8 / 4 / 2 / 1 warps to a row of 1, 2, 4, 8.
+template <typename T>
+__device__ void quantize_here(const T* x, int rows, int K, int8_t* codes, int pitch,
+                              float* scales) {
+  constexpr int V = Piece<T>::n;
+  __shared__ float tops[kNarrowWarps];
+  __shared__ int goods[kNarrowWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int each = rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;
+  const int row = warp / each, part = warp % each, step = each * 32 * V;
+  const T* xr = x + static_cast<int64_t>(row) * K;
+  const int first = (part * 32 + lane) * V;
+  Top top;
+  if (row < rows) {
+#pragma unroll 2
+    for (int k = first; k < K; k += step) top.look(read_piece(xr + k));
+    top.of_warp();
+  }
+  if (lane == 0) tops[warp] = top.most, goods[warp] = top.good;
+  __syncthreads();
+  if (row < rows) {
+    for (int w = row * each; w < (row + 1) * each; ++w)
+      top.most = fmaxf(top.most, tops[w]), top.good &= goods[w] != 0;
+    const Coder coder(top);
+    if (part == 0 && lane == 0) scales[row] = coder.scale;
+#pragma unroll 1
+    for (int k = first; k < K; k += step)
+      coder.put(read_piece(xr + k), codes + static_cast<int64_t>(row) * pitch + k);
+  }
+  __syncthreads();
+}
+
+// X: what x is; codes, or values that the kernel quantises itself (up to 8 rows).
+template <int NT, typename X>
+__global__ void __launch_bounds__(kNarrowWarps * 32, 2)
     narrow_kernel(const __grid_constant__ Args a, int parts, int first_row) {
+  constexpr bool kHere = !std::is_same<X, int8_t>::value;
+  extern __shared__ __align__(16) int8_t here[];
+  __shared__ float here_scales[8];
   __shared__ int sums[kNarrowWarps][16 * 8 * NT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int part = warp % parts, group = blockIdx.x * (kNarrowWarps / parts) + warp / parts;
@@ -157,10 +218,14 @@ __global__ void __launch_bounds__(kNarrowWarps * 32)
   // outputs and rows past the last one repeat it; what they give is not stored
   const int8_t* w0 = a.W + static_cast<int64_t>(min(n0 + g, a.N - 1)) * a.K + t * 16;
   const int8_t* w1 = a.W + static_cast<int64_t>(min(n0 + g + 8, a.N - 1)) * a.K + t * 16;
+  const int pitch = a.K + 64;  // neighbouring rows in other banks
   const int8_t* xs[NT];
 #pragma unroll
-  for (int c = 0; c < NT; ++c)
-    xs[c] = a.x + (row0 + min(c * 8 + g, rows - 1)) * a.K + t * 16;
+  for (int c = 0; c < NT; ++c) {
+    const int r = min(c * 8 + g, rows - 1);
+    xs[c] = kHere ? here + r * pitch + t * 16
+                  : static_cast<const int8_t*>(a.x) + (row0 + r) * a.K + t * 16;
+  }
   uint4 w[2][kSteps][2];
   auto load = [&](int set, int step) {
 #pragma unroll
@@ -172,7 +237,10 @@ __global__ void __launch_bounds__(kNarrowWarps * 32)
     }
   };
   load(0, begin);
-  pdl_wait();  // x
+  if constexpr (kHere)
+    quantize_here(static_cast<const X*>(a.x), rows, a.K, here, pitch, here_scales);
+  else
+    pdl_wait();  // x
   auto use = [&](int set, int step) {
     uint4 x[NT][kSteps];
 #pragma unroll
@@ -213,38 +281,36 @@ __global__ void __launch_bounds__(kNarrowWarps * 32)
     if (out >= a.N) continue;
     int sum = 0;
     for (int p = 0; p < parts; ++p) sum += sums[gr * parts + p][m * 16 + n];
-    const float v = scaled(sum, a.x_scale[row0 + m], a.w_scale[out], a.bias ? a.bias[out] : 0.f);
+    const float v = scaled(sum, kHere ? here_scales[m] : a.x_scale[row0 + m], a.w_scale[out], a.bias ? a.bias[out] : 0.f);
     const int64_t to = (row0 + m) * a.N + out;
     if (a.out_f32) static_cast<float*>(a.y)[to] = v;
     else static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
   }
 }
 
-// The kernel reads weights before it waits for the launch before it, which therefore
-// has to be this call's own quantising (itself begun after all that came earlier);
-// after anything else it is launched as usual.
-template <int NT>
+// X int8_t: the kernel reads weights before it waits for the launch before it, which
+// therefore has to be this call's own quantising (itself begun after all that came
+// earlier); after anything else it is launched as usual.
+template <typename X>
 cudaError_t narrow(const Args& a, bool after_own, cudaStream_t s) {
   // warps for 16 on each of 152 SMs, where the inputs allow it
   const int groups = (a.N + 15) / 16;
   int parts = 1;
   while (parts < kNarrowWarps && groups * parts < 2432 && a.K / (parts * 2) >= 256) parts *= 2;
   const int each = kNarrowWarps / parts;
-  for (int64_t r = 0; r < a.rows; r += 65535ll * 8 * NT) {
-    const int64_t left = (a.rows - r + 8 * NT - 1) / (8 * NT);
-    const dim3 grid((groups + each - 1) / each, static_cast<unsigned>(left < 65535 ? left : 65535));
-    const dim3 block(kNarrowWarps * 32);
-    cudaError_t st;
-    if (after_own) {
-      st = launch_dependent(narrow_kernel<NT>, grid, block, 0, s, a, parts, static_cast<int>(r));
-    } else {
-      narrow_kernel<NT><<<grid, block, 0, s>>>(a, parts, static_cast<int>(r));
-      st = cudaGetLastError();
-    }
-    if (st != cudaSuccess) return st;
-    after_own = false;
-  }
-  return cudaSuccess;
+  const dim3 grid((groups + each - 1) / each), block(kNarrowWarps * 32);
+  if (after_own) return launch_dependent(narrow_kernel<1, X>, grid, block, 0, s, a, parts, 0);
+  const size_t smem = std::is_same<X, int8_t>::value
+                          ? 0 : static_cast<size_t>(a.rows) * (a.K + 64);
+  narrow_kernel<1, X><<<grid, block, smem, s>>>(a, parts, 0);
+  return cudaGetLastError();
+}
+
+// Whether the narrow kernel's blocks quantise x themselves: it spares a launch (1 x 4096
+// bf16 by 4096 x 4096: 7.4 us on the device where two launches take 7.7, and 7.1 of the
+// host's time where those take 8.5), but each of them reads all of it.
+bool quantize_inside(int64_t rows, int K, int x_dtype) {
+  return rows * K * (x_dtype == MOE_F32 ? 4 : 2) <= 32 * 1024;
 }
 
 // Codes as fp16 numbers, for the wide kernel.
@@ -323,15 +389,18 @@ cudaError_t launch_linear_i8(int64_t rows, int N, int K, const void* x, int x_dt
   float* scales = reinterpret_cast<float*>(at + L.scales);
   const bool coded = x_dtype == MOE_I8;
   if (!coded) a.x_scale = scales;
+  a.x = x;
   if (rows <= kNarrowRows) {
-    a.x = static_cast<const int8_t*>(x);
+    if (!coded && i8::quantize_inside(rows, K, x_dtype))
+      return x_dtype == MOE_F32 ? i8::narrow<float>(a, false, s)
+                                : i8::narrow<__nv_bfloat16>(a, false, s);
     if (!coded) {
       int8_t* codes = reinterpret_cast<int8_t*>(at);
       const cudaError_t st = launch_quantize_rows_i8(rows, K, x_dtype, x, codes, scales, s);
       if (st != cudaSuccess) return st;
       a.x = codes;
     }
-    return i8::narrow<1>(a, !coded, s);
+    return i8::narrow<int8_t>(a, !coded, s);
   }
   __half* halves = reinterpret_cast<__half*>(at);
   cudaError_t st;

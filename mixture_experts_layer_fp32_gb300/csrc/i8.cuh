@@ -10,7 +10,7 @@ namespace i8 {
 // y[m, n] = (sum_k x[m, k] W[n, k]) x_scale[m] w_scale[n] + bias[n]
 struct Args {
   int rows, N, K;
-  const int8_t* x;        // narrow: codes
+  const void* x;          // narrow: codes, or values that it quantises
   const float* x_scale;
   const int8_t* W;
   const float *w_scale, *bias;
