@@ -198,7 +198,7 @@ __device__ void quantize_here(const T* x, int rows, int K, int8_t* codes, int pi
 // X: what x is; codes, or values that the kernel quantises itself (up to 8 rows).
 template <int NT, typename X>
 __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
-    narrow_kernel(const __grid_constant__ Args a, int parts, int first_row) {
+    narrow_kernel(const __grid_constant__ Args a, int parts) {
   constexpr bool kHere = !std::is_same<X, int8_t>::value;
   extern __shared__ __align__(16) int8_t here[];
   __shared__ float here_scales[8];
@@ -206,8 +206,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int part = warp % parts, group = blockIdx.x * (kNarrowWarps / parts) + warp / parts;
   const int n0 = group * 16;
-  const int64_t row0 = static_cast<int64_t>(first_row) + blockIdx.y * 8 * NT;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(8 * NT), a.rows - row0));
+  const int rows = a.rows;
   int acc[NT][4];
 #pragma unroll
   for (int c = 0; c < NT; ++c)
@@ -224,7 +223,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
   for (int c = 0; c < NT; ++c) {
     const int r = min(c * 8 + g, rows - 1);
     xs[c] = kHere ? here + r * pitch + t * 16
-                  : static_cast<const int8_t*>(a.x) + (row0 + r) * a.K + t * 16;
+                  : static_cast<const int8_t*>(a.x) + static_cast<int64_t>(r) * a.K + t * 16;
   }
   uint4 w[2][kSteps][2];
   auto load = [&](int set, int step) {
@@ -281,8 +280,8 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
     if (out >= a.N) continue;
     int sum = 0;
     for (int p = 0; p < parts; ++p) sum += sums[gr * parts + p][m * 16 + n];
-    const float v = scaled(sum, kHere ? here_scales[m] : a.x_scale[row0 + m], a.w_scale[out], a.bias ? a.bias[out] : 0.f);
-    const int64_t to = (row0 + m) * a.N + out;
+    const float v = scaled(sum, kHere ? here_scales[m] : a.x_scale[m], a.w_scale[out], a.bias ? a.bias[out] : 0.f);
+    const int64_t to = static_cast<int64_t>(m) * a.N + out;
     if (a.out_f32) static_cast<float*>(a.y)[to] = v;
     else static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
   }
@@ -291,7 +290,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 2)
 // X int8_t: the kernel reads weights before it waits for the launch before it, which
 // therefore has to be this call's own quantising (itself begun after all that came
 // earlier); after anything else it is launched as usual.
-template <typename X>
+template <int NT, typename X>
 cudaError_t narrow(const Args& a, bool after_own, cudaStream_t s) {
   // warps for 16 on each of 152 SMs, where the inputs allow it
   const int groups = (a.N + 15) / 16;
@@ -299,15 +298,15 @@ cudaError_t narrow(const Args& a, bool after_own, cudaStream_t s) {
   while (parts < kNarrowWarps && groups * parts < 2432 && a.K / (parts * 2) >= 256) parts *= 2;
   const int each = kNarrowWarps / parts;
   const dim3 grid((groups + each - 1) / each), block(kNarrowWarps * 32);
-  if (after_own) return launch_dependent(narrow_kernel<1, X>, grid, block, 0, s, a, parts, 0);
+  if (after_own) return launch_dependent(narrow_kernel<NT, X>, grid, block, 0, s, a, parts);
   const size_t smem = std::is_same<X, int8_t>::value
                           ? 0 : static_cast<size_t>(a.rows) * (a.K + 64);
-  narrow_kernel<1, X><<<grid, block, smem, s>>>(a, parts, 0);
+  narrow_kernel<NT, X><<<grid, block, smem, s>>>(a, parts);
   return cudaGetLastError();
 }
 
 // Whether the narrow kernel's blocks quantise x themselves: it spares a launch (1 x 4096
-// bf16 by 4096 x 4096: 7.4 us on the device where two launches take 7.7, and 7.1 of the
+// bf16 by 4096 x 4096: 7.2 us on the device where two launches take 7.7, and 7.1 of the
 // host's time where those take 8.5), but each of them reads all of it.
 bool quantize_inside(int64_t rows, int K, int x_dtype) {
   return rows * K * (x_dtype == MOE_F32 ? 4 : 2) <= 32 * 1024;
@@ -341,8 +340,13 @@ cudaError_t launch_quantize_rows_i8(int64_t rows, int K, int dtype, const void* 
                           : i8::quantize<__nv_bfloat16>(rows, K, x, codes, scales, s);
 }
 
-// Up to so many rows take the narrow kernel.
-constexpr int64_t kNarrowRows = 8;
+// Whether the narrow kernel takes it: up to 8 rows, and up to 16 where the weight is
+// small, as the integer instruction is the bound with two sets of columns (16 rows of
+// codes by 4096 x 4096: 8.3 us and 14.4 in the wide kernel, by 8192 x 4096 14.4 and 14.5;
+// 13 rows by 14337 x 7168: 41 and 27).
+static bool is_narrow(int64_t rows, int N, int K) {
+  return rows <= 8 || (rows <= 16 && static_cast<int64_t>(N) * K <= 1 << 25);
+}
 
 // x as codes or fp16 numbers, its scales, partial sums.
 struct LinearScratch {
@@ -350,9 +354,9 @@ struct LinearScratch {
 };
 static LinearScratch linear_scratch(int64_t rows, int N, int K) {
   LinearScratch L;
-  L.scales = i8::up256(static_cast<size_t>(rows) * K * (rows <= kNarrowRows ? 1 : 2));
+  L.scales = i8::up256(static_cast<size_t>(rows) * K * (is_narrow(rows, N, K) ? 1 : 2));
   L.part = L.scales + i8::up256(static_cast<size_t>(rows) * 4);
-  const int splits = rows <= kNarrowRows ? 1 : i8::wide_splits(rows, N, K);
+  const int splits = is_narrow(rows, N, K) ? 1 : i8::wide_splits(rows, N, K);
   L.total = L.part + (splits > 1 ? static_cast<size_t>(splits) * rows * N * 4 : 0);
   return L;
 }
@@ -367,7 +371,8 @@ size_t i8_linear_scratch_most(int64_t rows, int N, int K) {
     const size_t bytes = i8_linear_scratch(r < rows ? r : rows, N, K);
     most = bytes > most ? bytes : most;
   };
-  look(kNarrowRows);
+  look(8);
+  look(16);
   look(32);
   look(64);
   for (int64_t r = 128; r < rows && r <= 152 * 128; r += 128) look(r);
@@ -390,17 +395,17 @@ cudaError_t launch_linear_i8(int64_t rows, int N, int K, const void* x, int x_dt
   const bool coded = x_dtype == MOE_I8;
   if (!coded) a.x_scale = scales;
   a.x = x;
-  if (rows <= kNarrowRows) {
-    if (!coded && i8::quantize_inside(rows, K, x_dtype))
-      return x_dtype == MOE_F32 ? i8::narrow<float>(a, false, s)
-                                : i8::narrow<__nv_bfloat16>(a, false, s);
+  if (is_narrow(rows, N, K)) {
+    if (!coded && rows <= 8 && i8::quantize_inside(rows, K, x_dtype))
+      return x_dtype == MOE_F32 ? i8::narrow<1, float>(a, false, s)
+                                : i8::narrow<1, __nv_bfloat16>(a, false, s);
     if (!coded) {
       int8_t* codes = reinterpret_cast<int8_t*>(at);
       const cudaError_t st = launch_quantize_rows_i8(rows, K, x_dtype, x, codes, scales, s);
       if (st != cudaSuccess) return st;
       a.x = codes;
     }
-    return i8::narrow<int8_t>(a, !coded, s);
+    return rows <= 8 ? i8::narrow<1, int8_t>(a, !coded, s) : i8::narrow<2, int8_t>(a, !coded, s);
   }
   __half* halves = reinterpret_cast<__half*>(at);
   cudaError_t st;
