@@ -377,6 +377,14 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_tf32_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // v as two tf32 numbers: the nearest (halves away from zero, by the carry of half a
 // step), and that of the rest, whose last bits the instruction does not read.
 __device__ __forceinline__ void two_tf32(uint32_t v, uint32_t& p, uint32_t& q) {
@@ -509,9 +517,14 @@ __device__ __forceinline__ void run_units(Copies<T>& copies, int& slot, int unit
           two_tf32(load_shared(q8 + 256), wp[3], wq[3]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_tf32(acc[m][n], wp, xq[n][0], xq[n][1]);
-            mma_tf32(acc[m][n], wq, xp[n][0], xp[n][1]);
-            mma_tf32(acc[m][n], wp, xp[n][0], xp[n][1]);
+            // the instruction cuts its sums off, so that a long chain of them falls short:
+            // eight inputs at a time, added up with rounding
+            float part[4];
+            mma_tf32_first(part, wp, xq[n][0], xq[n][1]);
+            mma_tf32(part, wq, xp[n][0], xp[n][1]);
+            mma_tf32(part, wp, xp[n][0], xp[n][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][n][i] += part[i];
           }
         }
       }

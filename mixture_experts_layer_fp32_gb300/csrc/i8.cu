@@ -8,7 +8,7 @@ namespace i8 {
 namespace {
 
 // ------------------------------------------------------------------ quantising
-// A row's scale is its largest magnitude over 127, in fp32, a code the nearest whole
+// A row's scale is its largest magnitude times fp32's 1 / 127, a code the nearest whole
 // number of x over the scale, ties to even: the quotient is estimated by a product
 // with the reciprocal, and what is left of x (exact by fma: it has few bits) decides
 // whether the neighbour is nearer.  A row's values stay in registers between the
@@ -75,7 +75,7 @@ struct Coder {
   float scale, up, s, inverse;
   bool some;
   __device__ __forceinline__ explicit Coder(const Top& top) {
-    scale = top.good ? top.most / 127.f : NAN;
+    scale = top.good ? top.most * (1.f / 127.f) : NAN;
     // no reciprocal of a scale past 2^-126 is lost to overflow
     up = scale < 0x1p-100f ? 0x1p64f : 1.f;
     some = scale > 0.f;  // neither 0 nor NaN

@@ -13,8 +13,7 @@ def quantised(x):
     """Codes and scales by the definition, in 64 bits (a quotient of two fp32 numbers that is not
     half of an odd number is further from one than 64 bits lose)."""
     x = x.float()
-    # (torch multiplies fp32 by the reciprocal of a number, so the quotient is formed in 64 bits)
-    s = (x.abs().amax(-1).double() / 127).float()
+    s = x.abs().amax(-1) * torch.tensor(1 / 127, dtype=torch.float32, device=x.device)
     bad = ~torch.isfinite(x).all(-1)
     safe = torch.where((s > 0) & ~bad, s, 1.0)
     q = torch.round(x.double() / safe.double()[..., None]).clamp(-127, 127)
@@ -78,7 +77,7 @@ def test_quantise_borders_and_special_values():
     largest numbers, infinities and NaN."""
     import mixture_experts_layer_fp32_gb300 as moe
     K, rows = 256, 12
-    half = torch.arange(-127, 128, device="cuda").float() / 2     # scale 1: x / s = n / 2
+    half = torch.arange(-127, 128, device="cuda").float() / 2
     x = torch.zeros(rows, K, device="cuda")
     x[0, :255], x[0, 255] = half, 127.0
     x[1] = x[0] * 2.0 ** -100
