@@ -15,10 +15,11 @@
 //   combine: partial sums of a token's experts added in order, one rounding.
 // The barriers of all blocks are those around the top-k and the one before the combine:
 // a block's parts of the two streams are nearly the same experts', so that a slow
-// block delays its neighbours alone (a barrier and a step of its own for the hidden
-// values took XXX).
-// A block's part of both streams is one sequence of units, a unit the 4 KB of each
-// of its 8 warps: 32 (fp32: 16) inputs of 64 outputs.  A warp copies its own units
+// block delays its neighbours alone (with a barrier on either side of a step for the
+// hidden values, 32 tokens, 8 of 128 experts of 4096 x 1536, took 762 us where this takes
+// 718).
+// A block's part of both streams is one sequence of units, a unit 32 (fp32:
+// 16) inputs of a tile's 512 outputs, 64 (32) to each of its 8 (16) warps.  A warp copies its own units
 // with cp.async into a ring of its own, up to kSlots - 1 units ahead, from FC1 into FC2
 // too: the weights do not depend on the hidden values, so memory stays busy while those
 // are waited for.
@@ -34,8 +35,9 @@
 //     and y but y's own.
 //   fp32: each operand as two tf32 numbers, v = p + q with |q| <= 2^-11 |v| and q itself
 //     rounded (2^-22 of v); p p', p q' and q p' are multiplied, q q' (2^-22) is left out.
-//     Three instructions cost less than the FMAs from two rows on (7 tokens, 3 of 12 of
-//     1032 x 1416: XXX us with FMAs), and an infinity in x gives NaN.
+//     FMAs, two outputs to a lane, took longer from the first row on (7 tokens, 3 of 12 of
+//     1032 x 1416: 126 us where this took 71; 64 tokens, 2 of 8 of 1024 x 4096: 782 and
+//     168).  An infinity in x gives NaN.
 //
 // All partial sums are added in an order given by sizes alone: repeats are equal
 // bit for bit.
@@ -46,15 +48,15 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = 8;
 constexpr int kSlots = 6;                       // units of a warp's ring
-constexpr int kUnit = 4096;                     // bytes
-constexpr int kRing = kWarps * kSlots * kUnit;  // 192 KB
+constexpr int kRing = kSlots * 32 * 1024;       // of all warps: 192 KB
 constexpr int kTokens = MOE_FEW_MAX_TOKENS;
 constexpr int kPairs = kTokens * MOE_MAX_TOPK;
 constexpr int kRowsAtMost = kPairs + kTokens;
+constexpr int kGroups = kPairs / 64;
 constexpr int kChunk = 384;                     // features of the router's operands at a time
-constexpr int kColumns = 512;                   // a tile's outputs: 8 warps of 64
+constexpr int kColumns = 512;                   // a tile's outputs: all warps'
+constexpr int kMostThreads = 512;
 constexpr int kOwnTokens = 4;                   // up to so many every block chooses for itself
 // a grid barrier gives up after about a second
 constexpr long long kWaitCycles = 2000000000ll;
@@ -95,10 +97,10 @@ struct Plan {
   int16_t hit[MOE_MAX_EXPERTS];      // experts hit
   int16_t first[MOE_MAX_EXPERTS + 1];  // their first rows
   int16_t total[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS];
-  int16_t before[kWarps][MOE_MAX_EXPERTS];
+  int16_t before[kGroups][MOE_MAX_EXPERTS];  // of 64 pairs each
   uint8_t rank[kPairs];
   float logit[kOwnTokens][MOE_MAX_EXPERTS], gsel[kOwnTokens][MOE_MAX_EXPERTS];
-  float part[kThreads];
+  float part[kMostThreads];
   int on, dropped;
 };
 
@@ -180,12 +182,15 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A warp's unit: kInputs inputs of 128 bytes of outputs each.  More warps hide more of
+// what fp32 needs between the ring and the products (8 tokens, 2 experts of 2048 x 8192:
+// 100 us with 16 warps, 108 with 8); bf16 with 16 warps of 64 bytes of outputs takes
+// longer (one token, 2 of 8 of 4096 x 14336: 145 us and 130).
 template <typename T>
 struct Form;
 template <>
 struct Form<__nv_bfloat16> {
-  static constexpr int kInputs = 32;  // of a unit
-  static constexpr int kPieces = 8;   // 16-byte pieces of 64 outputs
+  static constexpr int kWarps = 8, kInputs = 32;
   // rows read together by ldmatrix differ in bits 0, 3 and 4 of the input
   __device__ static int place(int row, int piece) {
     return row * 128 + ((piece ^ (((row >> 3) & 3) * 2 + (row & 1))) << 4);
@@ -193,11 +198,22 @@ struct Form<__nv_bfloat16> {
 };
 template <>
 struct Form<float> {
-  static constexpr int kInputs = 16, kPieces = 16;
+  static constexpr int kWarps = 16, kInputs = 16;
   // rows read together differ in bits 2 and 3 of the input, eight outputs of each
   __device__ static int place(int row, int piece) {
-    return row * 256 + ((piece ^ (((row >> 2) & 3) * 2)) << 4);
+    return row * 128 + ((piece ^ (((row >> 2) & 3) * 2)) << 4);
   }
+};
+
+template <typename T>
+struct Shape : Form<T> {
+  static constexpr int kWarps = Form<T>::kWarps, kThreads = kWarps * 32;
+  static constexpr int kInputs = Form<T>::kInputs;
+  static constexpr int kStrip = 128 / sizeof(T);   // outputs of a unit
+  static constexpr int kUnit = kInputs * 128;      // bytes
+  static constexpr int kPieces = 8;                // of 16 bytes
+  static constexpr int kCopies = kUnit / 512;      // instructions
+  static_assert(kWarps * kStrip == kColumns && kWarps * kSlots * kUnit == kRing, "units");
 };
 
 // ------------------------------------------------------------------ the streams
@@ -272,7 +288,7 @@ __device__ __forceinline__ Tile tile_of(const Args& a, const Plan& plan, const S
 // A warp's copies: both streams' units in order.
 template <typename T>
 struct Copies {
-  using F = Form<T>;
+  using F = Shape<T>;
   static constexpr int kStep = 32 / F::kPieces;  // inputs of an instruction
   const Args& a;
   const Plan& plan;
@@ -283,14 +299,14 @@ struct Copies {
   int unit = 0, units = 0, inputs = 0, outputs = 0;
   bool real = false;
   const T* src = nullptr;
-  int dst[8];
+  int dst[F::kCopies];
 
   __device__ Copies(const Args& a_, const Plan& p, const Stream* s, const void* smem)
       : a(a_), plan(p), streams(s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    ring = smem_at(smem) + warp * kSlots * kUnit;
+    ring = smem_at(smem) + warp * kSlots * F::kUnit;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < F::kCopies; ++i)
       dst[i] = F::place(lane / F::kPieces + i * kStep, lane % F::kPieces);
     left = s[0].end - s[0].begin;
     next = s[0].begin;
@@ -306,11 +322,11 @@ struct Copies {
     int column;
     if (product == 0) {
       inputs = a.h, outputs = f;
-      column = t.at * 256 + (warp & 3) * 64;
-      W = shared ? (warp < 4 ? a.V1 : a.V3) : (warp < 4 ? a.W1 : a.W3);
+      column = t.at * 256 + warp % (F::kWarps / 2) * F::kStrip;
+      W = shared ? (warp < F::kWarps / 2 ? a.V1 : a.V3) : (warp < F::kWarps / 2 ? a.W1 : a.W3);
     } else {
       inputs = f, outputs = a.h;
-      column = t.at * kColumns + warp * 64;
+      column = t.at * kColumns + warp * F::kStrip;
       W = shared ? a.V2 : a.W2;
     }
     column += lane % F::kPieces * (16 / static_cast<int>(sizeof(T)));
@@ -338,9 +354,9 @@ struct Copies {
         enter(tile, u);
       }
       const int row = unit * F::kInputs + (threadIdx.x & 31) / F::kPieces;
-      const uint32_t to = ring + slot * kUnit;
+      const uint32_t to = ring + slot * F::kUnit;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < F::kCopies; ++i) {
         const bool there = real && row + i * kStep < inputs;
         copy16(to + dst[i], there ? src + static_cast<int64_t>(i) * kStep * outputs : src, there);
       }
@@ -407,7 +423,7 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   return v;
 }
 
-// Where a run's sums of a tile go: the row `n` of the tile's, an output of the warp's 64.
+// Where a run's sums of a tile go: the row `n` of the tile's, an output of the warp's.
 struct Out {
   float* at;
   int64_t stride;
@@ -420,13 +436,14 @@ template <typename T, int NT, int PIECES>
 __device__ __forceinline__ void run_units(Copies<T>& copies, int& slot, int units, const T* x,
                                           int64_t x_lo, const uint16_t* row_at, int first,
                                           int count, int width, int left, const Out& out) {
-  using F = Form<T>;
+  using F = Shape<T>;
   constexpr bool kHalf = sizeof(T) == 2;
   constexpr int kLane = F::kInputs / 4;  // inputs of a lane: 16 bytes
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float acc[4][NT][4];
+  constexpr int M = F::kStrip / 16;
+  float acc[M][NT][4];
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
+  for (int m = 0; m < M; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -442,11 +459,11 @@ __device__ __forceinline__ void run_units(Copies<T>& copies, int& slot, int unit
   // The unit's inputs are kLane to each t.  bf16: instruction s takes 8 t + 4 s .. + 3, its
   // slots 2 t, 2 t + 1 the first two and 2 t + 8, 2 t + 9 the others.  fp32: 4 t + 2 s, + 1,
   // the slots t and t + 4.
-  uint32_t from[2][4];
+  uint32_t from[2][M];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int m = 0; m < M; ++m) {
       if (kHalf) {
         const int j = lane >> 3, r = lane & 7;
         from[s][m] = F::place(8 * (r >> 1) + 2 * (j >> 1) + (r & 1) + 4 * s, m * 2 + (j & 1));
@@ -455,74 +472,85 @@ __device__ __forceinline__ void run_units(Copies<T>& copies, int& slot, int unit
       }
     }
 
-  uint4 v[PIECES][NT];
-  auto read = [&](int at) {  // inputs past the row's end are none
+  auto read = [&](uint4 (&v)[NT], int p, int at) {  // inputs past the row's end are none
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (kHalf) {
-          v[p][n] = load16(x + p * x_lo + off[n]);
-        } else {
-          v[p][n] = make_uint4(0u, 0u, 0u, 0u);
-          if (at + t * kLane < left) v[p][n] = load16(x + off[n]);
-        }
+    for (int n = 0; n < NT; ++n) {
+      if (kHalf) {
+        v[n] = load16(x + p * x_lo + at + off[n]);
+      } else {
+        v[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (at + t * kLane < left) v[n] = load16(x + at + off[n]);
       }
-    x += F::kInputs;
+    }
   };
-  constexpr bool kAhead = NT * PIECES <= 8;  // as the registers allow
-  if (kAhead) read(0);
+  constexpr bool kAhead = NT * PIECES <= 4;  // as the registers allow
+  uint4 ahead[PIECES][NT];
+  if (kAhead)
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) read(ahead[p], p, 0);
 #pragma unroll 1
   for (int u = 0; u < units; ++u) {
-    if (!kAhead) read(u * F::kInputs);
-    uint4 now[PIECES][NT];
+    uint4 now[PIECES][NT];  // without kAhead one piece after the other, in the first place
+    if (kAhead) {
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p)
+      for (int p = 0; p < PIECES; ++p)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) now[p][n] = v[p][n];
-    if (kAhead && u + 1 < units) read((u + 1) * F::kInputs);
+        for (int n = 0; n < NT; ++n) now[p][n] = ahead[p][n];
+      if (u + 1 < units)
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) read(ahead[p], p, (u + 1) * F::kInputs);
+    } else {
+      read(now[0], 0, u * F::kInputs);
+    }
     wait_copies<kSlots - 2>();
     __syncwarp();
     copies.issue();  // into the slot that was read last
-    const uint32_t at = copies.ring + slot * kUnit;
+    const uint32_t at = copies.ring + slot * F::kUnit;
     if (++slot == kSlots) slot = 0;
+    if constexpr (kHalf) {
+      uint32_t w[2][M][4];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if constexpr (kHalf) {
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          uint32_t w[4];
-          ldmatrix_x4_trans(at + from[s][m], w);
+        for (int m = 0; m < M; ++m) ldmatrix_x4_trans(at + from[s][m], w[s][m]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+      for (int p = 0; p < PIECES; ++p) {
+        if (!kAhead && p > 0) read(now[0], p, u * F::kInputs);
+        const uint4(&v)[NT] = now[kAhead ? p : 0];
 #pragma unroll
-            for (int p = 0; p < PIECES; ++p)
-              mma_bf16(acc[m][n], w, s ? now[p][n].z : now[p][n].x, s ? now[p][n].w : now[p][n].y);
-        }
-      } else {
-        uint32_t xp[NT][2], xq[NT][2];
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          two_tf32(s ? now[0][n].z : now[0][n].x, xp[n][0], xq[n][0]);
-          two_tf32(s ? now[0][n].w : now[0][n].y, xp[n][1], xq[n][1]);
-        }
+          for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+            for (int n = 0; n < NT; ++n)
+              mma_bf16(acc[m][n], w[s][m], s ? v[n].z : v[n].x, s ? v[n].w : v[n].y);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint32_t wp[M][4], wq[M][4];
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
           // outputs g and g + 8 of 16 (two pieces on), inputs of the slots t and t + 4
           const uint32_t q = at + from[s][m], q8 = at + (from[s][m] ^ 32);
-          uint32_t wp[4], wq[4];
-          two_tf32(load_shared(q), wp[0], wq[0]);
-          two_tf32(load_shared(q8), wp[1], wq[1]);
-          two_tf32(load_shared(q + 256), wp[2], wq[2]);
-          two_tf32(load_shared(q8 + 256), wp[3], wq[3]);
+          two_tf32(load_shared(q), wp[m][0], wq[m][0]);
+          two_tf32(load_shared(q8), wp[m][1], wq[m][1]);
+          two_tf32(load_shared(q + 128), wp[m][2], wq[m][2]);
+          two_tf32(load_shared(q8 + 128), wp[m][3], wq[m][3]);
+        }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n) {
+          uint32_t xp[2], xq[2];
+          two_tf32(s ? now[0][n].z : now[0][n].x, xp[0], xq[0]);
+          two_tf32(s ? now[0][n].w : now[0][n].y, xp[1], xq[1]);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
             // the instruction cuts its sums off, so that a long chain of them falls short:
             // eight inputs at a time, added up with rounding
             float part[4];
-            mma_tf32_first(part, wp, xq[n][0], xq[n][1]);
-            mma_tf32(part, wq, xp[n][0], xp[n][1]);
-            mma_tf32(part, wp, xp[n][0], xp[n][1]);
+            mma_tf32_first(part, wp[m], xq[0], xq[1]);
+            mma_tf32(part, wq[m], xp[0], xp[1]);
+            mma_tf32(part, wp[m], xp[0], xp[1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][n][i] += part[i];
           }
@@ -538,7 +566,7 @@ __device__ __forceinline__ void run_units(Copies<T>& copies, int& slot, int unit
       if (at < count) {
         float* o = out.at + at * out.stride;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < M; ++m) {
           if (m * 16 + g < out.limit) o[m * 16 + g] = acc[m][n][c];
           if (m * 16 + g + 8 < out.limit) o[m * 16 + g + 8] = acc[m][n][2 + c];
         }
@@ -561,6 +589,7 @@ template <typename T>
 __device__ void partial_logits(const Args& a, char* smem) {
   const int tiles = expert_tiles(a.E), n_slabs = slabs(gridDim.x, a.E, a.h);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = Shape<T>::kWarps;
   // more than G tiles of experts only where the grid is smaller than 8 blocks
   for (int job = blockIdx.x; job < tiles * n_slabs; job += gridDim.x) {
     const int e0 = job % tiles * 32, slab = job / tiles;
@@ -580,17 +609,17 @@ __device__ void partial_logits(const Args& a, char* smem) {
       const int rows = min(kChunk, end - r0);
       __syncthreads();
       if (ne == 32 && a.E % 4 == 0) {
-        for (int i = threadIdx.x; i < rows * 8; i += kThreads)
+        for (int i = threadIdx.x; i < rows * 8; i += blockDim.x)
           copy16(smem_at(ws + i * 4),
                  a.Wg + static_cast<int64_t>(r0 + i / 8) * a.E + e0 + i % 8 * 4, true);
       } else {
-        for (int i = threadIdx.x; i < rows * 32; i += kThreads)
+        for (int i = threadIdx.x; i < rows * 32; i += blockDim.x)
           if (i % 32 < ne)
             copy4(smem_at(ws + i), a.Wg + static_cast<int64_t>(r0 + i / 32) * a.E + e0 + i % 32);
       }
       commit();
       constexpr int V = 16 / sizeof(T);
-      for (int i = threadIdx.x; i < rows / V * a.T; i += kThreads) {
+      for (int i = threadIdx.x; i < rows / V * a.T; i += blockDim.x) {
         const int t = i % a.T, r = i / a.T * V;
         const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) +
                                                              static_cast<int64_t>(t) * a.h + r0 + r));
@@ -620,7 +649,7 @@ __device__ void partial_logits(const Args& a, char* smem) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) red[(split * Tp + tg * 16 + i) * width + le] = acc[i];
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * ne; i += kThreads) {
+    for (int i = threadIdx.x; i < a.T * ne; i += blockDim.x) {
       const int t = i / ne, e = i % ne;
       float sum = 0.f;
       for (int s = 0; s < splits; ++s) sum += red[(s * Tp + t) * width + e];
@@ -663,7 +692,7 @@ __device__ void choose_experts(const Args& a, Plan& plan, bool own) {
   const int n_slabs = slabs(gridDim.x, a.E, a.h);
   int width = 8;
   while (width < a.E) width *= 2;
-  const int parts = kThreads / width, e = threadIdx.x % width, part = threadIdx.x / width;
+  const int parts = blockDim.x / width, e = threadIdx.x % width, part = threadIdx.x / width;
   const int warp = threadIdx.x >> 5;
   const int first = own ? 0 : blockIdx.x, step = own ? a.T : gridDim.x, each = own ? a.T : 1;
   for (int t0 = first; t0 < a.T; t0 += step) {
@@ -697,11 +726,10 @@ __device__ void choose_experts(const Args& a, Plan& plan, bool own) {
 // Rows by expert: pairs counted and ranked in their order, 64 of them to a warp.
 __device__ void order_pairs(const Args& a, Plan& plan) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < kWarps * MOE_MAX_EXPERTS; i += kThreads)
+  for (int i = threadIdx.x; i < kGroups * MOE_MAX_EXPERTS; i += blockDim.x)
     plan.before[i / MOE_MAX_EXPERTS][i % MOE_MAX_EXPERTS] = 0;
   __syncthreads();
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
+  for (int r = 0; warp < kGroups && r < 2; ++r) {
     const int i = warp * 64 + r * 32 + lane;
     const int e = i < plan.pairs ? plan.expert[i] : -1;
     const uint32_t same = __match_any_sync(~0u, e);
@@ -717,7 +745,7 @@ __device__ void order_pairs(const Args& a, Plan& plan) {
   if (threadIdx.x < MOE_MAX_EXPERTS) {
     int sum = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kGroups; ++w) {
       const int n = plan.before[w][threadIdx.x];
       plan.before[w][threadIdx.x] = static_cast<int16_t>(sum);
       sum += n;
@@ -830,7 +858,7 @@ __device__ void make_plan(const Args& a, Plan& plan, bool own) {
   const int pairs = a.T * a.k;
   if (threadIdx.x == 0) plan.pairs = pairs, plan.dropped = 0;
   if (!own)
-    for (int i = threadIdx.x; i < pairs; i += kThreads) {
+    for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
       plan.expert[i] = static_cast<int16_t>(__ldcg(a.idx + i));
       plan.prob[i] = __ldcg(a.prob + i);
     }
@@ -842,25 +870,19 @@ __device__ void make_plan(const Args& a, Plan& plan, bool own) {
   }
   // A token without k experts to choose (NaN logits, reported) names one twice; the
   // first of them stands, so that no expert has more rows than there are tokens.
-  bool twice[2] = {false, false};
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int i = threadIdx.x + r * kThreads;
-    if (i < pairs)
-      for (int q = i - i % a.k; q < i; ++q) twice[r] |= plan.expert[q] == plan.expert[i];
-  }
+  uint32_t marked = 0;  // of this thread's pairs, two at most
+  for (int i = threadIdx.x, r = 0; i < pairs; i += blockDim.x, ++r)
+    for (int q = i - i % a.k; q < i; ++q)
+      if (plan.expert[q] == plan.expert[i]) marked |= 1u << r;
   __syncthreads();
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-    if (twice[r]) plan.expert[threadIdx.x + r * kThreads] = -1;
+  for (int i = threadIdx.x, r = 0; i < pairs; i += blockDim.x, ++r)
+    if (marked >> r & 1) plan.expert[i] = -1;
   __syncthreads();
   order_pairs(a, plan);
   if (a.capacity >= 0) {
-    bool drop[2] = {false, false};
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = threadIdx.x + r * kThreads;
-      const int e = i < pairs ? plan.expert[i] : -1;
+    marked = 0;
+    for (int i = threadIdx.x, r = 0; i < pairs; i += blockDim.x, ++r) {
+      const int e = plan.expert[i];
       if (e < 0 || plan.total[e] <= a.capacity) continue;
       int place = plan.before[i / 64][e] + plan.rank[i];
       if (a.policy == MOE_DROP_PROBS) {
@@ -872,13 +894,11 @@ __device__ void make_plan(const Args& a, Plan& plan, bool own) {
           place += plan.expert[q] == e && (o > p || (o == p && q < i));
         }
       }
-      drop[r] = place >= a.capacity;
+      if (place >= a.capacity) marked |= 1u << r;
     }
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (drop[r]) {
-        const int i = threadIdx.x + r * kThreads;
+    for (int i = threadIdx.x, r = 0; i < pairs; i += blockDim.x, ++r)
+      if (marked >> r & 1) {
         plan.expert[i] = -1;
         plan.dropped = 1;
         if (blockIdx.x == 0 && a.prob_out) a.prob_out[i] = 0.f;
@@ -886,7 +906,7 @@ __device__ void make_plan(const Args& a, Plan& plan, bool own) {
     __syncthreads();
     if (plan.dropped) order_pairs(a, plan);
   }
-  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
     const int e = plan.expert[i];
     int row = -1;
     if (e >= 0) {
@@ -895,13 +915,13 @@ __device__ void make_plan(const Args& a, Plan& plan, bool own) {
     }
     plan.row_of[i] = static_cast<int16_t>(row);
   }
-  for (int t = threadIdx.x; t < a.T; t += kThreads)
+  for (int t = threadIdx.x; t < a.T; t += blockDim.x)
     plan.token[plan.rows + t] = static_cast<uint16_t>(t);
-  for (int i = threadIdx.x; i < plan.hits; i += kThreads)
+  for (int i = threadIdx.x; i < plan.hits; i += blockDim.x)
     for (int r = plan.first[i]; r < plan.first[i + 1]; ++r)
       plan.hit_of_row[r] = static_cast<int16_t>(i);
   if (blockIdx.x == 0 && a.tpe_out)
-    for (int e = threadIdx.x; e < a.E; e += kThreads) a.tpe_out[e] = plan.total[e];
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.tpe_out[e] = plan.total[e];
   __syncthreads();
 }
 
@@ -944,7 +964,7 @@ template <typename T>
 __device__ void hidden_tile(const Args& a, const Plan& plan, const Tile& t, int first, int last) {
   const bool shared = t.hit == plan.hits;
   const int f = shared ? a.fs : a.f;
-  for (int i = threadIdx.x; i < t.rows * 64; i += kThreads) {
+  for (int i = threadIdx.x; i < t.rows * 64; i += blockDim.x) {
     const int n = i / 64, in = i % 64 * 4, column = t.at * 256 + in;
     if (column >= f) continue;
     const int row = t.first + n;
@@ -1000,6 +1020,7 @@ __device__ void tile_done(const Args& a, Plan& plan, const Stream& s, int tile, 
 template <typename T>
 __device__ bool stream_product(const Args& a, Plan& plan, const Stream* streams, int product,
                                Copies<T>& copies, int& slot) {
+  using F = Shape<T>;
   const Stream& s = streams[product];
   const int warp = threadIdx.x >> 5;
   int ready = -1;
@@ -1015,18 +1036,19 @@ __device__ bool stream_product(const Args& a, Plan& plan, const Stream* streams,
       ready = t.hit;
     }
     const int outputs = product ? a.h : f, inputs = product ? f : a.h;
-    const int column = product ? t.at * kColumns + warp * 64 : t.at * 256 + (warp & 3) * 64;
+    const int column = product ? t.at * kColumns + warp * F::kStrip
+                               : t.at * 256 + warp % (F::kWarps / 2) * F::kStrip;
     Out out;
     out.limit = outputs - column;
     if (unit == 0) {
       out.at = main_row(a, plan, product, t.first, shared) + column +
-               (product == 0 && warp >= 4 ? f : 0);
+               (product == 0 && warp >= F::kWarps / 2 ? f : 0);
       out.stride = product ? a.h : 2 * f;
     } else {
-      out.at = a.extra[product] + static_cast<int64_t>(blockIdx.x) * a.T * kColumns + warp * 64;
+      out.at = a.extra[product] + static_cast<int64_t>(blockIdx.x) * a.T * kColumns + warp * F::kStrip;
       out.stride = kColumns;
     }
-    const int k0 = unit * Form<T>::kInputs;
+    const int k0 = unit * F::kInputs;
     // FC1 reads the rows' tokens, FC2 the hidden values in the rows' order
     const uint16_t* row_at = product ? nullptr : plan.token;
     const T* x = product ? static_cast<const T*>(a.hid) + hid_row(a, plan, t.first, shared)
@@ -1062,8 +1084,8 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 template <typename T>
 __device__ void combine(const Args& a, const Plan& plan, const Stream& s) {
   const int per = a.h / 4;
-  for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < static_cast<int64_t>(a.T) * per;
-       i += gridDim.x * kThreads) {
+  for (int64_t i = blockIdx.x * blockDim.x + threadIdx.x; i < static_cast<int64_t>(a.T) * per;
+       i += gridDim.x * blockDim.x) {
     const int t = static_cast<int>(i / per);
     const int column = static_cast<int>(i - static_cast<int64_t>(t) * per) * 4;
     const int at = column / kColumns;
@@ -1092,12 +1114,12 @@ __device__ void combine(const Args& a, const Plan& plan, const Stream& s) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(Shape<T>::kThreads, 1) few_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) char smem[];
   Plan& plan = *reinterpret_cast<Plan*>(smem + kRing);
   __shared__ Stream streams[2];
   // nobody counts in these before the barrier after the logits
-  for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.counters; i += gridDim.x * kThreads)
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.counters; i += gridDim.x * blockDim.x)
     a.tiles[i] = 0;
   partial_logits<T>(a, smem);
   bool on = grid_barrier(a, plan, 1);
@@ -1109,7 +1131,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   if (on) {
     make_plan(a, plan, own);
     if (threadIdx.x < 2) {
-      constexpr int U = Form<T>::kInputs;
+      constexpr int U = Shape<T>::kInputs;
       auto up = [](int n, int d) { return (n + d - 1) / d; };
       if (threadIdx.x == 0)
         streams[0].set(plan.hits, up(a.f, 256), up(a.h, U), up(a.fs, 256), up(a.h, U));
@@ -1171,7 +1193,7 @@ cudaError_t launch(Args& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   const int sms = device_sm_count();
   cfg.gridDim = dim3(sms < kFewBlocks ? sms : kFewBlocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Shape<T>::kThreads);
   cfg.dynamicSmemBytes = kRing + sizeof(Plan);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
