@@ -5,8 +5,9 @@
 train_step runs it forward and backward: the norm, the layer's stages, the
 dropout with the residual sum, and back through all of them, with the dropout's
 mask drawn again from its seed and offset instead of stored.  decode_step runs
-it for a few tokens with the experts in 4 bits, then the next norm (which adds
-the residual as it reads it) and a head in 4 bits.
+it for a few tokens, with the experts in 4 bits or as they are (one launch for the
+whole layer), then the next norm (which adds the residual as it reads it) and a
+head in 4 or 8 bits; next_tokens draws from its logits.
 
     python -m examples.sublayer      (from the root of the repository)
 """
@@ -46,7 +47,9 @@ def train_step(cfg, h, d_out, weights, norm, p, rng, saved, grads, ws, norm_ws):
 
 
 class Decoder:
-    """Buffers and 4-bit weights of decode_step for cfg's number of tokens."""
+    """Buffers and weights of decode_step for cfg's number of tokens.  experts:
+    moe.W4Experts, or the layer's own (W1, W3, W2) (up to moe.FEW_MAX_TOKENS tokens);
+    head: moe.W4Weight or moe.I8Weight."""
 
     def __init__(self, cfg, Wg, experts, norms, head):
         self.cfg, self.Wg, self.experts, self.norms, self.head = cfg, Wg, experts, norms, head
@@ -56,19 +59,35 @@ class Decoder:
         self.logits = torch.empty((T, head.n), device="cuda")
         self.idx = torch.empty((T, k), dtype=torch.int32, device="cuda")
         self.prob = torch.empty((T, k), device="cuda")
-        self.ws = moe.alloc_workspace_w4(cfg)
-        self.head_ws = moe.alloc_workspace_linear_w4(T, head)
+        self.tokens = torch.empty(T, dtype=torch.int32, device="cuda")
+        self.in_4_bits = isinstance(experts, moe.W4Experts)
+        self.ws = (moe.alloc_workspace_w4 if self.in_4_bits else moe.alloc_workspace_few)(cfg)
+        self.head_in_4_bits = isinstance(head, moe.W4Weight)
+        self.head_ws = (moe.alloc_workspace_linear_w4 if self.head_in_4_bits
+                        else moe.alloc_workspace_linear_i8)(T, head)
 
     def decode_step(self, h):
         """h [T,h] bf16 -> logits [T, vocabulary] fp32; no allocation, so a step
         can be captured into a graph."""
         moe.layer_norm(h, self.norms[0], None, EPS, self.n, rms=True)
-        moe.forward_w4(self.cfg, self.n, self.Wg, None, None, self.experts, self.m, self.ws,
-                       topk_idx=self.idx, topk_prob=self.prob)
+        if self.in_4_bits:
+            moe.forward_w4(self.cfg, self.n, self.Wg, None, None, self.experts, self.m, self.ws,
+                           topk_idx=self.idx, topk_prob=self.prob)
+        else:
+            moe.forward_few(self.cfg, self.n, self.Wg, None, None, *self.experts, self.m, self.ws,
+                            topk_idx=self.idx, topk_prob=self.prob)
         moe.layer_norm(self.m, self.norms[1], None, EPS, self.n2, rms=True, residual=h,
                        z=self.out)
-        moe.linear_w4(self.n2, self.head, self.logits, self.head_ws)
+        if self.head_in_4_bits:
+            moe.linear_w4(self.n2, self.head, self.logits, self.head_ws)
+        else:
+            moe.linear_i8(self.n2, self.head, self.logits, self.head_ws)
         return self.logits
+
+    def next_tokens(self, u, **choices):
+        """The step's next tokens from random numbers u [T]; choices as in moe.sample."""
+        moe.sample(self.logits, u, self.tokens, **choices)
+        return self.tokens
 
 
 def main():
@@ -102,6 +121,14 @@ def main():
     logits = decoder.decode_step(h[:4].contiguous())
     moe.check(decoder.ws)
     print("decoding: next tokens", logits.argmax(-1).tolist())
+
+    decoder = Decoder(few, Wg, (W1, W3, W2), (norm[0], norm[0]),
+                      moe.quantize_i8(normal(vocabulary, hidden)))
+    decoder.decode_step(h[:4].contiguous())
+    tokens = decoder.next_tokens(torch.rand(4, device="cuda"), temperature=0.8, top_k=50,
+                                 top_p=0.95)
+    moe.check(decoder.ws)
+    print("decoding: drawn tokens", tokens.tolist())
 
 
 if __name__ == "__main__":

@@ -362,9 +362,9 @@ static LinearScratch linear_scratch(int64_t rows, int N, int K) {
 }
 size_t i8_linear_scratch(int64_t rows, int N, int K) { return linear_scratch(rows, N, K).total; }
 
-// What any call of up to so many rows needs: the most rows of each number of parts are
-// among those that fill 32, 64 or multiples of 128 columns, and past 152 chunks of 128
-// nothing is cut.
+// What any call of up to so many rows needs: rows of as many columns (32, 64, or chunks of
+// 128) are cut into as many parts, so the most of each are looked at; with 152 items or
+// more, and so from 152 chunks on, nothing is cut.
 size_t i8_linear_scratch_most(int64_t rows, int N, int K) {
   size_t most = i8_linear_scratch(rows, N, K);
   auto look = [&](int64_t r) {

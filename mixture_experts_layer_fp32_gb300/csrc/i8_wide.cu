@@ -461,7 +461,7 @@ int wide_splits(int64_t rows, int N, int K) {
   const int blocks = (K + 127) / 128;
   int best = 1;
   int64_t least = 0;
-  for (int s = 1; s <= 16 && s <= blocks; ++s) {
+  for (int s = 1; s == 1 || (s <= 16 && s <= blocks && items < kSMs); ++s) {
     const int64_t cost = (items * s + kSMs - 1) / kSMs * ((blocks + s - 1) / s + 3) + (s > 1 ? 3 : 0);
     if (s == 1 || cost < least) best = s, least = cost;
   }

@@ -80,3 +80,201 @@ def test_bf16(kw):
 def test_f32(kw):
     c = LayerCase(dtype="f32", **kw).cuda()
     verify(c, call(c))
+
+
+def same(a, b):
+    return all(torch.equal(u, v) for u, v in zip(a[:4], b[:4]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_repeats_and_a_workspace_of_more_tokens(dtype):
+    """Equal bits again and again, in a workspace of 64 tokens that other calls used before."""
+    import mixture_experts_layer_fp32_gb300 as moe
+    kw = dict(h=512, E=16, k=4, f=640, fs=128, dtype=dtype)
+    most = moe.config(T=64, h=512, E=16, k=4, f=640, dtype=dtype)
+    ws = moe.alloc_workspace_few(most, 128)
+    for T in (64, 1, 33, 4, 5, 9, 64, 2):
+        c = LayerCase(T=T, seed=T, **kw).cuda()
+        first = call(c)
+        verify(c, first)
+        for _ in range(3):
+            assert same(first, call(c, ws=ws))
+
+
+def test_a_token_alone_is_the_token_in_a_batch():
+    """Its row does not depend on the others in value, but for how sums are cut: within the bounds
+    of both."""
+    c = LayerCase(T=12, h=512, E=8, k=2, f=384).cuda()
+    y = call(c)[0]
+    for t in (0, 5, 11):
+        one = LayerCase(T=1, h=512, E=8, k=2, f=384).cuda()
+        for n in ("Wg", "gb", "W1", "W3", "W2"):
+            setattr(one, n, getattr(c, n))
+        one.x = c.x[t:t + 1].clone()
+        out = call(one)
+        verify(one, out)
+        ref, bound = one.reference()[3:]
+        assert bool(((out[0].double() - y[t:t + 1].double()).abs() <=
+                     2 * (bound + 2.0 ** -8 * (ref.abs() + bound))).all())
+
+
+def test_output_in_place_of_the_input_and_nothing_optional():
+    import mixture_experts_layer_fp32_gb300 as moe
+    c = LayerCase(T=9, h=512, E=8, k=2, f=384, fs=256).cuda()
+    want = call(c)[0]
+    x = c.x.clone()
+    cfg = moe.config(T=9, h=512, E=8, k=2, f=384)
+    ws = moe.alloc_workspace_few(cfg, 256)
+    moe.forward_few(cfg, x, c.Wg, c.gb, None, c.W1, c.W3, c.W2, x, ws, shared=c.shared)
+    moe.check(ws)
+    assert torch.equal(x, want)
+
+
+def test_no_tokens():
+    import mixture_experts_layer_fp32_gb300 as moe
+    cfg = moe.config(T=0, h=256, E=4, k=2, f=128)
+    c = LayerCase(T=1, h=256, E=4, k=2, f=128).cuda()
+    none = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    tpe = torch.full((4,), 7, dtype=torch.int32, device="cuda")
+    ws = moe.alloc_workspace_few(cfg)
+    moe.forward_few(cfg, none, c.Wg, None, None, c.W1, c.W3, c.W2, none, ws,
+                    tokens_per_expert=tpe)
+    moe.check(ws)
+    assert tpe.tolist() == [0] * 4
+
+
+def test_only_the_hit_experts_weights_count():
+    """What is not read cannot matter: experts that nobody chose hold NaN, and so do the shared
+    weights' neighbours."""
+    c = LayerCase(T=3, h=256, E=32, k=2, f=256, fs=128).cuda()
+    first = call(c)
+    hit = set(first[1].flatten().tolist())
+    for e in range(32):
+        if e not in hit:
+            for w in (c.W1, c.W3, c.W2):
+                w[e] = float("nan")
+    assert same(first, call(c))
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_rows_that_are_not_numbers_stay_alone(T):
+    """A token with an infinity or a NaN spoils its own row; NaN logits are reported and named."""
+    import mixture_experts_layer_fp32_gb300 as moe
+    for dtype in ("bf16", "f32"):
+        c = LayerCase(T=T, h=256, E=4, k=2, f=256, fs=128, dtype=dtype).cuda()
+        clean = call(c)[0]
+        x = c.x.clone()
+        x[1, 5], x[2, 9] = float("nan"), float("inf")
+        cfg = moe.config(T=T, h=256, E=4, k=2, f=256, dtype=dtype)
+        ws = moe.alloc_workspace_few(cfg, 128)
+        y = torch.zeros_like(x)
+        idx = torch.empty((T, 2), dtype=torch.int32, device="cuda")
+        for _ in range(2):
+            moe.forward_few(cfg, x, c.Wg, c.gb, None, c.W1, c.W3, c.W2, y, ws, topk_idx=idx,
+                            shared=c.shared)
+            with pytest.raises(moe.MoeError) as err:
+                moe.check(ws)
+            assert err.value.code == 5
+        assert bool(((idx >= 0) & (idx < 4)).all())
+        rest = [t for t in range(T) if t not in (1, 2)]
+        assert bool(torch.isfinite(y[rest]).all())
+        assert float((y[rest].double() - clean[rest].double()).abs().max()) <= 2.0 ** -6 * float(
+            clean.double().abs().max())
+        assert bool(torch.isnan(y[1]).all())
+        assert same(call(c), (clean,))
+
+
+@pytest.mark.parametrize("kw", [dict(T=1, h=512, E=8, k=2, f=384),
+                                dict(T=30, h=256, E=64, k=8, f=128, fs=128)], ids=str)
+def test_replays_in_graphs_that_share_a_workspace(kw):
+    import mixture_experts_layer_fp32_gb300 as moe
+    c = LayerCase(**kw).cuda()
+    cfg = moe.config(T=c.T, h=c.h, E=c.E, k=c.k, f=c.f)
+    ws = moe.alloc_workspace_few(cfg, c.fs)
+    ys = [torch.empty_like(c.x) for _ in range(2)]
+    xs = [c.x.clone(), c.x.flip(0).contiguous()]
+
+    def run(i):
+        moe.forward_few(cfg, xs[i], c.Wg, c.gb, None, c.W1, c.W3, c.W2, ys[i], ws,
+                        shared=c.shared)
+
+    run(0)
+    torch.cuda.synchronize()
+    graphs = []
+    stream = torch.cuda.Stream()
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            run(i)
+        graphs.append(g)
+    want = call(c)[0]
+    for _ in range(3):
+        for i in range(2):
+            ys[i].fill_(float("nan"))
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        moe.check(ws)
+        assert torch.equal(ys[0], want)
+    c.x = xs[1]
+    assert torch.equal(ys[1], call(c)[0])
+
+
+def test_two_streams_at_once():
+    """Two calls in flight, each with a workspace of its own, beside other work."""
+    import mixture_experts_layer_fp32_gb300 as moe
+    cases = [LayerCase(T=T, h=1024, E=16, k=4, f=1024, seed=T).cuda() for T in (4, 20)]
+    want = [call(c)[0] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    cfgs = [moe.config(T=c.T, h=c.h, E=c.E, k=c.k, f=c.f) for c in cases]
+    wss = [moe.alloc_workspace_few(cfg) for cfg in cfgs]
+    ys = [torch.empty_like(c.x) for c in cases]
+    a = torch.randn(2048, 2048, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, cfg, ws, y, s in zip(cases, cfgs, wss, ys, streams):
+            with torch.cuda.stream(s):
+                moe.forward_few(cfg, c.x, c.Wg, c.gb, None, c.W1, c.W3, c.W2, y, ws)
+        a = a @ a * 1e-3
+    torch.cuda.synchronize()
+    for y, w, ws in zip(ys, want, wss):
+        moe.check(ws)
+        assert torch.equal(y, w)
+
+
+def test_a_workspace_that_other_entry_points_used():
+    import mixture_experts_layer_fp32_gb300 as moe
+    c = LayerCase(T=16, h=256, E=8, k=2, f=256).cuda()
+    want = call(c)[0]
+    cfg = moe.config(T=16, h=256, E=8, k=2, f=256)
+    ws = torch.zeros(max(moe.workspace_size(cfg), moe.workspace_size_few(cfg)), dtype=torch.uint8,
+                     device="cuda")
+    y = torch.empty_like(c.x)
+    for _ in range(3):
+        moe.forward(cfg, c.x, c.Wg, c.gb, None, c.W1, c.W3, c.W2, y, ws)
+        full = y.clone()
+        moe.forward_few(cfg, c.x, c.Wg, c.gb, None, c.W1, c.W3, c.W2, y, ws)
+        moe.check(ws)
+        assert torch.equal(y, want)
+        # the layer rounds its hidden values to bf16 in between: 2e-2 of the output's RMS
+        rms = float(want.double().square().mean().sqrt())
+        assert float((full.double() - want.double()).abs().max()) <= 2e-2 * rms + \
+            2.0 ** -7 * float(want.double().abs().max())
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """Counters of the workspace that say the blocks have not come: every block gives up after a
+    second, and the next call is well."""
+    import mixture_experts_layer_fp32_gb300 as moe
+    c = LayerCase(T=5, h=256, E=4, k=2, f=128).cuda()
+    cfg = moe.config(T=5, h=256, E=4, k=2, f=128)
+    want = call(c)[0]
+    ws = moe.alloc_workspace_few(cfg)
+    ws[128:132].view(torch.int32).fill_(-1000000)
+    y = torch.empty_like(c.x)
+    moe.forward_few(cfg, c.x, c.Wg, c.gb, None, c.W1, c.W3, c.W2, y, ws)
+    with pytest.raises(moe.MoeError) as err:
+        moe.check(ws)
+    assert err.value.code == 6
+    moe.forward_few(cfg, c.x, c.Wg, c.gb, None, c.W1, c.W3, c.W2, y, ws)
+    moe.check(ws)
+    assert torch.equal(y, want)

@@ -190,3 +190,70 @@ def test_weights_just_quantised_are_read():
             got = y.clone()
             wq, wsc = quantised(W[i % 4])
             assert torch.equal(got, product(xq, xs, wq, wsc, torch.float32))
+
+
+@pytest.mark.parametrize("M,N,K", [(260, 4400, 272), (1000, 700, 2000), (70, 9000, 144),
+                                   (2000, 129, 400), (640, 2049, 1040)])
+def test_several_rounds_of_items(M, N, K):
+    xq, wq, xs, ws = codes((M, K), M + K), codes((N, K), N), scales(M, M), scales(N, N)
+    y = linear(xq, wq, ws, torch.float32, x_scale=xs)
+    assert torch.equal(y, product(xq, xs, wq, ws, torch.float32))
+
+
+@pytest.mark.parametrize("M,K", [(1, 1024), (8, 4096), (12, 512), (50, 2048), (200, 1024)])
+def test_replays_in_graphs_that_share_a_workspace(M, K):
+    import mixture_experts_layer_fp32_gb300 as moe
+    N = 1100
+    w = moe.I8Weight(codes((N, K), N), scales(N, N))
+    g = torch.Generator(device="cuda").manual_seed(M)
+    xs = [torch.randn(M, K, device="cuda", generator=g) for _ in range(2)]
+    ys = [torch.empty(M, N, device="cuda") for _ in range(2)]
+    ws = moe.alloc_workspace_linear_i8(M, w)
+    moe.linear_i8(xs[0], w, ys[0], ws)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    graphs = []
+    for x, y in zip(xs, ys):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            moe.linear_i8(x, w, y, ws)
+    for seed in range(3):
+        for i in range(2):
+            xs[i].copy_(torch.randn(M, K, device="cuda", generator=g))
+            ys[i].fill_(float("nan"))
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        moe.check(ws)
+        for x, y in zip(xs, ys):
+            xq, sc = quantised(x)
+            assert torch.equal(y, product(xq, sc, w.codes, w.scales, torch.float32))
+
+
+def test_two_streams_at_once():
+    import mixture_experts_layer_fp32_gb300 as moe
+    N, K = 2000, 2048
+    w = moe.I8Weight(codes((N, K), N), scales(N, N))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    xs = [torch.randn(M, K, device="cuda", generator=g) for M in (3, 40, 300)]
+    ys = [torch.empty(x.shape[0], N, device="cuda") for x in xs]
+    room = [moe.alloc_workspace_linear_i8(x.shape[0], w) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, y, ws, s in zip(xs, ys, room, streams):
+            with torch.cuda.stream(s):
+                moe.linear_i8(x, w, y, ws)
+    torch.cuda.synchronize()
+    for x, y in zip(xs, ys):
+        xq, sc = quantised(x)
+        assert torch.equal(y, product(xq, sc, w.codes, w.scales, torch.float32))
+
+
+def test_last_dimension_and_leading_ones():
+    import mixture_experts_layer_fp32_gb300 as moe
+    w = moe.I8Weight(codes((96, 128), 1), scales(96, 1))
+    x = torch.randn(2, 3, 5, 128, device="cuda").to(torch.bfloat16)
+    y = torch.empty(2, 3, 5, 96, device="cuda")
+    moe.linear_i8(x, w, y, moe.alloc_workspace_linear_i8(30, w))
+    xq, xs = quantised(x.view(30, 128))
+    assert torch.equal(y.view(30, 96), product(xq, xs, w.codes, w.scales, torch.float32))

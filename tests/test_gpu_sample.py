@@ -199,3 +199,37 @@ def test_replays_in_a_graph_on_another_stream():
         torch.cuda.synchronize()
         want, _ = run(l2, u2, top_k=50, top_p=0.9)
         assert np.array_equal(tokens.cpu().numpy(), want)
+
+
+def test_many_rows():
+    """More rows than a grid has in one direction."""
+    rows, V = 70001, 3
+    logits, u = draw(rows, V, 9)
+    got, _ = run(logits, u, top_k=2)
+    l = logits.double()
+    order = l.sort(dim=1, descending=True, stable=True)
+    w = torch.exp(l - order[0][:, :1])
+    w = torch.where(torch.zeros_like(w).scatter_(1, order[1][:, :2], 1.0) > 0, w, 0.0)
+    cum = w.cumsum(1)
+    at = u.double()[:, None] * cum[:, -1:]
+    want = (cum <= at).sum(1)
+    close = ((cum - at).abs() < 1e-5 * cum[:, -1:]).any(1)
+    assert bool(((torch.from_numpy(got).cuda() == want) | close).all())
+    assert float(close.double().mean()) < 0.01
+
+
+def test_streams_at_once():
+    import mixture_experts_layer_fp32_gb300 as moe
+    sets = [draw(r, V, V) for r, V in ((1, 100000), (30, 4000), (64, 20000))]
+    kw = dict(top_k=100, top_p=0.9, temperature=0.8)
+    want = [run(l, u, **kw)[0] for l, u in sets]
+    out = [torch.empty(l.shape[0], dtype=torch.int32, device="cuda") for l, _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (l, u), o, s in zip(sets, out, streams):
+            with torch.cuda.stream(s):
+                moe.sample(l, u, o, **kw)
+    torch.cuda.synchronize()
+    for o, w in zip(out, want):
+        assert np.array_equal(o.cpu().numpy(), w)
