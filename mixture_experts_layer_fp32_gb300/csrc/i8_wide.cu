@@ -15,9 +15,17 @@
 //   8 convert: an output of a tile to a thread, 128 inputs at a time;
 //   one copies W (TMA), one x (TMA), a thread of one more each multiplies a tile.
 // The two tiles' sums are read out 4 blocks of 128 inputs apart, and three places for
-// sums serve the two: a tile goes on in the spare one while its last is read (8192 x
-// 14336 x 4096, with one warp for all products: 837 us with two places, 805 with three,
-// and 712 with a warp for each tile's products, which are issued as fast as they run).
+// sums serve the two: a tile goes on in the spare one while its last is read.  8192 x
+// 14336 x 4096 (codes, bf16 results), step by step: 837 us with two places and a warp for
+// all products, 805 with three places, 712 with a warp for each tile's products (one
+// could not issue them as fast as they run), 653 with an epilogue without branches between
+// the rows (a tile's first sums wait for the eight warps that store the last item's).
+//
+// What bounds it: shared memory (x is read for each tile: 160 KB for 256 x 128 x 128
+// products, 1250 cycles where these take 1024) beside the reading of sums; with sums read
+// once an item, or codes not converted, the 712 were 623 and 670.  Few rows: memory (64 x
+// 151936 x 4096: 110 us, 5.9 TB/s).  Tried and left: pairs of blocks that share a product
+// (256 outputs a tile, half of x in each): 1280 us, whatever the number of slots.
 #include <type_traits>
 
 #include "i8.cuh"
@@ -111,7 +119,11 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
   return q;
 }
 
-template <int NC>
+__device__ __forceinline__ void store(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Out: what is stored, the type of y or whole numbers (parts of a sum)
+template <int NC, typename Out>
 __global__ void __launch_bounds__(kWarpsWide * 32, 1)
     wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ Args a, const __grid_constant__ Items items) {
@@ -204,29 +216,34 @@ __global__ void __launch_bounds__(kWarpsWide * 32, 1)
           places.next(d);
         }
       if (!on) break;
+      // No branch stands between one row and the next, so that loads and stores run on; the
+      // next item's first sums are ready for reading 4 blocks of inputs from now.
       const int row0 = it.chunk * NC + e * half;
       const int rows = min(half, a.rows - row0);
+      float row_scale[(half + 31) / 32];  // of the rows lane, lane + 32
+#pragma unroll
+      for (int i = 0; i < (half + 31) / 32; ++i) {
+        const int c = i * 32 + lane;
+        row_scale[i] = c < rows ? a.x_scale[row0 + c] : 0.f;
+      }
+      const int64_t first = static_cast<int64_t>(row0) * a.N;
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
-        const int o = it.tile * 256 + d * 128 + r;
-        if (o >= a.N) continue;
-        if (items.splits > 1) {
-          int32_t* to = a.part + (static_cast<int64_t>(it.part) * a.rows + row0) * a.N + o;
+        const int o = it.tile * 256 + d * 128 + r, at = min(o, a.N - 1);
+        const float scale = a.w_scale[at], bias = a.bias ? a.bias[at] : 0.f;
+        const int there = o < a.N ? rows : 0;
+        Out* p = (std::is_same<Out, int32_t>::value
+                      ? reinterpret_cast<Out*>(a.part) + static_cast<int64_t>(it.part) * a.rows * a.N
+                      : static_cast<Out*>(a.y)) + first + o;
 #pragma unroll
-          for (int c = 0; c < half; ++c) {
-            if (c >= rows) break;
-            to[static_cast<int64_t>(c) * a.N] = acc[d][c];
+        for (int c = 0; c < half; ++c, p += a.N) {
+          if constexpr (std::is_same<Out, int32_t>::value) {
+            if (c < there) *p = acc[d][c];
+          } else {
+            const float v =
+                scaled(acc[d][c], __shfl_sync(~0u, row_scale[c / 32], c % 32), scale, bias);
+            if (c < there) store(p, v);
           }
-          continue;
-        }
-        const float scale = a.w_scale[o], bias = a.bias ? a.bias[o] : 0.f;
-        const int64_t at = static_cast<int64_t>(row0) * a.N + o;
-#pragma unroll
-        for (int c = 0; c < half; ++c) {
-          if (c >= rows) break;
-          const float v = scaled(acc[d][c], __ldg(a.x_scale + row0 + c), scale, bias);
-          if (a.out_f32) static_cast<float*>(a.y)[at + static_cast<int64_t>(c) * a.N] = v;
-          else static_cast<__nv_bfloat16*>(a.y)[at + static_cast<int64_t>(c) * a.N] = __float2bfloat16_rn(v);
         }
       }
     }
@@ -427,9 +444,9 @@ int columns_of(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 constexpr int kSMs = 152;
 
-template <int NC>
+template <int NC, typename Out>
 cudaError_t launch(const Args& a, const __half* x, cudaStream_t s) {
-  cudaError_t st = allow_most_smem<wide_kernel<NC>>();
+  cudaError_t st = allow_most_smem<wide_kernel<NC, Out>>();
   if (st != cudaSuccess) return st;
   CUtensorMap mw, mx;
   if (!map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.W, a.K, a.N, 128) ||
@@ -442,7 +459,7 @@ cudaError_t launch(const Args& a, const __half* x, cudaStream_t s) {
   items.blocks = (a.K + 127) / 128;
   items.total = items.tiles * items.chunks * items.splits;
   const int grid = items.total < kSMs ? items.total : kSMs;
-  st = launch_dependent(wide_kernel<NC>, dim3(grid), dim3(kWarpsWide * 32), Wide<NC>::kSmem, s, mw,
+  st = launch_dependent(wide_kernel<NC, Out>, dim3(grid), dim3(kWarpsWide * 32), Wide<NC>::kSmem, s, mw,
                         mx, a, items);
   if (st != cudaSuccess || a.splits == 1) return st;
   const int64_t n = static_cast<int64_t>(a.rows) * a.N;
@@ -468,12 +485,18 @@ int wide_splits(int64_t rows, int N, int K) {
   return best;
 }
 
-cudaError_t launch_wide(const Args& a, const __half* x, cudaStream_t s) {
+template <typename Out>
+cudaError_t launch_columns(const Args& a, const __half* x, cudaStream_t s) {
   switch (columns_of(a.rows)) {
-    case 32: return launch<32>(a, x, s);
-    case 64: return launch<64>(a, x, s);
-    default: return launch<128>(a, x, s);
+    case 32: return launch<32, Out>(a, x, s);
+    case 64: return launch<64, Out>(a, x, s);
+    default: return launch<128, Out>(a, x, s);
   }
+}
+
+cudaError_t launch_wide(const Args& a, const __half* x, cudaStream_t s) {
+  if (a.splits > 1) return launch_columns<int32_t>(a, x, s);
+  return a.out_f32 ? launch_columns<float>(a, x, s) : launch_columns<__nv_bfloat16>(a, x, s);
 }
 
 }  // namespace i8
