@@ -11,11 +11,11 @@
 //
 // A row belongs to a cluster of up to 16 blocks, which hold it in their shared memory
 // from its only read to the end (rows too long for that are read again from L2).
-// With a top-k of up to 600 (or so few tokens in all) the largest logits of the threads'
+// With a top-k of up to 1200 (or with 2048 tokens in all) the largest logits of the threads'
 // tokens give a threshold above which there are that many and few more; those are
 // gathered and sorted by one block, which draws the token.  Otherwise one pass counts tokens and adds weights up in 1024 bins of 1/32 of a nat below the
 // largest; the bin that a border falls into is gathered and sorted, by its exact order
-// (a bin with more than 1024 tokens is first narrowed down by further passes over ever
+// (a bin with more than 2048 tokens is first narrowed down by further passes over ever
 // finer ranges of that order).  What bounds it: a row's latency (load, passes with
 // cluster barriers, sorts), not memory.
 #include <float.h>
@@ -29,12 +29,12 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 static_assert(kWarps == 32, "a warp looks at all warps' sums");
-constexpr int kBins = 1024, kList = 1024;
-constexpr int kLikely = 600;             // top-k that is searched for among the largest
+constexpr int kBins = 1024, kList = 2 * kThreads;
+constexpr int kLikely = 1200;            // top-k that is searched for among the largest
 constexpr float kBinsPerNat = 32.f;
 constexpr float kOne = 1099511627776.f;  // 2^40
 constexpr int kMaxBlocks = 16;           // of a cluster
-constexpr size_t kMaxData = 160 * 1024;  // bytes of a block's part of a row
+constexpr size_t kMaxData = 152 * 1024;  // bytes of a block's part of a row
 constexpr int kSMs = 152;
 constexpr int kFewest = 2048;            // tokens of a block, where a row is split
 
@@ -61,15 +61,17 @@ struct Shared {
   u64 mass[kBins];
   uint32_t counts[kBins];  // the row's
   u64 masses[kBins];
-  uint32_t fine_counts[kBins];  // the row's, of a narrowed range
-  u64 fine_masses[kBins];
   u64 list[kList];         // block 0's
   union {
     struct {
       u64 sums[kList];     // running sums of its weights
       u64 own[kList];      // what this block adds to it
     };
-    uint32_t pieces[3][kBins];  // of the masses while they are added up, 15 bits each
+    struct {
+      uint32_t pieces[3][kBins];    // of the masses while they are added up, 15 bits each
+      uint32_t fine_counts[kBins];  // the row's, of a narrowed range
+      u64 fine_masses[kBins];
+    };
   };
   uint32_t listed, owned, base;
   u64 warp_sum[kWarps];
@@ -583,6 +585,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   float min_p = a.c.min_p_of ? a.c.min_p_of[r] : a.c.min_p;
   const float u = fminf(fmaxf(a.u[r], 0.f), 0x1.fffffep-1f);  // NaN: 0
   min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
+  if (k >= a.V) k = 0;
   if (threadIdx.x == 0) s.listed = 0;
   __syncthreads();
 
@@ -636,7 +639,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   if (k > 0 || by_p) {
     const bool pieces = a.part <= 1 << 17;
     // Few tokens, or a top-k: those that it can be about are gathered at once.
-    if (a.V <= kList || (k > 0 && k <= kLikely)) {
+    // (the threshold is one of the threads' largest logits: of three times as many threads)
+    if (a.V <= kList || (k > 0 && k <= min(kLikely, blocks * kThreads / 3))) {
       float least = -FLT_MAX;
       if (a.V > kList) {
         for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = 0;
