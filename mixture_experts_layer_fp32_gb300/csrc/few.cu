@@ -673,14 +673,17 @@ __device__ void choose(const Args& a, Plan& plan, int t, int at, bool own) {
   float p;
   choose_topk<PL>(s, t, a.E, a.k, a.score, a.groups, a.group_topk, a.expert_bias, plan.gsel[at],
                   a.err, idx, p);
+  // A token without k experts to choose (NaN logits, reported) names one twice: the first
+  // of them stands, so that no expert has more rows than there are tokens.
+  const uint32_t same = __match_any_sync(~0u, lane < a.k ? idx : -1 - lane);
   if (lane >= a.k) return;
-  const int i = t * a.k + lane;
+  const int i = t * a.k + lane, e = __ffs(same) - 1 == lane ? idx : -1;
   if (own) {
-    plan.expert[i] = static_cast<int16_t>(idx);
+    plan.expert[i] = static_cast<int16_t>(e);
     plan.prob[i] = p;
     if (blockIdx.x != 0) return;
   } else {
-    a.idx[i] = idx;
+    a.idx[i] = e;
     a.prob[i] = p;
   }
   if (a.idx_out) a.idx_out[i] = idx;
@@ -695,13 +698,22 @@ __device__ void choose_experts(const Args& a, Plan& plan, bool own) {
   const int parts = blockDim.x / width, e = threadIdx.x % width, part = threadIdx.x / width;
   const int warp = threadIdx.x >> 5;
   const int first = own ? 0 : blockIdx.x, step = own ? a.T : gridDim.x, each = own ? a.T : 1;
+  const float bias = a.gate_bias && threadIdx.x < a.E ? __ldg(a.gate_bias + threadIdx.x) : 0.f;
   for (int t0 = first; t0 < a.T; t0 += step) {
     for (int q = 0; q < each; ++q) {
       float sum = 0.f;
       if (e < a.E) {
-#pragma unroll 16
-        for (int s = part; s < n_slabs; s += parts)
-          sum += __ldcg(a.logits + (static_cast<int64_t>(s) * a.T + t0 + q) * a.E + e);
+        const float* l = a.logits + static_cast<int64_t>(t0 + q) * a.E + e;
+        for (int s = part; s < n_slabs; s += 16 * parts) {  // sixteen loads at a time
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int at = s + i * parts;
+            v[i] = at < n_slabs ? __ldcg(l + static_cast<int64_t>(at) * a.T * a.E) : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum += v[i];
+        }
       }
       __syncthreads();
       plan.part[threadIdx.x] = sum;
@@ -709,7 +721,7 @@ __device__ void choose_experts(const Args& a, Plan& plan, bool own) {
       if (threadIdx.x < a.E) {
         float l = 0.f;
         for (int i = 0; i < parts; ++i) l += plan.part[i * width + threadIdx.x];
-        plan.logit[q][threadIdx.x] = a.gate_bias ? l + a.gate_bias[threadIdx.x] : l;
+        plan.logit[q][threadIdx.x] = a.gate_bias ? l + bias : l;
       }
     }
     __syncthreads();
@@ -791,15 +803,7 @@ __device__ void plan_of_few(const Args& a, Plan& plan) {
   const int lane = threadIdx.x, pairs = plan.pairs;
   int e = lane < pairs ? plan.expert[lane] : -1;
   const uint32_t bits = lane < pairs ? __float_as_uint(plan.prob[lane]) : 0u;
-  const int token = lane < pairs ? lane / a.k : -1;
-  // as in make_plan: an expert named twice by a token, drops
   int place = 0, members = 0;
-  bool twice = false;
-  for (int q = 0; q < pairs; ++q) {
-    const int oe = __shfl_sync(~0u, e, q), ot = __shfl_sync(~0u, token, q);
-    twice |= q < lane && oe == e && ot == token;
-  }
-  if (twice) e = -1;
   if (a.capacity >= 0) {
     for (int q = 0; q < pairs; ++q) {
       const int oe = __shfl_sync(~0u, e, q);
@@ -832,7 +836,7 @@ __device__ void plan_of_few(const Args& a, Plan& plan) {
     plan.row_of[lane] = static_cast<int16_t>(e >= 0 ? row : -1);
   }
   if (e >= 0) {
-    plan.token[row] = static_cast<uint16_t>(token);
+    plan.token[row] = static_cast<uint16_t>(lane / a.k);
     plan.hit_of_row[row] = static_cast<int16_t>(hit);
   }
   if (leads) {
@@ -868,19 +872,9 @@ __device__ void make_plan(const Args& a, Plan& plan, bool own) {
     __syncthreads();
     return;
   }
-  // A token without k experts to choose (NaN logits, reported) names one twice; the
-  // first of them stands, so that no expert has more rows than there are tokens.
-  uint32_t marked = 0;  // of this thread's pairs, two at most
-  for (int i = threadIdx.x, r = 0; i < pairs; i += blockDim.x, ++r)
-    for (int q = i - i % a.k; q < i; ++q)
-      if (plan.expert[q] == plan.expert[i]) marked |= 1u << r;
-  __syncthreads();
-  for (int i = threadIdx.x, r = 0; i < pairs; i += blockDim.x, ++r)
-    if (marked >> r & 1) plan.expert[i] = -1;
-  __syncthreads();
   order_pairs(a, plan);
   if (a.capacity >= 0) {
-    marked = 0;
+    uint32_t marked = 0;  // of this thread's pairs, two at most
     for (int i = threadIdx.x, r = 0; i < pairs; i += blockDim.x, ++r) {
       const int e = plan.expert[i];
       if (e < 0 || plan.total[e] <= a.capacity) continue;
@@ -1001,8 +995,8 @@ __device__ void tile_done(const Args& a, Plan& plan, const Stream& s, int tile, 
     if (last > first) {
       __threadfence();
       is_last = atomicAdd(a.tiles + tile, 1) == last - first;
+      __threadfence();
     }
-    __threadfence();
     plan.on = is_last;
   }
   __syncthreads();
@@ -1090,6 +1084,7 @@ __device__ void combine(const Args& a, const Plan& plan, const Stream& s) {
     const int column = static_cast<int>(i - static_cast<int64_t>(t) * per) * 4;
     const int at = column / kColumns;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int j = 0; j < a.k; ++j) {
       const int row = plan.row_of[t * a.k + j];
       if (row < 0) continue;
