@@ -96,7 +96,7 @@ struct Plan {
   int16_t hit_of_row[kRowsAtMost];
   int16_t hit[MOE_MAX_EXPERTS];      // experts hit
   int16_t first[MOE_MAX_EXPERTS + 1];  // their first rows
-  int16_t total[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS];
+  int16_t total[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS], hit_of[MOE_MAX_EXPERTS];
   int16_t before[kGroups][MOE_MAX_EXPERTS];  // of 64 pairs each
   uint8_t rank[kPairs];
   float logit[kOwnTokens][MOE_MAX_EXPERTS], gsel[kOwnTokens][MOE_MAX_EXPERTS];
@@ -790,6 +790,7 @@ __device__ void order_pairs(const Args& a, Plan& plan) {
       plan.start[lane * 8 + i] = static_cast<int16_t>(row);
       if (n[i] > 0) {
         plan.hit[hit] = static_cast<int16_t>(lane * 8 + i);
+        plan.hit_of[lane * 8 + i] = static_cast<int16_t>(hit);
         plan.first[hit++] = static_cast<int16_t>(row);
         row += n[i];
       }
@@ -907,14 +908,12 @@ __device__ void make_plan(const Args& a, Plan& plan, bool own) {
     if (e >= 0) {
       row = plan.start[e] + plan.before[i / 64][e] + plan.rank[i];
       plan.token[row] = static_cast<uint16_t>(i / a.k);
+      plan.hit_of_row[row] = plan.hit_of[e];
     }
     plan.row_of[i] = static_cast<int16_t>(row);
   }
   for (int t = threadIdx.x; t < a.T; t += blockDim.x)
     plan.token[plan.rows + t] = static_cast<uint16_t>(t);
-  for (int i = threadIdx.x; i < plan.hits; i += blockDim.x)
-    for (int r = plan.first[i]; r < plan.first[i + 1]; ++r)
-      plan.hit_of_row[r] = static_cast<int16_t>(i);
   if (blockIdx.x == 0 && a.tpe_out)
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.tpe_out[e] = plan.total[e];
   __syncthreads();
@@ -959,13 +958,33 @@ template <typename T>
 __device__ void hidden_tile(const Args& a, const Plan& plan, const Tile& t, int first, int last) {
   const bool shared = t.hit == plan.hits;
   const int f = shared ? a.fs : a.f;
+#pragma unroll 2
   for (int i = threadIdx.x; i < t.rows * 64; i += blockDim.x) {
     const int n = i / 64, in = i % 64 * 4, column = t.at * 256 + in;
     if (column >= f) continue;
     const int row = t.first + n;
     const float* m = main_row(a, plan, 0, row, shared) + column;
-    const float4 g = sum_runs(a, 0, m, first, last, n, in);
-    const float4 w = sum_runs(a, 0, m + f, first, last, n, 256 + in);
+    float4 g = __ldcg(reinterpret_cast<const float4*>(m));
+    float4 w = __ldcg(reinterpret_cast<const float4*>(m + f));
+    const float* e = a.extra[0] + (static_cast<int64_t>(first + 1) * a.T + n) * kColumns + in;
+    const int64_t step = static_cast<int64_t>(a.T) * kColumns;
+#pragma unroll 1
+    for (int b = first + 1; b <= last; b += 4, e += 4 * step) {
+      float4 v[4][2];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          v[q][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (b + q <= last)
+            v[q][c] = __ldcg(reinterpret_cast<const float4*>(e + q * step + c * 256));
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        g.x += v[q][0].x, g.y += v[q][0].y, g.z += v[q][0].z, g.w += v[q][0].w;
+        w.x += v[q][1].x, w.y += v[q][1].y, w.z += v[q][1].z, w.w += v[q][1].w;
+      }
+    }
     const float o[4] = {swiglu(g.x, w.x), swiglu(g.y, w.y), swiglu(g.z, w.z), swiglu(g.w, w.w)};
     T* to = static_cast<T*>(a.hid) + hid_row(a, plan, row, shared) + column;
     if constexpr (sizeof(T) == 4) {
