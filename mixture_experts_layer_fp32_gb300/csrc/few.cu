@@ -6,23 +6,29 @@
 // cooperative grid, a block to an SM, goes through
 //   logits: a block takes some features and up to 32 experts, partial sums out;
 //   top-k: a block takes a token, adds its partial sums up and chooses (one token: every
-//     block, which spares a barrier; 4 tokens so, 8 of 128 of 2048 x 768: 75 us and 72); then every block builds the same plan (rows
-//     by expert, drops) in its shared memory;
+//     block, which spares a barrier; 4 tokens so, 8 of 128 of 2048 x 768: 75 us and 72);
+//     then every block builds the same plan (rows by expert, drops) in its shared memory;
 //   FC1: the stream of all hit experts' W1 and W3, cut into equal runs of units;
 //   hidden values: the last block to bring a partial sum of a tile adds them up, in
 //     order, forms silu(a) b and counts the tile as done for its expert;
-//   FC2: the stream of W2, cut the same way, an expert's part as soon as it is ready;
+//   FC2: the stream of W2, an expert's part as soon as it is ready, cut the same way or
+//     into pieces that blocks take in turn;
 //   combine: partial sums of a token's experts added in order, one rounding.
 // The barriers of all blocks are those around the top-k and the one before the combine:
 // a block's parts of the two streams are nearly the same experts', so that a slow
 // block delays its neighbours alone (with a barrier on either side of a step for the
-// hidden values, 32 tokens, 8 of 128 experts of 4096 x 1536, took 762 us where this takes
+// hidden values, 32 tokens, 8 of 128 experts of 4096 x 1536, took 762 us where this took
 // 718).
-// A block's part of both streams is one sequence of units, a unit 32 (fp32:
-// 16) inputs of a tile's 512 outputs, 64 (32) to each of its 8 (16) warps.  A warp copies its own units
+// A block's part of both streams is one sequence of units, a unit 32 (fp32: 16) inputs of
+// a tile's 512 outputs, 64 (32) to each of its 8 (16) warps.  A warp copies its own units
 // with cp.async into a ring of its own, up to kSlots - 1 units ahead, from FC1 into FC2
 // too: the weights do not depend on the hidden values, so memory stays busy while those
 // are waited for.
+//
+// Measured, all of a call: 1 token, 2 of 8 experts of 4096 x 14336 bf16, 129 us (the bytes
+// at the copy rate: 105); 8 tokens 400 (379); 32 tokens, 8 of 128 of 4096 x 1536, 689 (630).
+// The 20 to 25 us above the bytes are the logits, two or three barriers, the plan and the
+// combine, through most of which memory idles.
 //
 // The products are mma.sync with the weights as the operand of 16 rows and 8 tokens as
 // the columns.  The tensor cores' rate does not matter here (tcgen05 would need 128 rows
@@ -57,7 +63,8 @@ constexpr int kGroups = kPairs / 64;
 constexpr int kChunk = 384;                     // features of the router's operands at a time
 constexpr int kColumns = 512;                   // a tile's outputs: all warps'
 constexpr int kMostThreads = 512;
-constexpr int kOwnTokens = 1;                   // up to so many every block chooses for itself
+constexpr int kInPieces = 2;                    // tiles of FC2 to a block from which on pieces pay
+constexpr int kLargePieces = 304, kSmallPieces = 304;  // at most
 // a grid barrier gives up after about a second
 constexpr long long kWaitCycles = 2000000000ll;
 
@@ -79,10 +86,11 @@ struct Args {
   int32_t* idx;
   float* prob;
   float* main[2];   // of a product: partial sums that begin a tile, rows x outputs
-  float* extra[2];  // those that go on with one: [block][T][512]
+  float* extra[2];  // those that go on with one: [run][T][512]
   int* tiles;       // partial sums that a tile of FC1 has
   int* ready;       // tiles of an expert whose hidden values are there
-  int counters;     // of the two
+  int* queue;       // pieces of FC2 that were taken
+  int counters;     // of the three
   void* hid;     // [rows, f]; bf16: twice (the second pieces)
   int64_t hid_lo;
 };
@@ -99,8 +107,9 @@ struct Plan {
   int16_t total[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS], hit_of[MOE_MAX_EXPERTS];
   int16_t before[kGroups][MOE_MAX_EXPERTS];  // of 64 pairs each
   uint8_t rank[kPairs];
-  float logit[kOwnTokens][MOE_MAX_EXPERTS], gsel[kOwnTokens][MOE_MAX_EXPERTS];
+  float logit[MOE_MAX_EXPERTS], gsel[MOE_MAX_EXPERTS];
   float part[kMostThreads];
+  int taken[kLargePieces + kSmallPieces + 1];  // this block's pieces, in turn; -1: not yet
   int on, dropped;
 };
 
@@ -221,6 +230,17 @@ struct Shape : Form<T> {
 // expert's one after another, the shared expert's last; a tile's units follow the
 // inputs.  They are cut into equal runs, one to a block.  Units are counted in 32 bits:
 // 2^31 of 32 KB are past any memory (the caller checks).
+//
+// Memory serves some blocks up to a fifth slower than others, and those with many rows have
+// more to store.  So of a large bf16 FC2 the blocks' runs are a quarter, and the rest is
+// pieces, the small ones last, which blocks take as they come to them: 8, 16, 32 and 64
+// tokens, 8 of 128 experts of 4096 x 1536, take 328, 529, 689 and 769 us, in one run to a
+// block 337, 547, 716 and 833; 32 tokens, 8 of 64 of 7168 x 2048 and a shared one, 922 and
+// 1218.  More partial sums go to the combine: where a block has less than two tiles, or
+// tiles are long, that costs more than it gives (1 and 4 tokens of the first layer: 88 and
+// 211 us where one run takes 77 and 209; 64 tokens, 2 of 8 of 4096 x 14336: 566 and 557),
+// and fp32, which has no registers left for it, is slower by 20 us.  Which piece goes to
+// which block differs between calls, the pieces and the order of their sums do not.
 struct Stream {
   int S, begin, end;
   int tiles, units;        // of a routed expert; of a tile
@@ -228,15 +248,28 @@ struct Stream {
   int shared_tiles;        // of the shared expert
   int shared_units;        // of one of the shared expert's tiles
   int routed_units;
-  int each, rest;          // units of a block; the first `rest` blocks have one more
+  int each, rest;          // units of a block's run; the first `rest` blocks have one more
+  int fixed, n0;           // units of all blocks' runs, and how many have any
+  int q1, n1, q2, n2;      // the rest: n1 pieces of q1 units, then n2 of q2 (the last fewer)
 
-  __device__ void set(int hits, int tiles_, int units_, int shared_tiles_, int shared_units_) {
+  __device__ void set(int hits, int tiles_, int units_, int shared_tiles_, int shared_units_,
+                      bool in_pieces) {
     tiles = tiles_, units = units_, shared_tiles = shared_tiles_, shared_units = shared_units_;
     routed = hits * tiles;
     routed_units = routed * units;
-    S = routed_units + shared_tiles * shared_units;
+    S = fixed = routed_units + shared_tiles * shared_units;
     const int G = gridDim.x, b = blockIdx.x;
-    each = S / G, rest = S - each * G;
+    q1 = q2 = 1, n1 = n2 = 0;
+    if (in_pieces && routed + shared_tiles >= kInPieces * G) {
+      const int small = S / 8, large = S / 8 * 5;
+      q2 = max(6, (small + kSmallPieces - 1) / kSmallPieces);
+      n2 = (small + q2 - 1) / q2;
+      q1 = max(8, (large + kLargePieces - 1) / kLargePieces);
+      n1 = large / q1;
+      fixed = S - small - n1 * q1;
+    }
+    each = fixed / G, rest = fixed - each * G;
+    n0 = min(G, fixed);
     begin = b * each + min(b, rest);
     end = begin + each + (b < rest);
   }
@@ -251,16 +284,29 @@ struct Stream {
     }
   }
   __device__ int units_of(int tile) const { return tile < routed ? units : shared_units; }
-  __device__ int block_of(int u) const {
-    const int longer = rest * (each + 1);
-    return u < longer ? u / (each + 1) : rest + (u - longer) / each;
+  __device__ void piece(int p, int& from, int& to) const {
+    if (p < n1) {
+      from = fixed + p * q1;
+      to = from + q1;
+    } else {
+      from = fixed + n1 * q1 + (p - n1) * q2;
+      to = min(S, from + q2);
+    }
   }
-  // the blocks that have a tile's units
-  __device__ void blocks(int tile, int& first, int& last) const {
+  // the blocks' runs (empty ones not counted), then the pieces
+  __device__ int run_of(int u) const {
+    const int longer = rest * (each + 1);
+    if (u < longer) return u / (each + 1);
+    if (u < fixed) return rest + (u - longer) / each;
+    u -= fixed;
+    return u < n1 * q1 ? n0 + u / q1 : n0 + n1 + (u - n1 * q1) / q2;
+  }
+  // the runs that have a tile's units
+  __device__ void runs(int tile, int& first, int& last) const {
     const int u =
         tile < routed ? tile * units : routed_units + (tile - routed) * shared_units;
-    first = block_of(u);
-    last = block_of(u + units_of(tile) - 1);
+    first = run_of(u);
+    last = run_of(u + units_of(tile) - 1);
   }
 };
 
@@ -286,22 +332,47 @@ __device__ __forceinline__ Tile tile_of(const Args& a, const Plan& plan, const S
 }
 
 // A warp's copies: both streams' units in order.
-template <typename T>
+// A block's next piece, the same for all its warps: the first that asks for it takes it.
+__device__ __noinline__ int take_piece(int* queue, int* turn, int none, int* err) {
+  int p = none;
+  if ((threadIdx.x & 31) == 0) {
+    volatile int* mine = turn;
+    p = *mine;
+    if (p == -1 && atomicCAS(turn, -1, -2) == -1) {
+      p = atomicAdd(queue, 1);
+      *mine = p;
+    } else if (p < 0) {
+      const long long began = clock64();
+      while ((p = *mine) < 0)
+        if (clock64() - began > kWaitCycles) {
+          report_error(err, DEV_ERR_TIMEOUT, none);
+          p = none;
+          break;
+        }
+    }
+  }
+  p = __shfl_sync(~0u, p, 0);
+  __syncwarp();
+  return p;
+}
+
+template <typename T, bool QUEUE>
 struct Copies {
   using F = Shape<T>;
   static constexpr int kStep = 32 / F::kPieces;  // inputs of an instruction
   const Args& a;
-  const Plan& plan;
+  Plan& plan;
   const Stream* streams;
   uint32_t ring;      // this lane's place in a slot
   int product = 0, left = 0, slot = 0;
+  int turn = 0;       // pieces so far; -1: no more
   int next = 0;       // unit
   int unit = 0, units = 0, inputs = 0, outputs = 0;
   bool real = false;
   const T* src = nullptr;
   int dst[F::kCopies];
 
-  __device__ Copies(const Args& a_, const Plan& p, const Stream* s, const void* smem)
+  __device__ Copies(const Args& a_, Plan& p, const Stream* s, const void* smem)
       : a(a_), plan(p), streams(s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ring = smem_at(smem) + warp * kSlots * F::kUnit;
@@ -339,14 +410,31 @@ struct Copies {
     units = s.units_of(tile);
   }
 
+  // What comes after a run: FC2's own run, then the pieces that the block takes.
+  __device__ __forceinline__ void next_run() {
+    unit = units = 0;
+    const Stream& s = streams[1];
+    if (product == 0) {
+      product = 1;
+      next = s.begin;
+      left = s.end - s.begin;
+      if (left > 0) return;
+    }
+    const int n = QUEUE ? s.n1 + s.n2 : 0;
+    const int p = n > 0 ? take_piece(a.queue, &plan.taken[turn], n, a.err) : n;
+    ++turn;
+    if (p < n) {
+      int to;
+      s.piece(p, next, to);
+      left = to - next;
+    } else {
+      turn = -1;
+    }
+  }
+
   // the next unit, if there is one, and a group in any case
   __device__ __forceinline__ void issue() {
-    if (left == 0 && product == 0) {
-      product = 1;
-      left = streams[1].end - streams[1].begin;
-      next = streams[1].begin;
-      unit = units = 0;
-    }
+    if (left == 0 && turn >= 0) next_run();
     if (left > 0) {
       if (unit == units) {
         int tile, u;
@@ -432,8 +520,8 @@ struct Out {
 
 // A run of units of one tile, up to 8 NT rows, PIECES numbers to an input of bf16.
 // x: the rows' inputs from this run's first on; `left`: how many there are.
-template <typename T, int NT, int PIECES>
-__device__ __forceinline__ void run_units(Copies<T>& copies, int& slot, int units, const T* x,
+template <typename T, bool QUEUE, int NT, int PIECES>
+__device__ __forceinline__ void run_units(Copies<T, QUEUE>& copies, int& slot, int units, const T* x,
                                           int64_t x_lo, const uint16_t* row_at, int first,
                                           int count, int width, int left, const Out& out) {
   using F = Shape<T>;
@@ -659,19 +747,19 @@ __device__ void partial_logits(const Args& a, char* smem) {
   }
 }
 
-// A token's experts, by one warp; logits in plan.logit[at].  own: into this block's plan.
+// A token's experts, by one warp; logits in plan.logit.  own: into this block's plan.
 template <int PL>
-__device__ void choose(const Args& a, Plan& plan, int t, int at, bool own) {
+__device__ void choose(const Args& a, Plan& plan, int t, bool own) {
   const int lane = threadIdx.x & 31;
   float s[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = lane + 32 * i;
-    s[i] = e < a.E ? plan.logit[at][e] : -FLT_MAX;
+    s[i] = e < a.E ? plan.logit[e] : -FLT_MAX;
   }
   int idx;
   float p;
-  choose_topk<PL>(s, t, a.E, a.k, a.score, a.groups, a.group_topk, a.expert_bias, plan.gsel[at],
+  choose_topk<PL>(s, t, a.E, a.k, a.score, a.groups, a.group_topk, a.expert_bias, plan.gsel,
                   a.err, idx, p);
   // A token without k experts to choose (NaN logits, reported) names one twice: the first
   // of them stands, so that no expert has more rows than there are tokens.
@@ -690,46 +778,43 @@ __device__ void choose(const Args& a, Plan& plan, int t, int at, bool own) {
   if (a.prob_out) a.prob_out[i] = p;
 }
 
-// own: every block for all tokens, else each block for its own.
+// own: every block for the one token, else each block for its tokens.
 __device__ void choose_experts(const Args& a, Plan& plan, bool own) {
   const int n_slabs = slabs(gridDim.x, a.E, a.h);
   int width = 8;
   while (width < a.E) width *= 2;
   const int parts = blockDim.x / width, e = threadIdx.x % width, part = threadIdx.x / width;
   const int warp = threadIdx.x >> 5;
-  const int first = own ? 0 : blockIdx.x, step = own ? a.T : gridDim.x, each = own ? a.T : 1;
   const float bias = a.gate_bias && threadIdx.x < a.E ? __ldg(a.gate_bias + threadIdx.x) : 0.f;
-  for (int t0 = first; t0 < a.T; t0 += step) {
-    for (int q = 0; q < each; ++q) {
-      float sum = 0.f;
-      if (e < a.E) {
-        const float* l = a.logits + static_cast<int64_t>(t0 + q) * a.E + e;
-        for (int s = part; s < n_slabs; s += 16 * parts) {  // sixteen loads at a time
-          float v[16];
+  for (int t = own ? 0 : blockIdx.x; t < a.T; t += gridDim.x) {
+    float sum = 0.f;
+    if (e < a.E) {
+      const float* l = a.logits + static_cast<int64_t>(t) * a.E + e;
+      for (int s = part; s < n_slabs; s += 16 * parts) {  // sixteen loads at a time
+        float v[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = s + i * parts;
-            v[i] = at < n_slabs ? __ldcg(l + static_cast<int64_t>(at) * a.T * a.E) : 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sum += v[i];
+        for (int i = 0; i < 16; ++i) {
+          const int at = s + i * parts;
+          v[i] = at < n_slabs ? __ldcg(l + static_cast<int64_t>(at) * a.T * a.E) : 0.f;
         }
-      }
-      __syncthreads();
-      plan.part[threadIdx.x] = sum;
-      __syncthreads();
-      if (threadIdx.x < a.E) {
-        float l = 0.f;
-        for (int i = 0; i < parts; ++i) l += plan.part[i * width + threadIdx.x];
-        plan.logit[q][threadIdx.x] = a.gate_bias ? l + bias : l;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum += v[i];
       }
     }
     __syncthreads();
-    if (warp < each) {
-      if (a.E <= 32) choose<1>(a, plan, t0 + warp, warp, own);
-      else if (a.E <= 64) choose<2>(a, plan, t0 + warp, warp, own);
-      else if (a.E <= 128) choose<4>(a, plan, t0 + warp, warp, own);
-      else choose<8>(a, plan, t0 + warp, warp, own);
+    plan.part[threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.x < a.E) {
+      float l = 0.f;
+      for (int i = 0; i < parts; ++i) l += plan.part[i * width + threadIdx.x];
+      plan.logit[threadIdx.x] = a.gate_bias ? l + bias : l;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      if (a.E <= 32) choose<1>(a, plan, t, own);
+      else if (a.E <= 64) choose<2>(a, plan, t, own);
+      else if (a.E <= 128) choose<4>(a, plan, t, own);
+      else choose<8>(a, plan, t, own);
     }
   }
   __syncthreads();
@@ -932,9 +1017,9 @@ __device__ __forceinline__ int64_t hid_row(const Args& a, const Plan& plan, int 
   return static_cast<int64_t>(plan.rows) * a.f + static_cast<int64_t>(row - plan.rows) * a.fs;
 }
 
-// A row's sums of four neighbouring outputs, the runs in order.
-__device__ __forceinline__ float4 sum_runs(const Args& a, int product, const float* main,
-                                           int first, int last, int row, int column) {
+// A row's sums of four neighbouring outputs of FC2, the runs in order.
+__device__ __forceinline__ float4 sum_runs(const Args& a, const float* main, int first, int last,
+                                           int row, int column) {
   float4 v = __ldcg(reinterpret_cast<const float4*>(main));
   for (int b = first + 1; b <= last; b += 8) {  // eight loads at a time
     float4 w[8];
@@ -943,7 +1028,7 @@ __device__ __forceinline__ float4 sum_runs(const Args& a, int product, const flo
       w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (b + i <= last)
         w[i] = __ldcg(reinterpret_cast<const float4*>(
-            a.extra[product] + (static_cast<int64_t>(b + i) * a.T + row) * kColumns + column));
+            a.extra[1] + (static_cast<int64_t>(b + i) * a.T + row) * kColumns + column));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) v.x += w[i].x, v.y += w[i].y, v.z += w[i].z, v.w += w[i].w;
@@ -1008,7 +1093,7 @@ __device__ void hidden_tile(const Args& a, const Plan& plan, const Tile& t, int 
 template <typename T>
 __device__ void tile_done(const Args& a, Plan& plan, const Stream& s, int tile, const Tile& t) {
   int first, last;
-  s.blocks(tile, first, last);
+  s.runs(tile, first, last);
   __syncthreads();
   if (threadIdx.x == 0) {
     int is_last = 1;
@@ -1031,19 +1116,27 @@ __device__ void tile_done(const Args& a, Plan& plan, const Stream& s, int tile, 
 }
 
 // This block's units of a product.  false where a wait ran out.
-template <typename T>
+template <typename T, bool QUEUE>
 __device__ bool stream_product(const Args& a, Plan& plan, const Stream* streams, int product,
-                               Copies<T>& copies, int& slot) {
+                               Copies<T, QUEUE>& copies, int& slot) {
   using F = Shape<T>;
   const Stream& s = streams[product];
   const int warp = threadIdx.x >> 5;
-  int ready = -1;
-  for (int u = s.begin; u < s.end;) {
+  int ready = -1, turn = 0, run = blockIdx.x;
+  for (int u = s.begin, end = s.end;;) {
+    if (u == end) {
+      // this warp's copies are ahead, so the next piece is known
+      if (!QUEUE || product == 0 || s.n1 + s.n2 == 0) break;
+      const int p = *const_cast<volatile int*>(&plan.taken[turn++]);
+      if (p < 0 || p >= s.n1 + s.n2) break;
+      s.piece(p, u, end);
+      run = s.n0 + p;
+    }
     int tile, unit;
     s.find(u, tile, unit);
     const Tile t = tile_of(a, plan, s, tile);
     const bool shared = t.hit == plan.hits;
-    const int f = shared ? a.fs : a.f, units = min(s.units_of(tile) - unit, s.end - u);
+    const int f = shared ? a.fs : a.f, units = min(s.units_of(tile) - unit, end - u);
     if (product == 1 && ready != t.hit) {
       if (!expert_ready(a, plan, t.hit, shared ? streams[0].shared_tiles : streams[0].tiles))
         return false;
@@ -1059,7 +1152,7 @@ __device__ bool stream_product(const Args& a, Plan& plan, const Stream* streams,
                (product == 0 && warp >= F::kWarps / 2 ? f : 0);
       out.stride = product ? a.h : 2 * f;
     } else {
-      out.at = a.extra[product] + static_cast<int64_t>(blockIdx.x) * a.T * kColumns + warp * F::kStrip;
+      out.at = a.extra[product] + static_cast<int64_t>(run) * a.T * kColumns + warp * F::kStrip;
       out.stride = kColumns;
     }
     const int k0 = unit * F::kInputs;
@@ -1070,7 +1163,7 @@ __device__ bool stream_product(const Args& a, Plan& plan, const Stream* streams,
     x += k0;
     constexpr int P2 = sizeof(T) == 2 ? 2 : 1;
     auto run = [&](auto nt, auto pieces) {
-      run_units<T, decltype(nt)::value, decltype(pieces)::value>(
+      run_units<T, QUEUE, decltype(nt)::value, decltype(pieces)::value>(
           copies, slot, units, x, a.hid_lo, row_at, t.first, t.rows, inputs, inputs - k0, out);
     };
     auto by_rows = [&](auto pieces) {
@@ -1111,16 +1204,16 @@ __device__ void combine(const Args& a, const Plan& plan, const Stream& s) {
       const int hit = plan.hit_of_row[row];
       const float p = plan.prob[t * a.k + j];
       int first, last;
-      s.blocks(hit * s.tiles + at, first, last);
-      const float4 v = sum_runs(a, 1, main_row(a, plan, 1, row, false) + column, first, last,
+      s.runs(hit * s.tiles + at, first, last);
+      const float4 v = sum_runs(a, main_row(a, plan, 1, row, false) + column, first, last,
                                 row - plan.first[hit], column % kColumns);
       y.x = fmaf(p, v.x, y.x), y.y = fmaf(p, v.y, y.y);
       y.z = fmaf(p, v.z, y.z), y.w = fmaf(p, v.w, y.w);
     }
     if (a.fs) {
       int first, last;
-      s.blocks(s.routed + at, first, last);
-      const float4 v = sum_runs(a, 1, main_row(a, plan, 1, plan.rows + t, true) + column, first,
+      s.runs(s.routed + at, first, last);
+      const float4 v = sum_runs(a, main_row(a, plan, 1, plan.rows + t, true) + column, first,
                                 last, t, column % kColumns);
       y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
     }
@@ -1128,7 +1221,7 @@ __device__ void combine(const Args& a, const Plan& plan, const Stream& s) {
   }
 }
 
-template <typename T>
+template <typename T, bool QUEUE>
 __global__ void __launch_bounds__(Shape<T>::kThreads, 1) few_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) char smem[];
   Plan& plan = *reinterpret_cast<Plan*>(smem + kRing);
@@ -1138,29 +1231,32 @@ __global__ void __launch_bounds__(Shape<T>::kThreads, 1) few_kernel(const __grid
     a.tiles[i] = 0;
   partial_logits<T>(a, smem);
   bool on = grid_barrier(a, plan, 1);
-  const bool own = a.T <= kOwnTokens;
+  const bool own = a.T == 1;
   if (on) {
     choose_experts(a, plan, own);
     if (!own) on = grid_barrier(a, plan, 2);
   }
   if (on) {
     make_plan(a, plan, own);
+    if constexpr (QUEUE)
+      for (int i = threadIdx.x; i < kLargePieces + kSmallPieces + 1; i += blockDim.x)
+        plan.taken[i] = -1;
     if (threadIdx.x < 2) {
       constexpr int U = Shape<T>::kInputs;
       auto up = [](int n, int d) { return (n + d - 1) / d; };
       if (threadIdx.x == 0)
-        streams[0].set(plan.hits, up(a.f, 256), up(a.h, U), up(a.fs, 256), up(a.h, U));
+        streams[0].set(plan.hits, up(a.f, 256), up(a.h, U), up(a.fs, 256), up(a.h, U), false);
       else
         streams[1].set(plan.hits, up(a.h, kColumns), up(a.f, U), a.fs ? up(a.h, kColumns) : 0,
-                       up(a.fs, U));
+                       up(a.fs, U), QUEUE);
     }
     __syncthreads();
-    Copies<T> copies(a, plan, streams, smem);
+    Copies<T, QUEUE> copies(a, plan, streams, smem);
 #pragma unroll 1
     for (int i = 0; i < kSlots - 1; ++i) copies.issue();
     int slot = 0;
-    on = stream_product<T>(a, plan, streams, 0, copies, slot) &&
-         stream_product<T>(a, plan, streams, 1, copies, slot);
+    on = stream_product<T, QUEUE>(a, plan, streams, 0, copies, slot) &&
+         stream_product<T, QUEUE>(a, plan, streams, 1, copies, slot);
     wait_copies<0>();
     on = on && grid_barrier(a, plan, own ? 2 : 3);
     if (on) combine<T>(a, plan, streams[1]);
@@ -1174,6 +1270,7 @@ struct Layout {
   size_t logits, idx, prob, main[2], extra[2], counters, hid, total;
   int64_t hid_lo;
   int tiles, all;  // counters
+  bool in_pieces;
 };
 Layout layout(int T, int h, int E, int k, int f, int fs, int dtype) {
   Layout L;
@@ -1190,10 +1287,15 @@ Layout layout(int T, int h, int E, int k, int f, int fs, int dtype) {
   L.prob = take(pairs * 4);
   L.main[0] = take(2 * values * 4);
   L.main[1] = take(rows * h * 4);
-  for (int i = 0; i < 2; ++i) L.extra[i] = take(static_cast<size_t>(kFewBlocks) * T * kColumns * 4);
   const int most = pairs < static_cast<size_t>(E) ? static_cast<int>(pairs) : E;  // experts hit
+  const int64_t fc2_tiles = static_cast<int64_t>(most + (fs > 0)) * ((h + kColumns - 1) / kColumns);
+  L.in_pieces = dtype == MOE_BF16 && fc2_tiles >= kInPieces * kFewBlocks;
+  for (int i = 0; i < 2; ++i) {
+    const int runs = kFewBlocks + (i && L.in_pieces ? kLargePieces + kSmallPieces : 0);
+    L.extra[i] = take(static_cast<size_t>(runs) * T * kColumns * 4);
+  }
   L.tiles = most * ((f + 255) / 256) + (fs + 255) / 256;
-  L.all = L.tiles + most + 1;
+  L.all = L.tiles + most + 1 + 1;  // the shared expert's, the queue's
   L.counters = take(static_cast<size_t>(L.all) * 4);
   L.hid_lo = static_cast<int64_t>(up256(values * 2) / 2);
   L.hid = take(dtype == MOE_F32 ? values * 4 : static_cast<size_t>(L.hid_lo) * 2 * 2);
@@ -1201,9 +1303,9 @@ Layout layout(int T, int h, int E, int k, int f, int fs, int dtype) {
   return L;
 }
 
-template <typename T>
+template <typename T, bool QUEUE>
 cudaError_t launch(Args& a, cudaStream_t s) {
-  cudaError_t st = allow_most_smem<few_kernel<T>>();
+  cudaError_t st = allow_most_smem<few_kernel<T, QUEUE>>();
   if (st != cudaSuccess) return st;
   cudaLaunchConfig_t cfg = {};
   const int sms = device_sm_count();
@@ -1216,7 +1318,7 @@ cudaError_t launch(Args& a, cudaStream_t s) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<T>, static_cast<const Args>(a));
+  return cudaLaunchKernelEx(&cfg, few_kernel<T, QUEUE>, static_cast<const Args>(a));
 }
 
 }  // namespace
@@ -1253,10 +1355,12 @@ cudaError_t launch_few(const moe_config& c, int fs, int64_t capacity, const void
   }
   a.tiles = reinterpret_cast<int*>(at + L.counters);
   a.ready = a.tiles + L.tiles;
+  a.queue = a.tiles + L.all - 1;
   a.counters = L.all;
   a.hid = at + L.hid;
   a.hid_lo = L.hid_lo;
-  return c.dtype == MOE_F32 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);
+  if (c.dtype == MOE_F32) return launch<float, false>(a, s);
+  return L.in_pieces ? launch<__nv_bfloat16, true>(a, s) : launch<__nv_bfloat16, false>(a, s);
 }
 
 }  // namespace moe

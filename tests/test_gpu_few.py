@@ -278,3 +278,20 @@ def test_a_wait_that_runs_out_is_reported():
     moe.forward_few(cfg, c.x, c.Wg, c.gb, None, c.W1, c.W3, c.W2, y, ws)
     moe.check(ws)
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=64, h=1024, E=256, k=8, f=128),                    # some 440 tiles of 4 units
+    dict(T=48, h=1024, E=256, k=8, f=128, fs=256, score="sigmoid", expert_bias=True),
+    dict(T=64, h=4096, E=48, k=8, f=384, capacity=0.5),
+    dict(T=64, h=1024, E=256, k=8, f=128, same=True),         # room for pieces, eight experts
+    dict(T=20, h=7168, E=32, k=8, f=128, fs=1408),            # long and short tiles
+], ids=str)
+def test_pieces_taken_in_turn(kw):
+    """Where FC2 has many tiles its stream is taken in pieces: which block has which is not the
+    same from call to call, the bits are."""
+    c = LayerCase(**kw).cuda()
+    out = call(c)
+    verify(c, out)
+    for _ in range(5):
+        assert same(out, call(c, ws=out[4]))
