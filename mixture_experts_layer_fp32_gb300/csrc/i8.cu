@@ -33,14 +33,27 @@ __device__ __forceinline__ int code_of(float x, float scale, float inverse) {
   return static_cast<int>(fminf(fmaxf(q, -127.f), 127.f));
 }
 
-__device__ __forceinline__ void store_codes(int8_t* at, const int (&c)[4]) {
-  const char4 v = make_char4(c[0], c[1], c[2], c[3]);
-  *reinterpret_cast<char4*>(at) = v;
+// n codes in one store: halves of a sector would be filled up from memory.
+template <int n>
+__device__ __forceinline__ void store_codes(int8_t* at, const int (&c)[n]) {
+  char v[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) v[i] = static_cast<char>(c[i]);
+  using Word = typename std::conditional<n == 8, uint2, uint32_t>::type;
+  Word w;
+  memcpy(&w, v, n);
+  *reinterpret_cast<Word*>(at) = w;
 }
-__device__ __forceinline__ void store_codes(__half* at, const int (&c)[4]) {
-  const __half2 v[2] = {__halves2half2(__int2half_rn(c[0]), __int2half_rn(c[1])),
-                        __halves2half2(__int2half_rn(c[2]), __int2half_rn(c[3]))};
-  memcpy(at, v, 8);
+template <int n>
+__device__ __forceinline__ void store_codes(__half* at, const int (&c)[n]) {
+  __half2 v[n / 2];
+#pragma unroll
+  for (int i = 0; i < n / 2; ++i)
+    v[i] = __halves2half2(__int2half_rn(c[2 * i]), __int2half_rn(c[2 * i + 1]));
+  using Word = typename std::conditional<n == 8, uint4, uint2>::type;
+  Word w;
+  memcpy(&w, v, 2 * n);
+  *reinterpret_cast<Word*>(at) = w;
 }
 
 template <typename T>
@@ -84,13 +97,11 @@ struct Coder {
   }
   template <typename T, typename Code>
   __device__ __forceinline__ void put(const Piece<T>& p, Code* out) const {
+    int c[Piece<T>::n];
 #pragma unroll
-    for (int i = 0; i < Piece<T>::n; i += 4) {
-      int c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = some ? code_of(as_float(p.v[i + j]) * up, s, inverse) : 0;
-      store_codes(out + i, c);
-    }
+    for (int j = 0; j < Piece<T>::n; ++j)
+      c[j] = some ? code_of(as_float(p.v[j]) * up, s, inverse) : 0;
+    store_codes(out, c);
   }
 };
 
