@@ -9,11 +9,12 @@ namespace {
 
 // ------------------------------------------------------------------ quantising
 // A row's scale is its largest magnitude times fp32's 1 / 127, a code the nearest whole
-// number of x over the scale, ties to even: the quotient is estimated by a product
-// with the reciprocal, and what is left of x (exact by fma: it has few bits) decides
-// whether the neighbour is nearer.  A row's values stay in registers between the
+// number of x over the scale, ties to even.  The quotient is estimated by a product with
+// the reciprocal, within 2^-15 of it (127 times two roundings of 2^-24); where that could
+// lie on the other side of a half, what is left of x (exact by fma: it has few bits)
+// decides whether the neighbour is nearer.  A row's values stay in registers between the
 // search and the codes as far as a block holds them (kHeld 16-byte pieces a thread).
-// Bound by memory.
+// 8192 x 4096 bf16 take 41 us (with the remainder of every value 51; the bytes 15), fp32 30 (47; 25).
 constexpr int kQuantThreads = 256, kHeld = 4;
 
 template <typename T>
@@ -24,32 +25,33 @@ struct Piece {
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-__device__ __forceinline__ int code_of(float x, float scale, float inverse) {
+__device__ __forceinline__ float code_of(float x, float scale, float inverse) {
   float q = rintf(x * inverse);
   const float twice = 2.f * fmaf(-q, scale, x);
   const bool odd = static_cast<int>(q) & 1;
   if (twice > scale || (twice == scale && odd)) q += 1.f;
   else if (-twice > scale || (-twice == scale && odd)) q -= 1.f;
-  return static_cast<int>(fminf(fmaxf(q, -127.f), 127.f));
+  return fminf(fmaxf(q, -127.f), 127.f);
 }
+
+constexpr float kWhole = 12582912.f;  // 1.5 2^23: a small number added to it is rounded
 
 // n codes in one store: halves of a sector would be filled up from memory.
 template <int n>
-__device__ __forceinline__ void store_codes(int8_t* at, const int (&c)[n]) {
+__device__ __forceinline__ void store_codes(int8_t* at, const float (&q)[n]) {
   char v[n];
 #pragma unroll
-  for (int i = 0; i < n; ++i) v[i] = static_cast<char>(c[i]);
+  for (int i = 0; i < n; ++i) v[i] = static_cast<char>(__float_as_int(q[i] + kWhole) & 0xff);
   using Word = typename std::conditional<n == 8, uint2, uint32_t>::type;
   Word w;
   memcpy(&w, v, n);
   *reinterpret_cast<Word*>(at) = w;
 }
 template <int n>
-__device__ __forceinline__ void store_codes(__half* at, const int (&c)[n]) {
+__device__ __forceinline__ void store_codes(__half* at, const float (&q)[n]) {
   __half2 v[n / 2];
 #pragma unroll
-  for (int i = 0; i < n / 2; ++i)
-    v[i] = __halves2half2(__int2half_rn(c[2 * i]), __int2half_rn(c[2 * i + 1]));
+  for (int i = 0; i < n / 2; ++i) v[i] = __floats2half2_rn(q[2 * i], q[2 * i + 1]);
   using Word = typename std::conditional<n == 8, uint4, uint2>::type;
   Word w;
   memcpy(&w, v, 2 * n);
@@ -86,22 +88,31 @@ struct Top {
 
 struct Coder {
   float scale, up, s, inverse;
-  bool some;
+  bool some, plain;
   __device__ __forceinline__ explicit Coder(const Top& top) {
     scale = top.good ? top.most * (1.f / 127.f) : NAN;
     // no reciprocal of a scale past 2^-126 is lost to overflow
     up = scale < 0x1p-100f ? 0x1p64f : 1.f;
     some = scale > 0.f;  // neither 0 nor NaN
+    plain = some && up == 1.f;
     s = scale * up;
     inverse = some ? 1.f / s : 0.f;
   }
   template <typename T, typename Code>
   __device__ __forceinline__ void put(const Piece<T>& p, Code* out) const {
-    int c[Piece<T>::n];
+    float q[Piece<T>::n];
+    bool sure = plain;
 #pragma unroll
-    for (int j = 0; j < Piece<T>::n; ++j)
-      c[j] = some ? code_of(as_float(p.v[j]) * up, s, inverse) : 0;
-    store_codes(out, c);
+    for (int j = 0; j < Piece<T>::n; ++j) {
+      const float t = as_float(p.v[j]) * inverse;
+      q[j] = (t + kWhole) - kWhole;
+      sure &= fabsf(t - q[j]) < 0.5f - 0x1p-14f;
+    }
+    if (!sure)
+#pragma unroll
+      for (int j = 0; j < Piece<T>::n; ++j)
+        q[j] = some ? code_of(as_float(p.v[j]) * up, s, inverse) : 0.f;
+    store_codes(out, q);
   }
 };
 
