@@ -331,7 +331,6 @@ __device__ __forceinline__ Tile tile_of(const Args& a, const Plan& plan, const S
   return t;
 }
 
-// A warp's copies: both streams' units in order.
 // A block's next piece, the same for all its warps: the first that asks for it takes it.
 __device__ __noinline__ int take_piece(int* queue, int* turn, int none, int* err) {
   int p = none;
@@ -356,6 +355,7 @@ __device__ __noinline__ int take_piece(int* queue, int* turn, int none, int* err
   return p;
 }
 
+// A warp's copies: both streams' units in order.  QUEUE: FC2's in pieces too.
 template <typename T, bool QUEUE>
 struct Copies {
   using F = Shape<T>;
@@ -521,9 +521,10 @@ struct Out {
 // A run of units of one tile, up to 8 NT rows, PIECES numbers to an input of bf16.
 // x: the rows' inputs from this run's first on; `left`: how many there are.
 template <typename T, bool QUEUE, int NT, int PIECES>
-__device__ __forceinline__ void run_units(Copies<T, QUEUE>& copies, int& slot, int units, const T* x,
-                                          int64_t x_lo, const uint16_t* row_at, int first,
-                                          int count, int width, int left, const Out& out) {
+__device__ __forceinline__ void run_units(Copies<T, QUEUE>& copies, int& slot, int units,
+                                          const T* x, int64_t x_lo, const uint16_t* row_at,
+                                          int first, int count, int width, int left,
+                                          const Out& out) {
   using F = Shape<T>;
   constexpr bool kHalf = sizeof(T) == 2;
   constexpr int kLane = F::kInputs / 4;  // inputs of a lane: 16 bytes

@@ -14,7 +14,8 @@ namespace {
 // lie on the other side of a half, what is left of x (exact by fma: it has few bits)
 // decides whether the neighbour is nearer.  A row's values stay in registers between the
 // search and the codes as far as a block holds them (kHeld 16-byte pieces a thread).
-// 8192 x 4096 bf16 take 41 us (with the remainder of every value 51; the bytes 15), fp32 30 (47; 25).
+// 8192 x 4096 bf16 take 41 us (with the remainder of every value 51; the bytes 15), fp32
+// 30 (47; 25): a row's load, search and store follow one another.
 constexpr int kQuantThreads = 256, kHeld = 4;
 
 template <typename T>
@@ -166,7 +167,10 @@ cudaError_t quantize(int64_t rows, int K, const void* x, Code* codes, float* sca
 // instruction m16n8k32, whose sums are whole.  64 inputs of a row of W are 16 bytes to
 // each of four lanes: the inputs are permuted within 64, the same for x, so that both
 // operands come straight from memory in 16-byte pieces.  A block's 8 warps share
-// 8 / parts groups of 16 outputs, `parts` warps to the inputs of one.
+// 8 / parts groups of 16 outputs, `parts` warps to the inputs of one.  What bounds it:
+// memory, and beside it the integer instruction (4 rows by 65536 x 4096: 51 us, 5.3 TB/s,
+// the tensor cores busy for 61% of it); one row by 4096 x 4096 (7.5 us, the bytes 2.5) a
+// launch, the row's quantising in every block and one round of loads.
 constexpr int kNarrowWarps = 8;
 constexpr int kSteps = 4;  // of 64 inputs, in flight
 

@@ -11,14 +11,18 @@
 //
 // A row belongs to a cluster of up to 16 blocks, which hold it in their shared memory
 // from its only read to the end (rows too long for that, or too many, are read again from
-// L2).
-// With a top-k of up to 1200 (or with 2048 tokens in all) the largest logits of the threads'
-// tokens give a threshold above which there are that many and few more; those are
-// gathered and sorted by one block, which draws the token.  Otherwise one pass counts tokens and adds weights up in 1024 bins of 1/32 of a nat below the
-// largest; the bin that a border falls into is gathered and sorted, by its exact order
-// (a bin with more than 2048 tokens is first narrowed down by further passes over ever
-// finer ranges of that order).  What bounds it: a row's latency (load, passes with
-// cluster barriers, sorts), not memory.
+// L2).  With a top-k of up to 1200 (or with 2048 tokens in all) the largest logits of the
+// threads' tokens give a threshold above which there are that many and few more; those
+// are gathered and sorted by one block, which draws the token.  Otherwise one pass counts
+// tokens and adds weights up in 1024 bins of 1/32 of a nat below the largest; the bin that
+// a border falls into is gathered and sorted, by its exact order (a bin with more than
+// 2048 tokens is first narrowed down by further passes over ever finer ranges of that
+// order).
+//
+// What bounds it: a row's latency (load, passes with cluster barriers, sorts), not memory.
+// One row of 128000 fp32 with top-k, top-p and min-p takes 25 us, 64 of 151936 bf16 23 (the
+// bytes at the copy rate 0.1 and 3).  With a top-p alone the 64 take 110: all tokens are
+// weighed, by integer instructions mostly (58% of the issue slots).
 #include <float.h>
 #include <math.h>
 

@@ -3,6 +3,8 @@ sampling, against the definitions in 64 bits."""
 
 import importlib.util
 import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -94,3 +96,43 @@ def test_a_step_with_4_bit_experts_and_a_head_in_8():
     moe.quantize_rows_i8(decoder.n2, codes, scales)
     want = (codes.double() @ head.codes.double().t()).float() * scales[:, None] * head.scales
     assert torch.equal(logits, want)
+
+
+def test_first_calls_are_captured():
+    """A process whose first calls of the three operators are captured into a graph."""
+    code = """
+import torch
+import mixture_experts_layer_fp32_gb300 as moe
+d = dict(device="cuda")
+bf = torch.bfloat16
+x = torch.randn(9, 256, **d).to(bf)
+Wg = torch.randn(256, 4, **d)
+W = [torch.randn(4, 256, 256, **d).to(bf) * 0.1 for _ in range(3)]
+cfg = moe.config(T=9, h=256, E=4, k=2, f=256)
+ws = moe.alloc_workspace_few(cfg)
+w = moe.I8Weight(torch.randint(-127, 128, (1000, 256), dtype=torch.int8, **d), torch.ones(1000, **d))
+wl = moe.alloc_workspace_linear_i8(20, w)
+x2 = torch.randn(20, 256, **d)
+u = torch.rand(20, **d)
+def step():
+    y = torch.zeros(9, 256, dtype=bf, **d)
+    moe.forward_few(cfg, x, Wg, None, None, *W, y, ws)
+    logits = torch.zeros(20, 1000, **d)
+    moe.linear_i8(x2, w, logits, wl)
+    tokens = torch.zeros(20, dtype=torch.int32, **d)
+    moe.sample(logits, u, tokens, top_k=30)
+    return y, logits, tokens
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+moe.check(ws), moe.check(wl)
+want = step()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert float(got[0].abs().max()) > 0 and int(got[2].max()) > 0
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                          timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]

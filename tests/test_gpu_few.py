@@ -295,3 +295,34 @@ def test_pieces_taken_in_turn(kw):
     verify(c, out)
     for _ in range(5):
         assert same(out, call(c, ws=out[4]))
+
+
+def test_weights_past_32_bits():
+    """Experts that lie more than 2^31 weights from the first give what a layer of those alone
+    does: scores are sigmoids, so leaving out the others changes no weight."""
+    import mixture_experts_layer_fp32_gb300 as moe
+    T, h, E, f = 5, 4096, 136, 4096
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def some(*shape, std):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(0, std, generator=g)
+
+    x, y = some(T, h, std=1), []
+    Wg = some(h, E, std=h ** -0.5).float()
+    W1, W3 = (some(E, h, f, std=h ** -0.5) for _ in range(2))
+    W2 = some(E, f, h, std=f ** -0.5)
+    bias = torch.zeros(E, device="cuda")
+    bias[-2:] = 10
+    for first in (0, E - 2):
+        cfg = moe.config(T=T, h=h, E=E - first, k=2, f=f, score="sigmoid")
+        ws = moe.alloc_workspace_few(cfg)
+        idx = torch.empty(T, 2, dtype=torch.int32, device="cuda")
+        y.append(torch.empty(T, h, dtype=torch.bfloat16, device="cuda"))
+        moe.forward_few(cfg, x, Wg[:, first:].contiguous(), None, bias[first:].clone(), W1[first:],
+                        W3[first:], W2[first:], y[-1], ws, topk_idx=idx)
+        moe.check(ws)
+        assert bool((idx + first >= E - 2).all())
+    # fp32 sums in another order, one rounding each: a step of bf16 of the largest at most
+    a, b = (v.double() for v in y)
+    assert float((a - b).abs().max()) <= 2.0 ** -7 * float(a.abs().max())
+    assert float(a.abs().max()) > 0.1

@@ -257,3 +257,18 @@ def test_last_dimension_and_leading_ones():
     moe.linear_i8(x, w, y, moe.alloc_workspace_linear_i8(30, w))
     xq, xs = quantised(x.view(30, 128))
     assert torch.equal(y.view(30, 96), product(xq, xs, w.codes, w.scales, torch.float32))
+
+
+def test_results_past_32_bits():
+    """70000 x 32768 results: the last rows' are those of a call of their own."""
+    import mixture_experts_layer_fp32_gb300 as moe
+    M, N, K = 70000, 32768, 48
+    xq, xs, wq, ws = codes((M, K), 1), scales(M, 2), codes((N, K), 3), scales(N, 4)
+    w = moe.I8Weight(wq, ws)
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    workspace = moe.alloc_workspace_linear_i8(M, w)
+    moe.linear_i8(xq, w, y, workspace, x_scale=xs)
+    moe.check(workspace)
+    for r in (0, 65535, M - 100):
+        part = slice(r, r + 100)
+        assert torch.equal(y[part], product(xq[part], xs[part], wq, ws, torch.bfloat16))

@@ -233,3 +233,18 @@ def test_streams_at_once():
     torch.cuda.synchronize()
     for o, w in zip(out, want):
         assert np.array_equal(o.cpu().numpy(), w)
+
+
+def test_logits_past_32_bits():
+    """20000 rows of 120001: the last rows' tokens are those of a call of their own."""
+    rows, V = 20000, 120001
+    g = torch.Generator(device="cuda").manual_seed(1)
+    logits = torch.empty(rows, V, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    u = torch.rand(rows, device="cuda", generator=g)
+    kw = dict(temperature=0.8, top_k=50, top_p=0.9)
+    got, prob = run(logits, u, **kw)
+    # 2400020000 logits: the last 16 rows, and those around the 2^31st
+    for r in (rows - 16, 2 ** 31 // V - 8):
+        l, v = logits[r:r + 16].clone(), u[r:r + 16].clone()
+        want, p = run(l, v, **kw)
+        assert np.array_equal(got[r:r + 16], want) and np.array_equal(prob[r:r + 16], p)
