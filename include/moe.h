@@ -770,8 +770,9 @@ moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, c
  * When to take it: fp32 layers and small bf16 ones at any number of tokens, large
  * bf16 layers up to about 8.  With more, bf16 experts that get many rows each are
  * faster in moe_forward, which rounds the hidden values to bf16 (2 of 8 experts of
- * 4096 x 14336, 1 / 8 / 32 / 64 tokens: 126 / 400 / 477 / 551 us here, 225 / 400 /
- * 415 / 417 there; 8 of 128 of 4096 x 1536, 1 / 8 / 32 / 64: FINE).
+ * 4096 x 14336, 1 / 8 / 16 / 64 tokens: 128 / 420 / 458 / 567 us here, 215 / 405 /
+ * 422 / 425 there; 8 of 128 of 4096 x 1536: 75 / 312 / 495 / 777 and 126 / 311 / 480 /
+ * 728; fp32, 2 of 8 of 1024 x 2048, 1 / 64: 34 / 104 and 180 / 258).
  *   ws: moe_workspace_size_few bytes; a workspace of cfg's num_tokens serves
  *   every call of fewer tokens too.
  */
