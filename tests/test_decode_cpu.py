@@ -227,3 +227,14 @@ def test_binding_sample(recorder):  # noqa: F811
         a.update(bad)
         with pytest.raises(ValueError):
             m.sample(**a)
+
+
+@pytest.mark.parametrize("fs", [0, 1408])
+def test_few_workspace_serves_fewer_tokens_where_pieces_begin(moe, fs):
+    """From some number of tokens on there are places for more partial sums: no size is above that
+    of more tokens."""
+    sizes = [moe.workspace_size_few(moe.config(T=T, h=4096, E=128, k=8, f=1536), fs)
+             for T in range(0, 65)]
+    assert sizes == sorted(sizes)
+    steps = [b - a for a, b in zip(sizes[1:], sizes[2:])]
+    assert max(steps) > 2 * sorted(steps)[len(steps) // 2]  # where they begin
