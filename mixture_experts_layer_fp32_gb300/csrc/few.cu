@@ -120,6 +120,12 @@ __device__ __forceinline__ int load_acquire(const int* p) {
   return v;
 }
 
+// What thread 0 finds out for its block it leaves in plan.on.  Whoever writes that word has
+// a barrier of the block before it, since warps may still be reading what was there, and
+// one after it.  (As the result of the barrier itself, without a word: fp32 spills more,
+// 7 tokens, 3 of 12 of 1032 x 1416, 69.9 us where this takes 67.9, 64 tokens, 2 of 8 of
+// 1024 x 2048, 115 and 108; bf16 alike.)
+
 // The n-th barrier of all blocks.  false, for the whole block, where the wait ran out.
 __device__ bool grid_barrier(const Args& a, Plan& plan, int n) {
   __syncthreads();
@@ -143,6 +149,7 @@ __device__ bool grid_barrier(const Args& a, Plan& plan, int n) {
 
 // Until an expert's hidden values are there.  false as above.
 __device__ bool expert_ready(const Args& a, Plan& plan, int hit, int tiles) {
+  __syncthreads();  // tile_done's word is read
   if (threadIdx.x == 0) {
     const long long began = clock64();
     int on = 1;

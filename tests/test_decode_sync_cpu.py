@@ -1,0 +1,44 @@
+"""Races that no run shows, held off by the form of the source: what the kernels of a decoding
+step may not do between two barriers, read from their text."""
+
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "mixture_experts_layer_fp32_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        text = f.read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def body(text, head):
+    """The function whose definition begins with `head`, to its closing brace."""
+    at = text.index(head)
+    end = at = text.index("{", at)
+    depth = 0
+    while True:
+        depth += {"{": 1, "}": -1}.get(text[end], 0)
+        end += 1
+        if depth == 0:
+            return text[at:end]
+
+
+def test_a_verdict_is_read_by_all_before_the_next_is_written():
+    """grid_barrier, expert_ready and tile_done follow one another within a block in any order, and
+    each leaves thread 0's verdict in one word of shared memory.  Every one of them has a barrier
+    of the block before it writes, as a warp may not have read the last verdict yet, and one before
+    it reads."""
+    text = source("few.cu")
+    assert len(re.findall(r"plan\.on\s*=[^=]", text)) == 3
+    for head in ("bool grid_barrier(", "bool expert_ready(", "void tile_done("):
+        f = body(text, head)
+        write = re.search(r"plan\.on\s*=[^=]", f).start()
+        read = re.search(r"plan\.on(?!\s*=[^=])", f).start()
+        sync = [m.start() for m in re.finditer(r"__syncthreads\(\);", f)]
+        assert any(s < write for s in sync), head
+        assert any(write < s < read for s in sync), head
+        first = min(sync)   # for the whole block, before thread 0's part
+        assert first < f.index("threadIdx.x == 0"), head

@@ -326,3 +326,18 @@ def test_weights_past_32_bits():
     a, b = (v.double() for v in y)
     assert float((a - b).abs().max()) <= 2.0 ** -7 * float(a.abs().max())
     assert float(a.abs().max()) > 0.1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=24, h=512, E=16, k=4, f=384),               # a tile of FC1 in several blocks' runs
+    dict(T=64, h=2048, E=4, k=2, f=640, fs=256),       # long tiles, many blocks to each
+    dict(T=9, h=264, E=8, k=2, f=520, dtype="f32"),
+], ids=str)
+def test_tiles_shared_by_blocks_repeat_bit_for_bit(kw):
+    """A block's last tile of FC1 is mostly finished by another one, and its own warps go on to the
+    next expert's hidden values at once."""
+    c = LayerCase(**kw).cuda()
+    out = call(c)
+    verify(c, out)
+    for _ in range(60):
+        assert same(out, call(c, ws=out[4]))
