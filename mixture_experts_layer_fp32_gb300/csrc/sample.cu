@@ -560,6 +560,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
   if (r >= a.rows) return;  // the whole cluster
+  // Another block's shared memory is there once that block has begun: waited for before
+  // the first store into it.
+  ptx::cluster_arrive();
   Row<T> row;
   const int64_t begin = min(a.V, static_cast<int64_t>(rank) * a.part);
   row.first = static_cast<int>(begin);
@@ -601,6 +604,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) s.warp_max[warp] = top;
   __syncthreads();
+  ptx::cluster_wait();
   if (warp == 0) {
     top = s.warp_max[lane];
 #pragma unroll

@@ -42,3 +42,17 @@ def test_a_verdict_is_read_by_all_before_the_next_is_written():
         assert any(write < s < read for s in sync), head
         first = min(sync)   # for the whole block, before thread 0's part
         assert first < f.index("threadIdx.x == 0"), head
+
+
+def test_no_store_into_another_block_before_it_has_begun():
+    """sample_kernel's clusters: distributed shared memory may be touched once all blocks of the
+    cluster run, which only a barrier of the cluster says."""
+    f = body(source("sample.cu"), "sample_kernel(")
+    first = f.index("put(there(")
+    arrive, wait = f.index("cluster_arrive()"), f.index("cluster_wait()")
+    assert arrive < wait < first
+    # both by all threads: nothing but the whole cluster's exit stands before them
+    assert f[:arrive].count("return;") == 1 and f.index("if (r >= a.rows) return;") < arrive
+    assert "return;" not in f[arrive:wait]
+    for helper in ("get32(there(", "get64(there(", "add32(there("):
+        assert helper not in f[:wait]
