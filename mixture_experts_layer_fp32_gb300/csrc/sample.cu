@@ -41,6 +41,7 @@ constexpr float kOne = 1099511627776.f;  // 2^40
 constexpr int kMaxBlocks = 16;           // of a cluster
 constexpr size_t kMaxData = 152 * 1024;  // bytes of a block's part of a row
 constexpr int kFewest = 2048;            // tokens of a block, where a row is split
+constexpr int kSumBy32 = 4095;           // tokens of a thread whose halves add up in 32 bits
 
 typedef unsigned long long u64;
 
@@ -150,7 +151,8 @@ struct Scale {
   }
   __device__ __forceinline__ float weight(float l) const { return expf(-below(l)); }
 };
-// w 2^40 for 0 <= w <= 1 as a whole number: its upper part, and 20 bits (rounded)
+// w 2^40 for 0 <= w <= 1 as a whole number: its upper part, 2^20 at most, and 20 bits
+// (rounded, so 2^20 at most too)
 __device__ __forceinline__ void whole(float w, uint32_t& hi, uint32_t& lo) {
   const float v = w * 0x1p20f;  // exact
   hi = __float2uint_rd(v);
@@ -726,8 +728,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   };
   u64 sum = 0;
   float w;
-  if (last == 0 && min_p <= 0.f && a.part <= kThreads * 4096) {
-    // all of them: a thread's halves of 20 bits over 4096 tokens stay in 32
+  if (last == 0 && min_p <= 0.f && a.part <= kThreads * kSumBy32) {
+    // all of them, a thread's halves apart: 2^20 each at most
+    static_assert(static_cast<u64>(kSumBy32) << 20 < u64{1} << 32, "sums of halves");
     uint32_t his = 0, los = 0;
     row.each([&](float l, int) {
       uint32_t hi, lo;
