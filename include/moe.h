@@ -804,7 +804,8 @@ moe_status moe_forward_few(const moe_config* cfg, int32_t fs, const void* x, con
  * Weights are whole numbers of 2^-40 in sums, so a row's token does not depend on the
  * batch, and repeats are equal.  Values for each row stand in the *_of arrays [rows] in
  * device memory; NULL: the one value for all (temperature >= 0, top_k >= 0, top_p and
- * min_p in [0, 1]; MOE_ERR_INVALID_ARG otherwise).  vocab is at most 2^30.
+ * min_p in [0, 1]; MOE_ERR_INVALID_ARG otherwise).  vocab is below 2^24, so that the sums
+ * stay below 2^64 (MOE_ERR_UNSUPPORTED from there on).
  *   logits [rows, vocab] dtype, u [rows] fp32, tokens [rows] int32 out, prob [rows] fp32 out.
  */
 typedef struct moe_sample_choices {

@@ -980,7 +980,7 @@ def forward_few(cfg, x, Wg, gate_bias, expert_bias, W1, W3, W2, y, ws, topk_idx=
 
 
 def sample(logits, u, tokens, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, prob=None):
-    """tokens [rows] int32 from logits [rows, V] (fp32 or bf16) and random numbers
+    """tokens [rows] int32 from logits [rows, V] (fp32 or bf16, V < 2^24) and random numbers
     u [rows] fp32 in [0, 1): the tokens that top_k, then top_p, then min_p leave, drawn
     by their probabilities at that temperature (0: the likeliest).  Each choice is a
     number or a device tensor [rows] (fp32; top_k int32).  prob [rows] fp32, where

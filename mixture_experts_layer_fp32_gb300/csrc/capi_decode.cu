@@ -106,7 +106,8 @@ moe_status moe_sample(int64_t rows, int32_t vocab, int32_t dtype, const void* lo
                       const float* u, const moe_sample_choices* choices, int32_t* tokens,
                       float* prob, moe_stream_t stream) {
   if (rows < 0 || vocab <= 0 || choices == nullptr || !is_dtype(dtype)) return MOE_ERR_INVALID_ARG;
-  if (vocab > (1 << 30) || rows >= (int64_t{1} << 31)) return MOE_ERR_UNSUPPORTED;
+  // sums of weights of up to 2^40 are held in 64 bits
+  if (vocab >= (1 << 24) || rows >= (int64_t{1} << 31)) return MOE_ERR_UNSUPPORTED;
   const moe_sample_choices& c = *choices;
   // false for NaN
   if (!(c.temperature >= 0.f) || c.top_k < 0 || !(c.top_p >= 0.f && c.top_p <= 1.f) ||

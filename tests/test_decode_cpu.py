@@ -238,3 +238,11 @@ def test_few_workspace_serves_fewer_tokens_where_pieces_begin(moe, fs):
     assert sizes == sorted(sizes)
     steps = [b - a for a, b in zip(sizes[1:], sizes[2:])]
     assert max(steps) > 2 * sorted(steps)[len(steps) // 2]  # where they begin
+
+
+def test_sample_refuses_vocabularies_whose_sums_overflow(moe):
+    """A weight is 2^40 at most: 2^24 of them would add up to 2^64."""
+    for V in (1 << 24, (1 << 24) + 1, 1 << 30):
+        assert sample(moe, V=V) == UNSUPPORTED
+        assert sample(moe, V=V, rows=0, logits=None, u=None, tokens=None) == UNSUPPORTED
+    assert sample(moe, V=(1 << 24) - 1, rows=0, logits=None, u=None, tokens=None) == OK
