@@ -7,6 +7,7 @@ library is missing, `lib()` raises.
 """
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -942,11 +943,19 @@ def forward_w4(cfg, x, Wg, gate_bias, expert_bias, q, y, ws, topk_idx=None, topk
 # ---------------------------------------------------------------- a decoding step
 
 FEW_MAX_TOKENS = 64
+_MOST = 2 ** 31 - 1
+
+
+def _int32(v):
+    """A whole number for a 32-bit argument.  ctypes would cut off what is past 32 bits; the end
+    of the range instead is what the library refuses, or all there are."""
+    return v if v.__class__ is int and -_MOST <= v <= _MOST else \
+        max(-_MOST - 1, min(_MOST, operator.index(v)))
 
 
 def workspace_size_few(cfg, fs=0):
     v = ctypes.c_size_t()
-    _check(lib().moe_workspace_size_few(ctypes.byref(cfg), int(fs), ctypes.byref(v)),
+    _check(lib().moe_workspace_size_few(ctypes.byref(cfg), _int32(fs), ctypes.byref(v)),
            "moe_workspace_size_few")
     return v.value
 
@@ -966,7 +975,7 @@ def forward_few(cfg, x, Wg, gate_bias, expert_bias, W1, W3, W2, y, ws, topk_idx=
     fs = 0
     if shared is not None:
         s1, s3, s2 = shared
-        fs = s1.shape[-1]
+        fs = _int32(s1.shape[-1])
     b, wb = _ws(ws)
     _check(lib().moe_forward_few(
         ctypes.byref(cfg), fs, _table(x, T, h, dt, "x"), _table(Wg, h, E, f32, "Wg"),
@@ -993,12 +1002,13 @@ def sample(logits, u, tokens, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, pr
     for v, off, dt, what in ((temperature, 1.0, f32, "temperature"), (top_k, 0, i32, "top_k"),
                              (top_p, 1.0, f32, "top_p"), (min_p, 0.0, f32, "min_p")):
         tensor = isinstance(v, torch.Tensor)
-        one.append(off if tensor else v)
+        one.append(off if tensor else v if dt is f32 else _int32(v))
         each.append(_vec(v, rows, dt, what) if tensor else None)
     choices = SampleChoices(*one, *each)
-    _check(lib().moe_sample(rows, V, _code(logits, "logits"), _p(logits), _vec(u, rows, f32, "u"),
-                            ctypes.byref(choices), _vec(tokens, rows, i32, "tokens"),
-                            _vec(prob, rows, f32, "prob"), _stream()), "moe_sample")
+    _check(lib().moe_sample(rows, V if V < _MOST else _MOST, _code(logits, "logits"), _p(logits),
+                            _vec(u, rows, f32, "u"), ctypes.byref(choices),
+                            _vec(tokens, rows, i32, "tokens"), _vec(prob, rows, f32, "prob"),
+                            _stream()), "moe_sample")
 
 
 def quantize_rows_i8(x, codes, scales):
@@ -1009,9 +1019,9 @@ def quantize_rows_i8(x, codes, scales):
     rows = x.numel() // K
     if codes.dtype != torch.int8 or codes.shape != x.shape:
         raise ValueError("codes must be int8, of x's shape")
-    _check(lib().moe_quantize_rows_i8(rows, K, _code(x, "x"), _p(x), _p(codes),
-                                      _vec(scales, rows, torch.float32, "scales"), _stream()),
-           "moe_quantize_rows_i8")
+    _check(lib().moe_quantize_rows_i8(rows, K if K < _MOST else _MOST, _code(x, "x"), _p(x),
+                                      _p(codes), _vec(scales, rows, torch.float32, "scales"),
+                                      _stream()), "moe_quantize_rows_i8")
 
 
 class I8Weight:
@@ -1025,6 +1035,7 @@ class I8Weight:
             raise ValueError("codes must be [N, K] and scales [N]")
         self._codes, self._scales = codes, scales
         self._n, self._k = codes.shape
+        self._sizes = _int32(self._n), _int32(self._k)
 
     codes = property(lambda self: self._codes)
     scales = property(lambda self: self._scales)
@@ -1044,7 +1055,7 @@ def quantize_i8(W):
 
 def workspace_size_linear_i8(rows, w):
     v = ctypes.c_size_t()
-    _check(lib().moe_workspace_size_linear_i8(int(rows), w.n, w.k, ctypes.byref(v)),
+    _check(lib().moe_workspace_size_linear_i8(int(rows), *w._sizes, ctypes.byref(v)),
            "moe_workspace_size_linear_i8")
     return v.value
 
@@ -1066,7 +1077,7 @@ def linear_i8(x, w, y, ws, x_scale=None, bias=None):
     if coded != (x_scale is not None):
         raise ValueError("x_scale belongs to codes (int8), and codes need it")
     b, wb = _ws(ws)
-    _check(lib().moe_linear_i8(rows, w.n, w.k, _p(x), 2 if coded else _code(x, "x"),
+    _check(lib().moe_linear_i8(rows, *w._sizes, _p(x), 2 if coded else _code(x, "x"),
                                _vec(x_scale, rows, torch.float32, "x_scale"), _p(w.codes),
                                _p(w.scales), _vec(bias, w.n, torch.float32, "bias"), _p(y),
                                _code(y, "y"), b, wb, _stream()), "moe_linear_i8")

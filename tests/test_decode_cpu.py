@@ -246,3 +246,25 @@ def test_sample_refuses_vocabularies_whose_sums_overflow(moe):
         assert sample(moe, V=V) == UNSUPPORTED
         assert sample(moe, V=V, rows=0, logits=None, u=None, tokens=None) == UNSUPPORTED
     assert sample(moe, V=(1 << 24) - 1, rows=0, logits=None, u=None, tokens=None) == OK
+
+
+def test_binding_hands_on_no_number_cut_to_32_bits(recorder):  # noqa: F811
+    """Sizes and a top-k past 32 bits: the end of the range (a size that the library refuses, a
+    top-k of all tokens), not what their lowest bits say."""
+    m, most = recorder, 2 ** 31 - 1
+    l, u, t = torch.zeros(3, 10), torch.zeros(3), torch.zeros(3, dtype=torch.int32)
+    for k, want in ((2 ** 32 + 5, most), (2 ** 31, most), (2 ** 63 - 1, most), (most, most),
+                    (-2 ** 32 + 7, -2 ** 31), (7, 7)):
+        m.sample(l, u, t, top_k=k)
+        assert m.calls[-1][1][5]._obj.top_k == want
+    with pytest.raises(TypeError):
+        m.sample(l, u, t, top_k=2.5)
+    none = torch.empty(0, 2 ** 32 + 16, dtype=BF)   # no rows: no memory
+    m.sample(none, u[:0], t[:0])
+    assert m.calls[-1][1][1] == most
+    codes = torch.empty(0, 2 ** 32 + 16, dtype=torch.int8)
+    m.quantize_rows_i8(none, codes, u[:0])
+    assert m.calls[-1][1][1] == most
+    w = m.I8Weight(codes, u[:0])
+    m.linear_i8(none, w, torch.empty(0, 0), torch.zeros(256, dtype=torch.uint8))
+    assert m.calls[-1][1][:3] == (0, 0, most)
