@@ -1,9 +1,9 @@
 """ctypes binding of libmoe_gb300.so (include/moe.h).
 
 Argument marshalling only: every step of the layer runs in the CUDA library.
-Tensors are torch CUDA tensors (contiguous); the current torch stream is
-passed to the library.  There is no CPU or PyTorch fallback: if the
-library is missing, `lib()` raises.
+Tensors are torch CUDA tensors (contiguous) of the current device, whose current
+torch stream is passed to the library.  There is no CPU or PyTorch fallback: if
+the library is missing, `lib()` raises.
 """
 
 import ctypes
@@ -191,13 +191,24 @@ def _check(code, where):
         raise MoeError(code, where, detail)
 
 
+# The current device and its current stream's handle without the checks and objects
+# around them (0.3 us, not 3); the names are not public ones, so a torch without them
+# takes the public way.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _p(t):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("expected a torch tensor")
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a CUDA device (no CPU path exists)")
+    try:
+        device = t.get_device()
+    except AttributeError:
+        raise TypeError("expected a torch tensor") from None
+    if device != _current_device():
+        raise ValueError("tensors must live on the current CUDA device, whose stream is used"
+                         if device >= 0 else
+                         "tensors must live on a CUDA device (no CPU path exists)")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
@@ -214,15 +225,10 @@ def _host(t):
     return t.data_ptr()
 
 
-# The current stream's handle without the object around it (0.3 us, not 3); the name
-# is not a public one, so a torch without it takes the public way.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream():
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(_current_device())
 
 
 def _ws(ws):
@@ -1068,18 +1074,19 @@ def linear_i8(x, w, y, ws, x_scale=None, bias=None):
     """y [..., N] (bf16 or fp32) = x [..., K] . W^T + bias; w: I8Weight [N,K].  x: codes
     int8 with x_scale (fp32, one a row), or bf16 or fp32 values, quantised in the call."""
     xs, ys = x.shape, y.shape
-    if not xs or xs[-1] != w.k:
+    n, k = w._sizes
+    if not xs or xs[-1] != k:
         raise ValueError("x must be [..., K]")
-    if not ys or ys[-1] != w.n or ys[:-1] != xs[:-1]:
+    if not ys or ys[-1] != n or ys[:-1] != xs[:-1]:
         raise ValueError("y must be [..., N]")
-    rows = x.numel() // w.k
+    rows = x.numel() // k
     coded = x.dtype == torch.int8
     if coded != (x_scale is not None):
         raise ValueError("x_scale belongs to codes (int8), and codes need it")
     b, wb = _ws(ws)
-    _check(lib().moe_linear_i8(rows, *w._sizes, _p(x), 2 if coded else _code(x, "x"),
-                               _vec(x_scale, rows, torch.float32, "x_scale"), _p(w.codes),
-                               _p(w.scales), _vec(bias, w.n, torch.float32, "bias"), _p(y),
+    _check(lib().moe_linear_i8(rows, n, k, _p(x), 2 if coded else _code(x, "x"),
+                               _vec(x_scale, rows, torch.float32, "x_scale"), _p(w._codes),
+                               _p(w._scales), _vec(bias, n, torch.float32, "bias"), _p(y),
                                _code(y, "y"), b, wb, _stream()), "moe_linear_i8")
 
 
