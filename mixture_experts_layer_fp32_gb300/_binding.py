@@ -205,10 +205,10 @@ def _p(t):
         device = t.get_device()
     except AttributeError:
         raise TypeError("expected a torch tensor") from None
+    if device < 0:
+        raise ValueError("tensors must live on a CUDA device (no CPU path exists)")
     if device != _current_device():
-        raise ValueError("tensors must live on the current CUDA device, whose stream is used"
-                         if device >= 0 else
-                         "tensors must live on a CUDA device (no CPU path exists)")
+        raise ValueError("tensors must live on the current CUDA device, whose stream is used")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
