@@ -824,7 +824,7 @@ moe_status moe_sample(int64_t rows, int32_t vocab, int32_t dtype, const void* lo
 
 /*
  * Rows in 8-bit integers: scales[r] = max |x[r]| * (1 / 127) in fp32 (the number nearest
- * 1 / 127, one rounding of the product), codes[r, k] the nearest whole number of
+ * 1 / 127, one rounding of the product: within 2^-23 of max |x[r]| / 127), codes[r, k] the nearest whole number of
  * x[r, k] / scales[r], ties to even, -127..127.  A row of zeros gets
  * the scale 0, one with an infinity or a NaN the scale NaN (codes 0 in both).
  *   x [rows, K] dtype (MOE_F32 or MOE_BF16), codes [rows, K] int8 out, scales [rows]

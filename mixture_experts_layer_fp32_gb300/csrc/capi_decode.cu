@@ -40,7 +40,8 @@ moe_status validate_few(const moe_config* cfg, int32_t fs) {
   // a row's inputs and all rows' inputs are counted in 32 bits
   constexpr int32_t most = 1 << 21;
   if (cfg->hidden > most || cfg->ffn_hidden > most || fs > most) return MOE_ERR_UNSUPPORTED;
-  // the weights of one kind are counted in units of 16 x 512 in 32 bits
+  // the weights of one kind are counted in units in 32 bits: 16 inputs of 512 outputs (of
+  // FC1, 256 of W1 and the same of W3) or more, here taken as 16 x 256
   auto units = [](int64_t in, int64_t out) { return (in + 15) / 16 * ((out + 255) / 256); };
   const int64_t h = cfg->hidden, f = cfg->ffn_hidden;
   const int64_t up = cfg->num_experts * units(h, f) + units(h, fs);

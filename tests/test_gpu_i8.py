@@ -272,3 +272,31 @@ def test_results_past_32_bits():
     for r in (0, 65535, M - 100):
         part = slice(r, r + 100)
         assert torch.equal(y[part], product(xq[part], xs[part], wq, ws, torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,K,N", [(6, 512, 100), (12, 4096, 300), (150, 1040, 260)])
+def test_against_the_quotient_by_127_in_64_bits(rows, K, N, dtype):
+    """The scale by its own formula, max / 127: fp32's 1 / 127 and the product are off by half a
+    step each, 2^-23 together.  A code is the nearest whole number over that scale, so it stands for
+    its value within half a scale; 127 times 2^-22 of one more where the largest is cut to 127.  And
+    so a product of values is off by no more than what the codes are, its sum's rounding to fp32 and
+    the two products', half a step each."""
+    import mixture_experts_layer_fp32_gb300 as moe
+    g = torch.Generator(device="cuda").manual_seed(rows * K)
+    x = (torch.randn(rows, K, device="cuda", generator=g) *
+         torch.rand(rows, 1, device="cuda", generator=g) * 10).to(DT[dtype])
+    q = torch.empty(x.shape, dtype=torch.int8, device="cuda")
+    s = torch.empty(rows, device="cuda")
+    moe.quantize_rows_i8(x, q, s)
+    exact = x.double().abs().amax(1) / 127
+    assert bool(((s.double() - exact).abs() <= 2.0 ** -23 * (1 + 1e-6) * exact).all())
+    most = s.double()[:, None] * (0.5 + 127 * 2.0 ** -22)
+    assert bool(((q.double() * s.double()[:, None] - x.double()).abs() <= most).all())
+    assert int(q.abs().amax(1).min()) == 127
+    wq, ws = codes((N, K), N), scales(N, N)
+    y = linear(x, wq, ws, torch.float32).double()
+    W = wq.double() * ws.double()[:, None]
+    want = x.double() @ W.t()
+    off = most * W.abs().sum(1)
+    assert bool(((y - want).abs() <= off + 3 * 2.0 ** -24 * (want.abs() + off)).all())
