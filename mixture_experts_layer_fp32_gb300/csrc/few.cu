@@ -28,7 +28,8 @@
 // Measured, all of a call: 1 token, 2 of 8 experts of 4096 x 14336 bf16, 129 us (the bytes
 // at the copy rate: 105); 8 tokens 400 (379); 32 tokens, 8 of 128 of 4096 x 1536, 689 (630).
 // The 20 to 25 us above the bytes are the logits, two or three barriers, the plan and the
-// combine, through most of which memory idles.
+// combine, through most of which memory idles.  Registers are short: bf16 takes 255 and
+// spills 24 bytes (48 with pieces), fp32 128 and 556.
 //
 // The products are mma.sync with the weights as the operand of 16 rows and 8 tokens as
 // the columns.  The tensor cores' rate does not matter here (tcgen05 would need 128 rows
@@ -37,13 +38,18 @@
 //   bf16: weights by ldmatrix.trans out of the ring, whose 16-byte pieces are swapped so
 //     that it meets no bank twice; the inputs of 32 are permuted between the instructions
 //     so that a lane's share of x is 16 bytes in a row.  A hidden value enters FC2 as two
-//     bf16 numbers (together within 2^-17 of it), so the layer has no rounding between x
-//     and y but y's own.
+//     bf16 numbers (together within 2^-17 of it), so nothing between x and y is rounded to
+//     16 bits but y.  Before that it is within 4.5e-5 of the RMS (the pieces, and sums that
+//     the instruction cuts off); 0.4 to 0.7% of the results are not the nearest bf16 number.
 //   fp32: each operand as two tf32 numbers, v = p + q with |q| <= 2^-11 |v| and q itself
 //     rounded (2^-22 of v); p p', p q' and q p' are multiplied, q q' (2^-22) is left out.
 //     FMAs, two outputs to a lane, took longer from the first row on (7 tokens, 3 of 12 of
 //     1032 x 1416: 126 us where this took 71; 64 tokens, 2 of 8 of 1024 x 4096: 782 and
-//     168).  An infinity in x gives NaN.
+//     168).  An infinity gives NaN, and so does a number within 2^-12 of the largest one,
+//     which rounds up to it.
+//     From 9 rows on the issue slots bound it: each of 16 warps splits the same x anew, and
+//     the sums of 64 rows spill.  64 tokens, 4 of 16 of 2048 x 1408: 221 us (the bytes 83), and
+//     443 where one expert has more than 32 of the rows.
 //
 // All partial sums are added in an order given by sizes alone: repeats are equal
 // bit for bit.

@@ -23,7 +23,9 @@
 //
 // What bounds it: shared memory (x is read for each tile: 160 KB for 256 x 128 x 128
 // products, 1250 cycles where these take 1024) beside the reading of sums; with sums read
-// once an item, or codes not converted, the 712 were 623 and 670.  Few rows: memory (64 x
+// once an item, or codes not converted, the 712 were 623 and 670.  The kernel of 128 columns
+// spills besides (128 sums and 16 loads in a thread's 152 registers: 592 bytes of stores,
+// 236 where parts of sums are stored; none with 64 and 32 columns).  Few rows: memory (64 x
 // 151936 x 4096: 110 us, 5.9 TB/s).  Tried and left: pairs of blocks that share a product
 // (256 outputs a tile, half of x in each): 1280 us, whatever the number of slots.
 #include <type_traits>

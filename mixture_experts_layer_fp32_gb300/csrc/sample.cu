@@ -20,9 +20,13 @@
 // order).
 //
 // What bounds it: a row's latency (load, passes with cluster barriers, sorts), not memory.
-// One row of 128000 fp32 with top-k, top-p and min-p takes 25 us, 64 of 151936 bf16 23 (the
-// bytes at the copy rate 0.1 and 3).  With a top-p alone the 64 take 110: all tokens are
-// weighed, by integer instructions mostly (58% of the issue slots).
+// One row of 128000 fp32 takes 25 us with a top-p, 15 with a top-k of 50 beside it, 27 with
+// one of 1000, 5 greedy (its bytes at the copy rate 0.1); 64 of 151936 bf16 with a top-k, top-p
+// and min-p 23 (bytes 3).  Without a top-k the 64 take longer, as all tokens are weighed:
+// 48 with a temperature alone, 57 with a min-p (a pass of weights, then one warp that goes
+// over its run again for the token), and 103 to 110 with a top-p (four additions in shared
+// memory a token, the border's bin searched for in further passes; integer instructions
+// mostly, 58% of the issue slots).
 #include <float.h>
 #include <math.h>
 
