@@ -763,12 +763,12 @@ moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, c
  * weight): tokens_per_expert counts kept pairs.  With bf16 the hidden values are
  * not rounded to bf16 between the products (they enter the second one as two
  * bf16 numbers each, within 2^-17), sums are fp32 (the tensor cores cut theirs off),
- * y is rounded once (before that it was within 5e-5 of y's RMS at the sizes that were
- * measured, h from 4096 to 7168).  With fp32 a
- * factor is two tf32 numbers, so that a product is within 3 2^-22 of itself, and sums
- * are fp32.  Not as in the other two: an infinite x, weight or hidden value may give NaN
- * where an infinity would be right, and with fp32 so does one that is within 2^-12 of
- * the largest number.  Repeats give equal bits.
+ * y is rounded once (before that, off by 5e-5 of its RMS at most where that was
+ * measured, h from 4096 to 7168).  With fp32 a factor is two tf32 numbers, so that a
+ * product is within 3 2^-22 of itself, and sums are fp32.  Not as in the other two: an
+ * infinite x, weight or hidden value may give NaN where an infinity would be right, and
+ * with fp32 so does one that is within 2^-12 of the largest number.  Repeats give equal
+ * bits.
  * y may be x.  A token whose logits are NaN is reported in ws (moe_check).
  * The kernel takes every SM's shared memory and its blocks wait for one another
  * (a cooperative launch; waits that run out are reported in ws): a call whose

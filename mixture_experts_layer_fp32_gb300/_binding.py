@@ -1041,7 +1041,6 @@ class I8Weight:
             raise ValueError("codes must be [N, K] and scales [N]")
         self._codes, self._scales = codes, scales
         self._n, self._k = codes.shape
-        self._sizes = _int32(self._n), _int32(self._k)
 
     codes = property(lambda self: self._codes)
     scales = property(lambda self: self._scales)
@@ -1061,8 +1060,8 @@ def quantize_i8(W):
 
 def workspace_size_linear_i8(rows, w):
     v = ctypes.c_size_t()
-    _check(lib().moe_workspace_size_linear_i8(int(rows), *w._sizes, ctypes.byref(v)),
-           "moe_workspace_size_linear_i8")
+    _check(lib().moe_workspace_size_linear_i8(int(rows), _int32(w.n), _int32(w.k),
+                                              ctypes.byref(v)), "moe_workspace_size_linear_i8")
     return v.value
 
 
@@ -1074,7 +1073,7 @@ def linear_i8(x, w, y, ws, x_scale=None, bias=None):
     """y [..., N] (bf16 or fp32) = x [..., K] . W^T + bias; w: I8Weight [N,K].  x: codes
     int8 with x_scale (fp32, one a row), or bf16 or fp32 values, quantised in the call."""
     xs, ys = x.shape, y.shape
-    n, k = w._sizes
+    n, k = w.n, w.k
     if not xs or xs[-1] != k:
         raise ValueError("x must be [..., K]")
     if not ys or ys[-1] != n or ys[:-1] != xs[:-1]:
@@ -1084,9 +1083,10 @@ def linear_i8(x, w, y, ws, x_scale=None, bias=None):
     if coded != (x_scale is not None):
         raise ValueError("x_scale belongs to codes (int8), and codes need it")
     b, wb = _ws(ws)
-    _check(lib().moe_linear_i8(rows, n, k, _p(x), 2 if coded else _code(x, "x"),
-                               _vec(x_scale, rows, torch.float32, "x_scale"), _p(w._codes),
-                               _p(w._scales), _vec(bias, n, torch.float32, "bias"), _p(y),
+    _check(lib().moe_linear_i8(rows, n if n < _MOST else _MOST, k if k < _MOST else _MOST, _p(x),
+                               2 if coded else _code(x, "x"),
+                               _vec(x_scale, rows, torch.float32, "x_scale"), _p(w.codes),
+                               _p(w.scales), _vec(bias, n, torch.float32, "bias"), _p(y),
                                _code(y, "y"), b, wb, _stream()), "moe_linear_i8")
 
 

@@ -266,5 +266,7 @@ def test_binding_hands_on_no_number_cut_to_32_bits(recorder):  # noqa: F811
     m.quantize_rows_i8(none, codes, u[:0])
     assert m.calls[-1][1][1] == most
     w = m.I8Weight(codes, u[:0])
-    with pytest.raises(ValueError):
-        m.linear_i8(none, w, torch.empty(0, 0), torch.zeros(256, dtype=torch.uint8))
+    m.linear_i8(none, w, torch.empty(0, 0), torch.zeros(256, dtype=torch.uint8))
+    assert m.calls[-1][1][:3] == (0, 0, most)
+    with pytest.raises(m.MoeError):   # the real library
+        m.workspace_size_linear_i8(1, w)

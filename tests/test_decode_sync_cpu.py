@@ -26,10 +26,10 @@ def body(text, head):
             return text[at:end]
 
 
-def test_a_verdict_is_read_by_all_before_the_next_is_written():
+def test_an_answer_is_read_by_all_before_the_next_is_written():
     """grid_barrier, expert_ready and tile_done follow one another within a block in any order, and
-    each leaves thread 0's verdict in one word of shared memory.  Every one of them has a barrier
-    of the block before it writes, as a warp may not have read the last verdict yet, and one before
+    each leaves thread 0's answer in one word of shared memory.  Every one of them has a barrier
+    of the block before it writes, as a warp may not have read the last answer yet, and one before
     it reads."""
     text = source("few.cu")
     assert len(re.findall(r"plan\.on\s*=[^=]", text)) == 3
